@@ -16,6 +16,62 @@ import torch
 from . import binding
 
 
+def _strided(t):
+    """t itself where the kernels can read its strides (heads of whole 16-byte
+    pieces), else a contiguous copy."""
+    s = t.stride()
+    if s[-1] == 1 and t.data_ptr() % 16 == 0 and not any(x % 8 for x in s[:-1]):
+        return t
+    return t.contiguous()
+
+
+class RotaryFunc(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, table, positions, period, interleaved):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(table, positions)
+        ctx.how = (period, interleaved)
+        return binding.dfa_rotary(_strided(q), None if k is None else _strided(k), table,
+                                  positions, period, interleaved, clear=True)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        table, positions = ctx.saved_tensors
+        period, interleaved = ctx.how
+
+        def turn(x, y):
+            return binding.dfa_rotary(_strided(x), None if y is None else _strided(y), table,
+                                      positions, period, interleaved, inverse=True, clear=True)
+
+        if dq is not None:
+            dq, dk = turn(dq, dk)
+        elif dk is not None:
+            dk = turn(dk, None)[0]
+        return dq, dk, None, None, None, None
+
+
+def rotary_func(q, k, table, positions=None, interleaved=False, period=None):
+    """Rotary positions of queries and keys; differentiable.
+
+    q (B, L, H, d) and k (B, L, Hk, d), or packed (rows, heads, d) with
+    ``positions`` (rows,); bf16, strided views (the slices of a fused
+    projection) are read in place.  k may be None.  ``table``: see
+    :func:`rotary_table`.  ``positions``: int32, a negative one marks a row
+    that is not in use (its output is 0).  Without positions row r has
+    position r mod ``period``; the default period L // 2 is the [noisy |
+    clean] layout, both halves counted from 0.
+    """
+    if q.dim() == 3:
+        if positions is None:
+            raise ValueError("packed rows need positions")
+        if positions.dim() != 1:
+            raise ValueError("positions of packed rows must be (rows,)")
+        q, k = q[None], None if k is None else k[None]
+        q, k = RotaryFunc.apply(q, k, table, positions[None], period, bool(interleaved))
+        return q[0], None if k is None else k[0]
+    return RotaryFunc.apply(q, k, table, positions, period, bool(interleaved))
+
+
 class DiffusionAttnFunc(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, block_size):
@@ -71,20 +127,36 @@ class DiffusionAttnVarlenFunc(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
-def diffusion_attn_varlen_func(q, k, v, cu_seqlens, block_size):
+def diffusion_attn_varlen_func(q, k, v, cu_seqlens, block_size, rotary_table=None,
+                               positions=None, interleaved=False):
     """Block-diffusion attention on a packed batch (the pages' varlen API).
 
     q: (rows, heads, headdim), k, v: (rows, kv_heads, headdim) bf16; sample b
     is rows [cu_seqlens[b], cu_seqlens[b+1]), [noisy | clean], even length.
+    ``rotary_table`` with ``positions`` (int32 (rows,)): q and k get rotary
+    positions first (:func:`rotary_func`).
     """
+    if rotary_table is not None:
+        q, k = rotary_func(q, k, rotary_table, positions, interleaved)
     return DiffusionAttnVarlenFunc.apply(q, k, v, cu_seqlens, block_size)
 
 
-def diffusion_attn_func(q, k, v, block_size):
-    """Attention under the block-diffusion mask; differentiable."""
+def diffusion_attn_func(q, k, v, block_size, rotary_table=None, interleaved=False):
+    """Attention under the block-diffusion mask; differentiable.
+
+    ``rotary_table``: q and k get rotary positions first, 0 .. n - 1 in either
+    half (:func:`rotary_func`).
+    """
+    if rotary_table is not None:
+        q, k = rotary_func(q, k, rotary_table, interleaved=interleaved)
     return DiffusionAttnFunc.apply(q, k, v, block_size)
 
 
-def causal_attn_func(q, k, v):
-    """Causal attention on (Bc, L, H, d), any Bc; the yardstick kernels."""
+def causal_attn_func(q, k, v, rotary_table=None, interleaved=False):
+    """Causal attention on (Bc, L, H, d), any Bc; the yardstick kernels.
+
+    ``rotary_table``: q and k get rotary positions 0 .. L - 1 first.
+    """
+    if rotary_table is not None:
+        q, k = rotary_func(q, k, rotary_table, interleaved=interleaved, period=max(q.shape[1], 1))
     return CausalAttnFunc.apply(q, k, v)

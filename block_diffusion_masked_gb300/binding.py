@@ -26,6 +26,9 @@ DFA_ETIMEOUT = -4
 DFA_EDEVICE = -5
 DFA_DETERMINISTIC = 1
 DFA_NOISY_DIAG_PASS = 2
+DFA_ROTARY_INTERLEAVED = 1
+DFA_ROTARY_INVERSE = 2
+DFA_ROTARY_CLEAR = 4
 MODE_DIFFUSION = 0
 MODE_CAUSAL = 1
 
@@ -50,6 +53,19 @@ _SIGNATURES = {
     "dfa_forward_fp8_vt": (_I, [_P] * 5 + [ctypes.c_float] * 3 + [_I] * 6 + [_P]),
     "dfa_causal_forward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "dfa_causal_backward": (_I, [_P] * 9 + [_I, _I, _I, _I, _P]),
+    "dfa_rotary": (_I, [_P] * 6 + [_I] * 8 + [_P] * 2 + [_I, _P]),
+    "dfa_cache_plan": (_I, [_P] * 10 + [_I] * 5 + [_P]),
+    "dfa_cache_release": (_I, [_P] * 5 + [_I] * 4 + [_P]),
+    "dfa_cache_append": (_I, [_P] * 9 + [_I] * 8 + [_P] * 3),
+    "dfa_cache_workspace_bytes": (ctypes.c_longlong, [_I] * 6),
+    "dfa_cache_forward": (_I, [_P] * 13 + [ctypes.c_longlong] + [_I] * 10 + [_P] * 4),
+    "dfa_cache_scale_exp": (_I, [ctypes.c_uint]),
+    "dfa_cache_page_ok": (_I, [_I] * 2),
+    "dfa_cache_append_pages": (_I, [_I] * 2),
+    "dfa_cache_append_span": (_I, [_I] * 4 + [ctypes.POINTER(_I)]),
+    "dfa_cache_chunk": (_I, [ctypes.c_longlong, _I]),
+    "dfa_cache_items": (_I, [_I] * 3),
+    "dfa_cache_own_end": (_I, [_I] * 4),
     "dfa_status": (_I, [_P]),
     "dfa_selftest_wait_timeout": (_I, [_I, _P]),
     "dfa_fwd_main": (_I, [_P] * 6 + [_I] * 6 + [_P]),
@@ -567,6 +583,224 @@ def dfa_bwd_dq_convert(dq_acc, dq, mode=MODE_DIFFUSION):
         rc = lib().dfa_bwd_dq_convert_ex(_ptr(dq_acc), _ptr(dq), B, n, H, d, int(mode),
                                          _stream_ptr(dq))
     _check("dfa_bwd_dq_convert_ex", rc)
+
+
+# ------------------------------------------- rotary positions, sampling cache
+
+def _call(fn, device, *args):
+    """Call entry point ``fn`` with ``device`` current, on its current stream."""
+    handle = lib()
+    if device.index == torch.cuda.current_device():
+        rc = getattr(handle, fn)(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(handle, fn)(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != DFA_OK:
+        raise DfaError(fn, rc)
+
+
+def _check_dense(t, shape, dtype, device, name):
+    """A contiguous input of the given shape (None: any size)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device
+            or t.dim() != len(shape) or not t.is_contiguous()
+            or any(s is not None and s != x for s, x in zip(shape, t.shape))):
+        want = ", ".join("any" if s is None else str(s) for s in shape)
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({want}) on {device}")
+    return t
+
+
+def _strides(t, name):
+    """Host array of a tensor's leading strides, None where it is contiguous.
+
+    The last dimension must be contiguous and the others multiples of 8
+    elements (16 bytes), as must be the storage offset's address.
+    """
+    if t.is_contiguous():
+        return None
+    s = t.stride()
+    if s[-1] != 1 or any(x % 8 for x in s[:-1]):
+        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides "
+                         "multiples of 8 elements")
+    return (ctypes.c_longlong * (len(s) - 1))(*s[:-1])
+
+
+def _check_heads(t, dim, name, device=None):
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dim
+            or not t.is_cuda or (device is not None and t.device != device)):
+        where = "a CUDA device" if device is None else str(device)
+        raise ValueError(f"{name} must be a {dim}-dimensional bfloat16 tensor on {where}")
+
+
+def dfa_rotary(q, k, table, positions=None, period=None, interleaved=False, inverse=False,
+               q_out=None, k_out=None, clear=False):
+    """Rotary positions of q (B, L, H, d) and k (B, L, Hk, d), bf16; k may be None.
+
+    ``table``: float32 (max_pos, rot_dim), cosines then sines.  ``positions``:
+    int32 (B, L), or None: row r has position r mod ``period`` (default L // 2,
+    the [noisy | clean] layout).  q and k may be strided views (the last
+    dimension contiguous).  Returns contiguous (q_out, k_out); rows of
+    negative positions are not written, or set to zero with ``clear``.
+    ``inverse`` is the transposed map.
+    """
+    _check_heads(q, 4, "q")
+    B, L, H, d = q.shape
+    dev = q.device
+    Hk = 0
+    if k is not None:
+        _check_heads(k, 4, "k", dev)
+        Hk = k.shape[2]
+        if k.shape[:2] != q.shape[:2] or k.shape[3] != d:
+            raise ValueError("k must be (batch, seqlen, kv_heads, headdim) like q")
+    _check_dense(table, (None, None), torch.float32, dev, "table")
+    if positions is not None:
+        _check_dense(positions, (B, L), torch.int32, dev, "positions")
+    elif period is None:
+        if L % 2:
+            raise ValueError("the sequence must be [noisy | clean] with an even length 2n")
+        period = max(L // 2, 1)
+    q_out = _out_or_new(q_out, q.shape, torch.bfloat16, dev, "q_out")
+    if k is not None:
+        k_out = _out_or_new(k_out, k.shape, torch.bfloat16, dev, "k_out")
+    flags = (DFA_ROTARY_INTERLEAVED if interleaved else 0) | (DFA_ROTARY_INVERSE if inverse else 0)
+    flags |= DFA_ROTARY_CLEAR if clear else 0
+    _call("dfa_rotary", dev, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+          None if k is None else k_out.data_ptr(), table.data_ptr(),
+          None if positions is None else positions.data_ptr(), B, L,
+          1 if period is None else int(period), H, Hk, d, table.shape[1], table.shape[0],
+          _strides(q, "q"), None if k is None else _strides(k, "k"), flags)
+    return q_out, k_out
+
+
+def dfa_cache_plan(cache_lens, new_lens, block_table, free_pages, free_count, page_size, rows):
+    """The pages of a sampling step (see dfa.h).  int32 CUDA tensors: cache_lens,
+    new_lens (B,), block_table (B, max_pages), free_pages (F,), free_count (1,).
+
+    Writes the new pages into ``block_table`` and returns (block_table, cu_new
+    (B + 1,), positions (rows,), next_lens (B,), next_free (1,), missing (1,)).
+    The caller's next step passes next_lens and next_free.
+    """
+    i32, dev = torch.int32, cache_lens.device
+    _check_dense(cache_lens, (None,), i32, dev, "cache_lens")
+    B = cache_lens.shape[0]
+    _check_dense(new_lens, (B,), i32, dev, "new_lens")
+    _check_dense(block_table, (B, None), i32, dev, "block_table")
+    _check_dense(free_pages, (None,), i32, dev, "free_pages")
+    _check_dense(free_count, (1,), i32, dev, "free_count")
+    if not cache_lens.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    rows = int(rows)
+    if rows < 0:
+        raise ValueError("rows must not be negative")
+    buf = torch.empty(2 * B + 3 + rows, dtype=i32, device=dev)
+    cu_new, next_lens, next_free, missing, positions = buf.split([B + 1, B, 1, 1, rows])
+    at = buf.data_ptr()
+    _call("dfa_cache_plan", dev, cache_lens.data_ptr(), new_lens.data_ptr(),
+          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at,
+          at + 4 * (2 * B + 3), at + 4 * (B + 1), at + 4 * (2 * B + 1), at + 4 * (2 * B + 2), B,
+          block_table.shape[1], free_pages.shape[0], int(page_size), rows)
+    return block_table, cu_new, positions, next_lens, next_free, missing
+
+
+def dfa_cache_release(finished, cache_lens, block_table, free_pages, free_count, page_size):
+    """Requests with finished != 0 give their pages back (in place; see dfa.h)."""
+    i32, dev = torch.int32, cache_lens.device
+    _check_dense(cache_lens, (None,), i32, dev, "cache_lens")
+    B = cache_lens.shape[0]
+    _check_dense(finished, (B,), i32, dev, "finished")
+    _check_dense(block_table, (B, None), i32, dev, "block_table")
+    _check_dense(free_pages, (None,), i32, dev, "free_pages")
+    _check_dense(free_count, (1,), i32, dev, "free_count")
+    if not cache_lens.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    _call("dfa_cache_release", dev, finished.data_ptr(), cache_lens.data_ptr(),
+          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B,
+          block_table.shape[1], free_pages.shape[0], int(page_size))
+
+
+def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new, dev, d):
+    """Shapes of a cache and its tables; returns (batch, kv_heads, page_size, pages, max_pages)."""
+    _check_dense(k_cache, (None, None, None, d), torch.float8_e4m3fn, dev, "k_cache")
+    P, Hk, ps, _ = k_cache.shape
+    _check_dense(v_cache, (P, Hk, ps, d), torch.float8_e4m3fn, dev, "v_cache")
+    _check_dense(k_scale, (P, Hk), torch.float32, dev, "k_scale")
+    _check_dense(v_scale, (P, Hk), torch.float32, dev, "v_scale")
+    _check_dense(cache_lens, (None,), torch.int32, dev, "cache_lens")
+    B = cache_lens.shape[0]
+    _check_dense(block_table, (B, None), torch.int32, dev, "block_table")
+    _check_dense(cu_new, (B + 1,), torch.int32, dev, "cu_new")
+    return B, Hk, ps, P, block_table.shape[1]
+
+
+def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_scale, v_scale,
+                     max_new):
+    """Append packed tokens k, v (rows, Hk, d) bf16 to the cache, in place (see dfa.h).
+
+    ``max_new``: a bound on the rows of one request, known to the host.
+    """
+    _check_heads(k, 3, "k")
+    dev = k.device
+    rows, Hk, d = k.shape
+    _check_heads(v, 3, "v", dev)
+    B, Hc, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                                      cu_new, dev, d)
+    if v.shape != k.shape or Hc != Hk:
+        raise ValueError("k and v must be (rows, kv_heads, headdim) with the cache's heads")
+    _call("dfa_cache_append", dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
+          cache_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), B, rows, int(max_new), Hk, d, ps, P, maxp,
+          _strides(k, "k"), _strides(v, "v"))
+
+
+def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim):
+    """Bytes of workspace dfa_cache_forward needs on the current device."""
+    n = lib().dfa_cache_workspace_bytes(batch, rows, int(max_new), heads, kv_heads, headdim)
+    if n < 0:
+        raise DfaError("dfa_cache_workspace_bytes", int(n))
+    return int(n)
+
+
+def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new,
+                      max_new, k=None, v=None, block_size=1, out=None, lse=None, workspace=None):
+    """Attention of packed new rows q (rows, H, d) over the cache and, with k and v
+    (rows, Hk, d) bf16, over their own blocks (see dfa.h).
+
+    ``max_new``: a bound on the rows of one request.  Returns out (rows, H, d)
+    bf16 and lse (H, rows) float32.  ``workspace``: a uint8 tensor of at least
+    dfa_cache_workspace_bytes(...) bytes; by default one is allocated.
+    """
+    _check_heads(q, 3, "q")
+    dev = q.device
+    rows, H, d = q.shape
+    B, Hk, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                                      cu_new, dev, d)
+    if Hk < 1 or H % Hk:
+        raise ValueError("kv_heads must divide the query heads")
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    if k is not None:
+        for x, name in ((k, "k"), (v, "v")):
+            _check_heads(x, 3, name, dev)
+            if x.shape != (rows, Hk, d):
+                raise ValueError(f"{name} must be (rows, kv_heads, headdim)")
+    out = _out_or_new(out, q.shape, torch.bfloat16, dev, "out")
+    lse = _out_or_new(lse, (H, rows), torch.float32, dev, "lse")
+    if workspace is None:
+        if dev.index == torch.cuda.current_device():
+            need = dfa_cache_workspace_bytes(B, rows, max_new, H, Hk, d)
+        else:
+            with torch.cuda.device(dev):
+                need = dfa_cache_workspace_bytes(B, rows, max_new, H, Hk, d)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    else:
+        _check_dense(workspace, (None,), torch.uint8, dev, "workspace")
+    _call("dfa_cache_forward", dev, q.data_ptr(), None if k is None else k.data_ptr(),
+          None if v is None else v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
+          cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+          workspace.numel(), B, rows, int(max_new), H, Hk, d, int(block_size), ps, P, maxp,
+          _strides(q, "q"), None if k is None else _strides(k, "k"),
+          None if v is None else _strides(v, "v"))
+    return out, lse
 
 
 def dfa_selftest_wait_timeout(limit_us=20000):

@@ -35,6 +35,7 @@ struct DeviceState {
   unsigned* status = nullptr;
   unsigned* sched = nullptr;  // kSchedSlots slots of 8 words
   long long l2_bytes = 0;
+  int sms = 0;
   const void* slot_key[kSchedSlots] = {};
   int slots_used = 0;
   int slot_next = 0;
@@ -116,6 +117,8 @@ int device_state(DeviceState** out) {
     int l2 = 0;
     if (cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev) != cudaSuccess) return DFA_ECUDA;
     s.l2_bytes = l2;
+    if (cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return DFA_ECUDA;
     if (s.supported) {
       void* addr = nullptr;
       if (cudaGetSymbolAddress(&addr, g_dfa_status) != cudaSuccess) return DFA_ECUDA;
@@ -828,6 +831,25 @@ int check_device(unsigned long long* ctx_id) {
   if (rc) return rc;
   if (ctx_id) *ctx_id = ds->ctx_id;
   return DFA_OK;
+}
+
+int device_info(DeviceInfo* info) {
+  DeviceState* ds = nullptr;
+  const int rc = device_state(&ds);
+  if (rc) return rc;
+  info->status = ds->status;
+  info->sms = ds->sms;
+  return DFA_OK;
+}
+
+int encode_map_u8(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  const CUresult r =
+      g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
+               const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DFA_OK : DFA_ECUDA;
 }
 
 int record_cuda_failure(cudaError_t e) { return cuda_fail(e); }

@@ -1,0 +1,72 @@
+// Paged 8-bit key/value cache: index arithmetic shared by the host (argument
+// checks, workspace sizes, tests) and the kernels.
+//
+// Layout.  k_cache, v_cache: (pages, kv_heads, page_size, headdim) e4m3, one
+// page of one head contiguous.  k_scale, v_scale: (pages, kv_heads) float32,
+// powers of two: a cached value is its e4m3 value times the scale of its page
+// and head.  block_table: (batch, max_pages) page numbers of each request.
+// A request's new rows are packed behind one another: request b has rows
+// [cu_new[b], cu_new[b + 1]), at positions cache_lens[b], cache_lens[b] + 1 ...
+#pragma once
+
+#include "geometry.cuh"
+
+namespace dfa {
+
+// Smallest exponent of a page scale, and the e4m3 range it maps to.
+constexpr int kCacheMinExp = -100;
+
+// Exponent e of the scale 2^e of a page whose largest finite magnitude has
+// the bf16 bits `bits` (sign cleared): the smallest e >= kCacheMinExp with
+// amax <= 448 * 2^e.  448 = 1.75 * 2^8, so a magnitude (1 + m / 128) * 2^E
+// needs e = E - 8 while m <= 96, else one more.  Subnormal bf16 magnitudes
+// are below 2^-126 and take kCacheMinExp like every magnitude below it.
+DFA_HD int cache_scale_exp(unsigned bits) {
+  const int e = static_cast<int>(bits >> 7) - 127 - 8 + ((bits & 0x7fu) > 96u ? 1 : 0);
+  return e < kCacheMinExp ? kCacheMinExp : e;
+}
+
+// Pages a request can touch when it appends up to max_new tokens.
+DFA_HD int cache_append_pages(int max_new, int page_size) {
+  return (max_new + page_size - 2) / page_size + 1;
+}
+
+// Tokens [lo, hi) that an append of n tokens behind `len` cached ones puts
+// into the j-th page it touches.
+DFA_HD Interval cache_append_range(int len, int n, int j, int page_size) {
+  const long long first = (static_cast<long long>(len / page_size) + j) * page_size;
+  const long long end = static_cast<long long>(len) + n;
+  const long long lo = first > len ? first : len;
+  const long long hi = first + page_size < end ? first + page_size : end;
+  if (lo >= hi) return {0, 0};
+  return {static_cast<int>(lo), static_cast<int>(hi)};
+}
+
+// A page number a kernel may follow.
+DFA_HD bool cache_page_ok(int page, int num_pages) { return page >= 0 && page < num_pages; }
+
+// Split of the cached keys over work items.  The items of all requests should
+// number about `target`: chunk = total / target keys each, rounded up to
+// whole 64-key steps and never below kCacheMinChunk, where an item's set-up
+// and its partial result would cost more than its keys.
+constexpr int kCacheMinChunk = 256;
+DFA_HD int cache_chunk(long long total_keys, int target) {
+  long long c = (total_keys + target - 1) / target;
+  c = (c + 63) / 64 * 64;
+  if (c < kCacheMinChunk) c = kCacheMinChunk;
+  return c > (1 << 30) ? (1 << 30) : static_cast<int>(c);
+}
+// Items of a request with `len` cached keys and `n` new rows.
+DFA_HD int cache_items(int len, int n, int chunk) {
+  if (n <= 0) return 0;
+  return len <= chunk ? 1 : (len + chunk - 1) / chunk;
+}
+
+// One past the last own key that own row i of n sees: the rows of its block
+// or earlier ones, for positions len + i and blocks of bs tokens from 0.
+DFA_HD int cache_own_end(int len, int i, int n, int bs) {
+  const long long e = ((static_cast<long long>(len) + i) / bs + 1) * bs - len;
+  return e < n ? static_cast<int>(e) : n;
+}
+
+}  // namespace dfa

@@ -1,0 +1,1143 @@
+// Attention of new rows over a paged 8-bit key/value cache and, optionally,
+// over the new rows' own keys and values in bf16: one block of a block
+// diffusion sampler against the clean tokens before it ("Fast Diffusion
+// Attention", "Block diffusion in one picture": a block sees itself and the
+// clean blocks before it).
+//
+// Mathematics.  Row i of request b (position len_b + i) and query head h see
+// the len_b cached tokens and the own rows of its block or earlier blocks:
+//   s_j = scale * q . (k8_j * ks(page of j, head))   cached
+//   s_j = scale * q . k_j                            own
+//   out = sum_j softmax(s)_j v_j,  lse = ln sum_j exp(s_j).
+// k8 is e4m3 and ks a power of two, so k8 converts to f16 exactly and the
+// page's scale multiplies the score.  q is bf16: a row is brought to f16 by a
+// power of two of its own (its largest magnitude lands in [2^14, 2^15)),
+// which keeps every value down to 2^-31 of the row's largest exact.  The
+// probabilities are rounded to f16 (2^-11) for P V while the sums use them
+// unrounded; a value page's scale, relative to the largest one met so far,
+// multiplies its probabilities.  Own keys and values are bf16 products.
+//
+// Work.  All query heads of a key/value head share its keys: row r of a tile
+// is query row r / G and head r % G.  Items are (request, chunk of its cached
+// keys); blocks of x = (key/value head, row tile), y = item.  A block's WK
+// warp groups take 32-key units of the chunk in turn, each with a ring of
+// stages of its own, filled by TMA boxes (32 tokens of one page and head) and
+// with softmax statistics of its own; the groups join through shared memory
+// at the end, the chunks of a request through a float32 workspace and a
+// second launch.  mma.sync fragments are read straight out of the swizzled
+// e4m3 tiles: the head dims (and the keys) may be numbered in any order
+// inside a product, so each thread takes 16 contiguous bytes of a token,
+// which are the operands of four k steps of Q K^T or 16 column tiles of P V.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "cache.cuh"
+#include "dfa.h"
+#include "params.cuh"
+#include "sm100.cuh"
+
+namespace dfa {
+namespace {
+
+constexpr int kUnit = 32;  // keys per unit
+
+struct CacheFwdParams {
+  CUtensorMap tm_k, tm_v;  // (headdim, kv_heads * page_size, pages) bytes
+  const __nv_bfloat16* q;  // (rows, heads, headdim), strided
+  const __nv_bfloat16* k;  // own keys (rows, kv_heads, headdim) or null
+  const __nv_bfloat16* v;
+  long long q_sr, q_sh, k_sr, k_sh, v_sr, v_sh;
+  const float* k_scale;  // (pages, kv_heads)
+  const float* v_scale;
+  const int* block_table;
+  const int* cache_lens;
+  const int* cu_new;
+  __nv_bfloat16* out;  // (rows, heads, headdim)
+  float* lse;          // (heads, rows)
+  float* part_o;       // (items, kv_heads, tile rows of the request, headdim)
+  float* part_lse;     // (items, kv_heads, tile rows of the request), log2
+  unsigned* status;
+  int batch, rows, max_new, H, Hk, G, bs;
+  int page_size, page_shift, num_pages, max_pages;
+  int tiles;    // row tiles per key/value head
+  int target;   // items wanted over all requests
+  int cap;      // items there is room for
+  int part_rows;  // rows of a partial result: tiles * tile rows
+  float scale_log2;
+};
+
+// One request's sizes, checked: a length past its table or rows past the
+// packed ones are errors, and the request is then taken as empty.
+struct Request {
+  int len, row0, n;
+};
+__device__ __forceinline__ Request load_request(const CacheFwdParams& p, int b, bool* bad) {
+  const int len = p.cache_lens[b], r0 = p.cu_new[b], r1 = p.cu_new[b + 1];
+  const bool ok = len >= 0 && len <= p.max_pages * p.page_size && r0 >= 0 && r1 >= r0 &&
+                  r1 <= p.rows && r1 - r0 <= p.max_new;
+  if (!ok) {
+    *bad = true;
+    return {0, 0, 0};
+  }
+  return {len, r0, r1 - r0};
+}
+
+// The split of the launch, found by every warp for itself: chunk from the
+// sum of the lengths, then the request that item x falls to.
+struct Item {
+  int b, split, splits, base;  // request, its chunk and number of chunks, its first item
+  int chunk, total;            // keys per chunk; items in all
+  Request rq;
+};
+__device__ __forceinline__ Item find_item(const CacheFwdParams& p, int x, bool* bad) {
+  const int lane = threadIdx.x & 31;
+  const int per = (p.batch + 31) / 32;
+  const int b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long keys = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(p, b, bad);
+    if (r.n > 0) keys += r.len;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, off);
+  Item it;
+  it.chunk = cache_chunk(keys, p.target);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(p, b, bad);
+    mine += cache_items(r.len, r.n, it.chunk);
+  }
+  int upto = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, upto, off);
+    if (lane >= off) upto += o;
+  }
+  it.total = min(__shfl_sync(0xffffffffu, upto, 31), p.cap);
+  it.b = -1;
+  if (x >= it.total) return it;
+  int at = upto - mine;
+  int fb = -1, fsplit = 0, fsplits = 0, fbase = 0;
+  Request frq = {0, 0, 0};
+  if (x >= at && x < upto) {
+    for (int b = b0; b < b1; ++b) {
+      const Request r = load_request(p, b, bad);
+      const int items = cache_items(r.len, r.n, it.chunk);
+      if (x < at + items) {
+        fb = b, fsplit = x - at, fsplits = items, fbase = at, frq = r;
+        break;
+      }
+      at += items;
+    }
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, fb >= 0)) - 1;
+  it.b = __shfl_sync(0xffffffffu, fb, src);
+  it.split = __shfl_sync(0xffffffffu, fsplit, src);
+  it.splits = __shfl_sync(0xffffffffu, fsplits, src);
+  it.base = __shfl_sync(0xffffffffu, fbase, src);
+  it.rq.len = __shfl_sync(0xffffffffu, frq.len, src);
+  it.rq.row0 = __shfl_sync(0xffffffffu, frq.row0, src);
+  it.rq.n = __shfl_sync(0xffffffffu, frq.n, src);
+  return it;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// D (16 x 8, float32) += A (16 x 16) B (16 x 8).
+__device__ __forceinline__ void mma_f16(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 values (low / high half of w) as f16, exact.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  ld_shared_v4(addr, v.x, v.y, v.z, v.w);
+  return v;
+}
+__device__ __forceinline__ float pow2_bits(int e) { return __int_as_float((e + 127) << 23); }
+
+// Probabilities are 2^(s - m + kShift); the reference maximum m follows a
+// new maximum only when that exceeds it by more than kSlack, so that most
+// units rescale nothing.  kShift + kSlack < 16 keeps f16 probabilities
+// finite, and kShift moves f16's smallest subnormal to 2^-30 of the maximum.
+constexpr float kShift = 6.f;
+constexpr float kSlack = 8.f;
+
+template <int D, int MT, int WR, int WK, int STAGES>
+struct CacheTile {
+  static constexpr int kThreads = 32 * WR * WK;
+  static constexpr int kRows = 16 * MT * WR;
+  static constexpr int kUnitBytes = kUnit * D;  // of k, and of v
+  static constexpr int kRing = WK * STAGES * 2 * kUnitBytes;
+  static constexpr int kFrags = (D / 64) * 4;  // k steps of Q K^T
+  static constexpr int kQ = WR * MT * kFrags * 512;
+  static constexpr int kPitch = D + 4;  // floats per row of a group's output at the join
+  static constexpr int kJoin = WK * kRows * kPitch * 4;
+  static constexpr int kArea = kRing > kJoin ? kRing : kJoin;
+  // ring (1024-byte aligned) | q fragments | row factors | statistics | barriers
+  static constexpr int kOffQ = kArea;
+  static constexpr int kOffFactor = kOffQ + kQ;
+  static constexpr int kOffStat = kOffFactor + kRows * 4;  // m, l per group and row
+  static constexpr int kOffC = kOffStat + WK * kRows * 8;
+  static constexpr int kOffBar = (kOffC + WK * WR * 4 + 7) / 8 * 8;
+  static constexpr int kOffFlag = kOffBar + WK * STAGES * 16;
+  static constexpr int kSmem = kOffFlag + 16 + 1024;
+};
+
+// 16-byte chunk c of token row r inside a TMA tile: the tile's swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int c) {
+  if constexpr (D == 64) return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return base + (c >> 3) * (kUnit * 128) + r * 128 + (((c ^ r) & 7) << 4);
+}
+
+// Keys of a fragment column pair.  headdim 64 numbers the eight keys of a
+// column tile in order; wider heads put keys t and t + 4 into columns 2t and
+// 2t + 1, so that the eight lanes of a shared-memory phase (two keys, four
+// chunks) fall on different banks under the 128-byte swizzle.
+template <int D>
+__device__ __forceinline__ int key_of(int n) {
+  return D == 64 ? n : (n >> 1) + 4 * (n & 1);
+}
+
+template <int D, int MT, int WR, int WK, int STAGES>
+__global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
+    dfa_cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
+  using T = CacheTile<D, MT, WR, WK, STAGES>;
+  constexpr int kSeg = D / 64;       // 64-dim segments of Q K^T
+  constexpr int kCols = D == 64 ? 8 : 16;  // column tiles of P V per value load
+  constexpr int kHalf = D == 256 ? 2 : 1;  // value loads per key
+  constexpr int kOut = kCols * kHalf;      // column tiles of the output, D / 8
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (smem0 - smem_u32(smem_raw));
+  float* s_factor = reinterpret_cast<float*>(smem + T::kOffFactor);
+  float* s_m = reinterpret_cast<float*>(smem + T::kOffStat);
+  float* s_l = s_m + WK * T::kRows;
+  float* s_c = reinterpret_cast<float*>(smem + T::kOffC);
+  volatile int* s_flag = reinterpret_cast<volatile int*>(smem + T::kOffFlag);
+  const uint32_t bars = smem0 + T::kOffBar;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int wr = warp % WR, wk = warp / WR;
+
+  if (tid == 0) {
+    for (int i = 0; i < WK * STAGES; ++i) {
+      mbar_init(bars + 16 * i, 1);       // full
+      mbar_init(bars + 16 * i + 8, WR);  // empty
+    }
+    fence_mbar_init();
+    *s_flag = 0;
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  bool bad = false;
+  const Item it = find_item(p, blockIdx.y, &bad);
+  if (bad) atomicOr(p.status, kStatusIndex);
+  if (it.b < 0) return;  // the whole block
+  const int h = blockIdx.x / p.tiles, tile = blockIdx.x - h * p.tiles;
+  const int R = it.rq.n * p.G;  // rows of the request and key/value head
+  const int row_base = tile * T::kRows;
+  if (row_base >= R) return;
+  const int key_lo = it.split * it.chunk;
+  const int key_hi = min(it.rq.len, key_lo + it.chunk);
+  const int units = key_hi > key_lo ? (key_hi - key_lo + kUnit - 1) / kUnit : 0;
+  __syncthreads();  // barriers initialised
+  const AbortFlag ab{const_cast<int*>(s_flag), p.status};
+
+  // The units of this group: wk, wk + WK, ...  Lane l keeps the pages and
+  // scales of the group's units 32 i + l; a unit of a 16-token page spans two.
+  const int my_units = units > wk ? (units - wk + WK - 1) / WK : 0;
+  const bool two = p.page_size < kUnit;
+  const int* table = p.block_table + static_cast<long long>(it.b) * p.max_pages;
+  auto load_pages = [&](int u, int* page) {  // of the group's u-th unit
+    page[0] = page[1] = -1;
+    if (u >= my_units) return;
+    const int key = key_lo + (wk + u * WK) * kUnit;
+    page[0] = table[key >> p.page_shift];
+    if (two && key + 16 < key_hi) page[1] = table[(key + 16) >> p.page_shift];
+    if (!cache_page_ok(page[0], p.num_pages) ||
+        (two && key + 16 < key_hi && !cache_page_ok(page[1], p.num_pages)))
+      atomicOr(p.status, kStatusIndex);
+    if (!two) page[1] = page[0];
+  };
+  auto load_scales = [&](const int* page, float* ks, float* vs) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool ok = cache_page_ok(page[i], p.num_pages);
+      const long long at = static_cast<long long>(page[i]) * p.Hk + h;
+      ks[i] = ok ? p.k_scale[at] : 0.f;
+      vs[i] = ok ? p.v_scale[at] : 0.f;
+    }
+  };
+  const uint32_t ring = smem0 + wk * STAGES * 2 * T::kUnitBytes;
+  const uint32_t gbar = bars + 16 * wk * STAGES;
+  // Lane 0 of the group's first warp fills stage s with a unit's boxes.
+  auto issue = [&](int u, int s, int page0, int page1) {
+    const uint32_t dst = ring + s * 2 * T::kUnitBytes, bar = gbar + 16 * s;
+    const int key = key_lo + (wk + u * WK) * kUnit;
+    const bool ok0 = cache_page_ok(page0, p.num_pages);
+    const bool ok1 = two && cache_page_ok(page1, p.num_pages);
+    const int rows = two ? 16 : kUnit;
+    const uint32_t bytes = (ok0 ? rows * D * 2 : 0) + (ok1 ? rows * D * 2 : 0);
+    mbar_arrive_expect_tx(bar, bytes);
+    const int off = h * p.page_size + (key & (p.page_size - 1));
+#pragma unroll
+    for (int half = 0; half < kHalf; ++half) {
+      const uint32_t d = dst + half * kUnit * 128;
+      if (ok0) {
+        tma_load_3d(d, &p.tm_k, bar, half * 128, off, page0);
+        tma_load_3d(d + T::kUnitBytes, &p.tm_v, bar, half * 128, off, page0);
+      }
+      if (ok1) {
+        constexpr int kRow = D == 64 ? 64 : 128;
+        const int off1 = h * p.page_size + ((key + 16) & (p.page_size - 1));
+        tma_load_3d(d + 16 * kRow, &p.tm_k, bar, half * 128, off1, page1);
+        tma_load_3d(d + T::kUnitBytes + 16 * kRow, &p.tm_v, bar, half * 128, off1, page1);
+      }
+    }
+  };
+  static_assert(STAGES < 16, "the next pages are read 24 units ahead");
+  int page[2], next_page[2] = {-1, -1};
+  float ks[2], vs[2], next_ks[2] = {0.f, 0.f}, next_vs[2] = {0.f, 0.f};
+  load_pages(lane, page);
+  if (wr == 0) {
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      const int p0 = __shfl_sync(0xffffffffu, page[0], s);
+      const int p1 = __shfl_sync(0xffffffffu, page[1], s);
+      if (lane == 0 && s < my_units) issue(s, s, p0, p1);
+    }
+  }
+  load_scales(page, ks, vs);
+
+  // Q fragments of the tile, built by the first group: f16 after the row's
+  // power of two, in the order the products read them.
+  if (wk == 0) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      int e[2];
+      uint4 w[2][kSeg][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+        unsigned top = 0;
+#pragma unroll
+        for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) w[i][sg][c] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < R) {
+          const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
+          const __nv_bfloat16* src = p.q + (it.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 16 * t;
+#pragma unroll
+          for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              w[i][sg][c] = *reinterpret_cast<const uint4*>(src + 64 * sg + 8 * c);
+        }
+#pragma unroll
+        for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t v[4] = {w[i][sg][c].x, w[i][sg][c].y, w[i][sg][c].z, w[i][sg][c].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const unsigned lo = v[x] & 0x7fffu, hi = (v[x] >> 16) & 0x7fffu;
+              top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            }
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e brings the row's largest magnitude into [2^14, 2^15)
+        e[i] = static_cast<int>(top >> 7) - 127 - 14;
+        if (e[i] < -100) e[i] = -100;
+        if (t == 0) s_factor[16 * (wr * MT + mt) + g + 8 * i] = pow2_bits(e[i]) * p.scale_log2;
+      }
+      const float inv[2] = {pow2_bits(-e[0]), pow2_bits(-e[1])};
+#pragma unroll
+      for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t a[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4& q4 = w[i][sg][s >> 1];
+            const uint32_t x0 = s & 1 ? q4.z : q4.x, x1 = s & 1 ? q4.w : q4.y;
+            a[i][0] = pack_f16x2(__uint_as_float(x0 << 16) * inv[i],
+                                 __uint_as_float(x0 & 0xffff0000u) * inv[i]);
+            a[i][1] = pack_f16x2(__uint_as_float(x1 << 16) * inv[i],
+                                 __uint_as_float(x1 & 0xffff0000u) * inv[i]);
+          }
+          const uint32_t at =
+              smem0 + T::kOffQ + (((wr * MT + mt) * T::kFrags + sg * 4 + s) * 32 + lane) * 16;
+          st_shared_v4(at, a[0][0], a[1][0], a[0][1], a[1][1]);
+        }
+    }
+  }
+  __syncthreads();
+
+  float o[MT][kOut][4];
+  float m[MT][2], l[MT][2], factor[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m[mt][i] = -INFINITY;
+      l[mt][i] = 0.f;
+      factor[mt][i] = s_factor[16 * (wr * MT + mt) + g + 8 * i];
+    }
+#pragma unroll
+    for (int e = 0; e < kOut; ++e)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[mt][e][x] = 0.f;
+  }
+  float c = pow2_bits(kCacheMinExp);  // the output's unit: the largest value scale so far
+  float inv_c = pow2_bits(-kCacheMinExp);
+  const uint32_t qbase = smem0 + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
+
+  // New maxima of a unit's scaled scores: returns the factors the output and
+  // the sums shrink by (1 where the reference stays).
+  auto rebase = [&](const float (&um)[MT][2], float c_new) {
+    float shrink[MT][2];
+    bool any = false;
+    float cr = 1.f;
+    if (c_new != c) {
+      cr = c / c_new;
+      c = c_new;
+      inv_c = 1.f / c;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x = um[mt][i];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        float a = 1.f;
+        if (x > m[mt][i] + kSlack) {  // also the first finite maximum
+          a = ex2_approx(m[mt][i] - x);
+          m[mt][i] = x;
+          l[mt][i] *= a;
+        }
+        shrink[mt][i] = a * cr;
+        any = any || shrink[mt][i] != 1.f;
+      }
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) {
+          o[mt][e][0] *= shrink[mt][0];
+          o[mt][e][1] *= shrink[mt][0];
+          o[mt][e][2] *= shrink[mt][1];
+          o[mt][e][3] *= shrink[mt][1];
+        }
+    }
+  };
+
+  int done = 0;  // units finished
+  for (; done < my_units; ++done) {
+    const int u = done, stage = u % STAGES;
+    const uint32_t phase = (u / STAGES) & 1;
+    // the next 32 units' pages and scales, read ahead of their use
+    if ((u & 31) == 8) load_pages(u + 24 + lane, next_page);
+    if ((u & 31) == 12) load_scales(next_page, next_ks, next_vs);
+    if ((u & 31) == 0 && u > 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) page[i] = next_page[i], ks[i] = next_ks[i], vs[i] = next_vs[i];
+    }
+    float ks0 = __shfl_sync(0xffffffffu, ks[0], u & 31);
+    float ks1 = __shfl_sync(0xffffffffu, ks[1], u & 31);
+    const float vs0 = __shfl_sync(0xffffffffu, vs[0], u & 31);
+    const float vs1 = __shfl_sync(0xffffffffu, vs[1], u & 31);
+    const int p0 = __shfl_sync(0xffffffffu, page[0], u & 31);
+    const int p1 = __shfl_sync(0xffffffffu, page[1], u & 31);
+    const int key = key_lo + (wk + u * WK) * kUnit;
+    // valid keys of the unit's 16-key halves
+    const int nv0 = cache_page_ok(p0, p.num_pages) ? min(16, key_hi - key) : 0;
+    const int nv1 = cache_page_ok(p1, p.num_pages) ? max(0, min(16, key_hi - key - 16)) : 0;
+    const uint32_t kt = ring + stage * 2 * T::kUnitBytes, vt = kt + T::kUnitBytes;
+    if (!mbar_wait_warp(gbar + 16 * stage, phase, ab)) break;
+
+    float sc[MT][4][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
+#pragma unroll
+    for (int sg = 0; sg < kSeg; ++sg) {
+      uint4 kw[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        kw[n] = lds128(tile_addr<D>(kt, 8 * n + key_of<D>(g), 4 * sg + t));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t b[4][2];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t w = s == 0 ? kw[n].x : s == 1 ? kw[n].y : s == 2 ? kw[n].z : kw[n].w;
+          b[n][0] = e4m3_lo(w);
+          b[n][1] = e4m3_hi(w);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 a = lds128(qbase + (mt * T::kFrags + sg * 4 + s) * 512);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) mma_f16(sc[mt][n], a, b[n][0], b[n][1]);
+        }
+      }
+    }
+    const bool whole = nv0 == 16 && nv1 == 16;
+    float um[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float ksn = n < 2 ? ks0 : ks1;
+        const int nv = n < 2 ? nv0 : nv1;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          sc[mt][n][x] *= factor[mt][x >> 1] * ksn;
+          if (!whole && 8 * (n & 1) + key_of<D>(2 * t + (x & 1)) >= nv) sc[mt][n][x] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        um[mt][i] = fmaxf(
+            fmax3(fmaxf(sc[mt][0][2 * i], sc[mt][0][2 * i + 1]), sc[mt][1][2 * i],
+                  sc[mt][1][2 * i + 1]),
+            fmax3(fmaxf(sc[mt][2][2 * i], sc[mt][2][2 * i + 1]), sc[mt][3][2 * i],
+                  sc[mt][3][2 * i + 1]));
+    }
+    rebase(um, fmaxf(c, fmaxf(vs0, vs1)));
+    const float w0 = vs0 * inv_c, w1 = vs1 * inv_c;
+    uint4 pf[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      // a row that has met no finite score keeps probabilities of 0
+      const float r0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kShift;
+      const float r1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kShift;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float wn = n < 2 ? w0 : w1;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float e = ex2_approx(sc[mt][n][x] - (x < 2 ? r0 : r1));
+          l[mt][x >> 1] += e;
+          sc[mt][n][x] = e * wn;
+        }
+      }
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        pf[mt][kk] = make_uint4(pack_f16x2(sc[mt][2 * kk][0], sc[mt][2 * kk][1]),
+                                pack_f16x2(sc[mt][2 * kk][2], sc[mt][2 * kk][3]),
+                                pack_f16x2(sc[mt][2 * kk + 1][0], sc[mt][2 * kk + 1][1]),
+                                pack_f16x2(sc[mt][2 * kk + 1][2], sc[mt][2 * kk + 1][3]));
+    }
+    // P V: the four keys of a thread's fragment rows, 16 dims each (headdim
+    // 64: 8).  What lies behind the last key may be anything, NaN included,
+    // and is replaced by zero.
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int nv = kk == 0 ? nv0 : nv1;
+#pragma unroll
+      for (int half = 0; half < kHalf; ++half) {
+        uint32_t vw[4][kCols / 4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 8 * (x >> 1) + key_of<D>(2 * t + (x & 1));
+          if constexpr (D == 64) {
+            const uint32_t at = tile_addr<D>(vt, 16 * kk + r, g >> 1) + 8 * (g & 1);
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(vw[x][0]), "=r"(vw[x][1])
+                         : "r"(at)
+                         : "memory");
+          } else {
+            const uint4 w = lds128(tile_addr<D>(vt, 16 * kk + r, 8 * half + key_of<D>(g)));
+            vw[x][0] = w.x, vw[x][1] = w.y, vw[x][2] = w.z, vw[x][3] = w.w;
+          }
+          if (!whole && r >= nv) {
+#pragma unroll
+            for (int y = 0; y < kCols / 4; ++y) vw[x][y] = 0u;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < kCols / 4; ++y) {
+          const uint32_t lo0 = __byte_perm(vw[0][y], vw[1][y], 0x5140);
+          const uint32_t hi0 = __byte_perm(vw[0][y], vw[1][y], 0x7362);
+          const uint32_t lo1 = __byte_perm(vw[2][y], vw[3][y], 0x5140);
+          const uint32_t hi1 = __byte_perm(vw[2][y], vw[3][y], 0x7362);
+          const uint32_t b[4][2] = {{e4m3_lo(lo0), e4m3_lo(lo1)},
+                                    {e4m3_hi(lo0), e4m3_hi(lo1)},
+                                    {e4m3_lo(hi0), e4m3_lo(hi1)},
+                                    {e4m3_hi(hi0), e4m3_hi(hi1)}};
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              mma_f16(o[mt][half * kCols + 4 * y + z], pf[mt][kk], b[z][0], b[z][1]);
+        }
+      }
+    }
+    mbar_arrive_warp(gbar + 16 * stage + 8);
+    // refill the stage
+    const int nu = u + STAGES;
+    if (wr == 0 && nu < my_units) {
+      const bool ahead = (nu >> 5) != (u >> 5);
+      const int n0 = __shfl_sync(0xffffffffu, ahead ? next_page[0] : page[0], nu & 31);
+      const int n1 = __shfl_sync(0xffffffffu, ahead ? next_page[1] : page[1], nu & 31);
+      if (!mbar_wait_warp(gbar + 16 * stage + 8, phase, ab)) break;
+      if (lane == 0) issue(nu, stage, n0, n1);
+    }
+  }
+  if (done < my_units && wr == 0 && lane == 0) {
+    // Giving up: nothing may land in shared memory after the block is gone.
+    for (int s = 0; s < STAGES; ++s) {
+      int last = -1;  // last unit that may have been issued to this stage
+      for (int u = s; u < my_units && u < done + 1 + STAGES; u += STAGES) last = u;
+      if (last >= 0) mbar_wait_limited(gbar + 16 * s, (last / STAGES) & 1, kWaitLimitNs / 8);
+    }
+  }
+
+  // Own keys and values, bf16, with the request's last chunk: units of 16
+  // keys, the groups in turn, operands straight from global memory.
+  if (p.k != nullptr && it.split == it.splits - 1) {
+    const int last_tok = min(R - 1, row_base + T::kRows - 1) / p.G;
+    const int own = cache_own_end(it.rq.len, last_tok, it.rq.n, p.bs);
+    for (int k0 = 16 * wk; k0 < own; k0 += 16 * WK) {
+      float sc[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
+#pragma unroll
+      for (int sg = 0; sg < kSeg; ++sg) {
+        uint4 kw[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = k0 + 8 * n + g;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            kw[n][x] = make_uint4(0u, 0u, 0u, 0u);
+            if (key < it.rq.n)
+              kw[n][x] = *reinterpret_cast<const uint4*>(
+                  p.k + (it.rq.row0 + key) * p.k_sr + h * p.k_sh + 64 * sg + 16 * t + 8 * x);
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint4 w[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+            const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              w[i][x] = make_uint4(0u, 0u, 0u, 0u);
+              if (r < R)
+                w[i][x] = *reinterpret_cast<const uint4*>(
+                    p.q + (it.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 64 * sg + 16 * t + 8 * x);
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint4 a = s & 1 ? make_uint4(w[0][s >> 1].z, w[1][s >> 1].z, w[0][s >> 1].w,
+                                               w[1][s >> 1].w)
+                                  : make_uint4(w[0][s >> 1].x, w[1][s >> 1].x, w[0][s >> 1].y,
+                                               w[1][s >> 1].y);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              mma_bf16(sc[mt][n], a, s & 1 ? kw[n][s >> 1].z : kw[n][s >> 1].x,
+                       s & 1 ? kw[n][s >> 1].w : kw[n][s >> 1].y);
+          }
+        }
+      }
+      float um[MT][2];
+      int end[MT][2];  // one past the last own key of the thread's rows
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+          end[mt][i] = r < R ? cache_own_end(it.rq.len, r / p.G, it.rq.n, p.bs) : 0;
+          um[mt][i] = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float& s = sc[mt][n][2 * i + x];
+              s = k0 + 8 * n + 2 * t + x < end[mt][i] ? s * p.scale_log2 : -INFINITY;
+              um[mt][i] = fmaxf(um[mt][i], s);
+            }
+        }
+      rebase(um, fmaxf(c, 1.f));
+      uint4 pf[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float r0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kShift;
+        const float r1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kShift;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float e = ex2_approx(sc[mt][n][x] - (x < 2 ? r0 : r1));
+            l[mt][x >> 1] += e;
+            sc[mt][n][x] = e * inv_c;
+          }
+        pf[mt] = make_uint4(pack_bf16x2(sc[mt][0][0], sc[mt][0][1]),
+                            pack_bf16x2(sc[mt][0][2], sc[mt][0][3]),
+                            pack_bf16x2(sc[mt][1][0], sc[mt][1][1]),
+                            pack_bf16x2(sc[mt][1][2], sc[mt][1][3]));
+      }
+      // A row's probability of an own key it does not see is 0, but 0 times a
+      // value that is not finite is not: such values leave the product and
+      // are added to the rows that see them.
+      bool odd = false;
+#pragma unroll
+      for (int half = 0; half < kHalf; ++half)
+#pragma unroll
+        for (int part = 0; part < kCols / 8; ++part) {  // 8 dims at a time
+          uint32_t vw[4][4];
+          const int dim = D == 64 ? 8 * g : 128 * half + 16 * key_of<D>(g) + 8 * part;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = k0 + 8 * (x >> 1) + 2 * t + (x & 1);
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (key < it.rq.n)
+              w = *reinterpret_cast<const uint4*>(p.v + (it.rq.row0 + key) * p.v_sr + h * p.v_sh +
+                                                  dim);
+            vw[x][0] = w.x, vw[x][1] = w.y, vw[x][2] = w.z, vw[x][3] = w.w;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if ((vw[x][y] & 0x7f80u) == 0x7f80u) vw[x][y] &= 0xffff0000u, odd = true;
+              if ((vw[x][y] & 0x7f800000u) == 0x7f800000u) vw[x][y] &= 0xffffu, odd = true;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t b0 = __byte_perm(vw[0][y], vw[1][y], z ? 0x7632 : 0x5410);
+              const uint32_t b1 = __byte_perm(vw[2][y], vw[3][y], z ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt], b0, b1);
+            }
+          }
+        }
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+        for (int key = k0; key < min(k0 + 16, it.rq.n); ++key) {
+          const __nv_bfloat16* src = p.v + (it.rq.row0 + key) * p.v_sr + h * p.v_sh;
+#pragma unroll
+          for (int e = 0; e < kOut; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float y = __bfloat162float(
+                  src[128 * (e / kCols) + kCols * key_of<D>(2 * t + x) + e % kCols]);
+              if (isfinite(y)) continue;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (key < end[mt][i]) o[mt][e][2 * i + x] += y;
+            }
+        }
+      }
+    }
+  }
+
+  // Join the groups: statistics first, then each group's output in a common
+  // unit, summed.
+  if (t == 0) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s_m[wk * T::kRows + 16 * (wr * MT + mt) + g + 8 * i] = m[mt][i];
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 1);
+      l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
+    }
+  if (lane == 0) s_c[warp] = c;
+  __syncthreads();  // statistics written; every tile of the ring has been read
+  float c_all = s_c[0];
+#pragma unroll
+  for (int i = 1; i < WK * WR; ++i) c_all = fmaxf(c_all, s_c[i]);
+  float* join = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 16 * (wr * MT + mt) + g + 8 * i;
+      float top = s_m[r];
+#pragma unroll
+      for (int x = 1; x < WK; ++x) top = fmaxf(top, s_m[x * T::kRows + r]);
+      const float f = m[mt][i] == -INFINITY ? 0.f : ex2_approx(m[mt][i] - top);
+      const float fo = f * (c / c_all);
+      if (t == 0) s_l[wk * T::kRows + r] = l[mt][i] * f;
+      float* dst = join + (wk * T::kRows + r) * T::kPitch;
+      // columns 2t and 2t + 1 of the column tiles are runs of kCols dims
+#pragma unroll
+      for (int half = 0; half < kHalf; ++half)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int dim = 128 * half + kCols * key_of<D>(2 * t + x);
+#pragma unroll
+          for (int e = 0; e < kCols; e += 4)
+            *reinterpret_cast<float4*>(dst + dim + e) =
+                make_float4(o[mt][half * kCols + e][2 * i + x] * fo,
+                            o[mt][half * kCols + e + 1][2 * i + x] * fo,
+                            o[mt][half * kCols + e + 2][2 * i + x] * fo,
+                            o[mt][half * kCols + e + 3][2 * i + x] * fo);
+        }
+    }
+  __syncthreads();
+  const bool single = it.splits == 1;
+  for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
+    const int r = i / (D / 4), d4 = i - r * (D / 4);
+    if (row_base + r >= R) break;
+    float sum = 0.f, top = -INFINITY;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < WK; ++x) {
+      sum += s_l[x * T::kRows + r];
+      top = fmaxf(top, s_m[x * T::kRows + r]);
+      const float4 y =
+          *reinterpret_cast<const float4*>(join + (x * T::kRows + r) * T::kPitch + 4 * d4);
+      a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+    }
+    // no key (sum 0): output 0 and -inf; scores that are not numbers: NaN
+    const bool none = top == -INFINITY && sum == 0.f;
+    const float inv = none ? 0.f : c_all / sum;
+    const float lse2 = none ? -INFINITY : top - kShift + lg2_approx(sum);
+    a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
+    if (single) {
+      const int tok = (row_base + r) / p.G, hq = h * p.G + (row_base + r - tok * p.G);
+      const long long row = it.rq.row0 + tok;
+      *reinterpret_cast<uint2*>(p.out + (row * p.H + hq) * D + 4 * d4) =
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      if (d4 == 0) p.lse[static_cast<long long>(hq) * p.rows + row] = lse2 * 0.6931471805599453f;
+    } else {
+      const long long at =
+          (static_cast<long long>(blockIdx.y) * p.Hk + h) * p.part_rows + row_base + r;
+      *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
+      if (d4 == 0) p.part_lse[at] = lse2;
+    }
+  }
+}
+
+// The chunks of a request, joined: weights 2^(lse_s - max), one warp a row
+// and query head, the chunks' outputs read once.  Blocks stride over the rows
+// of the requests that were split; nothing to do where none was.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    dfa_cache_join_kernel(const __grid_constant__ CacheFwdParams p) {
+  constexpr int kVec = D / 32;  // floats per lane
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool bad = false;
+  const int per = (p.batch + 31) / 32;
+  const int b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
+  const int chunk = find_item(p, 0x7fffffff, &bad).chunk;
+  // lane's share of the items and of the rows to join
+  int items = 0;
+  long long rows = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(p, b, &bad);
+    const int n = cache_items(r.len, r.n, chunk);
+    items += n;
+    if (n > 1) rows += static_cast<long long>(r.n) * p.H;
+  }
+  int items_upto = items;
+  long long rows_upto = rows;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, items_upto, off);
+    const long long c = __shfl_up_sync(0xffffffffu, rows_upto, off);
+    if (lane >= off) items_upto += a, rows_upto += c;
+  }
+  const long long total = __shfl_sync(0xffffffffu, rows_upto, 31);
+  for (long long w = static_cast<long long>(blockIdx.x) * kJoinWarps + warp; w < total;
+       w += static_cast<long long>(gridDim.x) * kJoinWarps) {
+    // the request of row w
+    int fb = -1, fbase = 0, fitems = 0, fin = 0;
+    Request frq = {0, 0, 0};
+    if (w >= rows_upto - rows && w < rows_upto) {
+      long long at = rows_upto - rows;
+      int base = items_upto - items;
+      for (int b = b0; b < b1; ++b) {
+        const Request r = load_request(p, b, &bad);
+        const int n = cache_items(r.len, r.n, chunk);
+        const long long mine = n > 1 ? static_cast<long long>(r.n) * p.H : 0;
+        if (w < at + mine) {
+          fb = b, fbase = base, fitems = n, frq = r, fin = static_cast<int>(w - at);
+          break;
+        }
+        at += mine;
+        base += n;
+      }
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, fb >= 0)) - 1;
+    const int base = __shfl_sync(0xffffffffu, fbase, src);
+    const int n = __shfl_sync(0xffffffffu, fitems, src);
+    const int in = __shfl_sync(0xffffffffu, fin, src);
+    const int row0 = __shfl_sync(0xffffffffu, frq.row0, src);
+    const int tok = in / p.H, hq = in - tok * p.H, h = hq / p.G;
+    const long long first = (static_cast<long long>(base) * p.Hk + h) * p.part_rows +
+                            tok * p.G + (hq - h * p.G);
+    const long long step = static_cast<long long>(p.Hk) * p.part_rows;
+    float top = -INFINITY;
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, p.part_lse[first + s * step]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float wgt = ex2_approx(p.part_lse[first + s * step] - ref);
+      sum += wgt;
+      const float* src_o = p.part_o + (first + s * step) * D + lane * kVec;
+      float x[kVec];
+      if constexpr (kVec == 2) {
+        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src_o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4)
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(src_o + i);
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(wgt, x[i], acc[i]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long row = row0 + tok;
+    __nv_bfloat16* dst = p.out + (row * p.H + hq) * D + lane * kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2)
+      *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0)
+      p.lse[static_cast<long long>(hq) * p.rows + row] =
+          sum == 0.f ? -INFINITY : (ref + lg2_approx(sum)) * 0.6931471805599453f;
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// The launch's shape for given sizes: tile rows, row tiles, item target and
+// room, blocks resident on the device.
+struct CachePlan {
+  int tile_rows, tiles, target, cap;
+};
+CachePlan cache_plan_for(int batch, int max_new, int G, int Hk, int d, int sms) {
+  CachePlan c;
+  const long long rows = static_cast<long long>(max_new) * G;
+  c.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  c.tiles = static_cast<int>((rows + c.tile_rows - 1) / c.tile_rows);
+  const int resident = sms * (d == 256 ? 1 : 2);
+  // about two waves of blocks, so that the blocks of a ragged batch even out
+  long long target = 2LL * resident / (static_cast<long long>(Hk) * c.tiles);
+  if (target < 1) target = 1;
+  c.target = static_cast<int>(target);
+  c.cap = c.target + batch;
+  return c;
+}
+
+template <int D, int MT, int WR, int WK, int STAGES>
+cudaError_t launch_cache_tile(const CacheFwdParams& p, cudaStream_t stream) {
+  using T = CacheTile<D, MT, WR, WK, STAGES>;
+  auto kern = dfa_cache_fwd_kernel<D, MT, WR, WK, STAGES>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, dim3(p.Hk * p.tiles, p.cap), dim3(T::kThreads), T::kSmem, stream, p);
+}
+
+template <int D>
+cudaError_t launch_cache_rows(const CacheFwdParams& p, int tile_rows, cudaStream_t stream) {
+  if constexpr (D == 256) {
+    if (tile_rows == 16) return launch_cache_tile<D, 1, 1, 4, 2>(p, stream);
+    if (tile_rows == 32) return launch_cache_tile<D, 1, 2, 4, 2>(p, stream);
+    return launch_cache_tile<D, 1, 4, 2, 4>(p, stream);
+  } else {
+    constexpr int kDeep = D == 64 ? 2 : 1;
+    if (tile_rows == 16) return launch_cache_tile<D, 1, 1, 4, 3 * kDeep>(p, stream);
+    if (tile_rows == 32) return launch_cache_tile<D, 2, 1, 4, 3 * kDeep>(p, stream);
+    return launch_cache_tile<D, 2, 2, 2, 5 * kDeep>(p, stream);
+  }
+}
+
+int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim) {
+  if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
+      max_new > (1 << 24) || heads < 1 || heads > (1 << 16) || kv_heads < 1 || kv_heads > heads ||
+      heads % kv_heads)
+    return DFA_EINVAL;
+  if (headdim != 64 && headdim != 128 && headdim != 256) return DFA_EUNSUPPORTED;
+  return DFA_OK;
+}
+
+}  // namespace
+}  // namespace dfa
+
+using namespace dfa;
+
+extern "C" {
+
+long long dfa_cache_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
+                                    int headdim) {
+  if (const int rc = check_cache_sizes(batch, rows, max_new, heads, kv_heads, headdim)) return rc;
+  if (batch == 0 || rows == 0 || max_new == 0) return 0;
+  DeviceInfo di;
+  if (const int rc = device_info(&di)) return rc;
+  if (max_new > rows) max_new = rows;
+  const CachePlan c = cache_plan_for(batch, max_new, heads / kv_heads, kv_heads, headdim, di.sms);
+  return static_cast<long long>(c.cap) * kv_heads * c.tiles * c.tile_rows * (headdim + 1) * 4;
+}
+
+int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k_cache,
+                      const void* v_cache, const float* k_scale, const float* v_scale,
+                      const int* block_table, const int* cache_lens, const int* cu_new, void* out,
+                      float* lse, void* workspace, long long workspace_bytes, int batch, int rows,
+                      int max_new, int heads, int kv_heads, int headdim, int block_size,
+                      int page_size, int num_pages, int max_pages, const long long* q_strides,
+                      const long long* k_strides, const long long* v_strides,
+                      dfa_stream_t stream) {
+  if (const int rc = check_cache_sizes(batch, rows, max_new, heads, kv_heads, headdim)) return rc;
+  if (block_size < 1 || num_pages < 1 || max_pages < 1 ||
+      (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
+      static_cast<long long>(max_pages) * page_size > (1 << 30))
+    return DFA_EINVAL;
+  if (batch == 0 || rows == 0 || max_new == 0) return DFA_OK;
+  auto aligned = [](const void* x, unsigned n) {
+    return x && (reinterpret_cast<uintptr_t>(x) & (n - 1)) == 0;
+  };
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(block_table, 4) || !aligned(cache_lens, 4) || !aligned(cu_new, 4) ||
+      !aligned(workspace, 16) || (k == nullptr) != (v == nullptr) ||
+      (k && (!aligned(k, 16) || !aligned(v, 16))))
+    return DFA_EINVAL;
+  DeviceInfo di;
+  if (const int rc = device_info(&di)) return rc;
+  if (max_new > rows) max_new = rows;
+  const int G = heads / kv_heads, d = headdim;
+  const CachePlan c = cache_plan_for(batch, max_new, G, kv_heads, d, di.sms);
+  const long long part_rows = static_cast<long long>(c.tiles) * c.tile_rows;
+  const long long parts = static_cast<long long>(c.cap) * kv_heads * part_rows;
+  if (workspace_bytes < parts * (d + 1) * 4) return DFA_EINVAL;
+  if (static_cast<long long>(kv_heads) * c.tiles > 0x7fffffffLL || c.cap > 65535)
+    return DFA_EINVAL;
+  CacheFwdParams p{};
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d),
+                              static_cast<cuuint64_t>(kv_heads) * page_size,
+                              static_cast<cuuint64_t>(num_pages)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), dims[1] * d};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(d < 128 ? d : 128),
+                             static_cast<cuuint32_t>(page_size < kUnit ? page_size : kUnit), 1};
+  const CUtensorMapSwizzle swizzle = d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (const int rc = encode_map_u8(&p.tm_k, k_cache, 3, dims, strides, box, swizzle)) return rc;
+  if (const int rc = encode_map_u8(&p.tm_v, v_cache, 3, dims, strides, box, swizzle)) return rc;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  auto set = [d](const long long* s, int n, long long* row, long long* head) {
+    *row = s ? s[0] : static_cast<long long>(n) * d;
+    *head = s ? s[1] : d;
+    return (*row & 7) == 0 && (*head & 7) == 0;
+  };
+  if (!set(q_strides, heads, &p.q_sr, &p.q_sh) || !set(k_strides, kv_heads, &p.k_sr, &p.k_sh) ||
+      !set(v_strides, kv_heads, &p.v_sr, &p.v_sh))
+    return DFA_EINVAL;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.cache_lens = cache_lens;
+  p.cu_new = cu_new;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + parts * d;
+  p.status = di.status;
+  p.batch = batch;
+  p.rows = rows;
+  p.max_new = max_new;
+  p.H = heads;
+  p.Hk = kv_heads;
+  p.G = G;
+  p.bs = block_size;
+  p.page_size = page_size;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.tiles = c.tiles;
+  p.target = c.target;
+  p.cap = c.cap;
+  p.part_rows = static_cast<int>(part_rows);
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = d == 64    ? launch_cache_rows<64>(p, c.tile_rows, s)
+                  : d == 128 ? launch_cache_rows<128>(p, c.tile_rows, s)
+                             : launch_cache_rows<256>(p, c.tile_rows, s);
+  // a request is split only where it holds more keys than the smallest chunk
+  if (e == cudaSuccess && static_cast<long long>(max_pages) * page_size > kCacheMinChunk) {
+    const long long warps = static_cast<long long>(rows) * heads;
+    const long long want = (warps + kJoinWarps - 1) / kJoinWarps;
+    const dim3 grid(static_cast<unsigned>(want < 4LL * di.sms ? want : 4LL * di.sms));
+    auto join = d == 64 ? dfa_cache_join_kernel<64>
+                        : d == 128 ? dfa_cache_join_kernel<128> : dfa_cache_join_kernel<256>;
+    e = launch_chained(join, grid, dim3(32 * kJoinWarps), 0, s, p);
+  }
+  return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);
+}
+
+}  // extern "C"

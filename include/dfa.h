@@ -323,6 +323,124 @@ int dfa_backward_noalloc(const void *q, const void *k, const void *v, const void
                          dfa_stream_t stream);
 
 /*
+ * Rotary positions.  The first rot_dim values of each head are rot_dim / 2
+ * pairs; pair i of a row at position pos turns by the angle whose cosine is
+ * table[pos][i] and whose sine is table[pos][rot_dim / 2 + i] (table: float32
+ * (max_pos, rot_dim), contiguous, 16-byte aligned):
+ *   y1 = c x1 - s x2,  y2 = s x1 + c x2.
+ * Pairs are (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ * DFA_ROTARY_INTERLEAVED; values past rot_dim are copied.  DFA_ROTARY_INVERSE
+ * applies the transposed map: the backward pass.
+ *
+ * q (batch, rows, heads, headdim), k (batch, rows, kv_heads, headdim) bf16
+ * with q_strides / k_strides (HOST arrays of three: batch, row and head
+ * strides in elements, multiples of 8; NULL: contiguous; the last dimension
+ * is contiguous), outputs contiguous.  An output may be its own contiguous
+ * input.  heads or kv_heads may be 0 (that tensor is then not read).
+ * positions: int32 (batch, rows), or NULL: row r has position r mod period
+ * (period n for [noisy | clean] samples of 2n rows, rows for plain
+ * sequences).  A row with a negative position is left as it was, or set to
+ * zero with DFA_ROTARY_CLEAR; a position >= max_pos is treated so too and sets
+ * DFA_EDEVICE.  rot_dim: a multiple of
+ * 16, at most headdim (64, 128 or 256).
+ */
+#define DFA_ROTARY_INTERLEAVED 1
+#define DFA_ROTARY_INVERSE 2
+#define DFA_ROTARY_CLEAR 4
+int dfa_rotary(const void *q, const void *k, void *q_out, void *k_out, const float *table,
+               const int *positions, int batch, int rows, int period, int heads, int kv_heads,
+               int headdim, int rot_dim, int max_pos, const long long *q_strides,
+               const long long *k_strides, int flags, dfa_stream_t stream);
+
+/*
+ * Paged 8-bit key/value cache, for sampling block by block: the clean tokens
+ * of finished blocks are kept, a new block attends to them and to itself.
+ * k_cache, v_cache: (num_pages, kv_heads, page_size, headdim) e4m3, page_size
+ * 16, 32, 64 or 128; k_scale, v_scale: float32 (num_pages, kv_heads), powers
+ * of two: a cached value is its e4m3 value times the scale of its page and
+ * head.  block_table: int32 (batch, max_pages), the pages of each request in
+ * order; cache_lens: int32 (batch), tokens held.  New rows are packed:
+ * request b has rows [cu_new[b], cu_new[b + 1]) of `rows`, at positions
+ * cache_lens[b], cache_lens[b] + 1, ...; rows past cu_new[batch] are left
+ * alone.  All of these are DEVICE pointers, so a captured graph follows them.
+ * max_pages * page_size is at most 2^30.
+ *
+ * What the host cannot see is checked by the kernels: a length past its table
+ * or negative, rows out of order or past `rows`, more than max_new of them, or
+ * a page number outside [0, num_pages) sets DFA_EDEVICE; nothing is read or
+ * written through it (keys of such a page count as masked, the request of bad
+ * lengths as empty).
+ */
+
+/*
+ * The pages of a sampling step.  new_lens: int32 (batch), rows each request
+ * adds.  Writes cu_new (batch + 1), positions (rows; -1 behind the last
+ * request's), next_lens (batch) = cache_lens + new_lens, and into block_table
+ * the pages the new tokens need, taken from the top of the stack free_pages
+ * (num_free entries, free_count[0] of them in use), requests in order, pages
+ * in order; next_free[0] = pages left on the stack, missing[0] = pages that
+ * were not to be had (the stack ran out, or a table is full): their entries
+ * are -1 and next_lens stops at the pages there are.  next_lens and next_free
+ * may be cache_lens and free_count themselves.  Rows beyond `rows` are cut and
+ * set DFA_EDEVICE.  Running it again on the same cache_lens and free_count
+ * writes the same.
+ */
+int dfa_cache_plan(const int *cache_lens, const int *new_lens, int *block_table,
+                   const int *free_pages, const int *free_count, int *cu_new, int *positions,
+                   int *next_lens, int *next_free, int *missing, int batch, int max_pages,
+                   int num_free, int page_size, int rows, dfa_stream_t stream);
+
+/*
+ * Requests with finished[b] != 0 (int32) give their pages back: pushed on the
+ * stack in order, their table entries set to -1, their cache_lens to 0.
+ */
+int dfa_cache_release(const int *finished, int *cache_lens, int *block_table, int *free_pages,
+                      int *free_count, int batch, int max_pages, int num_free, int page_size,
+                      dfa_stream_t stream);
+
+/*
+ * Append tokens: k, v (rows, kv_heads, headdim) bf16 (strides: HOST arrays of
+ * two, row and head, in elements, multiples of 8; NULL: contiguous), rounded
+ * to e4m3 (nearest even) after division by their page's scale.  A page whose
+ * tokens all come from this call takes the smallest scale 2^e, e >= -100,
+ * with its largest magnitude <= 448 * 2^e; a page that held tokens keeps the
+ * larger of that and its own, and its older tokens are rounded anew when the
+ * scale grows.  Values that are not finite are kept as NaN and do not count
+ * for the scale.  cache_lens are the lengths BEFORE the append.  A page
+ * belongs to one request of a call: two requests that append to one page race.
+ */
+int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int *cache_lens,
+                     const int *block_table, void *k_cache, void *v_cache, float *k_scale,
+                     float *v_scale, int batch, int rows, int max_new, int kv_heads, int headdim,
+                     int page_size, int num_pages, int max_pages, const long long *k_strides,
+                     const long long *v_strides, dfa_stream_t stream);
+
+/*
+ * Attention of the new rows over the cache: row i of request b sees its
+ * cache_lens[b] cached tokens and, if k and v are given (both or neither), the
+ * own rows (bf16, (rows, kv_heads, headdim)) of its block or earlier ones:
+ * blocks of block_size tokens counted from position 0, the rows at positions
+ * cache_lens[b] + i.  A block_size that covers the new rows makes them one
+ * block, seen both ways; block_size 1 is causal.  q (rows, heads, headdim)
+ * bf16, strides as for the append; out (rows, heads, headdim) bf16 contiguous,
+ * lse (heads, rows) float32.  A row that sees no key gets out 0 and lse -inf.
+ * kv_heads divides heads, head h reads key/value head h / (heads / kv_heads).
+ * batch <= 32768.  workspace: dfa_cache_workspace_bytes(...) bytes of device
+ * memory (16-byte aligned) for the partial results of long requests; calls
+ * that may run at the same time need workspaces of their own.
+ */
+long long dfa_cache_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
+                                    int headdim);
+int dfa_cache_forward(const void *q, const void *k, const void *v, const void *k_cache,
+                      const void *v_cache, const float *k_scale, const float *v_scale,
+                      const int *block_table, const int *cache_lens, const int *cu_new, void *out,
+                      float *lse, void *workspace, long long workspace_bytes, int batch, int rows,
+                      int max_new, int heads, int kv_heads, int headdim, int block_size,
+                      int page_size, int num_pages, int max_pages, const long long *q_strides,
+                      const long long *k_strides, const long long *v_strides,
+                      dfa_stream_t stream);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: DFA_OK, DFA_ETIMEOUT or DFA_EDEVICE (or DFA_ECUDA if the
  * synchronisation itself failed).
@@ -385,6 +503,25 @@ long long dfa_tile_visits(int mode, int n, int block_size, int block_m, int bloc
  */
 int dfa_work_item(int pass, int mode, int w, int batch, int heads, int tiles, int group,
                   int *item);
+
+/*
+ * Arithmetic of the sampling cache, host side, for tests and schedulers.
+ * dfa_cache_scale_exp: exponent of the scale of a page whose largest finite
+ * magnitude has the bf16 bits `bits`.  dfa_cache_page_ok: whether a kernel
+ * follows this page number.  dfa_cache_append_span: tokens [span[0], span[1])
+ * that appending n tokens behind len puts into the j-th page touched (equal
+ * when none), 0 <= j < dfa_cache_append_pages(n, page_size).
+ * dfa_cache_chunk: keys per work item for total_keys keys over about `target`
+ * items; dfa_cache_items: items of a request.  dfa_cache_own_end: one past the
+ * last own row that own row i of n sees.
+ */
+int dfa_cache_scale_exp(unsigned bits);
+int dfa_cache_page_ok(int page, int num_pages);
+int dfa_cache_append_pages(int max_new, int page_size);
+int dfa_cache_append_span(int len, int n, int j, int page_size, int *span);
+int dfa_cache_chunk(long long total_keys, int target);
+int dfa_cache_items(int len, int n, int chunk);
+int dfa_cache_own_end(int len, int i, int n, int block_size);
 
 /*
  * Tile shapes the kernels use for a head dimension: forward query rows and

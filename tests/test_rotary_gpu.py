@@ -1,0 +1,204 @@
+"""Rotary positions on the GPU against the float64 definition.
+
+Tolerance.  With x1, x2 exact in float32 and c, s float32, c x1 - s x2 is one
+product and one fused multiply-add (or two roundings more): at most
+3 * 2^-24 (|c x1| + |s x2|) <= 2^-22 max(|c|, |s|) max(|x1|, |x2|), then one
+rounding to bf16, at most 2^-8 of the value (half of eps 2^-7), plus the
+float32 error carried through it.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import sampling as osam
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def b():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from block_diffusion_masked_gb300 import binding, build
+
+    build.build()
+    binding.lib()
+    return binding
+
+
+def _f64(t):
+    return t.detach().float().cpu().double().numpy()
+
+
+def _randn(shape, seed):
+    g = torch.Generator("cpu").manual_seed(seed)
+    return torch.randn(shape, generator=g).to(torch.bfloat16).cuda()
+
+
+def _check(got, x, table, pos, inter, inverse=False):
+    """got, x (rows, heads, d)."""
+    ref = osam.rotary(_f64(x), table.cpu().numpy(), pos, inter, inverse)
+    rot = table.shape[1]
+    big = np.abs(_f64(x)).max(-1, keepdims=True) * max(1.0, float(table.abs().max()))
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -22 * big
+    err = np.abs(_f64(got) - ref)
+    used = np.asarray(pos) >= 0
+    assert (err[used] <= tol[used]).all(), (err - tol)[used].max()
+    # values past the turned ones are copied bit by bit
+    assert torch.equal(got[torch.tensor(used)][..., rot:], x[torch.tensor(used)][..., rot:])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("B,n,H,Hk,d,rot", [
+    (1, 1, 1, 1, 64, 64), (2, 5, 3, 1, 64, 16), (1, 33, 8, 2, 128, 128), (3, 7, 5, 5, 128, 96),
+    (1, 9, 4, 2, 256, 64), (2, 3, 1, 1, 256, 256), (1, 130, 6, 2, 128, 32)])
+def test_layouts_and_gradients(b, B, n, H, Hk, d, rot, inter):
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(n, rot, base=100.0)
+    q, k = _randn((B, 2 * n, H, d), 1).requires_grad_(), _randn((B, 2 * n, Hk, d), 2).requires_grad_()
+    yq, yk = rotary_func(q, k, table, interleaved=inter)
+    gq, gk = _randn(yq.shape, 3), _randn(yk.shape, 4)
+    dq, dk = torch.autograd.grad((yq, yk), (q, k), (gq, gk))
+    assert b.dfa_status() == 0
+    pos = list(range(n)) * 2
+    for i in range(B):
+        for y, x, inverse in ((yq, q, False), (yk, k, False), (dq, gq, True), (dk, gk, True)):
+            _check(y[i], x[i], table, pos, inter, inverse)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_gradient_against_differences(b, inter):
+    """<g, R(x + e) - R(x)> = <dx, e> for a linear map: in float64 up to the
+    bf16 roundings of R(x + e), R(x) and dx."""
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    n, H, d = 4, 2, 64
+    table = rotary_table(n, d)
+    x = _randn((1, 2 * n, H, d), 5).requires_grad_()
+    g = _randn(x.shape, 6)
+    y, _ = rotary_func(x, None, table, interleaved=inter)
+    (dx,) = torch.autograd.grad(y, x, g)
+    for seed in range(4):
+        e = _randn(x.shape, 20 + seed)
+        z, _ = rotary_func((x.detach().float() + 8 * e.float()).bfloat16(), None, table,
+                           interleaved=inter)
+        step = (x.detach().float() + 8 * e.float()).bfloat16().double() - x.detach().double()
+        lhs = float((g.double() * (z.double() - y.detach().double())).sum())
+        rhs = float((dx.double() * step).sum())
+        tol = 2.0 ** -8 * float((g.double().abs() * (z.double().abs() + y.detach().double().abs()))
+                                .sum() + (dx.double().abs() * step.abs()).sum()) * 1.01
+        assert abs(lhs - rhs) <= tol
+
+
+@pytest.mark.parametrize("d,inter", [(64, False), (128, True), (256, False)])
+def test_strided_views_and_packed_rows(b, d, inter):
+    """Slices of a fused projection, far positions, rows that are not in use."""
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    rows, H, Hk = 21, 4, 2
+    table = rotary_table(50000, d // 2, base=500000.0)
+    qkv = _randn((rows, H + 2 * Hk, d), 7)
+    q, k = qkv[:, :H], qkv[:, H:H + Hk]
+    pos = [0, 49999, 31, -1, 777] + list(range(1000, 1012)) + [-1, 5, 5, -7]
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    yq, yk = rotary_func(q, k, table, p, inter)
+    assert b.dfa_status() == 0
+    assert yq.is_contiguous() and yk.is_contiguous()
+    _check(yq, q, table, pos, inter)
+    _check(yk, k, table, pos, inter)
+    for r in (3, 17, 20):  # unused: zero here, left alone by the binding
+        assert not yq[r].any() and not yk[r].any()
+    out = torch.full((1, rows, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    b.dfa_rotary(q[None], None, table, p[None], interleaved=inter, q_out=out)
+    assert (out[0, 3] == 7).all() and (out[0, 17] == 7).all()
+    assert torch.equal(out[0, :3], yq[:3])
+
+
+def test_in_place_and_alone(b):
+    from block_diffusion_masked_gb300 import rotary_table
+
+    table = rotary_table(8, 128)
+    x, k = _randn((2, 16, 3, 128), 8), _randn((2, 16, 1, 128), 9)
+    want, wk = b.dfa_rotary(x, k, table)
+    y = x.clone()
+    got, none = b.dfa_rotary(y, None, table, q_out=y)
+    assert none is None and got is y and torch.equal(y, want)
+    # a plain sequence: positions 0 .. L - 1
+    t16 = rotary_table(16, 128)
+    p16 = torch.arange(16, dtype=torch.int32, device="cuda").expand(2, 16).contiguous()
+    a, _ = b.dfa_rotary(x, k, t16, period=16)
+    c, _ = b.dfa_rotary(x, k, t16, p16)
+    assert torch.equal(a, c)
+    assert b.dfa_status() == 0
+
+
+def test_positions_past_the_table(b):
+    from block_diffusion_masked_gb300 import rotary_table
+
+    table = rotary_table(8, 64)
+    x = _randn((1, 3, 2, 64), 10)
+    pos = torch.tensor([[7, 8, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")
+    out = torch.full_like(x, 3.0)
+    b.dfa_rotary(x, None, table, pos, q_out=out)
+    assert b.dfa_status() == b.DFA_EDEVICE
+    assert (out[0, 1:] == 3).all() and not (out[0, 0] == 3).all()
+    b.dfa_rotary(x, None, table, pos, q_out=out, clear=True)
+    assert b.dfa_status() == b.DFA_EDEVICE and not out[0, 1:].any()
+
+
+def test_refusals(b):
+    from block_diffusion_masked_gb300 import rotary_table
+
+    table = rotary_table(4, 64)
+    x = _randn((1, 8, 2, 64), 11)
+    with pytest.raises(ValueError):
+        b.dfa_rotary(x.float(), None, table)
+    with pytest.raises(ValueError):
+        b.dfa_rotary(x[:, :7], None, table)  # odd length without a period
+    with pytest.raises(ValueError):
+        b.dfa_rotary(x, x[:, :4], table)
+    with pytest.raises(ValueError):
+        b.dfa_rotary(x, None, table.double())
+    with pytest.raises(ValueError):
+        b.dfa_rotary(x, None, table, torch.zeros(8, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        b.dfa_rotary(x.transpose(2, 3), None, table)
+    with pytest.raises(b.DfaError):
+        b.dfa_rotary(x, None, rotary_table(3, 64))  # four positions, a table of three
+    with pytest.raises(b.DfaError):
+        b.dfa_rotary(x, None, table[:, :24].contiguous())
+
+
+@pytest.mark.parametrize("kind", ["diffusion", "varlen", "causal"])
+def test_attention_with_positions(b, kind):
+    """The attention functions turn q and k first: the same outputs and
+    gradients as the two calls one after the other."""
+    import block_diffusion_masked_gb300 as m
+
+    table = m.rotary_table(64, 64)
+    shape = (1, 64, 2, 64)
+    q, k, v = (_randn(shape, 30 + i).requires_grad_() for i in range(3))
+    g = _randn(shape, 33)
+    if kind == "diffusion":
+        one = m.diffusion_attn_func(q, k, v, 4, rotary_table=table)
+        two = m.diffusion_attn_func(*m.rotary_func(q, k, table), v, 4)
+    elif kind == "causal":
+        one = m.causal_attn_func(q, k, v, rotary_table=table)
+        two = m.causal_attn_func(*m.rotary_func(q, k, table, period=64), v)
+    else:
+        pos = torch.tensor(list(range(20)) * 2 + list(range(12)) * 2, dtype=torch.int32,
+                           device="cuda")
+        one = m.diffusion_attn_varlen_func(q[0], k[0], v[0], [0, 40, 64], 4, rotary_table=table,
+                                           positions=pos)[None]
+        a, c = m.rotary_func(q[0], k[0], table, pos)
+        two = m.diffusion_attn_varlen_func(a, c, v[0], [0, 40, 64], 4)[None]
+    assert torch.equal(one, two)
+    g1 = torch.autograd.grad(one, (q, k, v), g)
+    g2 = torch.autograd.grad(two, (q, k, v), g)
+    assert torch.equal(g1[1], g2[1]) and torch.equal(g1[2], g2[2])
+    # dq sums float32 atomics in any order, then two roundings to bf16
+    err = (g1[0].float() - g2[0].float()).abs().max() / g2[0].float().abs().max()
+    assert float(err) <= 2 * 2.0 ** -8
+    assert b.dfa_status() == 0
