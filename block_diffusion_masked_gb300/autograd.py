@@ -19,34 +19,38 @@ from . import binding
 def _strided(t):
     """t itself where the kernels can read its strides (heads of whole 16-byte
     pieces), else a contiguous copy."""
-    s = t.stride()
-    if s[-1] == 1 and t.data_ptr() % 16 == 0 and not any(x % 8 for x in s[:-1]):
-        return t
-    return t.contiguous()
+    if t.data_ptr() % 16 == 0:
+        if t.is_contiguous():
+            return t
+        s = t.stride()
+        if s[-1] == 1 and not any([x & 7 for x in s[:-1]]):
+            return t
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 class RotaryFunc(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, table, positions, period, interleaved):
+    def forward(ctx, q, k, table, positions, period, flags):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(table, positions)
-        ctx.how = (period, interleaved)
-        return binding.dfa_rotary(_strided(q), None if k is None else _strided(k), table,
-                                  positions, period, interleaved, clear=True)
+        sizes = binding._rotary_sizes(q, k, table, positions, period)
+        ctx.how = sizes, flags
+        return binding._rotary_launch(q, k, table, positions, sizes, flags)
 
     @staticmethod
     def backward(ctx, dq, dk):
+        # Gradients have the outputs' shapes and types, checked in the forward.
         table, positions = ctx.saved_tensors
-        period, interleaved = ctx.how
-
-        def turn(x, y):
-            return binding.dfa_rotary(_strided(x), None if y is None else _strided(y), table,
-                                      positions, period, interleaved, inverse=True, clear=True)
-
+        sizes, flags = ctx.how
+        flags |= binding.DFA_ROTARY_INVERSE
         if dq is not None:
-            dq, dk = turn(dq, dk)
+            dq, dk = binding._rotary_launch(_strided(dq), None if dk is None else _strided(dk),
+                                            table, positions,
+                                            sizes if dk is not None else (*sizes[:4], 0, *sizes[5:]),
+                                            flags)
         elif dk is not None:
-            dk = turn(dk, None)[0]
+            sizes = (*sizes[:3], sizes[4], 0, *sizes[5:])
+            dk = binding._rotary_launch(_strided(dk), None, table, positions, sizes, flags)[0]
         return dq, dk, None, None, None, None
 
 
@@ -61,15 +65,14 @@ def rotary_func(q, k, table, positions=None, interleaved=False, period=None):
     position r mod ``period``; the default period L // 2 is the [noisy |
     clean] layout, both halves counted from 0.
     """
-    if q.dim() == 3:
-        if positions is None:
-            raise ValueError("packed rows need positions")
-        if positions.dim() != 1:
-            raise ValueError("positions of packed rows must be (rows,)")
-        q, k = q[None], None if k is None else k[None]
-        q, k = RotaryFunc.apply(q, k, table, positions[None], period, bool(interleaved))
-        return q[0], None if k is None else k[0]
-    return RotaryFunc.apply(q, k, table, positions, period, bool(interleaved))
+    q = _strided(q)
+    if k is not None:
+        k = _strided(k)
+    flags = binding.DFA_ROTARY_CLEAR | (binding.DFA_ROTARY_INTERLEAVED if interleaved else 0)
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        return RotaryFunc.apply(q, k, table, positions, period, flags)
+    return binding._rotary_launch(q, k, table, positions,
+                                  binding._rotary_sizes(q, k, table, positions, period), flags)
 
 
 class DiffusionAttnFunc(torch.autograd.Function):

@@ -11,6 +11,7 @@ so a missing or unloadable library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -586,12 +587,20 @@ def dfa_bwd_dq_convert(dq_acc, dq, mode=MODE_DIFFUSION):
 
 
 # ------------------------------------------- rotary positions, sampling cache
+# A sampling step is many small calls, so these keep to few Python operations:
+# the checks read attributes only, and the device is made current only where
+# it is not.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 
 def _call(fn, device, *args):
     """Call entry point ``fn`` with ``device`` current, on its current stream."""
-    handle = lib()
-    if device.index == torch.cuda.current_device():
-        rc = getattr(handle, fn)(*args, torch.cuda.current_stream(device).cuda_stream)
+    handle = _lib or lib()
+    index = device.index
+    if index == torch.cuda.current_device():
+        stream = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+        rc = getattr(handle, fn)(*args, stream)
     else:
         with torch.cuda.device(device):
             rc = getattr(handle, fn)(*args, torch.cuda.current_stream(device).cuda_stream)
@@ -600,28 +609,17 @@ def _call(fn, device, *args):
 
 
 def _check_dense(t, shape, dtype, device, name):
-    """A contiguous input of the given shape (None: any size)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device
-            or t.dim() != len(shape) or not t.is_contiguous()
-            or any(s is not None and s != x for s, x in zip(shape, t.shape))):
-        want = ", ".join("any" if s is None else str(s) for s in shape)
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({want}) on {device}")
-    return t
+    """A contiguous input of the given shape."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
+            or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}")
 
 
-def _strides(t, name):
-    """Host array of a tensor's leading strides, None where it is contiguous.
-
-    The last dimension must be contiguous and the others multiples of 8
-    elements (16 bytes), as must be the storage offset's address.
-    """
-    if t.is_contiguous():
-        return None
-    s = t.stride()
-    if s[-1] != 1 or any(x % 8 for x in s[:-1]):
-        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides "
-                         "multiples of 8 elements")
-    return (ctypes.c_longlong * (len(s) - 1))(*s[:-1])
+def _check_dims(t, dim, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != dim:
+        raise ValueError(f"{name} must be a {dim}-dimensional tensor")
+    return t.shape
 
 
 def _check_heads(t, dim, name, device=None):
@@ -631,44 +629,106 @@ def _check_heads(t, dim, name, device=None):
         raise ValueError(f"{name} must be a {dim}-dimensional bfloat16 tensor on {where}")
 
 
+def _strides(t, name):
+    """Host array of a tensor's leading strides, None where it is contiguous.
+
+    The last dimension must be contiguous and the others multiples of 8
+    elements (16 bytes), as must be the address of the first element.
+    """
+    if t.is_contiguous():
+        return None
+    s = t.stride()
+    lead = s[:-1]
+    if s[-1] != 1 or any([x & 7 for x in lead]):
+        raise ValueError(f"{name}: the last dimension must be contiguous and the other strides "
+                         "multiples of 8 elements")
+    return (ctypes.c_longlong * len(lead))(*lead)
+
+
 def dfa_rotary(q, k, table, positions=None, period=None, interleaved=False, inverse=False,
                q_out=None, k_out=None, clear=False):
     """Rotary positions of q (B, L, H, d) and k (B, L, Hk, d), bf16; k may be None.
 
     ``table``: float32 (max_pos, rot_dim), cosines then sines.  ``positions``:
     int32 (B, L), or None: row r has position r mod ``period`` (default L // 2,
-    the [noisy | clean] layout).  q and k may be strided views (the last
-    dimension contiguous).  Returns contiguous (q_out, k_out); rows of
-    negative positions are not written, or set to zero with ``clear``.
-    ``inverse`` is the transposed map.
+    the [noisy | clean] layout).  Packed rows: q (rows, H, d), k (rows, Hk, d),
+    positions (rows,).  q and k may be strided views (the last dimension
+    contiguous).  Returns contiguous (q_out, k_out); rows of negative positions
+    are not written, or set to zero with ``clear``.  ``inverse`` is the
+    transposed map.
     """
-    _check_heads(q, 4, "q")
-    B, L, H, d = q.shape
-    dev = q.device
+    sizes = _rotary_sizes(q, k, table, positions, period)
+    if q_out is not None:
+        _check_dense(q_out, q.shape, torch.bfloat16, q.device, "q_out")
+    if k is not None and k_out is not None:
+        _check_dense(k_out, k.shape, torch.bfloat16, q.device, "k_out")
+    flags = ((DFA_ROTARY_INTERLEAVED if interleaved else 0)
+             | (DFA_ROTARY_INVERSE if inverse else 0) | (DFA_ROTARY_CLEAR if clear else 0))
+    return _rotary_launch(q, k, table, positions, sizes, flags, q_out, k_out)
+
+
+def _rotary_sizes(q, k, table, positions, period):
+    """Check dfa_rotary's inputs; returns its integer arguments."""
+    packed = isinstance(q, torch.Tensor) and q.dim() == 3
+    _check_heads(q, 3 if packed else 4, "q")
+    shape, dev = q.shape, q.device
+    if packed:
+        L, H, d = shape
+        B = 1
+    else:
+        B, L, H, d = shape
     Hk = 0
     if k is not None:
-        _check_heads(k, 4, "k", dev)
-        Hk = k.shape[2]
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != d:
+        _check_heads(k, 3 if packed else 4, "k", dev)
+        Hk = k.shape[-2]
+        if k.shape[:-2] != shape[:-2] or k.shape[-1] != d:
             raise ValueError("k must be (batch, seqlen, kv_heads, headdim) like q")
-    _check_dense(table, (None, None), torch.float32, dev, "table")
+    max_pos, rot = _check_dims(table, 2, "table")
+    _check_dense(table, (max_pos, rot), torch.float32, dev, "table")
     if positions is not None:
-        _check_dense(positions, (B, L), torch.int32, dev, "positions")
+        _check_dense(positions, shape[:-2], torch.int32, dev, "positions")
+        period = 1
+    elif packed:
+        raise ValueError("packed rows need positions")
     elif period is None:
         if L % 2:
             raise ValueError("the sequence must be [noisy | clean] with an even length 2n")
         period = max(L // 2, 1)
-    q_out = _out_or_new(q_out, q.shape, torch.bfloat16, dev, "q_out")
+    return B, L, int(period), H, Hk, d, rot, max_pos
+
+
+def _rotary_launch(q, k, table, positions, sizes, flags, q_out=None, k_out=None):
+    """dfa_rotary of tensors that _rotary_sizes (or a call like it) has checked."""
+    q_str, k_str, kp, kop = _strides(q, "q"), None, None, None
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if k is not None:
-        k_out = _out_or_new(k_out, k.shape, torch.bfloat16, dev, "k_out")
-    flags = (DFA_ROTARY_INTERLEAVED if interleaved else 0) | (DFA_ROTARY_INVERSE if inverse else 0)
-    flags |= DFA_ROTARY_CLEAR if clear else 0
-    _call("dfa_rotary", dev, q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-          None if k is None else k_out.data_ptr(), table.data_ptr(),
-          None if positions is None else positions.data_ptr(), B, L,
-          1 if period is None else int(period), H, Hk, d, table.shape[1], table.shape[0],
-          _strides(q, "q"), None if k is None else _strides(k, "k"), flags)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+        k_str, kp, kop = _strides(k, "k"), k.data_ptr(), k_out.data_ptr()
+    if len(q.shape) == 3:  # the strides of a batch of one
+        q_str = q_str and (ctypes.c_longlong * 3)(0, *q_str)
+        k_str = k_str and (ctypes.c_longlong * 3)(0, *k_str)
+    _call("dfa_rotary", q.device, q.data_ptr(), kp, q_out.data_ptr(), kop, table.data_ptr(),
+          None if positions is None else positions.data_ptr(), *sizes, q_str, k_str, flags)
     return q_out, k_out
+
+
+def _check_pages(cache_lens, per_request, block_table, free_pages, free_count, name):
+    """The int32 state of a page table; returns (device, batch, max_pages, free entries)."""
+    i32 = torch.int32
+    (B,) = _check_dims(cache_lens, 1, "cache_lens")
+    dev = cache_lens.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    _check_dense(cache_lens, (B,), i32, dev, "cache_lens")
+    _check_dense(per_request, (B,), i32, dev, name)
+    maxp = _check_dims(block_table, 2, "block_table")[1]
+    _check_dense(block_table, (B, maxp), i32, dev, "block_table")
+    (F,) = _check_dims(free_pages, 1, "free_pages")
+    _check_dense(free_pages, (F,), i32, dev, "free_pages")
+    _check_dense(free_count, (1,), i32, dev, "free_count")
+    return dev, B, maxp, F
 
 
 def dfa_cache_plan(cache_lens, new_lens, block_table, free_pages, free_count, page_size, rows):
@@ -679,56 +739,46 @@ def dfa_cache_plan(cache_lens, new_lens, block_table, free_pages, free_count, pa
     (B + 1,), positions (rows,), next_lens (B,), next_free (1,), missing (1,)).
     The caller's next step passes next_lens and next_free.
     """
-    i32, dev = torch.int32, cache_lens.device
-    _check_dense(cache_lens, (None,), i32, dev, "cache_lens")
-    B = cache_lens.shape[0]
-    _check_dense(new_lens, (B,), i32, dev, "new_lens")
-    _check_dense(block_table, (B, None), i32, dev, "block_table")
-    _check_dense(free_pages, (None,), i32, dev, "free_pages")
-    _check_dense(free_count, (1,), i32, dev, "free_count")
-    if not cache_lens.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
+    dev, B, maxp, F = _check_pages(cache_lens, new_lens, block_table, free_pages, free_count,
+                                   "new_lens")
     rows = int(rows)
     if rows < 0:
         raise ValueError("rows must not be negative")
-    buf = torch.empty(2 * B + 3 + rows, dtype=i32, device=dev)
-    cu_new, next_lens, next_free, missing, positions = buf.split([B + 1, B, 1, 1, rows])
+    buf = torch.empty(2 * B + 3 + rows, dtype=torch.int32, device=dev)
+    cu_new, next_lens, next_free, missing, positions = torch.split_with_sizes(
+        buf, (B + 1, B, 1, 1, rows))
     at = buf.data_ptr()
     _call("dfa_cache_plan", dev, cache_lens.data_ptr(), new_lens.data_ptr(),
           block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at,
           at + 4 * (2 * B + 3), at + 4 * (B + 1), at + 4 * (2 * B + 1), at + 4 * (2 * B + 2), B,
-          block_table.shape[1], free_pages.shape[0], int(page_size), rows)
+          maxp, F, int(page_size), rows)
     return block_table, cu_new, positions, next_lens, next_free, missing
 
 
 def dfa_cache_release(finished, cache_lens, block_table, free_pages, free_count, page_size):
     """Requests with finished != 0 give their pages back (in place; see dfa.h)."""
-    i32, dev = torch.int32, cache_lens.device
-    _check_dense(cache_lens, (None,), i32, dev, "cache_lens")
-    B = cache_lens.shape[0]
-    _check_dense(finished, (B,), i32, dev, "finished")
-    _check_dense(block_table, (B, None), i32, dev, "block_table")
-    _check_dense(free_pages, (None,), i32, dev, "free_pages")
-    _check_dense(free_count, (1,), i32, dev, "free_count")
-    if not cache_lens.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
+    dev, B, maxp, F = _check_pages(cache_lens, finished, block_table, free_pages, free_count,
+                                   "finished")
     _call("dfa_cache_release", dev, finished.data_ptr(), cache_lens.data_ptr(),
-          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B,
-          block_table.shape[1], free_pages.shape[0], int(page_size))
+          block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B, maxp, F,
+          int(page_size))
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new, dev, d):
     """Shapes of a cache and its tables; returns (batch, kv_heads, page_size, pages, max_pages)."""
-    _check_dense(k_cache, (None, None, None, d), torch.float8_e4m3fn, dev, "k_cache")
-    P, Hk, ps, _ = k_cache.shape
-    _check_dense(v_cache, (P, Hk, ps, d), torch.float8_e4m3fn, dev, "v_cache")
+    shape = _check_dims(k_cache, 4, "k_cache")
+    P, Hk, ps, dc = shape
+    if dc != d:
+        raise ValueError("the cache must have the head dimension of the rows")
+    _check_dense(k_cache, shape, torch.float8_e4m3fn, dev, "k_cache")
+    _check_dense(v_cache, shape, torch.float8_e4m3fn, dev, "v_cache")
     _check_dense(k_scale, (P, Hk), torch.float32, dev, "k_scale")
     _check_dense(v_scale, (P, Hk), torch.float32, dev, "v_scale")
-    _check_dense(cache_lens, (None,), torch.int32, dev, "cache_lens")
-    B = cache_lens.shape[0]
-    _check_dense(block_table, (B, None), torch.int32, dev, "block_table")
+    B, maxp = _check_dims(block_table, 2, "block_table")
+    _check_dense(block_table, (B, maxp), torch.int32, dev, "block_table")
+    _check_dense(cache_lens, (B,), torch.int32, dev, "cache_lens")
     _check_dense(cu_new, (B + 1,), torch.int32, dev, "cu_new")
-    return B, Hk, ps, P, block_table.shape[1]
+    return B, Hk, ps, P, maxp
 
 
 def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_scale, v_scale,
@@ -738,12 +788,12 @@ def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_
     ``max_new``: a bound on the rows of one request, known to the host.
     """
     _check_heads(k, 3, "k")
-    dev = k.device
-    rows, Hk, d = k.shape
+    dev, shape = k.device, k.shape
+    rows, Hk, d = shape
     _check_heads(v, 3, "v", dev)
     B, Hc, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
                                       cu_new, dev, d)
-    if v.shape != k.shape or Hc != Hk:
+    if v.shape != shape or Hc != Hk:
         raise ValueError("k and v must be (rows, kv_heads, headdim) with the cache's heads")
     _call("dfa_cache_append", dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
           cache_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -759,6 +809,13 @@ def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim):
     return int(n)
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(device_index, *sizes):
+    """dfa_cache_workspace_bytes on a device, which sizes alone determine."""
+    with torch.cuda.device(device_index):
+        return max(dfa_cache_workspace_bytes(*sizes), 16)
+
+
 def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new,
                       max_new, k=None, v=None, block_size=1, out=None, lse=None, workspace=None):
     """Attention of packed new rows q (rows, H, d) over the cache and, with k and v
@@ -769,37 +826,40 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
     dfa_cache_workspace_bytes(...) bytes; by default one is allocated.
     """
     _check_heads(q, 3, "q")
-    dev = q.device
-    rows, H, d = q.shape
+    dev, shape = q.device, q.shape
+    rows, H, d = shape
     B, Hk, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
                                       cu_new, dev, d)
     if Hk < 1 or H % Hk:
         raise ValueError("kv_heads must divide the query heads")
     if (k is None) != (v is None):
         raise ValueError("k and v go together")
+    kp = vp = ks = vs = None
     if k is not None:
-        for x, name in ((k, "k"), (v, "v")):
-            _check_heads(x, 3, name, dev)
-            if x.shape != (rows, Hk, d):
-                raise ValueError(f"{name} must be (rows, kv_heads, headdim)")
-    out = _out_or_new(out, q.shape, torch.bfloat16, dev, "out")
-    lse = _out_or_new(lse, (H, rows), torch.float32, dev, "lse")
-    if workspace is None:
-        if dev.index == torch.cuda.current_device():
-            need = dfa_cache_workspace_bytes(B, rows, max_new, H, Hk, d)
-        else:
-            with torch.cuda.device(dev):
-                need = dfa_cache_workspace_bytes(B, rows, max_new, H, Hk, d)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check_heads(k, 3, "k", dev)
+        _check_heads(v, 3, "v", dev)
+        if k.shape != (rows, Hk, d) or v.shape != (rows, Hk, d):
+            raise ValueError("k and v must be (rows, kv_heads, headdim)")
+        kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _strides(k, "k"), _strides(v, "v")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     else:
-        _check_dense(workspace, (None,), torch.uint8, dev, "workspace")
-    _call("dfa_cache_forward", dev, q.data_ptr(), None if k is None else k.data_ptr(),
-          None if v is None else v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _check_dense(out, shape, torch.bfloat16, dev, "out")
+    if lse is None:
+        lse = torch.empty((H, rows), dtype=torch.float32, device=dev)
+    else:
+        _check_dense(lse, (H, rows), torch.float32, dev, "lse")
+    max_new = int(max_new)
+    if workspace is None:
+        workspace = torch.empty(_workspace_bytes(dev.index, B, rows, max_new, H, Hk, d),
+                                dtype=torch.uint8, device=dev)
+    else:
+        _check_dense(workspace, (workspace.numel(),), torch.uint8, dev, "workspace")
+    _call("dfa_cache_forward", dev, q.data_ptr(), kp, vp, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
           cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel(), B, rows, int(max_new), H, Hk, d, int(block_size), ps, P, maxp,
-          _strides(q, "q"), None if k is None else _strides(k, "k"),
-          None if v is None else _strides(v, "v"))
+          workspace.numel(), B, rows, max_new, H, Hk, d, int(block_size), ps, P, maxp,
+          _strides(q, "q"), ks, vs)
     return out, lse
 
 

@@ -291,31 +291,33 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
 // exact but for subnormals.  A page whose tokens all arrive in this call
 // takes a fresh scale, whatever it held before.
 //
-// Bound by memory: 2 bytes read and 1 written per value.  NT threads hold
-// VPT vectors of 8 values each: a full 128-token page of headdim 256 is
-// 256 x 16 vectors; where a page gets at most 128 vectors (single tokens,
-// short blocks) one warp takes it.
+// Bound by memory: 2 bytes read and 1 written per value; for short appends by
+// the chain lengths -> page number -> scale -> tokens rounded anew, so the
+// rows are read while the page number is on its way.  NT threads hold VPT
+// vectors of 8 values each, the smallest block that holds a page's share:
+// registers limit how many blocks, and so how many bytes, are in flight.
 template <int D, int NT, int VPT>
 __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams p) {
   constexpr int kVec = D / 8;  // vectors per token and head
   __shared__ unsigned s_top[NT / 32];
   grid_dependency_wait();
-  const int b = blockIdx.x / p.touch, j = blockIdx.x - b * p.touch;
-  const int h = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
+  // heads fastest: neighbouring blocks read neighbouring pieces of the rows
+  const unsigned head = blockIdx.x % (2u * p.Hk), at = blockIdx.x / (2u * p.Hk);
+  const int which = head >= static_cast<unsigned>(p.Hk), h = head - which * p.Hk;
+  const int b = at / p.touch, j = at - b * p.touch, tid = threadIdx.x;
   const int r0 = p.cu_new[b], r1 = p.cu_new[b + 1], len = p.cache_lens[b];
   const bool ok = r0 >= 0 && r1 >= r0 && r1 <= p.rows && r1 - r0 <= p.max_new && len >= 0 &&
                   len <= (1 << 30);
   const int n = ok ? r1 - r0 : 0;
   const Interval span = ok ? cache_append_range(len, n, j, p.page_size) : Interval{0, 0};
   const int slot = len / p.page_size + j;
-  int page = -1;
-  if (span.lo < span.hi && slot < p.max_pages)
-    page = p.block_table[static_cast<long long>(b) * p.max_pages + slot];
-  const bool held = span.lo < span.hi && cache_page_ok(page, p.num_pages);
-  if (!held) {  // nothing for this page, or nowhere to put it
-    if (tid == 0 && (!ok || span.lo < span.hi)) atomicOr(p.status, kStatusIndex);
+  if (span.lo >= span.hi) {  // nothing for this page
+    if (tid == 0 && !ok) atomicOr(p.status, kStatusIndex);
     return;
   }
+  int page = -1;
+  if (slot < p.max_pages)
+    page = p.block_table[static_cast<long long>(b) * p.max_pages + slot];
   const int first = span.lo & (p.page_size - 1);  // older tokens of the page
   const int nvec = (span.hi - span.lo) * kVec;
   const long long sr = p.sr[which];
@@ -328,6 +330,12 @@ __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams
     w[u] = make_uint4(0u, 0u, 0u, 0u);
     if (i < nvec) w[u] = *reinterpret_cast<const uint4*>(x + (i / kVec) * sr + (i % kVec) * 8);
   }
+  if (!cache_page_ok(page, p.num_pages)) {  // nowhere to put it
+    if (tid == 0) atomicOr(p.status, kStatusIndex);
+    return;
+  }
+  float* scale = p.scale[which] + static_cast<long long>(page) * p.Hk + h;
+  const float was = *scale;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
@@ -338,8 +346,6 @@ __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams
     }
   }
   top = __reduce_max_sync(0xffffffffu, top);
-  float* scale = p.scale[which] + static_cast<long long>(page) * p.Hk + h;
-  const float was = *scale;
   if constexpr (NT > 32) {
     if ((tid & 31) == 0) s_top[tid >> 5] = top;
     __syncthreads();
@@ -378,15 +384,22 @@ __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams
   if (tid == 0) *scale = now;
 }
 
+template <int D, int NT, int VPT>
+cudaError_t launch_append_block(const AppendParams& p, unsigned blocks, cudaStream_t stream) {
+  return launch_chained(dfa_cache_append_kernel<D, NT, VPT>, dim3(blocks), dim3(NT), 0, stream, p);
+}
+
 template <int D>
 cudaError_t launch_append(const AppendParams& p, int batch, cudaStream_t stream) {
-  const long long blocks = static_cast<long long>(batch) * p.touch;
-  if (blocks > 0x7fffffffLL || p.Hk > 65535) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.Hk), 2);
-  const int tokens = p.max_new < p.page_size ? p.max_new : p.page_size;
-  if (tokens * (D / 8) <= 128)
-    return launch_chained(dfa_cache_append_kernel<D, 32, 4>, grid, dim3(32), 0, stream, p);
-  return launch_chained(dfa_cache_append_kernel<D, 256, D / 16>, grid, dim3(256), 0, stream, p);
+  const long long blocks = 2LL * p.Hk * batch * p.touch;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned n = static_cast<unsigned>(blocks);
+  const int vectors = (p.max_new < p.page_size ? p.max_new : p.page_size) * (D / 8);
+  if (vectors <= 128) return launch_append_block<D, 32, 4>(p, n, stream);
+  if (vectors <= 512) return launch_append_block<D, 128, 4>(p, n, stream);
+  if (vectors <= 1024) return launch_append_block<D, 128, 8>(p, n, stream);
+  if constexpr (D == 128) return launch_append_block<D, 256, 8>(p, n, stream);
+  return launch_append_block<D, 256, 16>(p, n, stream);  // headdim 256: up to 4096
 }
 
 }  // namespace
