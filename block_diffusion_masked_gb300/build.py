@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdfa.so")
 
 SOURCES = ["fwd.cu", "fwd2.cu", "bwd2.cu", "aux.cu", "rotary.cu", "cache.cu", "cache_fwd.cu",
-           "api.cu", "noalloc.cu"]
+           "cache_wide.cu", "api.cu", "noalloc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

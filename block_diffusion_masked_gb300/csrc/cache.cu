@@ -466,13 +466,21 @@ int dfa_cache_append_span(int len, int n, int j, int page_size, int* span) {
   span[1] = s.hi;
   return DFA_OK;
 }
-int dfa_cache_chunk(long long total_keys, int target) {
-  if (total_keys < 0 || target < 1) return DFA_EINVAL;
-  return cache_chunk(total_keys, target);
+int dfa_cache_units(int len, int n, int unit, int finish) {
+  if (len < 0 || unit < 0 || finish < 1) return DFA_EINVAL;
+  return cache_units(len, n, unit, finish);
 }
-int dfa_cache_items(int len, int n, int chunk) {
-  if (len < 0 || chunk < 1) return DFA_EINVAL;
-  return cache_items(len, n, chunk);
+int dfa_cache_blocks(long long total, int limit, int least) {
+  if (total < 0 || limit < 1 || least < 1) return DFA_EINVAL;
+  return cache_blocks(total, limit, least);
+}
+long long dfa_cache_run(int x, long long total, int blocks) {
+  if (total < 0 || blocks < 1 || x < 0 || x > blocks) return DFA_EINVAL;
+  return cache_run(x, total, blocks);
+}
+int dfa_cache_owner(long long w, long long total, int blocks) {
+  if (blocks < 1 || w < 0 || w >= total) return DFA_EINVAL;
+  return cache_owner(w, total, blocks);
 }
 int dfa_cache_own_end(int len, int i, int n, int block_size) {
   if (len < 0 || i < 0 || i >= n || block_size < 1) return DFA_EINVAL;

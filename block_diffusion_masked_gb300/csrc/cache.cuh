@@ -45,28 +45,37 @@ DFA_HD Interval cache_append_range(int len, int n, int j, int page_size) {
 // A page number a kernel may follow.
 DFA_HD bool cache_page_ok(int page, int num_pages) { return page >= 0 && page < num_pages; }
 
-// Split of the cached keys over work items.  The items of all requests should
-// number about `target`: chunk = total / target keys each, rounded up to
-// whole 64-key steps and never below kCacheMinChunk, where an item's set-up
-// and its partial result would cost more than its keys.
-constexpr int kCacheMinChunk = 256;
-DFA_HD int cache_chunk(long long total_keys, int target) {
-  long long c = (total_keys + target - 1) / target;
-  c = (c + 63) / 64 * 64;
-  if (c < kCacheMinChunk) c = kCacheMinChunk;
-  return c > (1 << 30) ? (1 << 30) : static_cast<int>(c);
+// Split of a launch over its blocks.  A segment is one request, key/value head
+// and tile of query rows; it counts a unit for every `unit` cached keys
+// (unit 0: none, the segment is not to be cut) and `finish` units more for
+// what every segment costs: its queries, own keys and read-out.  The units of
+// all segments, in order, are dealt to the blocks in equal runs: block x takes
+// [cache_run(x), cache_run(x + 1)).  A run may end among a segment's key
+// units, and the pieces are joined afterwards; the block that reaches the
+// finish units has the segment's end, a run that begins inside them skips the
+// rest.
+DFA_HD int cache_key_units(int len, int unit) { return unit > 0 && len > 0 ? (len - 1) / unit + 1 : 0; }
+DFA_HD int cache_units(int len, int n, int unit, int finish) {
+  return n > 0 ? cache_key_units(len, unit) + finish : 0;
 }
-// Items of a request with `len` cached keys and `n` new rows.
-DFA_HD int cache_items(int len, int n, int chunk) {
-  if (n <= 0) return 0;
-  return len <= chunk ? 1 : (len + chunk - 1) / chunk;
+// Blocks that get work: at most `limit`, at least `least` units each.
+DFA_HD int cache_blocks(long long total, int limit, int least) {
+  const long long n = (total + least - 1) / least;
+  return static_cast<int>(n < limit ? n : limit);
+}
+DFA_HD long long cache_run(int x, long long total, int blocks) { return x * total / blocks; }
+// The block whose run holds unit w.
+DFA_HD int cache_owner(long long w, long long total, int blocks) {
+  return static_cast<int>(((w + 1) * blocks - 1) / total);
 }
 
 // One past the last own key that own row i of n sees: the rows of its block
-// or earlier ones, for positions len + i and blocks of bs tokens from 0.
+// or earlier ones, for positions len + i and blocks of bs tokens from 0.  In
+// unsigned 32 bits: len <= 2^30, i < n <= 2^24 and bs < 2^31 leave room.
 DFA_HD int cache_own_end(int len, int i, int n, int bs) {
-  const long long e = ((static_cast<long long>(len) + i) / bs + 1) * bs - len;
-  return e < n ? static_cast<int>(e) : n;
+  const unsigned b = static_cast<unsigned>(bs);
+  const unsigned e = ((static_cast<unsigned>(len) + i) / b + 1u) * b - len;
+  return e < static_cast<unsigned>(n) ? static_cast<int>(e) : n;
 }
 
 }  // namespace dfa

@@ -28,204 +28,66 @@
 // e4m3 tiles: the head dims (and the keys) may be numbered in any order
 // inside a product, so each thread takes 16 contiguous bytes of a token,
 // which are the operands of four k steps of Q K^T or 16 column tiles of P V.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
 #include <cmath>
 
-#include "cache.cuh"
+#include "cache_fwd.cuh"
 #include "dfa.h"
-#include "params.cuh"
-#include "sm100.cuh"
 
 namespace dfa {
 namespace {
 
 constexpr int kUnit = 32;  // keys per unit
 
-struct CacheFwdParams {
-  CUtensorMap tm_k, tm_v;  // (headdim, kv_heads * page_size, pages) bytes
-  const __nv_bfloat16* q;  // (rows, heads, headdim), strided
-  const __nv_bfloat16* k;  // own keys (rows, kv_heads, headdim) or null
-  const __nv_bfloat16* v;
-  long long q_sr, q_sh, k_sr, k_sh, v_sr, v_sh;
-  const float* k_scale;  // (pages, kv_heads)
-  const float* v_scale;
-  const int* block_table;
-  const int* cache_lens;
-  const int* cu_new;
-  __nv_bfloat16* out;  // (rows, heads, headdim)
-  float* lse;          // (heads, rows)
-  float* part_o;       // (items, kv_heads, tile rows of the request, headdim)
-  float* part_lse;     // (items, kv_heads, tile rows of the request), log2
-  unsigned* status;
-  int batch, rows, max_new, H, Hk, G, bs;
-  int page_size, page_shift, num_pages, max_pages;
-  int tiles;    // row tiles per key/value head
-  int target;   // items wanted over all requests
-  int cap;      // items there is room for
-  int part_rows;  // rows of a partial result: tiles * tile rows
-  float scale_log2;
-};
-
-// One request's sizes, checked: a length past its table or rows past the
-// packed ones are errors, and the request is then taken as empty.
-struct Request {
-  int len, row0, n;
-};
-__device__ __forceinline__ Request load_request(const CacheFwdParams& p, int b, bool* bad) {
-  const int len = p.cache_lens[b], r0 = p.cu_new[b], r1 = p.cu_new[b + 1];
-  const bool ok = len >= 0 && len <= p.max_pages * p.page_size && r0 >= 0 && r1 >= r0 &&
-                  r1 <= p.rows && r1 - r0 <= p.max_new;
-  if (!ok) {
-    *bad = true;
-    return {0, 0, 0};
-  }
-  return {len, r0, r1 - r0};
-}
-
-// The split of the launch, found by every warp for itself: chunk from the
-// sum of the lengths, then the request that item x falls to.
-struct Item {
-  int b, split, splits, base;  // request, its chunk and number of chunks, its first item
-  int chunk, total;            // keys per chunk; items in all
-  Request rq;
-};
-__device__ __forceinline__ Item find_item(const CacheFwdParams& p, int x, bool* bad) {
-  const int lane = threadIdx.x & 31;
-  const int per = (p.batch + 31) / 32;
-  const int b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
-  long long keys = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(p, b, bad);
-    if (r.n > 0) keys += r.len;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, off);
-  Item it;
-  it.chunk = cache_chunk(keys, p.target);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(p, b, bad);
-    mine += cache_items(r.len, r.n, it.chunk);
-  }
-  int upto = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, upto, off);
-    if (lane >= off) upto += o;
-  }
-  it.total = min(__shfl_sync(0xffffffffu, upto, 31), p.cap);
-  it.b = -1;
-  if (x >= it.total) return it;
-  int at = upto - mine;
-  int fb = -1, fsplit = 0, fsplits = 0, fbase = 0;
-  Request frq = {0, 0, 0};
-  if (x >= at && x < upto) {
-    for (int b = b0; b < b1; ++b) {
-      const Request r = load_request(p, b, bad);
-      const int items = cache_items(r.len, r.n, it.chunk);
-      if (x < at + items) {
-        fb = b, fsplit = x - at, fsplits = items, fbase = at, frq = r;
-        break;
-      }
-      at += items;
-    }
-  }
-  const int src = __ffs(__ballot_sync(0xffffffffu, fb >= 0)) - 1;
-  it.b = __shfl_sync(0xffffffffu, fb, src);
-  it.split = __shfl_sync(0xffffffffu, fsplit, src);
-  it.splits = __shfl_sync(0xffffffffu, fsplits, src);
-  it.base = __shfl_sync(0xffffffffu, fbase, src);
-  it.rq.len = __shfl_sync(0xffffffffu, frq.len, src);
-  it.rq.row0 = __shfl_sync(0xffffffffu, frq.row0, src);
-  it.rq.n = __shfl_sync(0xffffffffu, frq.n, src);
-  return it;
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 // D (16 x 8, float32) += A (16 x 16) B (16 x 8).
 __device__ __forceinline__ void mma_f16(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 values (low / high half of w) as f16, exact.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
-      : "=r"(h)
-      : "r"(w));
-  return h;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}"
-      : "=r"(h)
-      : "r"(w));
-  return h;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  ld_shared_v4(addr, v.x, v.y, v.z, v.w);
-  return v;
-}
-__device__ __forceinline__ float pow2_bits(int e) { return __int_as_float((e + 127) << 23); }
-
-// Probabilities are 2^(s - m + kShift); the reference maximum m follows a
-// new maximum only when that exceeds it by more than kSlack, so that most
-// units rescale nothing.  kShift + kSlack < 16 keeps f16 probabilities
-// finite, and kShift moves f16's smallest subnormal to 2^-30 of the maximum.
-constexpr float kShift = 6.f;
-constexpr float kSlack = 8.f;
 
 template <int D, int MT, int WR, int WK, int STAGES>
 struct CacheTile {
   static constexpr int kThreads = 32 * WR * WK;
+  static constexpr int kResident = D == 256 ? 1 : D == 64 && MT == 1 ? 3 : 2;  // blocks per SM
   static constexpr int kRows = 16 * MT * WR;
   static constexpr int kUnitBytes = kUnit * D;  // of k, and of v
   static constexpr int kRing = WK * STAGES * 2 * kUnitBytes;
   static constexpr int kFrags = (D / 64) * 4;  // k steps of Q K^T
   static constexpr int kQ = WR * MT * kFrags * 512;
-  static constexpr int kPitch = D + 4;  // floats per row of a group's output at the join
-  static constexpr int kJoin = WK * kRows * kPitch * 4;
-  static constexpr int kArea = kRing > kJoin ? kRing : kJoin;
-  // ring (1024-byte aligned) | q fragments | row factors | statistics | barriers
-  static constexpr int kOffQ = kArea;
+  static constexpr int kPitch = D + 4;   // floats per row of a group's output at the join
+  static constexpr int kHalfK = WK / 2;  // groups that keep an output at the join
+  static constexpr int kJoin = kHalfK * kRows * kPitch * 4;
+  // ring (1024-byte aligned) | join | q fragments | row factors | statistics | barriers
+  static constexpr int kOffJoin = kRing;
+  static constexpr int kOffQ = kOffJoin + kJoin;
   static constexpr int kOffFactor = kOffQ + kQ;
   static constexpr int kOffStat = kOffFactor + kRows * 4;  // m, l per group and row
   static constexpr int kOffC = kOffStat + WK * kRows * 8;
   static constexpr int kOffBar = (kOffC + WK * WR * 4 + 7) / 8 * 8;
   static constexpr int kOffFlag = kOffBar + WK * STAGES * 16;
   static constexpr int kSmem = kOffFlag + 16 + 1024;
+  static_assert(WK % 2 == 0 && kSmem <= 232448, "shared memory budget");
 };
+
+// Plain loads: the compiler may move them among the products, but not over a
+// barrier wait (which clobbers memory).
+__device__ __forceinline__ uint4 load16(const uint8_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
 
 // 16-byte chunk c of token row r inside a TMA tile: the tile's swizzle.
 template <int D>
-__device__ __forceinline__ uint32_t tile_addr(uint32_t base, int r, int c) {
+__device__ __forceinline__ const uint8_t* tile_at(const uint8_t* base, int r, int c) {
   if constexpr (D == 64) return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   else return base + (c >> 3) * (kUnit * 128) + r * 128 + (((c ^ r) & 7) << 4);
 }
@@ -240,7 +102,8 @@ __device__ __forceinline__ int key_of(int n) {
 }
 
 template <int D, int MT, int WR, int WK, int STAGES>
-__global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
+__global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
+                                  CacheTile<D, MT, WR, WK, STAGES>::kResident)
     dfa_cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
   using T = CacheTile<D, MT, WR, WK, STAGES>;
   constexpr int kSeg = D / 64;       // 64-dim segments of Q K^T
@@ -273,36 +136,36 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
   grid_dependency_wait();
   grid_launch_dependents();
   bool bad = false;
-  const Item it = find_item(p, blockIdx.y, &bad);
+  Piece w = first_piece(p, blockIdx.x, &bad);
   if (bad) atomicOr(p.status, kStatusIndex);
-  if (it.b < 0) return;  // the whole block
-  const int h = blockIdx.x / p.tiles, tile = blockIdx.x - h * p.tiles;
-  const int R = it.rq.n * p.G;  // rows of the request and key/value head
-  const int row_base = tile * T::kRows;
-  if (row_base >= R) return;
-  const int key_lo = it.split * it.chunk;
-  const int key_hi = min(it.rq.len, key_lo + it.chunk);
-  const int units = key_hi > key_lo ? (key_hi - key_lo + kUnit - 1) / kUnit : 0;
-  __syncthreads();  // barriers initialised
+  if (w.b < 0) return;  // the whole block
+  __syncthreads();      // barriers initialised
   const AbortFlag ab{const_cast<int*>(s_flag), p.status};
 
-  // The units of this group: wk, wk + WK, ...  Lane l keeps the pages and
-  // scales of the group's units 32 i + l; a unit of a 16-token page spans two.
-  const int my_units = units > wk ? (units - wk + WK - 1) / WK : 0;
+  // A piece's 32-key units go to the groups in turn: group wk takes units wk,
+  // wk + WK, ...  Lane l keeps the pages (and scales) of the group's units 32 i
+  // + l; a unit of 16-token pages spans two.
   const bool two = p.page_size < kUnit;
-  const int* table = p.block_table + static_cast<long long>(it.b) * p.max_pages;
-  auto load_pages = [&](int u, int* page) {  // of the group's u-th unit
+  auto key_first = [&](const Piece& x) { return piece_begin(p, x); };
+  auto key_end = [&](const Piece& x) { return piece_end(p, x); };
+  auto group_units = [&](const Piece& x) {
+    const int n = key_end(x) - key_first(x);
+    const int units = n > 0 ? (n + kUnit - 1) / kUnit : 0;
+    return units > wk ? (units - wk + WK - 1) / WK : 0;
+  };
+  auto load_pages = [&](const Piece& x, int units, int u, int* page) {  // of the group's unit u
     page[0] = page[1] = -1;
-    if (u >= my_units) return;
-    const int key = key_lo + (wk + u * WK) * kUnit;
+    if (u >= units) return;
+    const int key = key_first(x) + (wk + u * WK) * kUnit;
+    const int* table = p.block_table + static_cast<long long>(x.b) * p.max_pages;
     page[0] = table[key >> p.page_shift];
-    if (two && key + 16 < key_hi) page[1] = table[(key + 16) >> p.page_shift];
-    if (!cache_page_ok(page[0], p.num_pages) ||
-        (two && key + 16 < key_hi && !cache_page_ok(page[1], p.num_pages)))
+    const bool second = two && key + 16 < key_end(x);
+    if (second) page[1] = table[(key + 16) >> p.page_shift];
+    if (!cache_page_ok(page[0], p.num_pages) || (second && !cache_page_ok(page[1], p.num_pages)))
       atomicOr(p.status, kStatusIndex);
     if (!two) page[1] = page[0];
   };
-  auto load_scales = [&](const int* page, float* ks, float* vs) {
+  auto load_scales = [&](int h, const int* page, float* ks, float* vs) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool ok = cache_page_ok(page[i], p.num_pages);
@@ -313,74 +176,147 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
   };
   const uint32_t ring = smem0 + wk * STAGES * 2 * T::kUnitBytes;
   const uint32_t gbar = bars + 16 * wk * STAGES;
-  // Lane 0 of the group's first warp fills stage s with a unit's boxes.
-  auto issue = [&](int u, int s, int page0, int page1) {
-    const uint32_t dst = ring + s * 2 * T::kUnitBytes, bar = gbar + 16 * s;
-    const int key = key_lo + (wk + u * WK) * kUnit;
-    const bool ok0 = cache_page_ok(page0, p.num_pages);
-    const bool ok1 = two && cache_page_ok(page1, p.num_pages);
-    const int rows = two ? 16 : kUnit;
-    const uint32_t bytes = (ok0 ? rows * D * 2 : 0) + (ok1 ? rows * D * 2 : 0);
-    mbar_arrive_expect_tx(bar, bytes);
-    const int off = h * p.page_size + (key & (p.page_size - 1));
+  // Loads run ahead of the products, over the ends of pieces: the first warp
+  // of a group walks the run on its own (`la`) and fills each stage of the
+  // group's ring as it comes free.
+  Piece la = w;
+  int la_units = group_units(la), la_u = 0, issued = 0;
+  int la_page[2];
+  auto ahead = [&]() -> bool {
+    while (la.b >= 0 && la_u >= la_units) {
+      next_piece(p, la);
+      if (la.b < 0) return true;
+      la_units = group_units(la);
+      la_u = 0;
+    }
+    if (la.b < 0) return true;
+    const int h = la.seg / row_tiles(p, la.rq);
+    if ((la_u & 31) == 0) {
+      load_pages(la, la_units, la_u + lane, la_page);
 #pragma unroll
-    for (int half = 0; half < kHalf; ++half) {
-      const uint32_t d = dst + half * kUnit * 128;
-      if (ok0) {
-        tma_load_3d(d, &p.tm_k, bar, half * 128, off, page0);
-        tma_load_3d(d + T::kUnitBytes, &p.tm_v, bar, half * 128, off, page0);
+      for (int i = 0; i < 2; ++i)
+        if (cache_page_ok(la_page[i], p.num_pages)) {  // the products read them next
+          const long long at = static_cast<long long>(la_page[i]) * p.Hk + h;
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(p.k_scale + at));
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(p.v_scale + at));
+        }
+    }
+    const int page0 = __shfl_sync(0xffffffffu, la_page[0], la_u & 31);
+    const int page1 = __shfl_sync(0xffffffffu, la_page[1], la_u & 31);
+    const int s = issued % STAGES;
+    const uint32_t dst = ring + s * 2 * T::kUnitBytes, bar = gbar + 16 * s;
+    if (issued >= STAGES && !mbar_wait_warp(bar + 8, (issued / STAGES - 1) & 1, ab)) return false;
+    if (lane == 0) {
+      const int key = key_first(la) + (wk + la_u * WK) * kUnit;
+      const bool ok0 = cache_page_ok(page0, p.num_pages);
+      const bool ok1 = two && cache_page_ok(page1, p.num_pages);
+      const int rows = two ? 16 : kUnit;
+      mbar_arrive_expect_tx(bar, (ok0 ? rows * D * 2 : 0) + (ok1 ? rows * D * 2 : 0));
+      const int off = h * p.page_size + (key & (p.page_size - 1));
+#pragma unroll
+      for (int half = 0; half < kHalf; ++half) {
+        const uint32_t d = dst + half * kUnit * 128;
+        if (ok0) {
+          tma_load_3d(d, &p.tm_k, bar, half * 128, off, page0);
+          tma_load_3d(d + T::kUnitBytes, &p.tm_v, bar, half * 128, off, page0);
+        }
+        if (ok1) {
+          constexpr int kRow = D == 64 ? 64 : 128;
+          const int off1 = h * p.page_size + ((key + 16) & (p.page_size - 1));
+          tma_load_3d(d + 16 * kRow, &p.tm_k, bar, half * 128, off1, page1);
+          tma_load_3d(d + T::kUnitBytes + 16 * kRow, &p.tm_v, bar, half * 128, off1, page1);
+        }
       }
-      if (ok1) {
-        constexpr int kRow = D == 64 ? 64 : 128;
-        const int off1 = h * p.page_size + ((key + 16) & (p.page_size - 1));
-        tma_load_3d(d + 16 * kRow, &p.tm_k, bar, half * 128, off1, page1);
-        tma_load_3d(d + T::kUnitBytes + 16 * kRow, &p.tm_v, bar, half * 128, off1, page1);
-      }
+    }
+    __syncwarp();
+    ++issued;
+    ++la_u;
+    return true;
+  };
+  if (wr == 0) {
+#pragma unroll 1
+    for (int s = 0; s < STAGES; ++s) ahead();
+  }
+  int consumed = 0;
+  bool ok = true;
+
+#pragma unroll 1
+  for (; w.b >= 0 && ok; next_piece(p, w)) {
+  const int rtiles = row_tiles(p, w.rq);
+  const int h = w.seg / rtiles, tile = w.seg - h * rtiles;
+  const int R = w.rq.n * p.G;  // rows of the request and key/value head
+  const int row_base = tile * T::kRows;
+  const int key_lo = key_first(w), key_hi = key_end(w), my_units = group_units(w);
+  // The piece's queries: the f16 fragments of the cached keys' products (built
+  // by the first group for all) and the bf16 ones of the own keys', which stay
+  // in registers where there is room (kHoldQ) and are read again where not.
+  constexpr bool kHoldQ = MT * D <= 128;
+  auto load_q = [&](int mt, int i, int sg, uint4* q2) {
+    const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+    q2[0] = q2[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < R) {
+      const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
+      const __nv_bfloat16* src =
+          p.q + (w.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 64 * sg + 16 * t;
+      q2[0] = *reinterpret_cast<const uint4*>(src);
+      q2[1] = *reinterpret_cast<const uint4*>(src + 8);
     }
   };
-  static_assert(STAGES < 16, "the next pages are read 24 units ahead");
-  int page[2], next_page[2] = {-1, -1};
-  float ks[2], vs[2], next_ks[2] = {0.f, 0.f}, next_vs[2] = {0.f, 0.f};
-  load_pages(lane, page);
-  if (wr == 0) {
+  uint4 qv[kHoldQ ? MT : 1][2][kSeg][2];
+  if constexpr (kHoldQ) {
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) {
-      const int p0 = __shfl_sync(0xffffffffu, page[0], s);
-      const int p1 = __shfl_sync(0xffffffffu, page[1], s);
-      if (lane == 0 && s < my_units) issue(s, s, p0, p1);
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int sg = 0; sg < kSeg; ++sg) load_q(mt, i, sg, qv[mt][i][sg]);
+  }
+  int own = 0;
+  if (p.k != nullptr && w.last())
+    own = cache_own_end(w.rq.len, min(R - 1, row_base + T::kRows - 1) / p.G, w.rq.n, p.bs);
+  auto load_own_k = [&](int k0, int sg, int n, uint4* k2) {
+    const int key = k0 + 8 * n + g;
+    k2[0] = k2[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (key < w.rq.n) {
+      const __nv_bfloat16* src =
+          p.k + (w.rq.row0 + key) * p.k_sr + h * p.k_sh + 64 * sg + 16 * t;
+      k2[0] = *reinterpret_cast<const uint4*>(src);
+      k2[1] = *reinterpret_cast<const uint4*>(src + 8);
+    }
+  };
+  // the first own unit's keys of this group, on their way early
+  uint4 kw0[kHoldQ ? kSeg : 1][2][2];
+  if constexpr (kHoldQ) {
+    if (16 * wk < own) {
+#pragma unroll
+      for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) load_own_k(16 * wk, sg, n, kw0[sg][n]);
     }
   }
-  load_scales(page, ks, vs);
-
-  // Q fragments of the tile, built by the first group: f16 after the row's
-  // power of two, in the order the products read them.
+  int page[2];
+  float ks[2], vs[2];
+  load_pages(w, my_units, lane, page);
+  load_scales(h, page, ks, vs);
   if (wk == 0) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      int e[2];
-      uint4 w[2][kSeg][2];
+      float inv[2];
+      uint4 qt[2][kSeg][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+#pragma unroll
+        for (int sg = 0; sg < kSeg; ++sg) {
+          if constexpr (kHoldQ) qt[i][sg][0] = qv[mt][i][sg][0], qt[i][sg][1] = qv[mt][i][sg][1];
+          else load_q(mt, i, sg, qt[i][sg]);
+        }
         unsigned top = 0;
 #pragma unroll
         for (int sg = 0; sg < kSeg; ++sg)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) w[i][sg][c] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R) {
-          const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
-          const __nv_bfloat16* src = p.q + (it.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 16 * t;
-#pragma unroll
-          for (int sg = 0; sg < kSeg; ++sg)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              w[i][sg][c] = *reinterpret_cast<const uint4*>(src + 64 * sg + 8 * c);
-        }
-#pragma unroll
-        for (int sg = 0; sg < kSeg; ++sg)
-#pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const uint32_t v[4] = {w[i][sg][c].x, w[i][sg][c].y, w[i][sg][c].z, w[i][sg][c].w};
+            const uint4& q4 = qt[i][sg][c];
+            const uint32_t v[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const unsigned lo = v[x] & 0x7fffu, hi = (v[x] >> 16) & 0x7fffu;
@@ -390,11 +326,11 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // 2^-e brings the row's largest magnitude into [2^14, 2^15)
-        e[i] = static_cast<int>(top >> 7) - 127 - 14;
-        if (e[i] < -100) e[i] = -100;
-        if (t == 0) s_factor[16 * (wr * MT + mt) + g + 8 * i] = pow2_bits(e[i]) * p.scale_log2;
+        int e = static_cast<int>(top >> 7) - 127 - 14;
+        if (e < -100) e = -100;
+        if (t == 0) s_factor[16 * (wr * MT + mt) + g + 8 * i] = pow2_bits(e) * p.scale_log2;
+        inv[i] = pow2_bits(-e);
       }
-      const float inv[2] = {pow2_bits(-e[0]), pow2_bits(-e[1])};
 #pragma unroll
       for (int sg = 0; sg < kSeg; ++sg)
 #pragma unroll
@@ -402,7 +338,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
           uint32_t a[2][2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint4& q4 = w[i][sg][s >> 1];
+            const uint4& q4 = qt[i][sg][s >> 1];
             const uint32_t x0 = s & 1 ? q4.z : q4.x, x1 = s & 1 ? q4.w : q4.y;
             a[i][0] = pack_f16x2(__uint_as_float(x0 << 16) * inv[i],
                                  __uint_as_float(x0 & 0xffff0000u) * inv[i]);
@@ -415,7 +351,6 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
         }
     }
   }
-  __syncthreads();
 
   float o[MT][kOut][4];
   float m[MT][2], l[MT][2], factor[MT][2];
@@ -425,7 +360,6 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
     for (int i = 0; i < 2; ++i) {
       m[mt][i] = -INFINITY;
       l[mt][i] = 0.f;
-      factor[mt][i] = s_factor[16 * (wr * MT + mt) + g + 8 * i];
     }
 #pragma unroll
     for (int e = 0; e < kOut; ++e)
@@ -434,7 +368,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
   }
   float c = pow2_bits(kCacheMinExp);  // the output's unit: the largest value scale so far
   float inv_c = pow2_bits(-kCacheMinExp);
-  const uint32_t qbase = smem0 + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
+  const uint8_t* qbase = smem + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
 
   // New maxima of a unit's scaled scores: returns the factors the output and
   // the sums shrink by (1 where the reference stays).
@@ -476,16 +410,163 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
     }
   };
 
-  int done = 0;  // units finished
-  for (; done < my_units; ++done) {
-    const int u = done, stage = u % STAGES;
-    const uint32_t phase = (u / STAGES) & 1;
-    // the next 32 units' pages and scales, read ahead of their use
-    if ((u & 31) == 8) load_pages(u + 24 + lane, next_page);
-    if ((u & 31) == 12) load_scales(next_page, next_ks, next_vs);
-    if ((u & 31) == 0 && u > 0) {
+  // Own keys and values first, bf16, with the segment's end, while the cached
+  // keys are on their way: units of 16 keys, the groups in turn, operands
+  // straight from global memory.
+  {
+#pragma unroll 1
+    for (int k0 = 16 * wk; k0 < own; k0 += 16 * WK) {
+      float sc[MT][2][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) page[i] = next_page[i], ks[i] = next_ks[i], vs[i] = next_vs[i];
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
+#pragma unroll
+      for (int sg = 0; sg < kSeg; ++sg) {
+        uint4 kx[2][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if (kHoldQ && k0 == 16 * wk) kx[n][0] = kw0[kHoldQ ? sg : 0][n][0], kx[n][1] = kw0[kHoldQ ? sg : 0][n][1];
+          else load_own_k(k0, sg, n, kx[n]);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint4 qx[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (kHoldQ) qx[i][0] = qv[mt][i][sg][0], qx[i][1] = qv[mt][i][sg][1];
+            else load_q(mt, i, sg, qx[i]);
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const uint4& q0 = qx[0][s >> 1];
+            const uint4& q1 = qx[1][s >> 1];
+            const uint4 a = s & 1 ? make_uint4(q0.z, q1.z, q0.w, q1.w)
+                                  : make_uint4(q0.x, q1.x, q0.y, q1.y);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint4& k4 = kx[n][s >> 1];
+              mma_bf16(sc[mt][n], a, s & 1 ? k4.z : k4.x, s & 1 ? k4.w : k4.y);
+            }
+          }
+        }
+      }
+      float um[MT][2];
+      int end[MT][2];  // one past the last own key of the thread's rows
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+          end[mt][i] = r < R ? cache_own_end(w.rq.len, r / p.G, w.rq.n, p.bs) : 0;
+          um[mt][i] = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float& s = sc[mt][n][2 * i + x];
+              s = k0 + 8 * n + 2 * t + x < end[mt][i] ? s * p.scale_log2 : -INFINITY;
+              um[mt][i] = fmaxf(um[mt][i], s);
+            }
+        }
+      rebase(um, fmaxf(c, 1.f));
+      uint4 pf[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float r0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kShift;
+        const float r1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kShift;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float e = ex2_approx(sc[mt][n][x] - (x < 2 ? r0 : r1));
+            l[mt][x >> 1] += e;
+            sc[mt][n][x] = e * inv_c;
+          }
+        pf[mt] = make_uint4(pack_bf16x2(sc[mt][0][0], sc[mt][0][1]),
+                            pack_bf16x2(sc[mt][0][2], sc[mt][0][3]),
+                            pack_bf16x2(sc[mt][1][0], sc[mt][1][1]),
+                            pack_bf16x2(sc[mt][1][2], sc[mt][1][3]));
+      }
+      // A row's probability of an own key it does not see is 0, but 0 times a
+      // value that is not finite is not: such values leave the product and
+      // are added to the rows that see them.
+      bool odd = false;
+#pragma unroll
+      for (int half = 0; half < kHalf; ++half)
+#pragma unroll
+        for (int part = 0; part < kCols / 8; ++part) {  // 8 dims at a time
+          uint32_t vw[4][4];
+          const int dim = D == 64 ? 8 * g : 128 * half + 16 * key_of<D>(g) + 8 * part;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = k0 + 8 * (x >> 1) + 2 * t + (x & 1);
+            uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
+            if (key < w.rq.n)
+              v4 = *reinterpret_cast<const uint4*>(p.v + (w.rq.row0 + key) * p.v_sr + h * p.v_sh +
+                                                   dim);
+            vw[x][0] = v4.x, vw[x][1] = v4.y, vw[x][2] = v4.z, vw[x][3] = v4.w;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if ((vw[x][y] & 0x7f80u) == 0x7f80u) vw[x][y] &= 0xffff0000u, odd = true;
+              if ((vw[x][y] & 0x7f800000u) == 0x7f800000u) vw[x][y] &= 0xffffu, odd = true;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t b0 = __byte_perm(vw[0][y], vw[1][y], z ? 0x7632 : 0x5410);
+              const uint32_t b1 = __byte_perm(vw[2][y], vw[3][y], z ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt], b0, b1);
+            }
+          }
+        }
+      if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+        for (int key = k0; key < min(k0 + 16, w.rq.n); ++key) {
+          const __nv_bfloat16* src = p.v + (w.rq.row0 + key) * p.v_sr + h * p.v_sh;
+#pragma unroll
+          for (int e = 0; e < kOut; ++e)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float y = __bfloat162float(
+                  src[128 * (e / kCols) + kCols * key_of<D>(2 * t + x) + e % kCols]);
+              if (isfinite(y)) continue;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (key < end[mt][i]) o[mt][e][2 * i + x] += y;
+            }
+        }
+      }
+    }
+  }
+
+  __syncthreads();  // the queries' fragments
+  uint4 qf[kHoldQ ? MT : 1][T::kFrags];
+  if constexpr (kHoldQ) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int f = 0; f < T::kFrags; ++f) qf[mt][f] = load16(qbase + (mt * T::kFrags + f) * 512);
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) factor[mt][i] = s_factor[16 * (wr * MT + mt) + g + 8 * i];
+
+#pragma unroll 1
+  for (int u = 0; u < my_units; ++u) {
+    const int stage = consumed % STAGES;
+    if ((u & 31) == 0 && u > 0) {
+      load_pages(w, my_units, u + lane, page);
+      load_scales(h, page, ks, vs);
     }
     float ks0 = __shfl_sync(0xffffffffu, ks[0], u & 31);
     float ks1 = __shfl_sync(0xffffffffu, ks[1], u & 31);
@@ -497,8 +578,9 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
     // valid keys of the unit's 16-key halves
     const int nv0 = cache_page_ok(p0, p.num_pages) ? min(16, key_hi - key) : 0;
     const int nv1 = cache_page_ok(p1, p.num_pages) ? max(0, min(16, key_hi - key - 16)) : 0;
-    const uint32_t kt = ring + stage * 2 * T::kUnitBytes, vt = kt + T::kUnitBytes;
-    if (!mbar_wait_warp(gbar + 16 * stage, phase, ab)) break;
+    const uint8_t* kt = smem + wk * STAGES * 2 * T::kUnitBytes + stage * 2 * T::kUnitBytes;
+    const uint8_t* vt = kt + T::kUnitBytes;
+    if (!(ok = mbar_wait_warp(gbar + 16 * stage, (consumed / STAGES) & 1, ab))) break;
 
     float sc[MT][4][4];
 #pragma unroll
@@ -512,7 +594,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
       uint4 kw[4];
 #pragma unroll
       for (int n = 0; n < 4; ++n)
-        kw[n] = lds128(tile_addr<D>(kt, 8 * n + key_of<D>(g), 4 * sg + t));
+        kw[n] = load16(tile_at<D>(kt, 8 * n + key_of<D>(g), 4 * sg + t));
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
         uint32_t b[4][2];
@@ -524,7 +606,8 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const uint4 a = lds128(qbase + (mt * T::kFrags + sg * 4 + s) * 512);
+          const uint4 a = kHoldQ ? qf[kHoldQ ? mt : 0][sg * 4 + s]
+                                 : load16(qbase + (mt * T::kFrags + sg * 4 + s) * 512);
 #pragma unroll
           for (int n = 0; n < 4; ++n) mma_f16(sc[mt][n], a, b[n][0], b[n][1]);
         }
@@ -590,14 +673,12 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
         for (int x = 0; x < 4; ++x) {
           const int r = 8 * (x >> 1) + key_of<D>(2 * t + (x & 1));
           if constexpr (D == 64) {
-            const uint32_t at = tile_addr<D>(vt, 16 * kk + r, g >> 1) + 8 * (g & 1);
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(vw[x][0]), "=r"(vw[x][1])
-                         : "r"(at)
-                         : "memory");
+            const uint2 w2 = *reinterpret_cast<const uint2*>(
+                tile_at<D>(vt, 16 * kk + r, g >> 1) + 8 * (g & 1));
+            vw[x][0] = w2.x, vw[x][1] = w2.y;
           } else {
-            const uint4 w = lds128(tile_addr<D>(vt, 16 * kk + r, 8 * half + key_of<D>(g)));
-            vw[x][0] = w.x, vw[x][1] = w.y, vw[x][2] = w.z, vw[x][3] = w.w;
+            const uint4 w4 = load16(tile_at<D>(vt, 16 * kk + r, 8 * half + key_of<D>(g)));
+            vw[x][0] = w4.x, vw[x][1] = w4.y, vw[x][2] = w4.z, vw[x][3] = w4.w;
           }
           if (!whole && r >= nv) {
 #pragma unroll
@@ -623,173 +704,8 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
       }
     }
     mbar_arrive_warp(gbar + 16 * stage + 8);
-    // refill the stage
-    const int nu = u + STAGES;
-    if (wr == 0 && nu < my_units) {
-      const bool ahead = (nu >> 5) != (u >> 5);
-      const int n0 = __shfl_sync(0xffffffffu, ahead ? next_page[0] : page[0], nu & 31);
-      const int n1 = __shfl_sync(0xffffffffu, ahead ? next_page[1] : page[1], nu & 31);
-      if (!mbar_wait_warp(gbar + 16 * stage + 8, phase, ab)) break;
-      if (lane == 0) issue(nu, stage, n0, n1);
-    }
-  }
-  if (done < my_units && wr == 0 && lane == 0) {
-    // Giving up: nothing may land in shared memory after the block is gone.
-    for (int s = 0; s < STAGES; ++s) {
-      int last = -1;  // last unit that may have been issued to this stage
-      for (int u = s; u < my_units && u < done + 1 + STAGES; u += STAGES) last = u;
-      if (last >= 0) mbar_wait_limited(gbar + 16 * s, (last / STAGES) & 1, kWaitLimitNs / 8);
-    }
-  }
-
-  // Own keys and values, bf16, with the request's last chunk: units of 16
-  // keys, the groups in turn, operands straight from global memory.
-  if (p.k != nullptr && it.split == it.splits - 1) {
-    const int last_tok = min(R - 1, row_base + T::kRows - 1) / p.G;
-    const int own = cache_own_end(it.rq.len, last_tok, it.rq.n, p.bs);
-    for (int k0 = 16 * wk; k0 < own; k0 += 16 * WK) {
-      float sc[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
-#pragma unroll
-      for (int sg = 0; sg < kSeg; ++sg) {
-        uint4 kw[2][2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = k0 + 8 * n + g;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            kw[n][x] = make_uint4(0u, 0u, 0u, 0u);
-            if (key < it.rq.n)
-              kw[n][x] = *reinterpret_cast<const uint4*>(
-                  p.k + (it.rq.row0 + key) * p.k_sr + h * p.k_sh + 64 * sg + 16 * t + 8 * x);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint4 w[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
-            const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              w[i][x] = make_uint4(0u, 0u, 0u, 0u);
-              if (r < R)
-                w[i][x] = *reinterpret_cast<const uint4*>(
-                    p.q + (it.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 64 * sg + 16 * t + 8 * x);
-            }
-          }
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint4 a = s & 1 ? make_uint4(w[0][s >> 1].z, w[1][s >> 1].z, w[0][s >> 1].w,
-                                               w[1][s >> 1].w)
-                                  : make_uint4(w[0][s >> 1].x, w[1][s >> 1].x, w[0][s >> 1].y,
-                                               w[1][s >> 1].y);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-              mma_bf16(sc[mt][n], a, s & 1 ? kw[n][s >> 1].z : kw[n][s >> 1].x,
-                       s & 1 ? kw[n][s >> 1].w : kw[n][s >> 1].y);
-          }
-        }
-      }
-      float um[MT][2];
-      int end[MT][2];  // one past the last own key of the thread's rows
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
-          end[mt][i] = r < R ? cache_own_end(it.rq.len, r / p.G, it.rq.n, p.bs) : 0;
-          um[mt][i] = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float& s = sc[mt][n][2 * i + x];
-              s = k0 + 8 * n + 2 * t + x < end[mt][i] ? s * p.scale_log2 : -INFINITY;
-              um[mt][i] = fmaxf(um[mt][i], s);
-            }
-        }
-      rebase(um, fmaxf(c, 1.f));
-      uint4 pf[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float r0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kShift;
-        const float r1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kShift;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float e = ex2_approx(sc[mt][n][x] - (x < 2 ? r0 : r1));
-            l[mt][x >> 1] += e;
-            sc[mt][n][x] = e * inv_c;
-          }
-        pf[mt] = make_uint4(pack_bf16x2(sc[mt][0][0], sc[mt][0][1]),
-                            pack_bf16x2(sc[mt][0][2], sc[mt][0][3]),
-                            pack_bf16x2(sc[mt][1][0], sc[mt][1][1]),
-                            pack_bf16x2(sc[mt][1][2], sc[mt][1][3]));
-      }
-      // A row's probability of an own key it does not see is 0, but 0 times a
-      // value that is not finite is not: such values leave the product and
-      // are added to the rows that see them.
-      bool odd = false;
-#pragma unroll
-      for (int half = 0; half < kHalf; ++half)
-#pragma unroll
-        for (int part = 0; part < kCols / 8; ++part) {  // 8 dims at a time
-          uint32_t vw[4][4];
-          const int dim = D == 64 ? 8 * g : 128 * half + 16 * key_of<D>(g) + 8 * part;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = k0 + 8 * (x >> 1) + 2 * t + (x & 1);
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (key < it.rq.n)
-              w = *reinterpret_cast<const uint4*>(p.v + (it.rq.row0 + key) * p.v_sr + h * p.v_sh +
-                                                  dim);
-            vw[x][0] = w.x, vw[x][1] = w.y, vw[x][2] = w.z, vw[x][3] = w.w;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              if ((vw[x][y] & 0x7f80u) == 0x7f80u) vw[x][y] &= 0xffff0000u, odd = true;
-              if ((vw[x][y] & 0x7f800000u) == 0x7f800000u) vw[x][y] &= 0xffffu, odd = true;
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t b0 = __byte_perm(vw[0][y], vw[1][y], z ? 0x7632 : 0x5410);
-              const uint32_t b1 = __byte_perm(vw[2][y], vw[3][y], z ? 0x7632 : 0x5410);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt], b0, b1);
-            }
-          }
-        }
-      if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-        for (int key = k0; key < min(k0 + 16, it.rq.n); ++key) {
-          const __nv_bfloat16* src = p.v + (it.rq.row0 + key) * p.v_sr + h * p.v_sh;
-#pragma unroll
-          for (int e = 0; e < kOut; ++e)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float y = __bfloat162float(
-                  src[128 * (e / kCols) + kCols * key_of<D>(2 * t + x) + e % kCols]);
-              if (isfinite(y)) continue;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (key < end[mt][i]) o[mt][e][2 * i + x] += y;
-            }
-        }
-      }
-    }
+    ++consumed;
+    if (wr == 0 && !(ok = ahead())) break;
   }
 
   // Join the groups: statistics first, then each group's output in a common
@@ -808,40 +724,53 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
       l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
     }
   if (lane == 0) s_c[warp] = c;
-  __syncthreads();  // statistics written; every tile of the ring has been read
+  __syncthreads();  // statistics written
   float c_all = s_c[0];
 #pragma unroll
   for (int i = 1; i < WK * WR; ++i) c_all = fmaxf(c_all, s_c[i]);
-  float* join = reinterpret_cast<float*>(smem);
+  // The upper half of the groups leaves its outputs, the lower half adds its
+  // own to them.
+  float* join = reinterpret_cast<float*>(smem + T::kOffJoin);
+  auto leave = [&](bool add) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = 16 * (wr * MT + mt) + g + 8 * i;
-      float top = s_m[r];
+      for (int i = 0; i < 2; ++i) {
+        const int r = 16 * (wr * MT + mt) + g + 8 * i;
+        float top = s_m[r];
 #pragma unroll
-      for (int x = 1; x < WK; ++x) top = fmaxf(top, s_m[x * T::kRows + r]);
-      const float f = m[mt][i] == -INFINITY ? 0.f : ex2_approx(m[mt][i] - top);
-      const float fo = f * (c / c_all);
-      if (t == 0) s_l[wk * T::kRows + r] = l[mt][i] * f;
-      float* dst = join + (wk * T::kRows + r) * T::kPitch;
-      // columns 2t and 2t + 1 of the column tiles are runs of kCols dims
+        for (int x = 1; x < WK; ++x) top = fmaxf(top, s_m[x * T::kRows + r]);
+        const float f = m[mt][i] == -INFINITY ? 0.f : ex2_approx(m[mt][i] - top);
+        const float fo = f * (c / c_all);
+        if (t == 0) s_l[wk * T::kRows + r] = l[mt][i] * f;
+        float* dst = join + ((wk % T::kHalfK) * T::kRows + r) * T::kPitch;
+        // columns 2t and 2t + 1 of the column tiles are runs of kCols dims
 #pragma unroll
-      for (int half = 0; half < kHalf; ++half)
+        for (int half = 0; half < kHalf; ++half)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int dim = 128 * half + kCols * key_of<D>(2 * t + x);
+          for (int x = 0; x < 2; ++x) {
+            const int dim = 128 * half + kCols * key_of<D>(2 * t + x);
 #pragma unroll
-          for (int e = 0; e < kCols; e += 4)
-            *reinterpret_cast<float4*>(dst + dim + e) =
-                make_float4(o[mt][half * kCols + e][2 * i + x] * fo,
-                            o[mt][half * kCols + e + 1][2 * i + x] * fo,
-                            o[mt][half * kCols + e + 2][2 * i + x] * fo,
-                            o[mt][half * kCols + e + 3][2 * i + x] * fo);
-        }
-    }
+            for (int e = 0; e < kCols; e += 4) {
+              float4 y = make_float4(o[mt][half * kCols + e][2 * i + x] * fo,
+                                     o[mt][half * kCols + e + 1][2 * i + x] * fo,
+                                     o[mt][half * kCols + e + 2][2 * i + x] * fo,
+                                     o[mt][half * kCols + e + 3][2 * i + x] * fo);
+              float4* at = reinterpret_cast<float4*>(dst + dim + e);
+              if (add) {
+                const float4 z = *at;
+                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+              }
+              *at = y;
+            }
+          }
+      }
+  };
+  if (wk >= T::kHalfK) leave(false);
   __syncthreads();
-  const bool single = it.splits == 1;
+  if (wk < T::kHalfK) leave(true);
+  __syncthreads();
+  const bool single = w.whole();
   for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
     const int r = i / (D / 4), d4 = i - r * (D / 4);
     if (row_base + r >= R) break;
@@ -851,6 +780,9 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
     for (int x = 0; x < WK; ++x) {
       sum += s_l[x * T::kRows + r];
       top = fmaxf(top, s_m[x * T::kRows + r]);
+    }
+#pragma unroll
+    for (int x = 0; x < T::kHalfK; ++x) {
       const float4 y =
           *reinterpret_cast<const float4*>(join + (x * T::kRows + r) * T::kPitch + 4 * d4);
       a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
@@ -862,134 +794,133 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads)
     a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
     if (single) {
       const int tok = (row_base + r) / p.G, hq = h * p.G + (row_base + r - tok * p.G);
-      const long long row = it.rq.row0 + tok;
+      const long long row = w.rq.row0 + tok;
       *reinterpret_cast<uint2*>(p.out + (row * p.H + hq) * D + 4 * d4) =
           make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
       if (d4 == 0) p.lse[static_cast<long long>(hq) * p.rows + row] = lse2 * 0.6931471805599453f;
     } else {
-      const long long at =
-          (static_cast<long long>(blockIdx.y) * p.Hk + h) * p.part_rows + row_base + r;
+      const long long at = (2LL * blockIdx.x + (w.first ? 0 : 1)) * T::kRows + r;
       *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
       if (d4 == 0) p.part_lse[at] = lse2;
     }
   }
+  }  // pieces
+  if (!ok && wr == 0 && lane == 0) {
+    // Giving up: nothing may land in shared memory after the block is gone.
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+      mbar_wait_limited(gbar + 16 * (i % STAGES), (i / STAGES) & 1, kWaitLimitNs / 8);
+  }
 }
 
-// The chunks of a request, joined: weights 2^(lse_s - max), one warp a row
-// and query head, the chunks' outputs read once.  Blocks stride over the rows
-// of the requests that were split; nothing to do where none was.
+// The pieces of the segments that a run's end has cut, joined: weights
+// 2^(lse_s - max), one warp a row and query head, the pieces' outputs read
+// once.  Blocks stride over the rows of the requests' cut segments; a request
+// whose segments are all whole is passed over.
 constexpr int kJoinWarps = 8;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     dfa_cache_join_kernel(const __grid_constant__ CacheFwdParams p) {
   constexpr int kVec = D / 32;  // floats per lane
-  grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
-  const int per = (p.batch + 31) / 32;
-  const int b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
-  const int chunk = find_item(p, 0x7fffffff, &bad).chunk;
-  // lane's share of the items and of the rows to join
-  int items = 0;
-  long long rows = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(p, b, &bad);
-    const int n = cache_items(r.len, r.n, chunk);
-    items += n;
-    if (n > 1) rows += static_cast<long long>(r.n) * p.H;
-  }
-  int items_upto = items;
-  long long rows_upto = rows;
+  // The sizes were complete before the launch whose pieces are joined let this
+  // one start; only its results have to be waited for.
+  const Census c = take_census(p, &bad);
+  bool waited = false;
+  // Segments that hold a run's end are found from the runs.
+  for (int x = blockIdx.x; x < c.blocks; x += gridDim.x) {
+    Piece w;
+    const long long lo = cache_run(x, c.total, c.blocks);
+    find_unit(p, c, lo, &bad, &w);
+    const long long start = lo - w.u0;
+    const int x0 = cache_owner(start, c.total, c.blocks);
+    const int x1 = cache_owner(start + w.keys, c.total, c.blocks);
+    // A cut segment is joined once: by the block that begins with it, or else
+    // by the next one, whose run begins inside it.
+    const bool at_start = cache_run(x0, c.total, c.blocks) == start;
+    if (x1 == x0 || x != (at_start ? x0 : x0 + 1)) continue;
+    if (!waited) grid_dependency_wait();
+    waited = true;
+    const int rtiles = row_tiles(p, w.rq);
+    const int h = w.seg / rtiles, row_base = (w.seg - h * rtiles) * p.tile_rows;
+    const int rows = min(p.tile_rows, w.rq.n * p.G - row_base);
+    // the first piece is its block's last unless the block begins with it
+    const int slot0 = 2 * x0 + (at_start ? 0 : 1), n = x1 - x0 + 1;
+    for (int r = warp + kJoinWarps * blockIdx.y; r < rows; r += kJoinWarps * gridDim.y) {
+      auto at = [&](int s) {
+        return static_cast<long long>(s == 0 ? slot0 : 2 * (x0 + s)) * p.tile_rows + r;
+      };
+      // kBatch pieces at a time: their outputs and, a lane each, their lse are
+      // read together, then weighed against the maximum so far
+      constexpr int kBatch = D == 256 ? 8 : 16;
+      float top = -INFINITY, sum = 0.f, acc[kVec];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, items_upto, off);
-    const long long c = __shfl_up_sync(0xffffffffu, rows_upto, off);
-    if (lane >= off) items_upto += a, rows_upto += c;
-  }
-  const long long total = __shfl_sync(0xffffffffu, rows_upto, 31);
-  for (long long w = static_cast<long long>(blockIdx.x) * kJoinWarps + warp; w < total;
-       w += static_cast<long long>(gridDim.x) * kJoinWarps) {
-    // the request of row w
-    int fb = -1, fbase = 0, fitems = 0, fin = 0;
-    Request frq = {0, 0, 0};
-    if (w >= rows_upto - rows && w < rows_upto) {
-      long long at = rows_upto - rows;
-      int base = items_upto - items;
-      for (int b = b0; b < b1; ++b) {
-        const Request r = load_request(p, b, &bad);
-        const int n = cache_items(r.len, r.n, chunk);
-        const long long mine = n > 1 ? static_cast<long long>(r.n) * p.H : 0;
-        if (w < at + mine) {
-          fb = b, fbase = base, fitems = n, frq = r, fin = static_cast<int>(w - at);
-          break;
+      for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+      for (int s0 = 0; s0 < n; s0 += kBatch) {
+        float y[kBatch][kVec];
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) {
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) y[s][i] = 0.f;
+          if (s0 + s < n) {
+            const float* src = p.part_o + at(s0 + s) * D + lane * kVec;
+            if constexpr (kVec == 2) {
+              *reinterpret_cast<float2*>(y[s]) = *reinterpret_cast<const float2*>(src);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kVec; i += 4)
+                *reinterpret_cast<float4*>(y[s] + i) = *reinterpret_cast<const float4*>(src + i);
+            }
+          }
         }
-        at += mine;
-        base += n;
+        const float lse = lane < kBatch && s0 + lane < n ? p.part_lse[at(s0 + lane)] : -INFINITY;
+        float m = lse;
+#pragma unroll
+        for (int off = kBatch / 2; off > 0; off >>= 1)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        m = fmaxf(top, __shfl_sync(0xffffffffu, m, 0));
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float shrink = ex2_approx(top - ref), wgt = ex2_approx(lse - ref);
+        top = m;
+        sum *= shrink;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] *= shrink;
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) {
+          const float ws = __shfl_sync(0xffffffffu, wgt, s);
+          sum += ws;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] = fmaf(ws, y[s][i], acc[i]);
+        }
       }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const int tok = (row_base + r) / p.G, hq = h * p.G + (row_base + r - tok * p.G);
+      const long long row = w.rq.row0 + tok;
+      __nv_bfloat16* dst = p.out + (row * p.H + hq) * D + lane * kVec;
+#pragma unroll
+      for (int i = 0; i < kVec; i += 2)
+        *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+      if (lane == 0)
+        p.lse[static_cast<long long>(hq) * p.rows + row] =
+            sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * 0.6931471805599453f;
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, fb >= 0)) - 1;
-    const int base = __shfl_sync(0xffffffffu, fbase, src);
-    const int n = __shfl_sync(0xffffffffu, fitems, src);
-    const int in = __shfl_sync(0xffffffffu, fin, src);
-    const int row0 = __shfl_sync(0xffffffffu, frq.row0, src);
-    const int tok = in / p.H, hq = in - tok * p.H, h = hq / p.G;
-    const long long first = (static_cast<long long>(base) * p.Hk + h) * p.part_rows +
-                            tok * p.G + (hq - h * p.G);
-    const long long step = static_cast<long long>(p.Hk) * p.part_rows;
-    float top = -INFINITY;
-    for (int s = lane; s < n; s += 32) top = fmaxf(top, p.part_lse[first + s * step]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc[kVec];
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float wgt = ex2_approx(p.part_lse[first + s * step] - ref);
-      sum += wgt;
-      const float* src_o = p.part_o + (first + s * step) * D + lane * kVec;
-      float x[kVec];
-      if constexpr (kVec == 2) {
-        *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src_o);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; i += 4)
-          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(src_o + i);
-      }
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = fmaf(wgt, x[i], acc[i]);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long row = row0 + tok;
-    __nv_bfloat16* dst = p.out + (row * p.H + hq) * D + lane * kVec;
-#pragma unroll
-    for (int i = 0; i < kVec; i += 2)
-      *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-    if (lane == 0)
-      p.lse[static_cast<long long>(hq) * p.rows + row] =
-          sum == 0.f ? -INFINITY : (ref + lg2_approx(sum)) * 0.6931471805599453f;
   }
+  // What comes after this launch may count on the one before it.
+  if (!waited) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host
 
-// The launch's shape for given sizes: tile rows, row tiles, item target and
-// room, blocks resident on the device.
+// The launch's shape for given sizes: query rows per segment, blocks.
 struct CachePlan {
-  int tile_rows, tiles, target, cap;
+  int tile_rows, blocks;
 };
-CachePlan cache_plan_for(int batch, int max_new, int G, int Hk, int d, int sms) {
+CachePlan cache_plan_for(int max_new, int G, int d, int sms) {
   CachePlan c;
   const long long rows = static_cast<long long>(max_new) * G;
-  c.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  c.tiles = static_cast<int>((rows + c.tile_rows - 1) / c.tile_rows);
-  const int resident = sms * (d == 256 ? 1 : 2);
-  // about two waves of blocks, so that the blocks of a ragged batch even out
-  long long target = 2LL * resident / (static_cast<long long>(Hk) * c.tiles);
-  if (target < 1) target = 1;
-  c.target = static_cast<int>(target);
-  c.cap = c.target + batch;
+  c.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : d == 256 ? 64 : 128;
+  // as many as are resident at once (CacheTile::kResident)
+  c.blocks = sms * (d == 256 || c.tile_rows == 128 ? 1 : d == 64 && c.tile_rows == 16 ? 3 : 2);
   return c;
 }
 
@@ -1000,7 +931,7 @@ cudaError_t launch_cache_tile(const CacheFwdParams& p, cudaStream_t stream) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, dim3(p.Hk * p.tiles, p.cap), dim3(T::kThreads), T::kSmem, stream, p);
+  return launch_chained(kern, dim3(p.blocks), dim3(T::kThreads), T::kSmem, stream, p);
 }
 
 template <int D>
@@ -1008,14 +939,15 @@ cudaError_t launch_cache_rows(const CacheFwdParams& p, int tile_rows, cudaStream
   if constexpr (D == 256) {
     if (tile_rows == 16) return launch_cache_tile<D, 1, 1, 4, 2>(p, stream);
     if (tile_rows == 32) return launch_cache_tile<D, 1, 2, 4, 2>(p, stream);
-    return launch_cache_tile<D, 1, 4, 2, 4>(p, stream);
+    return launch_cache_tile<D, 1, 4, 2, 3>(p, stream);
   } else {
-    constexpr int kDeep = D == 64 ? 2 : 1;
-    if (tile_rows == 16) return launch_cache_tile<D, 1, 1, 4, 3 * kDeep>(p, stream);
-    if (tile_rows == 32) return launch_cache_tile<D, 2, 1, 4, 3 * kDeep>(p, stream);
-    return launch_cache_tile<D, 2, 2, 2, 5 * kDeep>(p, stream);
+    if (tile_rows == 16) return launch_cache_tile<D, 1, 1, 4, D == 64 ? 3 : 2>(p, stream);
+    if (tile_rows == 32) return launch_cache_tile<D, 2, 1, 4, D == 64 ? 5 : 2>(p, stream);
+    return launch_cache_wide(p, D, stream);
   }
 }
+
+constexpr int kWholeKeys = 512, kFinish = 6, kLeast = 8;
 
 int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim) {
   if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
@@ -1040,8 +972,8 @@ long long dfa_cache_workspace_bytes(int batch, int rows, int max_new, int heads,
   DeviceInfo di;
   if (const int rc = device_info(&di)) return rc;
   if (max_new > rows) max_new = rows;
-  const CachePlan c = cache_plan_for(batch, max_new, heads / kv_heads, kv_heads, headdim, di.sms);
-  return static_cast<long long>(c.cap) * kv_heads * c.tiles * c.tile_rows * (headdim + 1) * 4;
+  const CachePlan c = cache_plan_for(max_new, heads / kv_heads, headdim, di.sms);
+  return 2LL * c.blocks * c.tile_rows * (headdim + 1) * 4;
 }
 
 int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k_cache,
@@ -1071,19 +1003,18 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   if (const int rc = device_info(&di)) return rc;
   if (max_new > rows) max_new = rows;
   const int G = heads / kv_heads, d = headdim;
-  const CachePlan c = cache_plan_for(batch, max_new, G, kv_heads, d, di.sms);
-  const long long part_rows = static_cast<long long>(c.tiles) * c.tile_rows;
-  const long long parts = static_cast<long long>(c.cap) * kv_heads * part_rows;
+  const CachePlan c = cache_plan_for(max_new, G, d, di.sms);
+  const long long parts = 2LL * c.blocks * c.tile_rows;
   if (workspace_bytes < parts * (d + 1) * 4) return DFA_EINVAL;
-  if (static_cast<long long>(kv_heads) * c.tiles > 0x7fffffffLL || c.cap > 65535)
-    return DFA_EINVAL;
   CacheFwdParams p{};
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d),
                               static_cast<cuuint64_t>(kv_heads) * page_size,
                               static_cast<cuuint64_t>(num_pages)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), dims[1] * d};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(d < 128 ? d : 128),
-                             static_cast<cuuint32_t>(page_size < kUnit ? page_size : kUnit), 1};
+                             static_cast<cuuint32_t>(c.tile_rows < 128 && page_size > kUnit ? kUnit
+                                                                                      : page_size),
+                             1};
   const CUtensorMapSwizzle swizzle = d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (const int rc = encode_map_u8(&p.tm_k, k_cache, 3, dims, strides, box, swizzle)) return rc;
   if (const int rc = encode_map_u8(&p.tm_v, v_cache, 3, dims, strides, box, swizzle)) return rc;
@@ -1119,22 +1050,24 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
-  p.tiles = c.tiles;
-  p.target = c.target;
-  p.cap = c.cap;
-  p.part_rows = static_cast<int>(part_rows);
+  p.tile_rows = c.tile_rows;
+  p.blocks = c.blocks;
+  // Requests that cannot hold more than kWholeKeys are not worth cutting: one
+  // unit each, and no join to launch.  Longer ones are cut into units of 128
+  // keys, kLeast of them at least to a block.
+  const bool whole = static_cast<long long>(max_pages) * page_size <= kWholeKeys;
+  p.unit = whole ? 0 : 128;
+  p.finish = whole ? 1 : kFinish;
+  p.least = whole ? 1 : kLeast;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = d == 64    ? launch_cache_rows<64>(p, c.tile_rows, s)
                   : d == 128 ? launch_cache_rows<128>(p, c.tile_rows, s)
                              : launch_cache_rows<256>(p, c.tile_rows, s);
-  // a request is split only where it holds more keys than the smallest chunk
-  if (e == cudaSuccess && static_cast<long long>(max_pages) * page_size > kCacheMinChunk) {
-    const long long warps = static_cast<long long>(rows) * heads;
-    const long long want = (warps + kJoinWarps - 1) / kJoinWarps;
-    const dim3 grid(static_cast<unsigned>(want < 4LL * di.sms ? want : 4LL * di.sms));
+  if (e == cudaSuccess && !whole) {
     auto join = d == 64 ? dfa_cache_join_kernel<64>
                         : d == 128 ? dfa_cache_join_kernel<128> : dfa_cache_join_kernel<256>;
+    const dim3 grid(c.blocks, (c.tile_rows + kJoinWarps - 1) / kJoinWarps);
     e = launch_chained(join, grid, dim3(32 * kJoinWarps), 0, s, p);
   }
   return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);

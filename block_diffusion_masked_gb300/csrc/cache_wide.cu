@@ -1,0 +1,655 @@
+// Attention over the paged 8-bit cache for many query rows per key (more than
+// 32: blocks of tokens times grouped heads), headdim 64 and 128, on the
+// tensor cores' tcgen05 path.  The mathematics is that of cache_fwd.cu.
+//
+// One CTA per SM takes a run of units (cache.cuh) and walks its pieces: a piece
+// is part of the keys of one request, key/value head and 128 query rows, in
+// 128-key tiles, the own keys last.
+//   TMA        raw e4m3 tiles of k and v, a box per page, into a ring;
+//   convert    e4m3 -> f16 (exact) into the 128-byte-swizzled operand tiles
+//              (own keys: bf16, copied from global memory), two of k and two
+//              of v;
+//   S = Q K^T  A = Q from TMEM (f16 after the row's power of two, or bf16 for
+//              own keys), B = the key tile; two score buffers, free again as
+//              soon as the softmax has them in registers;
+//   softmax    online, lazily moved reference maximum, times the value page's
+//              scale, into a P buffer in TMEM;
+//   O += P V   A = P from TMEM, B = the value tile (keys outermost).
+// So the softmax warps never wait for a product of the same tile: the scores
+// of the next one are there, and P V runs under the next tile's exponentials.
+// Rings, buffers and barrier phases run on across pieces.
+//
+// Q and P stay in TMEM because shared memory is the second bound: a
+// headdim-128 tile moves 32 KB of TMA writes, 32 KB of conversion reads, 64 KB
+// of writes and 64 KB of operand reads, 1536 cycles at 128 bytes a cycle, where
+// memory gives a tile about 1400 and the products take 1024.
+//
+// Warps: 0-7 softmax (16 rows each, thread t on row t % 16, key columns
+// [64 (t / 16), ...)), 8-11 convert k, 12-15 convert v, 16 TMA, 17 issues S,
+// 18 issues P V; the softmax warps take registers from the others (setmaxnreg).
+#include <type_traits>
+
+#include "cache_fwd.cuh"
+#include "dfa.h"
+
+namespace dfa {
+namespace {
+
+// Instruction descriptor of tcgen05.mma kind::f16 with f16 A and B (format
+// 0), f32 accumulator; fields as idesc_bf16.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int D, int RS>
+struct WideCfg {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int kSoftWarps = 8;
+  static constexpr int kWarpConvV = 12, kWarpLoad = 16, kWarpS = 17, kWarpPV = 18;
+  static constexpr int kThreads = 32 * 20;  // the last warp only fills its warpgroup
+  // setmaxnreg split of the launch's 96 registers a thread:
+  // 256 * 144 + 256 * 72 + 128 * 48 == 640 * 96
+  static constexpr int kRegSoft = 144, kRegConv = 72, kRegRest = 48;
+  static constexpr int kRaw = BN * D;       // a raw tile of k or of v
+  static constexpr int kTile = BN * D * 2;  // an operand tile
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + 2 * kTile;
+  static constexpr int kOffRaw = kOffV + 2 * kTile;
+  static constexpr int kOffBar = kOffRaw + RS * 2 * kRaw;
+  enum {
+    BAR_Q = 0,
+    BAR_RAWFULL = 1,
+    BAR_RAWEMPTY = BAR_RAWFULL + RS,
+    BAR_KFULL = BAR_RAWEMPTY + RS,  // [2] each, of the operand tiles
+    BAR_KEMPTY = BAR_KFULL + 2,
+    BAR_VFULL = BAR_KEMPTY + 2,
+    BAR_VEMPTY = BAR_VFULL + 2,
+    BAR_SFULL = BAR_VEMPTY + 2,   // [2] scores complete
+    BAR_SREAD = BAR_SFULL + 2,    // [2] scores in registers
+    BAR_PFULL = BAR_SREAD + 2,    // probabilities written
+    BAR_PVDONE = BAR_PFULL + 1,   // P V complete: P may be written, O read
+    BAR_DRAIN = BAR_PVDONE + 1,   // every product complete
+    NUM_BARS = BAR_DRAIN + 1
+  };
+  static constexpr int kOffTmem = kOffBar + NUM_BARS * 8;
+  static constexpr int kOffAbort = kOffTmem + 4;
+  static constexpr int kOffOdd = kOffAbort + 4;  // [4]: own values that are not finite
+  static constexpr int kSmem = kOffOdd + 16 + 1024;
+  // TMEM: S at 0 and 128, P, O, Q
+  static constexpr int kTmemP = 256, kTmemO = 320, kTmemQ = 448, kTmemCols = 512;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+template <int D, int RS>
+__global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
+    dfa_cache_wide_kernel(const __grid_constant__ CacheFwdParams p) {
+  using C = WideCfg<D, RS>;
+  constexpr int BN = C::BN;
+  constexpr int DH = D / 2;  // head dims of a softmax thread's half row
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
+  volatile int* s_odd = reinterpret_cast<volatile int*>(smem + C::kOffOdd);
+  const AbortFlag ab{const_cast<int*>(abort_flag), p.status};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#define BAR(i) (sbase + C::kOffBar + 8 * (i))
+
+  if (tid == 0) {
+    mbar_init(BAR(C::BAR_Q), C::kSoftWarps);
+    for (int s = 0; s < RS; ++s) {
+      mbar_init(BAR(C::BAR_RAWFULL + s), 1);
+      mbar_init(BAR(C::BAR_RAWEMPTY + s), 8);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(BAR(C::BAR_KFULL + s), 4);
+      mbar_init(BAR(C::BAR_KEMPTY + s), 1);
+      mbar_init(BAR(C::BAR_VFULL + s), 4);
+      mbar_init(BAR(C::BAR_VEMPTY + s), 1);
+      mbar_init(BAR(C::BAR_SFULL + s), 1);
+      mbar_init(BAR(C::BAR_SREAD + s), C::kSoftWarps);
+    }
+    mbar_init(BAR(C::BAR_PFULL), C::kSoftWarps);
+    mbar_init(BAR(C::BAR_PVDONE), 1);
+    mbar_init(BAR(C::BAR_DRAIN), 2);
+    fence_mbar_init();
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) s_odd[i] = 0;
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  bool bad = false;
+  Piece w = first_piece(p, blockIdx.x, &bad);
+  if (bad) atomicOr(p.status, kStatusIndex);
+  if (w.b < 0) return;  // the whole block
+  if (warp == C::kWarpPV) {
+    tmem_alloc(sbase + C::kOffTmem, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kOffTmem);
+
+  // A piece's tiles: its cached keys, then the own keys its rows can see.
+  struct Tiles {
+    int h, row_base, R, key_lo, key_hi, nc, own, all;
+  };
+  auto tiles_of = [&](const Piece& x) {
+    Tiles k;
+    const int rt = row_tiles(p, x.rq);
+    k.h = x.seg / rt;
+    k.row_base = (x.seg - k.h * rt) * C::BM;
+    k.R = x.rq.n * p.G;
+    k.key_lo = piece_begin(p, x);
+    k.key_hi = piece_end(p, x);
+    k.nc = k.key_hi > k.key_lo ? (k.key_hi - k.key_lo + BN - 1) / BN : 0;
+    k.own = 0;
+    if (p.k != nullptr && x.last())
+      k.own = cache_own_end(x.rq.len, min(k.R - 1, k.row_base + C::BM - 1) / p.G, x.rq.n, p.bs);
+    k.all = k.nc + (k.own + BN - 1) / BN;
+    return k;
+  };
+  // Pages of four tiles at a time, eight 16-key groups each: lane 8 t + g
+  // holds group g of tile `first` + t.  The load (-1: nothing there) and the
+  // look at what it brought are apart, a few tiles, so that nothing waits;
+  // group_keys is 0 for a page that may not be followed.
+  auto load_page = [&](const Piece& x, const Tiles& k, int first) {
+    const int j = first + (lane >> 3);
+    const int key = k.key_lo + BN * j + 16 * (lane & 7);
+    return j < k.nc && key < k.key_hi
+               ? p.block_table[static_cast<long long>(x.b) * p.max_pages + (key >> p.page_shift)]
+               : -1;
+  };
+  auto keys_of = [&](const Tiles& k, int first, int page) {
+    const int key = k.key_lo + BN * (first + (lane >> 3)) + 16 * (lane & 7);
+    return cache_page_ok(page, p.num_pages) ? max(0, min(16, k.key_hi - key)) : 0;
+  };
+
+  if (warp >= C::kWarpLoad) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegRest));
+   if (warp == C::kWarpLoad) {
+    // ------------------------------------------------------------ loads
+    bool ok = true;
+    int n = 0;  // raw tiles over all pieces
+    for (; w.b >= 0 && ok; next_piece(p, w)) {
+      const Tiles k = tiles_of(w);
+      int page = load_page(w, k, 0), next_page = -1;
+      int keys = keys_of(k, 0, page);
+      for (int j = 0; j < k.nc; ++j, ++n) {
+        if ((j & 3) == 1) next_page = load_page(w, k, j + 3);
+        if ((j & 3) == 0 && j > 0) page = next_page, keys = keys_of(k, j, page);
+        const int st = n % RS;
+        // the first group of each page of this tile issues the page's boxes
+        const int per = p.page_size >> 4;
+        const bool mine = (lane >> 3) == (j & 3) && (lane & 7) % per == 0;
+        if (mine && keys == 0 && k.key_lo + BN * j + 16 * (lane & 7) < k.key_hi)
+          atomicOr(p.status, kStatusIndex);
+        const bool load = mine && keys > 0;
+        const unsigned count = __popc(__ballot_sync(0xffffffffu, load));
+        if (n >= RS && !(ok = mbar_wait_warp(BAR(C::BAR_RAWEMPTY + st), (n / RS - 1) & 1, ab)))
+          break;
+        if (lane == 0)
+          mbar_arrive_expect_tx(BAR(C::BAR_RAWFULL + st), count * p.page_size * D * 2);
+        __syncwarp();
+        if (load) {
+          const uint32_t dst = sbase + C::kOffRaw + st * 2 * C::kRaw + (lane & 7) * 16 * D;
+          tma_load_3d(dst, &p.tm_k, BAR(C::BAR_RAWFULL + st), 0, k.h * p.page_size, page);
+          tma_load_3d(dst + C::kRaw, &p.tm_v, BAR(C::BAR_RAWFULL + st), 0, k.h * p.page_size, page);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok && lane == 0)  // giving up: what is in flight lands first
+      for (int i = n > RS ? n - RS : 0; i < n; ++i)
+        mbar_wait_limited(BAR(C::BAR_RAWFULL + i % RS), (i / RS) & 1, 100000000ull);
+    __syncwarp();
+   } else if (warp == C::kWarpS || warp == C::kWarpPV) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      bool ok = true;
+      int n = 0, q = 0;  // tiles, versions of Q
+      for (; w.b >= 0 && ok; next_piece(p, w)) {
+        const Tiles k = tiles_of(w);
+        for (int j = 0; j < k.all; ++j, ++n) {
+          const int b = n & 1;
+          if (warp == C::kWarpS) {
+            // Q as f16 at the first cached tile, as bf16 at the first own one
+            if ((j == 0 || j == k.nc) && !(ok = mbar_wait(BAR(C::BAR_Q), q++ & 1, ab))) break;
+            if (!(ok = mbar_wait(BAR(C::BAR_KFULL + b), (n >> 1) & 1, ab))) break;
+            if (n >= 2 && !(ok = mbar_wait(BAR(C::BAR_SREAD + b), ((n >> 1) - 1) & 1, ab))) break;
+            tc_fence_after();
+            const uint32_t id = j < k.nc ? idesc_f16(C::BM, BN, false, false)
+                                         : idesc_bf16(C::BM, BN, false, false);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t bd = sdesc_sw128(
+                  sbase + C::kOffK + b * C::kTile + (kk >> 2) * (BN * 128) + (kk & 3) * 32, 16,
+                  1024);
+              mma_ts(tmem + b * BN, tmem + C::kTmemQ + 8 * kk, bd, id, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(BAR(C::BAR_SFULL + b));
+            mma_commit(BAR(C::BAR_KEMPTY + b));
+          } else {
+            if (!(ok = mbar_wait(BAR(C::BAR_VFULL + b), (n >> 1) & 1, ab))) break;
+            if (!(ok = mbar_wait(BAR(C::BAR_PFULL), n & 1, ab))) break;
+            tc_fence_after();
+            const uint32_t id =
+                j < k.nc ? idesc_f16(C::BM, D, false, true) : idesc_bf16(C::BM, D, false, true);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk) {
+              const uint64_t bd = sdesc_sw128(
+                  sbase + C::kOffV + b * C::kTile + kk * 16 * 128, BN * 128, 1024);
+              mma_ts(tmem + C::kTmemO, tmem + C::kTmemP + 8 * kk, bd, id,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+            }
+            mma_commit(BAR(C::BAR_VEMPTY + b));
+            mma_commit(BAR(C::BAR_PVDONE));
+          }
+        }
+      }
+      mma_commit(BAR(C::BAR_DRAIN));
+      mbar_wait_limited(BAR(C::BAR_DRAIN), 0, 1000000000ull);
+    }
+    __syncwarp();
+   }
+  } else if (warp >= C::kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegConv));
+    // ------------------------------------------------------------ conversion
+    const bool isv = warp >= C::kWarpConvV;
+    const int cw = warp & 3;             // warp of its four
+    const int c = cw * 32 + lane;        // 0 .. 127
+    const int full = isv ? C::BAR_VFULL : C::BAR_KFULL, empty = full + 2;
+    const uint32_t tiles0 = sbase + (isv ? C::kOffV : C::kOffK);
+    const uint32_t raw0 = sbase + C::kOffRaw + (isv ? C::kRaw : 0);
+    // e4m3 -> f16: a thread turns 16 values (a 16-byte piece) into two pieces
+    // of its row.  Eight lanes, one phase of a shared-memory access, take four
+    // neighbouring pieces of rows r and r ^ 5: under either tile's swizzle
+    // their reads and their writes fall on different banks.
+    // `mask`: rows past their group's keys (lane g: those of group g) become
+    // zero, whatever the raw bytes are there, NaN included.
+    const int pc = lane & 3;
+    const int r8 = (lane >> 3) ^ (5 * ((lane >> 2) & 1));  // row of its eight
+    auto convert = [&](uint32_t raw, uint32_t dst, bool mask, int group_keys) {
+      constexpr int kChunks = D / 64;
+#pragma unroll
+      for (int half = 0; half < 4 * kChunks; half += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = half + i, f = at % kChunks;
+          const int r = 8 * (4 * (at / kChunks) + cw) + r8;
+          if constexpr (D == 64) x[i] = lds128(raw + r * 64 + ((pc ^ ((r >> 1) & 3)) << 4));
+          else x[i] = lds128(raw + r * 128 + (((pc + 4 * f) ^ r8) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = half + i, f = at % kChunks;
+          const int r = 8 * (4 * (at / kChunks) + cw) + r8;
+          if (mask && (r & 15) >= __shfl_sync(0xffffffffu, group_keys, r >> 4))
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t to = dst + f * (BN * 128) + r * 128;
+          st_shared_v4(to + (((2 * pc) ^ r8) << 4), e4m3_lo(x[i].x), e4m3_hi(x[i].x),
+                       e4m3_lo(x[i].y), e4m3_hi(x[i].y));
+          st_shared_v4(to + (((2 * pc + 1) ^ r8) << 4), e4m3_lo(x[i].z), e4m3_hi(x[i].z),
+                       e4m3_lo(x[i].w), e4m3_hi(x[i].w));
+        }
+      }
+    };
+    // Own rows as they are; what is not finite in v is kept out of the product
+    // (its weight is 0 in rows that do not see it) and noted.
+    auto copy_own = [&](const Piece& x, const Tiles& k, int first, uint32_t dst) {
+      const __nv_bfloat16* src = isv ? p.v + x.rq.row0 * p.v_sr + k.h * p.v_sh
+                                     : p.k + x.rq.row0 * p.k_sr + k.h * p.k_sh;
+      const long long sr = isv ? p.v_sr : p.k_sr;
+      bool odd = false;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const int at = i * 128 + c, r = at / (D / 8), u = at % (D / 8);
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+        if (first + r < x.rq.n) {
+          const uint4 y = *reinterpret_cast<const uint4*>(src + (first + r) * sr + 8 * u);
+          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+        }
+        if (isv) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if ((v[y] & 0x7f80u) == 0x7f80u) v[y] &= 0xffff0000u, odd = true;
+            if ((v[y] & 0x7f800000u) == 0x7f800000u) v[y] &= 0xffffu, odd = true;
+          }
+        }
+        st_shared_v4(dst + (u >> 3) * (BN * 128) + r * 128 + (((u ^ r) & 7) << 4), v[0], v[1], v[2],
+                     v[3]);
+      }
+      return odd;
+    };
+    bool ok = true;
+    int n = 0, raw = 0, owns = 0;  // operand tiles, raw tiles, pieces with own keys
+    for (; w.b >= 0 && ok; next_piece(p, w)) {
+      const Tiles k = tiles_of(w);
+      int keys = 0, next_page = -1;
+      if (isv) keys = keys_of(k, 0, load_page(w, k, 0));
+      for (int j = 0; j < k.all; ++j, ++n) {
+        const int b = n & 1;
+        if (isv && (j & 3) == 1) next_page = load_page(w, k, j + 3);
+        if (isv && (j & 3) == 0 && j > 0) keys = keys_of(k, j, next_page);
+        if (n >= 2 && !(ok = mbar_wait_warp(BAR(empty + b), ((n >> 1) - 1) & 1, ab))) break;
+        const uint32_t dst = tiles0 + b * C::kTile;
+        if (j < k.nc) {
+          const int st = raw % RS;
+          if (!(ok = mbar_wait_warp(BAR(C::BAR_RAWFULL + st), (raw / RS) & 1, ab))) break;
+          const uint32_t src = raw0 + st * 2 * C::kRaw;
+          const int group_keys = __shfl_sync(0xffffffffu, keys, 8 * (j & 3) + (lane & 7));
+          if (isv && __any_sync(0xffffffffu, group_keys < 16)) convert(src, dst, true, group_keys);
+          else convert(src, dst, false, 0);
+          mbar_arrive_warp(BAR(C::BAR_RAWEMPTY + st));
+          ++raw;
+        } else {
+          if (isv && j == k.nc) {
+            // The notes of the last four pieces with own keys; this piece's
+            // was cleared with the one before it, its readers are long past
+            // the one that is cleared now.
+            ++owns;
+            if (c == 0) s_odd[(owns + 1) & 3] = 0;
+          }
+          if (copy_own(w, k, BN * (j - k.nc), dst)) s_odd[owns & 3] = 1;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(BAR(full + b));
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
+    // ------------------------------------------------------------ softmax
+    const int half = lane >> 4;
+    const int lb = (warp & 3) * 32 + (warp >> 2) * 16;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(lb) << 16);
+    bool ok = true;
+    int n = 0, owns = 0;  // tiles and pieces with own keys so far
+    for (; w.b >= 0 && ok; next_piece(p, w)) {
+      const Tiles k = tiles_of(w);
+      const int r = k.row_base + lb + (lane & 15);  // row of the request and head
+      const int tok = min(r, k.R - 1) / p.G;
+      const int hq = k.h * p.G + (min(r, k.R - 1) - tok * p.G);
+      const int end = r < k.R ? cache_own_end(w.rq.len, tok, w.rq.n, p.bs) : 0;
+      const __nv_bfloat16* qsrc = p.q + (w.rq.row0 + tok) * p.q_sr + hq * p.q_sh + half * DH;
+      int keys = 0, next_page = -1;
+      float ks = 0.f, vs = 0.f, vmax = 0.f, next_ks = 0.f, next_vs = 0.f;
+      auto load_scales = [&](int page, float* a, float* b) {
+        const bool has = cache_page_ok(page, p.num_pages);
+        const long long at = static_cast<long long>(page) * p.Hk + k.h;
+        *a = has ? p.k_scale[at] : 0.f;
+        *b = has ? p.v_scale[at] : 0.f;
+      };
+      auto group_max = [&](float v) {  // over the eight groups of a tile
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+      };
+      next_page = load_page(w, k, 0);
+      // The row's half of Q into TMEM, f16 after a power of two or bf16.  The
+      // scores of the tiles before are complete, so Q may be replaced.
+      float factor = 0.f;  // undoes the row's power of two, with the softmax scale
+      auto put_q = [&](bool f16) {
+        uint32_t v[D / 4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint4 y = make_uint4(0u, 0u, 0u, 0u);
+          if (r < k.R) y = *reinterpret_cast<const uint4*>(qsrc + 8 * i);
+          v[4 * i] = y.x, v[4 * i + 1] = y.y, v[4 * i + 2] = y.z, v[4 * i + 3] = y.w;
+        }
+        if (f16) {
+          unsigned top = 0;
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) {
+            const unsigned lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
+            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          int e = static_cast<int>(top >> 7) - 127 - 14;
+          if (e < -100) e = -100;
+          const float inv = pow2_bits(-e);
+          factor = pow2_bits(e) * p.scale_log2;
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i)
+            v[i] = pack_f16x2(__uint_as_float(v[i] << 16) * inv,
+                              __uint_as_float(v[i] & 0xffff0000u) * inv);
+        }
+        tmem_st_half<D / 4, D / 4>(t_lane + C::kTmemQ, v);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(BAR(C::BAR_Q));
+      };
+      if (k.nc > 0) put_q(true);
+      load_scales(next_page, &ks, &vs);
+      keys = keys_of(k, 0, next_page);
+      vmax = group_max(vs);
+      float m = -INFINITY, l = 0.f;
+      float c = pow2_bits(kCacheMinExp), inv_c = pow2_bits(-kCacheMinExp);  // unit of O
+      // What tile j's softmax needs of its half row's four groups of 16 keys:
+      // score factors, value weights, keys; found ahead, while it would wait.
+      float fg[4], wg[4], c_tile;
+      int kg[4];
+      auto tile_groups = [&](int j) {
+        if ((j & 3) == 1) next_page = load_page(w, k, j + 3);
+        if ((j & 3) == 3) load_scales(next_page, &next_ks, &next_vs);
+        if ((j & 3) == 0 && j > 0) {
+          ks = next_ks, vs = next_vs;
+          keys = keys_of(k, j, next_page);
+          vmax = group_max(vs);
+        }
+        if (j < k.nc) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int src = 8 * (j & 3) + 4 * half + i;
+            // never 0 (a group without keys): 0 * -inf is not a number
+            fg[i] = fmaxf(factor * __shfl_sync(0xffffffffu, ks, src), 1.1754944e-38f);
+            wg[i] = __shfl_sync(0xffffffffu, vs, src);
+            kg[i] = __shfl_sync(0xffffffffu, keys, src);
+          }
+          c_tile = __shfl_sync(0xffffffffu, vmax, 8 * (j & 3));
+        } else {
+          const int first = BN * (j - k.nc) + 64 * half;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            fg[i] = p.scale_log2;
+            wg[i] = 1.f;
+            kg[i] = min(16, max(0, end - first - 16 * i));
+          }
+          c_tile = 1.f;
+        }
+      };
+#pragma unroll 1
+      for (int j = 0; j < k.all; ++j, ++n) {
+        const int b = n & 1;
+        const bool cached = j < k.nc;
+        if (j == k.nc) put_q(false);
+        tile_groups(j);
+        const float c_new = fmaxf(c, c_tile);
+        const bool whole =
+            __all_sync(0xffffffffu, kg[0] == 16 && kg[1] == 16 && kg[2] == 16 && kg[3] == 16);
+        if (!(ok = mbar_wait_warp(BAR(C::BAR_SFULL + b), (n >> 1) & 1, ab))) break;
+        tc_fence_after();
+        uint32_t sr[64];
+        tmem_ld_half<32, 64>(t_lane + b * BN, sr);
+        tmem_ld_half<32, 64>(t_lane + b * BN + 32, sr + 32);
+        tmem_wait_ld();
+        tmem_pin<64>(sr);
+        tc_fence_before();
+        mbar_arrive_warp(BAR(C::BAR_SREAD + b));
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t keep = (1u << kg[i]) - 1u;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t mk = bit_spread(keep, e);
+              sr[16 * i + e] = (sr[16 * i + e] & mk) | (0xff800000u & ~mk);
+            }
+          }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, max_tree<16>(sr + 16 * i) * fg[i]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        float shrink = 1.f;
+        if (c_new != c) {
+          shrink = c / c_new;
+          c = c_new;
+          inv_c = 1.f / c;
+        }
+        if (top > m + kSlack) {
+          const float a = ex2_approx(m - top);
+          m = top;
+          l *= a;
+          shrink *= a;
+        }
+        const float ref = m == -INFINITY ? 0.f : kShift - m;
+        const uint64_t ref2 = f2_pack(ref, ref);
+        uint64_t acc[2] = {0ull, 0ull};
+        uint32_t pk[32];  // held until P is free
+        auto probabilities = [&](auto f16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float wt = wg[i] * inv_c;
+            const uint64_t f2 = f2_pack(fg[i], fg[i]), w2 = f2_pack(wt, wt);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int at = 16 * i + 2 * e;
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[at]), __uint_as_float(sr[at + 1])), f2,
+                               ref2),
+                        x0, x1);
+              const uint64_t pr = f2_pack(ex2_approx(x0), ex2_approx(x1));
+              acc[e & 1] = f2_add(acc[e & 1], pr);
+              f2_unpack(f2_mul(pr, w2), x0, x1);
+              pk[8 * i + e] = decltype(f16)::value ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+            }
+          }
+        };
+        if (cached) probabilities(std::true_type{});
+        else probabilities(std::false_type{});
+        float a0, a1;
+        f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+        l += a0 + a1;
+        // P V of the tile before has read P and added to O
+        if (n > 0 && !(ok = mbar_wait_warp(BAR(C::BAR_PVDONE), (n - 1) & 1, ab))) break;
+        tc_fence_after();
+        if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+#pragma unroll
+          for (int x = 0; x < DH / 16; ++x) {
+            uint32_t o[16];
+            tmem_ld_half<16, DH>(t_lane + C::kTmemO + 16 * x, o);
+            tmem_wait_ld();
+            tmem_pin<16>(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+            tmem_st_half<16, DH>(t_lane + C::kTmemO + 16 * x, o);
+          }
+        }
+        tmem_st_half<32, 32>(t_lane + C::kTmemP, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive_warp(BAR(C::BAR_PFULL));
+      }
+
+      // -------------------------------------------------------- read-out
+      if (!ok) break;
+      if (k.all > 0 && !(ok = mbar_wait_warp(BAR(C::BAR_PVDONE), (n - 1) & 1, ab))) break;
+      tc_fence_after();
+      if (k.own > 0) ++owns;
+      const bool odd = k.own > 0 && s_odd[owns & 3] != 0;
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const bool none = m == -INFINITY && l == 0.f;
+      const float inv = none ? 0.f : c / l;
+      const float lse2 = none ? -INFINITY : m - kShift + lg2_approx(l);
+      const bool single = w.whole();
+      const long long at =
+          (2LL * blockIdx.x + (w.first ? 0 : 1)) * C::BM + lb + (lane & 15);
+      __nv_bfloat16* dst =
+          p.out + ((w.rq.row0 + static_cast<long long>(tok)) * p.H + hq) * D + half * DH;
+      float* part = p.part_o + at * D + half * DH;
+#pragma unroll
+      for (int x = 0; x < DH / 32; ++x) {
+        uint32_t o[32];
+        if (k.all > 0) {
+          tmem_ld_half<32, DH>(t_lane + C::kTmemO + 32 * x, o);
+          tmem_wait_ld();
+          tmem_pin<32>(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (odd) {  // own values that are not finite, for the rows that see them
+#pragma unroll 1
+          for (int key = 0; key < end; ++key) {
+            const __nv_bfloat16* v =
+                p.v + (w.rq.row0 + key) * p.v_sr + k.h * p.v_sh + half * DH + 32 * x;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __bfloat162float(v[e]);
+              if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
+            }
+          }
+        }
+        if (r < k.R) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+          if (single) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                v[y] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * y]),
+                                   __uint_as_float(o[8 * e + 2 * y + 1]));
+              st_global_v4(dst + 32 * x + 8 * e, v[0], v[1], v[2], v[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              st_global_v4(part + 32 * x + 4 * e, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                           o[4 * e + 3]);
+          }
+        }
+      }
+      if (r < k.R && half == 0) {
+        if (single)
+          p.lse[static_cast<long long>(hq) * p.rows + w.rq.row0 + tok] =
+              lse2 * 0.6931471805599453f;
+        else
+          p.part_lse[at] = lse2;
+      }
+    }
+  }
+#undef BAR
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpPV) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D, int RS>
+cudaError_t launch_wide(const CacheFwdParams& p, cudaStream_t stream) {
+  using C = WideCfg<D, RS>;
+  auto kern = dfa_cache_wide_kernel<D, RS>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kern, dim3(p.blocks), dim3(C::kThreads), C::kSmem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_wide(const CacheFwdParams& p, int headdim, cudaStream_t stream) {
+  if (headdim == 64) return launch_wide<64, 6>(p, stream);
+  if (headdim == 128) return launch_wide<128, 3>(p, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace dfa

@@ -511,16 +511,19 @@ int dfa_work_item(int pass, int mode, int w, int batch, int heads, int tiles, in
  * follows this page number.  dfa_cache_append_span: tokens [span[0], span[1])
  * that appending n tokens behind len puts into the j-th page touched (equal
  * when none), 0 <= j < dfa_cache_append_pages(n, page_size).
- * dfa_cache_chunk: keys per work item for total_keys keys over about `target`
- * items; dfa_cache_items: items of a request.  dfa_cache_own_end: one past the
- * last own row that own row i of n sees.
+ * dfa_cache_units: units of a segment, one for every `unit` keys and `finish`
+ * more; dfa_cache_blocks: blocks that share `total` units; dfa_cache_run: first unit of block x;
+ * dfa_cache_owner: the block of unit w.  dfa_cache_own_end: one past the last
+ * own row that own row i of n sees.
  */
 int dfa_cache_scale_exp(unsigned bits);
 int dfa_cache_page_ok(int page, int num_pages);
 int dfa_cache_append_pages(int max_new, int page_size);
 int dfa_cache_append_span(int len, int n, int j, int page_size, int *span);
-int dfa_cache_chunk(long long total_keys, int target);
-int dfa_cache_items(int len, int n, int chunk);
+int dfa_cache_units(int len, int n, int unit, int finish);
+int dfa_cache_blocks(long long total, int limit, int least);
+long long dfa_cache_run(int x, long long total, int blocks);
+int dfa_cache_owner(long long w, long long total, int blocks);
 int dfa_cache_own_end(int len, int i, int n, int block_size);
 
 /*

@@ -291,7 +291,9 @@ def _check(p, bs, out, lse):
     ([300, 64], [5, 9], 4, 4, 64, 3),
     ([129, 500, 1], [16, 7, 16], 4, 2, 128, 16),
     ([700, 90], [33, 12], 2, 1, 16, 64),
-    ([260], [40], 6, 3, 64, 1)])
+    ([260], [40], 6, 3, 64, 1),
+    ([0, 128, 257], [9, 5, 16], 16, 2, 32, 4),
+    ([1000, 3], [150, 70], 2, 1, 128, 50)])
 def test_attention(b, d, lens, new, H, Hk, ps, bs):
     p = _problem(lens, new, H, Hk, d, ps, seed=d + ps)
     out, lse = _run(b, p, bs)
@@ -309,37 +311,40 @@ def test_attention_split_over_chunks(b, d, G, T):
     _check(p, T, out, lse)
 
 
+@pytest.mark.parametrize("H", [4, 32])
 @pytest.mark.parametrize("lens", [[0], [5], [0, 70, 0, 16], [1000, 0]])
-def test_attention_without_own_keys(b, lens):
+def test_attention_without_own_keys(b, lens, H):
     """Rows of an empty cache see nothing: output 0, lse -inf."""
     new = [3] * len(lens)
-    p = _problem(lens, new, 4, 2, 64, 16, seed=9, own=False)
+    p = _problem(lens, new, H, 2, 64, 16, seed=9, own=False)
     out, lse = _run(b, p, 1)
     assert b.dfa_status() == 0
     _check(p, 1, out, lse)
 
 
-def test_attention_leaves_rows_behind_the_last_request(b):
-    p = _problem([40, 7], [3, 2], 4, 2, 128, 32, seed=10, tail=6)
+@pytest.mark.parametrize("H", [4, 32])
+def test_attention_leaves_rows_behind_the_last_request(b, H):
+    p = _problem([40, 7], [3, 2], H, 2, 128, 32, seed=10, tail=6)
     out = torch.full_like(p["q"], 9.0)
-    lse = torch.full((4, 11), 8.0, device=DEV)
+    lse = torch.full((H, 11), 8.0, device=DEV)
     _run(b, p, 4, out=out, lse=lse)
     assert b.dfa_status() == 0
     assert (out[5:] == 9).all() and (lse[:, 5:] == 8).all()
     _check(p, 4, out, lse)
 
 
-def test_attention_strided_and_large_magnitudes(b):
+@pytest.mark.parametrize("H", [4, 16])
+def test_attention_strided_and_large_magnitudes(b, H):
     """Slices of one projection; queries far above and below f16's range; page
     scales that differ by 2^20."""
-    p = _problem([100, 300], [6, 4], 4, 2, 128, 16, seed=11)
+    p = _problem([100, 300], [6, 4], H, 2, 128, 16, seed=11)
     qkv = torch.cat([p["q"], p["k"], p["v"]], 1)
     # scores stay below about 10: queries of 2^40 meet keys of 2^-40
     p["ks"] *= 2.0 ** -40
-    qkv[:, :4] *= 2.0 ** 40
-    qkv[:, 4:6] *= 2.0 ** -40
+    qkv[:, :H] *= 2.0 ** 40
+    qkv[:, H:H + 2] *= 2.0 ** -40
     p["vs"][::2] *= 2.0 ** 20
-    p["q"], p["k"], p["v"] = qkv[:, :4], qkv[:, 4:6], qkv[:, 6:]
+    p["q"], p["k"], p["v"] = qkv[:, :H], qkv[:, H:H + 2], qkv[:, H + 2:]
     out, lse = _run(b, p, 3)
     assert b.dfa_status() == 0
     _check(p, 3, out, lse)
@@ -347,30 +352,32 @@ def test_attention_strided_and_large_magnitudes(b):
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_own_values_that_are_not_finite(b, d, bad):
+@pytest.mark.parametrize("H", [4, 8])
+def test_own_values_that_are_not_finite(b, d, bad, H):
     """They reach the rows that see them and no others."""
-    p = _problem([20, 33], [12, 9], 4, 2, d, 16, seed=12)
+    p = _problem([20, 33], [12, 9], H, 2, d, 16, seed=12)
     clean = _run(b, p, 4)[0].clone()
     p["v"][9, 1, 5] = bad   # request 0, position 29: seen from block 7 (row 8) on
     p["k"][12 + 7, 0, 3] = float("nan")  # request 1, position 40: block 10, rows 7 ...
     out, lse = _run(b, p, 4)
     assert b.dfa_status() == 0
     hit = torch.zeros_like(out, dtype=torch.bool)
-    hit[8:12, 2:, 5] = True
-    hit[12 + 7:, :2] = True
+    hit[8:12, H // 2:, 5] = True
+    hit[12 + 7:, :H // 2] = True
     assert not torch.isfinite(out[hit]).any()
     if bad == bad:
-        assert (out[8:12, 2:, 5] == bad).all()
+        assert (out[8:12, H // 2:, 5] == bad).all()
     assert torch.isfinite(out[~hit]).all()
     assert torch.equal(out[~hit], clean[~hit])
 
 
 @pytest.mark.parametrize("what", ["page", "negative page", "length", "negative length", "order",
                                   "rows", "max_new"])
-def test_attention_bad_tables(b, what):
+@pytest.mark.parametrize("H", [2, 10])
+def test_attention_bad_tables(b, what, H):
     """A bad page counts as masked, a bad request as empty; the rest is right."""
     lens, new = [100, 50], [4, 5]
-    p = _problem(lens, new, 2, 1, 128, 16, seed=13)
+    p = _problem(lens, new, H, 1, 128, 16, seed=13)
     q = dict(p)
     q["table"], q["lens"], q["cu"] = p["table"].copy(), list(lens), list(p["cu"])
     maxn = 5

@@ -166,21 +166,36 @@ def test_append_spans(lib, ps):
             assert got == list(range(length, length + n))
 
 
-def test_split_covers_the_keys_within_the_room(lib):
-    """Chunks cover every request; the items fit target + requests."""
+def test_runs_share_the_units(lib):
+    """Blocks' runs are equal to within a unit, cover all units in order, and
+    name their owners."""
     g = np.random.default_rng(0)
-    for _ in range(300):
-        B, target = int(g.integers(1, 70)), int(g.integers(1, 400))
+    for _ in range(200):
+        B, limit, least = int(g.integers(1, 70)), int(g.integers(1, 400)), int(g.integers(1, 9))
         lens = (2.0 ** g.uniform(0, 17, B)).astype(int) * (g.random(B) < 0.9)
         rows = (g.random(B) < 0.9).astype(int)
-        total = int((lens * rows).sum())
-        chunk = lib.dfa_cache_chunk(total, target)
-        assert chunk >= 256 and chunk % 64 == 0
-        items = [lib.dfa_cache_items(int(n), int(r), chunk) for n, r in zip(lens, rows)]
-        for n, r, i in zip(lens, rows, items):
-            assert i == 0 if not r else i >= 1 and i * chunk >= n and (i == 1 or (i - 1) * chunk < n)
-        assert sum(items) <= target + B
-    assert lib.dfa_cache_chunk(2 ** 45, 1) == 2 ** 30
+        units = [lib.dfa_cache_units(int(n), int(r), 128, 3) for n, r in zip(lens, rows)]
+        assert units == [r * (3 - -int(n) // 128) for n, r in zip(lens, rows)]
+        total = sum(units) * int(g.integers(1, 9))
+        blocks = lib.dfa_cache_blocks(total, limit, least)
+        if total == 0:
+            assert blocks == 0
+            continue
+        assert 1 <= blocks <= limit and (blocks == limit or (blocks - 1) * least < total)
+        ends = [lib.dfa_cache_run(x, total, blocks) for x in range(blocks + 1)]
+        assert ends[0] == 0 and ends[-1] == total
+        sizes = np.diff(ends)
+        assert sizes.min() >= 1 and sizes.max() - sizes.min() <= 1
+        for w in {0, total - 1, *g.integers(0, total, 20).tolist(), *ends[:-1][::7]}:
+            x = lib.dfa_cache_owner(w, total, blocks)
+            assert ends[x] <= w < ends[x + 1]
+    # 64-bit products: a batch of 32768 requests of 2^30 keys, 256 heads
+    total = 32768 * 2 ** 23 * 256
+    ends = [lib.dfa_cache_run(x, total, 304) for x in (0, 1, 303, 304)]
+    assert ends == [x * total // 304 for x in (0, 1, 303, 304)]
+    assert lib.dfa_cache_owner(total - 1, total, 304) == 303
+    assert lib.dfa_cache_units(2 ** 30, 1, 128, 3) == 2 ** 23 + 3
+    assert lib.dfa_cache_units(500, 4, 0, 1) == 1 and lib.dfa_cache_units(500, 0, 0, 1) == 0
 
 
 def test_own_block_ends(lib):
