@@ -29,6 +29,7 @@
 // inside a product, so each thread takes 16 contiguous bytes of a token,
 // which are the operands of four k steps of Q K^T or 16 column tiles of P V.
 #include <cmath>
+#include <type_traits>
 
 #include "cache_fwd.cuh"
 #include "dfa.h"
@@ -370,33 +371,79 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
   float inv_c = pow2_bits(-kCacheMinExp);
   const uint8_t* qbase = smem + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
 
-  // New maxima of a unit's scaled scores: returns the factors the output and
-  // the sums shrink by (1 where the reference stays).
-  auto rebase = [&](const float (&um)[MT][2], float c_new) {
+  // Probabilities of a unit's raw scores sc (NT column tiles of 8 keys; -inf:
+  // not seen), packed as the products' A operand: score factors row[.][.] times
+  // f0 (first half of the column tiles) or f1, value weights w0 or w1 (times
+  // the new unit c_new's inverse).  They are taken against the reference as it
+  // stands; only where their sum says that one may have outgrown f16, or with
+  // `look`, is the maximum found and the unit done again.
+  auto soften = [&](auto nt, auto f16, auto& sc, const float (&row)[MT][2], float f0, float f1,
+                    float w0, float w1, float c_new, bool look, auto& pf) {
+    constexpr int NT = decltype(nt)::value;
     float shrink[MT][2];
-    bool any = false;
-    float cr = 1.f;
-    if (c_new != c) {
-      cr = c / c_new;
-      c = c_new;
-      inv_c = 1.f / c;
-    }
+    const float cr = c_new != c ? c / c_new : 1.f;
+    if (c_new != c) c = c_new, inv_c = 1.f / c;
+    w0 *= inv_c, w1 *= inv_c;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) shrink[mt][0] = shrink[mt][1] = cr;
+#pragma unroll 1
+    for (;;) {
+      if (look) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = um[mt][i];
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        float a = 1.f;
-        if (x > m[mt][i] + kSlack) {  // also the first finite maximum
-          a = ex2_approx(m[mt][i] - x);
-          m[mt][i] = x;
-          l[mt][i] *= a;
-        }
-        shrink[mt][i] = a * cr;
-        any = any || shrink[mt][i] != 1.f;
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+              x = fmax3(x, sc[mt][n][2 * i], sc[mt][n][2 * i + 1]);
+              y = fmax3(y, sc[mt][n + NT / 2][2 * i], sc[mt][n + NT / 2][2 * i + 1]);
+            }
+            x = fmaxf(x * (row[mt][i] * f0), y * (row[mt][i] * f1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            if (x > m[mt][i]) {
+              const float a = ex2_approx(m[mt][i] - x);
+              m[mt][i] = x;
+              l[mt][i] *= a;
+              shrink[mt][i] *= a;
+            }
+          }
       }
+      float sum[MT][2];
+      bool over = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // a row that has met no finite score keeps probabilities of 0
+          const float ref = m[mt][i] == -INFINITY ? 0.f : kShift - m[mt][i];
+          const float g0 = row[mt][i] * f0, g1 = row[mt][i] * f1;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float e0 = ex2_approx(fmaf(sc[mt][n][2 * i], n < NT / 2 ? g0 : g1, ref));
+            const float e1 = ex2_approx(fmaf(sc[mt][n][2 * i + 1], n < NT / 2 ? g0 : g1, ref));
+            s0 += e0;
+            s1 += e1;
+            const float wn = n < NT / 2 ? w0 : w1;
+            (&pf[mt][n / 2].x)[2 * (n & 1) + i] =
+                decltype(f16)::value ? pack_f16x2(e0 * wn, e1 * wn) : pack_bf16x2(e0 * wn, e1 * wn);
+          }
+          sum[mt][i] = s0 + s1;
+          over = over || sum[mt][i] > kMostSum || m[mt][i] == -INFINITY;
+        }
+      }
+      if (look || !__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) l[mt][0] += sum[mt][0], l[mt][1] += sum[mt][1];
+        break;
+      }
+      look = true;
+    }
+    bool any = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) any = any || shrink[mt][0] != 1.f || shrink[mt][1] != 1.f;
     if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -409,6 +456,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
         }
     }
   };
+  constexpr float kTiny = 1.1754944e-38f;  // a factor that is never 0: 0 * -inf is not a number
 
   // Own keys and values first, bf16, with the segment's end, while the cached
   // keys are on their way: units of 16 keys, the groups in turn, operands
@@ -453,43 +501,24 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
           }
         }
       }
-      float um[MT][2];
       int end[MT][2];  // one past the last own key of the thread's rows
+      float row[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
           end[mt][i] = r < R ? cache_own_end(w.rq.len, r / p.G, w.rq.n, p.bs) : 0;
-          um[mt][i] = -INFINITY;
+          row[mt][i] = p.scale_log2;
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float& s = sc[mt][n][2 * i + x];
-              s = k0 + 8 * n + 2 * t + x < end[mt][i] ? s * p.scale_log2 : -INFINITY;
-              um[mt][i] = fmaxf(um[mt][i], s);
-            }
+            for (int x = 0; x < 2; ++x)
+              if (k0 + 8 * n + 2 * t + x >= end[mt][i]) sc[mt][n][2 * i + x] = -INFINITY;
         }
-      rebase(um, fmaxf(c, 1.f));
-      uint4 pf[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float r0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kShift;
-        const float r1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kShift;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float e = ex2_approx(sc[mt][n][x] - (x < 2 ? r0 : r1));
-            l[mt][x >> 1] += e;
-            sc[mt][n][x] = e * inv_c;
-          }
-        pf[mt] = make_uint4(pack_bf16x2(sc[mt][0][0], sc[mt][0][1]),
-                            pack_bf16x2(sc[mt][0][2], sc[mt][0][3]),
-                            pack_bf16x2(sc[mt][1][0], sc[mt][1][1]),
-                            pack_bf16x2(sc[mt][1][2], sc[mt][1][3]));
-      }
+      uint4 pf[MT][1];
+      soften(std::integral_constant<int, 2>{}, std::false_type{}, sc, row, 1.f, 1.f, 1.f, 1.f,
+             fmaxf(c, 1.f), true, pf);
       // A row's probability of an own key it does not see is 0, but 0 times a
       // value that is not finite is not: such values leave the product and
       // are added to the rows that see them.
@@ -522,7 +551,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
               const uint32_t b1 = __byte_perm(vw[2][y], vw[3][y], z ? 0x7632 : 0x5410);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
-                mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt], b0, b1);
+                mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt][0], b0, b1);
             }
           }
         }
@@ -614,52 +643,19 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
       }
     }
     const bool whole = nv0 == 16 && nv1 == 16;
-    float um[MT][2];
+    if (!whole) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float ksn = n < 2 ? ks0 : ks1;
-        const int nv = n < 2 ? nv0 : nv1;
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sc[mt][n][x] *= factor[mt][x >> 1] * ksn;
-          if (!whole && 8 * (n & 1) + key_of<D>(2 * t + (x & 1)) >= nv) sc[mt][n][x] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        um[mt][i] = fmaxf(
-            fmax3(fmaxf(sc[mt][0][2 * i], sc[mt][0][2 * i + 1]), sc[mt][1][2 * i],
-                  sc[mt][1][2 * i + 1]),
-            fmax3(fmaxf(sc[mt][2][2 * i], sc[mt][2][2 * i + 1]), sc[mt][3][2 * i],
-                  sc[mt][3][2 * i + 1]));
+          for (int x = 0; x < 4; ++x)
+            if (8 * (n & 1) + key_of<D>(2 * t + (x & 1)) >= (n < 2 ? nv0 : nv1))
+              sc[mt][n][x] = -INFINITY;
     }
-    rebase(um, fmaxf(c, fmaxf(vs0, vs1)));
-    const float w0 = vs0 * inv_c, w1 = vs1 * inv_c;
     uint4 pf[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      // a row that has met no finite score keeps probabilities of 0
-      const float r0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0] - kShift;
-      const float r1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1] - kShift;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float wn = n < 2 ? w0 : w1;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float e = ex2_approx(sc[mt][n][x] - (x < 2 ? r0 : r1));
-          l[mt][x >> 1] += e;
-          sc[mt][n][x] = e * wn;
-        }
-      }
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
-        pf[mt][kk] = make_uint4(pack_f16x2(sc[mt][2 * kk][0], sc[mt][2 * kk][1]),
-                                pack_f16x2(sc[mt][2 * kk][2], sc[mt][2 * kk][3]),
-                                pack_f16x2(sc[mt][2 * kk + 1][0], sc[mt][2 * kk + 1][1]),
-                                pack_f16x2(sc[mt][2 * kk + 1][2], sc[mt][2 * kk + 1][3]));
-    }
+    soften(std::integral_constant<int, 4>{}, std::true_type{}, sc, factor, fmaxf(ks0, kTiny),
+           fmaxf(ks1, kTiny), vs0, vs1, fmaxf(c, fmaxf(vs0, vs1)), false, pf);
     // P V: the four keys of a thread's fragment rows, 16 dims each (headdim
     // 64: 8).  What lies behind the last key may be anything, NaN included,
     // and is replaced by zero.

@@ -216,12 +216,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 
 __device__ __forceinline__ float pow2_bits(int e) { return __int_as_float((e + 127) << 23); }
 
-// Probabilities are 2^(s - m + kShift); the reference maximum m follows a
-// new maximum only when that exceeds it by more than kSlack, so that most
-// units rescale nothing.  kShift + kSlack < 16 keeps f16 probabilities
-// finite, and kShift moves f16's smallest subnormal to 2^-30 of the maximum.
+// Probabilities are 2^(s - m + kShift) against a reference m that is a row's
+// largest score at some point: it moves only where the probabilities of a
+// tile's row sum to more than kMostSum, so that most tiles need no maximum and
+// rescale nothing.  No probability exceeds kMostSum then, which f16 holds; and
+// kShift moves f16's smallest subnormal to 2^-30 of the reference.
 constexpr float kShift = 6.f;
-constexpr float kSlack = 8.f;
+constexpr float kMostSum = 32768.f;
 
 // More than 32 query rows per key/value head, headdim 64 or 128 (tiles of 128
 // rows; the tensor maps' boxes are whole pages).

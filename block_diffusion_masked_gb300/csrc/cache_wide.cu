@@ -9,24 +9,19 @@
 //   convert    e4m3 -> f16 (exact) into the 128-byte-swizzled operand tiles
 //              (own keys: bf16, copied from global memory), two of k and two
 //              of v;
-//   S = Q K^T  A = Q from TMEM (f16 after the row's power of two, or bf16 for
-//              own keys), B = the key tile; two score buffers, free again as
-//              soon as the softmax has them in registers;
+//   S = Q K^T  A = Q (f16 after the row's power of two, or bf16 for own keys),
+//              B = the key tile, into one of three score buffers in TMEM;
 //   softmax    online, lazily moved reference maximum, times the value page's
-//              scale, into a P buffer in TMEM;
+//              scale, back into the columns of the scores;
 //   O += P V   A = P from TMEM, B = the value tile (keys outermost).
-// So the softmax warps never wait for a product of the same tile: the scores
-// of the next one are there, and P V runs under the next tile's exponentials.
-// Rings, buffers and barrier phases run on across pieces.
-//
-// Q and P stay in TMEM because shared memory is the second bound: a
-// headdim-128 tile moves 32 KB of TMA writes, 32 KB of conversion reads, 64 KB
-// of writes and 64 KB of operand reads, 1536 cycles at 128 bytes a cycle, where
-// memory gives a tile about 1400 and the products take 1024.
+// The chain scores - softmax - P V of a tile is some 3 us long, most of it
+// latency, and three buffers keep three tiles in it.  Rings, buffers and
+// barrier phases run on across pieces.
 //
 // Warps: 0-7 softmax (16 rows each, thread t on row t % 16, key columns
-// [64 (t / 16), ...)), 8-11 convert k, 12-15 convert v, 16 TMA, 17 issues S,
-// 18 issues P V; the softmax warps take registers from the others (setmaxnreg).
+// [64 (t / 16), ...)), 8-11 convert k, 12-15 convert v, 16 and 17 load k and
+// v, 18 issues S, 19 issues P V; the softmax warps take registers from the
+// others (setmaxnreg).
 #include <type_traits>
 
 #include "cache_fwd.cuh"
@@ -46,39 +41,49 @@ template <int D, int RS>
 struct WideCfg {
   static constexpr int BM = 128, BN = 128;
   static constexpr int kSoftWarps = 8;
-  static constexpr int kWarpConvV = 12, kWarpLoad = 16, kWarpS = 17, kWarpPV = 18;
-  static constexpr int kThreads = 32 * 20;  // the last warp only fills its warpgroup
+  static constexpr int kWarpConvV = 12, kWarpLoadK = 16, kWarpLoadV = 17, kWarpS = 18, kWarpPV = 19;
+  static constexpr int kThreads = 32 * 20;
   // setmaxnreg split of the launch's 96 registers a thread:
-  // 256 * 144 + 256 * 72 + 128 * 48 == 640 * 96
-  static constexpr int kRegSoft = 144, kRegConv = 72, kRegRest = 48;
-  static constexpr int kRaw = BN * D;       // a raw tile of k or of v
-  static constexpr int kTile = BN * D * 2;  // an operand tile
-  static constexpr int kOffK = 0;
+  // 256 * 136 + 256 * 72 + 128 * 64 == 640 * 96
+  static constexpr int kRegSoft = 136, kRegConv = 72, kRegRest = 64;
+  static constexpr int kRaw = BN * D;       // a raw tile of k or of v, RS of each
+  static constexpr int kTile = BN * D * 2;  // an operand tile, two of each
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + BM * D * 2;
   static constexpr int kOffV = kOffK + 2 * kTile;
-  static constexpr int kOffRaw = kOffV + 2 * kTile;
+  static constexpr int kOffRaw = kOffV + 2 * kTile;  // k, then v
   static constexpr int kOffBar = kOffRaw + RS * 2 * kRaw;
   enum {
     BAR_Q = 0,
-    BAR_RAWFULL = 1,
-    BAR_RAWEMPTY = BAR_RAWFULL + RS,
-    BAR_KFULL = BAR_RAWEMPTY + RS,  // [2] each, of the operand tiles
+    BAR_RAWFULL = 1,                    // [RS] of k, [RS] of v
+    BAR_RAWEMPTY = BAR_RAWFULL + 2 * RS,
+    BAR_KFULL = BAR_RAWEMPTY + 2 * RS,  // [2] each, of the operand tiles
     BAR_KEMPTY = BAR_KFULL + 2,
     BAR_VFULL = BAR_KEMPTY + 2,
     BAR_VEMPTY = BAR_VFULL + 2,
-    BAR_SFULL = BAR_VEMPTY + 2,   // [2] scores complete
-    BAR_SREAD = BAR_SFULL + 2,    // [2] scores in registers
-    BAR_PFULL = BAR_SREAD + 2,    // probabilities written
-    BAR_PVDONE = BAR_PFULL + 1,   // P V complete: P may be written, O read
-    BAR_DRAIN = BAR_PVDONE + 1,   // every product complete
+    BAR_SFULL = BAR_VEMPTY + 2,    // [2] scores complete
+    BAR_SREAD = BAR_SFULL + 2,     // [2] scores read
+    BAR_PFULL = BAR_SREAD + 2,     // [2] probabilities written
+    BAR_PVDONE = BAR_PFULL + 2,    // [2] P V complete: P free, the tile in O
+    BAR_DRAIN = BAR_PVDONE + 2,    // every product complete
     NUM_BARS = BAR_DRAIN + 1
   };
   static constexpr int kOffTmem = kOffBar + NUM_BARS * 8;
   static constexpr int kOffAbort = kOffTmem + 4;
   static constexpr int kOffOdd = kOffAbort + 4;  // [4]: own values that are not finite
   static constexpr int kSmem = kOffOdd + 16 + 1024;
-  // TMEM: S at 0 and 128, P, O, Q
-  static constexpr int kTmemP = 256, kTmemO = 320, kTmemQ = 448, kTmemCols = 512;
+  // TMEM: two buffers of scores, two of probabilities, O
+  static constexpr int kTmemP = 2 * BN, kTmemO = kTmemP + BN, kTmemCols = 512;
   static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// Position in a ring of N: slot and round, counted up one at a time.
+template <int N>
+struct Ring {
+  int slot = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) slot = 0, ++round;
+  }
 };
 
 template <int D, int RS>
@@ -98,20 +103,22 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
 
   if (tid == 0) {
     mbar_init(BAR(C::BAR_Q), C::kSoftWarps);
-    for (int s = 0; s < RS; ++s) {
+    for (int s = 0; s < 2 * RS; ++s) {
       mbar_init(BAR(C::BAR_RAWFULL + s), 1);
-      mbar_init(BAR(C::BAR_RAWEMPTY + s), 8);
+      mbar_init(BAR(C::BAR_RAWEMPTY + s), 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(BAR(C::BAR_KFULL + s), 4);
       mbar_init(BAR(C::BAR_KEMPTY + s), 1);
       mbar_init(BAR(C::BAR_VFULL + s), 4);
       mbar_init(BAR(C::BAR_VEMPTY + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(BAR(C::BAR_SFULL + s), 1);
       mbar_init(BAR(C::BAR_SREAD + s), C::kSoftWarps);
+      mbar_init(BAR(C::BAR_PFULL + s), C::kSoftWarps);
+      mbar_init(BAR(C::BAR_PVDONE + s), 1);
     }
-    mbar_init(BAR(C::BAR_PFULL), C::kSoftWarps);
-    mbar_init(BAR(C::BAR_PVDONE), 1);
     mbar_init(BAR(C::BAR_DRAIN), 2);
     fence_mbar_init();
     *abort_flag = 0;
@@ -169,43 +176,51 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     return cache_page_ok(page, p.num_pages) ? max(0, min(16, k.key_hi - key)) : 0;
   };
 
-  if (warp >= C::kWarpLoad) {
+  if (warp >= C::kWarpLoadK) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegRest));
-   if (warp == C::kWarpLoad) {
+   if (warp == C::kWarpLoadK || warp == C::kWarpLoadV) {
     // ------------------------------------------------------------ loads
+    // k and v each through a ring of its own: a tile of k is wanted, and its
+    // place free again, well before the same tile of v.
+    const bool isv = warp == C::kWarpLoadV;
+    const CUtensorMap* map = isv ? &p.tm_v : &p.tm_k;
+    const int full = C::BAR_RAWFULL + (isv ? RS : 0), empty = C::BAR_RAWEMPTY + (isv ? RS : 0);
+    const uint32_t raw0 = sbase + C::kOffRaw + (isv ? RS * C::kRaw : 0);
     bool ok = true;
-    int n = 0;  // raw tiles over all pieces
+    Ring<RS> at;
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
       int page = load_page(w, k, 0), next_page = -1;
       int keys = keys_of(k, 0, page);
-      for (int j = 0; j < k.nc; ++j, ++n) {
-        if ((j & 3) == 1) next_page = load_page(w, k, j + 3);
-        if ((j & 3) == 0 && j > 0) page = next_page, keys = keys_of(k, j, page);
-        const int st = n % RS;
-        // the first group of each page of this tile issues the page's boxes
+      for (int j = 0; j < k.nc; ++j) {
+        if ((j & 3) == 0) {
+          if (j > 0) page = next_page, keys = keys_of(k, j, page);
+          next_page = load_page(w, k, j + 4);
+        }
+        // the first group of each page of this tile issues the page's box
         const int per = p.page_size >> 4;
         const bool mine = (lane >> 3) == (j & 3) && (lane & 7) % per == 0;
         if (mine && keys == 0 && k.key_lo + BN * j + 16 * (lane & 7) < k.key_hi)
           atomicOr(p.status, kStatusIndex);
         const bool load = mine && keys > 0;
         const unsigned count = __popc(__ballot_sync(0xffffffffu, load));
-        if (n >= RS && !(ok = mbar_wait_warp(BAR(C::BAR_RAWEMPTY + st), (n / RS - 1) & 1, ab)))
+        if (at.round > 0 &&
+            !(ok = mbar_wait_warp(BAR(empty + at.slot), (at.round - 1) & 1, ab)))
           break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(BAR(C::BAR_RAWFULL + st), count * p.page_size * D * 2);
+        if (lane == 0) mbar_arrive_expect_tx(BAR(full + at.slot), count * p.page_size * D);
         __syncwarp();
-        if (load) {
-          const uint32_t dst = sbase + C::kOffRaw + st * 2 * C::kRaw + (lane & 7) * 16 * D;
-          tma_load_3d(dst, &p.tm_k, BAR(C::BAR_RAWFULL + st), 0, k.h * p.page_size, page);
-          tma_load_3d(dst + C::kRaw, &p.tm_v, BAR(C::BAR_RAWFULL + st), 0, k.h * p.page_size, page);
-        }
+        if (load)
+          tma_load_3d(raw0 + at.slot * C::kRaw + (lane & 7) * 16 * D, map, BAR(full + at.slot), 0,
+                      k.h * p.page_size, page);
         __syncwarp();
+        at.next();
       }
     }
     if (!ok && lane == 0)  // giving up: what is in flight lands first
-      for (int i = n > RS ? n - RS : 0; i < n; ++i)
-        mbar_wait_limited(BAR(C::BAR_RAWFULL + i % RS), (i / RS) & 1, 100000000ull);
+      for (int i = 1; i <= RS && i <= at.round * RS + at.slot; ++i) {
+        const int n = at.round * RS + at.slot - i;
+        mbar_wait_limited(BAR(full + n % RS), (n / RS) & 1, 100000000ull);
+      }
     __syncwarp();
    } else if (warp == C::kWarpS || warp == C::kWarpPV) {
     // ------------------------------------------------------------ products
@@ -214,40 +229,49 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
       int n = 0, q = 0;  // tiles, versions of Q
       for (; w.b >= 0 && ok; next_piece(p, w)) {
         const Tiles k = tiles_of(w);
+#pragma unroll 1
         for (int j = 0; j < k.all; ++j, ++n) {
           const int b = n & 1;
+          const uint32_t done = ((n >> 1) - 1) & 1, now = (n >> 1) & 1;
           if (warp == C::kWarpS) {
             // Q as f16 at the first cached tile, as bf16 at the first own one
             if ((j == 0 || j == k.nc) && !(ok = mbar_wait(BAR(C::BAR_Q), q++ & 1, ab))) break;
-            if (!(ok = mbar_wait(BAR(C::BAR_KFULL + b), (n >> 1) & 1, ab))) break;
-            if (n >= 2 && !(ok = mbar_wait(BAR(C::BAR_SREAD + b), ((n >> 1) - 1) & 1, ab))) break;
+            if (!(ok = mbar_wait(BAR(C::BAR_KFULL + b), now, ab))) break;
+            if (n >= 2 && !(ok = mbar_wait(BAR(C::BAR_SREAD + b), done, ab))) break;
             tc_fence_after();
             const uint32_t id = j < k.nc ? idesc_f16(C::BM, BN, false, false)
                                          : idesc_bf16(C::BM, BN, false, false);
+            uint64_t qd = sdesc_sw128(sbase + C::kOffQ, 16, 1024);
+            uint64_t kd = sdesc_sw128(sbase + C::kOffK + b * C::kTile, 16, 1024);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {  // descriptors count 16 bytes
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t bd = sdesc_sw128(
-                  sbase + C::kOffK + b * C::kTile + (kk >> 2) * (BN * 128) + (kk & 3) * 32, 16,
-                  1024);
-              mma_ts(tmem + b * BN, tmem + C::kTmemQ + 8 * kk, bd, id, kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss(tmem + b * BN, qd + 2 * kk, kd + 2 * kk, id, c > 0 || kk > 0 ? 1u : 0u);
+              qd += BN * 128 / 16;
+              kd += BN * 128 / 16;
             }
             mma_commit(BAR(C::BAR_SFULL + b));
             mma_commit(BAR(C::BAR_KEMPTY + b));
           } else {
-            if (!(ok = mbar_wait(BAR(C::BAR_VFULL + b), (n >> 1) & 1, ab))) break;
-            if (!(ok = mbar_wait(BAR(C::BAR_PFULL), n & 1, ab))) break;
+            if (!(ok = mbar_wait(BAR(C::BAR_VFULL + b), now, ab))) break;
+            if (!(ok = mbar_wait(BAR(C::BAR_PFULL + b), now, ab))) break;
             tc_fence_after();
             const uint32_t id =
                 j < k.nc ? idesc_f16(C::BM, D, false, true) : idesc_bf16(C::BM, D, false, true);
+            uint64_t vd = sdesc_sw128(sbase + C::kOffV + b * C::kTile, BN * 128, 1024);
+            uint32_t pa = tmem + C::kTmemP + b * (BN / 2);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk) {
-              const uint64_t bd = sdesc_sw128(
-                  sbase + C::kOffV + b * C::kTile + kk * 16 * 128, BN * 128, 1024);
-              mma_ts(tmem + C::kTmemO, tmem + C::kTmemP + 8 * kk, bd, id,
-                     (j > 0 || kk > 0) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tmem + C::kTmemO, pa + 8 * kk, vd + kk * (16 * 128 / 16), id,
+                       j > 0 || c > 0 || kk > 0 ? 1u : 0u);
+              pa += 32;
+              vd += 64 * 128 / 16;
             }
             mma_commit(BAR(C::BAR_VEMPTY + b));
-            mma_commit(BAR(C::BAR_PVDONE));
+            mma_commit(BAR(C::BAR_PVDONE + b));
           }
         }
       }
@@ -264,7 +288,8 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     const int c = cw * 32 + lane;        // 0 .. 127
     const int full = isv ? C::BAR_VFULL : C::BAR_KFULL, empty = full + 2;
     const uint32_t tiles0 = sbase + (isv ? C::kOffV : C::kOffK);
-    const uint32_t raw0 = sbase + C::kOffRaw + (isv ? C::kRaw : 0);
+    const uint32_t raw0 = sbase + C::kOffRaw + (isv ? RS * C::kRaw : 0);
+    const int rawfull = C::BAR_RAWFULL + (isv ? RS : 0), rawempty = C::BAR_RAWEMPTY + (isv ? RS : 0);
     // e4m3 -> f16: a thread turns 16 values (a 16-byte piece) into two pieces
     // of its row.  Eight lanes, one phase of a shared-memory access, take four
     // neighbouring pieces of rows r and r ^ 5: under either tile's swizzle
@@ -275,7 +300,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     const int r8 = (lane >> 3) ^ (5 * ((lane >> 2) & 1));  // row of its eight
     auto convert = [&](uint32_t raw, uint32_t dst, bool mask, int group_keys) {
       constexpr int kChunks = D / 64;
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 4 * kChunks; half += 4) {
         uint4 x[4];
 #pragma unroll
@@ -327,26 +352,27 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
       return odd;
     };
     bool ok = true;
-    int n = 0, raw = 0, owns = 0;  // operand tiles, raw tiles, pieces with own keys
+    int n = 0, owns = 0;  // operand tiles, pieces with own keys
+    Ring<RS> at;
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
       int keys = 0, next_page = -1;
       if (isv) keys = keys_of(k, 0, load_page(w, k, 0));
       for (int j = 0; j < k.all; ++j, ++n) {
         const int b = n & 1;
-        if (isv && (j & 3) == 1) next_page = load_page(w, k, j + 3);
-        if (isv && (j & 3) == 0 && j > 0) keys = keys_of(k, j, next_page);
+        if (isv && (j & 3) == 0) {
+          if (j > 0) keys = keys_of(k, j, next_page);
+          next_page = load_page(w, k, j + 4);
+        }
         if (n >= 2 && !(ok = mbar_wait_warp(BAR(empty + b), ((n >> 1) - 1) & 1, ab))) break;
         const uint32_t dst = tiles0 + b * C::kTile;
         if (j < k.nc) {
-          const int st = raw % RS;
-          if (!(ok = mbar_wait_warp(BAR(C::BAR_RAWFULL + st), (raw / RS) & 1, ab))) break;
-          const uint32_t src = raw0 + st * 2 * C::kRaw;
+          if (!(ok = mbar_wait_warp(BAR(rawfull + at.slot), at.round & 1, ab))) break;
+          const uint32_t src = raw0 + at.slot * C::kRaw;
           const int group_keys = __shfl_sync(0xffffffffu, keys, 8 * (j & 3) + (lane & 7));
-          if (isv && __any_sync(0xffffffffu, group_keys < 16)) convert(src, dst, true, group_keys);
-          else convert(src, dst, false, 0);
-          mbar_arrive_warp(BAR(C::BAR_RAWEMPTY + st));
-          ++raw;
+          convert(src, dst, isv && __any_sync(0xffffffffu, group_keys < 16), group_keys);
+          mbar_arrive_warp(BAR(rawempty + at.slot));
+          at.next();
         } else {
           if (isv && j == k.nc) {
             // The notes of the last four pieces with own keys; this piece's
@@ -376,8 +402,10 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
       const int hq = k.h * p.G + (min(r, k.R - 1) - tok * p.G);
       const int end = r < k.R ? cache_own_end(w.rq.len, tok, w.rq.n, p.bs) : 0;
       const __nv_bfloat16* qsrc = p.q + (w.rq.row0 + tok) * p.q_sr + hq * p.q_sh + half * DH;
-      int keys = 0, next_page = -1;
-      float ks = 0.f, vs = 0.f, vmax = 0.f, next_ks = 0.f, next_vs = 0.f;
+      // Pages two batches of four tiles ahead, scales one: they may come from
+      // memory under full load, microseconds away.
+      int next_page = load_page(w, k, 4), last_page = load_page(w, k, 0);
+      float next_ks = 0.f, next_vs = 0.f;
       auto load_scales = [&](int page, float* a, float* b) {
         const bool has = cache_page_ok(page, p.num_pages);
         const long long at = static_cast<long long>(page) * p.Hk + k.h;
@@ -389,9 +417,9 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
         return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
       };
-      next_page = load_page(w, k, 0);
-      // The row's half of Q into TMEM, f16 after a power of two or bf16.  The
-      // scores of the tiles before are complete, so Q may be replaced.
+      // The row's half of Q as the products' A operand, f16 after a power of two
+      // or bf16.  The scores of the tiles before are complete, so Q may be
+      // replaced.
       float factor = 0.f;  // undoes the row's power of two, with the softmax scale
       auto put_q = [&](bool f16) {
         uint32_t v[D / 4];
@@ -418,128 +446,146 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
             v[i] = pack_f16x2(__uint_as_float(v[i] << 16) * inv,
                               __uint_as_float(v[i] & 0xffff0000u) * inv);
         }
-        tmem_st_half<D / 4, D / 4>(t_lane + C::kTmemQ, v);
-        tmem_wait_st();
-        tc_fence_before();
+        // 16-byte unit u of row x: 64-dim chunk u / 8, swizzled by the row
+        const int x = lb + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int u = half * (D / 16) + i;
+          st_shared_v4(sbase + C::kOffQ + (u >> 3) * (C::BM * 128) + x * 128 + (((u ^ x) & 7) << 4),
+                       v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        fence_proxy_async_smem();
         mbar_arrive_warp(BAR(C::BAR_Q));
       };
       if (k.nc > 0) put_q(true);
-      load_scales(next_page, &ks, &vs);
-      keys = keys_of(k, 0, next_page);
-      vmax = group_max(vs);
+      float ks, vs;
+      load_scales(last_page, &ks, &vs);
+      int keys = keys_of(k, 0, last_page);
+      float vmax = group_max(vs);
       float m = -INFINITY, l = 0.f;
       float c = pow2_bits(kCacheMinExp), inv_c = pow2_bits(-kCacheMinExp);  // unit of O
-      // What tile j's softmax needs of its half row's four groups of 16 keys:
-      // score factors, value weights, keys; found ahead, while it would wait.
-      float fg[4], wg[4], c_tile;
-      int kg[4];
-      auto tile_groups = [&](int j) {
-        if ((j & 3) == 1) next_page = load_page(w, k, j + 3);
-        if ((j & 3) == 3) load_scales(next_page, &next_ks, &next_vs);
-        if ((j & 3) == 0 && j > 0) {
-          ks = next_ks, vs = next_vs;
-          keys = keys_of(k, j, next_page);
-          vmax = group_max(vs);
-        }
-        if (j < k.nc) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int src = 8 * (j & 3) + 4 * half + i;
-            // never 0 (a group without keys): 0 * -inf is not a number
-            fg[i] = fmaxf(factor * __shfl_sync(0xffffffffu, ks, src), 1.1754944e-38f);
-            wg[i] = __shfl_sync(0xffffffffu, vs, src);
-            kg[i] = __shfl_sync(0xffffffffu, keys, src);
-          }
-          c_tile = __shfl_sync(0xffffffffu, vmax, 8 * (j & 3));
-        } else {
-          const int first = BN * (j - k.nc) + 64 * half;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            fg[i] = p.scale_log2;
-            wg[i] = 1.f;
-            kg[i] = min(16, max(0, end - first - 16 * i));
-          }
-          c_tile = 1.f;
-        }
-      };
-#pragma unroll 1
-      for (int j = 0; j < k.all; ++j, ++n) {
+      unsigned full = __ballot_sync(0xffffffffu, keys == 16);  // groups with all 16 keys
+      // One tile, in three copies so that the common one is short: cached with
+      // all its keys, cached with some, own keys (bf16, row by row).
+      constexpr int kWhole = 0, kPart = 1, kOwn = 2;
+      auto tile = [&](auto kind, int j) -> bool {
+        constexpr int kKind = decltype(kind)::value;
         const int b = n & 1;
-        const bool cached = j < k.nc;
-        if (j == k.nc) put_q(false);
-        tile_groups(j);
-        const float c_new = fmaxf(c, c_tile);
-        const bool whole =
-            __all_sync(0xffffffffu, kg[0] == 16 && kg[1] == 16 && kg[2] == 16 && kg[3] == 16);
-        if (!(ok = mbar_wait_warp(BAR(C::BAR_SFULL + b), (n >> 1) & 1, ab))) break;
-        tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld_half<32, 64>(t_lane + b * BN, sr);
-        tmem_ld_half<32, 64>(t_lane + b * BN + 32, sr + 32);
-        tmem_wait_ld();
-        tmem_pin<64>(sr);
-        tc_fence_before();
-        mbar_arrive_warp(BAR(C::BAR_SREAD + b));
-        if (!whole) {
+        const uint32_t s_col = t_lane + b * BN, p_col = t_lane + C::kTmemP + b * (BN / 2);
+        // Of 32 keys of the half row: score factors and value weights of their two
+        // groups (never 0, where a group has no keys: 0 * -inf is not a
+        // number), and which of them count.
+        auto groups = [&](int x, float* f, float* wt) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t keep = (1u << kg[i]) - 1u;
+          for (int i = 0; i < 2; ++i) {
+            const int src = 8 * (j & 3) + 4 * half + 2 * x + i;
+            f[i] = kKind == kOwn ? p.scale_log2
+                                 : fmaxf(factor * __shfl_sync(0xffffffffu, ks, src), 1.1754944e-38f);
+            wt[i] = kKind == kOwn ? inv_c : __shfl_sync(0xffffffffu, vs, src) * inv_c;
+          }
+        };
+        auto scores = [&](int x, uint32_t* sr) {
+          tmem_ld_half<32, 64>(s_col + 32 * x, sr);
+          tmem_wait_ld();
+          tmem_pin<32>(sr);
+          if constexpr (kKind != kWhole) {
+            uint32_t keep;
+            if constexpr (kKind == kPart) {
+              const int src = 8 * (j & 3) + 4 * half + 2 * x;
+              const int k0 = __shfl_sync(0xffffffffu, keys, src);
+              const int k1 = __shfl_sync(0xffffffffu, keys, src + 1);
+              keep = ((1u << k0) - 1u) | (((1u << k1) - 1u) << 16);
+            } else {
+              const int left = end - BN * (j - k.nc) - 64 * half - 32 * x;
+              keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+            }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 32; ++e) {
               const uint32_t mk = bit_spread(keep, e);
-              sr[16 * i + e] = (sr[16 * i + e] & mk) | (0xff800000u & ~mk);
+              sr[e] = (sr[e] & mk) | (0xff800000u & ~mk);
             }
           }
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, max_tree<16>(sr + 16 * i) * fg[i]);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        };
+        const float c_new =
+            fmaxf(c, kKind == kOwn ? 1.f : __shfl_sync(0xffffffffu, vmax, 8 * (j & 3)));
         float shrink = 1.f;
         if (c_new != c) {
           shrink = c / c_new;
           c = c_new;
           inv_c = 1.f / c;
         }
-        if (top > m + kSlack) {
-          const float a = ex2_approx(m - top);
-          m = top;
-          l *= a;
-          shrink *= a;
-        }
-        const float ref = m == -INFINITY ? 0.f : kShift - m;
-        const uint64_t ref2 = f2_pack(ref, ref);
-        uint64_t acc[2] = {0ull, 0ull};
-        uint32_t pk[32];  // held until P is free
-        auto probabilities = [&](auto f16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float wt = wg[i] * inv_c;
-            const uint64_t f2 = f2_pack(fg[i], fg[i]), w2 = f2_pack(wt, wt);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int at = 16 * i + 2 * e;
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[at]), __uint_as_float(sr[at + 1])), f2,
-                               ref2),
-                        x0, x1);
-              const uint64_t pr = f2_pack(ex2_approx(x0), ex2_approx(x1));
-              acc[e & 1] = f2_add(acc[e & 1], pr);
-              f2_unpack(f2_mul(pr, w2), x0, x1);
-              pk[8 * i + e] = decltype(f16)::value ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+        if (!mbar_wait_warp(BAR(C::BAR_SFULL + b), (n >> 1) & 1, ab)) return false;
+        if (n >= 2 && !mbar_wait_warp(BAR(C::BAR_PVDONE + b), ((n >> 1) - 1) & 1, ab)) return false;
+        tc_fence_after();
+        // The probabilities are taken against the reference as it stands; only
+        // where their sum says that one may have outgrown f16, or where the
+        // piece begins, is the maximum looked for and the tile done (again).
+        // All loops are rolled: with five roles on a scheduler the fetching of
+        // instructions costs more than their issue.
+        bool look = j == 0;
+#pragma unroll 1
+        for (;;) {
+          if (look) {
+            float top = m;
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              uint32_t sr[32];
+              float f[2], wt[2];
+              groups(x, f, wt);
+              scores(x, sr);
+              top = fmaxf(top, fmaxf(max_tree<16>(sr) * f[0], max_tree<16>(sr + 16) * f[1]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (top > m) {
+              const float a = ex2_approx(m - top);
+              m = top;
+              l *= a;
+              shrink *= a;
             }
           }
-        };
-        if (cached) probabilities(std::true_type{});
-        else probabilities(std::false_type{});
-        float a0, a1;
-        f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-        l += a0 + a1;
-        // P V of the tile before has read P and added to O
-        if (n > 0 && !(ok = mbar_wait_warp(BAR(C::BAR_PVDONE), (n - 1) & 1, ab))) break;
-        tc_fence_after();
-        if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+          const float ref = m == -INFINITY ? 0.f : kShift - m;
+          const uint64_t ref2 = f2_pack(ref, ref);
+          uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            uint32_t sr[32], pk[16];
+            float f[2], wt[2];
+            groups(x, f, wt);
+            scores(x, sr);
 #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint64_t f2 = f2_pack(f[i], f[i]), w2 = f2_pack(wt[i], wt[i]);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int at = 16 * i + 2 * e;
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[at]), __uint_as_float(sr[at + 1])), f2,
+                                 ref2),
+                          x0, x1);
+                const uint64_t pr = f2_pack(ex2_approx(x0), ex2_approx(x1));
+                acc[e & 1] = f2_add(acc[e & 1], pr);
+                f2_unpack(f2_mul(pr, w2), x0, x1);
+                pk[8 * i + e] = kKind == kOwn ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
+              }
+            }
+            tmem_st_half<16, 32>(p_col + 16 * x, pk);
+          }
+          float a0, a1;
+          f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+          a0 += a1;
+          if (look || !__any_sync(0xffffffffu, a0 > kMostSum || m == -INFINITY)) {
+            l += a0;
+            break;
+          }
+          look = true;
+        }
+        tc_fence_before();
+        mbar_arrive_warp(BAR(C::BAR_SREAD + b));
+        // a moved reference or unit: O of the tiles before, once they are in it
+        if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+          if (!mbar_wait_warp(BAR(C::BAR_PVDONE + (b ^ 1)), ((n - 1) >> 1) & 1, ab)) return false;
+          tc_fence_after();
+#pragma unroll 1
           for (int x = 0; x < DH / 16; ++x) {
             uint32_t o[16];
             tmem_ld_half<16, DH>(t_lane + C::kTmemO + 16 * x, o);
@@ -550,15 +596,39 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
             tmem_st_half<16, DH>(t_lane + C::kTmemO + 16 * x, o);
           }
         }
-        tmem_st_half<32, 32>(t_lane + C::kTmemP, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive_warp(BAR(C::BAR_PFULL));
+        mbar_arrive_warp(BAR(C::BAR_PFULL + b));
+        return true;
+      };
+#pragma unroll 1
+      for (int j = 0; j < k.all && ok; ++j) {
+        if ((j & 3) == 0) {
+          if (j > 0) {
+            ks = next_ks, vs = next_vs;
+            keys = keys_of(k, j, last_page);
+            vmax = group_max(vs);
+            full = __ballot_sync(0xffffffffu, keys == 16);
+          }
+          last_page = next_page;
+          load_scales(last_page, &next_ks, &next_vs);
+          next_page = load_page(w, k, j + 8);
+        }
+        if (j == k.nc) put_q(false);
+        if (j >= k.nc)
+          ok = tile(std::integral_constant<int, kOwn>{}, j);
+        else if (((full >> (8 * (j & 3))) & 0xffu) == 0xffu)
+          ok = tile(std::integral_constant<int, kWhole>{}, j);
+        else
+          ok = tile(std::integral_constant<int, kPart>{}, j);
+        if (ok) ++n;
       }
 
       // -------------------------------------------------------- read-out
       if (!ok) break;
-      if (k.all > 0 && !(ok = mbar_wait_warp(BAR(C::BAR_PVDONE), (n - 1) & 1, ab))) break;
+      if (k.all > 0 &&
+          !(ok = mbar_wait_warp(BAR(C::BAR_PVDONE + ((n - 1) & 1)), ((n - 1) >> 1) & 1, ab)))
+        break;
       tc_fence_after();
       if (k.own > 0) ++owns;
       const bool odd = k.own > 0 && s_odd[owns & 3] != 0;
@@ -648,7 +718,7 @@ cudaError_t launch_wide(const CacheFwdParams& p, cudaStream_t stream) {
 
 cudaError_t launch_cache_wide(const CacheFwdParams& p, int headdim, cudaStream_t stream) {
   if (headdim == 64) return launch_wide<64, 6>(p, stream);
-  if (headdim == 128) return launch_wide<128, 3>(p, stream);
+  if (headdim == 128) return launch_wide<128, 2>(p, stream);
   return cudaErrorInvalidValue;
 }
 
