@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) dfa_cache_plan_kernel(const Plan
   __shared__ long long s_pages[kPlanThreads + 1], s_rows[kPlanThreads + 1];
   __shared__ int s_len[kPlanThreads], s_has[kPlanThreads];
   cg::cluster_group cluster = cg::this_cluster();
+  grid_launch_dependents();
   grid_dependency_wait();
   const int tid = threadIdx.x;
   const int part = static_cast<int>(cluster.block_rank());
@@ -198,6 +199,7 @@ struct ReleaseParams {
 __global__ void __launch_bounds__(kPlanThreads) dfa_cache_release_kernel(const ReleaseParams p) {
   constexpr int kWarps = kPlanThreads / 32;
   __shared__ int s_count[kWarps];
+  grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long capacity = static_cast<long long>(p.max_pages) * p.page_size;
@@ -300,6 +302,7 @@ template <int D, int NT, int VPT>
 __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams p) {
   constexpr int kVec = D / 8;  // vectors per token and head
   __shared__ unsigned s_top[NT / 32];
+  grid_launch_dependents();
   grid_dependency_wait();
   // heads fastest: neighbouring blocks read neighbouring pieces of the rows
   const unsigned head = blockIdx.x % (2u * p.Hk), at = blockIdx.x / (2u * p.Hk);

@@ -63,9 +63,17 @@ DFA_HD int cache_blocks(long long total, int limit, int least) {
   const long long n = (total + least - 1) / least;
   return static_cast<int>(n < limit ? n : limit);
 }
-DFA_HD long long cache_run(int x, long long total, int blocks) { return x * total / blocks; }
+DFA_HD long long cache_run(int x, long long total, int blocks) {
+  // 32-bit division where the product fits (blocks < 2^10): the usual case
+  if (total < (1 << 22) && blocks < (1 << 10))
+    return static_cast<unsigned>(x) * static_cast<unsigned>(total) / static_cast<unsigned>(blocks);
+  return x * total / blocks;
+}
 // The block whose run holds unit w.
 DFA_HD int cache_owner(long long w, long long total, int blocks) {
+  if (total < (1 << 22) && blocks < (1 << 10))
+    return static_cast<int>((static_cast<unsigned>(w + 1) * static_cast<unsigned>(blocks) - 1u) /
+                            static_cast<unsigned>(total));
   return static_cast<int>(((w + 1) * blocks - 1) / total);
 }
 

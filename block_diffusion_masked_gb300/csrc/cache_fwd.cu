@@ -234,11 +234,8 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
     ++la_u;
     return true;
   };
-  if (wr == 0) {
-#pragma unroll 1
-    for (int s = 0; s < STAGES; ++s) ahead();
-  }
   int consumed = 0;
+  bool primed = false;
   bool ok = true;
 
 #pragma unroll 1
@@ -272,6 +269,11 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
 #pragma unroll
         for (int sg = 0; sg < kSeg; ++sg) load_q(mt, i, sg, qv[mt][i][sg]);
   }
+  if (!primed && wr == 0) {  // the run's first loads, behind the queries'
+#pragma unroll 1
+    for (int s = 0; s < STAGES; ++s) ahead();
+  }
+  primed = true;
   int own = 0;
   if (p.k != nullptr && w.last())
     own = cache_own_end(w.rq.len, min(R - 1, row_base + T::kRows - 1) / p.G, w.rq.n, p.bs);
@@ -727,7 +729,10 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
   // The upper half of the groups leaves its outputs, the lower half adds its
   // own to them.
   float* join = reinterpret_cast<float*>(smem + T::kOffJoin);
-  auto leave = [&](bool add) {
+#pragma unroll 1
+  for (int turn = 0; turn < 2; ++turn) {
+    const bool add = turn == 1;
+    if ((wk >= T::kHalfK) != add) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -761,11 +766,9 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
             }
           }
       }
-  };
-  if (wk >= T::kHalfK) leave(false);
-  __syncthreads();
-  if (wk < T::kHalfK) leave(true);
-  __syncthreads();
+    }
+    __syncthreads();
+  }
   const bool single = w.whole();
   for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
     const int r = i / (D / 4), d4 = i - r * (D / 4);
@@ -808,101 +811,80 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
   }
 }
 
-// The pieces of the segments that a run's end has cut, joined: weights
-// 2^(lse_s - max), one warp a row and query head, the pieces' outputs read
-// once.  Blocks stride over the rows of the requests' cut segments; a request
-// whose segments are all whole is passed over.
-constexpr int kJoinWarps = 8;
+// The pieces of the segments that runs' ends have cut, joined: weights
+// 2^(lse_s - max), a warp a row and query head, the pieces' outputs read once.
+// Blocks (x, y): the cut that block x of the launch before answers for, rows y,
+// y + gridDim.y, ... of kJoinWarps.
+constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
     dfa_cache_join_kernel(const __grid_constant__ CacheFwdParams p) {
   constexpr int kVec = D / 32;  // floats per lane
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  bool bad = false;
-  // The sizes were complete before the launch whose pieces are joined let this
-  // one start; only its results have to be waited for.
-  const Census c = take_census(p, &bad);
-  bool waited = false;
-  // Segments that hold a run's end are found from the runs.
-  for (int x = blockIdx.x; x < c.blocks; x += gridDim.x) {
-    Piece w;
-    const long long lo = cache_run(x, c.total, c.blocks);
-    find_unit(p, c, lo, &bad, &w);
-    const long long start = lo - w.u0;
-    const int x0 = cache_owner(start, c.total, c.blocks);
-    const int x1 = cache_owner(start + w.keys, c.total, c.blocks);
-    // A cut segment is joined once: by the block that begins with it, or else
-    // by the next one, whose run begins inside it.
-    const bool at_start = cache_run(x0, c.total, c.blocks) == start;
-    if (x1 == x0 || x != (at_start ? x0 : x0 + 1)) continue;
-    if (!waited) grid_dependency_wait();
-    waited = true;
-    const int rtiles = row_tiles(p, w.rq);
-    const int h = w.seg / rtiles, row_base = (w.seg - h * rtiles) * p.tile_rows;
-    const int rows = min(p.tile_rows, w.rq.n * p.G - row_base);
-    // the first piece is its block's last unless the block begins with it
-    const int slot0 = 2 * x0 + (at_start ? 0 : 1), n = x1 - x0 + 1;
-    for (int r = warp + kJoinWarps * blockIdx.y; r < rows; r += kJoinWarps * gridDim.y) {
-      auto at = [&](int s) {
-        return static_cast<long long>(s == 0 ? slot0 : 2 * (x0 + s)) * p.tile_rows + r;
-      };
-      // kBatch pieces at a time: their outputs and, a lane each, their lse are
-      // read together, then weighed against the maximum so far
-      constexpr int kBatch = D == 256 ? 8 : 16;
-      float top = -INFINITY, sum = 0.f, acc[kVec];
+  const Cut cut = p.cuts[blockIdx.x];
+  const int n = cut.pieces;
+  if (n == 0) return;
+  for (int r = warp + kJoinWarps * blockIdx.y; r < cut.rows; r += kJoinWarps * gridDim.y) {
+    auto at = [&](int s) {
+      return static_cast<long long>(s == 0 ? cut.slot0 : 2 * (cut.x0 + s)) * p.tile_rows + r;
+    };
+    // kBatch pieces at a time: their outputs and, a lane each, their lse are
+    // read together, then weighed against the maximum so far
+    constexpr int kBatch = 8;
+    float top = -INFINITY, sum = 0.f, acc[kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
-      for (int s0 = 0; s0 < n; s0 += kBatch) {
-        float y[kBatch][kVec];
+    for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+    for (int s0 = 0; s0 < n; s0 += kBatch) {
+      float y[kBatch][kVec];
 #pragma unroll
-        for (int s = 0; s < kBatch; ++s) {
+      for (int s = 0; s < kBatch; ++s) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) y[s][i] = 0.f;
-          if (s0 + s < n) {
-            const float* src = p.part_o + at(s0 + s) * D + lane * kVec;
-            if constexpr (kVec == 2) {
-              *reinterpret_cast<float2*>(y[s]) = *reinterpret_cast<const float2*>(src);
-            } else {
+        for (int i = 0; i < kVec; ++i) y[s][i] = 0.f;
+        if (s0 + s < n) {
+          const float* src = p.part_o + at(s0 + s) * D + lane * kVec;
+          if constexpr (kVec == 2) {
+            *reinterpret_cast<float2*>(y[s]) = *reinterpret_cast<const float2*>(src);
+          } else {
 #pragma unroll
-              for (int i = 0; i < kVec; i += 4)
-                *reinterpret_cast<float4*>(y[s] + i) = *reinterpret_cast<const float4*>(src + i);
-            }
+            for (int i = 0; i < kVec; i += 4)
+              *reinterpret_cast<float4*>(y[s] + i) = *reinterpret_cast<const float4*>(src + i);
           }
         }
-        const float lse = lane < kBatch && s0 + lane < n ? p.part_lse[at(s0 + lane)] : -INFINITY;
-        float m = lse;
-#pragma unroll
-        for (int off = kBatch / 2; off > 0; off >>= 1)
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        m = fmaxf(top, __shfl_sync(0xffffffffu, m, 0));
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float shrink = ex2_approx(top - ref), wgt = ex2_approx(lse - ref);
-        top = m;
-        sum *= shrink;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) acc[i] *= shrink;
-#pragma unroll
-        for (int s = 0; s < kBatch; ++s) {
-          const float ws = __shfl_sync(0xffffffffu, wgt, s);
-          sum += ws;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) acc[i] = fmaf(ws, y[s][i], acc[i]);
-        }
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const int tok = (row_base + r) / p.G, hq = h * p.G + (row_base + r - tok * p.G);
-      const long long row = w.rq.row0 + tok;
-      __nv_bfloat16* dst = p.out + (row * p.H + hq) * D + lane * kVec;
+      const float lse = lane < kBatch && s0 + lane < n ? p.part_lse[at(s0 + lane)] : -INFINITY;
+      float m = lse;
 #pragma unroll
-      for (int i = 0; i < kVec; i += 2)
-        *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-      if (lane == 0)
-        p.lse[static_cast<long long>(hq) * p.rows + row] =
-            sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * 0.6931471805599453f;
+      for (int off = kBatch / 2; off > 0; off >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      m = fmaxf(top, __shfl_sync(0xffffffffu, m, 0));
+      const float ref = m == -INFINITY ? 0.f : m;
+      const float shrink = ex2_approx(top - ref), wgt = ex2_approx(lse - ref);
+      top = m;
+      sum *= shrink;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] *= shrink;
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, wgt, s);
+        sum += ws;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) acc[i] = fmaf(ws, y[s][i], acc[i]);
+      }
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int tok = (cut.row_base + r) / p.G;
+    const int hq = cut.h * p.G + (cut.row_base + r - tok * p.G);
+    const long long row = cut.row0 + tok;
+    __nv_bfloat16* dst = p.out + (row * p.H + hq) * D + lane * kVec;
+#pragma unroll
+    for (int i = 0; i < kVec; i += 2)
+      *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0)
+      p.lse[static_cast<long long>(hq) * p.rows + row] =
+          sum == 0.f ? -INFINITY : (top + lg2_approx(sum)) * 0.6931471805599453f;
   }
-  // What comes after this launch may count on the one before it.
-  if (!waited) grid_dependency_wait();
 }
 
 // ------------------------------------------------------------------ host
@@ -969,7 +951,8 @@ long long dfa_cache_workspace_bytes(int batch, int rows, int max_new, int heads,
   if (const int rc = device_info(&di)) return rc;
   if (max_new > rows) max_new = rows;
   const CachePlan c = cache_plan_for(max_new, heads / kv_heads, headdim, di.sms);
-  return 2LL * c.blocks * c.tile_rows * (headdim + 1) * 4;
+  return 2LL * c.blocks * c.tile_rows * (headdim + 1) * 4 +
+         c.blocks * static_cast<long long>(sizeof(Cut));
 }
 
 int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k_cache,
@@ -1001,7 +984,8 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   const int G = heads / kv_heads, d = headdim;
   const CachePlan c = cache_plan_for(max_new, G, d, di.sms);
   const long long parts = 2LL * c.blocks * c.tile_rows;
-  if (workspace_bytes < parts * (d + 1) * 4) return DFA_EINVAL;
+  if (workspace_bytes < parts * (d + 1) * 4 + c.blocks * static_cast<long long>(sizeof(Cut)))
+    return DFA_EINVAL;
   CacheFwdParams p{};
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d),
                               static_cast<cuuint64_t>(kv_heads) * page_size,
@@ -1034,6 +1018,7 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   p.lse = lse;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + parts * d;
+  p.cuts = reinterpret_cast<Cut*>(p.part_lse + parts);
   p.status = di.status;
   p.batch = batch;
   p.rows = rows;
@@ -1063,7 +1048,8 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   if (e == cudaSuccess && !whole) {
     auto join = d == 64 ? dfa_cache_join_kernel<64>
                         : d == 128 ? dfa_cache_join_kernel<128> : dfa_cache_join_kernel<256>;
-    const dim3 grid(c.blocks, (c.tile_rows + kJoinWarps - 1) / kJoinWarps);
+    const int rows = (c.tile_rows + kJoinWarps - 1) / kJoinWarps;
+    const dim3 grid(c.blocks, rows < 16 ? rows : 16);
     e = launch_chained(join, grid, dim3(32 * kJoinWarps), 0, s, p);
   }
   return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);

@@ -12,6 +12,14 @@
 
 namespace dfa {
 
+// A segment that runs' ends have cut, for the launch that joins its pieces:
+// `pieces` of them (0: nothing to join), the first in slot `slot0`, the s-th in
+// slot 2 (x0 + s); the segment's head, first row and rows, and its request's
+// first row.
+struct Cut {
+  int pieces, slot0, x0, h, row_base, rows, row0, unused;
+};
+
 struct CacheFwdParams {
   CUtensorMap tm_k, tm_v;  // (headdim, kv_heads * page_size, pages) bytes
   const __nv_bfloat16* q;  // (rows, heads, headdim), strided
@@ -27,6 +35,7 @@ struct CacheFwdParams {
   float* lse;          // (heads, rows)
   float* part_o;       // (2 * blocks, tile rows, headdim): pieces of split segments
   float* part_lse;     // (2 * blocks, tile rows), log2
+  Cut* cuts;           // (blocks), each written by the block it is numbered after
   unsigned* status;
   int batch, rows, max_new, H, Hk, G, bs;
   int page_size, page_shift, num_pages, max_pages;
@@ -44,7 +53,7 @@ struct Request {
   int len, row0, n;
 };
 __device__ __forceinline__ Request load_request(const CacheFwdParams& p, int b, bool* bad) {
-  const int len = __ldcg(p.cache_lens + b), r0 = __ldcg(p.cu_new + b), r1 = __ldcg(p.cu_new + b + 1);
+  const int len = p.cache_lens[b], r0 = p.cu_new[b], r1 = p.cu_new[b + 1];
   const bool ok = len >= 0 && len <= p.max_pages * p.page_size && r0 >= 0 && r1 >= r0 &&
                   r1 <= p.rows && r1 - r0 <= p.max_new;
   if (!ok) {
@@ -125,7 +134,14 @@ __device__ __forceinline__ void find_unit(const CacheFwdParams& p, const Census&
       const long long n = static_cast<long long>(u) * p.Hk * row_tiles(p, r);
       if (at < before + n) {
         const long long in = at - before;
-        fb = b, fseg = static_cast<int>(in / u), fu = static_cast<int>(in % u);
+        if (in < (1LL << 31)) {
+          fseg = static_cast<int>(in) / u;
+          fu = static_cast<int>(in) - fseg * u;
+        } else {
+          fseg = static_cast<int>(in / u);
+          fu = static_cast<int>(in % u);
+        }
+        fb = b;
         fkeys = u - p.finish, frq = r;
         break;
       }
@@ -166,17 +182,39 @@ __device__ __forceinline__ void next_piece(const CacheFwdParams& p, Piece& w) {
   }
   enter_segment(p, w, run);
 }
+// The first piece of block x's run.  The block's thread 0 also writes down the
+// segment that this block answers for at the join: one that is cut and begins
+// with the block's run, or began in the block before and goes on in this one.
 __device__ __forceinline__ Piece first_piece(const CacheFwdParams& p, int x, bool* bad) {
   const Census c = take_census(p, bad);
   Piece w;
   w.b = -1;
   w.first = 1;
-  if (x >= c.blocks) return w;
-  const long long lo = cache_run(x, c.total, c.blocks), hi = cache_run(x + 1, c.total, c.blocks);
-  if (lo >= hi) return w;
-  find_unit(p, c, lo, bad, &w);
-  enter_segment(p, w, hi - lo);
-  if (w.u0 > w.keys) next_piece(p, w);  // the segment's end is another block's
+  Cut cut = {};
+  if (x < c.blocks) {
+    const long long lo = cache_run(x, c.total, c.blocks), hi = cache_run(x + 1, c.total, c.blocks);
+    find_unit(p, c, lo, bad, &w);
+    enter_segment(p, w, hi - lo);
+    if (threadIdx.x == 0 && p.unit > 0 && w.u0 <= w.keys) {
+      const long long start = lo - w.u0;
+      const int x0 = cache_owner(start, c.total, c.blocks);
+      const int x1 = cache_owner(start + w.keys, c.total, c.blocks);
+      const bool at_start = cache_run(x0, c.total, c.blocks) == start;
+      if (x1 > x0 && x == (at_start ? x0 : x0 + 1)) {
+        const int rtiles = row_tiles(p, w.rq);
+        cut.pieces = x1 - x0 + 1;
+        // the first piece is its block's last unless the block begins with it
+        cut.slot0 = 2 * x0 + (at_start ? 0 : 1);
+        cut.x0 = x0;
+        cut.h = w.seg / rtiles;
+        cut.row_base = (w.seg - cut.h * rtiles) * p.tile_rows;
+        cut.rows = min(p.tile_rows, w.rq.n * p.G - cut.row_base);
+        cut.row0 = w.rq.row0;
+      }
+    }
+    if (w.u0 > w.keys) next_piece(p, w);  // the segment's end is another block's
+  }
+  if (threadIdx.x == 0 && p.unit > 0) p.cuts[x] = cut;
   return w;
 }
 

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(256) dfa_rotary_kernel(const RotaryParams p) {
   const long long thread = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long item = thread / kUnits;
   const int unit = static_cast<int>(thread % kUnits);
+  grid_launch_dependents();
   grid_dependency_wait();  // q and k come from the kernels before this one
   if (item >= p.items) return;
   const long long row = item / p.groups;  // over batch and rows
