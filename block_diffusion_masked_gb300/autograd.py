@@ -42,8 +42,14 @@ class RotaryFunc(torch.autograd.Function):
         # Gradients have the outputs' shapes and types, checked in the forward.
         table, positions = ctx.saved_tensors
         sizes, flags = ctx.how
-        flags |= binding.DFA_ROTARY_INVERSE
-        if dq is not None:
+        flags ^= binding.DFA_ROTARY_INVERSE
+        if torch.is_grad_enabled():  # the gradients are to have gradients: linear again
+            if dq is not None:
+                dq, dk = RotaryFunc.apply(_strided(dq), None if dk is None else _strided(dk),
+                                          table, positions, sizes[2], flags)
+            elif dk is not None:
+                dk = RotaryFunc.apply(_strided(dk), None, table, positions, sizes[2], flags)[0]
+        elif dq is not None:
             dq, dk = binding._rotary_launch(_strided(dq), None if dk is None else _strided(dk),
                                             table, positions,
                                             sizes if dk is not None else (*sizes[:4], 0, *sizes[5:]),
@@ -141,6 +147,8 @@ def diffusion_attn_varlen_func(q, k, v, cu_seqlens, block_size, rotary_table=Non
     """
     if rotary_table is not None:
         q, k = rotary_func(q, k, rotary_table, positions, interleaved)
+    elif positions is not None:
+        raise ValueError("positions need a rotary_table")
     return DiffusionAttnVarlenFunc.apply(q, k, v, cu_seqlens, block_size)
 
 

@@ -593,6 +593,8 @@ def dfa_bwd_dq_convert(dq_acc, dq, mode=MODE_DIFFUSION):
 # the checks read attributes only, and the device is made current only where
 # it is not.
 
+_INT_MAX = (1 << 31) - 1  # larger arguments stand for it: ctypes would wrap them
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -799,8 +801,8 @@ def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_
         raise ValueError("k and v must be (rows, kv_heads, headdim) with the cache's heads")
     _call("dfa_cache_append", dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
           cache_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          k_scale.data_ptr(), v_scale.data_ptr(), B, rows, int(max_new), Hk, d, ps, P, maxp,
-          _strides(k, "k"), _strides(v, "v"))
+          k_scale.data_ptr(), v_scale.data_ptr(), B, rows, min(int(max_new), _INT_MAX),
+          Hk, d, ps, P, maxp, _strides(k, "k"), _strides(v, "v"))
 
 
 def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim):
@@ -851,7 +853,7 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
         lse = torch.empty((H, rows), dtype=torch.float32, device=dev)
     else:
         _check_dense(lse, (H, rows), torch.float32, dev, "lse")
-    max_new = int(max_new)
+    max_new = min(int(max_new), _INT_MAX)
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(dev.index, B, rows, max_new, H, Hk, d),
                                 dtype=torch.uint8, device=dev)
@@ -860,7 +862,7 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
     _call("dfa_cache_forward", dev, q.data_ptr(), kp, vp, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
           cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel(), B, rows, max_new, H, Hk, d, int(block_size), ps, P, maxp,
+          workspace.numel(), B, rows, max_new, H, Hk, d, min(int(block_size), _INT_MAX), ps, P, maxp,
           _strides(q, "q"), ks, vs)
     return out, lse
 

@@ -98,6 +98,13 @@ __global__ void __launch_bounds__(kPlanThreads) dfa_cache_plan_kernel(const Plan
     int len = 0, n = 0, has = 0;
     Sums mine = {0, 0};
     long long past = 0;
+    auto wants = [&](int rows) {  // pages and rows of a request that adds `rows`
+      const long long want =
+          (static_cast<long long>(len) + rows + p.page_size - 1) / p.page_size - has;
+      const long long room = p.max_pages - has;
+      past = want > room ? want - room : 0;
+      mine = {want - past, rows};
+    };
     if (b < p.batch) {
       len = p.cache_lens[b];
       n = p.new_lens[b];
@@ -107,14 +114,16 @@ __global__ void __launch_bounds__(kPlanThreads) dfa_cache_plan_kernel(const Plan
         n = n < 0 ? 0 : n;
       }
       has = (len + p.page_size - 1) / p.page_size;
-      const long long want =
-          (static_cast<long long>(len) + n + p.page_size - 1) / p.page_size - has;
-      const long long room = p.max_pages - has;
-      past = want > room ? want - room : 0;
-      mine = {want - past, n};
+      wants(n);
     }
     Sums all;
-    const Sums upto = block_scan(mine, warp_sums, &all);
+    Sums upto = block_scan(mine, warp_sums, &all);
+    if (carry.rows + all.rows > p.rows) {  // rows are cut, and with them their pages
+      bad = true;
+      const long long room = p.rows - (carry.rows + upto.rows - mine.rows);
+      if (b < p.batch) wants(room < 0 ? 0 : room < n ? static_cast<int>(room) : n);
+      upto = block_scan(mine, warp_sums, &all);
+    }
     // the requests' own exclusive sums, and the end of the last
     s_pages[tid + 1] = upto.pages;
     s_rows[tid + 1] = upto.rows;
@@ -129,16 +138,13 @@ __global__ void __launch_bounds__(kPlanThreads) dfa_cache_plan_kernel(const Plan
     if (part == 0 && b < p.batch) {
       const long long r0 = carry.rows + upto.rows - mine.rows;
       const long long r1 = carry.rows + upto.rows;
-      p.cu_new[b] = static_cast<int>(r0 < p.rows ? r0 : p.rows);
-      if (b == p.batch - 1) p.cu_new[p.batch] = static_cast<int>(r1 < p.rows ? r1 : p.rows);
-      const long long fit_rows =
-          (r1 < p.rows ? r1 : p.rows) - (r0 < p.rows ? r0 : p.rows);  // rows there is room for
+      p.cu_new[b] = static_cast<int>(r0);
+      if (b == p.batch - 1) p.cu_new[p.batch] = static_cast<int>(r1);
       const long long before = carry.pages + upto.pages - mine.pages;
       const long long got = before >= top ? 0 : before + mine.pages > top ? top - before : mine.pages;
       const long long cap = (has + got) * p.page_size;
-      const long long next = len + fit_rows;
+      const long long next = len + mine.rows;
       p.next_lens[b] = static_cast<int>(next < cap ? next : cap);
-      if (r1 > p.rows) bad = true;
     }
     const int step = parts * kPlanThreads, me = part * kPlanThreads + tid;
     for (long long i = me; i < all.pages; i += step) {
@@ -152,8 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) dfa_cache_plan_kernel(const Plan
       p.block_table[static_cast<long long>(base + lo) * p.max_pages + s_has[lo] +
                     (i - s_pages[lo])] = at >= 0 ? p.free_pages[at] : -1;
     }
-    const long long room = p.rows - carry.rows;
-    for (long long i = me; i < all.rows && i < room; i += step) {
+    for (long long i = me; i < all.rows; i += step) {
       int lo = 0, hi = count - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -394,15 +399,17 @@ cudaError_t launch_append_block(const AppendParams& p, unsigned blocks, cudaStre
 
 template <int D>
 cudaError_t launch_append(const AppendParams& p, int batch, cudaStream_t stream) {
-  const long long blocks = 2LL * p.Hk * batch * p.touch;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned n = static_cast<unsigned>(blocks);
+  const unsigned n = 2u * p.Hk * batch * p.touch;
   const int vectors = (p.max_new < p.page_size ? p.max_new : p.page_size) * (D / 8);
   if (vectors <= 128) return launch_append_block<D, 32, 4>(p, n, stream);
   if (vectors <= 512) return launch_append_block<D, 128, 4>(p, n, stream);
-  if (vectors <= 1024) return launch_append_block<D, 128, 8>(p, n, stream);
-  if constexpr (D == 128) return launch_append_block<D, 256, 8>(p, n, stream);
-  return launch_append_block<D, 256, 16>(p, n, stream);  // headdim 256: up to 4096
+  // a page of 128 tokens is 1024, 2048 or 4096 vectors
+  if constexpr (D == 128) {
+    if (vectors > 1024) return launch_append_block<D, 256, 8>(p, n, stream);
+  } else if constexpr (D == 256) {
+    if (vectors > 1024) return launch_append_block<D, 256, 16>(p, n, stream);
+  }
+  return launch_append_block<D, 128, 8>(p, n, stream);
 }
 
 }  // namespace
@@ -523,6 +530,8 @@ int dfa_cache_append(const void* k, const void* v, const int* cu_new, const int*
     return DFA_EINVAL;
   if (headdim != 64 && headdim != 128 && headdim != 256) return DFA_EUNSUPPORTED;
   if (batch == 0 || rows == 0 || max_new == 0) return DFA_OK;
+  const int touch = cache_append_pages(max_new < rows ? max_new : rows, page_size);
+  if (static_cast<long long>(batch) * touch > 0x7fffffffLL / (2 * kv_heads)) return DFA_EINVAL;
   for (const void* q : {k, v, static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
     if (!q || !aligned_to(q, 16)) return DFA_EINVAL;
   for (const void* q : {static_cast<const void*>(cu_new), static_cast<const void*>(cache_lens),
@@ -551,7 +560,7 @@ int dfa_cache_append(const void* k, const void* v, const int* cu_new, const int*
   p.page_size = page_size;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
-  p.touch = cache_append_pages(p.max_new, page_size);
+  p.touch = touch;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = headdim == 64    ? launch_append<64>(p, batch, s)
                         : headdim == 128 ? launch_append<128>(p, batch, s)

@@ -930,7 +930,8 @@ constexpr int kWholeKeys = 512, kFinish = 6, kLeast = 8;
 int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim) {
   if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
       max_new > (1 << 24) || heads < 1 || heads > (1 << 16) || kv_heads < 1 || kv_heads > heads ||
-      heads % kv_heads)
+      heads % kv_heads ||
+      static_cast<long long>(max_new < rows ? max_new : rows) * (heads / kv_heads) > (1 << 30))
     return DFA_EINVAL;
   if (headdim != 64 && headdim != 128 && headdim != 256) return DFA_EUNSUPPORTED;
   return DFA_OK;

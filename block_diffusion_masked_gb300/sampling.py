@@ -67,7 +67,11 @@ def rotary_table(max_pos, rot_dim, base=10000.0, scaling=None, factor=1.0, origi
 
 @dataclasses.dataclass
 class Step:
-    """One sampling step's rows (see ``dfa_cache_plan``)."""
+    """One sampling step's rows (see ``dfa_cache_plan``).
+
+    ``cache_lens`` and ``block_table`` are the page table's own tensors: a step
+    is over once :meth:`PageTable.advance` has run.
+    """
 
     cu_new: torch.Tensor      # (batch + 1,) first row of each request
     positions: torch.Tensor   # (rows,), -1 behind the last request

@@ -381,8 +381,8 @@ int dfa_rotary(const void *q, const void *k, void *q_out, void *k_out, const flo
  * in order; next_free[0] = pages left on the stack, missing[0] = pages that
  * were not to be had (the stack ran out, or a table is full): their entries
  * are -1 and next_lens stops at the pages there are.  next_lens and next_free
- * may be cache_lens and free_count themselves.  Rows beyond `rows` are cut and
- * set DFA_EDEVICE.  Running it again on the same cache_lens and free_count
+ * may be cache_lens and free_count themselves.  Rows beyond `rows` are cut, take
+ * no pages, and set DFA_EDEVICE.  Running it again on the same cache_lens and free_count
  * writes the same.
  */
 int dfa_cache_plan(const int *cache_lens, const int *new_lens, int *block_table,
@@ -408,6 +408,7 @@ int dfa_cache_release(const int *finished, int *cache_lens, int *block_table, in
  * scale grows.  Values that are not finite are kept as NaN and do not count
  * for the scale.  cache_lens are the lengths BEFORE the append.  A page
  * belongs to one request of a call: two requests that append to one page race.
+ * 2 kv_heads * batch * (pages that max_new tokens can touch) is below 2^31.
  */
 int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int *cache_lens,
                      const int *block_table, void *k_cache, void *v_cache, float *k_scale,
@@ -425,7 +426,7 @@ int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int 
  * bf16, strides as for the append; out (rows, heads, headdim) bf16 contiguous,
  * lse (heads, rows) float32.  A row that sees no key gets out 0 and lse -inf.
  * kv_heads divides heads, head h reads key/value head h / (heads / kv_heads).
- * batch <= 32768.  workspace: dfa_cache_workspace_bytes(...) bytes of device
+ * batch <= 32768, and max_new times heads / kv_heads at most 2^30.  workspace: dfa_cache_workspace_bytes(...) bytes of device
  * memory (16-byte aligned) for the partial results of long requests; calls
  * that may run at the same time need workspaces of their own.
  */

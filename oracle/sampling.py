@@ -41,6 +41,7 @@ def plan(cache_lens, new_lens, table, free_pages, free_count, page_size, rows):
     top, missing = int(free_count), 0
     cu, positions, next_lens = [0], [], []
     for b, (n0, n) in enumerate(zip(cache_lens, new_lens)):
+        n = min(n, rows - cu[-1])
         have = -(-n0 // page_size)
         for j in range(have, -(-(n0 + n) // page_size)):
             if j >= table.shape[1]:
@@ -53,7 +54,6 @@ def plan(cache_lens, new_lens, table, free_pages, free_count, page_size, rows):
             else:
                 table[b, j] = -1
                 missing += 1
-        n = min(n, rows - cu[-1])
         positions += range(n0, n0 + n)
         cu.append(cu[-1] + n)
         next_lens.append(min(n0 + n, have * page_size))

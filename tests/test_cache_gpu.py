@@ -85,6 +85,30 @@ def test_plan_full_tables_and_cut_rows(b):
     assert got[2].tolist() == list(range(12)) * 2
 
 
+def test_plan_cut_rows_take_no_pages(b):
+    """Rows that are cut take no pages: after every step the pages held and the
+    pages free are all the pages there are."""
+    lens, new = [3, 16, 0] * 300, [20, 17, 40] * 300
+    lens, new = lens[:700], new[:700]
+    n = sum(-(-x // 16) for x in lens)
+    table = np.full((700, 4), -1)
+    at = 0
+    for i, x in enumerate(lens):
+        for j in range(-(-x // 16)):
+            table[i, j] = at
+            at += 1
+    free = list(range(n, n + 3000))
+    for rows in (0, 30, 5000, 14000, sum(new)):
+        t = _i32(table)
+        got = b.dfa_cache_plan(_i32(lens), _i32(new), t, _i32(free), _i32([3000]), 16, rows)
+        assert b.dfa_status() == (0 if rows == sum(new) else b.DFA_EDEVICE)
+        ref = osam.plan(lens, new, table, free, 3000, 16, rows)
+        for x, y in zip(got, ref):
+            assert np.array_equal(x.cpu().numpy().ravel(), np.ravel(y))
+        held = sum(-(-x // 16) for x in got[3].tolist())
+        assert held + got[4].item() == n + 3000
+
+
 def test_plan_bad_state(b):
     """Lengths and counts outside their ranges are errors; nothing is read
     through them."""
@@ -436,6 +460,17 @@ def test_refusals(b):
         b.dfa_cache_append(p["k"], p["v"], args[7], args[6], args[5], c, c, s, s, 2)
     torch.cuda.synchronize()
     assert b.dfa_status() == 0
+
+
+@pytest.mark.parametrize("block", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 1, 2 ** 40])
+def test_block_sizes_past_32_bits(b, block):
+    """A block of any size that covers the rows makes them one block."""
+    p = _problem([70, 3], [5, 9], 4, 2, 64, 32)
+    want = _run(b, p, 2 ** 30)
+    got = _run(b, p, block)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    causal = _run(b, p, 1)
+    assert not torch.equal(causal[0], want[0])
 
 
 # ------------------------------------------------------------------ together

@@ -92,6 +92,54 @@ def test_gradient_against_differences(b, inter):
         assert abs(lhs - rhs) <= tol
 
 
+def test_gradients_of_gradients(b):
+    """The map is linear in the gradients too: differentiating the backward
+    pass turns forward again; q and k, either alone."""
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(3, 64)
+    q, k = _randn((1, 6, 2, 64), 1).requires_grad_(), _randn((1, 6, 1, 64), 2).requires_grad_()
+    gq, gk = _randn(q.shape, 3).requires_grad_(), _randn(k.shape, 4).requires_grad_()
+    zq, zk = _randn(q.shape, 5), _randn(k.shape, 6)
+    yq, yk = rotary_func(q, k, table)
+    dq, dk = torch.autograd.grad((yq, yk), (q, k), (gq, gk), create_graph=True)
+    aq, ak = torch.autograd.grad((dq, dk), (gq, gk), (zq, zk))
+    pos = [0, 1, 2] * 2
+    for got, x in ((aq, zq), (ak, zk)):
+        _check(got[0], x[0], table, pos, False, False)
+    yq, yk = rotary_func(q, k, table)
+    (dk,) = torch.autograd.grad(yk, k, gk, create_graph=True)
+    (ak,) = torch.autograd.grad(dk, gk, zk)
+    _check(ak[0], zk[0], table, pos, False, False)
+    assert b.dfa_status() == 0
+
+
+def test_captured_forward_and_backward(b):
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(9, 64)
+    q, k = (_randn((2, 18, h, 64), h).requires_grad_() for h in (3, 1))
+    g = [_randn(x.shape, 7) for x in (q, k)]
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):  # warm-up, its graph gone before the capture
+        torch.autograd.grad(rotary_func(q, k, table), (q, k), g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        y = rotary_func(q, k, table)
+        d = torch.autograd.grad(y, (q, k), g)
+    for seed in (20, 30):
+        with torch.no_grad():
+            for x in (q, k, *g):
+                x.copy_(_randn(x.shape, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for got, x, inverse in zip((*y, *d), (q, k, *g), (False, False, True, True)):
+                _check(got[i].detach(), x[i].detach(), table, list(range(9)) * 2, False, inverse)
+    assert b.dfa_status() == 0
+
+
 @pytest.mark.parametrize("d,inter", [(64, False), (128, True), (256, False)])
 def test_strided_views_and_packed_rows(b, d, inter):
     """Slices of a fused projection, far positions, rows that are not in use."""

@@ -78,7 +78,8 @@ def test_append_refusals(lib):
                dict(kc=NULL), dict(vc=ODD), dict(ks=NULL), dict(vs=NULL), dict(batch=-1),
                dict(rows=-1), dict(max_new=-1), dict(heads=0), dict(heads=65536), dict(ps=24),
                dict(pages=0), dict(maxp=0), dict(kst=(ctypes.c_longlong * 2)(128, 65)),
-               dict(vst=(ctypes.c_longlong * 2)(100, 64))):
+               dict(vst=(ctypes.c_longlong * 2)(100, 64)),
+               dict(batch=20000, rows=1 << 21, max_new=1 << 21, heads=8)):  # too many blocks
         assert _append(lib, **kw) == EINVAL, kw
     assert _append(lib, d=96) == EUNSUPPORTED
     for kw in (dict(batch=0), dict(rows=0), dict(max_new=0)):
@@ -99,7 +100,8 @@ def test_forward_refusals(lib):
                dict(out=ODD), dict(lse=NULL), dict(work=NULL), dict(work=ODD), dict(batch=-1),
                dict(batch=40000), dict(rows=-1), dict(max_new=-1), dict(heads=0),
                dict(kv_heads=3), dict(kv_heads=0), dict(kv_heads=8), dict(bs=0), dict(ps=8),
-               dict(pages=0), dict(maxp=0), dict(maxp=1 << 27)):
+               dict(pages=0), dict(maxp=0), dict(maxp=1 << 27),
+               dict(heads=1 << 16, kv_heads=1, rows=1 << 15, max_new=1 << 15)):
         assert _forward(lib, **kw) == EINVAL, kw
     assert _forward(lib, d=80) == EUNSUPPORTED
     for kw in (dict(batch=0), dict(rows=0), dict(max_new=0)):
@@ -112,7 +114,7 @@ def test_forward_refusals(lib):
 def test_binding_refusals():
     """Wrong types, shapes and devices are refused before the library is asked."""
     from block_diffusion_masked_gb300 import binding as b
-    from block_diffusion_masked_gb300 import rotary_func
+    from block_diffusion_masked_gb300 import diffusion_attn_varlen_func, rotary_func
 
     x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
     t = torch.zeros(4, 64)
@@ -121,6 +123,8 @@ def test_binding_refusals():
         b.dfa_rotary(x, x, t)  # not on a GPU
     with pytest.raises(ValueError):
         rotary_func(x[0], x[0], t)  # packed rows need positions
+    with pytest.raises(ValueError):
+        diffusion_attn_varlen_func(x[0], x[0], x[0], i, 1, positions=i)  # without a table
     with pytest.raises(ValueError):
         b.dfa_cache_plan(i, i, torch.zeros(2, 2, dtype=torch.int32), i, i[:1], 64, 4)
     with pytest.raises(ValueError):
