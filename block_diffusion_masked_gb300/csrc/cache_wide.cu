@@ -37,6 +37,25 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// 16 bytes of global memory into shared memory, zeros instead where !there.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy16_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// What the softmax needs to know of a cached tile: scales and keys of its
+// eight 16-key groups, the largest value scale, whether every key is there.
+struct TileInfo {
+  float ks[8], vs[8];
+  unsigned char keys[8];
+  float vmax;
+  int whole;
+};
+
 template <int D, int RS>
 struct WideCfg {
   static constexpr int BM = 128, BN = 128;
@@ -52,7 +71,18 @@ struct WideCfg {
   static constexpr int kOffK = kOffQ + BM * D * 2;
   static constexpr int kOffV = kOffK + 2 * kTile;
   static constexpr int kOffRaw = kOffV + 2 * kTile;  // k, then v
-  static constexpr int kOffBar = kOffRaw + RS * 2 * kRaw;
+  // Infos of the last kInfo cached tiles.  The load of tile i has seen tile
+  // i - RS converted, so the product before the last before that one complete
+  // and the scores two further back read: those up to i - RS - 4 are done with.
+  static constexpr int kInfo = RS + 4 <= 8 ? 8 : 16;
+  static_assert(RS + 4 <= kInfo, "infos still in use");
+  // Row exponents of the last four versions of Q in f16.  A version is put
+  // when the products with the one before are complete: three versions on, the
+  // softmax is past the first tile of this one, where it reads them.
+  static constexpr int kExps = 4;
+  static constexpr int kOffInfo = kOffRaw + RS * 2 * kRaw;
+  static constexpr int kOffExp = kOffInfo + kInfo * static_cast<int>(sizeof(TileInfo));
+  static constexpr int kOffBar = kOffExp + kExps * BM;
   enum {
     BAR_Q = 0,
     BAR_RAWFULL = 1,                    // [RS] of k, [RS] of v
@@ -97,14 +127,16 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
   uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
   volatile int* s_odd = reinterpret_cast<volatile int*>(smem + C::kOffOdd);
+  TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + C::kOffInfo);
+  signed char* s_exp = reinterpret_cast<signed char*>(smem + C::kOffExp);
   const AbortFlag ab{const_cast<int*>(abort_flag), p.status};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 #define BAR(i) (sbase + C::kOffBar + 8 * (i))
 
   if (tid == 0) {
-    mbar_init(BAR(C::BAR_Q), C::kSoftWarps);
+    mbar_init(BAR(C::BAR_Q), 4);
     for (int s = 0; s < 2 * RS; ++s) {
-      mbar_init(BAR(C::BAR_RAWFULL + s), 1);
+      mbar_init(BAR(C::BAR_RAWFULL + s), s < RS ? 2 : 1);  // k: the tile, its info
       mbar_init(BAR(C::BAR_RAWEMPTY + s), 4);
     }
     for (int s = 0; s < 2; ++s) {
@@ -186,23 +218,38 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     const CUtensorMap* map = isv ? &p.tm_v : &p.tm_k;
     const int full = C::BAR_RAWFULL + (isv ? RS : 0), empty = C::BAR_RAWEMPTY + (isv ? RS : 0);
     const uint32_t raw0 = sbase + C::kOffRaw + (isv ? RS * C::kRaw : 0);
+    // The loads of k also write the tiles' infos; pages are asked for four tiles
+    // ahead, scales three: they may come from memory under full load.
+    auto load_scales = [&](int h, int page, float* ks, float* vs) {
+      const bool has = !isv && cache_page_ok(page, p.num_pages);
+      const long long at = static_cast<long long>(page) * p.Hk + h;
+      *ks = has ? p.k_scale[at] : 0.f;
+      *vs = has ? p.v_scale[at] : 0.f;
+    };
     bool ok = true;
+    int n = 0;  // cached tiles
     Ring<RS> at;
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
-      int page = load_page(w, k, 0), next_page = -1;
+      int page = load_page(w, k, 0), next_page = load_page(w, k, 4);
       int keys = keys_of(k, 0, page);
-      for (int j = 0; j < k.nc; ++j) {
+      float ks, vs, next_ks = 0.f, next_vs = 0.f;
+      load_scales(k.h, page, &ks, &vs);
+      for (int j = 0; j < k.nc; ++j, ++n) {
         if ((j & 3) == 0) {
-          if (j > 0) page = next_page, keys = keys_of(k, j, page);
-          next_page = load_page(w, k, j + 4);
+          if (j > 0) {
+            page = next_page, keys = keys_of(k, j, page);
+            ks = next_ks, vs = next_vs;
+            next_page = load_page(w, k, j + 4);
+          }
         }
         // the first group of each page of this tile issues the page's box
         const int per = p.page_size >> 4;
-        const bool mine = (lane >> 3) == (j & 3) && (lane & 7) % per == 0;
-        if (mine && keys == 0 && k.key_lo + BN * j + 16 * (lane & 7) < k.key_hi)
+        const bool mine = (lane >> 3) == (j & 3);
+        const bool first = mine && (lane & 7) % per == 0;
+        if (first && keys == 0 && k.key_lo + BN * j + 16 * (lane & 7) < k.key_hi)
           atomicOr(p.status, kStatusIndex);
-        const bool load = mine && keys > 0;
+        const bool load = first && keys > 0;
         const unsigned count = __popc(__ballot_sync(0xffffffffu, load));
         if (at.round > 0 &&
             !(ok = mbar_wait_warp(BAR(empty + at.slot), (at.round - 1) & 1, ab)))
@@ -212,6 +259,25 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         if (load)
           tma_load_3d(raw0 + at.slot * C::kRaw + (lane & 7) * 16 * D, map, BAR(full + at.slot), 0,
                       k.h * p.page_size, page);
+        if (!isv) {
+          if ((j & 3) == 1) load_scales(k.h, next_page, &next_ks, &next_vs);
+          float vmax = vs;
+#pragma unroll
+          for (int off = 1; off < 8; off <<= 1)
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+          const unsigned there = __ballot_sync(0xffffffffu, keys == 16) >> (8 * (j & 3));
+          if (mine) {
+            TileInfo& info = s_info[n & (C::kInfo - 1)];
+            info.ks[lane & 7] = ks;
+            info.vs[lane & 7] = vs;
+            info.keys[lane & 7] = static_cast<unsigned char>(keys);
+            if ((lane & 7) == 0) {
+              info.vmax = vmax;
+              info.whole = (there & 0xffu) == 0xffu;
+            }
+          }
+          mbar_arrive_warp(BAR(full + at.slot));
+        }
         __syncwarp();
         at.next();
       }
@@ -324,35 +390,86 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         }
       }
     };
-    // Own rows as they are; what is not finite in v is kept out of the product
-    // (its weight is 0 in rows that do not see it) and noted.
+    // Own rows as they are, and Q: all copies of a tile are in flight at once,
+    // straight into place; a thread looks again only at what it copied itself.
     auto copy_own = [&](const Piece& x, const Tiles& k, int first, uint32_t dst) {
       const __nv_bfloat16* src = isv ? p.v + x.rq.row0 * p.v_sr + k.h * p.v_sh
                                      : p.k + x.rq.row0 * p.k_sr + k.h * p.k_sh;
       const long long sr = isv ? p.v_sr : p.k_sr;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const int at = i * 128 + c, r = at / (D / 8), u = at % (D / 8);
+        const bool there = first + r < x.rq.n;
+        copy16_async(dst + (u >> 3) * (BN * 128) + r * 128 + (((u ^ r) & 7) << 4),
+                     src + (there ? first + r : 0) * sr + 8 * u, there);
+      }
+    };
+    auto copy_q = [&](const Piece& x, const Tiles& k) {
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const int at = i * 128 + c, row = at / (D / 8), u = at % (D / 8);
+        const int r = min(k.row_base + row, k.R - 1);
+        const int tok = r / p.G, hq = k.h * p.G + (r - tok * p.G);
+        copy16_async(sbase + C::kOffQ + (u >> 3) * (C::BM * 128) + row * 128 + (((u ^ row) & 7) << 4),
+                     p.q + (x.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 8 * u,
+                     k.row_base + row < k.R);
+      }
+    };
+    // Values that are not finite are kept out of the product (their weight is 0
+    // in rows that do not see them) and noted.
+    auto drop_odd = [&](uint32_t dst) {
       bool odd = false;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
         const int at = i * 128 + c, r = at / (D / 8), u = at % (D / 8);
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        if (first + r < x.rq.n) {
-          const uint4 y = *reinterpret_cast<const uint4*>(src + (first + r) * sr + 8 * u);
-          v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-        }
-        if (isv) {
+        const uint32_t to = dst + (u >> 3) * (BN * 128) + r * 128 + (((u ^ r) & 7) << 4);
+        const uint4 y = lds128(to);
+        uint32_t v[4] = {y.x, y.y, y.z, y.w};
+        bool drop = false;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if ((v[y] & 0x7f80u) == 0x7f80u) v[y] &= 0xffff0000u, odd = true;
-            if ((v[y] & 0x7f800000u) == 0x7f800000u) v[y] &= 0xffffu, odd = true;
-          }
+        for (int e = 0; e < 4; ++e) {
+          if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u, drop = true;
+          if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu, drop = true;
         }
-        st_shared_v4(dst + (u >> 3) * (BN * 128) + r * 128 + (((u ^ r) & 7) << 4), v[0], v[1], v[2],
-                     v[3]);
+        if (drop) st_shared_v4(to, v[0], v[1], v[2], v[3]);
+        odd = odd || drop;
       }
       return odd;
     };
+    // Q from bf16 to f16 after a power of two of each row's, whose exponents go
+    // to `exps`.
+    auto scale_q = [&](signed char* exps) {
+#pragma unroll 2
+      for (int i = 0; i < D / 8; ++i) {
+        const int at = i * 128 + c, row = at / (D / 8), u = at % (D / 8);
+        // 16-byte unit u of a row: 64-dim chunk u / 8, swizzled by the row
+        const uint32_t to =
+            sbase + C::kOffQ + (u >> 3) * (C::BM * 128) + row * 128 + (((u ^ row) & 7) << 4);
+        const uint4 y = lds128(to);
+        uint32_t v[4] = {y.x, y.y, y.z, y.w};
+        unsigned top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const unsigned lo = v[e] & 0x7fffu, hi = (v[e] >> 16) & 0x7fffu;
+          top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+#pragma unroll
+        for (int off = 1; off < D / 8; off <<= 1)
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+        int e = static_cast<int>(top >> 7) - 127 - 14;
+        if (e < -100) e = -100;
+        const float inv = pow2_bits(-e);
+        if (u == 0) exps[row] = static_cast<signed char>(e);
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          v[z] = pack_f16x2(__uint_as_float(v[z] << 16) * inv,
+                            __uint_as_float(v[z] & 0xffff0000u) * inv);
+        st_shared_v4(to, v[0], v[1], v[2], v[3]);
+      }
+    };
     bool ok = true;
     int n = 0, owns = 0;  // operand tiles, pieces with own keys
+    int q = 0;            // versions of Q in f16
     Ring<RS> at;
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
@@ -364,6 +481,11 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
           if (j > 0) keys = keys_of(k, j, next_page);
           next_page = load_page(w, k, j + 4);
         }
+        // A tile of k that comes with a new Q: the first cached one, the first
+        // own one.  Q may be replaced when the products with it are complete,
+        // which is when this tile is ready already.
+        const bool with_q = !isv && (j == 0 || j == k.nc);
+        if (with_q && n == 0) copy_q(w, k);
         if (n >= 2 && !(ok = mbar_wait_warp(BAR(empty + b), ((n >> 1) - 1) & 1, ab))) break;
         const uint32_t dst = tiles0 + b * C::kTile;
         if (j < k.nc) {
@@ -381,12 +503,27 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
             ++owns;
             if (c == 0) s_odd[(owns + 1) & 3] = 0;
           }
-          if (copy_own(w, k, BN * (j - k.nc), dst)) s_odd[owns & 3] = 1;
+          copy_own(w, k, BN * (j - k.nc), dst);
+        }
+        if (with_q) {
+          if (n > 0) {
+            if (!(ok = mbar_wait_warp(BAR(empty + (b ^ 1)), ((n - 1) >> 1) & 1, ab))) break;
+            copy_q(w, k);
+          }
+          copy16_wait();
+          if (j < k.nc) scale_q(s_exp + (q++ & (C::kExps - 1)) * C::BM);
+          fence_proxy_async_smem();
+          mbar_arrive_warp(BAR(C::BAR_Q));
+        }
+        if (j >= k.nc) {
+          copy16_wait();
+          if (isv && drop_odd(dst)) s_odd[owns & 3] = 1;
         }
         fence_proxy_async_smem();
         mbar_arrive_warp(BAR(full + b));
       }
     }
+    copy16_wait();  // giving up: nothing lands after the block is gone
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ------------------------------------------------------------ softmax
@@ -394,81 +531,20 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     const int lb = (warp & 3) * 32 + (warp >> 2) * 16;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(lb) << 16);
     bool ok = true;
-    int n = 0, owns = 0;  // tiles and pieces with own keys so far
+    int n = 0, cached = 0, owns = 0, q = 0;  // tiles, cached ones, pieces with own keys, versions of Q
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
       const int r = k.row_base + lb + (lane & 15);  // row of the request and head
       const int tok = min(r, k.R - 1) / p.G;
       const int hq = k.h * p.G + (min(r, k.R - 1) - tok * p.G);
       const int end = r < k.R ? cache_own_end(w.rq.len, tok, w.rq.n, p.bs) : 0;
-      const __nv_bfloat16* qsrc = p.q + (w.rq.row0 + tok) * p.q_sr + hq * p.q_sh + half * DH;
-      // Pages two batches of four tiles ahead, scales one: they may come from
-      // memory under full load, microseconds away.
-      int next_page = load_page(w, k, 4), last_page = load_page(w, k, 0);
-      float next_ks = 0.f, next_vs = 0.f;
-      auto load_scales = [&](int page, float* a, float* b) {
-        const bool has = cache_page_ok(page, p.num_pages);
-        const long long at = static_cast<long long>(page) * p.Hk + k.h;
-        *a = has ? p.k_scale[at] : 0.f;
-        *b = has ? p.v_scale[at] : 0.f;
-      };
-      auto group_max = [&](float v) {  // over the eight groups of a tile
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-      };
-      // The row's half of Q as the products' A operand, f16 after a power of two
-      // or bf16.  The scores of the tiles before are complete, so Q may be
-      // replaced.
       float factor = 0.f;  // undoes the row's power of two, with the softmax scale
-      auto put_q = [&](bool f16) {
-        uint32_t v[D / 4];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          uint4 y = make_uint4(0u, 0u, 0u, 0u);
-          if (r < k.R) y = *reinterpret_cast<const uint4*>(qsrc + 8 * i);
-          v[4 * i] = y.x, v[4 * i + 1] = y.y, v[4 * i + 2] = y.z, v[4 * i + 3] = y.w;
-        }
-        if (f16) {
-          unsigned top = 0;
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i) {
-            const unsigned lo = v[i] & 0x7fffu, hi = (v[i] >> 16) & 0x7fffu;
-            top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-          }
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          int e = static_cast<int>(top >> 7) - 127 - 14;
-          if (e < -100) e = -100;
-          const float inv = pow2_bits(-e);
-          factor = pow2_bits(e) * p.scale_log2;
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i)
-            v[i] = pack_f16x2(__uint_as_float(v[i] << 16) * inv,
-                              __uint_as_float(v[i] & 0xffff0000u) * inv);
-        }
-        // 16-byte unit u of row x: 64-dim chunk u / 8, swizzled by the row
-        const int x = lb + (lane & 15);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int u = half * (D / 16) + i;
-          st_shared_v4(sbase + C::kOffQ + (u >> 3) * (C::BM * 128) + x * 128 + (((u ^ x) & 7) << 4),
-                       v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive_warp(BAR(C::BAR_Q));
-      };
-      if (k.nc > 0) put_q(true);
-      float ks, vs;
-      load_scales(last_page, &ks, &vs);
-      int keys = keys_of(k, 0, last_page);
-      float vmax = group_max(vs);
       float m = -INFINITY, l = 0.f;
       float c = pow2_bits(kCacheMinExp), inv_c = pow2_bits(-kCacheMinExp);  // unit of O
-      unsigned full = __ballot_sync(0xffffffffu, keys == 16);  // groups with all 16 keys
       // One tile, in three copies so that the common one is short: cached with
       // all its keys, cached with some, own keys (bf16, row by row).
       constexpr int kWhole = 0, kPart = 1, kOwn = 2;
-      auto tile = [&](auto kind, int j) -> bool {
+      auto tile = [&](auto kind, int j, const TileInfo& info) -> bool {
         constexpr int kKind = decltype(kind)::value;
         const int b = n & 1;
         const uint32_t s_col = t_lane + b * BN, p_col = t_lane + C::kTmemP + b * (BN / 2);
@@ -476,12 +552,15 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         // groups (never 0, where a group has no keys: 0 * -inf is not a
         // number), and which of them count.
         auto groups = [&](int x, float* f, float* wt) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int src = 8 * (j & 3) + 4 * half + 2 * x + i;
-            f[i] = kKind == kOwn ? p.scale_log2
-                                 : fmaxf(factor * __shfl_sync(0xffffffffu, ks, src), 1.1754944e-38f);
-            wt[i] = kKind == kOwn ? inv_c : __shfl_sync(0xffffffffu, vs, src) * inv_c;
+          if constexpr (kKind == kOwn) {
+            f[0] = f[1] = p.scale_log2;
+            wt[0] = wt[1] = inv_c;
+          } else {
+            const float2 ks = *reinterpret_cast<const float2*>(info.ks + 4 * half + 2 * x);
+            const float2 vs = *reinterpret_cast<const float2*>(info.vs + 4 * half + 2 * x);
+            f[0] = fmaxf(factor * ks.x, 1.1754944e-38f);
+            f[1] = fmaxf(factor * ks.y, 1.1754944e-38f);
+            wt[0] = vs.x * inv_c, wt[1] = vs.y * inv_c;
           }
         };
         auto scores = [&](int x, uint32_t* sr) {
@@ -491,9 +570,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
           if constexpr (kKind != kWhole) {
             uint32_t keep;
             if constexpr (kKind == kPart) {
-              const int src = 8 * (j & 3) + 4 * half + 2 * x;
-              const int k0 = __shfl_sync(0xffffffffu, keys, src);
-              const int k1 = __shfl_sync(0xffffffffu, keys, src + 1);
+              const int k0 = info.keys[4 * half + 2 * x], k1 = info.keys[4 * half + 2 * x + 1];
               keep = ((1u << k0) - 1u) | (((1u << k1) - 1u) << 16);
             } else {
               const int left = end - BN * (j - k.nc) - 64 * half - 32 * x;
@@ -506,15 +583,13 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
             }
           }
         };
-        const float c_new =
-            fmaxf(c, kKind == kOwn ? 1.f : __shfl_sync(0xffffffffu, vmax, 8 * (j & 3)));
+        const float c_new = fmaxf(c, kKind == kOwn ? 1.f : info.vmax);
         float shrink = 1.f;
         if (c_new != c) {
           shrink = c / c_new;
           c = c_new;
           inv_c = 1.f / c;
         }
-        if (!mbar_wait_warp(BAR(C::BAR_SFULL + b), (n >> 1) & 1, ab)) return false;
         if (n >= 2 && !mbar_wait_warp(BAR(C::BAR_PVDONE + b), ((n >> 1) - 1) & 1, ab)) return false;
         tc_fence_after();
         // The probabilities are taken against the reference as it stands; only
@@ -603,24 +678,19 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
       };
 #pragma unroll 1
       for (int j = 0; j < k.all && ok; ++j) {
-        if ((j & 3) == 0) {
-          if (j > 0) {
-            ks = next_ks, vs = next_vs;
-            keys = keys_of(k, j, last_page);
-            vmax = group_max(vs);
-            full = __ballot_sync(0xffffffffu, keys == 16);
+        if (!(ok = mbar_wait_warp(BAR(C::BAR_SFULL + (n & 1)), (n >> 1) & 1, ab))) break;
+        const TileInfo& info = s_info[cached & (C::kInfo - 1)];
+        if (j >= k.nc) {
+          ok = tile(std::integral_constant<int, kOwn>{}, j, info);
+        } else {
+          if (j == 0) {
+            const int e = s_exp[(q++ & (C::kExps - 1)) * C::BM + lb + (lane & 15)];
+            factor = pow2_bits(e) * p.scale_log2;
           }
-          last_page = next_page;
-          load_scales(last_page, &next_ks, &next_vs);
-          next_page = load_page(w, k, j + 8);
+          if (info.whole) ok = tile(std::integral_constant<int, kWhole>{}, j, info);
+          else ok = tile(std::integral_constant<int, kPart>{}, j, info);
+          ++cached;
         }
-        if (j == k.nc) put_q(false);
-        if (j >= k.nc)
-          ok = tile(std::integral_constant<int, kOwn>{}, j);
-        else if (((full >> (8 * (j & 3))) & 0xffu) == 0xffu)
-          ok = tile(std::integral_constant<int, kWhole>{}, j);
-        else
-          ok = tile(std::integral_constant<int, kPart>{}, j);
         if (ok) ++n;
       }
 
