@@ -889,14 +889,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 // ------------------------------------------------------------------ host
 
-// The launch's shape for given sizes: query rows per segment, blocks.
+// The launch's shape for given sizes: query rows per segment, blocks, and the
+// units of 128 keys that a segment's end is taken to cost.  Too few, and blocks
+// with many ends finish last; too many, and blocks with few do.  Measured (us;
+// 32 ragged requests of up to 8192 tokens, a quarter of the heads for keys):
+//                      finish 3     4     6     8    10
+//   headdim 128,  16 rows    79    76    78    80    82
+//   headdim 128,  32 rows   137   130   116   111   113
+//   headdim 128, 128 rows   150   142   139   137   136
+//   headdim  64, 128 rows   203   199   195   196   196
+//   headdim 256,  16 rows   113   110   103   101   103
+//   headdim 256,  64 rows   215   217   226   235   242
 struct CachePlan {
-  int tile_rows, blocks;
+  int tile_rows, blocks, finish;
 };
 CachePlan cache_plan_for(int max_new, int G, int d, int sms) {
   CachePlan c;
   const long long rows = static_cast<long long>(max_new) * G;
   c.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : d == 256 ? 64 : 128;
+  c.finish = d == 256 && c.tile_rows == 64 ? 4 : d < 256 && c.tile_rows == 16 ? 5 : 8;
   // as many as are resident at once (CacheTile::kResident)
   c.blocks = sms * (d == 256 || c.tile_rows == 128 ? 1 : d == 64 && c.tile_rows == 16 ? 3 : 2);
   return c;
@@ -925,7 +936,7 @@ cudaError_t launch_cache_rows(const CacheFwdParams& p, int tile_rows, cudaStream
   }
 }
 
-constexpr int kWholeKeys = 512, kFinish = 6, kLeast = 8;
+constexpr int kWholeKeys = 512, kLeast = 8;
 
 int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim) {
   if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
@@ -1039,7 +1050,7 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   // keys, kLeast of them at least to a block.
   const bool whole = static_cast<long long>(max_pages) * page_size <= kWholeKeys;
   p.unit = whole ? 0 : 128;
-  p.finish = whole ? 1 : kFinish;
+  p.finish = whole ? 1 : c.finish;
   p.least = whole ? 1 : kLeast;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -367,17 +367,17 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     auto convert = [&](uint32_t raw, uint32_t dst, bool mask, int group_keys) {
       constexpr int kChunks = D / 64;
 #pragma unroll 1
-      for (int half = 0; half < 4 * kChunks; half += 4) {
-        uint4 x[4];
+      for (int half = 0; half < 4 * kChunks; half += 1) {
+        uint4 x[1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 1; ++i) {
           const int at = half + i, f = at % kChunks;
           const int r = 8 * (4 * (at / kChunks) + cw) + r8;
           if constexpr (D == 64) x[i] = lds128(raw + r * 64 + ((pc ^ ((r >> 1) & 3)) << 4));
           else x[i] = lds128(raw + r * 128 + (((pc + 4 * f) ^ r8) << 4));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 1; ++i) {
           const int at = half + i, f = at % kChunks;
           const int r = 8 * (4 * (at / kChunks) + cw) + r8;
           if (mask && (r & 15) >= __shfl_sync(0xffffffffu, group_keys, r >> 4))
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
       const __nv_bfloat16* src = isv ? p.v + x.rq.row0 * p.v_sr + k.h * p.v_sh
                                      : p.k + x.rq.row0 * p.k_sr + k.h * p.k_sh;
       const long long sr = isv ? p.v_sr : p.k_sr;
-#pragma unroll 4
+#pragma unroll 1
       for (int i = 0; i < D / 8; ++i) {
         const int at = i * 128 + c, r = at / (D / 8), u = at % (D / 8);
         const bool there = first + r < x.rq.n;
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
       }
     };
     auto copy_q = [&](const Piece& x, const Tiles& k) {
-#pragma unroll 4
+#pragma unroll 1
       for (int i = 0; i < D / 8; ++i) {
         const int at = i * 128 + c, row = at / (D / 8), u = at % (D / 8);
         const int r = min(k.row_base + row, k.R - 1);
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     // in rows that do not see them) and noted.
     auto drop_odd = [&](uint32_t dst) {
       bool odd = false;
-#pragma unroll 4
+#pragma unroll 1
       for (int i = 0; i < D / 8; ++i) {
         const int at = i * 128 + c, r = at / (D / 8), u = at % (D / 8);
         const uint32_t to = dst + (u >> 3) * (BN * 128) + r * 128 + (((u ^ r) & 7) << 4);
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     // Q from bf16 to f16 after a power of two of each row's, whose exponents go
     // to `exps`.
     auto scale_q = [&](signed char* exps) {
-#pragma unroll 2
+#pragma unroll 1
       for (int i = 0; i < D / 8; ++i) {
         const int at = i * 128 + c, row = at / (D / 8), u = at % (D / 8);
         // 16-byte unit u of a row: 64-dim chunk u / 8, swizzled by the row
