@@ -580,8 +580,11 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
   }
 
   __syncthreads();  // the queries' fragments
-  uint4 qf[kHoldQ ? MT : 1][T::kFrags];
-  if constexpr (kHoldQ) {
+  // Held in registers where there is room; headdim 64, three blocks to an SM,
+  // reads them for every unit (89.6 us against 93.9, 16 rows).
+  constexpr bool kHoldF = kHoldQ && D != 64;
+  uint4 qf[kHoldF ? MT : 1][T::kFrags];
+  if constexpr (kHoldF) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const uint4 a = kHoldQ ? qf[kHoldQ ? mt : 0][sg * 4 + s]
+          const uint4 a = kHoldF ? qf[kHoldF ? mt : 0][sg * 4 + s]
                                  : load16(qbase + (mt * T::kFrags + sg * 4 + s) * 512);
 #pragma unroll
           for (int n = 0; n < 4; ++n) mma_f16(sc[mt][n], a, b[n][0], b[n][1]);
