@@ -267,17 +267,22 @@ struct AppendParams {
   int rows, max_new, Hk, page_size, num_pages, max_pages, touch;
 };
 
-// Eight bf16 values times `inv`, as e4m3; values that are not finite become
-// NaN (e4m3 holds no infinity).
-__device__ __forceinline__ uint2 quantise8(const uint4& w, float inv) {
+// Eight bf16 values times `inv`, as e4m3; with `odd`, values that are not
+// finite become NaN (e4m3 holds no infinity).
+__device__ __forceinline__ uint2 quantise8(const uint4& w, float inv, bool odd) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     o[i] = pack_e4m3x2(__uint_as_float(u[i] << 16) * inv,
                        __uint_as_float(u[i] & 0xffff0000u) * inv);
-    if ((u[i] & 0x7f80u) == 0x7f80u) o[i] |= 0x007fu;
-    if ((u[i] & 0x7f800000u) == 0x7f800000u) o[i] |= 0x7f00u;
+  }
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((u[i] & 0x7f80u) == 0x7f80u) o[i] |= 0x007fu;
+      if ((u[i] & 0x7f800000u) == 0x7f800000u) o[i] |= 0x7f00u;
+    }
   }
   return make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
 }
@@ -344,21 +349,37 @@ __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams
   }
   float* scale = p.scale[which] + static_cast<long long>(page) * p.Hk + h;
   const float was = *scale;
+  // The page's largest magnitude, of every value first, two to an operation;
+  // only a page with values that are not finite is looked at value by value.
+  auto block_max = [&](unsigned x) {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if constexpr (NT > 32) {
+      if ((tid & 31) == 0) s_top[tid >> 5] = x;
+      __syncthreads();
 #pragma unroll
-  for (int u = 0; u < VPT; ++u) {
-    const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned lo = v[e] & 0x7fffu, hi = (v[e] >> 16) & 0x7fffu;
-      top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      for (int i = 0; i < NT / 32; ++i) x = max(x, s_top[i]);
     }
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if constexpr (NT > 32) {
-    if ((tid & 31) == 0) s_top[tid >> 5] = top;
-    __syncthreads();
+    return x;
+  };
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) top = max(top, s_top[i]);
+  for (int u = 0; u < VPT; ++u)
+    top = __vmaxu2(__vmaxu2(top, __vmaxu2(w[u].x & 0x7fff7fffu, w[u].y & 0x7fff7fffu)),
+                   __vmaxu2(w[u].z & 0x7fff7fffu, w[u].w & 0x7fff7fffu));
+  top = block_max(max(top & 0xffffu, top >> 16));
+  const bool odd = top >= 0x7f80u;
+  if (odd) {
+    top = 0;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned lo = v[e] & 0x7fffu, hi = (v[e] >> 16) & 0x7fffu;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+    }
+    if constexpr (NT > 32) __syncthreads();  // the first maxima have been read
+    top = block_max(top);
   }
   int e = cache_scale_exp(top);
   float now = __int_as_float((e + 127) << 23);
@@ -385,7 +406,7 @@ __global__ void __launch_bounds__(NT) dfa_cache_append_kernel(const AppendParams
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int i = u * NT + tid;
-    if (i < nvec) dst[i] = quantise8(w[u], inv);
+    if (i < nvec) dst[i] = quantise8(w[u], inv, odd);
   }
   if constexpr (NT > 32) __syncthreads();  // every thread has read the old scale
   else __syncwarp();

@@ -359,34 +359,32 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     // e4m3 -> f16: a thread turns 16 values (a 16-byte piece) into two pieces
     // of its row.  Eight lanes, one phase of a shared-memory access, take four
     // neighbouring pieces of rows r and r ^ 5: under either tile's swizzle
-    // their reads and their writes fall on different banks.
+    // their reads and their writes fall on different banks.  From 32 rows to
+    // the next the addresses differ by a constant.
     // `mask`: rows past their group's keys (lane g: those of group g) become
     // zero, whatever the raw bytes are there, NaN included.
     const int pc = lane & 3;
-    const int r8 = (lane >> 3) ^ (5 * ((lane >> 2) & 1));  // row of its eight
+    const int r0 = 8 * cw + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));  // row of 32
+    const uint32_t put_at = r0 * 128 + (((2 * pc) ^ (r0 & 7)) << 4);
+    const uint32_t get_at = D == 64 ? r0 * 64 + ((pc ^ ((r0 >> 1) & 3)) << 4)
+                                    : r0 * 128 + ((pc ^ (r0 & 7)) << 4);
     auto convert = [&](uint32_t raw, uint32_t dst, bool mask, int group_keys) {
-      constexpr int kChunks = D / 64;
+      uint32_t from = raw + get_at, to = dst + put_at;
 #pragma unroll 1
-      for (int half = 0; half < 4 * kChunks; half += 1) {
-        uint4 x[1];
+      for (int i = 0; i < 4; ++i, from += 32 * D, to += 32 * 128) {
+        uint4 x[D / 64];
 #pragma unroll
-        for (int i = 0; i < 1; ++i) {
-          const int at = half + i, f = at % kChunks;
-          const int r = 8 * (4 * (at / kChunks) + cw) + r8;
-          if constexpr (D == 64) x[i] = lds128(raw + r * 64 + ((pc ^ ((r >> 1) & 3)) << 4));
-          else x[i] = lds128(raw + r * 128 + (((pc + 4 * f) ^ r8) << 4));
+        for (int f = 0; f < D / 64; ++f) x[f] = lds128(from ^ (64 * f));
+        if (mask && (r0 & 15) >= __shfl_sync(0xffffffffu, group_keys, 2 * i + (r0 >> 4))) {
+#pragma unroll
+          for (int f = 0; f < D / 64; ++f) x[f] = make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int i = 0; i < 1; ++i) {
-          const int at = half + i, f = at % kChunks;
-          const int r = 8 * (4 * (at / kChunks) + cw) + r8;
-          if (mask && (r & 15) >= __shfl_sync(0xffffffffu, group_keys, r >> 4))
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t to = dst + f * (BN * 128) + r * 128;
-          st_shared_v4(to + (((2 * pc) ^ r8) << 4), e4m3_lo(x[i].x), e4m3_hi(x[i].x),
-                       e4m3_lo(x[i].y), e4m3_hi(x[i].y));
-          st_shared_v4(to + (((2 * pc + 1) ^ r8) << 4), e4m3_lo(x[i].z), e4m3_hi(x[i].z),
-                       e4m3_lo(x[i].w), e4m3_hi(x[i].w));
+        for (int f = 0; f < D / 64; ++f) {
+          st_shared_v4(to + f * (BN * 128), e4m3_lo(x[f].x), e4m3_hi(x[f].x), e4m3_lo(x[f].y),
+                       e4m3_hi(x[f].y));
+          st_shared_v4((to ^ 16) + f * (BN * 128), e4m3_lo(x[f].z), e4m3_hi(x[f].z),
+                       e4m3_lo(x[f].w), e4m3_hi(x[f].w));
         }
       }
     };
