@@ -65,7 +65,7 @@ _SIGNATURES = {
     "dfa_cache_append_pages": (_I, [_I] * 2),
     "dfa_cache_append_span": (_I, [_I] * 4 + [ctypes.POINTER(_I)]),
     "dfa_cache_units": (_I, [_I] * 4),
-    "dfa_cache_blocks": (_I, [ctypes.c_longlong, _I, _I]),
+    "dfa_cache_blocks": (_I, [ctypes.c_longlong, _I]),
     "dfa_cache_run": (ctypes.c_longlong, [_I, ctypes.c_longlong, _I]),
     "dfa_cache_owner": (_I, [ctypes.c_longlong, ctypes.c_longlong, _I]),
     "dfa_cache_own_end": (_I, [_I] * 4),

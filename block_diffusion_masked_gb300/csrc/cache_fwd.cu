@@ -17,17 +17,36 @@
 // unrounded; a value page's scale, relative to the largest one met so far,
 // multiplies its probabilities.  Own keys and values are bf16 products.
 //
-// Work.  All query heads of a key/value head share its keys: row r of a tile
-// is query row r / G and head r % G.  Items are (request, chunk of its cached
-// keys); blocks of x = (key/value head, row tile), y = item.  A block's WK
-// warp groups take 32-key units of the chunk in turn, each with a ring of
-// stages of its own, filled by TMA boxes (32 tokens of one page and head) and
-// with softmax statistics of its own; the groups join through shared memory
-// at the end, the chunks of a request through a float32 workspace and a
-// second launch.  mma.sync fragments are read straight out of the swizzled
-// e4m3 tiles: the head dims (and the keys) may be numbered in any order
-// inside a product, so each thread takes 16 contiguous bytes of a token,
-// which are the operands of four k steps of Q K^T or 16 column tiles of P V.
+// The reference of a row's exponentials moves only where a unit's
+// probabilities outgrow f16 (cache_fwd.cuh), so that most units need neither a
+// maximum nor a rescaling of the output.
+//
+// Work.  All query heads of a key/value head share its keys: row r of a
+// segment's tile is query row r / G and head r % G.  Segments (request,
+// key/value head, tile of rows) are dealt to the blocks in equal runs of
+// 128-key units (cache.cuh); a block walks its run piece by piece.  Its WK warp
+// groups take 32-key units of a piece in turn, each with a ring of stages of
+// its own, filled by TMA boxes (32 tokens of one page and head) that run ahead
+// over the pieces' ends, and with softmax statistics of its own; the groups
+// join through shared memory at a piece's end, the pieces of a cut segment
+// through a float32 workspace and a second launch.  mma.sync fragments are
+// read straight out of the swizzled e4m3 tiles: the head dims (and the keys)
+// may be numbered in any order inside a product, so each thread takes 16
+// contiguous bytes of a token, which are the operands of four k steps of
+// Q K^T or 16 column tiles of P V.
+//
+// For up to 32 rows to a key (headdim 256: any number), where the tcgen05
+// kernel's 128 rows would be mostly empty: 32 rows 107 us here, 122 there
+// (headdim 128), 132 and 183 (headdim 64); 64 rows as two tiles here 191, 126
+// there.  (32 ragged requests of up to 8192 tokens, 330 MB.)
+//
+// Measured, 16 rows, headdim 128: 73 us for those 330 MB (4.5 TB/s, 66% of
+// what a copy reaches), 60 us for 24 requests of up to 8000 tokens (3.9 TB/s).
+// Bound by latency: 255 registers a thread leave 8 warps to an SM, which issue
+// in 36% of the cycles (DRAM 50%, tensor pipe 20%), and some 7 us pass before
+// the first products (lengths, queries, first tiles: each a trip to memory),
+// 4 at a piece's end.  Two blocks of four groups: 60.1 us; four of two 62.5;
+// one of eight 73.7; loops over the products rolled 63 to 66.
 #include <cmath>
 #include <type_traits>
 
@@ -815,7 +834,9 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
 }
 
 // The pieces of the segments that runs' ends have cut, joined: weights
-// 2^(lse_s - max), a warp a row and query head, the pieces' outputs read once.
+// 2^(lse_s - max), a warp a row and query head, the pieces' outputs read once,
+// a batch of them in flight together.  4 us for 16 rows, 9 us for 128 (304 and
+// 152 blocks before it).
 // Blocks (x, y): the cut that block x of the launch before answers for, rows y,
 // y + gridDim.y, ... of kJoinWarps.
 constexpr int kJoinWarps = 4;
@@ -939,7 +960,7 @@ cudaError_t launch_cache_rows(const CacheFwdParams& p, int tile_rows, cudaStream
   }
 }
 
-constexpr int kWholeKeys = 512, kLeast = 8;
+constexpr int kWholeKeys = 512;  // see dfa_cache_forward
 
 int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim) {
   if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
@@ -1048,13 +1069,19 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   p.max_pages = max_pages;
   p.tile_rows = c.tile_rows;
   p.blocks = c.blocks;
-  // Requests that cannot hold more than kWholeKeys are not worth cutting: one
-  // unit each, and no join to launch.  Longer ones are cut into units of 128
-  // keys, kLeast of them at least to a block.
-  const bool whole = static_cast<long long>(max_pages) * page_size <= kWholeKeys;
+  // Short tables are not worth cutting, for one unit a segment needs no join
+  // (a launch): up to kWholeKeys keys, and up to twice that where the segments
+  // are half the blocks or more.  Measured, not cut against cut: 64 requests
+  // of 500 keys and 4 heads 15.0 and 18.8 us, of 1000 keys 22.3 and 26.5; one
+  // request of 250 keys 9.1 and 9.8, of 500 12.0 and 10.0 but for the second
+  // launch, of 1000 17.6 and 10.5.
+  const long long most_keys = static_cast<long long>(max_pages) * page_size;
+  const long long segments = static_cast<long long>(batch) * kv_heads *
+                             ((static_cast<long long>(max_new) * G - 1) / c.tile_rows + 1);
+  const bool whole =
+      most_keys <= kWholeKeys || (most_keys <= 2 * kWholeKeys && 2 * segments >= c.blocks);
   p.unit = whole ? 0 : 128;
   p.finish = whole ? 1 : c.finish;
-  p.least = whole ? 1 : kLeast;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = d == 64    ? launch_cache_rows<64>(p, c.tile_rows, s)

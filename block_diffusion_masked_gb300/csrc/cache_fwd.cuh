@@ -1,5 +1,5 @@
 // What the kernels of attention over the paged cache share: parameters, the
-// split of a launch into items, conversions.
+// walk over a block's run of units, conversions.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,7 +42,6 @@ struct CacheFwdParams {
   int tile_rows;  // query rows of a segment
   int unit;       // keys per unit of the split, 0: segments are not cut
   int finish;     // units a segment's end counts for
-  int least;      // units a block should get at least
   int blocks;     // blocks of the launch
   float scale_log2;
 };
@@ -116,7 +115,7 @@ __device__ __forceinline__ Census take_census(const CacheFwdParams& p, bool* bad
   }
   c.before = upto - c.mine;
   c.total = __shfl_sync(0xffffffffu, upto, 31);
-  c.blocks = cache_blocks(c.total, p.blocks, p.least);
+  c.blocks = cache_blocks(c.total, p.blocks);
   return c;
 }
 

@@ -522,7 +522,7 @@ int dfa_cache_page_ok(int page, int num_pages);
 int dfa_cache_append_pages(int max_new, int page_size);
 int dfa_cache_append_span(int len, int n, int j, int page_size, int *span);
 int dfa_cache_units(int len, int n, int unit, int finish);
-int dfa_cache_blocks(long long total, int limit, int least);
+int dfa_cache_blocks(long long total, int limit);
 long long dfa_cache_run(int x, long long total, int blocks);
 int dfa_cache_owner(long long w, long long total, int blocks);
 int dfa_cache_own_end(int len, int i, int n, int block_size);

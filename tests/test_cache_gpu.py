@@ -335,6 +335,19 @@ def test_attention_split_over_chunks(b, d, G, T):
     _check(p, T, out, lse)
 
 
+@pytest.mark.parametrize("longest", [500, 1000])
+@pytest.mark.parametrize("B,H,T", [(1, 4, 1), (80, 4, 1), (40, 16, 5), (3, 16, 20)])
+def test_attention_short_tables(b, B, H, T, longest):
+    """Tables of a few pages, few and many segments: whole segments and cut ones."""
+    g = np.random.default_rng(B + longest)
+    lens = g.integers(0, longest + 1, B).tolist()
+    lens[0] = longest
+    p = _problem(lens, [T] * B, H, 4, 64, 16, seed=B)
+    out, lse = _run(b, p, 8)
+    assert b.dfa_status() == 0
+    _check(p, 8, out, lse)
+
+
 @pytest.mark.parametrize("H", [4, 32])
 @pytest.mark.parametrize("lens", [[0], [5], [0, 70, 0, 16], [1000, 0]])
 def test_attention_without_own_keys(b, lens, H):

@@ -175,17 +175,17 @@ def test_runs_share_the_units(lib):
     name their owners."""
     g = np.random.default_rng(0)
     for _ in range(200):
-        B, limit, least = int(g.integers(1, 70)), int(g.integers(1, 400)), int(g.integers(1, 9))
+        B, limit = int(g.integers(1, 70)), int(g.integers(1, 400))
         lens = (2.0 ** g.uniform(0, 17, B)).astype(int) * (g.random(B) < 0.9)
         rows = (g.random(B) < 0.9).astype(int)
         units = [lib.dfa_cache_units(int(n), int(r), 128, 3) for n, r in zip(lens, rows)]
         assert units == [r * (3 - -int(n) // 128) for n, r in zip(lens, rows)]
         total = sum(units) * int(g.integers(1, 9))
-        blocks = lib.dfa_cache_blocks(total, limit, least)
+        blocks = lib.dfa_cache_blocks(total, limit)
         if total == 0:
             assert blocks == 0
             continue
-        assert 1 <= blocks <= limit and (blocks == limit or (blocks - 1) * least < total)
+        assert blocks == min(limit, total)
         ends = [lib.dfa_cache_run(x, total, blocks) for x in range(blocks + 1)]
         assert ends[0] == 0 and ends[-1] == total
         sizes = np.diff(ends)
