@@ -58,7 +58,7 @@ _SIGNATURES = {
     "dfa_cache_plan": (_I, [_P] * 10 + [_I] * 5 + [_P]),
     "dfa_cache_release": (_I, [_P] * 5 + [_I] * 4 + [_P]),
     "dfa_cache_append": (_I, [_P] * 9 + [_I] * 8 + [_P] * 3),
-    "dfa_cache_workspace_bytes": (ctypes.c_longlong, [_I] * 6),
+    "dfa_cache_workspace_bytes": (ctypes.c_longlong, [_I] * 8),
     "dfa_cache_forward": (_I, [_P] * 13 + [ctypes.c_longlong] + [_I] * 10 + [_P] * 4),
     "dfa_cache_scale_exp": (_I, [ctypes.c_uint]),
     "dfa_cache_page_ok": (_I, [_I] * 2),
@@ -595,6 +595,7 @@ def dfa_bwd_dq_convert(dq_acc, dq, mode=MODE_DIFFUSION):
 
 _INT_MAX = (1 << 31) - 1  # larger arguments stand for it: ctypes would wrap them
 
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -602,7 +603,7 @@ def _call(fn, device, *args):
     """Call entry point ``fn`` with ``device`` current, on its current stream."""
     handle = _lib or lib()
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _get_device():
         stream = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
         rc = getattr(handle, fn)(*args, stream)
     else:
@@ -633,20 +634,29 @@ def _check_heads(t, dim, name, device=None):
         raise ValueError(f"{name} must be a {dim}-dimensional bfloat16 tensor on {where}")
 
 
-def _strides(t, name):
-    """Host array of a tensor's leading strides, None where it is contiguous.
+@functools.lru_cache(maxsize=1024)
+def _stride_array(lead, *strides):
+    """Host array of ``lead`` zeros and the leading strides; None for strides the
+    kernels do not take."""
+    if strides[-1] != 1 or any(x & 7 for x in strides[:-1]):
+        return None
+    return (ctypes.c_longlong * (lead + len(strides) - 1))(*[0] * lead, *strides[:-1])
+
+
+def _strides(t, name, lead=0):
+    """Host array of a tensor's leading strides (behind ``lead`` zeros), None where
+    it is contiguous.
 
     The last dimension must be contiguous and the others multiples of 8
     elements (16 bytes), as must be the address of the first element.
     """
     if t.is_contiguous():
         return None
-    s = t.stride()
-    lead = s[:-1]
-    if s[-1] != 1 or any([x & 7 for x in lead]):
+    array = _stride_array(lead, *t.stride())
+    if array is None:
         raise ValueError(f"{name}: the last dimension must be contiguous and the other strides "
                          "multiples of 8 elements")
-    return (ctypes.c_longlong * len(lead))(*lead)
+    return array
 
 
 def dfa_rotary(q, k, table, positions=None, period=None, interleaved=False, inverse=False,
@@ -703,16 +713,14 @@ def _rotary_sizes(q, k, table, positions, period):
 
 def _rotary_launch(q, k, table, positions, sizes, flags, q_out=None, k_out=None):
     """dfa_rotary of tensors that _rotary_sizes (or a call like it) has checked."""
-    q_str, k_str, kp, kop = _strides(q, "q"), None, None, None
+    lead = 1 if len(q.shape) == 3 else 0  # packed rows: a batch of one
+    q_str, k_str, kp, kop = _strides(q, "q", lead), None, None, None
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if k is not None:
         if k_out is None:
             k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
-        k_str, kp, kop = _strides(k, "k"), k.data_ptr(), k_out.data_ptr()
-    if len(q.shape) == 3:  # the strides of a batch of one
-        q_str = q_str and (ctypes.c_longlong * 3)(0, *q_str)
-        k_str = k_str and (ctypes.c_longlong * 3)(0, *k_str)
+        k_str, kp, kop = _strides(k, "k", lead), k.data_ptr(), k_out.data_ptr()
     _call("dfa_rotary", q.device, q.data_ptr(), kp, q_out.data_ptr(), kop, table.data_ptr(),
           None if positions is None else positions.data_ptr(), *sizes, q_str, k_str, flags)
     return q_out, k_out
@@ -805,9 +813,11 @@ def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_
           Hk, d, ps, P, maxp, _strides(k, "k"), _strides(v, "v"))
 
 
-def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim):
-    """Bytes of workspace dfa_cache_forward needs on the current device."""
-    n = lib().dfa_cache_workspace_bytes(batch, rows, int(max_new), heads, kv_heads, headdim)
+def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim, page_size,
+                              max_pages):
+    """Bytes of workspace dfa_cache_forward needs on the current device (0: none)."""
+    n = lib().dfa_cache_workspace_bytes(batch, rows, int(max_new), heads, kv_heads, headdim,
+                                        page_size, max_pages)
     if n < 0:
         raise DfaError("dfa_cache_workspace_bytes", int(n))
     return int(n)
@@ -817,7 +827,7 @@ def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim):
 def _workspace_bytes(device_index, *sizes):
     """dfa_cache_workspace_bytes on a device, which sizes alone determine."""
     with torch.cuda.device(device_index):
-        return max(dfa_cache_workspace_bytes(*sizes), 16)
+        return dfa_cache_workspace_bytes(*sizes)
 
 
 def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new,
@@ -855,14 +865,16 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
         _check_dense(lse, (H, rows), torch.float32, dev, "lse")
     max_new = min(int(max_new), _INT_MAX)
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes(dev.index, B, rows, max_new, H, Hk, d),
-                                dtype=torch.uint8, device=dev)
+        nwork = _workspace_bytes(dev.index, B, rows, max_new, H, Hk, d, ps, maxp)
+        if nwork:
+            workspace = torch.empty(nwork, dtype=torch.uint8, device=dev)
     else:
-        _check_dense(workspace, (workspace.numel(),), torch.uint8, dev, "workspace")
+        nwork = workspace.numel()
+        _check_dense(workspace, (nwork,), torch.uint8, dev, "workspace")
     _call("dfa_cache_forward", dev, q.data_ptr(), kp, vp, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
-          cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-          workspace.numel(), B, rows, max_new, H, Hk, d, min(int(block_size), _INT_MAX), ps, P, maxp,
+          cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          None if workspace is None else workspace.data_ptr(), nwork, B, rows, max_new, H, Hk, d, min(int(block_size), _INT_MAX), ps, P, maxp,
           _strides(q, "q"), ks, vs)
     return out, lse
 

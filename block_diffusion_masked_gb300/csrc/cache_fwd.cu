@@ -913,8 +913,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 // ------------------------------------------------------------------ host
 
-// The launch's shape for given sizes: query rows per segment, blocks, and the
-// units of 128 keys that a segment's end is taken to cost.  Too few, and blocks
+// Tables of up to this many keys are not cut, see CachePlan.
+constexpr int kWholeKeys = 512;
+
+// The launch's shape for given sizes.
+//
+// tile_rows: query rows of a segment.  blocks: as many as are resident at once
+// (CacheTile::kResident).
+//
+// whole: segments are not cut.  Short tables are not worth it, for one unit a
+// segment needs no join (a launch) and no workspace: up to kWholeKeys keys, and
+// up to twice that where the segments are half the blocks or more.  Measured,
+// not cut against cut: 64 requests of 500 keys and 4 heads 15.0 and 18.8 us, of
+// 1000 keys 22.3 and 26.5; one request of 250 keys 9.1 and 9.8, of 500 12.0 and
+// 10.0 but for the second launch, of 1000 17.6 and 10.5.
+//
+// finish: units of 128 keys that a segment's end is taken to cost.  Too few, and blocks
 // with many ends finish last; too many, and blocks with few do.  Measured (us;
 // 32 ragged requests of up to 8192 tokens, a quarter of the heads for keys):
 //                      finish 3     4     6     8    10
@@ -926,14 +940,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 //   headdim 256,  64 rows   215   217   226   235   242
 struct CachePlan {
   int tile_rows, blocks, finish;
+  bool whole;
+  // bytes of the pieces' outputs and lse and of the cuts
+  long long workspace(int d) const {
+    return whole ? 0
+                 : 2LL * blocks * tile_rows * (d + 1) * 4 +
+                       blocks * static_cast<long long>(sizeof(Cut));
+  }
 };
-CachePlan cache_plan_for(int max_new, int G, int d, int sms) {
+CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, long long keys,
+                         int sms) {
   CachePlan c;
   const long long rows = static_cast<long long>(max_new) * G;
   c.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : d == 256 ? 64 : 128;
   c.finish = d == 256 && c.tile_rows == 64 ? 4 : d < 256 && c.tile_rows == 16 ? 5 : 8;
-  // as many as are resident at once (CacheTile::kResident)
   c.blocks = sms * (d == 256 || c.tile_rows == 128 ? 1 : d == 64 && c.tile_rows == 16 ? 3 : 2);
+  const long long segments = batch * kv_heads * ((rows - 1) / c.tile_rows + 1);
+  c.whole = keys <= kWholeKeys || (keys <= 2 * kWholeKeys && 2 * segments >= c.blocks);
   return c;
 }
 
@@ -960,13 +983,15 @@ cudaError_t launch_cache_rows(const CacheFwdParams& p, int tile_rows, cudaStream
   }
 }
 
-constexpr int kWholeKeys = 512;  // see dfa_cache_forward
-
-int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim) {
+int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim,
+                      int page_size, int max_pages) {
   if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
       max_new > (1 << 24) || heads < 1 || heads > (1 << 16) || kv_heads < 1 || kv_heads > heads ||
       heads % kv_heads ||
-      static_cast<long long>(max_new < rows ? max_new : rows) * (heads / kv_heads) > (1 << 30))
+      static_cast<long long>(max_new < rows ? max_new : rows) * (heads / kv_heads) > (1 << 30) ||
+      max_pages < 1 ||
+      (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
+      static_cast<long long>(max_pages) * page_size > (1 << 30))
     return DFA_EINVAL;
   if (headdim != 64 && headdim != 128 && headdim != 256) return DFA_EUNSUPPORTED;
   return DFA_OK;
@@ -980,15 +1005,17 @@ using namespace dfa;
 extern "C" {
 
 long long dfa_cache_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
-                                    int headdim) {
-  if (const int rc = check_cache_sizes(batch, rows, max_new, heads, kv_heads, headdim)) return rc;
+                                    int headdim, int page_size, int max_pages) {
+  if (const int rc = check_cache_sizes(batch, rows, max_new, heads, kv_heads, headdim, page_size,
+                                       max_pages))
+    return rc;
   if (batch == 0 || rows == 0 || max_new == 0) return 0;
   DeviceInfo di;
   if (const int rc = device_info(&di)) return rc;
   if (max_new > rows) max_new = rows;
-  const CachePlan c = cache_plan_for(max_new, heads / kv_heads, headdim, di.sms);
-  return 2LL * c.blocks * c.tile_rows * (headdim + 1) * 4 +
-         c.blocks * static_cast<long long>(sizeof(Cut));
+  return cache_plan_for(batch, max_new, heads / kv_heads, kv_heads, headdim,
+                        static_cast<long long>(max_pages) * page_size, di.sms)
+      .workspace(headdim);
 }
 
 int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k_cache,
@@ -999,11 +1026,10 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
                       int page_size, int num_pages, int max_pages, const long long* q_strides,
                       const long long* k_strides, const long long* v_strides,
                       dfa_stream_t stream) {
-  if (const int rc = check_cache_sizes(batch, rows, max_new, heads, kv_heads, headdim)) return rc;
-  if (block_size < 1 || num_pages < 1 || max_pages < 1 ||
-      (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
-      static_cast<long long>(max_pages) * page_size > (1 << 30))
-    return DFA_EINVAL;
+  if (const int rc = check_cache_sizes(batch, rows, max_new, heads, kv_heads, headdim, page_size,
+                                       max_pages))
+    return rc;
+  if (block_size < 1 || num_pages < 1) return DFA_EINVAL;
   if (batch == 0 || rows == 0 || max_new == 0) return DFA_OK;
   auto aligned = [](const void* x, unsigned n) {
     return x && (reinterpret_cast<uintptr_t>(x) & (n - 1)) == 0;
@@ -1011,17 +1037,16 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(lse, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
       !aligned(block_table, 4) || !aligned(cache_lens, 4) || !aligned(cu_new, 4) ||
-      !aligned(workspace, 16) || (k == nullptr) != (v == nullptr) ||
+      (workspace && !aligned(workspace, 16)) || (k == nullptr) != (v == nullptr) ||
       (k && (!aligned(k, 16) || !aligned(v, 16))))
     return DFA_EINVAL;
   DeviceInfo di;
   if (const int rc = device_info(&di)) return rc;
   if (max_new > rows) max_new = rows;
   const int G = heads / kv_heads, d = headdim;
-  const CachePlan c = cache_plan_for(max_new, G, d, di.sms);
-  const long long parts = 2LL * c.blocks * c.tile_rows;
-  if (workspace_bytes < parts * (d + 1) * 4 + c.blocks * static_cast<long long>(sizeof(Cut)))
-    return DFA_EINVAL;
+  const CachePlan c = cache_plan_for(batch, max_new, G, kv_heads, d,
+                                     static_cast<long long>(max_pages) * page_size, di.sms);
+  if (!c.whole && (!workspace || workspace_bytes < c.workspace(d))) return DFA_EINVAL;
   CacheFwdParams p{};
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d),
                               static_cast<cuuint64_t>(kv_heads) * page_size,
@@ -1052,9 +1077,12 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   p.cu_new = cu_new;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o + parts * d;
-  p.cuts = reinterpret_cast<Cut*>(p.part_lse + parts);
+  if (!c.whole) {
+    const long long parts = 2LL * c.blocks * c.tile_rows;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = p.part_o + parts * d;
+    p.cuts = reinterpret_cast<Cut*>(p.part_lse + parts);
+  }
   p.status = di.status;
   p.batch = batch;
   p.rows = rows;
@@ -1069,25 +1097,14 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
   p.max_pages = max_pages;
   p.tile_rows = c.tile_rows;
   p.blocks = c.blocks;
-  // Short tables are not worth cutting, for one unit a segment needs no join
-  // (a launch): up to kWholeKeys keys, and up to twice that where the segments
-  // are half the blocks or more.  Measured, not cut against cut: 64 requests
-  // of 500 keys and 4 heads 15.0 and 18.8 us, of 1000 keys 22.3 and 26.5; one
-  // request of 250 keys 9.1 and 9.8, of 500 12.0 and 10.0 but for the second
-  // launch, of 1000 17.6 and 10.5.
-  const long long most_keys = static_cast<long long>(max_pages) * page_size;
-  const long long segments = static_cast<long long>(batch) * kv_heads *
-                             ((static_cast<long long>(max_new) * G - 1) / c.tile_rows + 1);
-  const bool whole =
-      most_keys <= kWholeKeys || (most_keys <= 2 * kWholeKeys && 2 * segments >= c.blocks);
-  p.unit = whole ? 0 : 128;
-  p.finish = whole ? 1 : c.finish;
+  p.unit = c.whole ? 0 : 128;
+  p.finish = c.whole ? 1 : c.finish;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(d)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = d == 64    ? launch_cache_rows<64>(p, c.tile_rows, s)
                   : d == 128 ? launch_cache_rows<128>(p, c.tile_rows, s)
                              : launch_cache_rows<256>(p, c.tile_rows, s);
-  if (e == cudaSuccess && !whole) {
+  if (e == cudaSuccess && !c.whole) {
     auto join = d == 64 ? dfa_cache_join_kernel<64>
                         : d == 128 ? dfa_cache_join_kernel<128> : dfa_cache_join_kernel<256>;
     const int rows = (c.tile_rows + kJoinWarps - 1) / kJoinWarps;

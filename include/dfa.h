@@ -426,12 +426,14 @@ int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int 
  * bf16, strides as for the append; out (rows, heads, headdim) bf16 contiguous,
  * lse (heads, rows) float32.  A row that sees no key gets out 0 and lse -inf.
  * kv_heads divides heads, head h reads key/value head h / (heads / kv_heads).
- * batch <= 32768, and max_new times heads / kv_heads at most 2^30.  workspace: dfa_cache_workspace_bytes(...) bytes of device
- * memory (16-byte aligned) for the partial results of long requests; calls
- * that may run at the same time need workspaces of their own.
+ * batch <= 32768, and max_new times heads / kv_heads at most 2^30.
+ * workspace: dfa_cache_workspace_bytes(...) bytes of device memory (16-byte
+ * aligned; 0 for short tables, and then NULL will do) for the partial results
+ * of long requests; calls that may run at the same time need workspaces of
+ * their own.
  */
 long long dfa_cache_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
-                                    int headdim);
+                                    int headdim, int page_size, int max_pages);
 int dfa_cache_forward(const void *q, const void *k, const void *v, const void *k_cache,
                       const void *v_cache, const float *k_scale, const float *v_scale,
                       const int *block_table, const int *cache_lens, const int *cu_new, void *out,

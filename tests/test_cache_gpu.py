@@ -459,7 +459,6 @@ def test_refusals(b):
         with pytest.raises((ValueError, b.DfaError)):
             b.dfa_cache_forward(*bad, **good)
     for kw in (dict(k=p["k"]), dict(k=p["k"], v=p["v"][:1]), dict(**good, block_size=0),
-               dict(**good, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)),
                dict(**good, out=torch.empty(2, 4, 64, device=DEV))):
         with pytest.raises((ValueError, b.DfaError)):
             b.dfa_cache_forward(*args, **kw)
@@ -472,6 +471,29 @@ def test_refusals(b):
         s = torch.ones((3, 2), device=DEV)
         b.dfa_cache_append(p["k"], p["v"], args[7], args[6], args[5], c, c, s, s, 2)
     torch.cuda.synchronize()
+    assert b.dfa_status() == 0
+
+
+def test_workspaces(b):
+    """Short tables need none; long ones one of the size that is asked for, which
+    is then all that is written."""
+    p = _problem([10], [2], 4, 2, 64, 16)
+    assert b.dfa_cache_workspace_bytes(1, 2, 2, 4, 2, 64, 16, p["table"].shape[1]) == 0
+    want = _run(b, p, 2)
+    for n in (0, 16):
+        got = _run(b, p, 2, workspace=torch.empty(n, dtype=torch.uint8, device=DEV))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for T, H in ((2, 4), (7, 8), (40, 8)):
+        p = _problem([5000, 3], [T, T], H, 2, 64, 16)
+        want = _run(b, p, 2)
+        n = b.dfa_cache_workspace_bytes(2, 2 * T, T, H, 2, 64, 16, p["table"].shape[1])
+        assert n > 0
+        with pytest.raises(b.DfaError):
+            _run(b, p, 2, workspace=torch.empty(n - 1, dtype=torch.uint8, device=DEV))
+        buf = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+        got = _run(b, p, 2, workspace=buf[:n])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert bool((buf[n:] == 0xA5).all())
     assert b.dfa_status() == 0
 
 

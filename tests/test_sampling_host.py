@@ -97,7 +97,7 @@ def _forward(lib, **kw):
 def test_forward_refusals(lib):
     for kw in (dict(q=NULL), dict(k=NULL), dict(v=NULL), dict(k=ODD), dict(kc=NULL), dict(vc=ODD),
                dict(ks=NULL), dict(vs=NULL), dict(table=NULL), dict(lens=NULL), dict(cu=NULL),
-               dict(out=ODD), dict(lse=NULL), dict(work=NULL), dict(work=ODD), dict(batch=-1),
+               dict(out=ODD), dict(lse=NULL), dict(work=ODD), dict(batch=-1),
                dict(batch=40000), dict(rows=-1), dict(max_new=-1), dict(heads=0),
                dict(kv_heads=3), dict(kv_heads=0), dict(kv_heads=8), dict(bs=0), dict(ps=8),
                dict(pages=0), dict(maxp=0), dict(maxp=1 << 27),
@@ -106,9 +106,10 @@ def test_forward_refusals(lib):
     assert _forward(lib, d=80) == EUNSUPPORTED
     for kw in (dict(batch=0), dict(rows=0), dict(max_new=0)):
         assert _forward(lib, **kw) == 0
-    assert lib.dfa_cache_workspace_bytes(1, 8, 8, 4, 3, 64) == EINVAL
-    assert lib.dfa_cache_workspace_bytes(1, 8, 8, 4, 2, 72) == EUNSUPPORTED
-    assert lib.dfa_cache_workspace_bytes(0, 8, 8, 4, 2, 64) == 0
+    assert lib.dfa_cache_workspace_bytes(1, 8, 8, 4, 3, 64, 16, 2) == EINVAL
+    assert lib.dfa_cache_workspace_bytes(1, 8, 8, 4, 2, 64, 24, 2) == EINVAL
+    assert lib.dfa_cache_workspace_bytes(1, 8, 8, 4, 2, 72, 16, 2) == EUNSUPPORTED
+    assert lib.dfa_cache_workspace_bytes(0, 8, 8, 4, 2, 64, 16, 2) == 0
 
 
 def test_binding_refusals():
