@@ -757,7 +757,8 @@ def dfa_cache_plan(cache_lens, new_lens, block_table, free_pages, free_count, pa
     if rows < 0:
         raise ValueError("rows must not be negative")
     buf = torch.empty(2 * B + 3 + rows, dtype=torch.int32, device=dev)
-    cu_new, next_lens, next_free, missing, positions = torch.split_with_sizes(
+    # integers, of which autograd keeps no versions: views without its bookkeeping
+    cu_new, next_lens, next_free, missing, positions = torch.unsafe_split_with_sizes(
         buf, (B + 1, B, 1, 1, rows))
     at = buf.data_ptr()
     _call("dfa_cache_plan", dev, cache_lens.data_ptr(), new_lens.data_ptr(),

@@ -348,6 +348,50 @@ def test_attention_short_tables(b, B, H, T, longest):
     _check(p, 8, out, lse)
 
 
+@pytest.mark.parametrize("B,d,H,Hk,T", [(2100, 64, 2, 1, 1), (700, 128, 4, 1, 3),
+                                        (600, 64, 16, 2, 7), (600, 128, 8, 1, 9),
+                                        (150, 128, 16, 1, 20), (300, 256, 8, 1, 9)])
+@pytest.mark.parametrize("longest", [0, 3000])
+def test_attention_many_small_requests(b, B, d, H, Hk, T, longest):
+    """Many pieces to a block, most of one tile: the rings and buffers turn over
+    with every piece; with a long request among them, cut."""
+    g = np.random.default_rng(B + d)
+    lens = g.integers(0, 140, B) * (g.random(B) < 0.9)
+    lens[B // 2] = longest
+    new = g.integers(0, T + 1, B)
+    new[B // 2] = T
+    p = _problem(lens.tolist(), new.tolist(), H, Hk, d, 32, seed=B)
+    out, lse = _run(b, p, 5)
+    assert b.dfa_status() == 0
+    _check(p, 5, out, lse)
+
+
+@pytest.mark.parametrize("d,H", [(64, 8), (128, 8), (128, 2), (256, 8)])
+@pytest.mark.parametrize("longest", [0, 3000])
+def test_own_values_that_are_not_finite_stay_with_their_rows(b, d, H, longest):
+    """Every seventh of many small requests has an infinite value: causal rows
+    that do not see it, of that request or another, are as without it."""
+    B, T = 300, 9
+    g = np.random.default_rng(d)
+    lens = g.integers(0, 140, B).tolist()
+    lens[5] = longest
+    p = _problem(lens, [T] * B, H, 1, d, 32, seed=d)
+    want = _run(b, p, 1)
+    sees = torch.zeros(B * T, dtype=torch.bool)
+    v = p["v"].clone()
+    for i in range(0, B, 7):
+        j = i % T
+        v[i * T + j, 0, 3] = float("inf")
+        sees[i * T + j:(i + 1) * T] = True
+    got = _run(b, dict(p, v=v), 1)
+    assert b.dfa_status() == 0
+    sees = sees.to(DEV)
+    assert torch.equal(got[0][~sees], want[0][~sees]) and torch.equal(got[1], want[1])
+    assert bool((got[0][sees][..., 3] == float("inf")).all())
+    rest = [i for i in range(d) if i != 3]
+    assert torch.equal(got[0][sees][..., rest], want[0][sees][..., rest])
+
+
 @pytest.mark.parametrize("H", [4, 32])
 @pytest.mark.parametrize("lens", [[0], [5], [0, 70, 0, 16], [1000, 0]])
 def test_attention_without_own_keys(b, lens, H):
