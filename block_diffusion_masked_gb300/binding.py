@@ -614,11 +614,15 @@ def _call(fn, device, *args):
 
 
 def _check_dense(t, shape, dtype, device, name):
-    """A contiguous input of the given shape."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
-            or t.device != device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {device}")
+    """A contiguous input of the given shape on a CUDA device."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device.index and t.shape == shape
+                and t.is_contiguous()):
+            return
+    except AttributeError:  # not a tensor
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                     f"on {device}")
 
 
 def _check_dims(t, dim, name):
