@@ -918,8 +918,10 @@ constexpr int kWholeKeys = 512;
 
 // The launch's shape for given sizes.
 //
-// tile_rows: query rows of a segment.  blocks: as many as are resident at once
-// (CacheTile::kResident).
+// tile_rows: query rows of a segment, the fewest that hold a request's rows, for
+// every tile reads the keys anew (headdim 256: 32 rows 127 us in a tile of 32,
+// 210 in one of 64; 64 rows 212 in one of 64, 222 in two of 32; headdim 64 and
+// 128: above).  blocks: as many as are resident at once (CacheTile::kResident).
 //
 // whole: segments are not cut.  Short tables are not worth it, for one unit a
 // segment needs no join (a launch) and no workspace: up to kWholeKeys keys, and
@@ -928,9 +930,9 @@ constexpr int kWholeKeys = 512;
 // 1000 keys 22.3 and 26.5; one request of 250 keys 9.1 and 9.8, of 500 12.0 and
 // 10.0 but for the second launch, of 1000 17.6 and 10.5.
 //
-// finish: units of 128 keys that a segment's end is taken to cost.  Too few, and blocks
-// with many ends finish last; too many, and blocks with few do.  Measured (us;
-// 32 ragged requests of up to 8192 tokens, a quarter of the heads for keys):
+// finish: units of 128 keys that a segment's end is taken to cost.  Too few, and
+// blocks with many ends finish last; too many, and blocks with few do.  Measured
+// (us; 32 ragged requests of up to 8192 tokens, a quarter of the heads for keys):
 //                      finish 3     4     6     8    10
 //   headdim 128,  16 rows    79    76    78    80    82
 //   headdim 128,  32 rows   137   130   116   111   113
@@ -955,7 +957,8 @@ CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, lon
   c.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : d == 256 ? 64 : 128;
   c.finish = d == 256 && c.tile_rows == 64 ? 4 : d < 256 && c.tile_rows == 16 ? 5 : 8;
   c.blocks = sms * (d == 256 || c.tile_rows == 128 ? 1 : d == 64 && c.tile_rows == 16 ? 3 : 2);
-  const long long segments = batch * kv_heads * ((rows - 1) / c.tile_rows + 1);
+  const long long segments =
+      static_cast<long long>(batch) * kv_heads * ((rows - 1) / c.tile_rows + 1);
   c.whole = keys <= kWholeKeys || (keys <= 2 * kWholeKeys && 2 * segments >= c.blocks);
   return c;
 }
