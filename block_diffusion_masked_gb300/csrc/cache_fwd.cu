@@ -85,8 +85,11 @@ struct CacheTile {
   static constexpr int kFrags = (D / 64) * 4;  // k steps of Q K^T
   static constexpr int kQ = WR * MT * kFrags * 512;
   static constexpr int kPitch = D + 4;   // floats per row of a group's output at the join
-  static constexpr int kHalfK = WK / 2;  // groups that keep an output at the join
-  static constexpr int kJoin = kHalfK * kRows * kPitch * 4;
+  // Outputs that are kept at the join: every group's where there is room (one
+  // token over 500: 11.7 us, 12.0 with half as many), else half as many, to
+  // which the other half of the groups adds.
+  static constexpr int kKept = kRows == 16 && D <= 128 ? WK : WK / 2;
+  static constexpr int kJoin = kKept * kRows * kPitch * 4;
   // ring (1024-byte aligned) | join | q fragments | row factors | statistics | barriers
   static constexpr int kOffJoin = kRing;
   static constexpr int kOffQ = kOffJoin + kJoin;
@@ -748,13 +751,12 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
   float c_all = s_c[0];
 #pragma unroll
   for (int i = 1; i < WK * WR; ++i) c_all = fmaxf(c_all, s_c[i]);
-  // The upper half of the groups leaves its outputs, the lower half adds its
-  // own to them.
+  // The last kKept groups leave their outputs, the others add theirs to them.
   float* join = reinterpret_cast<float*>(smem + T::kOffJoin);
 #pragma unroll 1
-  for (int turn = 0; turn < 2; ++turn) {
+  for (int turn = 0; turn < WK / T::kKept; ++turn) {
     const bool add = turn == 1;
-    if ((wk >= T::kHalfK) != add) {
+    if ((wk >= WK - T::kKept) != add) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
         const float f = m[mt][i] == -INFINITY ? 0.f : ex2_approx(m[mt][i] - top);
         const float fo = f * (c / c_all);
         if (t == 0) s_l[wk * T::kRows + r] = l[mt][i] * f;
-        float* dst = join + ((wk % T::kHalfK) * T::kRows + r) * T::kPitch;
+        float* dst = join + ((wk % T::kKept) * T::kRows + r) * T::kPitch;
         // columns 2t and 2t + 1 of the column tiles are runs of kCols dims
 #pragma unroll
         for (int half = 0; half < kHalf; ++half)
@@ -803,7 +805,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
       top = fmaxf(top, s_m[x * T::kRows + r]);
     }
 #pragma unroll
-    for (int x = 0; x < T::kHalfK; ++x) {
+    for (int x = 0; x < T::kKept; ++x) {
       const float4 y =
           *reinterpret_cast<const float4*>(join + (x * T::kRows + r) * T::kPitch + 4 * d4);
       a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
