@@ -632,10 +632,16 @@ def _check_dims(t, dim, name):
 
 
 def _check_heads(t, dim, name, device=None):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dim
-            or not t.is_cuda or (device is not None and t.device != device)):
-        where = "a CUDA device" if device is None else str(device)
-        raise ValueError(f"{name} must be a {dim}-dimensional bfloat16 tensor on {where}")
+    """A bf16 input of ``dim`` dimensions on a CUDA device; returns its shape."""
+    try:
+        shape = t.shape
+        if (t.dtype is torch.bfloat16 and len(shape) == dim
+                and (t.is_cuda if device is None else t.get_device() == device.index)):
+            return shape
+    except AttributeError:  # not a tensor
+        pass
+    where = "a CUDA device" if device is None else str(device)
+    raise ValueError(f"{name} must be a {dim}-dimensional bfloat16 tensor on {where}")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -688,8 +694,8 @@ def dfa_rotary(q, k, table, positions=None, period=None, interleaved=False, inve
 def _rotary_sizes(q, k, table, positions, period):
     """Check dfa_rotary's inputs; returns its integer arguments."""
     packed = isinstance(q, torch.Tensor) and q.dim() == 3
-    _check_heads(q, 3 if packed else 4, "q")
-    shape, dev = q.shape, q.device
+    shape = _check_heads(q, 3 if packed else 4, "q")
+    dev = q.device
     if packed:
         L, H, d = shape
         B = 1
@@ -697,14 +703,14 @@ def _rotary_sizes(q, k, table, positions, period):
         B, L, H, d = shape
     Hk = 0
     if k is not None:
-        _check_heads(k, 3 if packed else 4, "k", dev)
-        Hk = k.shape[-2]
-        if k.shape[:-2] != shape[:-2] or k.shape[-1] != d:
+        kshape = _check_heads(k, 3 if packed else 4, "k", dev)
+        Hk = kshape[-2]
+        if kshape[0] != shape[0] or kshape[-3] != L or kshape[-1] != d:
             raise ValueError("k must be (batch, seqlen, kv_heads, headdim) like q")
     max_pos, rot = _check_dims(table, 2, "table")
     _check_dense(table, (max_pos, rot), torch.float32, dev, "table")
     if positions is not None:
-        _check_dense(positions, shape[:-2], torch.int32, dev, "positions")
+        _check_dense(positions, (L,) if packed else (B, L), torch.int32, dev, "positions")
         period = 1
     elif packed:
         raise ValueError("packed rows need positions")
@@ -717,15 +723,16 @@ def _rotary_sizes(q, k, table, positions, period):
 
 def _rotary_launch(q, k, table, positions, sizes, flags, q_out=None, k_out=None):
     """dfa_rotary of tensors that _rotary_sizes (or a call like it) has checked."""
-    lead = 1 if len(q.shape) == 3 else 0  # packed rows: a batch of one
+    shape, dev = q.shape, q.device
+    lead = 1 if len(shape) == 3 else 0  # packed rows: a batch of one
     q_str, k_str, kp, kop = _strides(q, "q", lead), None, None, None
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
         k_str, kp, kop = _strides(k, "k", lead), k.data_ptr(), k_out.data_ptr()
-    _call("dfa_rotary", q.device, q.data_ptr(), kp, q_out.data_ptr(), kop, table.data_ptr(),
+    _call("dfa_rotary", dev, q.data_ptr(), kp, q_out.data_ptr(), kop, table.data_ptr(),
           None if positions is None else positions.data_ptr(), *sizes, q_str, k_str, flags)
     return q_out, k_out
 
@@ -804,13 +811,12 @@ def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_
 
     ``max_new``: a bound on the rows of one request, known to the host.
     """
-    _check_heads(k, 3, "k")
-    dev, shape = k.device, k.shape
-    rows, Hk, d = shape
-    _check_heads(v, 3, "v", dev)
+    rows, Hk, d = shape = _check_heads(k, 3, "k")
+    dev = k.device
+    vshape = _check_heads(v, 3, "v", dev)
     B, Hc, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
                                       cu_new, dev, d)
-    if v.shape != shape or Hc != Hk:
+    if vshape != shape or Hc != Hk:
         raise ValueError("k and v must be (rows, kv_heads, headdim) with the cache's heads")
     _call("dfa_cache_append", dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
           cache_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -844,9 +850,8 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
     bf16 and lse (H, rows) float32.  ``workspace``: a uint8 tensor of at least
     dfa_cache_workspace_bytes(...) bytes; by default one is allocated.
     """
-    _check_heads(q, 3, "q")
-    dev, shape = q.device, q.shape
-    rows, H, d = shape
+    rows, H, d = shape = _check_heads(q, 3, "q")
+    dev = q.device
     B, Hk, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
                                       cu_new, dev, d)
     if Hk < 1 or H % Hk:
@@ -855,9 +860,8 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
         raise ValueError("k and v go together")
     kp = vp = ks = vs = None
     if k is not None:
-        _check_heads(k, 3, "k", dev)
-        _check_heads(v, 3, "v", dev)
-        if k.shape != (rows, Hk, d) or v.shape != (rows, Hk, d):
+        own = (rows, Hk, d)
+        if _check_heads(k, 3, "k", dev) != own or _check_heads(v, 3, "v", dev) != own:
             raise ValueError("k and v must be (rows, kv_heads, headdim)")
         kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), _strides(k, "k"), _strides(v, "v")
     if out is None:
