@@ -69,7 +69,9 @@ def rotary_func(q, k, table, positions=None, interleaved=False, period=None):
     :func:`rotary_table`.  ``positions``: int32, a negative one marks a row
     that is not in use (its output is 0).  Without positions row r has
     position r mod ``period``; the default period L // 2 is the [noisy |
-    clean] layout, both halves counted from 0.
+    clean] layout, both halves counted from 0.  ``table`` gets no gradient.  A
+    backward pass is captured into a CUDA graph only while no eager graph of
+    the same leaves is alive (a rule of autograd's, for any function).
     """
     q = _strided(q)
     if k is not None:

@@ -114,6 +114,30 @@ def test_gradients_of_gradients(b):
     assert b.dfa_status() == 0
 
 
+def test_broadcast_inputs(b):
+    """A batch and heads that are one in memory: read in place, and their
+    gradient is the sum (float32 in between: half a bf16 step of each term, and
+    of each partial sum)."""
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(5, 64)
+    q = _randn((1, 10, 1, 64), 1).requires_grad_()
+    k = _randn((1, 10, 1, 64), 2).requires_grad_()
+    gq, gk = _randn((3, 10, 4, 64), 3), _randn((3, 10, 2, 64), 4)
+    y = rotary_func(q.expand(3, 10, 4, 64), k.expand(3, 10, 2, 64), table)
+    d = torch.autograd.grad(y, (q, k), (gq, gk))
+    assert b.dfa_status() == 0
+    pos = [0, 1, 2, 3, 4] * 2
+    for got, x, g, out in ((d[0], q, gq, y[0]), (d[1], k, gk, y[1])):
+        for i in range(3):
+            _check(out[i].detach(), x[0].detach().expand(out.shape[1:]), table, pos, False, False)
+        terms = np.stack([osam.rotary(_f64(g[i]), table.cpu().numpy(), pos, False, True)
+                          for i in range(3)])
+        want, size = terms.sum((0, 2)), np.abs(terms).sum((0, 2))
+        n = terms.shape[0] * terms.shape[2]
+        assert (np.abs(_f64(got)[0, :, 0] - want) <= 2.0 ** -8 * (n + 1) * size).all()
+
+
 def test_captured_forward_and_backward(b):
     from block_diffusion_masked_gb300 import rotary_func, rotary_table
 
