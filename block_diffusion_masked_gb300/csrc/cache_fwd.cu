@@ -395,6 +395,11 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
   float inv_c = pow2_bits(-kCacheMinExp);
   const uint8_t* qbase = smem + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
 
+  // A score's factor (the row's power of two times the page's scale) is never 0,
+  // be the row zero, the page zero or not there: 0 * -inf is not a number.  A
+  // raw score is below 2^33, so what is raised to kTiny adds less than 2^-93.
+  constexpr float kTiny = 1.1754944e-38f;  // 2^-126
+
   // Probabilities of a unit's raw scores sc (NT column tiles of 8 keys; -inf:
   // not seen), packed as the products' A operand: score factors row[.][.] times
   // f0 (first half of the column tiles) or f1, value weights w0 or w1 (times
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
               x = fmax3(x, sc[mt][n][2 * i], sc[mt][n][2 * i + 1]);
               y = fmax3(y, sc[mt][n + NT / 2][2 * i], sc[mt][n + NT / 2][2 * i + 1]);
             }
-            x = fmaxf(x * (row[mt][i] * f0), y * (row[mt][i] * f1));
+            x = fmaxf(x * fmaxf(row[mt][i] * f0, kTiny), y * fmaxf(row[mt][i] * f1, kTiny));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
             if (x > m[mt][i]) {
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
         for (int i = 0; i < 2; ++i) {
           // a row that has met no finite score keeps probabilities of 0
           const float ref = m[mt][i] == -INFINITY ? 0.f : kShift - m[mt][i];
-          const float g0 = row[mt][i] * f0, g1 = row[mt][i] * f1;
+          const float g0 = fmaxf(row[mt][i] * f0, kTiny), g1 = fmaxf(row[mt][i] * f1, kTiny);
           float s0 = 0.f, s1 = 0.f;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -480,8 +485,6 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
         }
     }
   };
-  constexpr float kTiny = 1.1754944e-38f;  // a factor that is never 0: 0 * -inf is not a number
-
   // Own keys and values first, bf16, with the segment's end, while the cached
   // keys are on their way: units of 16 keys, the groups in turn, operands
   // straight from global memory.
@@ -681,8 +684,8 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
               sc[mt][n][x] = -INFINITY;
     }
     uint4 pf[MT][2];
-    soften(std::integral_constant<int, 4>{}, std::true_type{}, sc, factor, fmaxf(ks0, kTiny),
-           fmaxf(ks1, kTiny), vs0, vs1, fmaxf(c, fmaxf(vs0, vs1)), false, pf);
+    soften(std::integral_constant<int, 4>{}, std::true_type{}, sc, factor, ks0, ks1, vs0, vs1,
+           fmaxf(c, fmaxf(vs0, vs1)), false, pf);
     // P V: the four keys of a thread's fragment rows, 16 dims each (headdim
     // 64: 8).  What lies behind the last key may be anything, NaN included,
     // and is replaced by zero.

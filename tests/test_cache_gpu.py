@@ -708,3 +708,70 @@ def test_long_offsets(b):
     ref, _, _, _ = osam.cache_attention(_f64(q), _f64(small[0]), _f64(small[1]), _f64(small[2]),
                                         _f64(small[3]), [[0, 1]], [200], [0, 4])
     assert np.abs(_f64(out) - ref).max() <= 2.0 ** -6 * np.abs(ref).max()
+
+
+# --------------------------------------------------- small, zero and large magnitudes
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16])
+@pytest.mark.parametrize("size", [2.0 ** -10, 2.0 ** -40, 2.0 ** -120, 0.0])
+def test_attention_of_small_and_zero_queries(b, d, H, size):
+    """Units of which a half or more is not there, pages of 16: a masked key has
+    no weight however small the row's scores are."""
+    p = _problem([5, 48, 97, 33], [4, 4, 4, 4], H, 1, d, 16, seed=20)
+    p["q"] *= size
+    p["q"][1] = 0
+    for own in (True, False):
+        if not own:
+            p["k"] = p["v"] = None
+        out, lse = _run(b, p, 2)
+        assert b.dfa_status() == 0
+        _check(p, 2, out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [2, 16])
+@pytest.mark.parametrize("zero", ["k", "qk", "qkv"])
+def test_sampler_on_zeros(b, d, H, zero):
+    """Zero queries, keys and values through append and attend: every key counts
+    alike, lse is the logarithm of their number."""
+    from block_diffusion_masked_gb300 import KVCache, PageTable
+
+    Hk, ps, new = 1, 64, [3, 5]
+    pages, cache = PageTable(2, 4, 8, ps), KVCache(8, ps, Hk, d)
+    g = torch.Generator("cpu").manual_seed(d + H)
+
+    def rand(name, rows, heads):
+        x = torch.randn((rows, heads, d), generator=g) * (name not in zero)
+        return x.to(torch.bfloat16).to(DEV)
+
+    step = pages.plan(_i32([37, 70]), 107, 70)
+    cache.append(rand("k", 107, Hk), rand("v", 107, Hk), step)
+    pages.advance(step)
+    step = pages.plan(_i32(new), 8, 5)
+    q, k, v = rand("q", 8, H), rand("k", 8, Hk), rand("v", 8, Hk)
+    for own in (True, False):
+        out, lse = cache.attend(q, step, *((k, v) if own else ()), block_size=64)
+        assert b.dfa_status() == 0
+        p = dict(table=step.block_table.cpu().numpy(), cu=[0, 3, 8], lens=[37, 70], new=new, q=q,
+                 k=k if own else None, v=v if own else None, kc=cache.k, vc=cache.v,
+                 ks=cache.k_scale, vs=cache.v_scale)
+        _check(p, 64, out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [2, 16])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -10, 0.0])
+@pytest.mark.parametrize("page", [-1, 10 ** 6])
+def test_attention_refused_pages_and_small_queries(b, d, H, size, page):
+    """Keys of a page that may not be followed count as masked: as if the request
+    did not hold them (own rows one block, so that positions do not matter)."""
+    p = _problem([100, 50], [4, 5], H, 1, d, 16, seed=21)
+    p["q"] *= size
+    table = p["table"].copy()
+    table[0, 2] = page
+    out, lse = _run(b, dict(p, table=table), 2 ** 20)
+    assert b.dfa_status() == b.DFA_EDEVICE
+    rest = p["table"].copy()
+    rest[0, 2:6] = p["table"][0, 3:7]
+    _check(dict(p, table=rest, lens=[84, 50]), 2 ** 20, out, lse)
