@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
         }
       uint4 pf[MT][1];
       soften(std::integral_constant<int, 2>{}, std::false_type{}, sc, row, 1.f, 1.f, 1.f, 1.f,
-             fmaxf(c, 1.f), true, pf);
+             fmaxf(c, kOwnUnit), true, pf);
       // A row's probability of an own key it does not see is 0, but 0 times a
       // value that is not finite is not: such values leave the product and
       // are added to the rows that see them.
@@ -601,6 +601,35 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
             }
         }
       }
+    }
+    // Cached probabilities are f16 and relative to the output's unit, which the
+    // pages' scales alone are to set: it comes down to the largest of the group's
+    // first units, but not so far that the own keys' output, in the new unit,
+    // would pass 2^100 (what cached keys lose to that is below 2^-100 of it).
+    if (16 * wk < own && my_units > 0) {
+      unsigned top = 0;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < kOut; ++e)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const unsigned y = __float_as_uint(o[mt][e][x]) & 0x7fffffffu;
+            top = max(top, y < 0x7f800000u ? y : 0u);
+          }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1])));
+      const int want = kOwnExp - max(static_cast<int>(most >> 23) - 127, kCacheMinExp);
+      const int down = max(min(127 + 99 - static_cast<int>(top >> 23), want), 0);
+      const float grow = pow2_bits(down);
+      c *= pow2_bits(-down);
+      inv_c *= grow;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < kOut; ++e)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[mt][e][x] *= grow;
     }
   }
 

@@ -260,6 +260,11 @@ __device__ __forceinline__ float pow2_bits(int e) { return __int_as_float((e + 1
 // kShift moves f16's smallest subnormal to 2^-30 of the reference.
 constexpr float kShift = 6.f;
 constexpr float kMostSum = 32768.f;
+// The output's unit for own keys.  Their probabilities are bf16 and lose nothing
+// to any unit; this one keeps float32 sums of 2^10 own values of 2^127, the
+// probabilities' 2^kShift included, from overflowing, and the bits of 2^-126.
+constexpr int kOwnExp = 16;
+constexpr float kOwnUnit = 1 << kOwnExp;
 
 // More than 32 query rows per key/value head, headdim 64 or 128 (tiles of 128
 // rows; the tensor maps' boxes are whole pages).

@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
             }
           }
         };
-        const float c_new = fmaxf(c, kKind == kOwn ? 1.f : info.vmax);
+        const float c_new = fmaxf(c, kKind == kOwn ? kOwnUnit : info.vmax);
         float shrink = 1.f;
         if (c_new != c) {
           shrink = c / c_new;

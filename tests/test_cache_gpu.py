@@ -775,3 +775,40 @@ def test_attention_refused_pages_and_small_queries(b, d, H, size, page):
     rest = p["table"].copy()
     rest[0, 2:6] = p["table"][0, 3:7]
     _check(dict(p, table=rest, lens=[84, 50]), 2 ** 20, out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16])
+@pytest.mark.parametrize("e", [-60, -30, 60])
+@pytest.mark.parametrize("many", [False, True])
+def test_attention_scales_with_its_values(b, d, H, e, many):
+    """The output is linear in the values: own ones and the pages' scales times a
+    power of two give the same bits times that power, whatever its size.  Short
+    tables, whose segments are not cut, and many requests beside a long one."""
+    lens, new = [300, 40, 0, 500], [4, 5, 3, 4]
+    if many:
+        g = np.random.default_rng(d + H)
+        lens, new = g.integers(0, 400, 150).tolist(), g.integers(0, 6, 150).tolist()
+        lens[7], new[7] = 3000, 5
+    p = _problem(lens, new, H, 1, d, 32, seed=22)
+    p["q"] *= 2.0 ** -5  # scores of about 1: every key counts
+    want = _run(b, p, 2)
+    got = _run(b, dict(p, v=p["v"] * 2.0 ** e, vs=p["vs"] * 2.0 ** e), 2)
+    assert b.dfa_status() == 0
+    assert torch.equal(got[0].double(), want[0].double() * 2.0 ** e)
+    assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16])
+@pytest.mark.parametrize("own,cached", [(0, -40), (-40, 0), (0, 100), (122, 0), (100, -90),
+                                        (122, -90), (-110, -90)])
+def test_attention_own_and_cached_values_of_different_sizes(b, d, H, own, cached):
+    """Own values of 2^own beside cached ones of 2^cached, over bf16's range; rows
+    that see next to nothing of their own among them (scores of up to 30)."""
+    p = _problem([300, 40, 0], [4, 5, 3], H, 1, d, 32, seed=23)
+    p["v"] *= 2.0 ** own
+    p["vs"] *= 2.0 ** cached
+    out, lse = _run(b, p, 2)
+    assert b.dfa_status() == 0
+    _check(p, 2, out, lse)
