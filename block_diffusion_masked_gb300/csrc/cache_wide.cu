@@ -112,7 +112,8 @@ struct WideCfg {
   };
   static constexpr int kOffTmem = kOffBar + NUM_BARS * 8;
   static constexpr int kOffAbort = kOffTmem + 4;
-  static constexpr int kOffOdd = kOffAbort + 4;  // [4]: own values that are not finite
+  static constexpr int kOffOdd = kOffAbort + 4;  // [4][4 warps]: own values that are not finite
+  static_assert(kOffOdd % 4 == 0, "a piece's notes are read as a word");
   static constexpr int kSmem = kOffOdd + 16 + 1024;
   // TMEM: two buffers of scores, two of probabilities, O
   static constexpr int kTmemP = 2 * BN, kTmemO = kTmemP + BN, kTmemCols = 512;
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (sbase - smem_u32(smem_raw));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffAbort);
-  volatile int* s_odd = reinterpret_cast<volatile int*>(smem + C::kOffOdd);
+  volatile unsigned char* s_odd = smem + C::kOffOdd;
   TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + C::kOffInfo);
   signed char* s_exp = reinterpret_cast<signed char*>(smem + C::kOffExp);
   const AbortFlag ab{const_cast<int*>(abort_flag), p.status};
@@ -166,7 +167,6 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     mbar_init(BAR(C::BAR_DRAIN), 2);
     fence_mbar_init();
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) s_odd[i] = 0;
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
   }
@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     bool ok = true;
     int n = 0, owns = 0;  // operand tiles, pieces with own keys
     int q = 0;            // versions of Q in f16
+    bool odd = false;     // the piece has own values that are not finite
     Ring<RS> at;
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
@@ -506,12 +507,9 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
           mbar_arrive_warp(BAR(rawempty + at.slot));
           at.next();
         } else {
-          if (isv && j == k.nc) {
-            // The notes of the last four pieces with own keys; this piece's
-            // was cleared with the one before it, its readers are long past
-            // the one that is cleared now.
+          if (j == k.nc) {
             ++owns;
-            if (c == 0) s_odd[(owns + 1) & 3] = 0;
+            odd = false;
           }
           copy_own(w, k, BN * (j - k.nc), dst);
         }
@@ -527,7 +525,14 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         }
         if (j >= k.nc) {
           copy16_wait();
-          if (isv && drop_odd(dst)) s_odd[owns & 3] = 1;
+          if (isv) {
+            // Each warp writes a note of its own, four to a piece with own keys,
+            // a word for each of the last four such pieces.  This tile's place
+            // was free when the products two tiles back were complete: the
+            // softmax has read out all such pieces but this and two before it.
+            odd = __any_sync(0xffffffffu, drop_odd(dst)) || odd;
+            if (lane == 0) s_odd[4 * (owns & 3) + cw] = odd;
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive_warp(BAR(full + b));
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         break;
       tc_fence_after();
       if (k.own > 0) ++owns;
-      const bool odd = k.own > 0 && s_odd[owns & 3] != 0;
+      const bool odd = k.own > 0 && *reinterpret_cast<volatile int*>(s_odd + 4 * (owns & 3)) != 0;
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       const bool none = m == -INFINITY && l == 0.f;
       const float inv = none ? 0.f : c / l;

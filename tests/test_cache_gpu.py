@@ -812,3 +812,27 @@ def test_attention_own_and_cached_values_of_different_sizes(b, d, H, own, cached
     out, lse = _run(b, p, 2)
     assert b.dfa_status() == 0
     _check(p, 2, out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [9, 16])
+def test_own_values_that_are_not_finite_in_first_steps(b, d, T):
+    """Empty caches: every piece is one tile of own keys, the next one's behind
+    it.  Each request but every third has an infinite value, at every row in turn."""
+    B, H = 1500, 8
+    p = _problem([0] * B, [T] * B, H, 1, d, 32, seed=d + T)
+    want = _run(b, p, 1)
+    v, sees = p["v"].clone(), torch.zeros((B, T), dtype=torch.bool)
+    for i in range(B):
+        if i % 3:
+            j = (i + i // 7) % T
+            v[i * T + j, 0, i % d] = float("inf")
+            sees[i, j:] = True
+    sees = sees.reshape(-1).to(DEV)
+    dim = (torch.arange(B, device=DEV) % d).repeat_interleave(T)
+    hit = (sees[:, None] & (torch.arange(d, device=DEV) == dim[:, None]))[:, None].expand(-1, H, d)
+    for _ in range(5):
+        got = _run(b, dict(p, v=v), 1)
+        assert bool((got[0][hit] == float("inf")).all())
+        assert torch.equal(got[0][~hit], want[0][~hit]) and torch.equal(got[1], want[1])
+    assert b.dfa_status() == 0
