@@ -1022,10 +1022,10 @@ cudaError_t launch_cache_rows(const CacheFwdParams& p, int tile_rows, cudaStream
 
 int check_cache_sizes(int batch, int rows, int max_new, int heads, int kv_heads, int headdim,
                       int page_size, int max_pages) {
+  const int most = max_new < rows ? max_new : rows;  // rows of one request
   if (batch < 0 || batch > 32768 || rows < 0 || rows > (1 << 30) || max_new < 0 ||
-      max_new > (1 << 24) || heads < 1 || heads > (1 << 16) || kv_heads < 1 || kv_heads > heads ||
-      heads % kv_heads ||
-      static_cast<long long>(max_new < rows ? max_new : rows) * (heads / kv_heads) > (1 << 30) ||
+      most > (1 << 24) || heads < 1 || heads > (1 << 16) || kv_heads < 1 || kv_heads > heads ||
+      heads % kv_heads || static_cast<long long>(most) * (heads / kv_heads) > (1 << 30) ||
       max_pages < 1 ||
       (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) ||
       static_cast<long long>(max_pages) * page_size > (1 << 30))

@@ -426,7 +426,8 @@ int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int 
  * bf16, strides as for the append; out (rows, heads, headdim) bf16 contiguous,
  * lse (heads, rows) float32.  A row that sees no key gets out 0 and lse -inf.
  * kv_heads divides heads, head h reads key/value head h / (heads / kv_heads).
- * batch <= 32768, and max_new times heads / kv_heads at most 2^30.
+ * batch <= 32768; the rows of one request, min(max_new, rows), are at most 2^24,
+ * and 2^30 over heads / kv_heads.  With max_new 0 nothing is read or written.
  * workspace: dfa_cache_workspace_bytes(...) bytes of device memory (16-byte
  * aligned; 0 for short tables, and then NULL will do) for the partial results
  * of long requests; calls that may run at the same time need workspaces of

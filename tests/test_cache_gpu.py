@@ -836,3 +836,14 @@ def test_own_values_that_are_not_finite_in_first_steps(b, d, T):
         assert bool((got[0][hit] == float("inf")).all())
         assert torch.equal(got[0][~hit], want[0][~hit]) and torch.equal(got[1], want[1])
     assert b.dfa_status() == 0
+
+
+@pytest.mark.parametrize("H", [2, 16])
+def test_loose_bounds_on_the_rows_of_a_request(b, H):
+    """max_new is an upper bound: one far above the rows changes nothing."""
+    p = _problem([700, 3], [5, 9], H, 1, 64, 32, seed=24)
+    want = _run(b, p, 4)
+    for bound in (14, 2 ** 24 + 1, 2 ** 31 - 1, 2 ** 40):
+        got = _run(b, dict(p, new=[bound]), 4)
+        assert b.dfa_status() == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -276,3 +276,14 @@ def test_oracle_cache_attention_is_the_training_mask():
                                              [start], [0, bs], noisy[1][sl], noisy[2][sl], bs)
         assert np.abs(out - ref[0, sl]).max() < 1e-12
         assert np.abs(l2 - lse[0, :, sl]).max() < 1e-12
+
+
+def test_forward_bounds_on_the_rows_of_a_request(lib):
+    """The limit holds for the rows there can be, not for a loose bound on them.
+    (Sizes are looked at before the head dimension, which is refused here.)"""
+    for m in (1 << 24, (1 << 24) + 1, (1 << 31) - 1):
+        assert _forward(lib, max_new=m, d=80) == EUNSUPPORTED
+        assert lib.dfa_cache_workspace_bytes(1, 8, m, 4, 2, 72, 16, 2) == EUNSUPPORTED
+    for rows, m in (((1 << 24) + 1, (1 << 24) + 1), (1 << 30, (1 << 31) - 1)):
+        assert _forward(lib, heads=1, kv_heads=1, rows=rows, max_new=m, d=80) == EINVAL
+        assert lib.dfa_cache_workspace_bytes(1, rows, m, 1, 1, 72, 16, 2) == EINVAL
