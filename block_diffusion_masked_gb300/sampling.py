@@ -70,7 +70,7 @@ class Step:
     """One sampling step's rows (see ``dfa_cache_plan``).
 
     ``cache_lens`` and ``block_table`` are the page table's own tensors: a step
-    is over once :meth:`PageTable.advance` has run.
+    is over once :meth:`PageTable.advance` or :meth:`PageTable.release` has run.
     """
 
     cu_new: torch.Tensor      # (batch + 1,) first row of each request
@@ -81,6 +81,7 @@ class Step:
     next_free: torch.Tensor
     missing: torch.Tensor     # (1,) pages that were not to be had
     max_new: int
+    turn: int = 0             # the page table's at the plan; negative: at the advance
 
 
 class PageTable:
@@ -96,6 +97,7 @@ class PageTable:
         self.cache_lens = torch.zeros(batch, **i32)
         self.free_pages = torch.arange(num_pages, **i32).flip(0).contiguous()
         self.free_count = torch.full((1,), num_pages, **i32)
+        self._turn = 1  # counts what makes planned steps stale: advance, release
 
     def plan(self, new_lens, rows, max_new):
         """Pages and positions for ``new_lens`` (int32 (batch,)) more tokens in
@@ -105,16 +107,29 @@ class PageTable:
                                      self.free_count, self.page_size, rows)
         table, cu_new, positions, next_lens, next_free, missing = got
         return Step(cu_new, positions, self.cache_lens, table, next_lens, next_free, missing,
-                    max_new)
+                    max_new, self._turn)
 
     def advance(self, step):
         """The step's tokens are in the caches: they count as held from now on.
-        Copied in place, so captured graphs see the new lengths."""
+        Copied in place, so captured graphs see the new lengths.
+
+        A step that was planned before the last :meth:`advance` or :meth:`release`
+        is refused: its lengths and free pages are not the table's any more.
+        (Graphs are not looked into: a release between the replay of a plan and
+        that of its advance loses pages.)"""
+        if step.turn == self._turn:
+            self._turn += 1
+            step.turn = -self._turn
+        elif step.turn != -self._turn:  # nor the one whose advance came last
+            raise ValueError("the step was planned before the last advance or release: "
+                             "plan it again")
         self.cache_lens.copy_(step.next_lens)
         self.free_count.copy_(step.next_free)
 
     def release(self, finished):
-        """Requests with finished != 0 (int32 (batch,)) give their pages back."""
+        """Requests with finished != 0 (int32 (batch,)) give their pages back.
+        Steps that are planned and not advanced are over: plan them again."""
+        self._turn += 1
         binding.dfa_cache_release(finished, self.cache_lens, self.block_table, self.free_pages,
                                   self.free_count, self.page_size)
 

@@ -392,7 +392,9 @@ int dfa_cache_plan(const int *cache_lens, const int *new_lens, int *block_table,
 
 /*
  * Requests with finished[b] != 0 (int32) give their pages back: pushed on the
- * stack in order, their table entries set to -1, their cache_lens to 0.
+ * stack in order, their table entries set to -1, their cache_lens to 0.  What a
+ * plan before it wrote to next_lens and next_free is stale then: taking it over
+ * would lose the pages given back.
  */
 int dfa_cache_release(const int *finished, int *cache_lens, int *block_table, int *free_pages,
                       int *free_count, int batch, int max_pages, int num_free, int page_size,

@@ -847,3 +847,21 @@ def test_loose_bounds_on_the_rows_of_a_request(b, H):
         got = _run(b, dict(p, new=[bound]), 4)
         assert b.dfa_status() == 0
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_release_between_plan_and_advance(b):
+    """The planned step is refused; planned again, no page is lost and the released
+    request begins anew."""
+    from block_diffusion_masked_gb300 import PageTable
+
+    pages = PageTable(2, 8, 12, 16)
+    pages.advance(pages.plan(_i32([40, 20]), 60, 40))
+    step = pages.plan(_i32([16, 16]), 32, 16)
+    pages.release(_i32([1, 0]))
+    with pytest.raises(ValueError):
+        pages.advance(step)
+    pages.advance(pages.plan(_i32([5, 16]), 21, 16))
+    assert b.dfa_status() == 0
+    assert pages.cache_lens.tolist() == [5, 36] and int(pages.free_count) == 12 - 1 - 3
+    held = pages.block_table[0, :1].tolist() + pages.block_table[1, :3].tolist()
+    assert sorted(held + pages.free_pages[:8].tolist()) == list(range(12))

@@ -287,3 +287,36 @@ def test_forward_bounds_on_the_rows_of_a_request(lib):
     for rows, m in (((1 << 24) + 1, (1 << 24) + 1), (1 << 30, (1 << 31) - 1)):
         assert _forward(lib, heads=1, kv_heads=1, rows=rows, max_new=m, d=80) == EINVAL
         assert lib.dfa_cache_workspace_bytes(1, rows, m, 1, 1, 72, 16, 2) == EINVAL
+
+
+# ------------------------------------------------------------- steps of a page table
+
+def test_stale_steps_are_refused(monkeypatch):
+    """advance takes over a plan's lengths and free pages, so nothing may have
+    changed them since: a release, or another step's advance."""
+    from block_diffusion_masked_gb300 import PageTable, sampling
+
+    def plan(lens, new, table, free, count, ps, rows):
+        return table, None, None, lens + new, count - 1, None
+
+    calls = []
+    monkeypatch.setattr(sampling.binding, "dfa_cache_plan", plan)
+    monkeypatch.setattr(sampling.binding, "dfa_cache_release", lambda *a: calls.append(a))
+    pages = PageTable(2, 4, 8, 16, device="cpu")
+    new = torch.tensor([3, 1], dtype=torch.int32)
+    step = pages.plan(new, 4, 3)
+    again = pages.plan(new, 4, 3)  # the same step may be planned again
+    pages.advance(again)
+    pages.advance(again)           # and advanced again: nothing changes
+    assert pages.cache_lens.tolist() == [3, 1] and pages.free_count.item() == 7
+    with pytest.raises(ValueError):
+        pages.advance(step)
+    step = pages.plan(new, 4, 3)
+    pages.release(new)
+    assert len(calls) == 1
+    for stale in (step, again):
+        with pytest.raises(ValueError):
+            pages.advance(stale)
+    assert pages.cache_lens.tolist() == [3, 1] and pages.free_count.item() == 7
+    pages.advance(pages.plan(new, 4, 3))
+    assert pages.cache_lens.tolist() == [6, 2] and pages.free_count.item() == 6
