@@ -12,6 +12,7 @@ log-sum-exp, and the backward recomputes from them (section 4.5 of
 from __future__ import annotations
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from . import binding
 
@@ -28,14 +29,34 @@ def _strided(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _followed():
+    """Whether autograd follows what is computed: backward, or with tangents."""
+    return torch.is_grad_enabled() or forward_ad._current_level >= 0
+
+
 class RotaryFunc(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, table, positions, period, flags):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(table, positions)
+        ctx.save_for_forward(table, positions)
         sizes = binding._rotary_sizes(q, k, table, positions, period)
-        ctx.how = sizes, flags
+        ctx.how, ctx.has_k = (sizes, flags), k is not None
         return binding._rotary_launch(q, k, table, positions, sizes, flags)
+
+    @staticmethod
+    def jvp(ctx, tq, tk, *_):
+        # The map is linear: a tangent turns as its input does, or stays zero.
+        table, positions = ctx.saved_tensors
+        (_, _, period, heads, kv_heads, d, _, _), flags = ctx.how
+        if tq is None:
+            yq = tk.new_zeros((*tk.shape[:-2], heads, d))
+            return yq, RotaryFunc.apply(_strided(tk), None, table, positions, period, flags)[0]
+        yq, yk = RotaryFunc.apply(_strided(tq), None if tk is None else _strided(tk), table,
+                                  positions, period, flags)
+        if tk is None and ctx.has_k:
+            yk = tq.new_zeros((*tq.shape[:-2], kv_heads, d))
+        return yq, yk
 
     @staticmethod
     def backward(ctx, dq, dk):
@@ -43,7 +64,7 @@ class RotaryFunc(torch.autograd.Function):
         table, positions = ctx.saved_tensors
         sizes, flags = ctx.how
         flags ^= binding.DFA_ROTARY_INVERSE
-        if torch.is_grad_enabled():  # the gradients are to have gradients: linear again
+        if _followed():  # the gradients are to have gradients: linear again
             if dq is not None:
                 dq, dk = RotaryFunc.apply(_strided(dq), None if dk is None else _strided(dk),
                                           table, positions, sizes[2], flags)
@@ -61,7 +82,8 @@ class RotaryFunc(torch.autograd.Function):
 
 
 def rotary_func(q, k, table, positions=None, interleaved=False, period=None):
-    """Rotary positions of queries and keys; differentiable.
+    """Rotary positions of queries and keys; differentiable, backward and with
+    tangents (``torch.autograd.forward_ad``).
 
     q (B, L, H, d) and k (B, L, Hk, d), or packed (rows, heads, d) with
     ``positions`` (rows,); bf16, strided views (the slices of a fused
@@ -77,7 +99,8 @@ def rotary_func(q, k, table, positions=None, interleaved=False, period=None):
     if k is not None:
         k = _strided(k)
     flags = binding.DFA_ROTARY_CLEAR | (binding.DFA_ROTARY_INTERLEAVED if interleaved else 0)
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and (
+            q.requires_grad or (k is not None and k.requires_grad)):
         return RotaryFunc.apply(q, k, table, positions, period, flags)
     return binding._rotary_launch(q, k, table, positions,
                                   binding._rotary_sizes(q, k, table, positions, period), flags)

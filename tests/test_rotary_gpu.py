@@ -274,3 +274,57 @@ def test_attention_with_positions(b, kind):
     err = (g1[0].float() - g2[0].float()).abs().max() / g2[0].float().abs().max()
     assert float(err) <= 2 * 2.0 ** -8
     assert b.dfa_status() == 0
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_forward_mode_tangents(b, packed):
+    """A tangent turns like its input: the map is linear.  q and k, either alone,
+    and beside a backward pass of the tangent."""
+    import torch.autograd.forward_ad as fwad
+
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(5, 64)
+    q, k, tq, tk = (_randn((1, 10, h, 64), s) for s, h in enumerate((3, 1, 3, 1)))
+    pos, at = None, list(range(5)) * 2
+    if packed:
+        at = [0, 4, 2, 2, 1, 0, 3, 3, 4, 1]
+        pos = torch.tensor(at, dtype=torch.int32, device="cuda")
+        q, k, tq, tk = q[0], k[0], tq[0], tk[0]
+
+    def rows(x):
+        return x if packed else x[0]
+
+    for with_q, with_k in ((True, True), (True, False), (False, True)):
+        with fwad.dual_level():
+            a = fwad.make_dual(q, tq) if with_q else q
+            c = fwad.make_dual(k, tk) if with_k else k
+            (yq, dyq), (yk, dyk) = (fwad.unpack_dual(y) for y in rotary_func(a, c, table, pos))
+        for y, x in ((yq, q), (yk, k)):
+            _check(rows(y), rows(x), table, at, False)
+        if with_q:
+            _check(rows(dyq), rows(tq), table, at, False)
+        else:
+            assert dyq is None or not dyq.any()
+        if with_k:
+            _check(rows(dyk), rows(tk), table, at, False)
+        else:
+            assert dyk is None or not dyk.any()
+    with fwad.dual_level():  # q alone
+        y, none = rotary_func(fwad.make_dual(q, tq), None, table, pos)
+        assert none is None
+        _check(rows(fwad.unpack_dual(y).tangent), rows(tq), table, at, False)
+    # the gradient's tangent, and the gradient of a tangent
+    x = q.clone().requires_grad_()
+    with fwad.dual_level():
+        y, _ = rotary_func(x, k, table, pos)
+        (dx,) = torch.autograd.grad(y, x, fwad.make_dual(q, tq))
+        primal, tangent = fwad.unpack_dual(dx)
+    _check(rows(primal), rows(q), table, at, False, True)
+    _check(rows(tangent), rows(tq), table, at, False, True)
+    t = tq.clone().requires_grad_()
+    with fwad.dual_level():
+        y, _ = rotary_func(fwad.make_dual(q, t), k, table, pos)
+        (dt,) = torch.autograd.grad(fwad.unpack_dual(y).tangent, t, q)
+    _check(rows(dt), rows(q), table, at, False, True)
+    assert b.dfa_status() == 0
