@@ -64,6 +64,10 @@ class RotaryFunc(torch.autograd.Function):
         table, positions = ctx.saved_tensors
         sizes, flags = ctx.how
         flags ^= binding.DFA_ROTARY_INVERSE
+        if not ctx.needs_input_grad[0]:
+            dq = None
+        if not ctx.needs_input_grad[1]:
+            dk = None
         if _followed():  # the gradients are to have gradients: linear again
             if dq is not None:
                 dq, dk = RotaryFunc.apply(_strided(dq), None if dk is None else _strided(dk),

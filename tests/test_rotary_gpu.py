@@ -328,3 +328,19 @@ def test_forward_mode_tangents(b, packed):
         (dt,) = torch.autograd.grad(fwad.unpack_dual(y).tangent, t, q)
     _check(rows(dt), rows(q), table, at, False, True)
     assert b.dfa_status() == 0
+
+
+@pytest.mark.parametrize("frozen", ["q", "k"])
+def test_gradients_beside_a_frozen_input(b, frozen):
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(5, 64)
+    q, k = _randn((1, 10, 3, 64), 1), _randn((1, 10, 1, 64), 2)
+    gq, gk = _randn(q.shape, 3), _randn(k.shape, 4)
+    x, g = (k, gk) if frozen == "q" else (q, gq)
+    x.requires_grad_()
+    y = rotary_func(q, k, table)
+    torch.autograd.backward(y, (gq, gk))
+    assert (q.grad is None) == (frozen == "q") and (k.grad is None) == (frozen == "k")
+    _check(x.grad[0], g[0], table, list(range(5)) * 2, False, True)
+    assert b.dfa_status() == 0

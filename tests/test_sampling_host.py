@@ -320,3 +320,34 @@ def test_stale_steps_are_refused(monkeypatch):
     assert pages.cache_lens.tolist() == [3, 1] and pages.free_count.item() == 7
     pages.advance(pages.plan(new, 4, 3))
     assert pages.cache_lens.tolist() == [6, 2] and pages.free_count.item() == 6
+
+
+# ------------------------------------------------------------- the rotary autograd function
+
+@pytest.mark.parametrize("frozen", ["q", "k", None])
+def test_rotary_backward_leaves_frozen_inputs_out(monkeypatch, frozen):
+    """No gradient is read or written for an input that needs none."""
+    from block_diffusion_masked_gb300 import autograd
+
+    launches = []
+
+    def launch(q, k, table, positions, sizes, flags):
+        launches.append((tuple(q.shape), None if k is None else tuple(k.shape), sizes[3:5]))
+        return q.clone(), None if k is None else k.clone()
+
+    monkeypatch.setattr(autograd.binding, "_rotary_sizes",
+                        lambda q, k, *a: (1, 4, 2, q.shape[2], k.shape[2], 64, 64, 2))
+    monkeypatch.setattr(autograd.binding, "_rotary_launch", launch)
+    q, k = (torch.randn(1, 4, h, 64, dtype=torch.bfloat16).requires_grad_() for h in (3, 1))
+    if frozen:
+        (q if frozen == "q" else k).requires_grad_(False)
+    yq, yk = autograd.rotary_func(q, k, torch.zeros(2, 64))
+    (yq.sum() + yk.sum()).backward()
+    assert (q.grad is None) == (frozen == "q") and (k.grad is None) == (frozen == "k")
+    assert len(launches) == 2
+    shapes, heads = launches[1][:2], launches[1][2]
+    if frozen is None:
+        assert shapes == (q.shape, k.shape) and heads == (3, 1)
+    else:
+        x = k if frozen == "q" else q
+        assert shapes == (x.shape, None) and heads == (x.shape[2], 0)
