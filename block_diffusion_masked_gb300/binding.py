@@ -593,7 +593,14 @@ def dfa_bwd_dq_convert(dq_acc, dq, mode=MODE_DIFFUSION):
 # the checks read attributes only, and the device is made current only where
 # it is not.
 
-_INT_MAX = (1 << 31) - 1  # larger arguments stand for it: ctypes would wrap them
+_INT_MAX = (1 << 31) - 1
+
+
+def _int32(x):
+    """An integer argument in 32 bits, which ctypes would wrap it to: one past them
+    is the largest, and any negative one, which no entry point takes, -1."""
+    return max(min(int(x), _INT_MAX), -1)
+
 
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -718,7 +725,7 @@ def _rotary_sizes(q, k, table, positions, period):
         if L % 2:
             raise ValueError("the sequence must be [noisy | clean] with an even length 2n")
         period = max(L // 2, 1)
-    return B, L, int(period), H, Hk, d, rot, max_pos
+    return B, L, _int32(period), H, Hk, d, rot, max_pos
 
 
 def _rotary_launch(q, k, table, positions, sizes, flags, q_out=None, k_out=None):
@@ -765,8 +772,8 @@ def dfa_cache_plan(cache_lens, new_lens, block_table, free_pages, free_count, pa
     dev, B, maxp, F = _check_pages(cache_lens, new_lens, block_table, free_pages, free_count,
                                    "new_lens")
     rows = int(rows)
-    if rows < 0:
-        raise ValueError("rows must not be negative")
+    if not 0 <= rows <= 1 << 30:
+        raise ValueError("rows must be 0 to 2^30")
     buf = torch.empty(2 * B + 3 + rows, dtype=torch.int32, device=dev)
     # integers, of which autograd keeps no versions: views without its bookkeeping
     cu_new, next_lens, next_free, missing, positions = torch.unsafe_split_with_sizes(
@@ -775,7 +782,7 @@ def dfa_cache_plan(cache_lens, new_lens, block_table, free_pages, free_count, pa
     _call("dfa_cache_plan", dev, cache_lens.data_ptr(), new_lens.data_ptr(),
           block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at,
           at + 4 * (2 * B + 3), at + 4 * (B + 1), at + 4 * (2 * B + 1), at + 4 * (2 * B + 2), B,
-          maxp, F, int(page_size), rows)
+          maxp, F, _int32(page_size), rows)
     return block_table, cu_new, positions, next_lens, next_free, missing
 
 
@@ -785,7 +792,7 @@ def dfa_cache_release(finished, cache_lens, block_table, free_pages, free_count,
                                    "finished")
     _call("dfa_cache_release", dev, finished.data_ptr(), cache_lens.data_ptr(),
           block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), B, maxp, F,
-          int(page_size))
+          _int32(page_size))
 
 
 def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new, dev, d):
@@ -820,15 +827,15 @@ def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_
         raise ValueError("k and v must be (rows, kv_heads, headdim) with the cache's heads")
     _call("dfa_cache_append", dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
           cache_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          k_scale.data_ptr(), v_scale.data_ptr(), B, rows, min(int(max_new), _INT_MAX),
-          Hk, d, ps, P, maxp, _strides(k, "k"), _strides(v, "v"))
+          k_scale.data_ptr(), v_scale.data_ptr(), B, rows, _int32(max_new), Hk,
+          d, ps, P, maxp, _strides(k, "k"), _strides(v, "v"))
 
 
 def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim, page_size,
                               max_pages):
     """Bytes of workspace dfa_cache_forward needs on the current device (0: none)."""
-    n = lib().dfa_cache_workspace_bytes(batch, rows, int(max_new), heads, kv_heads, headdim,
-                                        page_size, max_pages)
+    n = lib().dfa_cache_workspace_bytes(*map(_int32, (batch, rows, max_new, heads, kv_heads, headdim,
+                                                      page_size, max_pages)))
     if n < 0:
         raise DfaError("dfa_cache_workspace_bytes", int(n))
     return int(n)
@@ -872,7 +879,7 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
         lse = torch.empty((H, rows), dtype=torch.float32, device=dev)
     else:
         _check_dense(lse, (H, rows), torch.float32, dev, "lse")
-    max_new = min(int(max_new), _INT_MAX)
+    max_new = _int32(max_new)
     if workspace is None:
         nwork = _workspace_bytes(dev.index, B, rows, max_new, H, Hk, d, ps, maxp)
         if nwork:
@@ -883,8 +890,8 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
     _call("dfa_cache_forward", dev, q.data_ptr(), kp, vp, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
           cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          None if workspace is None else workspace.data_ptr(), nwork, B, rows, max_new, H, Hk, d, min(int(block_size), _INT_MAX), ps, P, maxp,
-          _strides(q, "q"), ks, vs)
+          None if workspace is None else workspace.data_ptr(), nwork, B, rows, max_new, H, Hk, d,
+          _int32(block_size), ps, P, maxp, _strides(q, "q"), ks, vs)
     return out, lse
 
 

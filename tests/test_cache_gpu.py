@@ -865,3 +865,23 @@ def test_release_between_plan_and_advance(b):
     assert pages.cache_lens.tolist() == [5, 36] and int(pages.free_count) == 12 - 1 - 3
     held = pages.block_table[0, :1].tolist() + pages.block_table[1, :3].tolist()
     assert sorted(held + pages.free_pages[:8].tolist()) == list(range(12))
+
+
+def test_arguments_past_32_bits(b):
+    """Page sizes, rows and bounds past 32 bits are refused, not wrapped."""
+    p = _problem([10], [2], 4, 2, 64, 16)
+    for bound in (-1, -2 ** 32 + 2):
+        with pytest.raises(b.DfaError):
+            _run(b, dict(p, new=[bound]), 2)
+        with pytest.raises(b.DfaError):
+            b.dfa_cache_append(p["k"], p["v"], _i32(p["cu"]), _i32([10]), _i32(p["table"]), p["kc"],
+                               p["vc"], p["ks"], p["vs"], bound)
+    with pytest.raises(b.DfaError):
+        _run(b, p, -2 ** 32 + 2)
+    state = (_i32([0]), _i32([1]), _i32([[-1]]), _i32([0]), _i32([1]))
+    for ps, rows in ((2 ** 32 + 16, 4), (16, 2 ** 32 + 4), (16, -2 ** 32 + 4)):
+        with pytest.raises((ValueError, b.DfaError)):
+            b.dfa_cache_plan(*state, ps, rows)
+    with pytest.raises(b.DfaError):
+        b.dfa_cache_release(state[1], state[0], *state[2:], 2 ** 32 + 16)
+    assert b.dfa_status() == 0

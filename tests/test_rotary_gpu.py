@@ -344,3 +344,20 @@ def test_gradients_beside_a_frozen_input(b, frozen):
     assert (q.grad is None) == (frozen == "q") and (k.grad is None) == (frozen == "k")
     _check(x.grad[0], g[0], table, list(range(5)) * 2, False, True)
     assert b.dfa_status() == 0
+
+
+def test_periods_past_32_bits(b):
+    """A period above the rows leaves their positions, however large it is; one
+    below 1 is refused, however small."""
+    from block_diffusion_masked_gb300 import rotary_func, rotary_table
+
+    table = rotary_table(16, 64)
+    x = _randn((1, 16, 2, 64), 12)
+    want, _ = b.dfa_rotary(x, None, table, period=16)
+    for period in (17, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 40 + 1):
+        assert torch.equal(b.dfa_rotary(x, None, table, period=period)[0], want)
+        assert torch.equal(rotary_func(x, None, table, period=period)[0], want)
+    for period in (0, -1, -2 ** 32 + 5, -2 ** 40 + 16):
+        with pytest.raises(b.DfaError):
+            b.dfa_rotary(x, None, table, period=period)
+    assert b.dfa_status() == 0

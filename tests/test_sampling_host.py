@@ -351,3 +351,19 @@ def test_rotary_backward_leaves_frozen_inputs_out(monkeypatch, frozen):
     else:
         x = k if frozen == "q" else q
         assert shapes == (x.shape, None) and heads == (x.shape[2], 0)
+
+
+def test_arguments_past_32_bits():
+    """They are not wrapped to arguments that would be taken."""
+    from block_diffusion_masked_gb300 import binding as b
+
+    assert b._int32(2 ** 32 + 5) == b._int32(2 ** 40) == 2 ** 31 - 1
+    assert b._int32(-2 ** 32 + 5) == b._int32(-2 ** 40) == -1 and b._int32(7) == 7
+    good = [1, 8, 8, 4, 2, 64, 16, 2]
+    for i, x in ((0, -2 ** 32 + 1), (1, 2 ** 32 + 8), (2, -2 ** 32 + 8), (3, 2 ** 32 + 4),
+                 (4, 2 ** 32 + 2), (6, 2 ** 32 + 16), (7, 2 ** 32 + 2)):
+        bad = list(good)
+        bad[i] = x
+        with pytest.raises(b.DfaError) as e:
+            b.dfa_cache_workspace_bytes(*bad)
+        assert e.value.code == b.DFA_EINVAL, i
