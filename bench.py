@@ -120,11 +120,15 @@ def measured_peaks():
 # ------------------------------------------------------------------ kernels and traffic
 
 # The translation unit that defines each kernel; a kernel's identity for the
-# traffic records is the hash of that file and of the shared headers.
+# traffic records is the hash of that file and of the headers it includes.
 KERNEL_SOURCES = {
     "dfa_fwd2_kernel": "fwd2.cu",
     "dfa_fwd_kernel": "fwd.cu",
     "dfa_bwd2_kernel": "bwd2.cu",
+    "dfa_rotary_kernel": "rotary.cu",
+    "dfa_cache_append_kernel": "cache.cu",
+    "dfa_cache_fwd_kernel": "cache_fwd.cu",
+    "dfa_cache_wide_kernel": "cache_wide.cu",
 }
 
 
@@ -135,13 +139,22 @@ def kernel_names(d):
     return fwd, bwd
 
 
+def source_files(source):
+    """A translation unit of csrc/ and the .cuh files it includes, by name."""
+    headers, todo = set(), [source]
+    while todo:
+        with open(os.path.join(CSRC, todo.pop()), encoding="utf-8") as f:
+            found = set(re.findall(r'^\s*#\s*include\s+"([^"]+\.cuh)"', f.read(), re.M))
+        todo += found - headers
+        headers |= found
+    return [os.path.join(CSRC, f) for f in [source, *sorted(headers)]]
+
+
 def source_hash(kernel):
-    """sha256 over the kernel's own .cu file and every shared header."""
-    base = kernel.split("<")[0]
-    files = [os.path.join(CSRC, KERNEL_SOURCES[base])]
-    files += sorted(glob.glob(os.path.join(CSRC, "*.cuh")))
+    """sha256 over the kernel's own .cu file and the headers it includes, directly
+    or through one another, in the order of their names."""
     h = hashlib.sha256()
-    for f in files:
+    for f in source_files(KERNEL_SOURCES[kernel.split("<")[0]]):
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode() + b"\0" + fh.read())
     return h.hexdigest()[:16]

@@ -9,6 +9,7 @@
 #include <cstring>
 #include <vector>
 
+#include "device.cuh"
 #include "dfa.h"
 #include "geometry.cuh"
 #include "params.cuh"

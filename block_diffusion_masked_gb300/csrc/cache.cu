@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "cache.cuh"
+#include "device.cuh"
 #include "dfa.h"
 #include "params.cuh"
 #include "sm100.cuh"

@@ -51,6 +51,7 @@
 #include <type_traits>
 
 #include "cache_fwd.cuh"
+#include "device.cuh"
 #include "dfa.h"
 
 namespace dfa {

@@ -193,17 +193,7 @@ cudaError_t launch_chained(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
 // destroyed and re-created.  record_cuda_failure: remember a failing CUDA
 // call for dfa_last_cuda_error and return DFA_ECUDA.  check_backward_args:
 // the shape checks of dfa_backward.
-// device_info: the same check, and the current device's status word and SM
-// count.  encode_map_u8: a tensor map of a byte array (a null pointer, an
-// alignment or an extent the driver refuses: DFA_ECUDA).
 int check_device(unsigned long long* ctx_id);
-struct DeviceInfo {
-  unsigned* status;
-  int sms;
-};
-int device_info(DeviceInfo* info);
-int encode_map_u8(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
-                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 int record_cuda_failure(cudaError_t e);
 int check_backward_args(int B, int n, int H, int d, int bs);
 

@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "device.cuh"
 #include "dfa.h"
 #include "params.cuh"
 #include "sm100.cuh"

@@ -71,3 +71,30 @@ def test_max_over_ranks_gloo_world_2():
 def test_single_rank_is_identity():
     assert bench.max_over_ranks([3.0, 4.0]) == [3.0, 4.0]
     assert bench.job_tflops(2e12, 1000.0, 1) == 2.0
+
+
+def test_source_hash_covers_what_a_kernel_includes(tmp_path, monkeypatch):
+    """The headers that its source includes, one through another, and no others:
+    a record of a kernel's traffic outlives a header of other kernels."""
+    (tmp_path / "k.cu").write_text('#include <cuda.h>\n#include "b.cuh"\nint k;\n')
+    (tmp_path / "b.cuh").write_text('#pragma once\n  #include "a.cuh"\n')
+    (tmp_path / "a.cuh").write_text('#pragma once\n#include "b.cuh"\n')
+    (tmp_path / "other.cuh").write_text("int x;\n")
+    monkeypatch.setattr(bench, "CSRC", str(tmp_path))
+    monkeypatch.setattr(bench, "KERNEL_SOURCES", {"kern": "k.cu"})
+    assert [os.path.basename(f) for f in bench.source_files("k.cu")] == ["k.cu", "a.cuh", "b.cuh"]
+    first = bench.source_hash("kern<64>")
+    (tmp_path / "other.cuh").write_text("int y;\n")
+    assert bench.source_hash("kern<64>") == first
+    for name in ("k.cu", "a.cuh", "b.cuh"):
+        text = (tmp_path / name).read_text()
+        (tmp_path / name).write_text(text + "int z;\n")
+        assert bench.source_hash("kern<64>") != first
+        (tmp_path / name).write_text(text)
+    assert bench.source_hash("kern<64>") == first
+
+
+def test_training_kernels_do_not_include_the_samplers_headers():
+    for source in ("fwd.cu", "fwd2.cu", "bwd2.cu"):
+        names = {os.path.basename(f) for f in bench.source_files(source)}
+        assert names == {source, "geometry.cuh", "params.cuh", "sm100.cuh"}
