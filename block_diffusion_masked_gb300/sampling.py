@@ -31,9 +31,11 @@ def rotary_table(max_pos, rot_dim, base=10000.0, scaling=None, factor=1.0, origi
       frequency is divided by ``factor`` and the highest is kept;
     * ``"parts"``: a frequency that turns more than ``beta_fast`` times within
       ``original_max_pos`` is kept, one that turns less than ``beta_slow`` times
-      is divided by ``factor``, a linear ramp over i between; cosines and sines
-      are multiplied by 0.1 ln(factor) + 1 ("YaRN: Efficient Context Window
-      Extension of Large Language Models", sections 3.2 and 3.4).
+      is divided by ``factor``, and the part that is divided grows linearly with
+      i between (from the whole i below to the one above); cosines and sines are
+      multiplied by 0.1 ln(factor) + 1.  After "YaRN: Efficient Context Window
+      Extension of Large Language Models", sections 3.2 and 3.4, whose ramp is
+      linear in the number of turns instead.
     """
     if max_pos < 1 or rot_dim < 16 or rot_dim % 16:
         raise ValueError("max_pos must be at least 1 and rot_dim a multiple of 16")
@@ -54,8 +56,7 @@ def rotary_table(max_pos, rot_dim, base=10000.0, scaling=None, factor=1.0, origi
             return rot_dim * math.log(original_max_pos / (turns * 2 * math.pi)) / \
                 (2 * math.log(base))
 
-        lo = max(math.floor(index_of(beta_fast)), 0)
-        hi = min(math.ceil(index_of(beta_slow)), rot_dim // 2 - 1)
+        lo, hi = math.floor(index_of(beta_fast)), math.ceil(index_of(beta_slow))
         ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
         freq = freq * (1 - ramp) + freq / factor * ramp
         mult = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0

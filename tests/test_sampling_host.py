@@ -367,3 +367,33 @@ def test_arguments_past_32_bits():
         with pytest.raises(b.DfaError) as e:
             b.dfa_cache_workspace_bytes(*bad)
         assert e.value.code == b.DFA_EINVAL, i
+
+
+@pytest.mark.parametrize("base,rot,length", [(10000.0, 128, 131072), (10000.0, 64, 4096),
+                                             (500000.0, 128, 8192), (10000.0, 32, 128)])
+def test_rotary_table_by_parts(base, rot, length):
+    """Kept, divided, or in between by the frequency's place between the two that
+    turn beta_fast and beta_slow times: also where those lie outside the table.
+    Tolerance: an angle below 2 in float64, one rounding to float32 of at most m."""
+    from block_diffusion_masked_gb300 import rotary_table
+
+    factor, m = 8.0, 0.1 * math.log(8.0) + 1.0
+    t = rotary_table(2, rot, base=base, scaling="parts", factor=factor, original_max_pos=length,
+                     device="cpu").double()
+    place = [rot * math.log(length / (turns * 2 * math.pi)) / (2 * math.log(base))
+             for turns in (32.0, 1.0)]
+    lo, hi = math.floor(place[0]), math.ceil(place[1])
+    between = 0
+    for i in range(rot // 2):
+        f = base ** (-2 * i / rot)
+        turns = length * f / (2 * math.pi)
+        part = min(max((i - lo) / (hi - lo), 0.0), 1.0)
+        if turns >= 32 and i <= lo:
+            assert part == 0
+        if turns <= 1 and i >= hi:
+            assert part == 1
+        between += 0 < part < 1
+        a = f * (1 - part) + f / factor * part
+        assert abs(t[1, i] - m * math.cos(a)) <= 2.0 ** -23
+        assert abs(t[1, rot // 2 + i] - m * math.sin(a)) <= 2.0 ** -23
+    assert between
