@@ -263,603 +263,608 @@ __global__ void __launch_bounds__(CacheTile<D, MT, WR, WK, STAGES>::kThreads,
 
 #pragma unroll 1
   for (; w.b >= 0 && ok; next_piece(p, w)) {
-  const int rtiles = row_tiles(p, w.rq);
-  const int h = w.seg / rtiles, tile = w.seg - h * rtiles;
-  const int R = w.rq.n * p.G;  // rows of the request and key/value head
-  const int row_base = tile * T::kRows;
-  const int key_lo = key_first(w), key_hi = key_end(w), my_units = group_units(w);
-  // The piece's queries: the f16 fragments of the cached keys' products (built
-  // by the first group for all) and the bf16 ones of the own keys', which stay
-  // in registers where there is room (kHoldQ) and are read again where not.
-  constexpr bool kHoldQ = MT * D <= 128;
-  auto load_q = [&](int mt, int i, int sg, uint4* q2) {
-    const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
-    q2[0] = q2[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < R) {
-      const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
-      const __nv_bfloat16* src =
-          p.q + (w.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 64 * sg + 16 * t;
-      q2[0] = *reinterpret_cast<const uint4*>(src);
-      q2[1] = *reinterpret_cast<const uint4*>(src + 8);
+    const int rtiles = row_tiles(p, w.rq);
+    const int h = w.seg / rtiles, tile = w.seg - h * rtiles;
+    const int R = w.rq.n * p.G;  // rows of the request and key/value head
+    const int row_base = tile * T::kRows;
+    const int key_lo = key_first(w), key_hi = key_end(w), my_units = group_units(w);
+    // The piece's queries: the f16 fragments of the cached keys' products (built
+    // by the first group for all) and the bf16 ones of the own keys', which stay
+    // in registers where there is room (kHoldQ) and are read again where not.
+    constexpr bool kHoldQ = MT * D <= 128;
+    auto load_q = [&](int mt, int i, int sg, uint4* q2) {
+      const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+      q2[0] = q2[1] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < R) {
+        const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
+        const __nv_bfloat16* src =
+            p.q + (w.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 64 * sg + 16 * t;
+        q2[0] = *reinterpret_cast<const uint4*>(src);
+        q2[1] = *reinterpret_cast<const uint4*>(src + 8);
+      }
+    };
+    uint4 qv[kHoldQ ? MT : 1][2][kSeg][2];
+    if constexpr (kHoldQ) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int sg = 0; sg < kSeg; ++sg) load_q(mt, i, sg, qv[mt][i][sg]);
     }
-  };
-  uint4 qv[kHoldQ ? MT : 1][2][kSeg][2];
-  if constexpr (kHoldQ) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int sg = 0; sg < kSeg; ++sg) load_q(mt, i, sg, qv[mt][i][sg]);
-  }
-  if (!primed && wr == 0) {  // the run's first loads, behind the queries'
+    if (!primed && wr == 0) {  // the run's first loads, behind the queries'
 #pragma unroll 1
-    for (int s = 0; s < STAGES; ++s) ahead();
-  }
-  primed = true;
-  int own = 0;
-  if (p.k != nullptr && w.last())
-    own = cache_own_end(w.rq.len, min(R - 1, row_base + T::kRows - 1) / p.G, w.rq.n, p.bs);
-  auto load_own_k = [&](int k0, int sg, int n, uint4* k2) {
-    const int key = k0 + 8 * n + g;
-    k2[0] = k2[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (key < w.rq.n) {
-      const __nv_bfloat16* src =
-          p.k + (w.rq.row0 + key) * p.k_sr + h * p.k_sh + 64 * sg + 16 * t;
-      k2[0] = *reinterpret_cast<const uint4*>(src);
-      k2[1] = *reinterpret_cast<const uint4*>(src + 8);
+      for (int s = 0; s < STAGES; ++s) ahead();
     }
-  };
-  // the first own unit's keys of this group, on their way early
-  uint4 kw0[kHoldQ ? kSeg : 1][2][2];
-  if constexpr (kHoldQ) {
-    if (16 * wk < own) {
-#pragma unroll
-      for (int sg = 0; sg < kSeg; ++sg)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) load_own_k(16 * wk, sg, n, kw0[sg][n]);
-    }
-  }
-  int page[2];
-  float ks[2], vs[2];
-  load_pages(w, my_units, lane, page);
-  load_scales(h, page, ks, vs);
-  if (wk == 0) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float inv[2];
-      uint4 qt[2][kSeg][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int sg = 0; sg < kSeg; ++sg) {
-          if constexpr (kHoldQ) qt[i][sg][0] = qv[mt][i][sg][0], qt[i][sg][1] = qv[mt][i][sg][1];
-          else load_q(mt, i, sg, qt[i][sg]);
-        }
-        unsigned top = 0;
+    primed = true;
+    int own = 0;
+    if (p.k != nullptr && w.last())
+      own = cache_own_end(w.rq.len, min(R - 1, row_base + T::kRows - 1) / p.G, w.rq.n, p.bs);
+    auto load_own_k = [&](int k0, int sg, int n, uint4* k2) {
+      const int key = k0 + 8 * n + g;
+      k2[0] = k2[1] = make_uint4(0u, 0u, 0u, 0u);
+      if (key < w.rq.n) {
+        const __nv_bfloat16* src =
+            p.k + (w.rq.row0 + key) * p.k_sr + h * p.k_sh + 64 * sg + 16 * t;
+        k2[0] = *reinterpret_cast<const uint4*>(src);
+        k2[1] = *reinterpret_cast<const uint4*>(src + 8);
+      }
+    };
+    // the first own unit's keys of this group, on their way early
+    uint4 kw0[kHoldQ ? kSeg : 1][2][2];
+    if constexpr (kHoldQ) {
+      if (16 * wk < own) {
 #pragma unroll
         for (int sg = 0; sg < kSeg; ++sg)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint4& q4 = qt[i][sg][c];
-            const uint32_t v[4] = {q4.x, q4.y, q4.z, q4.w};
+          for (int n = 0; n < 2; ++n) load_own_k(16 * wk, sg, n, kw0[sg][n]);
+      }
+    }
+    int page[2];
+    float ks[2], vs[2];
+    load_pages(w, my_units, lane, page);
+    load_scales(h, page, ks, vs);
+    if (wk == 0) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const unsigned lo = v[x] & 0x7fffu, hi = (v[x] >> 16) & 0x7fffu;
-              top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-            }
+      for (int mt = 0; mt < MT; ++mt) {
+        float inv[2];
+        uint4 qt[2][kSeg][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int sg = 0; sg < kSeg; ++sg) {
+            if constexpr (kHoldQ) qt[i][sg][0] = qv[mt][i][sg][0], qt[i][sg][1] = qv[mt][i][sg][1];
+            else load_q(mt, i, sg, qt[i][sg]);
           }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-e brings the row's largest magnitude into [2^14, 2^15)
-        int e = static_cast<int>(top >> 7) - 127 - 14;
-        if (e < -100) e = -100;
-        if (t == 0) s_factor[16 * (wr * MT + mt) + g + 8 * i] = pow2_bits(e) * p.scale_log2;
-        inv[i] = pow2_bits(-e);
+          unsigned top = 0;
+#pragma unroll
+          for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint4& q4 = qt[i][sg][c];
+              const uint32_t v[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const unsigned lo = v[x] & 0x7fffu, hi = (v[x] >> 16) & 0x7fffu;
+                top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+              }
+            }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^-e brings the row's largest magnitude into [2^14, 2^15)
+          int e = static_cast<int>(top >> 7) - 127 - 14;
+          if (e < -100) e = -100;
+          if (t == 0) s_factor[16 * (wr * MT + mt) + g + 8 * i] = pow2_bits(e) * p.scale_log2;
+          inv[i] = pow2_bits(-e);
+        }
+#pragma unroll
+        for (int sg = 0; sg < kSeg; ++sg)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint32_t a[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4& q4 = qt[i][sg][s >> 1];
+              const uint32_t x0 = s & 1 ? q4.z : q4.x, x1 = s & 1 ? q4.w : q4.y;
+              a[i][0] = pack_f16x2(__uint_as_float(x0 << 16) * inv[i],
+                                   __uint_as_float(x0 & 0xffff0000u) * inv[i]);
+              a[i][1] = pack_f16x2(__uint_as_float(x1 << 16) * inv[i],
+                                   __uint_as_float(x1 & 0xffff0000u) * inv[i]);
+            }
+            const uint32_t at =
+                smem0 + T::kOffQ + (((wr * MT + mt) * T::kFrags + sg * 4 + s) * 32 + lane) * 16;
+            st_shared_v4(at, a[0][0], a[1][0], a[0][1], a[1][1]);
+          }
+      }
+    }
+
+    float o[MT][kOut][4];
+    float m[MT][2], l[MT][2], factor[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[mt][i] = -INFINITY;
+        l[mt][i] = 0.f;
       }
 #pragma unroll
-      for (int sg = 0; sg < kSeg; ++sg)
+      for (int e = 0; e < kOut; ++e)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t a[2][2];
+        for (int x = 0; x < 4; ++x) o[mt][e][x] = 0.f;
+    }
+    float c = pow2_bits(kCacheMinExp);  // the output's unit: the largest value scale so far
+    float inv_c = pow2_bits(-kCacheMinExp);
+    const uint8_t* qbase = smem + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
+
+    // A score's factor (the row's power of two times the page's scale) is never 0,
+    // be the row zero, the page zero or not there: 0 * -inf is not a number.  A
+    // raw score is below 2^33, so what is raised to kTiny adds less than 2^-93.
+    constexpr float kTiny = 1.1754944e-38f;  // 2^-126
+
+    // Probabilities of a unit's raw scores sc (NT column tiles of 8 keys; -inf:
+    // not seen), packed as the products' A operand: score factors row[.][.] times
+    // f0 (first half of the column tiles) or f1, value weights w0 or w1 (times
+    // the new unit c_new's inverse).  They are taken against the reference as it
+    // stands; only where their sum says that one may have outgrown f16, or with
+    // `look`, is the maximum found and the unit done again.
+    auto soften = [&](auto nt, auto f16, auto& sc, const float (&row)[MT][2], float f0, float f1,
+                      float w0, float w1, float c_new, bool look, auto& pf) {
+      constexpr int NT = decltype(nt)::value;
+      float shrink[MT][2];
+      const float cr = c_new != c ? c / c_new : 1.f;
+      if (c_new != c) c = c_new, inv_c = 1.f / c;
+      w0 *= inv_c, w1 *= inv_c;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) shrink[mt][0] = shrink[mt][1] = cr;
+#pragma unroll 1
+      for (;;) {
+        if (look) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+              for (int n = 0; n < NT / 2; ++n) {
+                x = fmax3(x, sc[mt][n][2 * i], sc[mt][n][2 * i + 1]);
+                y = fmax3(y, sc[mt][n + NT / 2][2 * i], sc[mt][n + NT / 2][2 * i + 1]);
+              }
+              x = fmaxf(x * fmaxf(row[mt][i] * f0, kTiny), y * fmaxf(row[mt][i] * f1, kTiny));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              if (x > m[mt][i]) {
+                const float a = ex2_approx(m[mt][i] - x);
+                m[mt][i] = x;
+                l[mt][i] *= a;
+                shrink[mt][i] *= a;
+              }
+            }
+        }
+        float sum[MT][2];
+        bool over = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint4& q4 = qt[i][sg][s >> 1];
-            const uint32_t x0 = s & 1 ? q4.z : q4.x, x1 = s & 1 ? q4.w : q4.y;
-            a[i][0] = pack_f16x2(__uint_as_float(x0 << 16) * inv[i],
-                                 __uint_as_float(x0 & 0xffff0000u) * inv[i]);
-            a[i][1] = pack_f16x2(__uint_as_float(x1 << 16) * inv[i],
-                                 __uint_as_float(x1 & 0xffff0000u) * inv[i]);
+            // a row that has met no finite score keeps probabilities of 0
+            const float ref = m[mt][i] == -INFINITY ? 0.f : kShift - m[mt][i];
+            const float g0 = fmaxf(row[mt][i] * f0, kTiny), g1 = fmaxf(row[mt][i] * f1, kTiny);
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const float e0 = ex2_approx(fmaf(sc[mt][n][2 * i], n < NT / 2 ? g0 : g1, ref));
+              const float e1 = ex2_approx(fmaf(sc[mt][n][2 * i + 1], n < NT / 2 ? g0 : g1, ref));
+              s0 += e0;
+              s1 += e1;
+              const float wn = n < NT / 2 ? w0 : w1;
+              (&pf[mt][n / 2].x)[2 * (n & 1) + i] =
+                  decltype(f16)::value ? pack_f16x2(e0 * wn, e1 * wn)
+                                       : pack_bf16x2(e0 * wn, e1 * wn);
+            }
+            sum[mt][i] = s0 + s1;
+            over = over || sum[mt][i] > kMostSum || m[mt][i] == -INFINITY;
           }
-          const uint32_t at =
-              smem0 + T::kOffQ + (((wr * MT + mt) * T::kFrags + sg * 4 + s) * 32 + lane) * 16;
-          st_shared_v4(at, a[0][0], a[1][0], a[0][1], a[1][1]);
         }
-    }
-  }
-
-  float o[MT][kOut][4];
-  float m[MT][2], l[MT][2], factor[MT][2];
+        if (look || !__any_sync(0xffffffffu, over)) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) l[mt][0] += sum[mt][0], l[mt][1] += sum[mt][1];
+          break;
+        }
+        look = true;
+      }
+      bool any = false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[mt][i] = -INFINITY;
-      l[mt][i] = 0.f;
-    }
+      for (int mt = 0; mt < MT; ++mt) any = any || shrink[mt][0] != 1.f || shrink[mt][1] != 1.f;
+      if (__any_sync(0xffffffffu, any)) {
 #pragma unroll
-    for (int e = 0; e < kOut; ++e)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[mt][e][x] = 0.f;
-  }
-  float c = pow2_bits(kCacheMinExp);  // the output's unit: the largest value scale so far
-  float inv_c = pow2_bits(-kCacheMinExp);
-  const uint8_t* qbase = smem + T::kOffQ + (wr * MT * T::kFrags * 32 + lane) * 16;
-
-  // A score's factor (the row's power of two times the page's scale) is never 0,
-  // be the row zero, the page zero or not there: 0 * -inf is not a number.  A
-  // raw score is below 2^33, so what is raised to kTiny adds less than 2^-93.
-  constexpr float kTiny = 1.1754944e-38f;  // 2^-126
-
-  // Probabilities of a unit's raw scores sc (NT column tiles of 8 keys; -inf:
-  // not seen), packed as the products' A operand: score factors row[.][.] times
-  // f0 (first half of the column tiles) or f1, value weights w0 or w1 (times
-  // the new unit c_new's inverse).  They are taken against the reference as it
-  // stands; only where their sum says that one may have outgrown f16, or with
-  // `look`, is the maximum found and the unit done again.
-  auto soften = [&](auto nt, auto f16, auto& sc, const float (&row)[MT][2], float f0, float f1,
-                    float w0, float w1, float c_new, bool look, auto& pf) {
-    constexpr int NT = decltype(nt)::value;
-    float shrink[MT][2];
-    const float cr = c_new != c ? c / c_new : 1.f;
-    if (c_new != c) c = c_new, inv_c = 1.f / c;
-    w0 *= inv_c, w1 *= inv_c;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) shrink[mt][0] = shrink[mt][1] = cr;
+          for (int e = 0; e < kOut; ++e) {
+            o[mt][e][0] *= shrink[mt][0];
+            o[mt][e][1] *= shrink[mt][0];
+            o[mt][e][2] *= shrink[mt][1];
+            o[mt][e][3] *= shrink[mt][1];
+          }
+      }
+    };
+    // Own keys and values first, bf16, with the segment's end, while the cached
+    // keys are on their way: units of 16 keys, the groups in turn, operands
+    // straight from global memory.
+    {
 #pragma unroll 1
-    for (;;) {
-      if (look) {
+      for (int k0 = 16 * wk; k0 < own; k0 += 16 * WK) {
+        float sc[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
+#pragma unroll
+        for (int sg = 0; sg < kSeg; ++sg) {
+          uint4 kx[2][2];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (kHoldQ && k0 == 16 * wk) {
+              kx[n][0] = kw0[kHoldQ ? sg : 0][n][0];
+              kx[n][1] = kw0[kHoldQ ? sg : 0][n][1];
+            } else {
+              load_own_k(k0, sg, n, kx[n]);
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint4 qx[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if constexpr (kHoldQ) qx[i][0] = qv[mt][i][sg][0], qx[i][1] = qv[mt][i][sg][1];
+              else load_q(mt, i, sg, qx[i]);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint4& q0 = qx[0][s >> 1];
+              const uint4& q1 = qx[1][s >> 1];
+              const uint4 a = s & 1 ? make_uint4(q0.z, q1.z, q0.w, q1.w)
+                                    : make_uint4(q0.x, q1.x, q0.y, q1.y);
+#pragma unroll
+              for (int n = 0; n < 2; ++n) {
+                const uint4& k4 = kx[n][s >> 1];
+                mma_bf16(sc[mt][n], a, s & 1 ? k4.z : k4.x, s & 1 ? k4.w : k4.y);
+              }
+            }
+          }
+        }
+        int end[MT][2];  // one past the last own key of the thread's rows
+        float row[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = -INFINITY, y = -INFINITY;
+            const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
+            end[mt][i] = r < R ? cache_own_end(w.rq.len, r / p.G, w.rq.n, p.bs) : 0;
+            row[mt][i] = p.scale_log2;
 #pragma unroll
-            for (int n = 0; n < NT / 2; ++n) {
-              x = fmax3(x, sc[mt][n][2 * i], sc[mt][n][2 * i + 1]);
-              y = fmax3(y, sc[mt][n + NT / 2][2 * i], sc[mt][n + NT / 2][2 * i + 1]);
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                if (k0 + 8 * n + 2 * t + x >= end[mt][i]) sc[mt][n][2 * i + x] = -INFINITY;
+          }
+        uint4 pf[MT][1];
+        soften(std::integral_constant<int, 2>{}, std::false_type{}, sc, row, 1.f, 1.f, 1.f, 1.f,
+               fmaxf(c, kOwnUnit), true, pf);
+        // A row's probability of an own key it does not see is 0, but 0 times a
+        // value that is not finite is not: such values leave the product and
+        // are added to the rows that see them.
+        bool odd = false;
+#pragma unroll
+        for (int half = 0; half < kHalf; ++half)
+#pragma unroll
+          for (int part = 0; part < kCols / 8; ++part) {  // 8 dims at a time
+            uint32_t vw[4][4];
+            const int dim = D == 64 ? 8 * g : 128 * half + 16 * key_of<D>(g) + 8 * part;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = k0 + 8 * (x >> 1) + 2 * t + (x & 1);
+              uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
+              if (key < w.rq.n)
+                v4 = *reinterpret_cast<const uint4*>(p.v + (w.rq.row0 + key) * p.v_sr + h * p.v_sh +
+                                                     dim);
+              vw[x][0] = v4.x, vw[x][1] = v4.y, vw[x][2] = v4.z, vw[x][3] = v4.w;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if ((vw[x][y] & 0x7f80u) == 0x7f80u) vw[x][y] &= 0xffff0000u, odd = true;
+                if ((vw[x][y] & 0x7f800000u) == 0x7f800000u) vw[x][y] &= 0xffffu, odd = true;
+              }
             }
-            x = fmaxf(x * fmaxf(row[mt][i] * f0, kTiny), y * fmaxf(row[mt][i] * f1, kTiny));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            if (x > m[mt][i]) {
-              const float a = ex2_approx(m[mt][i] - x);
-              m[mt][i] = x;
-              l[mt][i] *= a;
-              shrink[mt][i] *= a;
-            }
-          }
-      }
-      float sum[MT][2];
-      bool over = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // a row that has met no finite score keeps probabilities of 0
-          const float ref = m[mt][i] == -INFINITY ? 0.f : kShift - m[mt][i];
-          const float g0 = fmaxf(row[mt][i] * f0, kTiny), g1 = fmaxf(row[mt][i] * f1, kTiny);
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float e0 = ex2_approx(fmaf(sc[mt][n][2 * i], n < NT / 2 ? g0 : g1, ref));
-            const float e1 = ex2_approx(fmaf(sc[mt][n][2 * i + 1], n < NT / 2 ? g0 : g1, ref));
-            s0 += e0;
-            s1 += e1;
-            const float wn = n < NT / 2 ? w0 : w1;
-            (&pf[mt][n / 2].x)[2 * (n & 1) + i] =
-                decltype(f16)::value ? pack_f16x2(e0 * wn, e1 * wn) : pack_bf16x2(e0 * wn, e1 * wn);
-          }
-          sum[mt][i] = s0 + s1;
-          over = over || sum[mt][i] > kMostSum || m[mt][i] == -INFINITY;
-        }
-      }
-      if (look || !__any_sync(0xffffffffu, over)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) l[mt][0] += sum[mt][0], l[mt][1] += sum[mt][1];
-        break;
-      }
-      look = true;
-    }
-    bool any = false;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) any = any || shrink[mt][0] != 1.f || shrink[mt][1] != 1.f;
-    if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < kOut; ++e) {
-          o[mt][e][0] *= shrink[mt][0];
-          o[mt][e][1] *= shrink[mt][0];
-          o[mt][e][2] *= shrink[mt][1];
-          o[mt][e][3] *= shrink[mt][1];
-        }
-    }
-  };
-  // Own keys and values first, bf16, with the segment's end, while the cached
-  // keys are on their way: units of 16 keys, the groups in turn, operands
-  // straight from global memory.
-  {
-#pragma unroll 1
-    for (int k0 = 16 * wk; k0 < own; k0 += 16 * WK) {
-      float sc[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
-#pragma unroll
-      for (int sg = 0; sg < kSeg; ++sg) {
-        uint4 kx[2][2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          if (kHoldQ && k0 == 16 * wk) kx[n][0] = kw0[kHoldQ ? sg : 0][n][0], kx[n][1] = kw0[kHoldQ ? sg : 0][n][1];
-          else load_own_k(k0, sg, n, kx[n]);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint4 qx[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if constexpr (kHoldQ) qx[i][0] = qv[mt][i][sg][0], qx[i][1] = qv[mt][i][sg][1];
-            else load_q(mt, i, sg, qx[i]);
-          }
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint4& q0 = qx[0][s >> 1];
-            const uint4& q1 = qx[1][s >> 1];
-            const uint4 a = s & 1 ? make_uint4(q0.z, q1.z, q0.w, q1.w)
-                                  : make_uint4(q0.x, q1.x, q0.y, q1.y);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint4& k4 = kx[n][s >> 1];
-              mma_bf16(sc[mt][n], a, s & 1 ? k4.z : k4.x, s & 1 ? k4.w : k4.y);
-            }
-          }
-        }
-      }
-      int end[MT][2];  // one past the last own key of the thread's rows
-      float row[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = row_base + 16 * (wr * MT + mt) + g + 8 * i;
-          end[mt][i] = r < R ? cache_own_end(w.rq.len, r / p.G, w.rq.n, p.bs) : 0;
-          row[mt][i] = p.scale_log2;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (k0 + 8 * n + 2 * t + x >= end[mt][i]) sc[mt][n][2 * i + x] = -INFINITY;
-        }
-      uint4 pf[MT][1];
-      soften(std::integral_constant<int, 2>{}, std::false_type{}, sc, row, 1.f, 1.f, 1.f, 1.f,
-             fmaxf(c, kOwnUnit), true, pf);
-      // A row's probability of an own key it does not see is 0, but 0 times a
-      // value that is not finite is not: such values leave the product and
-      // are added to the rows that see them.
-      bool odd = false;
-#pragma unroll
-      for (int half = 0; half < kHalf; ++half)
-#pragma unroll
-        for (int part = 0; part < kCols / 8; ++part) {  // 8 dims at a time
-          uint32_t vw[4][4];
-          const int dim = D == 64 ? 8 * g : 128 * half + 16 * key_of<D>(g) + 8 * part;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = k0 + 8 * (x >> 1) + 2 * t + (x & 1);
-            uint4 v4 = make_uint4(0u, 0u, 0u, 0u);
-            if (key < w.rq.n)
-              v4 = *reinterpret_cast<const uint4*>(p.v + (w.rq.row0 + key) * p.v_sr + h * p.v_sh +
-                                                   dim);
-            vw[x][0] = v4.x, vw[x][1] = v4.y, vw[x][2] = v4.z, vw[x][3] = v4.w;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              if ((vw[x][y] & 0x7f80u) == 0x7f80u) vw[x][y] &= 0xffff0000u, odd = true;
-              if ((vw[x][y] & 0x7f800000u) == 0x7f800000u) vw[x][y] &= 0xffffu, odd = true;
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t b0 = __byte_perm(vw[0][y], vw[1][y], z ? 0x7632 : 0x5410);
+                const uint32_t b1 = __byte_perm(vw[2][y], vw[3][y], z ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt][0], b0, b1);
+              }
             }
           }
+        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+          for (int key = k0; key < min(k0 + 16, w.rq.n); ++key) {
+            const __nv_bfloat16* src = p.v + (w.rq.row0 + key) * p.v_sr + h * p.v_sh;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
+            for (int e = 0; e < kOut; ++e)
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t b0 = __byte_perm(vw[0][y], vw[1][y], z ? 0x7632 : 0x5410);
-              const uint32_t b1 = __byte_perm(vw[2][y], vw[3][y], z ? 0x7632 : 0x5410);
+              for (int x = 0; x < 2; ++x) {
+                const float y = __bfloat162float(
+                    src[128 * (e / kCols) + kCols * key_of<D>(2 * t + x) + e % kCols]);
+                if (isfinite(y)) continue;
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                mma_bf16(o[mt][half * kCols + 8 * part + 2 * y + z], pf[mt][0], b0, b1);
-            }
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (key < end[mt][i]) o[mt][e][2 * i + x] += y;
+              }
           }
         }
-      if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-        for (int key = k0; key < min(k0 + 16, w.rq.n); ++key) {
-          const __nv_bfloat16* src = p.v + (w.rq.row0 + key) * p.v_sr + h * p.v_sh;
+      }
+      // Cached probabilities are f16 and relative to the output's unit, which the
+      // pages' scales alone are to set: it comes down to the largest of the group's
+      // first units, but not so far that the own keys' output, in the new unit,
+      // would pass 2^100 (what cached keys lose to that is below 2^-100 of it).
+      if (16 * wk < own && my_units > 0) {
+        unsigned top = 0;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int e = 0; e < kOut; ++e)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float y = __bfloat162float(
-                  src[128 * (e / kCols) + kCols * key_of<D>(2 * t + x) + e % kCols]);
-              if (isfinite(y)) continue;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  if (key < end[mt][i]) o[mt][e][2 * i + x] += y;
+            for (int x = 0; x < 4; ++x) {
+              const unsigned y = __float_as_uint(o[mt][e][x]) & 0x7fffffffu;
+              top = max(top, y < 0x7f800000u ? y : 0u);
             }
-        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1])));
+        const int want = kOwnExp - max(static_cast<int>(most >> 23) - 127, kCacheMinExp);
+        const int down = max(min(127 + 99 - static_cast<int>(top >> 23), want), 0);
+        const float grow = pow2_bits(down);
+        c *= pow2_bits(-down);
+        inv_c *= grow;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < kOut; ++e)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[mt][e][x] *= grow;
       }
     }
-    // Cached probabilities are f16 and relative to the output's unit, which the
-    // pages' scales alone are to set: it comes down to the largest of the group's
-    // first units, but not so far that the own keys' output, in the new unit,
-    // would pass 2^100 (what cached keys lose to that is below 2^-100 of it).
-    if (16 * wk < own && my_units > 0) {
-      unsigned top = 0;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < kOut; ++e)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const unsigned y = __float_as_uint(o[mt][e][x]) & 0x7fffffffu;
-            top = max(top, y < 0x7f800000u ? y : 0u);
-          }
-      top = __reduce_max_sync(0xffffffffu, top);
-      const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1])));
-      const int want = kOwnExp - max(static_cast<int>(most >> 23) - 127, kCacheMinExp);
-      const int down = max(min(127 + 99 - static_cast<int>(top >> 23), want), 0);
-      const float grow = pow2_bits(down);
-      c *= pow2_bits(-down);
-      inv_c *= grow;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < kOut; ++e)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) o[mt][e][x] *= grow;
-    }
-  }
 
-  __syncthreads();  // the queries' fragments
-  // Held in registers where there is room; headdim 64, three blocks to an SM,
-  // reads them for every unit (89.6 us against 93.9, 16 rows).
-  constexpr bool kHoldF = kHoldQ && D != 64;
-  uint4 qf[kHoldF ? MT : 1][T::kFrags];
-  if constexpr (kHoldF) {
+    __syncthreads();  // the queries' fragments
+    // Held in registers where there is room; headdim 64, three blocks to an SM,
+    // reads them for every unit (89.6 us against 93.9, 16 rows).
+    constexpr bool kHoldF = kHoldQ && D != 64;
+    uint4 qf[kHoldF ? MT : 1][T::kFrags];
+    if constexpr (kHoldF) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int f = 0; f < T::kFrags; ++f) qf[mt][f] = load16(qbase + (mt * T::kFrags + f) * 512);
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int f = 0; f < T::kFrags; ++f) qf[mt][f] = load16(qbase + (mt * T::kFrags + f) * 512);
-  }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) factor[mt][i] = s_factor[16 * (wr * MT + mt) + g + 8 * i];
+      for (int i = 0; i < 2; ++i) factor[mt][i] = s_factor[16 * (wr * MT + mt) + g + 8 * i];
 
 #pragma unroll 1
-  for (int u = 0; u < my_units; ++u) {
-    const int stage = consumed % STAGES;
-    if ((u & 31) == 0 && u > 0) {
-      load_pages(w, my_units, u + lane, page);
-      load_scales(h, page, ks, vs);
-    }
-    float ks0 = __shfl_sync(0xffffffffu, ks[0], u & 31);
-    float ks1 = __shfl_sync(0xffffffffu, ks[1], u & 31);
-    const float vs0 = __shfl_sync(0xffffffffu, vs[0], u & 31);
-    const float vs1 = __shfl_sync(0xffffffffu, vs[1], u & 31);
-    const int p0 = __shfl_sync(0xffffffffu, page[0], u & 31);
-    const int p1 = __shfl_sync(0xffffffffu, page[1], u & 31);
-    const int key = key_lo + (wk + u * WK) * kUnit;
-    // valid keys of the unit's 16-key halves
-    const int nv0 = cache_page_ok(p0, p.num_pages) ? min(16, key_hi - key) : 0;
-    const int nv1 = cache_page_ok(p1, p.num_pages) ? max(0, min(16, key_hi - key - 16)) : 0;
-    const uint8_t* kt = smem + wk * STAGES * 2 * T::kUnitBytes + stage * 2 * T::kUnitBytes;
-    const uint8_t* vt = kt + T::kUnitBytes;
-    if (!(ok = mbar_wait_warp(gbar + 16 * stage, (consumed / STAGES) & 1, ab))) break;
-
-    float sc[MT][4][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
-#pragma unroll
-    for (int sg = 0; sg < kSeg; ++sg) {
-      uint4 kw[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        kw[n] = load16(tile_at<D>(kt, 8 * n + key_of<D>(g), 4 * sg + t));
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        uint32_t b[4][2];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t w = s == 0 ? kw[n].x : s == 1 ? kw[n].y : s == 2 ? kw[n].z : kw[n].w;
-          b[n][0] = e4m3_lo(w);
-          b[n][1] = e4m3_hi(w);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint4 a = kHoldF ? qf[kHoldF ? mt : 0][sg * 4 + s]
-                                 : load16(qbase + (mt * T::kFrags + sg * 4 + s) * 512);
-#pragma unroll
-          for (int n = 0; n < 4; ++n) mma_f16(sc[mt][n], a, b[n][0], b[n][1]);
-        }
+    for (int u = 0; u < my_units; ++u) {
+      const int stage = consumed % STAGES;
+      if ((u & 31) == 0 && u > 0) {
+        load_pages(w, my_units, u + lane, page);
+        load_scales(h, page, ks, vs);
       }
-    }
-    const bool whole = nv0 == 16 && nv1 == 16;
-    if (!whole) {
+      float ks0 = __shfl_sync(0xffffffffu, ks[0], u & 31);
+      float ks1 = __shfl_sync(0xffffffffu, ks[1], u & 31);
+      const float vs0 = __shfl_sync(0xffffffffu, vs[0], u & 31);
+      const float vs1 = __shfl_sync(0xffffffffu, vs[1], u & 31);
+      const int p0 = __shfl_sync(0xffffffffu, page[0], u & 31);
+      const int p1 = __shfl_sync(0xffffffffu, page[1], u & 31);
+      const int key = key_lo + (wk + u * WK) * kUnit;
+      // valid keys of the unit's 16-key halves
+      const int nv0 = cache_page_ok(p0, p.num_pages) ? min(16, key_hi - key) : 0;
+      const int nv1 = cache_page_ok(p1, p.num_pages) ? max(0, min(16, key_hi - key - 16)) : 0;
+      const uint8_t* kt = smem + wk * STAGES * 2 * T::kUnitBytes + stage * 2 * T::kUnitBytes;
+      const uint8_t* vt = kt + T::kUnitBytes;
+      if (!(ok = mbar_wait_warp(gbar + 16 * stage, (consumed / STAGES) & 1, ab))) break;
+
+      float sc[MT][4][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (8 * (n & 1) + key_of<D>(2 * t + (x & 1)) >= (n < 2 ? nv0 : nv1))
-              sc[mt][n][x] = -INFINITY;
-    }
-    uint4 pf[MT][2];
-    soften(std::integral_constant<int, 4>{}, std::true_type{}, sc, factor, ks0, ks1, vs0, vs1,
-           fmaxf(c, fmaxf(vs0, vs1)), false, pf);
-    // P V: the four keys of a thread's fragment rows, 16 dims each (headdim
-    // 64: 8).  What lies behind the last key may be anything, NaN included,
-    // and is replaced by zero.
+          for (int x = 0; x < 4; ++x) sc[mt][n][x] = 0.f;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int nv = kk == 0 ? nv0 : nv1;
+      for (int sg = 0; sg < kSeg; ++sg) {
+        uint4 kw[4];
 #pragma unroll
-      for (int half = 0; half < kHalf; ++half) {
-        uint32_t vw[4][kCols / 4];
+        for (int n = 0; n < 4; ++n)
+          kw[n] = load16(tile_at<D>(kt, 8 * n + key_of<D>(g), 4 * sg + t));
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = 8 * (x >> 1) + key_of<D>(2 * t + (x & 1));
-          if constexpr (D == 64) {
-            const uint2 w2 = *reinterpret_cast<const uint2*>(
-                tile_at<D>(vt, 16 * kk + r, g >> 1) + 8 * (g & 1));
-            vw[x][0] = w2.x, vw[x][1] = w2.y;
-          } else {
-            const uint4 w4 = load16(tile_at<D>(vt, 16 * kk + r, 8 * half + key_of<D>(g)));
-            vw[x][0] = w4.x, vw[x][1] = w4.y, vw[x][2] = w4.z, vw[x][3] = w4.w;
+        for (int s = 0; s < 4; ++s) {
+          uint32_t b[4][2];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t w = s == 0 ? kw[n].x : s == 1 ? kw[n].y : s == 2 ? kw[n].z : kw[n].w;
+            b[n][0] = e4m3_lo(w);
+            b[n][1] = e4m3_hi(w);
           }
-          if (!whole && r >= nv) {
 #pragma unroll
-            for (int y = 0; y < kCols / 4; ++y) vw[x][y] = 0u;
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint4 a = kHoldF ? qf[kHoldF ? mt : 0][sg * 4 + s]
+                                   : load16(qbase + (mt * T::kFrags + sg * 4 + s) * 512);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mma_f16(sc[mt][n], a, b[n][0], b[n][1]);
           }
-        }
-#pragma unroll
-        for (int y = 0; y < kCols / 4; ++y) {
-          const uint32_t lo0 = __byte_perm(vw[0][y], vw[1][y], 0x5140);
-          const uint32_t hi0 = __byte_perm(vw[0][y], vw[1][y], 0x7362);
-          const uint32_t lo1 = __byte_perm(vw[2][y], vw[3][y], 0x5140);
-          const uint32_t hi1 = __byte_perm(vw[2][y], vw[3][y], 0x7362);
-          const uint32_t b[4][2] = {{e4m3_lo(lo0), e4m3_lo(lo1)},
-                                    {e4m3_hi(lo0), e4m3_hi(lo1)},
-                                    {e4m3_lo(hi0), e4m3_lo(hi1)},
-                                    {e4m3_hi(hi0), e4m3_hi(hi1)}};
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma_f16(o[mt][half * kCols + 4 * y + z], pf[mt][kk], b[z][0], b[z][1]);
         }
       }
+      const bool whole = nv0 == 16 && nv1 == 16;
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (8 * (n & 1) + key_of<D>(2 * t + (x & 1)) >= (n < 2 ? nv0 : nv1))
+                sc[mt][n][x] = -INFINITY;
+      }
+      uint4 pf[MT][2];
+      soften(std::integral_constant<int, 4>{}, std::true_type{}, sc, factor, ks0, ks1, vs0, vs1,
+             fmaxf(c, fmaxf(vs0, vs1)), false, pf);
+      // P V: the four keys of a thread's fragment rows, 16 dims each (headdim
+      // 64: 8).  What lies behind the last key may be anything, NaN included,
+      // and is replaced by zero.
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const int nv = kk == 0 ? nv0 : nv1;
+#pragma unroll
+        for (int half = 0; half < kHalf; ++half) {
+          uint32_t vw[4][kCols / 4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 8 * (x >> 1) + key_of<D>(2 * t + (x & 1));
+            if constexpr (D == 64) {
+              const uint2 w2 = *reinterpret_cast<const uint2*>(
+                  tile_at<D>(vt, 16 * kk + r, g >> 1) + 8 * (g & 1));
+              vw[x][0] = w2.x, vw[x][1] = w2.y;
+            } else {
+              const uint4 w4 = load16(tile_at<D>(vt, 16 * kk + r, 8 * half + key_of<D>(g)));
+              vw[x][0] = w4.x, vw[x][1] = w4.y, vw[x][2] = w4.z, vw[x][3] = w4.w;
+            }
+            if (!whole && r >= nv) {
+#pragma unroll
+              for (int y = 0; y < kCols / 4; ++y) vw[x][y] = 0u;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < kCols / 4; ++y) {
+            const uint32_t lo0 = __byte_perm(vw[0][y], vw[1][y], 0x5140);
+            const uint32_t hi0 = __byte_perm(vw[0][y], vw[1][y], 0x7362);
+            const uint32_t lo1 = __byte_perm(vw[2][y], vw[3][y], 0x5140);
+            const uint32_t hi1 = __byte_perm(vw[2][y], vw[3][y], 0x7362);
+            const uint32_t b[4][2] = {{e4m3_lo(lo0), e4m3_lo(lo1)},
+                                      {e4m3_hi(lo0), e4m3_hi(lo1)},
+                                      {e4m3_lo(hi0), e4m3_lo(hi1)},
+                                      {e4m3_hi(hi0), e4m3_hi(hi1)}};
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                mma_f16(o[mt][half * kCols + 4 * y + z], pf[mt][kk], b[z][0], b[z][1]);
+          }
+        }
+      }
+      mbar_arrive_warp(gbar + 16 * stage + 8);
+      ++consumed;
+      if (wr == 0 && !(ok = ahead())) break;
     }
-    mbar_arrive_warp(gbar + 16 * stage + 8);
-    ++consumed;
-    if (wr == 0 && !(ok = ahead())) break;
-  }
 
-  // Join the groups: statistics first, then each group's output in a common
-  // unit, summed.
-  if (t == 0) {
+    // Join the groups: statistics first, then each group's output in a common
+    // unit, summed.
+    if (t == 0) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) s_m[wk * T::kRows + 16 * (wr * MT + mt) + g + 8 * i] = m[mt][i];
-  }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 1);
-      l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
+        for (int i = 0; i < 2; ++i) s_m[wk * T::kRows + 16 * (wr * MT + mt) + g + 8 * i] = m[mt][i];
     }
-  if (lane == 0) s_c[warp] = c;
-  __syncthreads();  // statistics written
-  float c_all = s_c[0];
-#pragma unroll
-  for (int i = 1; i < WK * WR; ++i) c_all = fmaxf(c_all, s_c[i]);
-  // The last kKept groups leave their outputs, the others add theirs to them.
-  float* join = reinterpret_cast<float*>(smem + T::kOffJoin);
-#pragma unroll 1
-  for (int turn = 0; turn < WK / T::kKept; ++turn) {
-    const bool add = turn == 1;
-    if ((wk >= WK - T::kKept) != add) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = 16 * (wr * MT + mt) + g + 8 * i;
-        float top = s_m[r];
+        l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 1);
+        l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
+      }
+    if (lane == 0) s_c[warp] = c;
+    __syncthreads();  // statistics written
+    float c_all = s_c[0];
 #pragma unroll
-        for (int x = 1; x < WK; ++x) top = fmaxf(top, s_m[x * T::kRows + r]);
-        const float f = m[mt][i] == -INFINITY ? 0.f : ex2_approx(m[mt][i] - top);
-        const float fo = f * (c / c_all);
-        if (t == 0) s_l[wk * T::kRows + r] = l[mt][i] * f;
-        float* dst = join + ((wk % T::kKept) * T::kRows + r) * T::kPitch;
-        // columns 2t and 2t + 1 of the column tiles are runs of kCols dims
+    for (int i = 1; i < WK * WR; ++i) c_all = fmaxf(c_all, s_c[i]);
+    // The last kKept groups leave their outputs, the others add theirs to them.
+    float* join = reinterpret_cast<float*>(smem + T::kOffJoin);
+#pragma unroll 1
+    for (int turn = 0; turn < WK / T::kKept; ++turn) {
+      const bool add = turn == 1;
+      if ((wk >= WK - T::kKept) != add) {
 #pragma unroll
-        for (int half = 0; half < kHalf; ++half)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int dim = 128 * half + kCols * key_of<D>(2 * t + x);
+          for (int i = 0; i < 2; ++i) {
+            const int r = 16 * (wr * MT + mt) + g + 8 * i;
+            float top = s_m[r];
 #pragma unroll
-            for (int e = 0; e < kCols; e += 4) {
-              float4 y = make_float4(o[mt][half * kCols + e][2 * i + x] * fo,
-                                     o[mt][half * kCols + e + 1][2 * i + x] * fo,
-                                     o[mt][half * kCols + e + 2][2 * i + x] * fo,
-                                     o[mt][half * kCols + e + 3][2 * i + x] * fo);
-              float4* at = reinterpret_cast<float4*>(dst + dim + e);
-              if (add) {
-                const float4 z = *at;
-                y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+            for (int x = 1; x < WK; ++x) top = fmaxf(top, s_m[x * T::kRows + r]);
+            const float f = m[mt][i] == -INFINITY ? 0.f : ex2_approx(m[mt][i] - top);
+            const float fo = f * (c / c_all);
+            if (t == 0) s_l[wk * T::kRows + r] = l[mt][i] * f;
+            float* dst = join + ((wk % T::kKept) * T::kRows + r) * T::kPitch;
+            // columns 2t and 2t + 1 of the column tiles are runs of kCols dims
+#pragma unroll
+            for (int half = 0; half < kHalf; ++half)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int dim = 128 * half + kCols * key_of<D>(2 * t + x);
+#pragma unroll
+                for (int e = 0; e < kCols; e += 4) {
+                  float4 y = make_float4(o[mt][half * kCols + e][2 * i + x] * fo,
+                                         o[mt][half * kCols + e + 1][2 * i + x] * fo,
+                                         o[mt][half * kCols + e + 2][2 * i + x] * fo,
+                                         o[mt][half * kCols + e + 3][2 * i + x] * fo);
+                  float4* at = reinterpret_cast<float4*>(dst + dim + e);
+                  if (add) {
+                    const float4 z = *at;
+                    y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
+                  }
+                  *at = y;
+                }
               }
-              *at = y;
-            }
           }
       }
+      __syncthreads();
     }
-    __syncthreads();
-  }
-  const bool single = w.whole();
-  for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
-    const int r = i / (D / 4), d4 = i - r * (D / 4);
-    if (row_base + r >= R) break;
-    float sum = 0.f, top = -INFINITY;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool single = w.whole();
+    for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
+      const int r = i / (D / 4), d4 = i - r * (D / 4);
+      if (row_base + r >= R) break;
+      float sum = 0.f, top = -INFINITY;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int x = 0; x < WK; ++x) {
-      sum += s_l[x * T::kRows + r];
-      top = fmaxf(top, s_m[x * T::kRows + r]);
-    }
+      for (int x = 0; x < WK; ++x) {
+        sum += s_l[x * T::kRows + r];
+        top = fmaxf(top, s_m[x * T::kRows + r]);
+      }
 #pragma unroll
-    for (int x = 0; x < T::kKept; ++x) {
-      const float4 y =
-          *reinterpret_cast<const float4*>(join + (x * T::kRows + r) * T::kPitch + 4 * d4);
-      a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+      for (int x = 0; x < T::kKept; ++x) {
+        const float4 y =
+            *reinterpret_cast<const float4*>(join + (x * T::kRows + r) * T::kPitch + 4 * d4);
+        a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+      }
+      // no key (sum 0): output 0 and -inf; scores that are not numbers: NaN
+      const bool none = top == -INFINITY && sum == 0.f;
+      const float inv = none ? 0.f : c_all / sum;
+      const float lse2 = none ? -INFINITY : top - kShift + lg2_approx(sum);
+      a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
+      if (single) {
+        const int tok = (row_base + r) / p.G, hq = h * p.G + (row_base + r - tok * p.G);
+        const long long row = w.rq.row0 + tok;
+        *reinterpret_cast<uint2*>(p.out + (row * p.H + hq) * D + 4 * d4) =
+            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        if (d4 == 0) p.lse[static_cast<long long>(hq) * p.rows + row] = lse2 * 0.6931471805599453f;
+      } else {
+        const long long at = (2LL * blockIdx.x + (w.first ? 0 : 1)) * T::kRows + r;
+        *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
+        if (d4 == 0) p.part_lse[at] = lse2;
+      }
     }
-    // no key (sum 0): output 0 and -inf; scores that are not numbers: NaN
-    const bool none = top == -INFINITY && sum == 0.f;
-    const float inv = none ? 0.f : c_all / sum;
-    const float lse2 = none ? -INFINITY : top - kShift + lg2_approx(sum);
-    a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
-    if (single) {
-      const int tok = (row_base + r) / p.G, hq = h * p.G + (row_base + r - tok * p.G);
-      const long long row = w.rq.row0 + tok;
-      *reinterpret_cast<uint2*>(p.out + (row * p.H + hq) * D + 4 * d4) =
-          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-      if (d4 == 0) p.lse[static_cast<long long>(hq) * p.rows + row] = lse2 * 0.6931471805599453f;
-    } else {
-      const long long at = (2LL * blockIdx.x + (w.first ? 0 : 1)) * T::kRows + r;
-      *reinterpret_cast<float4*>(p.part_o + at * D + 4 * d4) = a;
-      if (d4 == 0) p.part_lse[at] = lse2;
-    }
-  }
   }  // pieces
   if (!ok && wr == 0 && lane == 0) {
     // Giving up: nothing may land in shared memory after the block is gone.
@@ -1094,7 +1099,8 @@ int dfa_cache_forward(const void* q, const void* k, const void* v, const void* k
                              static_cast<cuuint32_t>(c.tile_rows < 128 && page_size > kUnit ? kUnit
                                                                                       : page_size),
                              1};
-  const CUtensorMapSwizzle swizzle = d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle swizzle =
+      d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (const int rc = encode_map_u8(&p.tm_k, k_cache, 3, dims, strides, box, swizzle)) return rc;
   if (const int rc = encode_map_u8(&p.tm_v, v_cache, 3, dims, strides, box, swizzle)) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);
