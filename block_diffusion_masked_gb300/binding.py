@@ -855,7 +855,8 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
 
     ``max_new``: a bound on the rows of one request.  Returns out (rows, H, d)
     bf16 and lse (H, rows) float32.  ``workspace``: a uint8 tensor of at least
-    dfa_cache_workspace_bytes(...) bytes; by default one is allocated.
+    dfa_cache_workspace_bytes(...) bytes; by default one is allocated.  For
+    sampling: no gradients, the outputs are detached from q, k and v.
     """
     rows, H, d = shape = _check_heads(q, 3, "q")
     dev = q.device

@@ -14,8 +14,9 @@
 // power of two of its own (its largest magnitude lands in [2^14, 2^15)),
 // which keeps every value down to 2^-31 of the row's largest exact.  The
 // probabilities are rounded to f16 (2^-11) for P V while the sums use them
-// unrounded; a value page's scale, relative to the largest one met so far,
-// multiplies its probabilities.  Own keys and values are bf16 products.
+// unrounded; a value page's scale, relative to the largest one met so far (the
+// output's unit), multiplies its probabilities.  Own keys and values are bf16
+// products, exact in any unit but for the probabilities' 2^-8.
 //
 // The reference of a row's exponentials moves only where a unit's
 // probabilities outgrow f16 (cache_fwd.cuh), so that most units need neither a
@@ -36,17 +37,18 @@
 // Q K^T or 16 column tiles of P V.
 //
 // For up to 32 rows to a key (headdim 256: any number), where the tcgen05
-// kernel's 128 rows would be mostly empty: 32 rows 107 us here, 122 there
-// (headdim 128), 132 and 183 (headdim 64); 64 rows as two tiles here 191, 126
+// kernel's 128 rows would be mostly empty: 32 rows 111 us here, 121 there
+// (headdim 128), 132 and 188 (headdim 64); 64 rows as two tiles here 197, 124
 // there.  (32 ragged requests of up to 8192 tokens, 330 MB.)
 //
-// Measured, 16 rows, headdim 128: 73 us for those 330 MB (4.5 TB/s, 66% of
-// what a copy reaches), 60 us for 24 requests of up to 8000 tokens (3.9 TB/s).
+// Measured, 16 rows, headdim 128: 74 us for those 330 MB (4.5 TB/s, 66% of
+// what a copy reaches), 58 us for 24 requests of up to 8000 tokens (4.1 TB/s).
 // Bound by latency: 255 registers a thread leave 8 warps to an SM, which issue
 // in 36% of the cycles (DRAM 50%, tensor pipe 20%), and some 7 us pass before
 // the first products (lengths, queries, first tiles: each a trip to memory),
-// 4 at a piece's end.  Two blocks of four groups: 60.1 us; four of two 62.5;
-// one of eight 73.7; loops over the products rolled 63 to 66.
+// 4 at a piece's end.  Two blocks of four groups against others, when the 24
+// requests took 60.1 us: four of two 62.5; one of eight 73.7; loops over the
+// products rolled 63 to 66.
 #include <cmath>
 #include <type_traits>
 
@@ -959,27 +961,27 @@ constexpr int kWholeKeys = 512;
 // The launch's shape for given sizes.
 //
 // tile_rows: query rows of a segment, the fewest that hold a request's rows, for
-// every tile reads the keys anew (headdim 256: 32 rows 127 us in a tile of 32,
-// 210 in one of 64; 64 rows 212 in one of 64, 222 in two of 32; headdim 64 and
+// every tile reads the keys anew (headdim 256: 32 rows 128 us in a tile of 32,
+// 211 in one of 64; 64 rows 214 in one of 64, 225 in two of 32; headdim 64 and
 // 128: above).  blocks: as many as are resident at once (CacheTile::kResident).
 //
 // whole: segments are not cut.  Short tables are not worth it, for one unit a
 // segment needs no join (a launch) and no workspace: up to kWholeKeys keys, and
 // up to twice that where the segments are half the blocks or more.  Measured,
-// not cut against cut: 64 requests of 500 keys and 4 heads 15.0 and 18.8 us, of
-// 1000 keys 22.3 and 26.5; one request of 250 keys 9.1 and 9.8, of 500 12.0 and
-// 10.0 but for the second launch, of 1000 17.6 and 10.5.
+// not cut against cut: 64 requests of 500 keys and 4 heads 14.7 and 18.5 us, of
+// 1000 keys 22.3 and 26.2; one request of 250 keys 8.8 and 9.8, of 500 11.7 and
+// 9.8 but for the second launch, of 1000 17.9 and 10.5.
 //
 // finish: units of 128 keys that a segment's end is taken to cost.  Too few, and
 // blocks with many ends finish last; too many, and blocks with few do.  Measured
 // (us; 32 ragged requests of up to 8192 tokens, a quarter of the heads for keys):
-//                      finish 3     4     6     8    10
-//   headdim 128,  16 rows    79    76    78    80    82
-//   headdim 128,  32 rows   137   130   116   111   113
-//   headdim 128, 128 rows   150   142   139   137   136
-//   headdim  64, 128 rows   203   199   195   196   196
-//   headdim 256,  16 rows   113   110   103   101   103
-//   headdim 256,  64 rows   215   217   226   235   242
+//                      finish 3     4     5     6     8    10
+//   headdim 128,  16 rows    76    74    74    75    77    79
+//   headdim 128,  32 rows   139   132   125   118   111   112
+//   headdim 128, 128 rows   143   136   135   133   132   131
+//   headdim  64, 128 rows   205   200   197   196   197   197
+//   headdim 256,  16 rows   113   110   106   104   101   102
+//   headdim 256,  64 rows   214   214   219   224   233   240
 struct CachePlan {
   int tile_rows, blocks, finish;
   bool whole;

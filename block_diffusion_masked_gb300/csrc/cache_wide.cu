@@ -25,8 +25,8 @@
 // others (setmaxnreg).
 //
 // Measured, 128 rows, headdim 128, 32 ragged requests of up to 8192 tokens
-// (342 MB, 81 GFLOP): 134 us, 2.6 TB/s, 610 TFLOP/s; 64 rows 127, headdim 64
-// 195 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
+// (342 MB, 81 GFLOP): 132 us, 2.6 TB/s, 610 TFLOP/s; 64 rows 124, headdim 64
+// 197 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
 // takes them some 2400 cycles, of which its 128 x 128 exponentials need 512 of
 // the special function units'; what is left is latency (waits that find their
 // barrier complete, TMEM round trips) and the fetching of instructions, five

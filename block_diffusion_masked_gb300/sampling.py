@@ -152,7 +152,8 @@ class KVCache:
 
     def attend(self, q, step, k=None, v=None, block_size=1, **kwargs):
         """Attention of the step's rows over the tokens held before it and, with
-        k and v, over their own blocks; returns (out, lse) (``dfa_cache_forward``)."""
+        k and v, over their own blocks; returns (out, lse), detached from autograd
+        (``dfa_cache_forward``)."""
         return binding.dfa_cache_forward(q, self.k, self.v, self.k_scale, self.v_scale,
                                          step.block_table, step.cache_lens, step.cu_new,
                                          step.max_new, k=k, v=v, block_size=block_size, **kwargs)

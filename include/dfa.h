@@ -427,6 +427,9 @@ int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int 
  * block, seen both ways; block_size 1 is causal.  q (rows, heads, headdim)
  * bf16, strides as for the append; out (rows, heads, headdim) bf16 contiguous,
  * lse (heads, rows) float32.  A row that sees no key gets out 0 and lse -inf.
+ * Probabilities are rounded to f16 against cached values (2^-11; a value below
+ * 2^-30 of the largest cached ones may be lost beside them) and to bf16 against
+ * own ones (2^-8); scores, sums and the output are float32 in between.
  * kv_heads divides heads, head h reads key/value head h / (heads / kv_heads).
  * batch <= 32768; the rows of one request, min(max_new, rows), are at most 2^24,
  * and 2^30 over heads / kv_heads.  With max_new 0 nothing is read or written.
