@@ -17,7 +17,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128; }
-bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool aligned_to(const void* p, unsigned n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
 
 // ------------------------------------------------------------------ plan
 
@@ -143,7 +145,8 @@ __global__ void __launch_bounds__(kPlanThreads) dfa_cache_plan_kernel(const Plan
       p.cu_new[b] = static_cast<int>(r0);
       if (b == p.batch - 1) p.cu_new[p.batch] = static_cast<int>(r1);
       const long long before = carry.pages + upto.pages - mine.pages;
-      const long long got = before >= top ? 0 : before + mine.pages > top ? top - before : mine.pages;
+      const long long left = before >= top ? 0 : top - before;
+      const long long got = mine.pages > left ? left : mine.pages;
       const long long cap = (has + got) * p.page_size;
       const long long next = len + mine.rows;
       p.next_lens[b] = static_cast<int>(next < cap ? next : cap);
@@ -202,7 +205,11 @@ struct ReleaseParams {
 
 // Finished requests give their pages back: pushed on the free stack in the
 // order of the requests and of their pages, table entries set to -1, lengths
-// to 0.  One CTA; a warp takes one request of a group of 16 at a time.
+// to 0.  One CTA; a warp takes one request of a group of 16 at a time: bound by
+// the chain of trips to memory of a group, 64 groups one after another for 1024
+// requests.  Measured: half of 8 requests of up to 2000 tokens (81 pages of 64)
+// 5 us, half of 64 of up to 8000 (2020 pages) 11, half of 1024 of up to 16000
+// (62.7 k pages) 190.
 __global__ void __launch_bounds__(kPlanThreads) dfa_cache_release_kernel(const ReleaseParams p) {
   constexpr int kWarps = kPlanThreads / 32;
   __shared__ int s_count[kWarps];

@@ -54,7 +54,9 @@ DFA_HD bool cache_page_ok(int page, int num_pages) { return page >= 0 && page < 
 // units, and the pieces are joined afterwards; the block that reaches the
 // finish units has the segment's end, a run that begins inside them skips the
 // rest.
-DFA_HD int cache_key_units(int len, int unit) { return unit > 0 && len > 0 ? (len - 1) / unit + 1 : 0; }
+DFA_HD int cache_key_units(int len, int unit) {
+  return unit > 0 && len > 0 ? (len - 1) / unit + 1 : 0;
+}
 DFA_HD int cache_units(int len, int n, int unit, int finish) {
   return n > 0 ? cache_key_units(len, unit) + finish : 0;
 }

@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     const int full = isv ? C::BAR_VFULL : C::BAR_KFULL, empty = full + 2;
     const uint32_t tiles0 = sbase + (isv ? C::kOffV : C::kOffK);
     const uint32_t raw0 = sbase + C::kOffRaw + (isv ? RS * C::kRaw : 0);
-    const int rawfull = C::BAR_RAWFULL + (isv ? RS : 0), rawempty = C::BAR_RAWEMPTY + (isv ? RS : 0);
+    const int rawfull = C::BAR_RAWFULL + (isv ? RS : 0);
+    const int rawempty = C::BAR_RAWEMPTY + (isv ? RS : 0);
     // e4m3 -> f16: a thread turns 16 values (a 16-byte piece) into two pieces
     // of its row.  Eight lanes, one phase of a shared-memory access, take four
     // neighbouring pieces of rows r and r ^ 5: under either tile's swizzle
@@ -420,7 +421,8 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
         const int at = i * 128 + c, row = at / (D / 8), u = at % (D / 8);
         const int r = min(k.row_base + row, k.R - 1);
         const int tok = r / p.G, hq = k.h * p.G + (r - tok * p.G);
-        copy16_async(sbase + C::kOffQ + (u >> 3) * (C::BM * 128) + row * 128 + (((u ^ row) & 7) << 4),
+        const uint32_t to = (u >> 3) * (C::BM * 128) + row * 128 + (((u ^ row) & 7) << 4);
+        copy16_async(sbase + C::kOffQ + to,
                      p.q + (x.rq.row0 + tok) * p.q_sr + hq * p.q_sh + 8 * u,
                      k.row_base + row < k.R);
       }
@@ -546,7 +548,8 @@ __global__ void __launch_bounds__(WideCfg<D, RS>::kThreads, 1)
     const int lb = (warp & 3) * 32 + (warp >> 2) * 16;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(lb) << 16);
     bool ok = true;
-    int n = 0, cached = 0, owns = 0, q = 0;  // tiles, cached ones, pieces with own keys, versions of Q
+    // tiles, cached ones, pieces with own keys, versions of Q
+    int n = 0, cached = 0, owns = 0, q = 0;
     for (; w.b >= 0 && ok; next_piece(p, w)) {
       const Tiles k = tiles_of(w);
       const int r = k.row_base + lb + (lane & 15);  // row of the request and head
