@@ -82,7 +82,13 @@ class Step:
     next_free: torch.Tensor
     missing: torch.Tensor     # (1,) pages that were not to be had
     max_new: int
-    turn: int = 0             # the page table's at the plan; negative: at the advance
+    # the page table's turn at the plan, negative: at the advance; 0: not known,
+    # for replays of a captured plan are not seen on the host
+    turn: int = 0
+
+
+def _capturing(t):
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
 
 
 class PageTable:
@@ -108,22 +114,24 @@ class PageTable:
                                      self.free_count, self.page_size, rows)
         table, cu_new, positions, next_lens, next_free, missing = got
         return Step(cu_new, positions, self.cache_lens, table, next_lens, next_free, missing,
-                    max_new, self._turn)
+                    max_new, 0 if _capturing(new_lens) else self._turn)
 
     def advance(self, step):
         """The step's tokens are in the caches: they count as held from now on.
         Copied in place, so captured graphs see the new lengths.
 
         A step that was planned before the last :meth:`advance` or :meth:`release`
-        is refused: its lengths and free pages are not the table's any more.
-        (Graphs are not looked into: a release between the replay of a plan and
-        that of its advance loses pages.)"""
-        if step.turn == self._turn:
+        is refused: its lengths and free pages are not the table's any more.  Not
+        so the step of a plan that was captured into a graph, which each replay
+        plans anew: there a release between the plan's replay and the advance
+        loses pages."""
+        if step.turn != -self._turn:  # not the one whose advance came last
+            if step.turn not in (0, self._turn):
+                raise ValueError("the step was planned before the last advance or release: "
+                                 "plan it again")
             self._turn += 1
-            step.turn = -self._turn
-        elif step.turn != -self._turn:  # nor the one whose advance came last
-            raise ValueError("the step was planned before the last advance or release: "
-                             "plan it again")
+            if step.turn:
+                step.turn = -self._turn
         self.cache_lens.copy_(step.next_lens)
         self.free_count.copy_(step.next_free)
 

@@ -885,3 +885,27 @@ def test_arguments_past_32_bits(b):
     with pytest.raises(b.DfaError):
         b.dfa_cache_release(state[1], state[0], *state[2:], 2 ** 32 + 16)
     assert b.dfa_status() == 0
+
+
+def test_captured_plan_advanced_outside_its_graph(b):
+    """A graph of the plan alone, replayed; advances and releases between replays."""
+    from block_diffusion_masked_gb300 import PageTable
+
+    pages = PageTable(2, 8, 12, 16)
+    new = _i32([20, 5])
+    pages.plan(new, 25, 20)  # warm-up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step = pages.plan(new, 25, 20)
+    for lens in ([20, 5], [40, 10]):
+        graph.replay()
+        pages.advance(step)
+        assert pages.cache_lens.tolist() == lens
+    pages.release(_i32([1, 0]))
+    graph.replay()
+    pages.advance(step)
+    assert b.dfa_status() == 0
+    assert pages.cache_lens.tolist() == [20, 15] and int(pages.free_count) == 12 - 2 - 1
+    held = pages.block_table[0, :2].tolist() + pages.block_table[1, :1].tolist()
+    assert sorted(held + pages.free_pages[:9].tolist()) == list(range(12))

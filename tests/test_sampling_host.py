@@ -397,3 +397,28 @@ def test_rotary_table_by_parts(base, rot, length):
         assert abs(t[1, i] - m * math.cos(a)) <= 2.0 ** -23
         assert abs(t[1, rot // 2 + i] - m * math.sin(a)) <= 2.0 ** -23
     assert between
+
+
+def test_captured_plans_are_not_refused(monkeypatch):
+    """A replay plans anew without the host: the captured step may be advanced
+    after every one, releases in between or not, and makes other steps stale."""
+    from block_diffusion_masked_gb300 import PageTable, sampling
+
+    def plan(lens, new, table, free, count, ps, rows):
+        return table, None, None, lens + new, count - 1, None
+
+    monkeypatch.setattr(sampling.binding, "dfa_cache_plan", plan)
+    monkeypatch.setattr(sampling.binding, "dfa_cache_release", lambda *a: None)
+    pages = PageTable(2, 4, 8, 16, device="cpu")
+    new = torch.tensor([3, 1], dtype=torch.int32)
+    with monkeypatch.context() as m:
+        m.setattr(sampling, "_capturing", lambda t: True)
+        captured = pages.plan(new, 4, 3)
+    eager = pages.plan(new, 4, 3)
+    pages.advance(captured)
+    with pytest.raises(ValueError):
+        pages.advance(eager)
+    pages.release(new)
+    captured.next_lens += new  # what a replay does
+    pages.advance(captured)
+    assert pages.cache_lens.tolist() == [6, 2]
