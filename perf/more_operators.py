@@ -1,0 +1,570 @@
+"""More operators of a block-diffusion sampler and its training, as calls to be measured.
+
+Two groups: a key/value cache in 4 bits (append, reading back, attention over
+it; reading the 8-bit cache back too), and the scores of tokens from logits
+(log probability, entropy, the likeliest alternatives, and the gradient).
+``run`` computes each in elementary torch operations, or, where ``own`` is
+true, through the package.
+
+4-bit cache: k_cache, v_cache (pages, kv_heads, page_size, headdim / 2) bytes,
+byte i of a token holding the codes n of dims 2i (low half) and 2i + 1;
+k_scale, v_scale (pages, kv_heads, headdim / 32, page_size) e5m2, a signed
+scale s for every token and 32 dims: a value is (n - 8) s.  s is the group's
+largest magnitude over 8, rounded up to three significant bits, within
+[2^-14, 896], negative where that magnitude is a positive value's alone (its
+code is then the lower one, -8 having no counterpart); n - 8 is x / s, to the
+nearest, ties away from 0, within [-8, 7].
+
+8-bit cache, block_table, cache_lens, cu_new: as in perf/operators.py.
+"""
+
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+GROUP = 32
+
+
+# ------------------------------------------------------------------ the cases
+
+def listed():
+    return [
+        # one token for each of 64 requests, kept and looked at as the cache holds it: latency
+        dict(name="append4 one token", op="append", B=64, ctx=1000, new=1, Hk=8, d=128, ps=64,
+             fused=True),
+        # the prompts of 8 requests
+        dict(name="append4 prompts", op="append", B=8, ctx=0, new=8190, Hk=8, d=128, ps=64,
+             fused=False),
+        # a few requests' last finished blocks, from the 8-bit cache: latency
+        dict(name="read last blocks", op="read", bits=8, B=5, ctx=700, rows=32, Hk=4, d=64, ps=64),
+        # requests that leave the GPU for a while: all of their tokens
+        dict(name="read4 requests", op="read", bits=4, B=7, ctx=16000, rows=16000, Hk=8, d=128,
+             ps=32),
+        # one request, one token that was appended before: the latency of a step
+        dict(name="attn4 one token", op="attn", B=1, ctx=500, new=1, H=16, Hk=4, d=128, ps=64, bs=1,
+             ragged=False, mine=False),
+        # a full batch of long requests, block_size 1: four rows to a key
+        dict(name="attn4 many requests", op="attn", B=64, ctx=16000, new=1, H=32, Hk=8, d=128,
+             ps=64, bs=1, ragged=True, mine=True),
+        # ragged batch, blocks of 4 as in the mid workload: 16 rows to a key
+        dict(name="attn4 blocks of 4", op="attn", B=24, ctx=8000, new=4, H=32, Hk=8, d=128, ps=64,
+             bs=4, ragged=True, mine=True),
+        # blocks of 32 with four query heads to a key head: 128 rows to a key
+        dict(name="attn4 blocks of 32", op="attn", B=32, ctx=8192, new=32, H=32, Hk=8, d=128, ps=64,
+             bs=32, ragged=True, mine=True),
+        # the positions of a few blocks of 4, their 8 likeliest tokens: the latency of a step
+        dict(name="scores of 5 blocks", op="scores", rows=20, V=32768, top=8, dtype="bfloat16",
+             pad=0, back=False, ent=False),
+        # every position of a long draft, float32 logits cut out of a padded vocabulary
+        dict(name="scores of a draft", op="scores", rows=511, V=131001, top=32, dtype="float32",
+             pad=71, back=False, ent=False),
+        # the loss of the mid workload's noisy half (4 x 2048 positions), odd vocabulary
+        dict(name="loss mid", op="scores", rows=8192, V=50001, top=0, dtype="bfloat16", pad=0,
+             back=True, ent=False),
+        # the same with a weight on the entropy, a small vocabulary in half precision
+        dict(name="loss small", op="scores", rows=130, V=4099, top=0, dtype="float16", pad=0,
+             back=True, ent=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "read", "attn", "attn", "scores", "scores"])
+    ps = rng.choice([16, 32, 64, 128])
+    d = rng.choice([64, 128, 256])
+    if op == "append":
+        B = _log(rng, 1, 128)
+        return dict(op=op, B=B, ctx=_log(rng, 1, 4000), new=_log(rng, 1, min(8190, 32768 // B)),
+                    Hk=rng.choice([1, 2, 4, 8]), d=d, ps=ps, fused=rng.random() < 0.5)
+    if op == "read":
+        B, Hk = _log(rng, 1, 32), rng.choice([1, 2, 4, 8])
+        ctx = _log(rng, 1, min(16000, 7 * 16000 * 8 * 128 // (B * Hk * d)))
+        return dict(op=op, bits=rng.choice([4, 8]), B=B, ctx=ctx, rows=_log(rng, 1, ctx), Hk=Hk,
+                    d=d, ps=ps)
+    if op == "attn":
+        Hk, G = rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 4, 8])
+        B, new = _log(rng, 1, 64), _log(rng, 1, 64)
+        ctx = _log(rng, 1, 131000)
+        # at most the keys and the products of the largest listed cases
+        ctx = max(1, min(ctx, 64 * 16000 * 8 * 128 // (B * Hk * d), 2 ** 28 // (B * Hk * G * new)))
+        return dict(op=op, B=B, ctx=ctx, new=new, H=Hk * G, Hk=Hk, d=d, ps=ps,
+                    bs=rng.choice([1, 4, new, new]), ragged=rng.random() < 0.6,
+                    mine=rng.random() < 0.8)
+    V = _log(rng, 2, 131072)
+    back = rng.random() < 0.5
+    rows = min(_log(rng, 1, 8192), 2 ** 28 // V if back else 2 ** 26 // V)
+    return dict(op=op, rows=rows, V=V, top=0 if back else rng.choice([0, 1, 5, 16, 32]),
+                dtype=rng.choice(["bfloat16", "float16", "float32"]),
+                pad=rng.choice([0, 0, 1, 24]), back=back, ent=rng.random() < 0.5)
+
+
+def _lens(case):
+    """Tokens cached and new of each request: from the case alone."""
+    B, ctx, new = case["B"], case["ctx"], case.get("new", 0)
+    if case["op"] == "attn" and not case["ragged"]:
+        return [ctx] * B, [new] * B
+    old = [int(ctx * (0.25 + 0.75 * ((0.6180339887 * b) % 1.0))) for b in range(B)]
+    old[0] = ctx
+    add = [new] * B
+    if B > 6:
+        old[3] = 0              # a request that has just begun
+        add[5] = 0              # one that has nothing to add
+        add[6] = (new + 1) // 2  # a short last block
+    return old, add
+
+
+def _spans(case):
+    """First token and number of tokens that are read of each request."""
+    old, _ = _lens(case)
+    n = [min(o, case["rows"]) for o in old]
+    return old, [o - x for o, x in zip(old, n)], n
+
+
+def _token_bytes(d, bits):
+    """Bytes of a token and head, keys or values: the 8-bit cache's scales are its pages'."""
+    return d if bits == 8 else d // 2 + d // GROUP
+
+
+def work(case):
+    op = case["op"]
+    if op == "scores":
+        n, e = case["rows"] * case["V"], 4 if case["dtype"] == "float32" else 2
+        passes = 2 if case["back"] else 1  # the logits, and their gradient
+        return {"bytes": passes * n * e + case["rows"] * (16 + 8 * case["top"]),
+                "flops": (10 if case["back"] else 5) * n}
+    Hk, d = case["Hk"], case["d"]
+    if op == "read":
+        n = sum(_spans(case)[2])
+        return {"bytes": 2 * n * Hk * (_token_bytes(d, case["bits"]) + 2 * d),
+                "flops": 2 * n * Hk * d}
+    old, add = _lens(case)
+    if op == "append":  # the rows in, the cache's bytes out and in, the values out
+        return {"bytes": 2 * sum(add) * Hk * (4 * d + 2 * _token_bytes(d, 4)),
+                "flops": 6 * sum(add) * Hk * d}
+    H = case["H"]
+    keys = sum(o for o, a in zip(old, add) if a)
+    pairs = sum(a * o + case["mine"] * _own_pairs(o, a, case["bs"]) for o, a in zip(old, add))
+    return {"bytes": 2 * keys * Hk * _token_bytes(d, 4)
+            + sum(add) * (4 * (H + case["mine"] * Hk) * d + 4 * H),
+            "flops": 4 * pairs * H * d}
+
+
+def _own_pairs(o, a, bs):
+    """Pairs of own rows and own keys of the rows' blocks or earlier ones."""
+    return sum(min(a, ((o + i) // bs + 1) * bs - o) for i in range(a))
+
+
+# ------------------------------------------------------------------ the inputs
+
+def _gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV, dtype=torch.float32)
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _scan(x):
+    return [0] + torch.tensor(x).cumsum(0).tolist()
+
+
+def _pages(case, old, add, g):
+    """Page numbers in random order for every request, unused entries -1."""
+    ps = case["ps"]
+    need = [-(-(o + a) // ps) for o, a in zip(old, add)]
+    maxp = max(1, max(need))
+    total = sum(need) + 3
+    perm = torch.randperm(total, generator=g, device=DEV).to(torch.int32)
+    start = _ints(_scan(need)[:-1])[:, None]
+    j = torch.arange(maxp, device=DEV)
+    table = perm[(start + j).clamp(max=total - 1).long()]
+    return torch.where(j < _ints(need)[:, None], table, -1).to(torch.int32).contiguous(), total
+
+
+def _cache(case, g, pages, old, table):
+    """Pages of random keys or values, as tokens leave them; what lies behind a
+    request's last token is not a number."""
+    Hk, ps, d = case["Hk"], case["ps"], case["d"]
+    x = _randn(g, pages, Hk, ps, d)
+    x *= torch.exp(0.5 * _randn(g, pages, Hk, ps, 1))
+    j = torch.arange(table.shape[1], device=DEV)
+    left = (_ints(old)[:, None] - j * ps).clamp(0, ps)            # tokens of each page
+    page = torch.where(table >= 0, table, pages).long()
+    keep = torch.zeros(pages + 1, device=DEV, dtype=torch.int64)
+    keep[page.reshape(-1)] = left.reshape(-1).long()
+    dead = torch.arange(ps, device=DEV) >= keep[:pages, None]
+    if case.get("bits", 4) == 8:
+        m, e = torch.frexp(x.abs().amax((2, 3)))  # the smallest 2^e with amax <= 448 * 2^e
+        scale = _pow2(torch.where(m <= 0.875, e - 9, e - 8))
+        c = (x / scale[:, :, None, None]).to(torch.float8_e4m3fn)
+        c.view(torch.uint8).masked_fill_(dead[:, None, :, None], 0x7F)
+        return c, scale
+    codes, scale = _encode(x)
+    scale = scale.transpose(2, 3).contiguous().to(torch.float8_e5m2)
+    scale.view(torch.uint8).masked_fill_(dead[:, None, None, :], 0x7F)
+    return codes, scale
+
+
+def prepare(case, seed):
+    g, op = _gen(seed), case["op"]
+    if op == "scores":
+        return _prepare_scores(case, g)
+    Hk, d, ps = case["Hk"], case["d"], case["ps"]
+    if op == "read":
+        old, first, n = _spans(case)
+        table, total = _pages(case, old, [0] * len(old), g)
+        kc, ks = _cache(case, g, total, old, table)
+        vc, vs = _cache(case, g, total, old, table)
+        return dict(op=op, bits=case["bits"], kc=kc, ks=ks, vc=vc, vs=vs, table=table,
+                    lens=_ints(old), first=_ints(first), cu=_ints(_scan(n)), rows=sum(n), ps=ps)
+    old, add = _lens(case)
+    table, total = _pages(case, old, add, g)
+    kc, ks = _cache(case, g, total, old, table)
+    vc, vs = _cache(case, g, total, old, table)
+    rows = sum(add)
+    amp = torch.exp(0.5 * _randn(g, rows, Hk, 1))
+    kv = _randn(g, rows, 2 * Hk, d)
+    k, v = (kv[:, :Hk] * amp).bfloat16(), (kv[:, Hk:] * amp).bfloat16()
+    if case.get("fused"):  # views of one projection's output
+        kv = torch.cat([k, v], 1)
+        k, v = kv[:, :Hk], kv[:, Hk:]
+    s = dict(op=op, kc=kc, ks=ks, vc=vc, vs=vs, table=table, lens=_ints(old), cu=_ints(_scan(add)),
+             k=k, v=v, max_new=max(add), ps=ps, rows=rows)
+    if op == "append":
+        return dict(s, next=_ints([o + a for o, a in zip(old, add)]))
+    q = _randn(g, rows, case["H"], d).bfloat16()
+    if not case["mine"]:  # the rows' own tokens are in the cache, or are none of its
+        s["k"] = s["v"] = None
+    return dict(s, q=q, bs=case["bs"], ctx=max(old))
+
+
+def _prepare_scores(case, g):
+    rows, V = case["rows"], case["V"]
+    x = torch.empty((rows, V + case["pad"]), dtype=getattr(torch, case["dtype"]), device=DEV)
+    x.copy_(_randn(g, rows, V + case["pad"]))
+    # rows between nearly even and nearly certain ones
+    x *= 1 + 3 * torch.rand((rows, 1), generator=g, device=DEV).to(x.dtype)
+    x = x[:, :V]
+    tokens = torch.randint(0, V, (rows,), generator=g, device=DEV)
+    if V > 2:  # the mask's own token is never an answer
+        x[:, V // 3] = -math.inf
+        tokens = torch.where(tokens == V // 3, tokens + 1, tokens)
+    if case["back"]:  # positions that were not masked take no part in the loss
+        tokens = torch.where(torch.rand((rows,), generator=g, device=DEV) < 0.5, tokens, -1)
+    s = dict(op="scores", x=x, tokens=tokens, top=case["top"], back=case["back"], ge=None)
+    if case["back"]:
+        s["x"] = x.detach().requires_grad_()
+        s["gl"] = -torch.rand((rows,), generator=g, device=DEV) * (tokens >= 0)
+        if case["ent"]:
+            s["ge"] = 0.1 * torch.rand((rows,), generator=g, device=DEV)
+    return s
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(state):
+    return {"append": _append, "read": _read, "attn": _attn, "scores": _scores}[state["op"]](state)
+
+
+def _pow2(e):
+    """2^e as float32, -126 <= e <= 127, from its bits."""
+    return ((e + 127) << 23).to(torch.int32).view(torch.float32)
+
+
+def _encode(x):
+    """Codes and scales of float32 values (..., d): bytes (..., d / 2), float32 (..., d / 32)."""
+    y = x.unflatten(-1, (-1, GROUP))
+    hi, lo = y.amax(-1), -y.amin(-1)
+    m, e = torch.frexp(torch.maximum(hi, lo) / 8)  # m * 2^e, 0.5 <= m < 1
+    s = (torch.ceil(m * 8) / 8 * _pow2(e)).clamp(2.0 ** -14, 896)
+    s = torch.where(hi > lo, -s, s)
+    n = y / s[..., None]
+    n = (torch.sign(n) * torch.floor(n.abs() + 0.5)).clamp(-8, 7) + 8
+    n = n.to(torch.uint8).flatten(-2)
+    return n[..., 0::2] | n[..., 1::2] << 4, s
+
+
+def _decode(codes, scale):
+    """Values of bytes (..., d / 2) and float32 scales (..., d / 32)."""
+    n = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).float() - 8
+    return (n.unflatten(-1, (-1, GROUP)) * scale[..., None]).flatten(-2)
+
+
+def _tokens(cache, scale, page, at):
+    """Float32 values of the tokens `at` of pages `page`: (..., kv_heads, d)."""
+    if cache.dtype == torch.uint8:
+        return _decode(cache[page, :, at], scale.view(torch.uint8)[page, :, :, at]
+                       .view(torch.float8_e5m2).float())
+    x = cache.view(torch.uint8)[page, :, at].view(torch.float8_e4m3fn).float()
+    return x * scale[page][..., None]
+
+
+def _row_owner(cu, rows):
+    r = torch.arange(rows, device=cu.device)
+    b = torch.searchsorted(cu[1:].contiguous(), r, right=True).clamp(max=cu.numel() - 2)
+    return b, r - cu[b]
+
+
+def _append(s):
+    if own:
+        from block_diffusion_masked_gb300 import binding
+
+        binding.dfa_cache4_append(s["k"], s["v"], s["cu"], s["lens"], s["table"], s["kc"], s["vc"],
+                                  s["ks"], s["vs"], s["max_new"])
+        k, v = binding.dfa_cache4_read(s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["next"],
+                                       s["cu"], s["rows"], first=s["lens"])
+        return [k, v, s["kc"], s["vc"], s["ks"], s["vs"]]
+    ps = s["ps"]
+    b, i = _row_owner(s["cu"].long(), s["rows"])
+    pos = s["lens"].long()[b] + i
+    page, at = s["table"][b, pos // ps].long(), pos % ps
+    got = [_append_one(s["k"], s["kc"], s["ks"], page, at),
+           _append_one(s["v"], s["vc"], s["vs"], page, at)]
+    return got + [s["kc"], s["vc"], s["ks"], s["vs"]]
+
+
+def _append_one(x, cache, scale, page, at):
+    codes, s = _encode(x.float())
+    cache[page, :, at] = codes
+    scale.view(torch.uint8)[page, :, :, at] = s.to(torch.float8_e5m2).view(torch.uint8)
+    return _decode(codes, s).to(x.dtype)
+
+
+def _read(s):
+    if own:
+        from block_diffusion_masked_gb300 import binding
+
+        read = binding.dfa_cache4_read if s["bits"] == 4 else binding.dfa_cache_read
+        return list(read(s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"], s["cu"],
+                         s["rows"], first=s["first"]))
+    b, i = _row_owner(s["cu"].long(), s["rows"])
+    pos = s["first"].long()[b] + i
+    page, at = s["table"][b, pos // s["ps"]].long(), pos % s["ps"]
+    return [_tokens(s["kc"], s["ks"], page, at).bfloat16(),
+            _tokens(s["vc"], s["vs"], page, at).bfloat16()]
+
+
+def _attn(s):
+    if own:
+        from block_diffusion_masked_gb300 import binding
+
+        return list(binding.dfa_cache4_forward(
+            s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"], s["cu"],
+            s["max_new"], k=s["k"], v=s["v"], block_size=s["bs"]))
+    q, ps, bs, T, S = s["q"], s["ps"], s["bs"], s["max_new"], s["ctx"]
+    rows, H, d = q.shape
+    Hk = s["kc"].shape[1]
+    lens, cu = s["lens"].long(), s["cu"].long()
+    B = lens.numel()
+    at = torch.arange(S, device=q.device)
+    page = s["table"][:, at // ps].clamp(min=0).long()
+    row = (cu[:-1, None] + torch.arange(T, device=q.device)).clamp(max=rows - 1)
+    seen = at < lens[:, None]
+
+    def keys(cache, scale, mine):
+        x = _tokens(cache, scale, page, (at % ps).expand(B, S))
+        x.masked_fill_(~seen[:, :, None, None], 0.0)
+        if mine is not None:
+            x = torch.cat([x, mine[row].float()], 1)
+        return x.transpose(1, 2)  # (B, Hk, S + T, d)
+
+    qg = q[row].float().view(B, T, Hk, H // Hk, d).permute(0, 2, 3, 1, 4).reshape(B, Hk, -1, d)
+    w = (qg @ keys(s["kc"], s["ks"], s["k"]).transpose(2, 3)) / math.sqrt(d)
+    i = torch.arange(T, device=q.device)
+    there = i < (cu[1:] - cu[:-1])[:, None]
+    blk = (lens[:, None] + i) // bs
+    mine = there[:, None, :] & (blk[:, None, :] <= blk[:, :, None])
+    see = seen[:, None, :].expand(B, T, S)
+    if s["k"] is not None:
+        see = torch.cat([see, mine], 2)
+    see = see[:, None, None].expand(B, 1, H // Hk, T, -1).reshape(B, 1, H // Hk * T, -1)
+    w = w.masked_fill_(~see, -math.inf)
+    m = w.amax(-1, keepdim=True).clamp(min=-1e30)
+    w = w.sub_(m).exp_()
+    den = w.sum(-1, keepdim=True)
+    o = (w @ keys(s["vc"], s["vs"], s["v"])) / den.clamp(min=1e-38)
+    lse = torch.where(den > 0, m + den.log(), -math.inf)
+    shape = (B, Hk, H // Hk, T)
+    o = o.view(*shape, d).permute(0, 3, 1, 2, 4).reshape(B, T, H, d)
+    lse = lse.view(shape).permute(0, 3, 1, 2).reshape(B, T, H)
+    b, i = _row_owner(cu, rows)
+    return [o[b, i].to(q.dtype), lse[b, i].t().contiguous()]
+
+
+def _scores(s):
+    x, t, top = s["x"], s["tokens"], s["top"]
+    if own:
+        import block_diffusion_masked_gb300 as m
+
+        got = m.token_logprobs_func(x, t, top=top)
+        if not s["back"]:
+            return list(got) if top else list(got[:2])
+        outs, gs = (got[:2], (s["gl"], s["ge"])) if s["ge"] is not None else (got[:1], (s["gl"],))
+        return [*got[:2], *torch.autograd.grad(outs, (x,), gs)]
+    x = x.detach()
+    y = x.float()
+    y = y - y.amax(-1, keepdim=True)
+    p = y.exp()
+    den = p.sum(-1, keepdim=True)
+    p /= den
+    y -= den.log()  # log probabilities
+    ent = -(p * y.clamp(min=-1e4)).sum(-1)
+    at = t.clamp(min=0)[:, None]
+    lp = torch.where(t >= 0, y.gather(1, at)[:, 0], 0.0)
+    if top:
+        best, which = torch.sort(y, dim=-1, descending=True, stable=True)
+        k = min(top, y.shape[1])
+        lack = (0, top - k)  # alternatives that a small vocabulary does not have
+        best = torch.nn.functional.pad(best[:, :k], lack, value=-math.inf)
+        which = torch.where(best > -math.inf,
+                            torch.nn.functional.pad(which[:, :k], lack, value=-1), -1)
+        return [lp, ent, best, which.to(torch.int32)]
+    if not s["back"]:
+        return [lp, ent]
+    gl = (s["gl"] * (t >= 0))[:, None]
+    g = -gl * p
+    if s["ge"] is not None:
+        g -= s["ge"][:, None] * p * (y.clamp(min=-1e4) + ent[:, None])
+    g.scatter_add_(1, at, gl)
+    return [lp, ent, g.to(x.dtype)]
+
+
+# ------------------------------------------------------------------ in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"append": _exact_append, "read": _exact_read, "attn": _exact_attn,
+            "scores": _exact_scores}[s["op"]](s)
+
+
+def _exact_quantised(x):
+    """Codes 0 .. 15 and scales of one request's rows (n, kv_heads, d), in 64 bits."""
+    x = x.double().unflatten(-1, (-1, GROUP))
+    top = x.abs().amax(-1)
+    # three significant bits: a grid of 4, 5, 6, 7 times a power of two, by comparison
+    grid = torch.tensor([m * 2.0 ** e for e in range(-16, 8) for m in (4, 5, 6, 7)],
+                        dtype=torch.float64, device=x.device)
+    grid = grid[(grid >= 2.0 ** -14) & (grid <= 896)]
+    at = torch.searchsorted(grid, top / 8).clamp(max=grid.numel() - 1)
+    s = grid[at]
+    positive = (x == top[..., None]).any(-1) & ~(x == -top[..., None]).any(-1)
+    s = torch.where(positive, -s, s)
+    z = x / s[..., None]
+    n = torch.trunc(z + torch.where(z < 0, -0.5, 0.5)).clamp(-8, 7)
+    return n, s
+
+
+def _exact_append(s):
+    kc, vc, ks, vs = (s[c].clone() for c in ("kc", "vc", "ks", "vs"))
+    got, ps = [], s["ps"]
+    cu, lens, table = s["cu"].tolist(), s["lens"].tolist(), s["table"].long()
+    for x, cache, scale in ((s["k"], kc, ks), (s["v"], vc, vs)):
+        n, sc = _exact_quantised(x)
+        code = (n + 8).long().flatten(-2)
+        both = (code[..., 0::2] + 16 * code[..., 1::2]).to(torch.uint8)
+        raw = sc.float().to(torch.float8_e5m2).view(torch.uint8)
+        for b, o in enumerate(lens):
+            pos = torch.arange(o, o + cu[b + 1] - cu[b], device=x.device)
+            page = table[b, pos // ps]
+            cache[page, :, pos % ps] = both[cu[b]:cu[b + 1]]
+            scale.view(torch.uint8)[page, :, :, pos % ps] = raw[cu[b]:cu[b + 1]]
+        got.append((n * sc[..., None]).flatten(-2))
+    return [*got, kc, vc, ks.double(), vs.double()]
+
+
+def _exact_pages(cache, scale, pages):
+    """Values (kv_heads, tokens, d) of whole pages, in 64 bits."""
+    if cache.dtype != torch.uint8:
+        x = cache[pages].double() * scale[pages].double()[:, :, None, None]
+    else:
+        c = cache[pages].long()
+        n = torch.empty((*c.shape[:-1], 2 * c.shape[-1]), dtype=torch.float64, device=c.device)
+        n[..., 0::2], n[..., 1::2] = c % 16 - 8, c // 16 - 8
+        x = n * scale[pages].double().transpose(2, 3).repeat_interleave(GROUP, -1)
+    return x.transpose(0, 1).reshape(x.shape[1], -1, x.shape[-1])
+
+
+def _exact_read(s):
+    cu, first, table, ps = s["cu"].tolist(), s["first"].tolist(), s["table"].long(), s["ps"]
+    got = []
+    for cache, scale in ((s["kc"], s["ks"]), (s["vc"], s["vs"])):
+        parts = []
+        for b, f in enumerate(first):
+            n = cu[b + 1] - cu[b]
+            p0 = f // ps
+            x = _exact_pages(cache, scale, table[b, p0:-(-(f + n) // ps)])
+            parts.append(x[:, f - p0 * ps:f - p0 * ps + n].transpose(0, 1))
+        got.append(torch.cat(parts))
+    return got
+
+
+def _exact_attn(s):
+    q, ps, bs = s["q"].double(), s["ps"], s["bs"]
+    rows, H, d = q.shape
+    Hk = s["kc"].shape[1]
+    out = torch.zeros(rows, H, d, dtype=torch.float64, device=q.device)
+    lse = torch.zeros(H, rows, dtype=torch.float64, device=q.device)
+    cu = s["cu"].tolist()
+    for b, n in enumerate(s["lens"].tolist()):
+        lo, hi = cu[b], cu[b + 1]
+        if lo == hi:
+            continue
+        pages = s["table"][b, :-(-n // ps)].long()
+
+        def side(cache, scale, new):
+            x = _exact_pages(cache, scale, pages)[:, :n]
+            return x if new is None else torch.cat([x, new[lo:hi].double().transpose(0, 1)], 1)
+
+        k, v = side(s["kc"], s["ks"], s["k"]), side(s["vc"], s["vs"], s["v"])
+        w = torch.einsum("ihgd,hjd->hgij", q[lo:hi].view(hi - lo, Hk, H // Hk, d), k) * d ** -0.5
+        if not w.shape[-1]:  # no key at all
+            lse[:, lo:hi] = -math.inf
+            continue
+        pos = torch.arange(n + hi - lo, device=q.device)
+        see = (pos[None] < n) | (pos[None] // bs <= pos[n:, None] // bs)
+        w = w.masked_fill(~see[:, :w.shape[-1]], -math.inf)
+        z = w.logsumexp(-1)
+        lse[:, lo:hi] = z.reshape(H, -1)
+        o = torch.einsum("hgij,hjd->ihgd", (w - z[..., None]).exp(), v)
+        out[lo:hi] = o.reshape(hi - lo, H, d)
+    return [out, lse]
+
+
+def _exact_scores(s):
+    """Some rows at a time: probabilities, then what follows from them."""
+    got = []
+    rows, V = s["x"].shape
+    for r in range(0, rows, max(1, 2 ** 27 // V)):
+        r = slice(r, min(rows, r + max(1, 2 ** 27 // V)))
+        x, t = s["x"].detach()[r].double(), s["tokens"][r]
+        lp = torch.log_softmax(x, -1)
+        p = lp.exp()
+        ent = -torch.special.xlogy(p, p).sum(-1)
+        hit = torch.arange(V, device=x.device) == t[:, None]
+        has = (t >= 0).double()
+        parts = [torch.where(hit, lp, 0.0).sum(-1), ent]
+        if s["top"]:
+            k = min(s["top"], V)
+            which = torch.sort(x, dim=-1, descending=True, stable=True)[1][:, :k]
+            best = torch.full((x.shape[0], s["top"]), -math.inf, dtype=torch.float64, device=DEV)
+            best[:, :k] = lp.gather(1, which)
+            ids = torch.full(best.shape, -1, dtype=torch.int32, device=DEV)
+            ids[:, :k] = which.to(torch.int32)
+            parts += [best, ids.masked_fill(best == -math.inf, -1)]
+        if s["back"]:
+            g = (s["gl"][r].double() * has)[:, None] * (hit.double() - p)
+            if s["ge"] is not None:  # d/dx of -sum p log p
+                g = g - s["ge"][r].double()[:, None] * (torch.special.xlogy(p, p) + p * ent[:, None])
+            parts.append(g)
+        got.append(parts)
+    return [torch.cat(c) for c in zip(*got)]
