@@ -7,8 +7,8 @@ it; reading the 8-bit cache back too), and the scores of tokens from logits
 true, through the package.
 
 4-bit cache: k_cache, v_cache (pages, kv_heads, page_size, headdim / 2) bytes,
-byte i of a token holding the codes n of dims 2i (low half) and 2i + 1;
-k_scale, v_scale (pages, kv_heads, headdim / 32, page_size) e5m2, a signed
+four of them for the codes n of eight neighbouring dims, in the order 0, 2, 4, 6, 1,
+3, 5, 7 from the lowest bits of the first byte to the highest of the last; k_scale, v_scale (pages, kv_heads, headdim / 32, page_size) e5m2, a signed
 scale s for every token and 32 dims: a value is (n - 8) s.  s is the group's
 largest magnitude over 8, rounded up to three significant bits, within
 [2^-14, 896], negative where that magnitude is a positive value's alone (its
@@ -290,13 +290,14 @@ def _encode(x):
     s = torch.where(hi > lo, -s, s)
     n = y / s[..., None]
     n = (torch.sign(n) * torch.floor(n.abs() + 0.5)).clamp(-8, 7) + 8
-    n = n.to(torch.uint8).flatten(-2)
+    n = n.to(torch.uint8).flatten(-2).unflatten(-1, (-1, 4, 2)).transpose(-1, -2).flatten(-3)
     return n[..., 0::2] | n[..., 1::2] << 4, s
 
 
 def _decode(codes, scale):
     """Values of bytes (..., d / 2) and float32 scales (..., d / 32)."""
-    n = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).float() - 8
+    n = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
+    n = n.unflatten(-1, (-1, 2, 4)).transpose(-1, -2).flatten(-3).float() - 8
     return (n.unflatten(-1, (-1, GROUP)) * scale[..., None]).flatten(-2)
 
 
@@ -470,8 +471,10 @@ def _exact_append(s):
     cu, lens, table = s["cu"].tolist(), s["lens"].tolist(), s["table"].long()
     for x, cache, scale in ((s["k"], kc, ks), (s["v"], vc, vs)):
         n, sc = _exact_quantised(x)
-        code = (n + 8).long().flatten(-2)
-        both = (code[..., 0::2] + 16 * code[..., 1::2]).to(torch.uint8)
+        code = (n + 8).long().flatten(-2).unflatten(-1, (-1, 8))
+        both = torch.stack([code[..., a] + 16 * code[..., b]
+                            for a, b in ((0, 2), (4, 6), (1, 3), (5, 7))], -1)
+        both = both.flatten(-2).to(torch.uint8)
         raw = sc.float().to(torch.float8_e5m2).view(torch.uint8)
         for b, o in enumerate(lens):
             pos = torch.arange(o, o + cu[b + 1] - cu[b], device=x.device)
@@ -487,9 +490,11 @@ def _exact_pages(cache, scale, pages):
     if cache.dtype != torch.uint8:
         x = cache[pages].double() * scale[pages].double()[:, :, None, None]
     else:
-        c = cache[pages].long()
-        n = torch.empty((*c.shape[:-1], 2 * c.shape[-1]), dtype=torch.float64, device=c.device)
-        n[..., 0::2], n[..., 1::2] = c % 16 - 8, c // 16 - 8
+        c = cache[pages].long().unflatten(-1, (-1, 4))
+        n = torch.empty((*c.shape[:-1], 8), dtype=torch.float64, device=c.device)
+        for i, (a, b) in enumerate(((0, 2), (4, 6), (1, 3), (5, 7))):
+            n[..., a], n[..., b] = c[..., i] % 16 - 8, c[..., i] // 16 - 8
+        n = n.flatten(-2)
         x = n * scale[pages].double().transpose(2, 3).repeat_interleave(GROUP, -1)
     return x.transpose(0, 1).reshape(x.shape[1], -1, x.shape[-1])
 
