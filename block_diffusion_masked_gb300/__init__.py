@@ -25,7 +25,7 @@ The binding is imported lazily so that ``inputs`` can be used without CUDA.
 from __future__ import annotations
 
 __all__ = ["diffusion_attn_func", "diffusion_attn_varlen_func", "causal_attn_func",
-           "rotary_func", "rotary_table", "PageTable", "KVCache", "binding"]
+           "rotary_func", "rotary_table", "token_logprobs_func", "PageTable", "KVCache", "binding"]
 
 
 def __getattr__(name):
@@ -34,8 +34,8 @@ def __getattr__(name):
     if name in ("rotary_table", "PageTable", "KVCache"):
         return getattr(importlib.import_module(__name__ + ".sampling"), name)
     if name in ("diffusion_attn_func", "diffusion_attn_varlen_func", "causal_attn_func",
-                "rotary_func", "DiffusionAttnFunc", "DiffusionAttnVarlenFunc", "CausalAttnFunc",
-                "RotaryFunc"):
+                "rotary_func", "token_logprobs_func", "DiffusionAttnFunc", "DiffusionAttnVarlenFunc", "CausalAttnFunc",
+                "RotaryFunc", "TokenLogprobsFunc"):
         return getattr(importlib.import_module(__name__ + ".autograd"), name)
     if name in ("binding", "autograd", "inputs", "build", "sampling"):
         return importlib.import_module(__name__ + "." + name)

@@ -110,6 +110,65 @@ def rotary_func(q, k, table, positions=None, interleaved=False, period=None):
                                   binding._rotary_sizes(q, k, table, positions, period), flags)
 
 
+class TokenLogprobsFunc(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top):
+        ctx.set_materialize_grads(False)
+        logprobs, entropy, stats, best, which = binding.dfa_token_logprobs(logits, tokens, top)
+        ctx.mark_non_differentiable(best, which)
+        ctx.save_for_backward(logits, tokens, stats, entropy)
+        return logprobs, entropy, best, which
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogprobs, dentropy, *_):
+        logits, tokens, stats, entropy = ctx.saved_tensors
+        if dlogprobs is None and dentropy is None:
+            return None, None, None
+        return binding.dfa_token_logprobs_backward(
+            logits, tokens, stats, entropy, None if dlogprobs is None else dlogprobs.contiguous(),
+            None if dentropy is None else dentropy.contiguous()), None, None
+
+
+def token_logprobs_func(logits, tokens=None, top=0):
+    """Log probabilities of tokens, entropies and the likeliest tokens from logits.
+
+    logits (..., V) bf16, f16 or f32; rows of a padded vocabulary (a slice of the last
+    dimension) are read in place.  ``tokens`` int32 or int64 (...,): a negative one
+    marks a row without a token, whose log probability is 0, with no gradient (the
+    positions of a block-diffusion loss that were not masked).  Returns float32
+    (logprobs, entropy) of shape (...,) -- logprobs None without tokens -- and
+    (..., top) top_logprobs and int32 top_tokens, in order, equal ones lowest index
+    first, -inf and -1 behind the last token that can be; top is at most 32.  A logit
+    of -inf is a token that cannot be; a row with a NaN or +inf gives NaN.
+
+    Log probabilities and entropies are differentiable in the logits, once; the
+    alternatives are not.  Arithmetic in float32, sums relative to the row's largest
+    logit; the gradient is rounded once, to the logits' type.
+    """
+    if not isinstance(logits, torch.Tensor) or logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError("logits must be a tensor (..., vocab)")
+    shape = logits.shape[:-1]
+    if tokens is not None:
+        if not isinstance(tokens, torch.Tensor) or tokens.shape != shape:
+            raise ValueError("tokens must have the logits' leading dimensions")
+        tokens = tokens.reshape(-1).contiguous()
+    if logits.dim() != 2:
+        logits = logits.reshape(-1, logits.shape[-1])
+    if logits.shape[1] > 1 and logits.stride(1) != 1 or logits.stride(0) < 0:
+        logits = logits.contiguous()
+    if torch.is_grad_enabled() and logits.requires_grad:
+        logprobs, entropy, best, which = TokenLogprobsFunc.apply(logits, tokens, top)
+    else:
+        logprobs, entropy, _, best, which = binding.dfa_token_logprobs(logits, tokens, top)
+    if len(shape) != 1:
+        if logprobs is not None:
+            logprobs = logprobs.view(shape)
+        entropy = entropy.view(shape)
+        best, which = best.view(*shape, top), which.view(*shape, top)
+    return logprobs, entropy, best, which
+
+
 class DiffusionAttnFunc(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, block_size):

@@ -30,6 +30,9 @@ DFA_NOISY_DIAG_PASS = 2
 DFA_ROTARY_INTERLEAVED = 1
 DFA_ROTARY_INVERSE = 2
 DFA_ROTARY_CLEAR = 4
+DFA_BF16 = 0
+DFA_F16 = 1
+DFA_F32 = 2
 MODE_DIFFUSION = 0
 MODE_CAUSAL = 1
 
@@ -60,6 +63,17 @@ _SIGNATURES = {
     "dfa_cache_append": (_I, [_P] * 9 + [_I] * 8 + [_P] * 3),
     "dfa_cache_workspace_bytes": (ctypes.c_longlong, [_I] * 8),
     "dfa_cache_forward": (_I, [_P] * 13 + [ctypes.c_longlong] + [_I] * 10 + [_P] * 4),
+    "dfa_cache_read": (_I, [_P] * 10 + [_I] * 7 + [_P]),
+    "dfa_cache4_append": (_I, [_P] * 9 + [_I] * 8 + [_P] * 3),
+    "dfa_cache4_workspace_bytes": (ctypes.c_longlong, [_I] * 8),
+    "dfa_cache4_forward": (_I, [_P] * 13 + [ctypes.c_longlong] + [_I] * 10 + [_P] * 4),
+    "dfa_cache4_read": (_I, [_P] * 10 + [_I] * 7 + [_P]),
+    "dfa_cache4_scale_byte": (_I, [ctypes.c_uint]),
+    "dfa_token_logprobs_workspace_bytes": (ctypes.c_longlong, [_I] * 4),
+    "dfa_token_logprobs": (_I, [_P] * 2 + [_I] + [_P] * 6 + [ctypes.c_longlong] + [_I] * 3
+                           + [ctypes.c_longlong, _I, _P]),
+    "dfa_token_logprobs_backward": (_I, [_P] * 2 + [_I] + [_P] * 5 + [_I] * 2
+                                    + [ctypes.c_longlong, _I, _P]),
     "dfa_cache_scale_exp": (_I, [ctypes.c_uint]),
     "dfa_cache_page_ok": (_I, [_I] * 2),
     "dfa_cache_append_pages": (_I, [_I] * 2),
@@ -795,16 +809,21 @@ def dfa_cache_release(finished, cache_lens, block_table, free_pages, free_count,
           _int32(page_size))
 
 
-def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new, dev, d):
+def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new, dev, d,
+                 bits=8):
     """Shapes of a cache and its tables; returns (batch, kv_heads, page_size, pages, max_pages)."""
     shape = _check_dims(k_cache, 4, "k_cache")
     P, Hk, ps, dc = shape
-    if dc != d:
+    if dc * 8 != d * bits:
         raise ValueError("the cache must have the head dimension of the rows")
-    _check_dense(k_cache, shape, torch.float8_e4m3fn, dev, "k_cache")
-    _check_dense(v_cache, shape, torch.float8_e4m3fn, dev, "v_cache")
-    _check_dense(k_scale, (P, Hk), torch.float32, dev, "k_scale")
-    _check_dense(v_scale, (P, Hk), torch.float32, dev, "v_scale")
+    if bits == 8:
+        kind, scales, scale_kind = torch.float8_e4m3fn, (P, Hk), torch.float32
+    else:
+        kind, scales, scale_kind = torch.uint8, (P, Hk, d // 32, ps), torch.float8_e5m2
+    _check_dense(k_cache, shape, kind, dev, "k_cache")
+    _check_dense(v_cache, shape, kind, dev, "v_cache")
+    _check_dense(k_scale, scales, scale_kind, dev, "k_scale")
+    _check_dense(v_scale, scales, scale_kind, dev, "v_scale")
     B, maxp = _check_dims(block_table, 2, "block_table")
     _check_dense(block_table, (B, maxp), torch.int32, dev, "block_table")
     _check_dense(cache_lens, (B,), torch.int32, dev, "cache_lens")
@@ -818,34 +837,107 @@ def dfa_cache_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_
 
     ``max_new``: a bound on the rows of one request, known to the host.
     """
+    _append("dfa_cache_append", 8, k, v, cu_new, cache_lens, block_table, k_cache, v_cache,
+            k_scale, v_scale, max_new)
+
+
+def dfa_cache4_append(k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_scale, v_scale,
+                      max_new):
+    """dfa_cache_append for the 4-bit cache: k_cache, v_cache uint8 (pages, Hk,
+    page_size, d / 2), k_scale, v_scale float8_e5m2 (pages, Hk, d / 32, page_size)."""
+    _append("dfa_cache4_append", 4, k, v, cu_new, cache_lens, block_table, k_cache, v_cache,
+            k_scale, v_scale, max_new)
+
+
+def _append(fn, bits, k, v, cu_new, cache_lens, block_table, k_cache, v_cache, k_scale, v_scale,
+            max_new):
     rows, Hk, d = shape = _check_heads(k, 3, "k")
     dev = k.device
     vshape = _check_heads(v, 3, "v", dev)
     B, Hc, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
-                                      cu_new, dev, d)
+                                      cu_new, dev, d, bits)
     if vshape != shape or Hc != Hk:
         raise ValueError("k and v must be (rows, kv_heads, headdim) with the cache's heads")
-    _call("dfa_cache_append", dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
+    _call(fn, dev, k.data_ptr(), v.data_ptr(), cu_new.data_ptr(),
           cache_lens.data_ptr(), block_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), B, rows, _int32(max_new), Hk,
           d, ps, P, maxp, _strides(k, "k"), _strides(v, "v"))
 
 
+def dfa_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_rows, rows,
+                   first=None, k=None, v=None):
+    """Tokens read back from the 8-bit cache, packed (see dfa.h): request b's tokens
+    from first[b] (int32 (B,); None: 0) on in rows [cu_rows[b], cu_rows[b + 1]).
+
+    Returns k, v (rows, Hk, d) bf16, the cached values exactly.  ``cache_lens``: the
+    tokens held now.  Rows behind the last request's are not written.
+    """
+    return _read("dfa_cache_read", 8, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                 cu_rows, rows, first, k, v)
+
+
+def dfa_cache4_read(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_rows, rows,
+                    first=None, k=None, v=None):
+    """dfa_cache_read for the 4-bit cache (see dfa_cache4_append for its tensors)."""
+    return _read("dfa_cache4_read", 4, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                 cu_rows, rows, first, k, v)
+
+
+def _read(fn, bits, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_rows, rows,
+          first, k, v):
+    d = _check_dims(k_cache, 4, "k_cache")[3] * 8 // bits
+    dev = k_cache.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    B, Hk, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                                      cu_rows, dev, d, bits)
+    rows = int(rows)
+    if not 0 <= rows <= 1 << 30:
+        raise ValueError("rows must be 0 to 2^30")
+    if first is not None:
+        _check_dense(first, (B,), torch.int32, dev, "first")
+    shape = (rows, Hk, d)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_dense(k, shape, torch.bfloat16, dev, "k")
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_dense(v, shape, torch.bfloat16, dev, "v")
+    _call(fn, dev, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
+          None if first is None else first.data_ptr(), cu_rows.data_ptr(), k.data_ptr(),
+          v.data_ptr(), B, rows, Hk, d, ps, P, maxp)
+    return k, v
+
+
 def dfa_cache_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim, page_size,
                               max_pages):
     """Bytes of workspace dfa_cache_forward needs on the current device (0: none)."""
-    n = lib().dfa_cache_workspace_bytes(*map(_int32, (batch, rows, max_new, heads, kv_heads, headdim,
-                                                      page_size, max_pages)))
+    return _bytes("dfa_cache_workspace_bytes", batch, rows, max_new, heads, kv_heads, headdim,
+                  page_size, max_pages)
+
+
+def dfa_cache4_workspace_bytes(batch, rows, max_new, heads, kv_heads, headdim, page_size,
+                               max_pages):
+    """Bytes of workspace dfa_cache4_forward needs on the current device (0: none)."""
+    return _bytes("dfa_cache4_workspace_bytes", batch, rows, max_new, heads, kv_heads, headdim,
+                  page_size, max_pages)
+
+
+def _bytes(fn, *sizes):
+    n = getattr(lib(), fn)(*map(_int32, sizes))
     if n < 0:
-        raise DfaError("dfa_cache_workspace_bytes", int(n))
+        raise DfaError(fn, int(n))
     return int(n)
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_bytes(device_index, *sizes):
-    """dfa_cache_workspace_bytes on a device, which sizes alone determine."""
+def _workspace_bytes(bits, device_index, *sizes):
+    """The attention's workspace on a device, which sizes alone determine."""
     with torch.cuda.device(device_index):
-        return dfa_cache_workspace_bytes(*sizes)
+        return (dfa_cache_workspace_bytes if bits == 8 else dfa_cache4_workspace_bytes)(*sizes)
 
 
 def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new,
@@ -858,10 +950,24 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
     dfa_cache_workspace_bytes(...) bytes; by default one is allocated.  For
     sampling: no gradients, the outputs are detached from q, k and v.
     """
+    return _attend("dfa_cache_forward", 8, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                   cache_lens, cu_new, max_new, k, v, block_size, out, lse, workspace)
+
+
+def dfa_cache4_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new,
+                       max_new, k=None, v=None, block_size=1, out=None, lse=None, workspace=None):
+    """dfa_cache_forward for the 4-bit cache (see dfa_cache4_append for its tensors);
+    a workspace is of dfa_cache4_workspace_bytes(...)."""
+    return _attend("dfa_cache4_forward", 4, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                   cache_lens, cu_new, max_new, k, v, block_size, out, lse, workspace)
+
+
+def _attend(fn, bits, q, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu_new,
+            max_new, k, v, block_size, out, lse, workspace):
     rows, H, d = shape = _check_heads(q, 3, "q")
     dev = q.device
     B, Hk, ps, P, maxp = _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
-                                      cu_new, dev, d)
+                                      cu_new, dev, d, bits)
     if Hk < 1 or H % Hk:
         raise ValueError("kv_heads must divide the query heads")
     if (k is None) != (v is None):
@@ -882,18 +988,119 @@ def dfa_cache_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, cache_
         _check_dense(lse, (H, rows), torch.float32, dev, "lse")
     max_new = _int32(max_new)
     if workspace is None:
-        nwork = _workspace_bytes(dev.index, B, rows, max_new, H, Hk, d, ps, maxp)
+        nwork = _workspace_bytes(bits, dev.index, B, rows, max_new, H, Hk, d, ps, maxp)
         if nwork:
             workspace = torch.empty(nwork, dtype=torch.uint8, device=dev)
     else:
         nwork = workspace.numel()
         _check_dense(workspace, (nwork,), torch.uint8, dev, "workspace")
-    _call("dfa_cache_forward", dev, q.data_ptr(), kp, vp, k_cache.data_ptr(), v_cache.data_ptr(),
+    _call(fn, dev, q.data_ptr(), kp, vp, k_cache.data_ptr(), v_cache.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), cache_lens.data_ptr(),
           cu_new.data_ptr(), out.data_ptr(), lse.data_ptr(),
           None if workspace is None else workspace.data_ptr(), nwork, B, rows, max_new, H, Hk, d,
           _int32(block_size), ps, P, maxp, _strides(q, "q"), ks, vs)
     return out, lse
+
+
+# ------------------------------------------------------- scores of tokens
+
+_LOGIT_TYPES = {torch.bfloat16: DFA_BF16, torch.float16: DFA_F16, torch.float32: DFA_F32}
+_TOKEN_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _check_logits(logits, tokens):
+    """Check logits (rows, vocab) and their tokens; returns (rows, vocab, row stride,
+    dtype code, bytes of a token)."""
+    rows, V = _check_dims(logits, 2, "logits")
+    dtype = _LOGIT_TYPES.get(logits.dtype)
+    if dtype is None or not logits.is_cuda:
+        raise ValueError("logits must be a bfloat16, float16 or float32 tensor on a CUDA device")
+    if V < 1:
+        raise ValueError("the vocabulary is empty")
+    stride, last = logits.stride()
+    if last != 1 and V > 1:
+        raise ValueError("logits: the last dimension must be contiguous")
+    if tokens is None:
+        return rows, V, stride, dtype, 4
+    size = _TOKEN_BYTES.get(tokens.dtype) if isinstance(tokens, torch.Tensor) else None
+    if size is None:
+        raise ValueError("tokens must be an int32 or int64 tensor")
+    _check_dense(tokens, (rows,), tokens.dtype, logits.device, "tokens")
+    return rows, V, stride, dtype, size
+
+
+def dfa_token_logprobs_workspace_bytes(rows, vocab, top, dtype):
+    """Bytes of workspace dfa_token_logprobs needs on the current device (0: none);
+    ``dtype``: the logits' torch dtype."""
+    return _bytes("dfa_token_logprobs_workspace_bytes", rows, vocab, top,
+                  _LOGIT_TYPES.get(dtype, -1))
+
+
+@functools.lru_cache(maxsize=1024)
+def _scores_bytes(device_index, *sizes):
+    """dfa_token_logprobs_workspace_bytes on a device, which sizes alone determine."""
+    with torch.cuda.device(device_index):
+        return dfa_token_logprobs_workspace_bytes(*sizes)
+
+
+def dfa_token_logprobs(logits, tokens=None, top=0, workspace=None):
+    """Scores of tokens from logits (rows, V) (see dfa.h): bf16, f16 or f32, the last
+    dimension contiguous.  ``tokens``: int32 or int64 (rows,), negative: none.
+
+    Returns (logprobs, entropy, stats, top_logprobs, top_tokens): float32 (rows,)
+    twice, (rows, 2), (rows, top), and int32 (rows, top); without tokens logprobs is
+    None.  ``workspace``: a uint8 tensor of at least
+    dfa_token_logprobs_workspace_bytes(...) bytes; by default one is allocated.
+    """
+    rows, V, stride, dtype, token_bytes = _check_logits(logits, tokens)
+    dev, top = logits.device, int(top)
+    if not 0 <= top <= 32:
+        raise ValueError("top must be 0 to 32")
+    # one allocation: stats, entropy, log probabilities, alternatives
+    n = 3 if tokens is None else 4
+    buf = torch.empty((n + 2 * top) * rows, dtype=torch.float32, device=dev)
+    at = buf.data_ptr()
+    parts = torch.unsafe_split_with_sizes(buf, (2 * rows, rows, (n - 3) * rows, top * rows,
+                                                top * rows))
+    if workspace is None:
+        nwork = _scores_bytes(dev.index, rows, V, top, logits.dtype)
+        if nwork:
+            workspace = torch.empty(nwork, dtype=torch.uint8, device=dev)
+    else:
+        nwork = workspace.numel()
+        _check_dense(workspace, (nwork,), torch.uint8, dev, "workspace")
+    _call("dfa_token_logprobs", dev, logits.data_ptr(),
+          None if tokens is None else tokens.data_ptr(), token_bytes,
+          None if tokens is None else at + 12 * rows, at + 8 * rows, at,
+          at + 4 * n * rows, at + 4 * (n + top) * rows,
+          None if workspace is None else workspace.data_ptr(), nwork, rows, V, top, stride, dtype)
+    return (None if tokens is None else parts[2], parts[1], parts[0].view(rows, 2),
+            parts[3].view(rows, top), parts[4].view(torch.int32).view(rows, top))
+
+
+def dfa_token_logprobs_backward(logits, tokens, stats, entropy, dlogprobs=None, dentropy=None,
+                                dlogits=None):
+    """Gradient of the log probabilities and the entropy (see dfa.h), of the logits'
+    type, contiguous; dlogprobs, dentropy: float32 (rows,) or None."""
+    rows, V, stride, dtype, token_bytes = _check_logits(logits, tokens)
+    dev, f32 = logits.device, torch.float32
+    _check_dense(stats, (rows, 2), f32, dev, "stats")
+    if dlogprobs is not None:
+        _check_dense(dlogprobs, (rows,), f32, dev, "dlogprobs")
+    if dentropy is not None:
+        _check_dense(dentropy, (rows,), f32, dev, "dentropy")
+        _check_dense(entropy, (rows,), f32, dev, "entropy")
+    if dlogits is None:
+        dlogits = torch.empty((rows, V), dtype=logits.dtype, device=dev)
+    else:
+        _check_dense(dlogits, (rows, V), logits.dtype, dev, "dlogits")
+    _call("dfa_token_logprobs_backward", dev, logits.data_ptr(),
+          None if tokens is None else tokens.data_ptr(), token_bytes, stats.data_ptr(),
+          None if dentropy is None else entropy.data_ptr(),
+          None if dlogprobs is None else dlogprobs.data_ptr(),
+          None if dentropy is None else dentropy.data_ptr(), dlogits.data_ptr(), rows, V, stride,
+          dtype)
+    return dlogits
 
 
 def dfa_selftest_wait_timeout(limit_us=20000):

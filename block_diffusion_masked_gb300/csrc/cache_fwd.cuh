@@ -46,6 +46,22 @@ struct CacheFwdParams {
   float scale_log2;
 };
 
+// Over the 4-bit cache: the scales' maps too, (page_size, kv_heads * headdim / 32,
+// pages) bytes; k_scale and v_scale are not used.
+struct Cache4FwdParams : CacheFwdParams {
+  CUtensorMap tm_ks, tm_vs;
+};
+template <int BITS>
+struct CacheParamsOf {
+  using Type = CacheFwdParams;
+};
+template <>
+struct CacheParamsOf<4> {
+  using Type = Cache4FwdParams;
+};
+template <int BITS>
+using CacheParams = typename CacheParamsOf<BITS>::Type;
+
 // One request's sizes, checked: a length past its table or rows past the
 // packed ones are errors, and the request is then taken as empty.
 struct Request {
@@ -266,8 +282,12 @@ constexpr float kMostSum = 32768.f;
 constexpr int kOwnExp = 16;
 constexpr float kOwnUnit = 1 << kOwnExp;
 
-// More than 32 query rows per key/value head, headdim 64 or 128 (tiles of 128
-// rows; the tensor maps' boxes are whole pages).
+// Up to 32 query rows per key/value head, and headdim 256 (cache_rows.cuh), in tiles
+// of `tile_rows`; more rows, headdim 64 or 128 (cache_wide.cuh): tiles of 128 rows,
+// the tensor maps' boxes are whole pages.
+cudaError_t launch_cache4_rows(const Cache4FwdParams& p, int headdim, int tile_rows,
+                               cudaStream_t stream);
 cudaError_t launch_cache_wide(const CacheFwdParams& p, int headdim, cudaStream_t stream);
+cudaError_t launch_cache_wide(const Cache4FwdParams& p, int headdim, cudaStream_t stream);
 
 }  // namespace dfa

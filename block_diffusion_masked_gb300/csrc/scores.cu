@@ -1,0 +1,686 @@
+// Scores of tokens from logits: log probability of a given token, entropy of the
+// distribution, the likeliest alternatives, and the gradient of the first two.
+//
+// Mathematics.  For a row x of V logits, m = max x, S = sum_j exp(x_j - m):
+//   log p_j  = x_j - m - ln S
+//   entropy  = -sum_j p_j log p_j = ln S - (sum_j exp(x_j - m) (x_j - m)) / S
+//   d(log p_t) / dx_j    = [j = t] - p_j
+//   d(entropy) / dx_j    = -p_j (log p_j + entropy).
+// Everything is taken relative to m, so that nothing cancels where the logits are
+// large against their spread; sums are float32 (a thread's own, then a tree).  A
+// logit of -inf is a token that cannot be: it counts for nothing.
+//
+// The alternatives are those of the largest keys: a logit's bits, ordered as
+// unsigned integers (-0 as 0), above the complement of its index, so that equal
+// logits come lowest index first and no two keys are equal.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "device.cuh"
+#include "dfa.h"
+#include "params.cuh"
+#include "sm100.cuh"
+
+namespace dfa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTop = 32;
+constexpr int kMaxSplits = 64;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A logit this far below the maximum has probability 0 in float32; what is
+// further, -inf too, is taken as this far, for 0 * inf is not a number.
+constexpr float kFar = -150.f;
+
+// ------------------------------------------------------------------ rows of logits
+
+template <typename T>
+struct Logit;
+template <>
+struct Logit<__nv_bfloat16> {
+  static constexpr int kPer = 8;  // values of a 16-byte vector
+  static constexpr uint32_t kNone = 0xff80ff80u;
+  __device__ static void unpack(const uint4& w, float* f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  __device__ static uint4 pack(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+  __device__ static float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+  __device__ static __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Logit<__half> {
+  static constexpr int kPer = 8;
+  static constexpr uint32_t kNone = 0xfc00fc00u;
+  __device__ static void unpack(const uint4& w, float* f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      f[2 * i] = y.x, f[2 * i + 1] = y.y;
+    }
+  }
+  __device__ static uint4 pack(const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 y = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  __device__ static float get(__half x) { return __half2float(x); }
+  __device__ static __half put(float x) { return __float2half_rn(x); }
+};
+template <>
+struct Logit<float> {
+  static constexpr int kPer = 4;
+  static constexpr uint32_t kNone = 0xff800000u;
+  __device__ static void unpack(const uint4& w, float* f) {
+    f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
+  }
+  __device__ static uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+  __device__ static float get(float x) { return x; }
+  __device__ static float put(float x) { return x; }
+};
+
+// A row as 16-byte vectors of the memory it lies in: vector v holds the row's
+// values v * kPer - lead ..., of which the first and the last vector may hold some
+// only.  Those are read value by value, so that nothing outside the row is read.
+template <typename T>
+struct Row {
+  static constexpr int kPer = Logit<T>::kPer;
+  const T* x;
+  int vocab, lead, vectors;
+  __device__ Row(const T* at, int v) : x(at), vocab(v) {
+    lead = static_cast<int>((reinterpret_cast<uintptr_t>(at) & 15) / sizeof(T));
+    vectors = (lead + vocab + kPer - 1) / kPer;
+  }
+  __device__ __forceinline__ uint4 load(int v, int end) const {
+    constexpr uint32_t none = Logit<T>::kNone;
+    uint4 w = make_uint4(none, none, none, none);
+    if (v >= end) return w;
+    const int e0 = v * kPer - lead;
+    if (e0 >= 0 && e0 + kPer <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + e0));
+    alignas(16) T part[kPer];
+    *reinterpret_cast<uint4*>(part) = w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (e0 + i >= 0 && e0 + i < vocab) part[i] = x[e0 + i];
+    return *reinterpret_cast<const uint4*>(part);
+  }
+};
+
+// max(x, kFar), NaN kept.
+__device__ __forceinline__ float not_far(float x) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(kFar));
+  return x;
+}
+
+// Running statistics of a softmax: the maximum m, the sum s of exp(x - m) and the
+// sum t of exp(x - m) (x - m).  Nothing yet: m -inf, s and t 0.
+struct Stats {
+  float m, s, t;
+};
+// a against the maximum m >= a.m.
+__device__ __forceinline__ Stats rebase(const Stats& a, float m) {
+  if (a.m == -INFINITY) return {m, a.s, a.t};  // nothing yet, or not a number
+  const float d = not_far(a.m - m), f = ex2_approx(d * kLog2e);
+  return {m, a.s * f, f * fmaf(a.s, d, a.t)};
+}
+__device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
+  const float m = fmaxf(a.m, b.m);
+  const Stats x = rebase(a, m), y = rebase(b, m);
+  return {m, x.s + y.s, x.t + y.t};
+}
+__device__ __forceinline__ Stats warp_join(Stats a) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
+                 __shfl_xor_sync(0xffffffffu, a.t, off)});
+  return a;
+}
+
+// ------------------------------------------------------------------ keys
+
+using Key = unsigned long long;
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 as 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t kOrderedNone = 0x007fffffu;  // of -inf: no alternative
+__device__ __forceinline__ Key make_key(float x, int index) {
+  return static_cast<Key>(ordered(x)) << 32 | static_cast<uint32_t>(~index);
+}
+// The largest of the warp's keys (0: none).
+__device__ __forceinline__ Key warp_max(Key k) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
+  const uint32_t lo = __reduce_max_sync(
+      0xffffffffu, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+  return static_cast<Key>(hi) << 32 | lo;
+}
+
+struct ScoresParams {
+  const void* x;       // (rows, vocab), rows `stride` values apart
+  const void* tokens;  // (rows) or null
+  long long stride;
+  float* logprobs;      // (rows) or null
+  float* entropy;       // (rows)
+  float* stats;         // (rows, 2): m, ln S
+  float* top_logprobs;  // (rows, top)
+  int* top_tokens;
+  Stats* part;    // (rows, splits): of a split row's pieces
+  Key* part_top;  // (rows, splits, top)
+  unsigned* status;
+  int rows, vocab, top, splits;
+  bool wide_tokens;  // 64 bits
+};
+
+// The row's token: -1 where none is given, or one that there is not.
+__device__ __forceinline__ int load_token(const ScoresParams& p, int row) {
+  if (p.tokens == nullptr) return -1;
+  const long long t = p.wide_tokens ? static_cast<const long long*>(p.tokens)[row]
+                                    : static_cast<const int*>(p.tokens)[row];
+  if (t >= p.vocab) {
+    atomicOr(p.status, kStatusIndex);
+    return -1;
+  }
+  return t < 0 ? -1 : static_cast<int>(t);
+}
+
+// What every thread needs of a finished row.
+struct Finished {
+  float m, log_s;
+  bool none, nan;  // no token can be (every logit -inf); a logit is not a number
+};
+__device__ __forceinline__ Finished finish(const Stats& a) {
+  Finished f;
+  f.none = a.m == -INFINITY && a.s == 0.f;
+  f.nan = !f.none && !(a.s < INFINITY);
+  f.m = f.nan ? NAN : a.m;
+  f.log_s = f.none ? 0.f : lg2_approx(a.s) * kLn2;
+  return f;
+}
+// One thread writes the row's numbers.
+template <typename T>
+__device__ __forceinline__ void write_row(const ScoresParams& p, int row, const Stats& a,
+                                          const Finished& f) {
+  p.entropy[row] = f.none ? 0.f : f.nan ? NAN : fmaxf(f.log_s - a.t / a.s, 0.f);
+  *reinterpret_cast<float2*>(p.stats + 2LL * row) = make_float2(f.m, f.log_s);
+  const int token = load_token(p, row);
+  if (p.logprobs == nullptr) return;
+  float y = 0.f;
+  if (token >= 0) {
+    const T* x = static_cast<const T*>(p.x) + row * p.stride;
+    y = f.none ? -INFINITY : (Logit<T>::get(x[token]) - f.m) - f.log_s;
+  }
+  p.logprobs[row] = y;
+}
+// Alternative i of a row, of its key (0: there is none).
+__device__ __forceinline__ void write_top(const ScoresParams& p, int row, int i, Key key,
+                                          const Finished& f) {
+  const uint32_t order = static_cast<uint32_t>(key >> 32);
+  const bool is = order > kOrderedNone && !f.nan;
+  const long long at = static_cast<long long>(row) * p.top + i;
+  p.top_logprobs[at] = f.nan ? NAN : is ? (unordered(order) - f.m) - f.log_s : -INFINITY;
+  p.top_tokens[at] = is ? static_cast<int>(~static_cast<uint32_t>(key)) : -1;
+}
+
+// ------------------------------------------------------------------ forward
+
+// Alternatives are gathered in shared memory: a list that a round of the block's
+// threads may add a vector each to, and a place for the best of it.
+constexpr int kListMost = kThreads * 8;   // what a round adds at most
+constexpr int kListKeep = 512;            // a longer list is cut down between rounds
+struct TopSpace {
+  Key list[kListKeep + kListMost];
+  Key best[kMaxTop];
+  float top[kThreads];  // the threads' largest logits
+  int hot[kThreads];    // threads that may have one of the alternatives
+  int count, hots;
+  uint32_t least;       // no alternative is below this (ordered)
+};
+
+// The `top` largest keys of the list, in order, into `best` (0 behind the last).
+__device__ __forceinline__ void best_of_list(TopSpace& s, int top) {
+  const int n = s.count;
+  for (int i = threadIdx.x; i < top; i += kThreads)
+    if (i >= n) s.best[i] = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Key key = s.list[i];
+    int above = 0;
+    for (int j = 0; j < n; ++j) above += s.list[j] > key;
+    if (above < top) s.best[above] = key;
+  }
+}
+
+// One block per row, or per piece of one: a thread walks vectors of the piece, the
+// block's width apart, with statistics of its own against its own maximum, the next
+// vectors on their way; one join at the end.
+//
+// Alternatives: the block's `top` largest logits are among the threads whose
+// largest is one of the `top` largest of the threads' largest.  Only those threads'
+// vectors (top of 256) are read again, from L2, by the whole block, in the order of
+// their indexes, and what is not below the bound goes to a list.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) dfa_scores_kernel(const ScoresParams p) {
+  using L = Logit<T>;
+  constexpr int kPer = L::kPer, kAhead = 4;
+  __shared__ Stats s_warp[kThreads / 32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / p.splits, piece = blockIdx.x - row * p.splits;
+  const Row<T> r(static_cast<const T*>(p.x) + row * p.stride, p.vocab);
+  const int per = (r.vectors + p.splits - 1) / p.splits;
+  const int lo = min(piece * per, r.vectors), hi = min(lo + per, r.vectors);
+
+  Stats a = {-INFINITY, 0.f, 0.f};
+  uint4 w[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) w[u] = r.load(lo + tid + u * kThreads, hi);
+  for (int v = lo + tid; v < hi; v += kAhead * kThreads) {
+    uint4 next[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) next[u] = r.load(v + (kAhead + u) * kThreads, hi);
+    float m = a.m;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float f[kPer];
+      L::unpack(w[u], f);
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) m = fmax3(m, f[i], f[i + 1]);
+    }
+    if (m > a.m) a = rebase(a, m);
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float f[kPer];
+      L::unpack(w[u], f);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float d = not_far(f[i] - ref), e = ex2_approx(d * kLog2e);
+        a.s += e;
+        a.t = fmaf(e, d, a.t);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) w[u] = next[u];
+  }
+  const float mine = a.m;
+  a = warp_join(a);
+  if (lane == 0) s_warp[warp] = a;
+
+  if constexpr (TOP) {
+    __shared__ TopSpace s;
+    s.top[tid] = mine;
+    if (tid == 0) s.count = s.hots = 0;
+    __syncthreads();
+    // The bound: the top-th largest of the threads' largest, one at a time.
+    if (warp == 0) {
+      uint32_t own[kThreads / 32];
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) own[i] = ordered(s.top[lane + 32 * i]);
+      uint32_t least = 0;
+      for (int n = 0; n < p.top; ++n) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) x = max(x, own[i]);
+        least = __reduce_max_sync(0xffffffffu, x);
+        const int first = __ffs(__ballot_sync(0xffffffffu, x == least)) - 1;
+        bool gone = lane != first;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i)
+          if (!gone && own[i] == least) own[i] = 0, gone = true;
+      }
+      if (lane == 0) s.least = max(least, kOrderedNone + 1);
+    }
+    __syncthreads();
+    if (ordered(mine) >= s.least) s.hot[atomicAdd(&s.hots, 1)] = tid;
+    __syncthreads();
+    const int hots = s.hots, steps = (hi - lo + kThreads - 1) / kThreads;
+    Key bound = static_cast<Key>(s.least) << 32;  // below every key of that logit
+    for (int q0 = 0; q0 < hots * steps; q0 += kThreads) {
+      const int q = q0 + tid, step = q / hots;
+      if (q < hots * steps) {
+        const int v = lo + step * kThreads + s.hot[q - step * hots];
+        float f[kPer];
+        L::unpack(r.load(v, hi), f);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const Key key = make_key(f[i], v * kPer - r.lead + i);
+          if (key >= bound) s.list[atomicAdd(&s.count, 1)] = key;
+        }
+      }
+      __syncthreads();
+      const bool full = s.count > kListKeep;
+      __syncthreads();  // the count has been read
+      if (full) {
+        best_of_list(s, p.top);
+        __syncthreads();
+        bound = s.best[p.top - 1];  // the list holds more than `top` keys
+        if (tid < p.top) s.list[tid] = s.best[tid];
+        if (tid == 0) s.count = p.top;
+        __syncthreads();
+      }
+    }
+    best_of_list(s, p.top);
+    __syncthreads();
+    if (p.splits > 1) {
+      if (tid < p.top)
+        p.part_top[static_cast<long long>(blockIdx.x) * p.top + tid] = s.best[tid];
+    } else if (warp == 0) {
+      Stats b = lane < kThreads / 32 ? s_warp[lane] : Stats{-INFINITY, 0.f, 0.f};
+      const Finished f = finish(warp_join(b));
+      if (lane < p.top) write_top(p, row, lane, s.best[lane], f);
+    }
+  } else {
+    __syncthreads();
+  }
+  if (warp == 0) {
+    Stats b = lane < kThreads / 32 ? s_warp[lane] : Stats{-INFINITY, 0.f, 0.f};
+    b = warp_join(b);
+    if (lane == 0) {
+      if (p.splits > 1) p.part[blockIdx.x] = b;
+      else write_row<T>(p, row, b, finish(b));
+    }
+  }
+}
+
+// The pieces of split rows, a warp a row: statistics joined, then the alternatives
+// one at a time, each lane at the head of its pieces' lists.
+constexpr int kJoinRows = 4;
+template <typename T>
+__global__ void __launch_bounds__(32 * kJoinRows) dfa_scores_join_kernel(const ScoresParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, row = blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  constexpr int kLists = kMaxSplits / 32;
+  const long long first = static_cast<long long>(row) * p.splits;
+  Stats a = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kLists; ++i)
+    if (lane + 32 * i < p.splits) a = join(a, p.part[first + lane + 32 * i]);
+  a = warp_join(a);
+  const Finished f = finish(a);
+  if (lane == 0) write_row<T>(p, row, a, f);
+  if (p.top == 0) return;
+  const Key* lists = p.part_top + first * p.top;
+  Key head[kLists];
+  int at[kLists];
+#pragma unroll
+  for (int i = 0; i < kLists; ++i) {
+    at[i] = 0;
+    head[i] = lane + 32 * i < p.splits ? lists[(lane + 32 * i) * p.top] : 0;
+  }
+  Key mine = 0;
+  for (int n = 0; n < p.top; ++n) {
+    Key k = 0;
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) k = max(k, head[i]);
+    const Key best = warp_max(k);
+    if (lane == n) mine = best;
+#pragma unroll
+    for (int i = 0; i < kLists; ++i)
+      if (best != 0 && head[i] == best)
+        head[i] = ++at[i] < p.top ? lists[(lane + 32 * i) * p.top + at[i]] : 0;
+  }
+  if (lane < p.top) write_top(p, row, lane, mine, f);
+}
+
+// ------------------------------------------------------------------ backward
+
+struct ScoresGradParams {
+  const void* x;
+  const void* tokens;
+  long long stride;
+  const float* stats;
+  const float* entropy;
+  const float* dlogprobs;  // (rows) or null
+  const float* dentropy;   // (rows) or null
+  void* dx;                // (rows, vocab) contiguous
+  int rows, vocab, splits;
+  bool wide_tokens;
+};
+
+// dx_j = g ([j = t] - p_j) - h p_j (log p_j + entropy), for the gradients g of the
+// row's log probability and h of its entropy: one pass, logits in, gradient out,
+// vectors of the gradient's memory.  A row of zero gradients, or where no token can
+// be, is set to zero and not read.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dfa_scores_grad_kernel(const ScoresGradParams p) {
+  using L = Logit<T>;
+  constexpr int kPer = L::kPer;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int row = blockIdx.x / p.splits, piece = blockIdx.x - row * p.splits;
+  const T* x = static_cast<const T*>(p.x) + row * p.stride;
+  T* dx = static_cast<T*>(p.dx) + static_cast<long long>(row) * p.vocab;
+  const Row<T> r(dx, p.vocab);
+  const int per = (r.vectors + p.splits - 1) / p.splits;
+  const int lo = min(piece * per, r.vectors), hi = min(lo + per, r.vectors);
+  const float2 st = *reinterpret_cast<const float2*>(p.stats + 2LL * row);
+  const float ent = p.dentropy ? p.entropy[row] : 0.f;
+  const float h = p.dentropy ? p.dentropy[row] : 0.f;
+  int token = -1;
+  if (p.tokens != nullptr) {
+    const long long t = p.wide_tokens ? static_cast<const long long*>(p.tokens)[row]
+                                      : static_cast<const int*>(p.tokens)[row];
+    token = t >= 0 && t < p.vocab ? static_cast<int>(t) : -1;
+  }
+  const float g = p.dlogprobs && token >= 0 ? p.dlogprobs[row] : 0.f;
+  const bool zero = (g == 0.f && h == 0.f) || st.x == -INFINITY;
+  // whether the logits lie in their vectors as the gradient does in its own
+  const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == (reinterpret_cast<uintptr_t>(dx) & 15);
+  const float base = fmaf(h, ent, g);  // dx_j = -p_j (g + h (log p_j + ent))
+  for (int v = lo + threadIdx.x; v < hi; v += kThreads) {
+    const int e0 = v * kPer - r.lead;
+    const bool whole = e0 >= 0 && e0 + kPer <= p.vocab;
+    float f[kPer];
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) f[i] = 0.f;
+    } else {
+      if (whole && aligned) {
+        L::unpack(__ldg(reinterpret_cast<const uint4*>(x + e0)), f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          f[i] = e0 + i >= 0 && e0 + i < p.vocab ? L::get(x[e0 + i]) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float lp = not_far((f[i] - st.x) - st.y);
+        f[i] = -ex2_approx(lp * kLog2e) * fmaf(h, lp, base);
+      }
+      if (token >= e0 && token < e0 + kPer) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (e0 + i == token) f[i] += g;
+      }
+    }
+    if (whole) {
+      *reinterpret_cast<uint4*>(dx + e0) = L::pack(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (e0 + i >= 0 && e0 + i < p.vocab) dx[e0 + i] = L::put(f[i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int kBlocksPerSm = 4;
+
+// Pieces of a row: enough that the blocks fill the device once, at least two
+// vectors a thread, and such that the last wave is not mostly empty.
+int splits_for(int rows, int vocab, int size, int sms) {
+  const long long vectors = (static_cast<long long>(vocab) * size + 15) / 16;
+  const long long most = vectors / (2 * kThreads);
+  const long long slots = static_cast<long long>(sms) * kBlocksPerSm;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || s <= most); ++s) {
+    const long long waves = (static_cast<long long>(rows) * s + slots - 1) / slots;
+    // a block's own cost is that of about two vectors a thread
+    const double cost = static_cast<double>(waves) * (static_cast<double>(vectors) / s + 2 * kThreads);
+    if (s == 1 || cost < 0.97 * least) best = s, least = cost;
+  }
+  return best;
+}
+
+int type_size(int dtype) {
+  return dtype == DFA_BF16 || dtype == DFA_F16 ? 2 : dtype == DFA_F32 ? 4 : 0;
+}
+
+int check_scores(const void* logits, const void* tokens, int token_bytes, int rows, int vocab,
+                 long long stride, int dtype) {
+  if (rows < 0 || rows > (1 << 24) || vocab < 1 || vocab > (1 << 30) || !type_size(dtype))
+    return DFA_EINVAL;
+  if (tokens && token_bytes != 4 && token_bytes != 8) return DFA_EINVAL;
+  if (rows == 0) return DFA_OK;
+  auto aligned = [](const void* x, unsigned n) { return (reinterpret_cast<uintptr_t>(x) & (n - 1)) == 0; };
+  if (!logits || !aligned(logits, type_size(dtype)) ||
+      (tokens && !aligned(tokens, static_cast<unsigned>(token_bytes))) || stride < 0 ||
+      stride > (1LL << 40))
+    return DFA_EINVAL;
+  return DFA_OK;
+}
+
+long long scores_workspace(int rows, int top, int splits) {
+  if (splits == 1) return 0;
+  const long long pieces = static_cast<long long>(rows) * splits;
+  return pieces * top * static_cast<long long>(sizeof(Key)) +
+         pieces * static_cast<long long>(sizeof(Stats));
+}
+
+template <typename T>
+cudaError_t launch_scores(const ScoresParams& p, cudaStream_t stream) {
+  auto kern = p.top > 0 ? dfa_scores_kernel<T, true> : dfa_scores_kernel<T, false>;
+  const unsigned blocks = static_cast<unsigned>(p.rows) * static_cast<unsigned>(p.splits);
+  cudaError_t e = launch_chained(kern, dim3(blocks), dim3(kThreads), 0, stream, p);
+  if (e == cudaSuccess && p.splits > 1)
+    e = launch_chained(dfa_scores_join_kernel<T>,
+                       dim3((static_cast<unsigned>(p.rows) + kJoinRows - 1) / kJoinRows),
+                       dim3(32 * kJoinRows), 0, stream, p);
+  return e;
+}
+
+}  // namespace
+}  // namespace dfa
+
+using namespace dfa;
+
+extern "C" {
+
+long long dfa_token_logprobs_workspace_bytes(int rows, int vocab, int top, int dtype) {
+  if (rows < 0 || rows > (1 << 24) || vocab < 1 || vocab > (1 << 30) || !type_size(dtype) ||
+      top < 0 || top > kMaxTop)
+    return DFA_EINVAL;
+  if (rows == 0) return 0;
+  DeviceInfo di;
+  if (const int rc = device_info(&di)) return rc;
+  return scores_workspace(rows, top, splits_for(rows, vocab, type_size(dtype), di.sms));
+}
+
+int dfa_token_logprobs(const void* logits, const void* tokens, int token_bytes, float* logprobs,
+                       float* entropy, float* stats, float* top_logprobs, int* top_tokens,
+                       void* workspace, long long workspace_bytes, int rows, int vocab, int top,
+                       long long stride, int dtype, dfa_stream_t stream) {
+  if (top < 0 || top > kMaxTop) return DFA_EINVAL;
+  if (const int rc = check_scores(logits, tokens, token_bytes, rows, vocab, stride, dtype))
+    return rc;
+  if (rows == 0) return DFA_OK;
+  auto aligned = [](const void* x, unsigned n) {
+    return x && (reinterpret_cast<uintptr_t>(x) & (n - 1)) == 0;
+  };
+  if (!aligned(entropy, 4) || !aligned(stats, 8) || (tokens && !logprobs) ||
+      (logprobs && !aligned(logprobs, 4)) ||
+      (top && (!aligned(top_logprobs, 4) || !aligned(top_tokens, 4))) ||
+      (workspace && !aligned(workspace, 8)))
+    return DFA_EINVAL;
+  DeviceInfo di;
+  if (const int rc = device_info(&di)) return rc;
+  const int splits = splits_for(rows, vocab, type_size(dtype), di.sms);
+  const long long need = scores_workspace(rows, top, splits);
+  if (need && (!workspace || workspace_bytes < need)) return DFA_EINVAL;
+  ScoresParams p{};
+  p.x = logits;
+  p.tokens = tokens;
+  p.stride = stride;
+  p.logprobs = logprobs;
+  p.entropy = entropy;
+  p.stats = stats;
+  p.top_logprobs = top_logprobs;
+  p.top_tokens = top_tokens;
+  p.part_top = static_cast<Key*>(workspace);
+  p.part = reinterpret_cast<Stats*>(p.part_top + static_cast<long long>(rows) * splits * top);
+  p.status = di.status;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.top = top;
+  p.splits = splits;
+  p.wide_tokens = token_bytes == 8;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == DFA_BF16  ? launch_scores<__nv_bfloat16>(p, s)
+                        : dtype == DFA_F16 ? launch_scores<__half>(p, s)
+                                           : launch_scores<float>(p, s);
+  return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);
+}
+
+int dfa_token_logprobs_backward(const void* logits, const void* tokens, int token_bytes,
+                                const float* stats, const float* entropy, const float* dlogprobs,
+                                const float* dentropy, void* dlogits, int rows, int vocab,
+                                long long stride, int dtype, dfa_stream_t stream) {
+  if (const int rc = check_scores(logits, tokens, token_bytes, rows, vocab, stride, dtype))
+    return rc;
+  if (rows == 0) return DFA_OK;
+  auto aligned = [](const void* x, unsigned n) {
+    return x && (reinterpret_cast<uintptr_t>(x) & (n - 1)) == 0;
+  };
+  if (!aligned(stats, 8) || !aligned(dlogits, 16) || (dentropy && !aligned(dentropy, 4)) ||
+      (dentropy && !aligned(entropy, 4)) || (dlogprobs && !aligned(dlogprobs, 4)))
+    return DFA_EINVAL;
+  DeviceInfo di;
+  if (const int rc = device_info(&di)) return rc;
+  ScoresGradParams p{};
+  p.x = logits;
+  p.tokens = tokens;
+  p.stride = stride;
+  p.stats = stats;
+  p.entropy = entropy;
+  p.dlogprobs = dlogprobs;
+  p.dentropy = dentropy;
+  p.dx = dlogits;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.splits = splits_for(rows, vocab, type_size(dtype), di.sms);
+  p.wide_tokens = token_bytes == 8;
+  const unsigned blocks = static_cast<unsigned>(rows) * static_cast<unsigned>(p.splits);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto kern = dtype == DFA_BF16  ? dfa_scores_grad_kernel<__nv_bfloat16>
+              : dtype == DFA_F16 ? dfa_scores_grad_kernel<__half>
+                                 : dfa_scores_grad_kernel<float>;
+  const cudaError_t e = launch_chained(kern, dim3(blocks), dim3(kThreads), 0, s, p);
+  return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);
+}
+
+}  // extern "C"

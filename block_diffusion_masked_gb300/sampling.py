@@ -1,11 +1,11 @@
-"""Sampling block by block: rotary tables, page tables, the 8-bit cache.
+"""Sampling block by block: rotary tables, page tables, the 8-bit and 4-bit caches.
 
 A block-diffusion sampler denoises one block of tokens at a time against the
 clean tokens of the blocks before it ("Fast Diffusion Attention", "Block
 diffusion in one picture": a block sees itself and the earlier clean blocks).
 ``PageTable`` holds the requests' pages and lengths, shared by all layers;
 ``KVCache`` holds one layer's keys and values in e4m3 with a power-of-two
-scale per page and head.  All state lives on the GPU and every step is a few
+scale per page and head, or in 4 bits with a scale per token and 32 dims.  All state lives on the GPU and every step is a few
 launches of fixed shape, so a step can be captured into a CUDA graph.
 """
 
@@ -144,24 +144,51 @@ class PageTable:
 
 
 class KVCache:
-    """One layer's keys and values: e4m3 pages, a scale per page and head."""
+    """One layer's keys and values: pages of 8 or 4 bits a value.
 
-    def __init__(self, num_pages, page_size, kv_heads, headdim, device="cuda"):
-        shape = (num_pages, kv_heads, page_size, headdim)
-        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device)
-                          .view(torch.float8_e4m3fn) for _ in range(2))
-        self.k_scale, self.v_scale = (torch.ones(shape[:2], dtype=torch.float32, device=device)
-                                      for _ in range(2))
+    ``bits=8``: k, v e4m3 (pages, kv_heads, page_size, headdim), k_scale, v_scale
+    float32 (pages, kv_heads), a power-of-two scale for each page and head.
+    ``bits=4``: k, v uint8 (pages, kv_heads, page_size, headdim / 2), k_scale, v_scale
+    float8_e5m2 (pages, kv_heads, headdim / 32, page_size), a scale for each token, head
+    and 32 dims (``dfa_cache4_append``): 4.25 bits a value, an error of up to a 16th of
+    the largest of the 32 values (an 8th where it is of the other sign).
+    """
+
+    def __init__(self, num_pages, page_size, kv_heads, headdim, device="cuda", bits=8):
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8")
+        self.bits = bits
+        shape = (num_pages, kv_heads, page_size, headdim * bits // 8)
+        self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        if bits == 8:
+            self.k, self.v = (x.view(torch.float8_e4m3fn) for x in (self.k, self.v))
+            self.k_scale, self.v_scale = (
+                torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
+        else:
+            scales = (num_pages, kv_heads, headdim // 32, page_size)
+            self.k_scale, self.v_scale = (
+                torch.zeros(scales, dtype=torch.uint8, device=device).view(torch.float8_e5m2)
+                for _ in range(2))
 
     def append(self, k, v, step):
         """Keep the step's tokens: k, v packed (rows, kv_heads, headdim) bf16."""
-        binding.dfa_cache_append(k, v, step.cu_new, step.cache_lens, step.block_table, self.k,
-                                 self.v, self.k_scale, self.v_scale, step.max_new)
+        append = binding.dfa_cache_append if self.bits == 8 else binding.dfa_cache4_append
+        append(k, v, step.cu_new, step.cache_lens, step.block_table, self.k,
+               self.v, self.k_scale, self.v_scale, step.max_new)
 
     def attend(self, q, step, k=None, v=None, block_size=1, **kwargs):
         """Attention of the step's rows over the tokens held before it and, with
         k and v, over their own blocks; returns (out, lse), detached from autograd
-        (``dfa_cache_forward``)."""
-        return binding.dfa_cache_forward(q, self.k, self.v, self.k_scale, self.v_scale,
-                                         step.block_table, step.cache_lens, step.cu_new,
-                                         step.max_new, k=k, v=v, block_size=block_size, **kwargs)
+        (``dfa_cache_forward``, ``dfa_cache4_forward``)."""
+        forward = binding.dfa_cache_forward if self.bits == 8 else binding.dfa_cache4_forward
+        return forward(q, self.k, self.v, self.k_scale, self.v_scale,
+                       step.block_table, step.cache_lens, step.cu_new,
+                       step.max_new, k=k, v=v, block_size=block_size, **kwargs)
+
+    def read(self, pages, cu_rows, rows, first=None, **kwargs):
+        """Tokens that ``pages`` (a :class:`PageTable`) counts as held, as the cache
+        holds them: request b's from first[b] (None: 0) on, in rows [cu_rows[b],
+        cu_rows[b + 1]) of k, v (rows, kv_heads, headdim) bf16 (``dfa_cache_read``)."""
+        read = binding.dfa_cache_read if self.bits == 8 else binding.dfa_cache4_read
+        return read(self.k, self.v, self.k_scale, self.v_scale, pages.block_table,
+                    pages.cache_lens, cu_rows, rows, first=first, **kwargs)

@@ -450,6 +450,111 @@ int dfa_cache_forward(const void *q, const void *k, const void *v, const void *k
                       dfa_stream_t stream);
 
 /*
+ * The same cache in 4 bits.  k_cache, v_cache: (num_pages, kv_heads, page_size,
+ * headdim / 2) bytes, a 32-bit word (little-endian) for the codes n of eight
+ * neighbouring head dims of a token: dim 2i of them in bits 4i to 4i + 3, dim 2i + 1
+ * in bits 16 + 4i to 19 + 4i.  k_scale, v_scale: (num_pages, kv_heads, headdim / 32,
+ * page_size) e5m2, one scale s for every token, head and 32 neighbouring dims.  All
+ * four are 16-byte aligned.  A
+ * cached value is (n - 8) s.  Tables, lengths, rows, plan and release: as above;
+ * what the host cannot see is checked and flagged as above.
+ */
+
+/*
+ * Append tokens, arguments as for dfa_cache_append.  Each token's bytes are written
+ * once and do not depend on what else a page holds.  s is the group's largest
+ * magnitude over 8, rounded up to three significant bits and kept within 2^-14 and
+ * 896; it is negative where the largest magnitude is that of positive values only
+ * (whose code is then 0, as 15 stands for 7 s).  n - 8 is x / s to the nearest,
+ * ties away from 0, within -8 and 7: off by at most |s| / 2 where 8 |s| is the
+ * group's range, |s| for values of the other sign next to it.  Magnitudes past 7168
+ * are cut, those below 2^-15 become 0.  A group with a value that is not finite is
+ * kept as NaN, all 32 values of it.
+ */
+int dfa_cache4_append(const void *k, const void *v, const int *cu_new, const int *cache_lens,
+                      const int *block_table, void *k_cache, void *v_cache, void *k_scale,
+                      void *v_scale, int batch, int rows, int max_new, int kv_heads, int headdim,
+                      int page_size, int num_pages, int max_pages, const long long *k_strides,
+                      const long long *v_strides, dfa_stream_t stream);
+
+/*
+ * Attention over it: arguments, results, limits and workspaces are those of
+ * dfa_cache_forward (with a workspace size of its own).  The products run on the
+ * cached values exactly; probabilities are rounded to f16 against them (2^-11).
+ */
+long long dfa_cache4_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
+                                     int headdim, int page_size, int max_pages);
+int dfa_cache4_forward(const void *q, const void *k, const void *v, const void *k_cache,
+                       const void *v_cache, const void *k_scale, const void *v_scale,
+                       const int *block_table, const int *cache_lens, const int *cu_new, void *out,
+                       float *lse, void *workspace, long long workspace_bytes, int batch, int rows,
+                       int max_new, int heads, int kv_heads, int headdim, int block_size,
+                       int page_size, int num_pages, int max_pages, const long long *q_strides,
+                       const long long *k_strides, const long long *v_strides,
+                       dfa_stream_t stream);
+
+/*
+ * Read tokens back, from either cache.  Request b's tokens first[b], first[b] + 1,
+ * ... (first NULL: 0) go to rows [cu_rows[b], cu_rows[b + 1]) of k, v (rows,
+ * kv_heads, headdim) bf16, contiguous: the cached values, exactly (both formats'
+ * values are bf16 values).  cache_lens: the tokens held NOW.  Rows past
+ * cu_rows[batch] are left alone.  A row whose token is not held (a position
+ * negative or past the length), a page that may not be followed or a length past its
+ * table gives zeros; rows out of order are left alone; each sets DFA_EDEVICE.
+ * batch <= 32768.
+ */
+int dfa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale,
+                   const float *v_scale, const int *block_table, const int *cache_lens,
+                   const int *first, const int *cu_rows, void *k, void *v, int batch, int rows,
+                   int kv_heads, int headdim, int page_size, int num_pages, int max_pages,
+                   dfa_stream_t stream);
+int dfa_cache4_read(const void *k_cache, const void *v_cache, const void *k_scale,
+                    const void *v_scale, const int *block_table, const int *cache_lens,
+                    const int *first, const int *cu_rows, void *k, void *v, int batch, int rows,
+                    int kv_heads, int headdim, int page_size, int num_pages, int max_pages,
+                    dfa_stream_t stream);
+
+/*
+ * Scores of tokens.  logits (rows, vocab), rows `stride` values apart (>= 0), the
+ * values of a row contiguous, of type DFA_BF16, DFA_F16 or DFA_F32, aligned to their
+ * size only.  Of each row, in float32:
+ *   stats[row] = (m, ln S): the largest logit and the log of the sum of exp(x - m),
+ *     so that log p_j = (x_j - m) - ln S;
+ *   logprobs[row] = log p of its token, 0 where the token is negative (none given);
+ *     tokens (rows) of token_bytes 4 or 8, or NULL (logprobs may then be NULL);
+ *   entropy[row] = -sum_j p_j log p_j;
+ *   top_logprobs, top_tokens (rows, top), top <= 32: the likeliest tokens in order,
+ *     equal ones lowest index first; behind the last token that can be -inf and -1.
+ * A logit of -inf is a token that cannot be.  Where no token can be (every logit
+ * -inf) the entropy is 0, a token's log probability -inf, stats (-inf, 0).  A row
+ * with a NaN or +inf gives NaN (and -1 for the alternatives).  A token >= vocab sets
+ * DFA_EDEVICE and counts as none.  rows <= 2^24, vocab <= 2^30, stride <= 2^40.
+ * workspace: dfa_token_logprobs_workspace_bytes(...) bytes of device memory (8-byte
+ * aligned; 0 for many rows); calls that may run at the same time need their own.
+ */
+#define DFA_BF16 0
+#define DFA_F16 1
+#define DFA_F32 2
+long long dfa_token_logprobs_workspace_bytes(int rows, int vocab, int top, int dtype);
+int dfa_token_logprobs(const void *logits, const void *tokens, int token_bytes, float *logprobs,
+                       float *entropy, float *stats, float *top_logprobs, int *top_tokens,
+                       void *workspace, long long workspace_bytes, int rows, int vocab, int top,
+                       long long stride, int dtype, dfa_stream_t stream);
+/*
+ * Their gradient: dlogits (rows, vocab) contiguous, 16-byte aligned, of the logits'
+ * type, for the gradients dlogprobs and dentropy (rows) float32 (NULL: zero), from
+ * the logits, tokens, stats and (with dentropy) entropy of the forward:
+ *   dlogits_j = dlogprobs ([j = token] - p_j) - dentropy p_j (log p_j + entropy).
+ * A row without a token has no use for dlogprobs.  A row of zero gradients, or where
+ * no token can be, gets zeros, whatever its logits are.  dlogits must not overlap the
+ * logits.
+ */
+int dfa_token_logprobs_backward(const void *logits, const void *tokens, int token_bytes,
+                                const float *stats, const float *entropy, const float *dlogprobs,
+                                const float *dentropy, void *dlogits, int rows, int vocab,
+                                long long stride, int dtype, dfa_stream_t stream);
+
+/*
  * Synchronise `stream`, then return and clear the device status word of the
  * current device: DFA_OK, DFA_ETIMEOUT or DFA_EDEVICE (or DFA_ECUDA if the
  * synchronisation itself failed).
@@ -534,6 +639,11 @@ int dfa_cache_blocks(long long total, int limit);
 long long dfa_cache_run(int x, long long total, int blocks);
 int dfa_cache_owner(long long w, long long total, int blocks);
 int dfa_cache_own_end(int len, int i, int n, int block_size);
+/*
+ * dfa_cache4_scale_byte: the e5m2 byte of a group's scale, from the largest of its
+ * values' keys; a value's key is 2 |x| + sign, |x| its bf16 bits without the sign.
+ */
+int dfa_cache4_scale_byte(unsigned top);
 
 /*
  * Tile shapes the kernels use for a head dimension: forward query rows and

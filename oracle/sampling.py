@@ -112,6 +112,72 @@ def append(x, cu_new, cache_lens, table, cache, scale):
     return cache, scale
 
 
+def quantise4(x):
+    """Codes 0 .. 15 and scales of x (..., d) in groups of 32 along d: the scale's size
+    is the smallest of {4, 5, 6, 7} 2^e, within [2^-14, 896], that is at least the
+    largest magnitude over 8; negative where a positive value alone has that magnitude.
+    Codes are 8 + x / scale to the nearest, ties away from 0, within 0 .. 15.  A group
+    with a value that is not finite has scale NaN (and codes of no meaning)."""
+    x = np.asarray(x, np.float64)
+    g = x.reshape(*x.shape[:-1], -1, 32)
+    codes, scales = np.zeros(g.shape, np.int64), np.full(g.shape[:-1], np.nan)
+    sizes = [m * 2.0 ** e for e in range(-16, 8) for m in (4, 5, 6, 7)]
+    assert sizes[0] == 2.0 ** -14 and sizes[-1] == 896
+    for at in np.ndindex(scales.shape):
+        y = g[at]
+        if not np.isfinite(y).all():
+            continue
+        top = np.abs(y).max()
+        s = next((s for s in sizes if 8 * s >= top), sizes[-1])
+        if top > 0 and -top not in y:
+            s = -s
+        n = np.sign(y / s) * np.floor(np.abs(y / s) + 0.5)
+        codes[at], scales[at] = np.clip(n, -8, 7) + 8, s
+    return codes.reshape(x.shape), scales
+
+
+def codes4(packed):
+    """Codes (..., d) of bytes (..., d / 2): eight to a little-endian 32-bit word, those
+    of even dims in its low half, of odd ones in its high half."""
+    words = np.ascontiguousarray(packed, np.uint8).view("<u4")
+    at = [16 * (i % 2) + 4 * (i // 2) for i in range(8)]
+    out = np.stack([(words >> a) & 15 for a in at], -1).astype(np.int64)
+    return out.reshape(*words.shape[:-1], -1)
+
+
+def values4(codes, scales):
+    """Values (..., ps, d) of codes (..., ps, d) and scales (..., d / 32, ps)."""
+    s = np.repeat(np.swapaxes(scales, -1, -2), 32, -1)
+    return (np.asarray(codes, np.float64) - 8) * s
+
+
+def append4(x, cu_new, cache_lens, table, codes, scales):
+    """Append packed x (rows, kv_heads, d) to codes (pages, kv_heads, ps, d) and scales
+    (pages, kv_heads, d / 32, ps); returns new copies."""
+    codes, scales = np.array(codes), np.array(scales, np.float64)
+    n, s = quantise4(x)
+    ps = codes.shape[2]
+    for b, n0 in enumerate(cache_lens):
+        for row in range(cu_new[b], cu_new[b + 1]):
+            pos = n0 + row - cu_new[b]
+            page = table[b][pos // ps]
+            codes[page, :, pos % ps] = n[row]
+            scales[page, :, :, pos % ps] = s[row]
+    return codes, scales
+
+
+def cache_read(values, table, first, cu_rows):
+    """Rows (rows, kv_heads, d) of the tokens first[b], first[b] + 1, ... of each
+    request, from values (pages, kv_heads, ps, d); rows of no request are NaN."""
+    ps = values.shape[2]
+    out = np.full((cu_rows[-1], values.shape[1], values.shape[3]), np.nan)
+    for b, f in enumerate(first):
+        for row in range(cu_rows[b], cu_rows[b + 1]):
+            pos = f + row - cu_rows[b]
+            out[row] = values[table[b][pos // ps], :, pos % ps]
+    return out
+
+
 def cache_attention(q, k_cache, v_cache, k_scale, v_scale, table, cache_lens, cu_new, k=None,
                     v=None, block_size=1):
     """Attention of packed rows q (rows, H, d); caches are float64 e4m3 values.
