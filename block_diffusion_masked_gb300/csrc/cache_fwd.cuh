@@ -282,12 +282,13 @@ constexpr float kMostSum = 32768.f;
 constexpr int kOwnExp = 16;
 constexpr float kOwnUnit = 1 << kOwnExp;
 
-// Up to 32 query rows per key/value head, and headdim 256 (cache_rows.cuh), in tiles
-// of `tile_rows`; more rows, headdim 64 or 128 (cache_wide.cuh): tiles of 128 rows,
-// the tensor maps' boxes are whole pages.
-cudaError_t launch_cache4_rows(const Cache4FwdParams& p, int headdim, int tile_rows,
-                               cudaStream_t stream);
+// More than 32 query rows per key/value head, headdim 64 or 128 (tiles of 128
+// rows; the tensor maps' boxes are whole pages).
 cudaError_t launch_cache_wide(const CacheFwdParams& p, int headdim, cudaStream_t stream);
 cudaError_t launch_cache_wide(const Cache4FwdParams& p, int headdim, cudaStream_t stream);
+// Over the 4-bit cache, up to 32 rows, and headdim 256, in tiles of 8, 16, 32 or 64.
+cudaError_t launch_cache4_rows(const Cache4FwdParams& p, int headdim, int tile_rows,
+                               cudaStream_t stream);
+int cache4_blocks_per_sm(int headdim, int tile_rows);
 
 }  // namespace dfa
