@@ -29,10 +29,11 @@
 // moves only where a unit's probabilities outgrow f16 (cache_fwd.cuh).
 //
 // Work.  Segments (request, key/value head, tile of rows) are dealt to the blocks in
-// equal runs of 128-key units (cache.cuh).  A warp of a block loads them, a ring of
-// stages of 128 keys ahead, over the pieces' ends; four warps take the stage's 32-key
-// units in turn, each with softmax statistics of its own, and join through shared memory
-// at a piece's end.  The pieces of a cut segment are joined by a second launch.
+// equal runs of 128-key units (cache.cuh).  A block's four warps take the 32-key units of
+// a piece in turn, each with a ring of stages of its own, filled by asynchronous copies
+// that run ahead over the pieces' ends, and with softmax statistics of its own: no warp
+// waits for another but at a piece's end, where they join through shared memory.  The
+// pieces of a cut segment are joined by a second launch.
 #include <type_traits>
 
 #include "cache4.cuh"
@@ -41,8 +42,7 @@
 namespace dfa {
 namespace {
 
-constexpr int kUnit = 32;    // keys a warp takes at a time
-constexpr int kStage = 128;  // keys of a stage
+constexpr int kUnit = 32;  // keys a warp takes at a time
 
 // D (16 x 8, float32) = A (16 x 16) B (16 x 8) + C.
 __device__ __forceinline__ void mma_f16(float* d, const uint32_t* a, const uint32_t* b,
@@ -88,37 +88,42 @@ __device__ __forceinline__ T lds(uint32_t addr) {
   return v;
 }
 
-// What the consumers need to know of a stage: valid keys of its eight groups of 16.
-struct StageInfo {
-  unsigned char keys[8];
-};
+// 16 bytes of global memory into shared memory; zeros instead where !there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end_group() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // until all but the last N groups are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-// NT tiles of 8 query rows to a warp, WR warps side by side in rows.
-template <int D, int NT, int WR, int STAGES, int RESIDENT>
+// NT tiles of 8 query rows; WK warps, RESIDENT blocks per SM; STAGES units on their way to
+// a warp; KEPT outputs kept at the join, to which the other warps add theirs.
+template <int D, int NT, int WK, int STAGES, int RESIDENT, int KEPT>
 struct Cache4Tile {
-  static constexpr int kWarps = 4, kWK = kWarps / WR;
-  static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kResident = RESIDENT;  // blocks per SM
-  static constexpr int kRows = 8 * NT * WR;
-  static constexpr int kTile = kStage * D / 2;  // bytes of k, and of v
-  static constexpr int kScales = 1024;          // as in cache_wide.cuh
-  static constexpr int kPitch = D + 4;          // floats per row of a warp's output at the join
-  static constexpr int kKept = kWK > 1 && kRows * D > 2048 ? kWK / 2 : kWK;
+  static constexpr int kThreads = 32 * WK;
+  static constexpr int kResident = RESIDENT;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTile = kUnit * D / 2;  // bytes of a unit's k, and of its v
+  static constexpr int kScales = D;            // and of either's scales, a group after another
+  static constexpr int kPitch = D + 4;         // floats per row of a warp's output at the join
   static constexpr bool kHoldQ = NT * D <= 256;  // query fragments in registers
-  static constexpr int kJoin = kKept * kRows * kPitch * 4;
-  static constexpr int kQ = kHoldQ ? 0 : WR * NT * (D / 16) * 32 * 8;
-  // ring (1024-byte aligned): k, v of each stage | scales | join, before it the query
-  // fragments | statistics
-  static constexpr int kOffScale = STAGES * 2 * kTile;
-  static constexpr int kOffJoin = kOffScale + STAGES * 2 * kScales;
+  static constexpr int kJoin = KEPT * kRows * kPitch * 4;
+  static constexpr int kQ = kHoldQ ? 0 : NT * (D / 16) * 32 * 8;
+  // rings (1024-byte aligned): k, v of each stage | scales | join, before it the query
+  // fragments | statistics | valid keys
+  static constexpr int kOffScale = WK * STAGES * 2 * kTile;
+  static constexpr int kOffJoin = kOffScale + WK * STAGES * 2 * kScales;
   static constexpr int kOffStat = kOffJoin + (kJoin > kQ ? kJoin : kQ);
-  static constexpr int kOffC = kOffStat + kWK * kRows * 8;
-  static constexpr int kOffInfo = kOffC + kWarps * 4;
-  static constexpr int kOffBar = kOffInfo + STAGES * static_cast<int>(sizeof(StageInfo));
-  static constexpr int kOffFlag = kOffBar + STAGES * 16;
-  static constexpr int kSmem = kOffFlag + 16 + 1024;
-  static_assert(kOffBar % 8 == 0 && kSmem <= 232448 && (kSmem + 1024) * RESIDENT <= 233472,
-                "shared memory budget");
+  static constexpr int kOffC = kOffStat + WK * kRows * 8;
+  static constexpr int kOffKeys = kOffC + WK * 4;
+  static constexpr int kSmem = kOffKeys + WK * STAGES * 4 + 1024;
+  static_assert(kSmem <= 232448 && (kSmem + 1024) * RESIDENT <= 233472, "shared memory budget");
 };
 
 // Key of a 16-key tile's row: such that the rows of a matrix, and the keys of a value
@@ -128,7 +133,7 @@ template <int D>
 __device__ __forceinline__ int key_of_row(int r) {
   return D == 256 ? r : 2 * (r & 7) + (r >> 3);
 }
-// Byte `at` of token `key` inside a stage's tile: rows of 128 bytes (headdim 64: of 64),
+// Byte `at` of token `key` inside a unit's tile: rows of 128 bytes (headdim 64: of 64),
 // two tokens each (headdim 256: one), under the row's own swizzle.
 template <int D>
 __device__ __forceinline__ uint32_t tile4_at(uint32_t base, int key, int at) {
@@ -136,10 +141,10 @@ __device__ __forceinline__ uint32_t tile4_at(uint32_t base, int key, int at) {
   return base + (x ^ (((x >> 7) & (D == 64 ? 3 : 7)) << 4));
 }
 
-template <int D, int NT, int WR, int STAGES, int RESIDENT>
-__global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThreads, RESIDENT)
+template <int D, int NT, int WK, int STAGES, int RESIDENT, int KEPT>
+__global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>::kThreads, RESIDENT)
     dfa_cache4_rows_kernel(const __grid_constant__ Cache4FwdParams p) {
-  using T = Cache4Tile<D, NT, WR, STAGES, RESIDENT>;
+  using T = Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>;
   constexpr int kGroups = D / kCache4Group;
   constexpr int kHalf = D == 256 ? 2 : 1;  // value accesses per key
   constexpr int kM = D == 64 ? 4 : 8;      // tiles of 16 head dims per access
@@ -147,125 +152,138 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (smem0 - smem_u32(smem_raw));
   float* s_m = reinterpret_cast<float*>(smem + T::kOffStat);
-  float* s_l = s_m + T::kWK * T::kRows;
+  float* s_l = s_m + WK * T::kRows;
   float* s_c = reinterpret_cast<float*>(smem + T::kOffC);
-  StageInfo* s_info = reinterpret_cast<StageInfo*>(smem + T::kOffInfo);
-  volatile int* s_flag = reinterpret_cast<volatile int*>(smem + T::kOffFlag);
-  const uint32_t bars = smem0 + T::kOffBar;  // of a stage: full, empty
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, wk = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
 
-  if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(bars + 16 * i, 2);                // the stage's bytes, its info
-      mbar_init(bars + 16 * i + 8, T::kWarps);
-    }
-    fence_mbar_init();
-    *s_flag = 0;
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_v);
-    tma_prefetch_desc(&p.tm_ks);
-    tma_prefetch_desc(&p.tm_vs);
-  }
   grid_dependency_wait();
   grid_launch_dependents();
   bool bad = false;
   Piece w = first_piece(p, blockIdx.x, &bad);
   if (bad) atomicOr(p.status, kStatusIndex);
   if (w.b < 0) return;  // the whole block
-  __syncthreads();      // barriers initialised
-  const AbortFlag ab{const_cast<int*>(s_flag), p.status};
 
-  auto stages_of = [&](const Piece& x) {
+  // A piece's units go to the warps in turn: warp wk takes units wk, wk + WK, ...  A unit of
+  // 16-token pages spans two.
+  const bool two = p.page_size < kUnit;
+  auto warp_units = [&](const Piece& x) {
     const int n = piece_end(p, x) - piece_begin(p, x);
-    return n > 0 ? (n + kStage - 1) / kStage : 0;
+    const int units = n > 0 ? (n + kUnit - 1) / kUnit : 0;
+    return units > wk ? (units - wk + WK - 1) / WK : 0;
+  };
+  const uint32_t ring = smem0 + wk * STAGES * 2 * T::kTile;
+  const uint32_t scales = smem0 + T::kOffScale + wk * STAGES * 2 * T::kScales;
+  uint32_t* valid = reinterpret_cast<uint32_t*>(smem + T::kOffKeys) + wk * STAGES;
+  // Copies run ahead of the products, over the ends of pieces: each warp walks the run on
+  // its own (`la`) and fills a stage of its ring as it comes free.  Lane l keeps the pages
+  // of the warp's units 32 i + l.
+  Piece la = w;
+  int la_units, la_u, la_h, la_key, la_end, to_fill = 0;
+  int la_page[2] = {-1, -1};
+  auto enter = [&] {
+    la_units = warp_units(la);
+    la_u = 0;
+    la_h = la.seg / row_tiles(p, la.rq);
+    la_key = piece_begin(p, la) + wk * kUnit;
+    la_end = piece_end(p, la);
+  };
+  enter();
+  auto ahead = [&] {
+    while (la.b >= 0 && la_u >= la_units) {
+      next_piece(p, la);
+      if (la.b >= 0) enter();
+    }
+    if (la.b >= 0) {
+      if ((la_u & 31) == 0) {
+        la_page[0] = la_page[1] = -1;
+        if (la_u + lane < la_units) {
+          const int key = la_key + lane * (WK * kUnit);
+          const int* table = p.block_table + static_cast<long long>(la.b) * p.max_pages;
+          la_page[0] = table[key >> p.page_shift];
+          const bool second = two && key + 16 < la_end;
+          if (second) la_page[1] = table[(key + 16) >> p.page_shift];
+          if (!cache_page_ok(la_page[0], p.num_pages) ||
+              (second && !cache_page_ok(la_page[1], p.num_pages)))
+            atomicOr(p.status, kStatusIndex);
+        }
+      }
+      constexpr int kCopies = T::kTile / 512;
+      const uint32_t dst = ring + to_fill * 2 * T::kTile;
+      const uint32_t dst_scale = scales + to_fill * 2 * T::kScales + 16 * lane;
+      // the i-th 512 bytes of the unit's k or v: 16 bytes a lane
+      auto to = [&](int i) {
+        return dst + 512 * i + (16 * lane ^ ((((lane >> 3) + 4 * i) & (D == 64 ? 3 : 7)) << 4));
+      };
+      // a lane's scales, 16 tokens of a group: of k, then of v
+      const int half = lane & 1, grp = (lane >> 1) % kGroups;
+      const uint8_t* scale = lane >= 2 * kGroups ? p.v4_scale : p.k4_scale;
+      const int page = __shfl_sync(0xffffffffu, la_page[0], la_u & 31);
+      const bool ok = cache_page_ok(page, p.num_pages);
+      int count = ok ? min(16, la_end - la_key) : 0;  // valid keys of either half
+      if (!two) {
+        const int in_page = la_key & (p.page_size - 1);
+        const long long head = static_cast<long long>(ok ? page : 0) * p.Hk + la_h;
+        const long long from = (head * p.page_size + in_page) * (D / 2) + 16 * lane;
+        const uint8_t *k = p.k4 + from, *v = p.v4 + from;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          copy16(to(i), k + 512 * i, ok);
+          copy16(to(i) + T::kTile, v + 512 * i, ok);
+        }
+        if (lane < 4 * kGroups)
+          copy16(dst_scale, scale + (head * kGroups + grp) * p.page_size + in_page + 16 * half, ok);
+        if (ok) count |= max(0, min(16, la_end - la_key - 16)) << 8;
+      } else {
+        const int page1 = __shfl_sync(0xffffffffu, la_page[1], la_u & 31);
+        const bool ok1 = cache_page_ok(page1, p.num_pages);
+        const long long heads[2] = {static_cast<long long>(ok ? page : 0) * p.Hk + la_h,
+                                    static_cast<long long>(ok1 ? page1 : 0) * p.Hk + la_h};
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+          const int x = i / (kCopies / 2);
+          const long long from = heads[x] * (16 * D / 2) + 512 * (i % (kCopies / 2)) + 16 * lane;
+          copy16(to(i), p.k4 + from, x ? ok1 : ok);
+          copy16(to(i) + T::kTile, p.v4 + from, x ? ok1 : ok);
+        }
+        if (lane < 4 * kGroups)
+          copy16(dst_scale, scale + ((half ? heads[1] : heads[0]) * kGroups + grp) * 16,
+                 half ? ok1 : ok);
+        if (ok1) count |= max(0, min(16, la_end - la_key - 16)) << 8;
+      }
+      if (lane == 0) valid[to_fill] = count;
+      ++la_u;
+      la_key += WK * kUnit;
+    }
+    copies_end_group();
+    if (++to_fill == STAGES) to_fill = 0;
   };
 
-  if (warp == T::kWarps) {
-    // ------------------------------------------------------------ loads
-    // Pages of four stages at a time, eight 16-key groups each: lane 8 j + i holds group
-    // i of stage `first` + j.  The load (-1: nothing there) and the look at what it
-    // brought are four stages apart.
-    auto load_page = [&](const Piece& x, int stages, int first) {
-      const int j = first + (lane >> 3);
-      const int key = piece_begin(p, x) + kStage * j + 16 * (lane & 7);
-      return j < stages && key < piece_end(p, x)
-                 ? p.block_table[static_cast<long long>(x.b) * p.max_pages + (key >> p.page_shift)]
-                 : -1;
-    };
-    auto keys_of = [&](const Piece& x, int first, int page) {
-      const int key = piece_begin(p, x) + kStage * (first + (lane >> 3)) + 16 * (lane & 7);
-      return cache_page_ok(page, p.num_pages) ? max(0, min(16, piece_end(p, x) - key)) : 0;
-    };
-    constexpr int kToken = 2 * (D / 2 + kGroups);  // bytes of k and v
-    constexpr int kPair = D == 256 ? 1 : 2;        // tokens of a row of the maps
-    const int per = p.page_size >> 4;
-    int issued = 0;
-    bool ok = true;
-    for (; w.b >= 0 && ok; next_piece(p, w)) {
-      const int h = w.seg / row_tiles(p, w.rq), stages = stages_of(w);
-      int page = load_page(w, stages, 0), next_page = load_page(w, stages, 4);
-      int keys = keys_of(w, 0, page);
-#pragma unroll 1
-      for (int j = 0; j < stages; ++j, ++issued) {
-        if ((j & 3) == 0 && j > 0) {
-          page = next_page, keys = keys_of(w, j, page);
-          next_page = load_page(w, stages, j + 4);
-        }
-        // the first group of each page of this stage issues the page's boxes
-        const bool mine = (lane >> 3) == (j & 3);
-        const bool first = mine && (lane & 7) % per == 0;
-        if (first && keys == 0 &&
-            piece_begin(p, w) + kStage * j + 16 * (lane & 7) < piece_end(p, w))
-          atomicOr(p.status, kStatusIndex);
-        const bool load = first && keys > 0;
-        const unsigned count = __popc(__ballot_sync(0xffffffffu, load));
-        const int s = issued % STAGES;
-        const uint32_t bar = bars + 16 * s;
-        if (issued >= STAGES && !(ok = mbar_wait_warp(bar + 8, (issued / STAGES - 1) & 1, ab)))
-          break;
-        if (lane == 0) mbar_arrive_expect_tx(bar, count * p.page_size * kToken);
-        __syncwarp();
-        if (load) {
-          const uint32_t dst = smem0 + s * 2 * T::kTile + (lane & 7) * (16 * D / 2);
-          const uint32_t sc = smem0 + T::kOffScale + s * 2 * T::kScales + (lane & 7) * 128;
-          const int row = h * p.page_size / kPair;
-          tma_load_3d(dst, &p.tm_k, bar, 0, row, page);
-          tma_load_3d(sc, &p.tm_ks, bar, 0, h * kGroups, page);
-          tma_load_3d(dst + T::kTile, &p.tm_v, bar, 0, row, page);
-          tma_load_3d(sc + T::kScales, &p.tm_vs, bar, 0, h * kGroups, page);
-        }
-        if (mine) s_info[s].keys[lane & 7] = static_cast<unsigned char>(keys);
-        mbar_arrive_warp(bar);
-      }
-    }
-    if (!ok && lane == 0)  // giving up: what is in flight lands first
-      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-        mbar_wait_limited(bars + 16 * (i % STAGES), (i / STAGES) & 1, kWaitLimitNs / 8);
-    return;
-  }
-
-  // -------------------------------------------------------------- attention
-  const int wr = warp % WR, wk = warp / WR;
-  auto consumers = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
   // rows of the matrices that this lane addresses: matrix i = lane / 8 holds rows 8 (i %
   // 2) ... of the 16-key tile i / 2
   const int mat_key = 16 * (lane >> 4) + key_of_row<D>((lane & 7) + (lane & 8));
   const uint32_t mat_at = tile4_at<D>(0, mat_key, 0);
-  int consumed = 0;
-  bool ok = true;
+  // where the values of this lane's four keys of a 16-key tile begin (headdim 256: the
+  // first half's), and the scales of its keys of either product's first group
+  uint32_t val_at[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    val_at[x] = tile4_at<D>(T::kTile, key_of_row<D>(2 * t + (x & 1) + 8 * (x >> 1)), kM * g);
+  const uint32_t ks_at = D == 256 ? g : 2 * g;
+  const uint32_t vs_at =
+      T::kScales + (D == 256 ? 2 * t : 4 * t) + (D == 64 ? g >> 2 : g >> 1) * kUnit;
+  int stage = 0;
+  bool primed = false;
 
-  // A warp that has given up goes on from barrier to barrier, for the others wait there.
 #pragma unroll 1
   for (; w.b >= 0; next_piece(p, w)) {
     const int rtiles = row_tiles(p, w.rq);
     const int h = w.seg / rtiles, tile = w.seg - h * rtiles;
     const int R = w.rq.n * p.G;  // rows of the request and key/value head
-    const int row_base = tile * T::kRows, my_row = row_base + 8 * NT * wr;
-    const int stages = stages_of(w);
+    const int row_base = tile * T::kRows, units = warp_units(w);
     // 8 head dims of a query row: those of word t of a group of 32
     auto load_q = [&](int nt, int grp) {
-      const int r = my_row + 8 * nt + g;
+      const int r = row_base + 8 * nt + g;
       uint4 q = make_uint4(0u, 0u, 0u, 0u);
       if (r < R) {
         const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
@@ -276,9 +294,11 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
     };
     // The queries' fragments for the cached keys, the powers of two, and what the groups'
     // scores begin at.
+    // (as the operand they are, or where registers are short the two that differ)
+    constexpr int kBegin = NT * D <= 128 ? 4 : 2;
     uint32_t qb[T::kHoldQ ? NT : 1][D / 16][2];
-    float factor[NT][2], begin[NT][kGroups][2];
-    const uint32_t q_at = smem0 + T::kOffJoin + (wr * NT * (D / 16) * 32 + lane) * 8;
+    float factor[NT][2], begin[NT][kGroups][kBegin];
+    const uint32_t q_at = smem0 + T::kOffJoin + lane * 8;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint4 q[kGroups];
@@ -321,7 +341,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
         float c[4];
         mma_f16(c, minus8, b, zero);
         mma_f16(c, minus8, b + 2, c);
-        begin[nt][grp][0] = c[0], begin[nt][grp][1] = c[1];
+#pragma unroll
+        for (int x = 0; x < kBegin; ++x) begin[nt][grp][x] = c[x];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if constexpr (T::kHoldQ) {
@@ -334,6 +355,11 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
           }
         }
       }
+    }
+    if (!primed) {  // the run's first copies, behind the queries' loads
+      primed = true;
+#pragma unroll 1
+      for (int i = 0; i < STAGES; ++i) ahead();
     }
     int own = 0;
     if (p.k != nullptr && w.last())
@@ -356,15 +382,17 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
     float unit = 1.f;
 
     // Probabilities of raw scores sc (KT tiles of 16 keys; -inf: not seen) times the rows'
-    // factors f, in the products' other operand's order.  They are taken against the
+    // factors f, over the output's unit if `scaled`, in the products' other operand's order.
+    // They are taken against the
     // reference as it stands; only where their sum says that one may have outgrown f16, or
     // with `look`, is the maximum found and the unit done again.
-    auto soften = [&](auto kt, auto f16, auto& sc, const float (&f)[NT][2], bool look, auto& pf) {
+    auto soften = [&](auto kt, auto f16, auto scaled, auto& sc, const float (&f)[NT][2], bool look,
+                      auto& pf) {
       constexpr int KT = decltype(kt)::value;
       float shrink[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) shrink[nt][0] = shrink[nt][1] = 1.f;
-      const float weight = 1.f / unit;
+      const float weight = decltype(scaled)::value ? 1.f / unit : 1.f;
 #pragma unroll 1
       for (;;) {
         if (look) {
@@ -406,7 +434,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
               float e1 = ex2_approx(fmaf(sc[nt][i][2 * y + 1], f[nt][1], ref[1]));
               sum[nt][0] += e0;
               sum[nt][1] += e1;
-              if (weight != 1.f) e0 *= weight, e1 *= weight;
+              if (decltype(scaled)::value) e0 *= weight, e1 *= weight;
               pf[nt][i][y] = transposed(decltype(f16)::value ? pack_f16x2(e0, e1)
                                                              : pack_bf16x2(e0, e1));
             }
@@ -448,7 +476,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) own_factor[nt][0] = own_factor[nt][1] = p.scale_log2;
 #pragma unroll 1
-      for (int k0 = 16 * wk; k0 < own; k0 += 16 * T::kWK) {
+      for (int k0 = 16 * wk; k0 < own; k0 += 16 * WK) {
         float sc[NT][1][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -480,14 +508,15 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int r = my_row + 8 * nt + 2 * t + x;
+            const int r = row_base + 8 * nt + 2 * t + x;
             end[nt][x] = r < R ? cache_own_end(w.rq.len, r / p.G, w.rq.n, p.bs) : 0;
 #pragma unroll
             for (int y = 0; y < 2; ++y)
               if (k0 + 8 * y + g >= end[nt][x]) sc[nt][0][2 * y + x] = -INFINITY;
           }
         uint32_t pf[NT][1][2];
-        soften(std::integral_constant<int, 1>{}, std::false_type{}, sc, own_factor, true, pf);
+        soften(std::integral_constant<int, 1>{}, std::false_type{}, std::true_type{}, sc, own_factor,
+               true, pf);
         // A row's probability of an own key it does not see is 0, but 0 times a value that is
         // not finite is not: such values leave the product and are added to the rows that
         // see them.
@@ -545,7 +574,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
       // Cached probabilities are f16 and relative to the output's unit, which is to be 1: it
       // comes down, but not so far that the own keys' output, in the new unit, would pass
       // 2^100 (what cached keys lose to that is below 2^-100 of it).
-      if (stages > 0) {
+      if (units > 0) {
         unsigned top = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -568,30 +597,22 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
             for (int x = 0; x < 4; ++x) o[nt][i][x] *= grow;
       }
     }
-    if constexpr (!T::kHoldQ) consumers();  // the queries' fragments
+    if constexpr (!T::kHoldQ) __syncthreads();  // the queries' fragments
 
 #pragma unroll 1
-    for (int j = 0; j < stages && ok; ++j, ++consumed) {
-      const int stage = consumed % STAGES;
-      const uint32_t bar = bars + 16 * stage;
-      if (!(ok = mbar_wait_warp(bar, (consumed / STAGES) & 1, ab))) break;
-      const uint32_t kt = smem0 + stage * 2 * T::kTile;
-      const uint32_t sct = smem0 + T::kOffScale + stage * 2 * T::kScales;
-#pragma unroll 1
-      for (int u = wk; u < kStage / kUnit; u += T::kWK) {
-        const int nv[2] = {s_info[stage].keys[2 * u], s_info[stage].keys[2 * u + 1]};
-        if (nv[0] + nv[1] == 0) continue;  // nothing here, or nothing to be followed
-        const bool whole = nv[0] + nv[1] == 32;
-        // where the scales of the unit's two 16-key tiles lie
-        uint32_t sc_at[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int key = kUnit * u + 16 * i, in_page = key & (p.page_size - 1);
-          sc_at[i] = sct + (key - in_page) * 8 + in_page;
-        }
+    for (int u = 0; u < units; ++u) {
+      copies_wait<STAGES - 1>();
+      __syncwarp();  // every lane's copies
+      const uint32_t kt = ring + stage * 2 * T::kTile;
+      const uint32_t sct = scales + stage * 2 * T::kScales;
+      const unsigned both = valid[stage];
+      if (++stage == STAGES) stage = 0;
+      const int nv[2] = {static_cast<int>(both & 255u), static_cast<int>(both >> 8)};
+      if (both != 0) {  // else nothing is to be followed
+        const bool whole = both == 0x1010u;
         // Scores: sums over the groups of 32 dims.
         float sc[NT][2][4];
-        const uint32_t k_at = kt + u * (kUnit * D / 2) + mat_at;
+        const uint32_t k_at = kt + mat_at;
 #pragma unroll
         for (int grp = 0; grp < kGroups; ++grp) {
           uint32_t word[4];
@@ -603,13 +624,13 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
             {
               uint32_t s2;
               if constexpr (D == 256) {
-                const uint32_t at = sc_at[i] + grp * p.page_size + g;
+                const uint32_t at = sct + ks_at + 16 * i + kUnit * grp;
                 uint32_t s0, s1;
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s0) : "r"(at) : "memory");
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s1) : "r"(at + 8) : "memory");
                 s2 = s0 << 8 | s1 << 24;
               } else {
-                s2 = __byte_perm(lds<unsigned short>(sc_at[i] + grp * p.page_size + 2 * g), 0,
+                s2 = __byte_perm(lds<unsigned short>(sct + ks_at + 16 * i + kUnit * grp), 0,
                                  0x1404);
               }
               const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&s2));
@@ -632,8 +653,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
                   b[s][0] = x.x, b[s][1] = x.y;
                 }
               }
-              const float c0[4] = {begin[nt][grp][0], begin[nt][grp][1], begin[nt][grp][0],
-                                   begin[nt][grp][1]};
+              const float* bg = begin[nt][grp];
+              const float c0[4] = {bg[0], bg[1], bg[kBegin - 2], bg[kBegin - 1]};
               float c[4];
               mma_f16(c, a[0], b[0], c0);
               mma_f16(c, a[1], b[1], c);
@@ -653,26 +674,26 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
                 if (key_of_row<D>(g + 8 * (x >> 1)) >= nv[i]) sc[nt][i][x] = -INFINITY;
         }
         uint32_t pf[NT][2][2];
-        soften(std::integral_constant<int, 2>{}, std::true_type{}, sc, factor, false, pf);
+        const std::integral_constant<int, 2> kt2;
+        if (unit == 1.f)
+          soften(kt2, std::true_type{}, std::false_type{}, sc, factor, false, pf);
+        else
+          soften(kt2, std::true_type{}, std::true_type{}, sc, factor, false, pf);
         // Values: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of a tile's rows, the thread's run of
         // dims of each.  What lies behind the last key may be anything: its scale becomes
         // zero, and with it the value.
-        const uint32_t vt = kt + T::kTile + u * (kUnit * D / 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int half = 0; half < kHalf; ++half) {
-            const int group = (D == 64 ? g >> 2 : g >> 1) + 4 * half;
+            const uint32_t s_at = sct + vs_at + 16 * i + 4 * kUnit * half;
             uint32_t s2[2];
             if constexpr (D == 256) {
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                s2[y] = __byte_perm(lds<unsigned short>(sc_at[i] + T::kScales +
-                                                        group * p.page_size + 2 * t + 8 * y),
-                                    0, 0x1404);
+                s2[y] = __byte_perm(lds<unsigned short>(s_at + 8 * y), 0, 0x1404);
             } else {  // keys 4t, 4t + 2, then 4t + 1, 4t + 3
-              const uint32_t s4 =
-                  lds<uint32_t>(sc_at[i] + T::kScales + group * p.page_size + 4 * t);
+              const uint32_t s4 = lds<uint32_t>(s_at);
               s2[0] = __byte_perm(s4, 0, 0x2404), s2[1] = __byte_perm(s4, 0, 0x3414);
             }
             uint32_t vw[4][kM / 4];
@@ -681,15 +702,15 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
             for (int y = 0; y < 2; ++y) {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const int key = key_of_row<D>(2 * t + x + 8 * y);
-                const uint32_t at = tile4_at<D>(vt, 16 * i + key, kM * g + 64 * half);
+                const uint32_t at = kt + (val_at[2 * y + x] ^ (64 * half)) + i * (16 * D / 2);
                 if constexpr (D == 64) {
                   vw[2 * y + x][0] = lds<uint32_t>(at);
                 } else {
                   const uint2 w2 = lds<uint2>(at);
                   vw[2 * y + x][0] = w2.x, vw[2 * y + x][1] = w2.y;
                 }
-                if (!whole && key >= nv[i]) s2[y] &= x ? 0x0000ffffu : 0xffff0000u;
+                if (!whole && key_of_row<D>(2 * t + x + 8 * y) >= nv[i])
+                  s2[y] &= x ? 0x0000ffffu : 0xffff0000u;
               }
               sv[y] = cache4_prepare(s2[y]);
             }
@@ -713,7 +734,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
           }
         }
       }
-      mbar_arrive_warp(bar + 8);
+      __syncwarp();  // the unit has been read
+      ahead();
     }
 
     // Join the warps: statistics first, then each warp's output in a common unit, summed.
@@ -724,31 +746,31 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
           l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], off);
-        if (g == 0) s_m[wk * T::kRows + 8 * (NT * wr + nt) + 2 * t + x] = m[nt][x];
+        if (g == 0) s_m[wk * T::kRows + 8 * nt + 2 * t + x] = m[nt][x];
       }
-    if (lane == 0) s_c[warp] = unit;
-    consumers();  // statistics written, the last piece's join read
+    if (lane == 0) s_c[wk] = unit;
+    __syncthreads();  // statistics written, the last piece's join read
     float unit_all = s_c[0];
 #pragma unroll
-    for (int i = 1; i < T::kWarps; ++i) unit_all = fmaxf(unit_all, s_c[i]);
-    // The last kKept warps of a row leave their outputs, the others add theirs to them.
+    for (int i = 1; i < WK; ++i) unit_all = fmaxf(unit_all, s_c[i]);
+    // kKept warps of a row leave their outputs, the others, as many at a time, add theirs.
     float* join = reinterpret_cast<float*>(smem + T::kOffJoin);
 #pragma unroll 1
-    for (int turn = 0; turn < T::kWK / T::kKept; ++turn) {
-      const bool add = turn == 1;
-      if ((wk >= T::kWK - T::kKept) != add) {
+    for (int turn = 0; turn < (WK + KEPT - 1) / KEPT; ++turn) {
+      const bool add = turn > 0;
+      if (wk / KEPT == turn) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int r = 8 * (NT * wr + nt) + 2 * t + x;
+            const int r = 8 * nt + 2 * t + x;
             float top = s_m[r];
 #pragma unroll
-            for (int i = 1; i < T::kWK; ++i) top = fmaxf(top, s_m[i * T::kRows + r]);
+            for (int i = 1; i < WK; ++i) top = fmaxf(top, s_m[i * T::kRows + r]);
             const float f = m[nt][x] == -INFINITY ? 0.f : ex2_approx(m[nt][x] - top);
             const float fo = f * (unit / unit_all);
             if (g == 0) s_l[wk * T::kRows + r] = l[nt][x] * f;
-            float* dst = join + ((wk % T::kKept) * T::kRows + r) * T::kPitch;
+            float* dst = join + ((wk % KEPT) * T::kRows + r) * T::kPitch;
 #pragma unroll
             for (int i = 0; i < kHalf * kM; i += 2) {
               float4* at = reinterpret_cast<float4*>(dst + 128 * (i / kM) + 2 * kM * g +
@@ -763,21 +785,21 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
             }
           }
       }
-      consumers();
+      __syncthreads();
     }
     const bool single = w.whole();
-    for (int i = tid; i < T::kRows * (D / 4); i += 32 * T::kWarps) {
+    for (int i = tid; i < T::kRows * (D / 4); i += T::kThreads) {
       const int r = i / (D / 4), d4 = i - r * (D / 4);
       if (row_base + r >= R) break;
       float sum = 0.f, top = -INFINITY;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < T::kWK; ++x) {
+      for (int x = 0; x < WK; ++x) {
         sum += s_l[x * T::kRows + r];
         top = fmaxf(top, s_m[x * T::kRows + r]);
       }
 #pragma unroll
-      for (int x = 0; x < T::kKept; ++x) {
+      for (int x = 0; x < KEPT; ++x) {
         const float4 y =
             *reinterpret_cast<const float4*>(join + (x * T::kRows + r) * T::kPitch + 4 * d4);
         a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
@@ -799,29 +821,35 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WR, STAGES, RESIDENT>::kThre
         if (d4 == 0) p.part_lse[at] = lse2;
       }
     }
-    consumers();  // the join has been read
+    __syncthreads();  // the join has been read
   }  // pieces
 }
 
 // Row tiles, stages and blocks per SM for a head dimension and a segment's rows.
 template <int D, int ROWS>
 struct Variant;
-template <> struct Variant<64, 8> { using T = Cache4Tile<64, 1, 1, 4, 4>; };
-template <> struct Variant<64, 16> { using T = Cache4Tile<64, 2, 1, 4, 3>; };
-template <> struct Variant<64, 32> { using T = Cache4Tile<64, 4, 1, 4, 2>; };
-template <> struct Variant<128, 8> { using T = Cache4Tile<128, 1, 1, 3, 3>; };
-template <> struct Variant<128, 16> { using T = Cache4Tile<128, 2, 1, 4, 2>; };
-template <> struct Variant<128, 32> { using T = Cache4Tile<128, 4, 1, 3, 2>; };
-template <> struct Variant<256, 8> { using T = Cache4Tile<256, 1, 1, 2, 2>; };
-template <> struct Variant<256, 16> { using T = Cache4Tile<256, 2, 1, 2, 2>; };
-template <> struct Variant<256, 32> { using T = Cache4Tile<256, 2, 2, 2, 2>; };
-template <> struct Variant<256, 64> { using T = Cache4Tile<256, 2, 4, 4, 1>; };
+#define V64_8 1, 4, 4, 4, 4
+#define V64_16 2, 4, 5, 3, 4
+#define V64_32 4, 4, 5, 2, 4
+#define V128_8 1, 4, 3, 3, 4
+#define V128_16 2, 4, 4, 2, 4
+#define V128_32 4, 4, 4, 2, 2
+#define V256_8 1, 4, 2, 2, 4
+#define V256_16 2, 4, 2, 2, 2
+template <> struct Variant<64, 8> { using T = Cache4Tile<64, V64_8>; };
+template <> struct Variant<64, 16> { using T = Cache4Tile<64, V64_16>; };
+template <> struct Variant<64, 32> { using T = Cache4Tile<64, V64_32>; };
+template <> struct Variant<128, 8> { using T = Cache4Tile<128, V128_8>; };
+template <> struct Variant<128, 16> { using T = Cache4Tile<128, V128_16>; };
+template <> struct Variant<128, 32> { using T = Cache4Tile<128, V128_32>; };
+template <> struct Variant<256, 8> { using T = Cache4Tile<256, V256_8>; };
+template <> struct Variant<256, 16> { using T = Cache4Tile<256, V256_16>; };
 
-template <int D, int NT, int WR, int STAGES, int RESIDENT>
-cudaError_t launch_tile(Cache4Tile<D, NT, WR, STAGES, RESIDENT>, const Cache4FwdParams& p,
+template <int D, int NT, int WK, int STAGES, int RESIDENT, int KEPT>
+cudaError_t launch_tile(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>, const Cache4FwdParams& p,
                         cudaStream_t stream) {
-  using T = Cache4Tile<D, NT, WR, STAGES, RESIDENT>;
-  auto kern = dfa_cache4_rows_kernel<D, NT, WR, STAGES, RESIDENT>;
+  using T = Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>;
+  auto kern = dfa_cache4_rows_kernel<D, NT, WK, STAGES, RESIDENT, KEPT>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   if (e != cudaSuccess) return e;
@@ -842,8 +870,6 @@ R for_variant(int d, int rows, R none, F f) {
   } else if (d == 256) {
     if (rows == 8) return f(Variant<256, 8>::T{});
     if (rows == 16) return f(Variant<256, 16>::T{});
-    if (rows == 32) return f(Variant<256, 32>::T{});
-    if (rows == 64) return f(Variant<256, 64>::T{});
   }
   return none;
 }

@@ -1011,7 +1011,7 @@ CachePlan cache4_plan_for(int batch, int max_new, int G, int kv_heads, int d, lo
                           int sms) {
   CachePlan c;
   const long long rows = static_cast<long long>(max_new) * G;
-  c.tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : d == 256 ? 64 : 128;
+  c.tile_rows = rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : rows <= 32 ? 32 : 128;
   c.finish = 6;
   c.blocks = sms * cache4_blocks_per_sm(d, c.tile_rows);
   const long long segments =
@@ -1107,30 +1107,40 @@ int cache_forward(const void* q, const void* k, const void* v, const void* k_cac
                                      static_cast<long long>(max_pages) * page_size, di.sms);
   if (!c.whole && (!workspace || workspace_bytes < c.workspace(d))) return DFA_EINVAL;
   CacheParams<BITS> p{};
-  // boxes are whole pages but for the 8-bit kernel of few rows
-  const int box_keys = BITS == 8 && c.tile_rows < 128 && page_size > kUnit ? kUnit : page_size;
-  const cuuint64_t head_keys = static_cast<cuuint64_t>(kv_heads) * page_size;
-  // A row of a map: a token's values, or 4 bits: of two tokens up to headdim 128.
-  const int pair = BITS == 4 && d < 256 ? 2 : 1, width = d * pair * BITS / 8;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), head_keys / pair,
-                              static_cast<cuuint64_t>(num_pages)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width), dims[1] * width};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(width < 128 ? width : 128),
-                             static_cast<cuuint32_t>(box_keys / pair), 1};
-  const CUtensorMapSwizzle swizzle =
-      d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  if (const int rc = encode_map_u8(&p.tm_k, k_cache, 3, dims, strides, box, swizzle)) return rc;
-  if (const int rc = encode_map_u8(&p.tm_v, v_cache, 3, dims, strides, box, swizzle)) return rc;
+  const bool wide = c.tile_rows == 128;
+  if (BITS == 8 || wide) {
+    // boxes are whole pages but for the 8-bit kernel of few rows
+    const int box_keys = !wide && page_size > kUnit ? kUnit : page_size;
+    const cuuint64_t head_keys = static_cast<cuuint64_t>(kv_heads) * page_size;
+    // A row of a map: a token's values; 4 bits: those of two.
+    const int pair = BITS == 4 ? 2 : 1, width = d * pair * BITS / 8;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), head_keys / pair,
+                                static_cast<cuuint64_t>(num_pages)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width), dims[1] * width};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(width < 128 ? width : 128),
+                               static_cast<cuuint32_t>(box_keys / pair), 1};
+    const CUtensorMapSwizzle swizzle =
+        d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (const int rc = encode_map_u8(&p.tm_k, k_cache, 3, dims, strides, box, swizzle)) return rc;
+    if (const int rc = encode_map_u8(&p.tm_v, v_cache, 3, dims, strides, box, swizzle)) return rc;
+  }
   if constexpr (BITS == 4) {
-    const cuuint64_t groups = static_cast<cuuint64_t>(kv_heads) * (d / kCache4Group);
-    const cuuint64_t sdims[3] = {static_cast<cuuint64_t>(page_size), groups, dims[2]};
-    const cuuint64_t sstrides[2] = {sdims[0], sdims[0] * groups};
-    const cuuint32_t sbox[3] = {static_cast<cuuint32_t>(box_keys),
-                                static_cast<cuuint32_t>(d / kCache4Group), 1};
-    for (int i = 0; i < 2; ++i)
-      if (const int rc = encode_map_u8(i ? &p.tm_vs : &p.tm_ks, i ? v_scale : k_scale, 3, sdims,
-                                       sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE))
-        return rc;
+    p.k4 = static_cast<const uint8_t*>(k_cache);
+    p.v4 = static_cast<const uint8_t*>(v_cache);
+    p.k4_scale = static_cast<const uint8_t*>(k_scale);
+    p.v4_scale = static_cast<const uint8_t*>(v_scale);
+    if (wide) {
+      const cuuint64_t groups = static_cast<cuuint64_t>(kv_heads) * (d / kCache4Group);
+      const cuuint64_t dims[3] = {static_cast<cuuint64_t>(page_size), groups,
+                                  static_cast<cuuint64_t>(num_pages)};
+      const cuuint64_t strides[2] = {dims[0], dims[0] * groups};
+      const cuuint32_t box[3] = {static_cast<cuuint32_t>(page_size),
+                                 static_cast<cuuint32_t>(d / kCache4Group), 1};
+      for (int i = 0; i < 2; ++i)
+        if (const int rc = encode_map_u8(i ? &p.tm_vs : &p.tm_ks, i ? v_scale : k_scale, 3, dims,
+                                         strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+          return rc;
+    }
   } else {
     p.k_scale = static_cast<const float*>(k_scale);
     p.v_scale = static_cast<const float*>(v_scale);
@@ -1177,7 +1187,7 @@ int cache_forward(const void* q, const void* k, const void* v, const void* k_cac
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if constexpr (BITS == 4)
-    e = c.tile_rows == 128 ? launch_cache_wide(p, d, s) : launch_cache4_rows(p, d, c.tile_rows, s);
+    e = wide ? launch_cache_wide(p, d, s) : launch_cache4_rows(p, d, c.tile_rows, s);
   else
     e = d == 64    ? launch_cache_rows<64>(p, c.tile_rows, s)
         : d == 128 ? launch_cache_rows<128>(p, c.tile_rows, s)

@@ -46,10 +46,11 @@ struct CacheFwdParams {
   float scale_log2;
 };
 
-// Over the 4-bit cache: the scales' maps too, (page_size, kv_heads * headdim / 32,
-// pages) bytes; k_scale and v_scale are not used.
+// Over the 4-bit cache (cache4.cuh): its arrays, and for cache_wide.cuh the scales' maps,
+// (page_size, kv_heads * headdim / 32, pages) bytes; k_scale and v_scale are not used.
 struct Cache4FwdParams : CacheFwdParams {
   CUtensorMap tm_ks, tm_vs;
+  const uint8_t *k4, *v4, *k4_scale, *v4_scale;
 };
 template <int BITS>
 struct CacheParamsOf {
@@ -286,7 +287,8 @@ constexpr float kOwnUnit = 1 << kOwnExp;
 // rows; the tensor maps' boxes are whole pages).
 cudaError_t launch_cache_wide(const CacheFwdParams& p, int headdim, cudaStream_t stream);
 cudaError_t launch_cache_wide(const Cache4FwdParams& p, int headdim, cudaStream_t stream);
-// Over the 4-bit cache, up to 32 rows, and headdim 256, in tiles of 8, 16, 32 or 64.
+// Over the 4-bit cache, up to 32 rows, and headdim 256, in tiles of 8, 16 or 32
+// (headdim 256: 8 or 16).
 cudaError_t launch_cache4_rows(const Cache4FwdParams& p, int headdim, int tile_rows,
                                cudaStream_t stream);
 int cache4_blocks_per_sm(int headdim, int tile_rows);
