@@ -52,24 +52,30 @@ __device__ __forceinline__ float cache4_scale(unsigned byte) {
   return __half2float(*reinterpret_cast<const __half*>(&h));
 }
 
-// Two scales as f16x2, prepared for cache4_decode: s / 16 and -72 s.
+// cache4_decode gives a sixteenth of the values: all of its steps are exact then, with
+// half of the codes left where they stand.
+constexpr float kCache4Unit = 16.f;
+// Two scales s as f16x2, prepared for it.
 struct Cache4Scale {
-  __half2 sixteenth, bias;
+  __half2 low, low_bias, high, high_bias;  // s / 16, -64.5 s; s / 256, -4.5 s
 };
 __device__ __forceinline__ Cache4Scale cache4_prepare(uint32_t s2) {
   const __half2 s = *reinterpret_cast<const __half2*>(&s2);
-  return {__hmul2(s, __float2half2_rn(0.0625f)), __hmul2(s, __float2half2_rn(-72.f))};
+  return {__hmul2(s, __float2half2_rn(0.0625f)), __hmul2(s, __float2half2_rn(-64.5f)),
+          __hmul2(s, __float2half2_rn(0.00390625f)), __hmul2(s, __float2half2_rn(-4.5f))};
 }
-// Codes 4 i .. 4 i + 3 of the low half of w and of its high half, as four pairs of
-// f16 values, low half first.  A code n in bits 4 to 7 of f16's 1024 makes it
-// 1024 + 16 n; times s / 16 less 72 s that is (n - 8) s, exactly: 72 s has 6 bits and
-// is at most 64512.
+// Codes 4 i .. 4 i + 3 of the low half of w and of its high half, as four pairs of f16
+// values, low half first, each (n - 8) s / 16.  A code n in bits 0 to 3 of f16's 1024 makes
+// it 1024 + n: times s / 16 less 1032 s / 16; in bits 4 to 7, 1024 + 16 n: times s / 256
+// less 72 s / 16.  The factors are products of s' three bits with powers of two, 129 / 2 and
+// 9 / 2, at most 57792 and at least steps of 2^-24: exact in f16, and so are the sums.
 __device__ __forceinline__ void cache4_decode(uint32_t w, const Cache4Scale& s, uint32_t (&f)[4]) {
-  const uint32_t at[4] = {w << 4, w, w >> 4, w >> 8};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t x = (at[i] & 0x00f000f0u) | 0x64006400u;
-    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x), s.sixteenth, s.bias);
+    const uint32_t from = i < 2 ? w : w >> 8;
+    const uint32_t x = (from & (i & 1 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+    const __half2 n = *reinterpret_cast<const __half2*>(&x);
+    const __half2 y = i & 1 ? __hfma2(n, s.high, s.high_bias) : __hfma2(n, s.low, s.low_bias);
     f[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
 }

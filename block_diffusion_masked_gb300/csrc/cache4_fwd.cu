@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[nt][i][x] = 0.f;
     }
-    // The output's unit, a power of two: 1, the cached values' own, or larger for own ones.
-    float unit = 1.f;
+    // The output's unit, a power of two: the cached values' own, or larger for own ones.
+    float unit = kCache4Unit;
 
     // Probabilities of raw scores sc (KT tiles of 16 keys; -inf: not seen) times the rows'
     // factors f, over the output's unit if `scaled`, in the products' other operand's order.
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
       float shrink[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) shrink[nt][0] = shrink[nt][1] = 1.f;
-      const float weight = decltype(scaled)::value ? 1.f / unit : 1.f;
+      const float weight = decltype(scaled)::value ? (decltype(f16)::value ? kCache4Unit : 1.f) / unit : 1.f;
 #pragma unroll 1
       for (;;) {
         if (look) {
@@ -571,8 +571,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
           }
         }
       }
-      // Cached probabilities are f16 and relative to the output's unit, which is to be 1: it
-      // comes down, but not so far that the own keys' output, in the new unit, would pass
+      // Cached probabilities are f16 and relative to the output's unit, which is to be theirs:
+      // it comes down, but not so far that the own keys' output, in the new unit, would pass
       // 2^100 (what cached keys lose to that is below 2^-100 of it).
       if (units > 0) {
         unsigned top = 0;
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
               top = max(top, y < 0x7f800000u ? y : 0u);
             }
         top = __reduce_max_sync(0xffffffffu, top);
-        const int down = max(min(127 + 99 - static_cast<int>(top >> 23), kOwnExp), 0);
+        const int down = max(min(127 + 99 - static_cast<int>(top >> 23), kOwnExp - 4), 0);
         const float grow = pow2_bits(down);
         unit *= pow2_bits(-down);
 #pragma unroll
@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
         }
         uint32_t pf[NT][2][2];
         const std::integral_constant<int, 2> kt2;
-        if (unit == 1.f)
+        if (unit == kCache4Unit)
           soften(kt2, std::true_type{}, std::false_type{}, sc, factor, false, pf);
         else
           soften(kt2, std::true_type{}, std::true_type{}, sc, factor, false, pf);

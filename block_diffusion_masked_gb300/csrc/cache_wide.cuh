@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
     // The loads of k also write the tiles' infos; pages are asked for four tiles
     // ahead, scales three: they may come from memory under full load.
     auto load_scales = [&](int h, int page, float* ks, float* vs) {
-      if constexpr (BITS == 4) {  // they come with the tile: a page's own is 1
-        *ks = *vs = 1.f;
+      if constexpr (BITS == 4) {  // they come with the tile, whose values are sixteenths
+        *ks = *vs = kCache4Unit;
         return;
       }
       const bool has = !isv && cache_page_ok(page, p.num_pages);
