@@ -17,6 +17,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "device.cuh"
 #include "dfa.h"
 #include "params.cuh"
@@ -26,12 +28,13 @@ namespace dfa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 4;  // of the kernel that reads the logits
 constexpr int kMaxTop = 32;
 constexpr int kMaxSplits = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// A logit this far below the maximum has probability 0 in float32; what is
-// further, -inf too, is taken as this far, for 0 * inf is not a number.
-constexpr float kFar = -150.f;
+// A logit this far below the maximum, in powers of two, has probability 0 in float32;
+// what is further, -inf too, is taken as this far, for 0 * inf is not a number.
+constexpr float kFar = -220.f;
 
 // ------------------------------------------------------------------ rows of logits
 
@@ -52,6 +55,33 @@ struct Logit<__nv_bfloat16> {
   __device__ static uint4 pack(const float* f) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
+  }
+  // Values no lower than one whose product with log2 e is finite (a NaN stays), two to an
+  // operation.
+  __device__ static uint4 finite(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w}, low = 0xff00ff00u;  // -2^127
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 x = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&u[i]),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&low));
+      y[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  // Whether what finite() replaces, and whatever else is far, is out of m's reach.
+  __device__ static bool plain(float m) { return fabsf(m) < 1e30f; }
+  // The largest of m and N vectors' values.
+  template <int N>
+  __device__ static float most(float m, const uint4* w) {
+    __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[0].x);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x = __hmax2(x, *reinterpret_cast<const __nv_bfloat162*>(&v[i]));
+    }
+    return fmax3(m, __low2float(x), __high2float(x));
   }
   __device__ static float get(__nv_bfloat16 x) { return __bfloat162float(x); }
   __device__ static __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
@@ -77,6 +107,29 @@ struct Logit<__half> {
     }
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
+  __device__ static uint4 finite(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w}, low = 0xfbfffbffu;
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 x = __hmax2_nan(*reinterpret_cast<const __half2*>(&u[i]),
+                                    *reinterpret_cast<const __half2*>(&low));
+      y[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  __device__ static bool plain(float m) { return m > -60000.f && m < INFINITY; }
+  template <int N>
+  __device__ static float most(float m, const uint4* w) {
+    __half2 x = *reinterpret_cast<const __half2*>(&w[0].x);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x = __hmax2(x, *reinterpret_cast<const __half2*>(&v[i]));
+    }
+    return fmax3(m, __low2float(x), __high2float(x));
+  }
   __device__ static float get(__half x) { return __half2float(x); }
   __device__ static __half put(float x) { return __float2half_rn(x); }
 };
@@ -91,6 +144,16 @@ struct Logit<float> {
   __device__ static uint4 pack(const float* f) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                       __float_as_uint(f[3]));
+  }
+  __device__ static uint4 finite(const uint4& w) { return w; }
+  __device__ static bool plain(float m) { return fabsf(m) < 1e30f; }
+  template <int N>
+  __device__ static float most(float m, const uint4* w) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      m = fmax3(fmax3(m, __uint_as_float(w[u].x), __uint_as_float(w[u].y)),
+                __uint_as_float(w[u].z), __uint_as_float(w[u].w));
+    return m;
   }
   __device__ static float get(float x) { return x; }
   __device__ static float put(float x) { return x; }
@@ -129,15 +192,27 @@ __device__ __forceinline__ float not_far(float x) {
   return x;
 }
 
-// Running statistics of a softmax: the maximum m, the sum s of exp(x - m) and the
-// sum t of exp(x - m) (x - m).  Nothing yet: m -inf, s and t 0.
+// Running statistics of a softmax: the maximum m, and against its reference r = m log2 e,
+// rounded, with z = x log2 e - r, the sum s of 2^z and the sum t of 2^z z.  A z is one
+// operation, rounded once, relative to itself; what the rounding of r adds to all of them
+// is taken off at the end (finish).  Nothing yet: m -inf, s and t 0.
 struct Stats {
   float m, s, t;
 };
+// Where r would overflow, or nearly (a row of the type's lowest value), z is (x - m) log2 e
+// in its place.
+__device__ __forceinline__ bool extreme(float m) { return fabsf(m) > 1e30f && m != -INFINITY; }
+// (__fmul_rn: the rounding is to be the same wherever r appears, so the product is not to be
+// drawn into a sum.)
+__device__ __forceinline__ float reference(float m) {
+  return m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e);
+}
 // a against the maximum m >= a.m.
 __device__ __forceinline__ Stats rebase(const Stats& a, float m) {
   if (a.m == -INFINITY) return {m, a.s, a.t};  // nothing yet, or not a number
-  const float d = not_far(a.m - m), f = ex2_approx(d * kLog2e);
+  const float d = not_far(extreme(a.m) || extreme(m) ? (a.m - m) * kLog2e
+                                                     : reference(a.m) - reference(m));
+  const float f = ex2_approx(d);
   return {m, a.s * f, f * fmaf(a.s, d, a.t)};
 }
 __device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
@@ -146,10 +221,15 @@ __device__ __forceinline__ Stats join(const Stats& a, const Stats& b) {
   return {m, x.s + y.s, x.t + y.t};
 }
 __device__ __forceinline__ Stats warp_join(Stats a) {
+  float m = a.m;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    a = join(a, {__shfl_xor_sync(0xffffffffu, a.m, off), __shfl_xor_sync(0xffffffffu, a.s, off),
-                 __shfl_xor_sync(0xffffffffu, a.t, off)});
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  a = rebase(a, m);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    a.s += __shfl_xor_sync(0xffffffffu, a.s, off);
+    a.t += __shfl_xor_sync(0xffffffffu, a.t, off);
+  }
   return a;
 }
 
@@ -192,21 +272,9 @@ struct ScoresParams {
   bool wide_tokens;  // 64 bits
 };
 
-// The row's token: -1 where none is given, or one that there is not.
-__device__ __forceinline__ int load_token(const ScoresParams& p, int row) {
-  if (p.tokens == nullptr) return -1;
-  const long long t = p.wide_tokens ? static_cast<const long long*>(p.tokens)[row]
-                                    : static_cast<const int*>(p.tokens)[row];
-  if (t >= p.vocab) {
-    atomicOr(p.status, kStatusIndex);
-    return -1;
-  }
-  return t < 0 ? -1 : static_cast<int>(t);
-}
-
 // What every thread needs of a finished row.
 struct Finished {
-  float m, log_s;
+  float m, log_s, entropy;
   bool none, nan;  // no token can be (every logit -inf); a logit is not a number
 };
 __device__ __forceinline__ Finished finish(const Stats& a) {
@@ -214,23 +282,39 @@ __device__ __forceinline__ Finished finish(const Stats& a) {
   f.none = a.m == -INFINITY && a.s == 0.f;
   f.nan = !f.none && !(a.s < INFINITY);
   f.m = f.nan ? NAN : a.m;
-  f.log_s = f.none ? 0.f : lg2_approx(a.s) * kLn2;
+  // every z is too large by what r is too small
+  const float off =
+      f.none || f.nan || extreme(a.m) ? 0.f : fmaf(a.m, kLog2e, -reference(a.m));
+  const float log2_s = lg2_approx(a.s) - off;
+  f.log_s = f.none ? 0.f : f.nan ? NAN : log2_s * kLn2;
+  f.entropy = f.none ? 0.f : f.nan ? NAN : fmaxf((log2_s - (a.t / a.s - off)) * kLn2, 0.f);
   return f;
 }
-// One thread writes the row's numbers.
+// The row's token and its logit.
+struct Token {
+  int index;  // -1: none
+  float logit;
+};
 template <typename T>
-__device__ __forceinline__ void write_row(const ScoresParams& p, int row, const Stats& a,
-                                          const Finished& f) {
-  p.entropy[row] = f.none ? 0.f : f.nan ? NAN : fmaxf(f.log_s - a.t / a.s, 0.f);
-  *reinterpret_cast<float2*>(p.stats + 2LL * row) = make_float2(f.m, f.log_s);
-  const int token = load_token(p, row);
-  if (p.logprobs == nullptr) return;
-  float y = 0.f;
-  if (token >= 0) {
-    const T* x = static_cast<const T*>(p.x) + row * p.stride;
-    y = f.none ? -INFINITY : (Logit<T>::get(x[token]) - f.m) - f.log_s;
+__device__ __forceinline__ Token load_token(const ScoresParams& p, int row) {
+  Token t = {-1, 0.f};
+  if (p.tokens == nullptr) return t;
+  const long long i = p.wide_tokens ? static_cast<const long long*>(p.tokens)[row]
+                                    : static_cast<const int*>(p.tokens)[row];
+  if (i >= p.vocab) atomicOr(p.status, kStatusIndex);
+  if (i >= 0 && i < p.vocab) {
+    t.index = static_cast<int>(i);
+    t.logit = Logit<T>::get((static_cast<const T*>(p.x) + row * p.stride)[t.index]);
   }
-  p.logprobs[row] = y;
+  return t;
+}
+// One thread writes the row's numbers.
+__device__ __forceinline__ void write_row(const ScoresParams& p, int row, const Finished& f,
+                                          const Token& t) {
+  p.entropy[row] = f.entropy;
+  *reinterpret_cast<float2*>(p.stats + 2LL * row) = make_float2(f.m, f.log_s);
+  if (p.logprobs == nullptr) return;
+  p.logprobs[row] = t.index < 0 ? 0.f : f.none ? -INFINITY : (t.logit - f.m) - f.log_s;
 }
 // Alternative i of a row, of its key (0: there is none).
 __device__ __forceinline__ void write_top(const ScoresParams& p, int row, int i, Key key,
@@ -244,18 +328,47 @@ __device__ __forceinline__ void write_top(const ScoresParams& p, int row, int i,
 
 // ------------------------------------------------------------------ forward
 
-// Alternatives are gathered in shared memory: a list that a round of the block's
-// threads may add a vector each to, and a place for the best of it.
-constexpr int kListMost = kThreads * 8;   // what a round adds at most
+// Alternatives are gathered in shared memory, in a list.  Where there may be more than it
+// has room for, some threads add a vector each and it is cut down between such rounds.
+constexpr int kListThreads = 64;          // that add to it in a round
+constexpr int kListMost = kListThreads * 8;
 constexpr int kListKeep = 512;            // a longer list is cut down between rounds
+constexpr int kListMore = 16;             // the two vectors that are not whole
+constexpr int kList = kListKeep + kListMost + kListMore;
+constexpr int kSlots = 32;
 struct TopSpace {
-  Key list[kListKeep + kListMost];
+  Key list[kList];
   Key best[kMaxTop];
-  float top[kThreads];  // the threads' largest logits
-  int hot[kThreads];    // threads that may have one of the alternatives
+  float slot[kSlots][kThreads];  // the largest logit of every run of a thread's batches
+  uint32_t top[kThreads];  // the threads' largest logits, ordered; each warp's sorted
+  int hot[kThreads];       // threads that may have one of the alternatives
   int count, hots;
-  uint32_t least;       // no alternative is below this (ordered)
+  uint32_t least;          // no alternative is below this (ordered)
 };
+
+// The larger of x and lane ^ mask's in the lanes that `up` says, the smaller in the others.
+__device__ __forceinline__ uint32_t exchange(uint32_t x, int mask, bool up) {
+  const uint32_t y = __shfl_xor_sync(0xffffffffu, x, mask);
+  return up ? max(x, y) : min(x, y);
+}
+// The warp's values, the largest in lane 0: a bitonic sort.
+__device__ __forceinline__ uint32_t warp_sorted(uint32_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int mask = size >> 1; mask > 0; mask >>= 1)
+      x = exchange(x, mask, ((lane & mask) == 0) == ((lane & size) == 0));
+  return x;
+}
+// The 32 largest of the warp's and of another sorted 32, sorted.
+__device__ __forceinline__ uint32_t warp_merged(uint32_t x, const uint32_t* other) {
+  const int lane = threadIdx.x & 31;
+  x = max(x, other[31 - lane]);  // rises, then falls
+#pragma unroll
+  for (int mask = 16; mask > 0; mask >>= 1) x = exchange(x, mask, (lane & mask) == 0);
+  return x;
+}
 
 // The `top` largest keys of the list, in order, into `best` (0 behind the last).
 __device__ __forceinline__ void best_of_list(TopSpace& s, int top) {
@@ -265,130 +378,273 @@ __device__ __forceinline__ void best_of_list(TopSpace& s, int top) {
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const Key key = s.list[i];
     int above = 0;
-    for (int j = 0; j < n; ++j) above += s.list[j] > key;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 8) {
+      Key other[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) other[e] = j + e < n ? s.list[j + e] : 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) above += other[e] > key;
+    }
     if (above < top) s.best[above] = key;
   }
 }
 
-// One block per row, or per piece of one: a thread walks vectors of the piece, the
-// block's width apart, with statistics of its own against its own maximum, the next
-// vectors on their way; one join at the end.
+// A block takes rows, or pieces of rows, one after another: a thread walks vectors of a
+// piece, the block's width apart, with statistics of its own against its own maximum, the
+// next vectors on their way; one join at the piece's end, while the next piece's first
+// vectors are.
 //
-// Alternatives: the block's `top` largest logits are among the threads whose
-// largest is one of the `top` largest of the threads' largest.  Only those threads'
-// vectors (top of 256) are read again, from L2, by the whole block, in the order of
-// their indexes, and what is not below the bound goes to a list.
+// Alternatives: the block's `top` largest logits are not below the top-th largest of the
+// threads' largest.  The threads have noted the largest logit of each of up to 32 runs of
+// their vectors; those of the few runs that reach that bound are read again, and what is
+// not below it goes to a list.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) dfa_scores_kernel(const ScoresParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    dfa_scores_kernel(const ScoresParams p) {
   using L = Logit<T>;
-  constexpr int kPer = L::kPer, kAhead = 4;
+  constexpr int kPer = L::kPer, kAhead = TOP ? 2 : 3;
   __shared__ Stats s_warp[kThreads / 32];
+  extern __shared__ uint4 smem[];
+  TopSpace& space = *reinterpret_cast<TopSpace*>(smem);  // with TOP
   grid_launch_dependents();
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / p.splits, piece = blockIdx.x - row * p.splits;
-  const Row<T> r(static_cast<const T*>(p.x) + row * p.stride, p.vocab);
-  const int per = (r.vectors + p.splits - 1) / p.splits;
-  const int lo = min(piece * per, r.vectors), hi = min(lo + per, r.vectors);
-
-  Stats a = {-INFINITY, 0.f, 0.f};
-  uint4 w[kAhead];
+  const int items = p.rows * p.splits;
+  // A thread's vectors of a piece: whole ones, `step` apart, batches of kAhead and the rest;
+  // the piece's first or last vector, where the row holds some of its values only, is one
+  // more, of the block's first or last thread.
+  struct Piece {
+    int row, lo, hi;   // vectors [lo, hi)
+    int at, end;       // the thread's first whole one, one past the piece's last
+    bool ragged;       // the thread has a vector that is not whole: v
+    int v;
+  };
+  auto row_of = [&](int row) {
+    return Row<T>(static_cast<const T*>(p.x) + row * p.stride, p.vocab);
+  };
+  auto enter = [&](int item) {
+    Piece c;
+    c.row = item / p.splits;
+    const Row<T> r = row_of(c.row);
+    const int per = (r.vectors + p.splits - 1) / p.splits;
+    c.lo = min((item - c.row * p.splits) * per, r.vectors), c.hi = min(c.lo + per, r.vectors);
+    const bool head = c.lo == 0 && (r.lead > 0 || r.vocab < kPer);
+    const bool tail = c.hi == r.vectors && (r.lead + r.vocab) % kPer != 0 && c.hi - c.lo > head;
+    c.at = c.lo + head + tid, c.end = c.hi - tail;
+    c.ragged = (head && tid == 0) || (tail && tid == kThreads - 1);
+    c.v = tid == 0 ? c.lo : c.hi - 1;
+    return c;
+  };
+  // The first batch of a piece (a batch is whole or not loaded).
+  auto load = [&](const uint4* x, int v, int end, uint4 (&w)[kAhead]) {
+    if (v + (kAhead - 1) * kThreads < end) {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) w[u] = r.load(lo + tid + u * kThreads, hi);
-  for (int v = lo + tid; v < hi; v += kAhead * kThreads) {
-    uint4 next[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) next[u] = r.load(v + (kAhead + u) * kThreads, hi);
-    float m = a.m;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float f[kPer];
-      L::unpack(w[u], f);
-#pragma unroll
-      for (int i = 0; i < kPer; i += 2) m = fmax3(m, f[i], f[i + 1]);
+      for (int u = 0; u < kAhead; ++u) w[u] = __ldg(x + v + u * kThreads);
     }
-    if (m > a.m) a = rebase(a, m);
-    const float ref = m == -INFINITY ? 0.f : m;
+  };
+  auto vectors_of = [&](const Row<T>& r) {
+    return reinterpret_cast<const uint4*>(r.x - r.lead);
+  };
+  uint4 w[kAhead];
+  Piece c = {};
+  if (static_cast<int>(blockIdx.x) < items) {
+    c = enter(blockIdx.x);
+    load(vectors_of(row_of(c.row)), c.at, c.end, w);
+  }
+#pragma unroll 1
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    Stats a = {-INFINITY, 0.f, 0.f};
+    float run = -INFINITY;  // the largest logit of the run of batches
+    // N vectors against the maximum so far.
+    auto take = [&](auto count, const uint4* x) {
+      constexpr int N = decltype(count)::value;
+      const float m = fmaxf(a.m, run = L::template most<N>(run, x));
+      if (m > a.m) a = rebase(a, m);
+      if (L::plain(m)) {
+        const float ref = -reference(m);
+        float s1 = 0.f, t1 = 0.f;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float f[kPer];
-      L::unpack(w[u], f);
+        for (int u = 0; u < N; ++u) {
+          float f[kPer];
+          L::unpack(L::finite(x[u]), f);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float d = not_far(f[i] - ref), e = ex2_approx(d * kLog2e);
-        a.s += e;
-        a.t = fmaf(e, d, a.t);
+          for (int i = 0; i < kPer; i += 2) {
+            float z0 = fmaf(f[i], kLog2e, ref), z1 = fmaf(f[i + 1], kLog2e, ref);
+            if constexpr (sizeof(T) == 4) z0 = not_far(z0), z1 = not_far(z1);
+            const float e0 = ex2_approx(z0), e1 = ex2_approx(z1);
+            a.s += e0, s1 += e1;
+            a.t = fmaf(e0, z0, a.t), t1 = fmaf(e1, z1, t1);
+          }
+        }
+        a.s += s1, a.t += t1;
+      } else {  // one by one, differences first unless there is nothing but -inf
+#pragma unroll 1
+        for (int u = 0; u < N; ++u) {
+          float f[kPer];
+          uint4 y = x[0];
+#pragma unroll
+          for (int i = 1; i < N; ++i)
+            if (u == i) y = x[i];
+          L::unpack(y, f);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const float z = extreme(m) ? not_far((f[i] - m) * kLog2e)
+                                       : not_far(fmaf(f[i], kLog2e, -reference(m)));
+            const float e = ex2_approx(z);
+            a.s += e;
+            a.t = fmaf(e, z, a.t);
+          }
+        }
+      }
+    };
+    const Row<T> r = row_of(c.row);
+    const uint4* x = vectors_of(r);
+    constexpr int kBatch = kAhead * kThreads;
+    const int batches = (c.end - (c.at - tid) + kBatch - 1) / kBatch;  // of whole vectors
+    const int per_slot = TOP ? (batches + kSlots - 1) / kSlots : 1;
+    int slot = 0, in_slot = 0;
+    auto note = [&](bool last) {  // a batch has been taken
+      if constexpr (TOP) {
+        if (++in_slot == per_slot || last) {
+          space.slot[slot][tid] = run;
+          ++slot, in_slot = 0;
+          run = -INFINITY;
+        }
+      }
+    };
+    int v = c.at;
+#pragma unroll 1
+    for (; v + kBatch - kThreads < c.end; v += 2 * kBatch) {
+      uint4 w2[kAhead];
+      load(x, v + kBatch, c.end, w2);
+      take(std::integral_constant<int, kAhead>{}, w);
+      note(false);
+      if (v + 2 * kBatch - kThreads >= c.end) {
+        v += kBatch;
+        break;
+      }
+      load(x, v + 2 * kBatch, c.end, w);
+      take(std::integral_constant<int, kAhead>{}, w2);
+      note(false);
+    }
+    {  // the rest: fewer than kAhead, and the one that is not whole
+      uint4 rest[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead - 1; ++u)
+        if (v + u * kThreads < c.end) rest[u] = __ldg(x + v + u * kThreads);
+      if (c.ragged) rest[kAhead - 1] = r.load(c.v, c.hi);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (u == kAhead - 1 && slot < kSlots) note(true);  // the rest is the last run's
+        if (u < kAhead - 1 ? v + u * kThreads < c.end : c.ragged)
+          take(std::integral_constant<int, 1>{}, rest + u);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) w[u] = next[u];
-  }
   const float mine = a.m;
+    const Piece c0 = c;  // the piece that is done
+    if (item + static_cast<int>(gridDim.x) < items) {
+      c = enter(item + gridDim.x);
+      load(vectors_of(row_of(c.row)), c.at, c.end, w);
+    }
   a = warp_join(a);
   if (lane == 0) s_warp[warp] = a;
 
   if constexpr (TOP) {
-    __shared__ TopSpace s;
-    s.top[tid] = mine;
+    TopSpace& s = space;
     if (tid == 0) s.count = s.hots = 0;
-    __syncthreads();
-    // The bound: the top-th largest of the threads' largest, one at a time.
-    if (warp == 0) {
-      uint32_t own[kThreads / 32];
+    // The bound: the top-th largest of the threads' largest.
+    uint32_t most = warp_sorted(ordered(mine));
+    s.top[tid] = most;
 #pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) own[i] = ordered(s.top[lane + 32 * i]);
-      uint32_t least = 0;
-      for (int n = 0; n < p.top; ++n) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) x = max(x, own[i]);
-        least = __reduce_max_sync(0xffffffffu, x);
-        const int first = __ffs(__ballot_sync(0xffffffffu, x == least)) - 1;
-        bool gone = lane != first;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i)
-          if (!gone && own[i] == least) own[i] = 0, gone = true;
+    for (int n = kThreads / 64; n > 0; n >>= 1) {  // warps below n take those n behind in
+      __syncthreads();
+      if (warp < n) {
+        most = warp_merged(most, s.top + 32 * (warp + n));
+        s.top[tid] = most;
       }
-      if (lane == 0) s.least = max(least, kOrderedNone + 1);
     }
+    if (tid == p.top - 1) s.least = max(most, kOrderedNone + 1);
     __syncthreads();
     if (ordered(mine) >= s.least) s.hot[atomicAdd(&s.hots, 1)] = tid;
     __syncthreads();
-    const int hots = s.hots, steps = (hi - lo + kThreads - 1) / kThreads;
+    const int first = c0.at - tid;  // whole vectors of the piece: [first, c0.end)
+    const int hots = s.hots, steps = (c0.end - first + kThreads - 1) / kThreads;
+    const float least = unordered(s.least);
     Key bound = static_cast<Key>(s.least) << 32;  // below every key of that logit
-    for (int q0 = 0; q0 < hots * steps; q0 += kThreads) {
-      const int q = q0 + tid, step = q / hots;
-      if (q < hots * steps) {
-        const int v = lo + step * kThreads + s.hot[q - step * hots];
-        float f[kPer];
-        L::unpack(r.load(v, hi), f);
+    auto offer = [&](const uint4& x, int v) {
+      float f[kPer];
+      L::unpack(x, f);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+      for (int i = 0; i < kPer; ++i)
+        if (f[i] >= least) {
           const Key key = make_key(f[i], v * kPer - r.lead + i);
-          if (key >= bound) s.list[atomicAdd(&s.count, 1)] = key;
+          if (key >= bound) {
+            const int at = atomicAdd(&s.count, 1);
+            if (at < kList) s.list[at] = key;
+          }
+        }
+    };
+    auto vector_of = [&](int q) {  // of the hot threads' whole vectors, in order
+      const int step = q / hots;
+      return first + step * kThreads + s.hot[q - step * hots];
+    };
+    const bool offers = c0.ragged && ordered(mine) >= s.least;
+    if (offers) offer(r.load(c0.v, c0.hi), c0.v);
+    // Of the hot threads the runs that reach the bound; then, where the list was too short,
+    // all of their vectors in rounds.
+    if (ordered(mine) >= s.least) {
+      unsigned reach = 0;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (i < slot && space.slot[i][tid] >= least) reach |= 1u << i;
+      for (; reach != 0; reach &= reach - 1) {
+        const int i = __ffs(reach) - 1;
+        for (int j = 0; j < per_slot; ++j) {
+          const int v = first + tid + (i * per_slot + j) * kBatch;
+          uint4 y[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (v + u * kThreads < c0.end) y[u] = __ldg(x + v + u * kThreads);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (v + u * kThreads < c0.end) offer(y[u], v + u * kThreads);
         }
       }
+    }
+    __syncthreads();
+    const bool again = s.count > kList;
+    __syncthreads();  // the count has been read
+    if (again) {
+      if (tid == 0) s.count = 0;
       __syncthreads();
-      const bool full = s.count > kListKeep;
-      __syncthreads();  // the count has been read
-      if (full) {
-        best_of_list(s, p.top);
+      if (offers) offer(r.load(c0.v, c0.hi), c0.v);
+#pragma unroll 1
+      for (int q0 = 0; q0 < hots * steps; q0 += kListThreads) {
+        const int v = tid < kListThreads && q0 + tid < hots * steps ? vector_of(q0 + tid) : c0.end;
+        if (v < c0.end) offer(__ldg(x + v), v);
         __syncthreads();
-        bound = s.best[p.top - 1];  // the list holds more than `top` keys
-        if (tid < p.top) s.list[tid] = s.best[tid];
-        if (tid == 0) s.count = p.top;
-        __syncthreads();
+        const bool full = s.count > kListKeep;
+        __syncthreads();  // the count has been read
+        if (full) {
+          best_of_list(s, p.top);
+          __syncthreads();
+          bound = s.best[p.top - 1];  // the list holds more than `top` keys
+          if (tid < p.top) s.list[tid] = s.best[tid];
+          if (tid == 0) s.count = p.top;
+          __syncthreads();
+        }
       }
     }
     best_of_list(s, p.top);
     __syncthreads();
     if (p.splits > 1) {
       if (tid < p.top)
-        p.part_top[static_cast<long long>(blockIdx.x) * p.top + tid] = s.best[tid];
+        p.part_top[static_cast<long long>(item) * p.top + tid] = s.best[tid];
     } else if (warp == 0) {
       Stats b = lane < kThreads / 32 ? s_warp[lane] : Stats{-INFINITY, 0.f, 0.f};
       const Finished f = finish(warp_join(b));
-      if (lane < p.top) write_top(p, row, lane, s.best[lane], f);
+      if (lane < p.top) write_top(p, c0.row, lane, s.best[lane], f);
     }
   } else {
     __syncthreads();
@@ -397,9 +653,11 @@ __global__ void __launch_bounds__(kThreads) dfa_scores_kernel(const ScoresParams
     Stats b = lane < kThreads / 32 ? s_warp[lane] : Stats{-INFINITY, 0.f, 0.f};
     b = warp_join(b);
     if (lane == 0) {
-      if (p.splits > 1) p.part[blockIdx.x] = b;
-      else write_row<T>(p, row, b, finish(b));
+      if (p.splits > 1) p.part[item] = b;
+      else write_row(p, c0.row, finish(b), load_token<T>(p, c0.row));
     }
+  }
+  __syncthreads();  // the statistics and the list have been read
   }
 }
 
@@ -413,6 +671,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) dfa_scores_join_kernel(const S
   const int lane = threadIdx.x & 31, row = blockIdx.x * kJoinRows + (threadIdx.x >> 5);
   if (row >= p.rows) return;
   constexpr int kLists = kMaxSplits / 32;
+  Token token;
+  if (lane == 0) token = load_token<T>(p, row);
   const long long first = static_cast<long long>(row) * p.splits;
   Stats a = {-INFINITY, 0.f, 0.f};
 #pragma unroll
@@ -420,7 +680,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) dfa_scores_join_kernel(const S
     if (lane + 32 * i < p.splits) a = join(a, p.part[first + lane + 32 * i]);
   a = warp_join(a);
   const Finished f = finish(a);
-  if (lane == 0) write_row<T>(p, row, a, f);
+  if (lane == 0) write_row(p, row, f, token);
   if (p.top == 0) return;
   const Key* lists = p.part_top + first * p.top;
   Key head[kLists];
@@ -528,11 +788,9 @@ __global__ void __launch_bounds__(kThreads) dfa_scores_grad_kernel(const ScoresG
 
 // ------------------------------------------------------------------ host
 
-constexpr int kBlocksPerSm = 4;
-
 // Pieces of a row: enough that the blocks fill the device once, at least two
 // vectors a thread, and such that the last wave is not mostly empty.
-int splits_for(int rows, int vocab, int size, int sms) {
+int splits_for(int rows, int vocab, int size, int top, int sms) {
   const long long vectors = (static_cast<long long>(vocab) * size + 15) / 16;
   const long long most = vectors / (2 * kThreads);
   const long long slots = static_cast<long long>(sms) * kBlocksPerSm;
@@ -540,8 +798,9 @@ int splits_for(int rows, int vocab, int size, int sms) {
   double least = 0;
   for (int s = 1; s <= kMaxSplits && (s == 1 || s <= most); ++s) {
     const long long waves = (static_cast<long long>(rows) * s + slots - 1) / slots;
-    // a block's own cost is that of about two vectors a thread
-    const double cost = static_cast<double>(waves) * (static_cast<double>(vectors) / s + 2 * kThreads);
+    // a piece's end costs as much as about two vectors a thread, alternatives some more
+    const double cost =
+        static_cast<double>(waves) * (static_cast<double>(vectors) / s + (top ? 4 : 2) * kThreads);
     if (s == 1 || cost < 0.97 * least) best = s, least = cost;
   }
   return best;
@@ -573,10 +832,16 @@ long long scores_workspace(int rows, int top, int splits) {
 }
 
 template <typename T>
-cudaError_t launch_scores(const ScoresParams& p, cudaStream_t stream) {
+cudaError_t launch_scores(const ScoresParams& p, int sms, cudaStream_t stream) {
   auto kern = p.top > 0 ? dfa_scores_kernel<T, true> : dfa_scores_kernel<T, false>;
-  const unsigned blocks = static_cast<unsigned>(p.rows) * static_cast<unsigned>(p.splits);
-  cudaError_t e = launch_chained(kern, dim3(blocks), dim3(kThreads), 0, stream, p);
+  const long long items = static_cast<long long>(p.rows) * p.splits;
+  const long long most = static_cast<long long>(sms) * kBlocksPerSm;
+  const unsigned blocks = static_cast<unsigned>(items < most ? items : most);
+  const size_t smem = p.top > 0 ? sizeof(TopSpace) : 0;
+  cudaError_t e = smem ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(smem))
+                       : cudaSuccess;
+  if (e == cudaSuccess) e = launch_chained(kern, dim3(blocks), dim3(kThreads), smem, stream, p);
   if (e == cudaSuccess && p.splits > 1)
     e = launch_chained(dfa_scores_join_kernel<T>,
                        dim3((static_cast<unsigned>(p.rows) + kJoinRows - 1) / kJoinRows),
@@ -598,7 +863,7 @@ long long dfa_token_logprobs_workspace_bytes(int rows, int vocab, int top, int d
   if (rows == 0) return 0;
   DeviceInfo di;
   if (const int rc = device_info(&di)) return rc;
-  return scores_workspace(rows, top, splits_for(rows, vocab, type_size(dtype), di.sms));
+  return scores_workspace(rows, top, splits_for(rows, vocab, type_size(dtype), top, di.sms));
 }
 
 int dfa_token_logprobs(const void* logits, const void* tokens, int token_bytes, float* logprobs,
@@ -619,7 +884,7 @@ int dfa_token_logprobs(const void* logits, const void* tokens, int token_bytes, 
     return DFA_EINVAL;
   DeviceInfo di;
   if (const int rc = device_info(&di)) return rc;
-  const int splits = splits_for(rows, vocab, type_size(dtype), di.sms);
+  const int splits = splits_for(rows, vocab, type_size(dtype), top, di.sms);
   const long long need = scores_workspace(rows, top, splits);
   if (need && (!workspace || workspace_bytes < need)) return DFA_EINVAL;
   ScoresParams p{};
@@ -640,9 +905,9 @@ int dfa_token_logprobs(const void* logits, const void* tokens, int token_bytes, 
   p.splits = splits;
   p.wide_tokens = token_bytes == 8;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == DFA_BF16  ? launch_scores<__nv_bfloat16>(p, s)
-                        : dtype == DFA_F16 ? launch_scores<__half>(p, s)
-                                           : launch_scores<float>(p, s);
+  const cudaError_t e = dtype == DFA_BF16  ? launch_scores<__nv_bfloat16>(p, di.sms, s)
+                        : dtype == DFA_F16 ? launch_scores<__half>(p, di.sms, s)
+                                           : launch_scores<float>(p, di.sms, s);
   return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);
 }
 
@@ -672,7 +937,7 @@ int dfa_token_logprobs_backward(const void* logits, const void* tokens, int toke
   p.dx = dlogits;
   p.rows = rows;
   p.vocab = vocab;
-  p.splits = splits_for(rows, vocab, type_size(dtype), di.sms);
+  p.splits = splits_for(rows, vocab, type_size(dtype), 0, di.sms);
   p.wide_tokens = token_bytes == 8;
   const unsigned blocks = static_cast<unsigned>(rows) * static_cast<unsigned>(p.splits);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -118,12 +118,12 @@ def test_scores(b, dtype, rows, V, pad, lead, top):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("kind", ["equal", "up", "down", "few values", "one", "far", "large",
-                                  "tail", "stripe"])
+                                  "tail", "stripe", "lowest", "lowest mask", "highest"])
 @pytest.mark.parametrize("V", [300, 40000])
 def test_scores_of_unusual_rows(b, dtype, kind, V):
     """All alike, in order either way, many ties, one possible token, logits far apart or
     large against their spread, the largest ones all at the end or all in one thread's
-    share."""
+    share; rows of the type's lowest value, masks of it, its highest value."""
     at = torch.arange(V, dtype=torch.float64)
     if kind == "equal":
         x = torch.full((V,), 0.5)
@@ -138,6 +138,13 @@ def test_scores_of_unusual_rows(b, dtype, kind, V):
         x = torch.where(at % 100 == 7, 3e4, -3e4)
     elif kind == "large":
         x = 2e4 + 64 * (at % 17)
+    elif kind == "lowest":
+        x = torch.full((V,), torch.finfo(dtype).min)
+        x[::3] = -math.inf
+    elif kind == "lowest mask":
+        x = torch.where(at % 5 == 0, at % 7, torch.finfo(dtype).min)
+    elif kind == "highest":
+        x = torch.where(at % 90 == 4, torch.finfo(dtype).max, at % 7)
     elif kind == "tail":
         x = torch.where(at >= V - 40, 5 + at / V, 0.0)
     else:
