@@ -33,29 +33,47 @@ struct Append4Params {
   int rows, max_new, Hk, page_size, num_pages, max_pages, touch;
 };
 
-// The keys (cache4_scale_byte) of the two bf16 values of a word: each turned left by
-// one bit.
-__device__ __forceinline__ uint32_t keys2(uint32_t w) {
-  return ((w << 1) & 0xfffefffeu) | ((w >> 15) & 0x00010001u);
+// The key (cache4_scale_byte) of a group of 32 values of which this thread and its three
+// neighbours hold eight each: the largest value and the largest negated one, two to an
+// operation, NaN where there is one.
+__device__ __forceinline__ unsigned group_key(const uint4& w) {
+  auto as2 = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+  auto bits = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  const uint32_t hi = bits(__hmax2_nan(__hmax2_nan(as2(w.x), as2(w.y)),
+                                       __hmax2_nan(as2(w.z), as2(w.w))));
+  const uint32_t lo = bits(__hmin2_nan(__hmin2_nan(as2(w.x), as2(w.y)),
+                                       __hmin2_nan(as2(w.z), as2(w.w)))) ^
+                      0x80008000u;
+  // the largest value in the low half, the largest negated one in the high half
+  uint32_t top = bits(__hmax2_nan(as2(__byte_perm(hi, lo, 0x5410)), as2(__byte_perm(hi, lo, 0x7632))));
+  top = bits(__hmax2_nan(as2(top), as2(__shfl_xor_sync(0xffffffffu, top, 1))));
+  top = bits(__hmax2_nan(as2(top), as2(__shfl_xor_sync(0xffffffffu, top, 2))));
+  // Of the two the larger is the group's largest magnitude (both are negative zeros at
+  // least): as signed integers, of which a NaN's is the largest.
+  const int pos = static_cast<short>(top & 0xffffu), neg = static_cast<short>(top >> 16);
+  return 2u * static_cast<unsigned>(max(max(pos, neg), 0)) + (neg >= pos ? 1u : 0u);
 }
 
 // Codes of eight values whose group has the scale s, packed.
 //
-// x / s to the nearest, ties away from 0, without a division: x times r, the
-// reciprocal of s made larger by 2^-20.  x / s is half of an odd number exactly or
-// off by at least 2^-8 of itself (x has 8 significant bits, s has 3, |x / s| <= 8.5
-// below), so the excess moves ties away from 0 and nothing else over a border.  The
-// product is exact in the fma that adds 1.5 * 2^23 + 8, which leaves the code in the
-// lowest bits of its sum.
+// x / s to the nearest, ties away from 0, without a division: x times r, the reciprocal of s
+// made larger by 2^-14.  x / s is half of an odd number exactly or off by at least 2^-8 of
+// itself (x has 8 significant bits, s has 3, |x / s| <= 8.5 below), so the excess moves ties
+// away from 0, by 2^-15 at least, and nothing else over a border; what the roundings below
+// may be off by is less than 2^-18 of a code.  The first product, with 8 more, is kept within
+// 0 and 15.4375 by taking it as a fraction of that, within 0 and 1; the second is rounded by
+// 1.5 * 2^23, which leaves the code in the sum's lowest bits.
+constexpr float kMost = 15.4375f;  // rounds to 15
 __device__ __forceinline__ uint32_t encode8(const uint4& w, float r) {
-  constexpr float kBase = 12582912.f;  // 1.5 * 2^23, whose bits are 0x4b400000
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t out = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
-    const float y = fminf(fmaxf(fmaf(x, r, kBase + 8.f), kBase), kBase + 15.f);
-    out += (__float_as_uint(y) - 0x4b400000u) << (16 * (i & 1) + 4 * (i >> 1));
+  for (int i = 7; i >= 0; --i) {
+    const int at = i < 4 ? 2 * i : 2 * i - 7;  // dims 0, 2, 4, 6, 1, 3, 5, 7 from the lowest bits
+    const float x =
+        __uint_as_float(at & 1 ? u[at >> 1] & 0xffff0000u : u[at >> 1] << 16);
+    const float y = __saturatef(fmaf(x, r, 8.f / kMost));
+    out = (out << 4) + (__float_as_uint(fmaf(y, kMost, 12582912.f)) - 0x4b400000u);
   }
   return out;
 }
@@ -67,6 +85,9 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float r) {
 template <int D, int NT, int VPT>
 __global__ void __launch_bounds__(NT) dfa_cache4_append_kernel(const Append4Params p) {
   constexpr int kVec = D / 8;  // vectors per token and head
+  constexpr int kTokens = NT * VPT / kVec < 128 ? NT * VPT / kVec : 128;
+  constexpr int kGroups = D / kCache4Group;
+  __shared__ uint8_t s_scale[kGroups][kTokens + 4];  // of tokens from a multiple of four on
   grid_launch_dependents();
   grid_dependency_wait();
   // heads fastest: neighbouring blocks read neighbouring pieces of the rows
@@ -108,17 +129,29 @@ __global__ void __launch_bounds__(NT) dfa_cache4_append_kernel(const Append4Para
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int i = u * NT + tid;
-    uint32_t top = __vmaxu2(__vmaxu2(keys2(w[u].x), keys2(w[u].y)),
-                            __vmaxu2(keys2(w[u].z), keys2(w[u].w)));
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int byte = cache4_scale_byte(max(top & 0xffffu, top >> 16));
-    const float r = __frcp_rn(cache4_scale(byte)) * (1.f + 0x1p-20f);
+    const int byte = cache4_scale_byte(group_key(w[u]));
+    const float r = __frcp_rn(cache4_scale(byte)) * ((1.f + 0x1p-14f) / kMost);
     if (i < nvec) {
       codes[i] = encode8(w[u], r);
       const int token = i / kVec, vec = i % kVec;
-      if ((vec & 3) == 0)
-        scale[(vec >> 2) * p.page_size + first + token] = static_cast<uint8_t>(byte);
+      if ((vec & 3) == 0) s_scale[vec >> 2][(first & 3) + token] = static_cast<uint8_t>(byte);
+    }
+  }
+  // The scales, tokens of a group next to one another: four at a time where all are new.
+  if constexpr (NT > 32) __syncthreads();
+  else __syncwarp();
+  const int from = first & ~3, words = (nvec / kVec + (first & 3) + 3) >> 2;
+  const int end = first + nvec / kVec;
+  for (int i = tid; i < kGroups * words; i += NT) {
+    const int grp = i / words, word = i - grp * words, token = from + 4 * word;
+    uint8_t* dst = scale + grp * p.page_size + token;
+    const uint8_t* src = &s_scale[grp][4 * word];
+    if (token >= first && token + 4 <= end) {
+      *reinterpret_cast<uchar4*>(dst) = make_uchar4(src[0], src[1], src[2], src[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (token + e >= first && token + e < end) dst[e] = src[e];
     }
   }
 }
@@ -156,7 +189,9 @@ struct ReadParams {
   const int* first;  // or null
   const int* cu_rows;
   unsigned* status;
-  int batch, rows, Hk, page_size, num_pages, max_pages, vec_shift;  // headdim 8 << vec_shift
+  int batch, rows, Hk, page_size, page_shift, num_pages, max_pages;
+  int vec_shift;  // headdim 8 << vec_shift
+  int per_block;  // rows
 };
 
 // The last request b with cu[b] <= row, among [0, batch), by 32 looks at a time; all
@@ -176,76 +211,108 @@ __device__ __forceinline__ int find_request(const int* cu, int batch, int row) {
   return lo - 1;
 }
 
-constexpr int kReadWarps = 8;
+constexpr int kReadWarps = 8, kReadRows = 32;  // a row for each lane of a warp
 
-// A warp takes a row: it finds the row's request and page, then moves the row's heads,
-// keys and values, 16 bytes of output a lane at a time.
+// A block takes up to 32 rows.  The lanes of its first warp find a row's request, page and
+// place each, so that the chain of their loads is paid once; then every warp moves rows,
+// their heads' keys and values, 16 bytes of output a lane and access, several on their way.
 template <int BITS>
 __global__ void __launch_bounds__(32 * kReadWarps) dfa_cache_read_kernel(const ReadParams p) {
+  __shared__ int s_page[kReadRows], s_at[kReadRows];  // page -1: zeros; place -1: leave alone
   grid_launch_dependents();
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kReadWarps + (threadIdx.x >> 5);
-  if (row >= p.rows || p.batch == 0) return;
-  const int b = find_request(p.cu_rows, p.batch, row);
-  const int r0 = b >= 0 ? p.cu_rows[b] : -1, r1 = b >= 0 ? p.cu_rows[b + 1] : 0;
-  if (r0 < 0 || row < r0 || row >= r1) {
-    // behind the last request's rows, or rows out of order
-    if (lane == 0 && row < p.cu_rows[p.batch]) atomicOr(p.status, kStatusIndex);
-    return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row0 = blockIdx.x * p.per_block, rows = min(p.per_block, p.rows - row0);
+  if (warp == 0) {
+    int b = find_request(p.cu_rows, p.batch, row0);
+    const int row = row0 + lane;
+    int page = -1, place = -1;
+    if (lane < rows) {
+      while (b + 1 < p.batch && p.cu_rows[b + 1] <= row) ++b;
+      const int r0 = b >= 0 ? p.cu_rows[b] : -1, r1 = b >= 0 ? p.cu_rows[b + 1] : 0;
+      if (r0 < 0 || row < r0 || row >= r1) {
+        // behind the last request's rows, or rows out of order
+        if (row < p.cu_rows[p.batch]) atomicOr(p.status, kStatusIndex);
+      } else {
+        const int len = p.cache_lens[b];
+        const long long pos = static_cast<long long>(p.first ? p.first[b] : 0) + (row - r0);
+        if (len >= 0 && len <= p.max_pages << p.page_shift && pos >= 0 && pos < len)
+          page = p.block_table[static_cast<long long>(b) * p.max_pages + (pos >> p.page_shift)];
+        place = static_cast<int>(pos) & (p.page_size - 1);
+        if (!cache_page_ok(page, p.num_pages)) {
+          page = -1;
+          atomicOr(p.status, kStatusIndex);
+        }
+      }
+    }
+    s_page[lane] = page;
+    s_at[lane] = place;
   }
-  const int len = p.cache_lens[b];
-  const long long pos = static_cast<long long>(p.first ? p.first[b] : 0) + (row - r0);
-  int page = -1;
-  if (len >= 0 && len <= p.max_pages * p.page_size && pos >= 0 && pos < len)
-    page = p.block_table[static_cast<long long>(b) * p.max_pages + pos / p.page_size];
-  const bool ok = cache_page_ok(page, p.num_pages);
-  if (!ok && lane == 0) atomicOr(p.status, kStatusIndex);
-  const int at = static_cast<int>(pos) & (p.page_size - 1);
+  __syncthreads();
   const int per = p.Hk << p.vec_shift;  // vectors of a row
-  const long long heads = static_cast<long long>(page) * p.Hk;
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    uint4* dst = reinterpret_cast<uint4*>(p.y[which]) + static_cast<long long>(row) * per;
-    const uint8_t* cache = p.cache[which];
-#pragma unroll 4
-    for (int i = lane; i < per; i += 32) {
-      uint4 out = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) {
+  for (int r = warp; r < 2 * rows; r += kReadWarps) {
+    const int which = r >= rows, row = r - which * rows, page = s_page[row], at = s_at[row];
+    if (at < 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(which ? p.y[1] : p.y[0]) +
+                 static_cast<long long>(row0 + row) * per;
+    if (page < 0) {
+      for (int i = lane; i < per; i += 32) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const uint8_t* cache = which ? p.cache[1] : p.cache[0];
+    const void* scales = which ? p.scale[1] : p.scale[0];
+    const long long heads = static_cast<long long>(page) * p.Hk;
+    constexpr int kAtOnce = 8;
+#pragma unroll 1
+    for (int i0 = lane; i0 < per; i0 += 32 * kAtOnce) {
+      uint2 w[kAtOnce];
+      float s[kAtOnce];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int i = i0 + 32 * e;
+        if (i >= per) break;
         const int h = i >> p.vec_shift, vec = i & ((1 << p.vec_shift) - 1);
-        const long long token = (heads + h) * p.page_size + at;
+        const long long token = ((heads + h) << p.page_shift) + at;
+        const uint8_t* src = cache + ((token << p.vec_shift) + vec) * BITS;
         if constexpr (BITS == 4) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(
-              cache + ((token << p.vec_shift) + vec) * 4);
-          const uint8_t* scale = static_cast<const uint8_t*>(p.scale[which]);
+          w[e].x = __ldg(reinterpret_cast<const uint32_t*>(src));
           const long long group = ((heads + h) << p.vec_shift >> 2) + (vec >> 2);
-          const float s = cache4_scale(scale[group * p.page_size + at]);
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            f[e] = static_cast<float>(
-                       static_cast<int>((w >> (16 * (e & 1) + 4 * (e >> 1))) & 15u) - 8) * s;
-          out = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+          s[e] = __uint_as_float(
+              __ldg(static_cast<const uint8_t*>(scales) + (group << p.page_shift) + at));
         } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(
-              cache + ((token << p.vec_shift) + vec) * 8);
-          const float s = static_cast<const float*>(p.scale[which])[heads + h];
-          const uint32_t u[2] = {w.x, w.y};
-          uint32_t o[4];
+          w[e] = __ldg(reinterpret_cast<const uint2*>(src));
+          s[e] = __ldg(static_cast<const float*>(scales) + heads + h);
+        }
+      }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kAtOnce; ++e) {
+        const int i = i0 + 32 * e;
+        if (i >= per) break;
+        uint32_t o[4];
+        if constexpr (BITS == 4) {
+          uint32_t f[4];
+          const uint32_t byte = __float_as_uint(s[e]);
+          cache4_decode(w[e].x, cache4_prepare(byte << 8 | byte << 24), f);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[x]));
+            o[x] = pack_bf16x2(y.x * kCache4Unit, y.y * kCache4Unit);
+          }
+        } else {
+          const uint32_t u[2] = {w[e].x, w[e].y};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
             uint32_t f16;
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
                 : "=r"(f16)
-                : "h"(static_cast<uint16_t>(u[e >> 1] >> (16 * (e & 1)))));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16));
-            o[e] = pack_bf16x2(f.x * s, f.y * s);
+                : "h"(static_cast<uint16_t>(u[x >> 1] >> (16 * (x & 1)))));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f16));
+            o[x] = pack_bf16x2(y.x * s[e], y.y * s[e]);
           }
-          out = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      dst[i] = out;
     }
   }
 }
@@ -290,9 +357,12 @@ int cache_read(int bits, const void* k_cache, const void* v_cache, const void* k
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.vec_shift = headdim == 64 ? 3 : headdim == 128 ? 4 : 5;
+  p.page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+  // A few rows are spread over the device.
+  p.per_block = rows <= 4 * kReadWarps * di.sms ? kReadWarps / 2 : kReadRows;
   const cudaError_t e = launch_chained(
       bits == 4 ? dfa_cache_read_kernel<4> : dfa_cache_read_kernel<8>,
-      dim3((static_cast<unsigned>(rows) + kReadWarps - 1) / kReadWarps), dim3(32 * kReadWarps), 0,
+      dim3((static_cast<unsigned>(rows) + p.per_block - 1) / p.per_block), dim3(32 * kReadWarps), 0,
       static_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? DFA_OK : record_cuda_failure(e);
 }
