@@ -32,11 +32,15 @@ def __getattr__(name):
     import importlib
 
     if name in ("rotary_table", "PageTable", "KVCache"):
-        return getattr(importlib.import_module(__name__ + ".sampling"), name)
-    if name in ("diffusion_attn_func", "diffusion_attn_varlen_func", "causal_attn_func",
-                "rotary_func", "token_logprobs_func", "DiffusionAttnFunc", "DiffusionAttnVarlenFunc", "CausalAttnFunc",
-                "RotaryFunc", "TokenLogprobsFunc"):
-        return getattr(importlib.import_module(__name__ + ".autograd"), name)
-    if name in ("binding", "autograd", "inputs", "build", "sampling"):
+        value = getattr(importlib.import_module(__name__ + ".sampling"), name)
+    elif name in ("diffusion_attn_func", "diffusion_attn_varlen_func", "causal_attn_func",
+                  "rotary_func", "token_logprobs_func", "DiffusionAttnFunc",
+                  "DiffusionAttnVarlenFunc", "CausalAttnFunc", "RotaryFunc",
+                  "TokenLogprobsFunc"):
+        value = getattr(importlib.import_module(__name__ + ".autograd"), name)
+    elif name in ("binding", "autograd", "inputs", "build", "sampling"):
         return importlib.import_module(__name__ + "." + name)
-    raise AttributeError(name)
+    else:
+        raise AttributeError(name)
+    globals()[name] = value  # not looked up again
+    return value

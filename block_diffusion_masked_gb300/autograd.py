@@ -120,14 +120,23 @@ class TokenLogprobsFunc(torch.autograd.Function):
         return logprobs, entropy, best, which
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dlogprobs, dentropy, *_):
+        if torch.is_grad_enabled():  # the gradient is to have one: it has not
+            return TokenLogprobsFunc._refuse_second(ctx, dlogprobs, dentropy)
         logits, tokens, stats, entropy = ctx.saved_tensors
         if dlogprobs is None and dentropy is None:
             return None, None, None
-        return binding.dfa_token_logprobs_backward(
-            logits, tokens, stats, entropy, None if dlogprobs is None else dlogprobs.contiguous(),
-            None if dentropy is None else dentropy.contiguous()), None, None
+        if dlogprobs is not None and not dlogprobs.is_contiguous():
+            dlogprobs = dlogprobs.contiguous()
+        if dentropy is not None and not dentropy.is_contiguous():
+            dentropy = dentropy.contiguous()
+        return binding.dfa_token_logprobs_backward(logits, tokens, stats, entropy, dlogprobs,
+                                                   dentropy), None, None
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def _refuse_second(ctx, dlogprobs, dentropy):
+        return TokenLogprobsFunc.backward(ctx, dlogprobs, dentropy)
 
 
 def token_logprobs_func(logits, tokens=None, top=0):
@@ -152,7 +161,8 @@ def token_logprobs_func(logits, tokens=None, top=0):
     if tokens is not None:
         if not isinstance(tokens, torch.Tensor) or tokens.shape != shape:
             raise ValueError("tokens must have the logits' leading dimensions")
-        tokens = tokens.reshape(-1).contiguous()
+        if tokens.dim() != 1 or not tokens.is_contiguous():
+            tokens = tokens.reshape(-1).contiguous()
     if logits.dim() != 2:
         logits = logits.reshape(-1, logits.shape[-1])
     if logits.shape[1] > 1 and logits.stride(1) != 1 or logits.stride(0) < 0:

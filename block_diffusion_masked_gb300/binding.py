@@ -1056,12 +1056,12 @@ def dfa_token_logprobs(logits, tokens=None, top=0, workspace=None):
     dev, top = logits.device, int(top)
     if not 0 <= top <= 32:
         raise ValueError("top must be 0 to 32")
-    # one allocation: stats, entropy, log probabilities, alternatives
-    n = 3 if tokens is None else 4
-    buf = torch.empty((n + 2 * top) * rows, dtype=torch.float32, device=dev)
-    at = buf.data_ptr()
-    parts = torch.unsafe_split_with_sizes(buf, (2 * rows, rows, (n - 3) * rows, top * rows,
-                                                top * rows))
+    f32 = torch.float32
+    stats = torch.empty((rows, 2), dtype=f32, device=dev)
+    entropy = torch.empty(rows, dtype=f32, device=dev)
+    logprobs = None if tokens is None else torch.empty(rows, dtype=f32, device=dev)
+    best = torch.empty((rows, top), dtype=f32, device=dev)
+    which = torch.empty((rows, top), dtype=torch.int32, device=dev)
     if workspace is None:
         nwork = _scores_bytes(dev.index, rows, V, top, logits.dtype)
         if nwork:
@@ -1071,11 +1071,10 @@ def dfa_token_logprobs(logits, tokens=None, top=0, workspace=None):
         _check_dense(workspace, (nwork,), torch.uint8, dev, "workspace")
     _call("dfa_token_logprobs", dev, logits.data_ptr(),
           None if tokens is None else tokens.data_ptr(), token_bytes,
-          None if tokens is None else at + 12 * rows, at + 8 * rows, at,
-          at + 4 * n * rows, at + 4 * (n + top) * rows,
-          None if workspace is None else workspace.data_ptr(), nwork, rows, V, top, stride, dtype)
-    return (None if tokens is None else parts[2], parts[1], parts[0].view(rows, 2),
-            parts[3].view(rows, top), parts[4].view(torch.int32).view(rows, top))
+          None if tokens is None else logprobs.data_ptr(), entropy.data_ptr(), stats.data_ptr(),
+          best.data_ptr(), which.data_ptr(), None if workspace is None else workspace.data_ptr(),
+          nwork, rows, V, top, stride, dtype)
+    return logprobs, entropy, stats, best, which
 
 
 def dfa_token_logprobs_backward(logits, tokens, stats, entropy, dlogprobs=None, dentropy=None,
