@@ -80,6 +80,8 @@ struct WideCfg {
   // setmaxnreg split of the launch's 96 registers a thread:
   // 256 * 136 + 256 * 72 + 128 * 64 == 640 * 96
   static constexpr int kRegSoft = 136, kRegConv = 72, kRegRest = 64;
+  static_assert(256 * kRegSoft + 256 * kRegConv + 128 * kRegRest <= kThreads * 96,
+                "a split above the launch's registers waits forever");
   static constexpr int kRaw = BN * D * BITS / 8;  // a raw tile of k or of v, RS of each
   // 4 bits: its scales, 128 bytes for every 16 keys; a page's begin where its first keys'
   // do, the page's keys of one group of dims after another
