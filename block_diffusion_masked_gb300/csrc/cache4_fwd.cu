@@ -1,6 +1,6 @@
 // Attention of new rows over a paged 4-bit key/value cache (cache4.cuh) and, optionally,
-// over the new rows' own keys and values in bf16, up to 32 rows to a key, and headdim
-// 256: one block of a block diffusion sampler against the clean tokens before it ("Fast
+// over the new rows' own keys and values in bf16, for few rows to a key, and headdim
+// 256 (many: cache_wide.cuh): one block of a block diffusion sampler against the clean tokens before it ("Fast
 // Diffusion Attention", "Block diffusion in one picture").
 //
 // Mathematics.  Row i of request b (position len_b + i) and query head h see the len_b
@@ -18,7 +18,7 @@
 // shift more; the queries make up for the powers of two.  The scores of a group of 32
 // dims are two products, begun at -8 times the sum of the group's queries (a product of
 // its own, once per piece) and added up in float32 times the keys' scales: 5 operations
-// for eight codes and one per group and score instead of the 11 that decoding takes.
+// for eight codes and one per group and score instead of the 9 that decoding takes.
 // q is bf16: a row is brought to f16 by a power of two of its own (its largest magnitude
 // lands in [2^14, 2^15)), which keeps every value down to 2^-27 of the row's largest
 // exact.
@@ -34,6 +34,15 @@
 // that run ahead over the pieces' ends, and with softmax statistics of its own: no warp
 // waits for another but at a piece's end, where they join through shared memory.  The
 // pieces of a cut segment are joined by a second launch.
+//
+// Measured (headdim 128, 8 heads for keys): 64 ragged requests of up to 16000 tokens, 4 rows
+// to a key, 689 MB: 185 us, 3.7 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
+// rows, 126 MB: 59 us against 18.5; one request of 500 tokens, 4 heads: 10.8 us, launches
+// and latency.  Bound by the decoding: a unit is some 790 instructions of a warp, and the
+// schedulers issue in 70% of the cycles while all warps have work (a copy of the kernel that
+// only loads moves 6.5 TB/s).  Ends of pieces cost a block some 10000 cycles (requests'
+// sizes, queries, own keys, join: one latency after another), which is what the shorter
+// requests pay for.
 #include <type_traits>
 
 #include "cache4.cuh"
@@ -825,25 +834,26 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
   }  // pieces
 }
 
-// Row tiles, stages and blocks per SM for a head dimension and a segment's rows.
+// Row tiles, warps, stages, blocks per SM and outputs kept, for a head dimension and a
+// segment's rows.
+//
+// Blocks per SM: what the registers of the fragments allow without spilling much (3 blocks
+// of 168 registers for 8 rows, 2 of 255 for 16).  More lose to spills, fewer to idle
+// schedulers (us, 32 ragged requests of up to 8192 tokens, 512 / headdim heads for keys):
+// headdim 128, 16 rows 42 with 2 and 52 with 3; headdim 64, 8 rows 38 with 4 and 41 with 3;
+// headdim 256 8 rows 39 with 2, 40 with 1, 16 rows 68 with 2, 75 with 1; headdim 128, 8 rows
+// 33 with 3 and with 2.  Stages: two keep enough in flight with 8 or 12 warps (headdim 128:
+// 185.5, 186.1 and 186.6 us for 64 requests of up to 16000 tokens with 2, 3 and 4), and
+// what they leave is L1 for what the registers spill.
 template <int D, int ROWS>
 struct Variant;
-#define V64_8 1, 4, 4, 4, 4
-#define V64_16 2, 4, 5, 3, 4
-#define V64_32 4, 4, 5, 2, 4
-#define V128_8 1, 4, 3, 3, 4
-#define V128_16 2, 4, 4, 2, 4
-#define V128_32 4, 4, 4, 2, 2
-#define V256_8 1, 4, 2, 2, 4
-#define V256_16 2, 4, 2, 2, 2
-template <> struct Variant<64, 8> { using T = Cache4Tile<64, V64_8>; };
-template <> struct Variant<64, 16> { using T = Cache4Tile<64, V64_16>; };
-template <> struct Variant<64, 32> { using T = Cache4Tile<64, V64_32>; };
-template <> struct Variant<128, 8> { using T = Cache4Tile<128, V128_8>; };
-template <> struct Variant<128, 16> { using T = Cache4Tile<128, V128_16>; };
-template <> struct Variant<128, 32> { using T = Cache4Tile<128, V128_32>; };
-template <> struct Variant<256, 8> { using T = Cache4Tile<256, V256_8>; };
-template <> struct Variant<256, 16> { using T = Cache4Tile<256, V256_16>; };
+template <> struct Variant<64, 8> { using T = Cache4Tile<64, 1, 4, 4, 4, 4>; };
+template <> struct Variant<64, 16> { using T = Cache4Tile<64, 2, 4, 5, 3, 4>; };
+template <> struct Variant<64, 32> { using T = Cache4Tile<64, 4, 4, 3, 2, 4>; };
+template <> struct Variant<128, 8> { using T = Cache4Tile<128, 1, 4, 2, 3, 4>; };
+template <> struct Variant<128, 16> { using T = Cache4Tile<128, 2, 4, 2, 2, 4>; };
+template <> struct Variant<256, 8> { using T = Cache4Tile<256, 1, 4, 2, 2, 4>; };
+template <> struct Variant<256, 16> { using T = Cache4Tile<256, 2, 4, 2, 2, 2>; };
 
 template <int D, int NT, int WK, int STAGES, int RESIDENT, int KEPT>
 cudaError_t launch_tile(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>, const Cache4FwdParams& p,
@@ -866,7 +876,6 @@ R for_variant(int d, int rows, R none, F f) {
   } else if (d == 128) {
     if (rows == 8) return f(Variant<128, 8>::T{});
     if (rows == 16) return f(Variant<128, 16>::T{});
-    if (rows == 32) return f(Variant<128, 32>::T{});
   } else if (d == 256) {
     if (rows == 8) return f(Variant<256, 8>::T{});
     if (rows == 16) return f(Variant<256, 16>::T{});

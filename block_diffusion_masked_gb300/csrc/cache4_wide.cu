@@ -1,4 +1,4 @@
-// Attention over the paged 4-bit cache for more than 32 rows to a key, headdim 64 and
+// Attention over the paged 4-bit cache for many rows to a key, headdim 64 (more than 32) and
 // 128: the kernel of cache_wide.cuh for 4 bits.
 #include "cache_wide.cuh"
 

@@ -287,8 +287,8 @@ constexpr float kOwnUnit = 1 << kOwnExp;
 // rows; the tensor maps' boxes are whole pages).
 cudaError_t launch_cache_wide(const CacheFwdParams& p, int headdim, cudaStream_t stream);
 cudaError_t launch_cache_wide(const Cache4FwdParams& p, int headdim, cudaStream_t stream);
-// Over the 4-bit cache, up to 32 rows, and headdim 256, in tiles of 8, 16 or 32
-// (headdim 256: 8 or 16).
+// Over the 4-bit cache: headdim 64 up to 32 rows in tiles of 8, 16 or 32, headdim 128 up to
+// 16 rows and headdim 256 in tiles of 8 or 16.
 cudaError_t launch_cache4_rows(const Cache4FwdParams& p, int headdim, int tile_rows,
                                cudaStream_t stream);
 int cache4_blocks_per_sm(int headdim, int tile_rows);
