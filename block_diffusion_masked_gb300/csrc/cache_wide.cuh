@@ -636,6 +636,9 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
           if constexpr (kKind == kOwn) {
             f[0] = f[1] = p.scale_log2;
             wt[0] = wt[1] = inv_c;
+          } else if constexpr (BITS == 4) {  // the values' unit is O's until own keys come
+            f[0] = f[1] = factor;
+            wt[0] = wt[1] = 1.f;
           } else {
             const float2 ks = *reinterpret_cast<const float2*>(info.ks + 4 * half + 2 * x);
             const float2 vs = *reinterpret_cast<const float2*>(info.vs + 4 * half + 2 * x);
@@ -664,7 +667,8 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
             }
           }
         };
-        const float c_new = fmaxf(c, kKind == kOwn ? kOwnUnit : info.vmax);
+        const float c_new =
+            fmaxf(c, kKind == kOwn ? kOwnUnit : BITS == 4 ? kCache4Unit : info.vmax);
         float shrink = 1.f;
         if (c_new != c) {
           shrink = c / c_new;
@@ -720,7 +724,7 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
                           x0, x1);
                 const uint64_t pr = f2_pack(ex2_approx(x0), ex2_approx(x1));
                 acc[e & 1] = f2_add(acc[e & 1], pr);
-                f2_unpack(f2_mul(pr, w2), x0, x1);
+                f2_unpack(BITS == 4 && kKind != kOwn ? pr : f2_mul(pr, w2), x0, x1);
                 pk[8 * i + e] = kKind == kOwn ? pack_bf16x2(x0, x1) : pack_f16x2(x0, x1);
               }
             }
@@ -767,6 +771,7 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
           if (j == 0) {
             const int e = s_exp[(q++ & (C::kExps - 1)) * C::BM + lb + (lane & 15)];
             factor = pow2_bits(e) * p.scale_log2;
+            if constexpr (BITS == 4) factor = fmaxf(factor * kCache4Unit, 1.1754944e-38f);
           }
           if (info.whole) ok = tile(std::integral_constant<int, kWhole>{}, j, info);
           else ok = tile(std::integral_constant<int, kPart>{}, j, info);
