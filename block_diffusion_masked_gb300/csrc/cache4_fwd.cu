@@ -36,7 +36,7 @@
 // pieces of a cut segment are joined by a second launch.
 //
 // Measured (headdim 128, 8 heads for keys): 64 ragged requests of up to 16000 tokens, 4 rows
-// to a key, 689 MB: 185 us, 3.7 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
+// to a key, 689 MB: 181 us, 3.8 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
 // rows, 126 MB: 59 us against 18.5; one request of 500 tokens, 4 heads: 10.8 us, launches
 // and latency.  Bound by the decoding: a unit is some 790 instructions of a warp, and the
 // schedulers issue in 70% of the cycles while all warps have work (a copy of the kernel that
@@ -391,17 +391,17 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
     float unit = kCache4Unit;
 
     // Probabilities of raw scores sc (KT tiles of 16 keys; -inf: not seen) times the rows'
-    // factors f, over the output's unit if `scaled`, in the products' other operand's order.
-    // They are taken against the
-    // reference as it stands; only where their sum says that one may have outgrown f16, or
-    // with `look`, is the maximum found and the unit done again.
-    auto soften = [&](auto kt, auto f16, auto scaled, auto& sc, const float (&f)[NT][2], bool look,
-                      auto& pf) {
+    // factors f, over the output's unit, in the products' other operand's order.  They are
+    // taken against the reference as it stands; only where their sum says that one may have
+    // outgrown f16, or with `look`, is the maximum found and the unit done again.
+    // (The weight is 1 but behind own keys.  A copy of the code without it costs more in
+    // instructions to be fetched than the products do: 184 us against 181 for 64 requests.)
+    auto soften = [&](auto kt, auto f16, auto& sc, const float (&f)[NT][2], bool look, auto& pf) {
       constexpr int KT = decltype(kt)::value;
       float shrink[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) shrink[nt][0] = shrink[nt][1] = 1.f;
-      const float weight = decltype(scaled)::value ? (decltype(f16)::value ? kCache4Unit : 1.f) / unit : 1.f;
+      const float weight = (decltype(f16)::value ? kCache4Unit : 1.f) / unit;
 #pragma unroll 1
       for (;;) {
         if (look) {
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
               float e1 = ex2_approx(fmaf(sc[nt][i][2 * y + 1], f[nt][1], ref[1]));
               sum[nt][0] += e0;
               sum[nt][1] += e1;
-              if (decltype(scaled)::value) e0 *= weight, e1 *= weight;
+              e0 *= weight, e1 *= weight;
               pf[nt][i][y] = transposed(decltype(f16)::value ? pack_f16x2(e0, e1)
                                                              : pack_bf16x2(e0, e1));
             }
@@ -524,8 +524,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
               if (k0 + 8 * y + g >= end[nt][x]) sc[nt][0][2 * y + x] = -INFINITY;
           }
         uint32_t pf[NT][1][2];
-        soften(std::integral_constant<int, 1>{}, std::false_type{}, std::true_type{}, sc, own_factor,
-               true, pf);
+        soften(std::integral_constant<int, 1>{}, std::false_type{}, sc, own_factor, true, pf);
         // A row's probability of an own key it does not see is 0, but 0 times a value that is
         // not finite is not: such values leave the product and are added to the rows that
         // see them.
@@ -683,11 +682,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
                 if (key_of_row<D>(g + 8 * (x >> 1)) >= nv[i]) sc[nt][i][x] = -INFINITY;
         }
         uint32_t pf[NT][2][2];
-        const std::integral_constant<int, 2> kt2;
-        if (unit == kCache4Unit)
-          soften(kt2, std::true_type{}, std::false_type{}, sc, factor, false, pf);
-        else
-          soften(kt2, std::true_type{}, std::true_type{}, sc, factor, false, pf);
+        soften(std::integral_constant<int, 2>{}, std::true_type{}, sc, factor, false, pf);
         // Values: keys 2t, 2t + 1 and 2t + 8, 2t + 9 of a tile's rows, the thread's run of
         // dims of each.  What lies behind the last key may be anything: its scale becomes
         // zero, and with it the value.

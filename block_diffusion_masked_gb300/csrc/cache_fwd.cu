@@ -1008,7 +1008,7 @@ CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, lon
 
 // The same for the 4-bit cache (cache4_fwd.cu, cache_wide.cuh).  Measured (us) as above,
 // 512 / headdim heads for keys:
-//   headdim 128, 32 rows: 71 in a tile of 128 (the tcgen05 kernel), 82 in one of 32 (whose
+//   headdim 128, 32 rows: 69 in a tile of 128 (the tcgen05 kernel), 82 in one of 32 (whose
 //     fragments spill), 42 for 16 rows in one of 16; headdim 64, 32 rows: 98 in one of 128,
 //     72 in one of 32, 36 rows 98 in one of 128 and 128 in two of 32.
 //                      finish 4     5     6     8    10    12
@@ -1018,7 +1018,7 @@ CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, lon
 //   headdim  64, 128 rows   112   106   105   105   107   106
 //   headdim 128,   8 rows    34    34    34    35
 //   headdim 128,  16 rows    45    42    42    43
-//   headdim 128, 128 rows    91    84    82    79    80    83
+//   headdim 128, 128 rows    91    84    82    79    80    83  (76 by now)
 //   headdim 256,   8 rows    38    39    39    41
 //   headdim 256,  16 rows    68    69    67    70
 // Not cut against cut: 64 requests of 500 keys and 4 heads, 8 rows 17.2 and 19.4, 16 rows

@@ -1,12 +1,13 @@
-// Attention over the paged 8-bit cache for many query rows per key (more than
-// 32: blocks of tokens times grouped heads), headdim 64 and 128, on the
-// tensor cores' tcgen05 path.  The mathematics is that of cache_fwd.cu.
+// Attention over the paged 8- or 4-bit cache for many query rows per key (more than
+// 32; 4 bits, headdim 128: more than 16: blocks of tokens times grouped heads),
+// headdim 64 and 128, on the tensor cores' tcgen05 path.  The mathematics is that of
+// cache_fwd.cu, for 4 bits that of cache4_fwd.cu with the keys decoded as the values are.
 //
 // One CTA per SM takes a run of units (cache.cuh) and walks its pieces: a piece
 // is part of the keys of one request, key/value head and 128 query rows, in
 // 128-key tiles, the own keys last.
-//   TMA        raw e4m3 tiles of k and v, a box per page, into a ring;
-//   convert    e4m3 -> f16 (exact) into the 128-byte-swizzled operand tiles
+//   TMA        raw tiles of k and v, a box per page, into a ring; 4 bits: and of scales;
+//   convert    e4m3 -> f16, or 4 bits times their scale (exact either way), into the 128-byte-swizzled operand tiles
 //              (own keys: bf16, copied from global memory), two of k and two
 //              of v;
 //   S = Q K^T  A = Q (f16 after the row's power of two, or bf16 for own keys;
@@ -25,7 +26,7 @@
 // others (setmaxnreg).
 //
 // Measured, 128 rows, headdim 128, 32 ragged requests of up to 8192 tokens
-// (342 MB, 81 GFLOP): 132 us, 2.6 TB/s, 610 TFLOP/s; 64 rows 124, headdim 64
+// (342 MB, 81 GFLOP): 127 us, 2.7 TB/s, 640 TFLOP/s; 64 rows 124, headdim 64
 // 197 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
 // takes them some 2400 cycles, of which its 128 x 128 exponentials need 512 of
 // the special function units'; what is left is latency (waits that find their
@@ -33,7 +34,10 @@
 // roles on each scheduler: code that only got longer (the second half's scores
 // loaded ahead, loops unrolled) made the kernel 30% slower, and rolled
 // converters made it 5% faster.  Ends of pieces take 10 us each, of which the
-// last tiles' chain is most, and the first products come after 11.
+// last tiles' chain is most, and the first products come after 11.  4 bits, the same
+// requests, 128 rows and 8 heads: 139 us against 43 for the products; a tile takes 2800
+// cycles, 1470 of them the softmax warps' own, and the converters 1800, which the rings'
+// two operand tiles hide.
 #pragma once
 
 #include <type_traits>
@@ -798,24 +802,25 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
       __nv_bfloat16* dst =
           p.out + ((w.rq.row0 + static_cast<long long>(tok)) * p.H + hq) * D + half * DH;
       float* part = p.part_o + at * D + half * DH;
-#pragma unroll
-      for (int x = 0; x < DH / 32; ++x) {
-        uint32_t o[32];
+      // (unrolled: 133 us instead of 127, for the code is fetched anew for each piece)
+#pragma unroll 1
+      for (int x = 0; x < DH / 16; ++x) {
+        uint32_t o[16];
         if (k.all > 0) {
-          tmem_ld_half<32, DH>(t_lane + C::kTmemO + 32 * x, o);
+          tmem_ld_half<16, DH>(t_lane + C::kTmemO + 16 * x, o);
           tmem_wait_ld();
-          tmem_pin<32>(o);
+          tmem_pin<16>(o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
         }
         if (odd) {  // own values that are not finite, for the rows that see them
 #pragma unroll 1
           for (int key = 0; key < end; ++key) {
             const __nv_bfloat16* v =
-                p.v + (w.rq.row0 + key) * p.v_sr + k.h * p.v_sh + half * DH + 32 * x;
+                p.v + (w.rq.row0 + key) * p.v_sr + k.h * p.v_sh + half * DH + 16 * x;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 16; ++e) {
               const float y = __bfloat162float(v[e]);
               if (!isfinite(y)) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
             }
@@ -823,21 +828,21 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
         }
         if (r < k.R) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
           if (single) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t v[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 v[y] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * y]),
                                    __uint_as_float(o[8 * e + 2 * y + 1]));
-              st_global_v4(dst + 32 * x + 8 * e, v[0], v[1], v[2], v[3]);
+              st_global_v4(dst + 16 * x + 8 * e, v[0], v[1], v[2], v[3]);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              st_global_v4(part + 32 * x + 4 * e, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+            for (int e = 0; e < 4; ++e)
+              st_global_v4(part + 16 * x + 4 * e, o[4 * e], o[4 * e + 1], o[4 * e + 2],
                            o[4 * e + 3]);
           }
         }
