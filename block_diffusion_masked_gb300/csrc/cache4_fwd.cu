@@ -1,7 +1,7 @@
 // Attention of new rows over a paged 4-bit key/value cache (cache4.cuh) and, optionally,
-// over the new rows' own keys and values in bf16, for few rows to a key, and headdim
-// 256 (many: cache_wide.cuh): one block of a block diffusion sampler against the clean tokens before it ("Fast
-// Diffusion Attention", "Block diffusion in one picture").
+// over the new rows' own keys and values in bf16, for few rows to a key and for headdim 256
+// (many: cache_wide.cuh): one block of a block diffusion sampler against the clean tokens
+// before it ("Fast Diffusion Attention", "Block diffusion in one picture").
 //
 // Mathematics.  Row i of request b (position len_b + i) and query head h see the len_b
 // cached tokens and the own rows of its block or earlier blocks:

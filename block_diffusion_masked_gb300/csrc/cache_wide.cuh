@@ -7,9 +7,9 @@
 // is part of the keys of one request, key/value head and 128 query rows, in
 // 128-key tiles, the own keys last.
 //   TMA        raw tiles of k and v, a box per page, into a ring; 4 bits: and of scales;
-//   convert    e4m3 -> f16, or 4 bits times their scale (exact either way), into the 128-byte-swizzled operand tiles
-//              (own keys: bf16, copied from global memory), two of k and two
-//              of v;
+//   convert    e4m3 -> f16, or 4 bits times their scale (exact either way), into
+//              the 128-byte-swizzled operand tiles (own keys: bf16, copied from
+//              global memory), two of k and two of v;
 //   S = Q K^T  A = Q (f16 after the row's power of two, or bf16 for own keys;
 //              put into shared memory by the warps that convert k, as soon as
 //              the products with the Q before are complete), B = the key tile,

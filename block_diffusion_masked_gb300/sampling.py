@@ -5,8 +5,9 @@ clean tokens of the blocks before it ("Fast Diffusion Attention", "Block
 diffusion in one picture": a block sees itself and the earlier clean blocks).
 ``PageTable`` holds the requests' pages and lengths, shared by all layers;
 ``KVCache`` holds one layer's keys and values in e4m3 with a power-of-two
-scale per page and head, or in 4 bits with a scale per token and 32 dims.  All state lives on the GPU and every step is a few
-launches of fixed shape, so a step can be captured into a CUDA graph.
+scale per page and head, or in 4 bits with a scale per token and 32 dims.  All
+state lives on the GPU and every step is a few launches of fixed shape, so a
+step can be captured into a CUDA graph.
 """
 
 from __future__ import annotations

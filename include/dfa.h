@@ -455,9 +455,8 @@ int dfa_cache_forward(const void *q, const void *k, const void *v, const void *k
  * neighbouring head dims of a token: dim 2i of them in bits 4i to 4i + 3, dim 2i + 1
  * in bits 16 + 4i to 19 + 4i.  k_scale, v_scale: (num_pages, kv_heads, headdim / 32,
  * page_size) e5m2, one scale s for every token, head and 32 neighbouring dims.  All
- * four are 16-byte aligned.  A
- * cached value is (n - 8) s.  Tables, lengths, rows, plan and release: as above;
- * what the host cannot see is checked and flagged as above.
+ * four are 16-byte aligned.  A cached value is (n - 8) s.  Tables, lengths, rows, plan
+ * and release: as above; what the host cannot see is checked and flagged as above.
  */
 
 /*
