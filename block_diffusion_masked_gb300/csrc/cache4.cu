@@ -61,7 +61,8 @@ __device__ __forceinline__ unsigned group_key(const uint4& w) {
 // made larger by 2^-14.  x / s is half of an odd number exactly or off by at least 2^-8 of
 // itself (x has 8 significant bits, s has 3, |x / s| <= 8.5 below), so the excess moves ties
 // away from 0, by 2^-15 at least, and nothing else over a border; what the roundings below
-// may be off by is less than 2^-18 of a code.  The first product, with 8 more, is kept within
+// may be off by (the reciprocal by 2^-23 of itself, the products by 2^-22 of 8.5 codes) is
+// less than 2^-18 of a code.  The first product, with 8 more, is kept within
 // 0 and 15.4375 by taking it as a fraction of that, within 0 and 1; the second is rounded by
 // 1.5 * 2^23, which leaves the code in the sum's lowest bits.
 constexpr float kMost = 15.4375f;  // rounds to 15
@@ -74,15 +75,16 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float r) {
     const float x =
         __uint_as_float(at & 1 ? u[at >> 1] & 0xffff0000u : u[at >> 1] << 16);
     const float y = __saturatef(fmaf(x, r, 8.f / kMost));
-    out = (out << 4) + (__float_as_uint(fmaf(y, kMost, 12582912.f)) - 0x4b400000u);
+    out = (out << 4) + __float_as_uint(fmaf(y, kMost, 12582912.f));
   }
-  return out;
+  // the sum's own bits, 0x4b400000, have come in eight times, moved by 0, 4, 8, ... bits
+  return out - (0x4b400000u + 0xb4000000u + 0x40000000u);
 }
 
-// Bound by memory for prompts, by latency for single tokens (2.8 us; lengths, page and
-// tokens one after another).  Packed extremes, codes without a division and scales written
-// by words took the prompts of 8 requests (8190 tokens of 8 heads of 128) with their reading
-// back from 145 us to 107.
+// Single tokens are bound by latency (lengths, page and tokens one after another), prompts
+// by issue (85% of the cycles) close to memory: 8 requests of 8190 tokens, 8 heads of 128,
+// 340 MB, in 60 us, 5.6 TB/s; with their reading back 106 us, 145 before extremes were
+// packed, codes made without a division and scales written by words.
 //
 // One CTA per (request, touched page; key/value head; k or v), as for the 8-bit
 // append; but the tokens do not depend on one another.  Four neighbouring threads
@@ -136,7 +138,9 @@ __global__ void __launch_bounds__(NT) dfa_cache4_append_kernel(const Append4Para
   for (int u = 0; u < VPT; ++u) {
     const int i = u * NT + tid;
     const int byte = cache4_scale_byte(group_key(w[u]));
-    const float r = __frcp_rn(cache4_scale(byte)) * ((1.f + 0x1p-14f) / kMost);
+    float r;  // off by 2^-23 of itself at most
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(cache4_scale(byte)));
+    r *= (1.f + 0x1p-14f) / kMost;
     if (i < nvec) {
       codes[i] = encode8(w[u], r);
       const int token = i / kVec, vec = i % kVec;
