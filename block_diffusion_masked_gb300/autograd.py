@@ -152,8 +152,10 @@ def token_logprobs_func(logits, tokens=None, top=0):
     of -inf is a token that cannot be; a row with a NaN or +inf gives NaN.
 
     Log probabilities and entropies are differentiable in the logits, once; the
-    alternatives are not.  Arithmetic in float32, sums relative to the row's largest
-    logit; the gradient is rounded once, to the logits' type.
+    alternatives are not; forward-mode tangents are refused.  Arithmetic in float32, sums
+    relative to the row's largest logit; the gradient is rounded once, to the logits' type.
+    As with ``rotary_func``, a backward pass is captured into a CUDA graph only while no
+    eager graph of the same leaves lives.
     """
     if not isinstance(logits, torch.Tensor) or logits.dim() < 1 or logits.shape[-1] < 1:
         raise ValueError("logits must be a tensor (..., vocab)")
@@ -167,7 +169,7 @@ def token_logprobs_func(logits, tokens=None, top=0):
         logits = logits.reshape(-1, logits.shape[-1])
     if logits.shape[1] > 1 and logits.stride(1) != 1 or logits.stride(0) < 0:
         logits = logits.contiguous()
-    if torch.is_grad_enabled() and logits.requires_grad:
+    if forward_ad._current_level >= 0 or torch.is_grad_enabled() and logits.requires_grad:
         logprobs, entropy, best, which = TokenLogprobsFunc.apply(logits, tokens, top)
     else:
         logprobs, entropy, _, best, which = binding.dfa_token_logprobs(logits, tokens, top)

@@ -1016,8 +1016,8 @@ def _check_logits(logits, tokens):
     dtype = _LOGIT_TYPES.get(logits.dtype)
     if dtype is None or not logits.is_cuda:
         raise ValueError("logits must be a bfloat16, float16 or float32 tensor on a CUDA device")
-    if V < 1:
-        raise ValueError("the vocabulary is empty")
+    if not 1 <= V <= 1 << 30 or rows > 1 << 24:
+        raise ValueError("logits must be up to 2^24 rows of 1 to 2^30 values")
     stride, last = logits.stride()
     if last != 1 and V > 1:
         raise ValueError("logits: the last dimension must be contiguous")

@@ -317,6 +317,28 @@ def test_autograd_rules(b):
         assert not token_logprobs_func(x)[1].requires_grad
 
 
+def test_tangents_are_refused(b):
+    """Forward-mode tangents are not dropped silently; a level alone changes nothing."""
+    import torch.autograd.forward_ad as fwad
+    from block_diffusion_masked_gb300 import token_logprobs_func
+
+    x, t = _logits(4, 30, torch.float32, 6), torch.zeros(4, dtype=torch.int64, device=DEV)
+    want = token_logprobs_func(x, t)[0]
+    with fwad.dual_level():
+        assert torch.equal(token_logprobs_func(x, t)[0], want)
+        with pytest.raises(RuntimeError):
+            token_logprobs_func(fwad.make_dual(x, torch.ones_like(x)), t)
+
+
+def test_sizes_past_32_bits_are_not_wrapped(b):
+    """2^32 + 5 rows (of one value, expanded) are refused, not taken as 5."""
+    x = torch.zeros((1, 1), device=DEV).expand(2 ** 32 + 5, 1)
+    with pytest.raises(ValueError):
+        b.dfa_token_logprobs(x)
+    with pytest.raises(ValueError):
+        b.dfa_token_logprobs_backward(x, None, x, x)
+
+
 def test_refusals(b):
     x, t = _logits(4, 30, torch.float32), torch.zeros(4, dtype=torch.int64, device=DEV)
     _, ent, stats, _, _ = b.dfa_token_logprobs(x, t)
