@@ -826,6 +826,8 @@ def _check_cache(k_cache, v_cache, k_scale, v_scale, block_table, cache_lens, cu
     _check_dense(k_scale, scales, scale_kind, dev, "k_scale")
     _check_dense(v_scale, scales, scale_kind, dev, "v_scale")
     B, maxp = _check_dims(block_table, 2, "block_table")
+    if B > _INT_MAX or maxp > _INT_MAX or P > _INT_MAX:
+        raise ValueError("requests, pages and pages of a request must fit 32 bits")
     _check_dense(block_table, (B, maxp), torch.int32, dev, "block_table")
     _check_dense(cache_lens, (B,), torch.int32, dev, "cache_lens")
     _check_dense(cu_new, (B + 1,), torch.int32, dev, "cu_new")
