@@ -36,8 +36,8 @@
 // pieces of a cut segment are joined by a second launch.
 //
 // Measured (headdim 128, 8 heads for keys): 64 ragged requests of up to 16000 tokens, 4 rows
-// to a key, 689 MB: 181 us, 3.8 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
-// rows, 126 MB: 59 us against 18.5; one request of 500 tokens, 4 heads: 10.8 us, launches
+// to a key, 689 MB: 177 us, 3.9 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
+// rows, 126 MB: 57 us against 18.5; one request of 500 tokens, 4 heads: 10.1 us, launches
 // and latency.  Bound by the decoding: a unit is some 790 instructions of a warp, and the
 // schedulers issue in 70% of the cycles while all warps have work (a copy of the kernel that
 // only loads moves 6.5 TB/s).  Ends of pieces cost a block some 10000 cycles (requests'
@@ -97,6 +97,10 @@ __device__ __forceinline__ T lds(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void sts(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
 // 16 bytes of global memory into shared memory; zeros instead where !there.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -121,9 +125,9 @@ struct Cache4Tile {
   static constexpr int kTile = kUnit * D / 2;  // bytes of a unit's k, and of its v
   static constexpr int kScales = D;            // and of either's scales, a group after another
   static constexpr int kPitch = D + 4;         // floats per row of a warp's output at the join
-  static constexpr bool kHoldQ = NT * D <= 256;  // query fragments in registers
   static constexpr int kJoin = KEPT * kRows * kPitch * 4;
-  static constexpr int kQ = kHoldQ ? 0 : NT * (D / 16) * 32 * 8;
+  static constexpr int kBeginAt = NT * (D / 16) * 32 * 8;  // behind the query fragments
+  static constexpr int kQ = kBeginAt + NT * (D / 32) * 32 * 8;
   // rings (1024-byte aligned): k, v of each stage | scales | join, before it the query
   // fragments | statistics | valid keys
   static constexpr int kOffScale = WK * STAGES * 2 * kTile;
@@ -302,12 +306,12 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
       return q;
     };
     // The queries' fragments for the cached keys, the powers of two, and what the groups'
-    // scores begin at.
-    // (as the operand they are, or where registers are short the two that differ)
-    constexpr int kBegin = NT * D <= 128 ? 4 : 2;
-    uint32_t qb[T::kHoldQ ? NT : 1][D / 16][2];
-    float factor[NT][2], begin[NT][kGroups][kBegin];
-    const uint32_t q_at = smem0 + T::kOffJoin + lane * 8;
+    // scores begin at.  Fragments and beginnings are read from shared memory by every unit:
+    // registers are better spent on the sums (held in registers: 181 us against 177 for 64
+    // requests of 4 rows, 68 against 52 for 32 requests of 16 rows of headdim 256).
+    float factor[NT][2];
+    const uint32_t q_at = smem0 + T::kOffJoin + lane * 16;
+    const uint32_t begin_at = smem0 + T::kOffJoin + T::kBeginAt + lane * 8;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       uint4 q[kGroups];
@@ -350,18 +354,9 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
         float c[4];
         mma_f16(c, minus8, b, zero);
         mma_f16(c, minus8, b + 2, c);
-#pragma unroll
-        for (int x = 0; x < kBegin; ++x) begin[nt][grp][x] = c[x];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if constexpr (T::kHoldQ) {
-            qb[nt][2 * grp + s][0] = b[2 * s], qb[nt][2 * grp + s][1] = b[2 * s + 1];
-          } else if (wk == 0) {
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(q_at + (nt * (D / 16) + 2 * grp +
-                                                                         s) * 256),
-                         "r"(b[2 * s]), "r"(b[2 * s + 1])
-                         : "memory");
-          }
+        if (wk == 0) {
+          st_shared_v4(q_at + (nt * kGroups + grp) * 512, b[0], b[1], b[2], b[3]);
+          sts(begin_at + (nt * kGroups + grp) * 256, __float_as_uint(c[0]), __float_as_uint(c[1]));
         }
       }
     }
@@ -395,7 +390,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
     // taken against the reference as it stands; only where their sum says that one may have
     // outgrown f16, or with `look`, is the maximum found and the unit done again.
     // (The weight is 1 but behind own keys.  A copy of the code without it costs more in
-    // instructions to be fetched than the products do: 184 us against 181 for 64 requests.)
+    // instructions to be fetched than the products do: 3 us of 184 for 64 requests.)
     auto soften = [&](auto kt, auto f16, auto& sc, const float (&f)[NT][2], bool look, auto& pf) {
       constexpr int KT = decltype(kt)::value;
       float shrink[NT][2];
@@ -605,7 +600,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
             for (int x = 0; x < 4; ++x) o[nt][i][x] *= grow;
       }
     }
-    if constexpr (!T::kHoldQ) __syncthreads();  // the queries' fragments
+    __syncthreads();  // the queries' fragments
 
 #pragma unroll 1
     for (int u = 0; u < units; ++u) {
@@ -625,6 +620,15 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
         for (int grp = 0; grp < kGroups; ++grp) {
           uint32_t word[4];
           load_matrices(k_at ^ (16 * grp), word);
+          uint4 b[NT];
+          float c0[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            b[nt] = lds128(q_at + (nt * kGroups + grp) * 512);
+            const uint2 x = lds<uint2>(begin_at + (nt * kGroups + grp) * 256);
+            c0[nt][0] = c0[nt][2] = __uint_as_float(x.x);
+            c0[nt][1] = c0[nt][3] = __uint_as_float(x.y);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             // the scales of the thread's two keys
@@ -651,21 +655,10 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
                  (hi >> 8) & 0x00f000f0u}};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              uint32_t b[2][2];
-#pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                if constexpr (T::kHoldQ) {
-                  b[s][0] = qb[nt][2 * grp + s][0], b[s][1] = qb[nt][2 * grp + s][1];
-                } else {
-                  const uint2 x = lds<uint2>(q_at + (nt * (D / 16) + 2 * grp + s) * 256);
-                  b[s][0] = x.x, b[s][1] = x.y;
-                }
-              }
-              const float* bg = begin[nt][grp];
-              const float c0[4] = {bg[0], bg[1], bg[kBegin - 2], bg[kBegin - 1]};
+              const uint32_t b0[2] = {b[nt].x, b[nt].y}, b1[2] = {b[nt].z, b[nt].w};
               float c[4];
-              mma_f16(c, a[0], b[0], c0);
-              mma_f16(c, a[1], b[1], c);
+              mma_f16(c, a[0], b0, c0[nt]);
+              mma_f16(c, a[1], b1, c);
 #pragma unroll
               for (int x = 0; x < 4; ++x)
                 sc[nt][i][x] = grp == 0 ? c[x] * ks[x >> 1] : fmaf(c[x], ks[x >> 1], sc[nt][i][x]);
@@ -832,16 +825,13 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
 // Row tiles, warps, stages, blocks per SM and outputs kept, for a head dimension and a
 // segment's rows.
 //
-// Blocks per SM: what the registers of the fragments allow without spilling much (3 blocks
-// of 168 registers for 8 rows, 2 of 255 for 16).  More lose to spills, fewer to idle
-// schedulers (us, 32 ragged requests of up to 8192 tokens, 512 / headdim heads for keys):
-// headdim 128, 16 rows 42 with 2 and 52 with 3; headdim 64, 8 rows 38 with 4 and 41 with 3;
-// headdim 256 8 rows 39 with 2, 40 with 1, 16 rows 68 with 2, 75 with 1; headdim 128, 8 rows
-// 33 with 3 and with 2.  Stages: two keep enough in flight with 8 or 12 warps (headdim 128:
-// 185.5, 186.1 and 186.6 us for 64 requests of up to 16000 tokens with 2, 3 and 4), and
-// what they leave is L1 for what the registers spill.
-template <int D, int ROWS>
-struct Variant;
+// Blocks per SM: what the registers allow without spilling much (headdim 128: 3 blocks of
+// 161 registers for 8 rows, 2 of 244 for 16).  More lose to spills, fewer to idle schedulers
+// (us, 32 ragged requests of up to 8192 tokens, 512 / headdim heads for keys): headdim 128,
+// 16 rows 41 with 2 and 44 with 3; headdim 64, 8 rows 38 with 4 and 41 with 3, 16 rows 46
+// with 3 and 49 with 4.  Stages: two keep enough in flight with 8 or 12 warps (headdim 128,
+// 64 requests of up to 16000 tokens: two, three and four within 1 us of 186), and what they
+// leave is L1 for what the registers spill.
 template <> struct Variant<64, 8> { using T = Cache4Tile<64, 1, 4, 4, 4, 4>; };
 template <> struct Variant<64, 16> { using T = Cache4Tile<64, 2, 4, 5, 3, 4>; };
 template <> struct Variant<64, 32> { using T = Cache4Tile<64, 4, 4, 3, 2, 4>; };

@@ -1008,22 +1008,22 @@ CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, lon
 
 // The same for the 4-bit cache (cache4_fwd.cu, cache_wide.cuh).  Measured (us) as above,
 // 512 / headdim heads for keys:
-//   headdim 128, 32 rows: 69 in a tile of 128 (the tcgen05 kernel), 82 in one of 32 (whose
-//     fragments spill), 42 for 16 rows in one of 16; headdim 64, 32 rows: 98 in one of 128,
-//     72 in one of 32, 36 rows 98 in one of 128 and 128 in two of 32.
+//   headdim 128, 32 rows: 68 in a tile of 128 (the tcgen05 kernel), 82 in one of 32 (whose
+//     fragments spill); 16 rows 41 in one of 16.  Headdim 64, 32 rows: 98 in one of 128, 67
+//     in one of 32; 36 rows 101 in one of 128, 128 in two of 32.
 //                      finish 4     5     6     8    10    12
-//   headdim  64,   8 rows    38    39    39    41
-//   headdim  64,  16 rows    47    47    47    49
-//   headdim  64,  32 rows    81    77    77    72    74
-//   headdim  64, 128 rows   112   106   105   105   107   106
-//   headdim 128,   8 rows    34    34    34    35
-//   headdim 128,  16 rows    45    42    42    43
-//   headdim 128, 128 rows    91    84    82    79    80    83  (76 by now)
-//   headdim 256,   8 rows    38    39    39    41
-//   headdim 256,  16 rows    68    69    67    70
-// Not cut against cut: 64 requests of 500 keys and 4 heads, 8 rows 17.2 and 19.4, 16 rows
-// 18.6 and 24.5; of 1000 keys 24.8 and 24.6, 24.9 and 30.1; one request of 250 keys 10.3
-// and 9.7 but for the second launch, of 500 12.2 and 9.9, of 1000 17.0 and 10.0.
+//   headdim  64,   8 rows    38    38    39    41    43    44
+//   headdim  64,  16 rows    47    46    47    47    49    50
+//   headdim  64,  32 rows    75    72    71    67    70    71
+//   headdim  64, 128 rows   111   109   108   107   110   109
+//   headdim 128,   8 rows    32    32    32    33    34    35
+//   headdim 128,  16 rows    43    41    41    42    43    45
+//   headdim 128, 128 rows    88    82    79    76    76    80
+//   headdim 256,   8 rows    34    33    33    34    34    36
+//   headdim 256,  16 rows    57    54    53    54    52    55
+// Not cut against cut: 64 requests of 500 keys and 4 heads, 8 rows 16.6 and 19.3, 16 rows
+// 19.2 and 24.3; of 1000 keys 23.9 and 23.4, 25.4 and 29.4; one request of 250 keys 9.9 and
+// 9.3 but for the second launch, of 500 11.8 and 9.5, of 1000 15.9 and 9.7.
 CachePlan cache4_plan_for(int batch, int max_new, int G, int kv_heads, int d, long long keys,
                           int sms) {
   CachePlan c;

@@ -650,10 +650,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       if (p.splits > 1) {
         if (tid < p.top)
           p.part_top[static_cast<long long>(item) * p.top + tid] = s.best[tid];
-      } else if (warp == 0) {
-        Stats b = lane < kThreads / 32 ? s_warp[lane] : Stats{-INFINITY, 0.f, 0.f};
-        const Finished f = finish(warp_join(b));
-        if (lane < p.top) write_top(p, c0.row, lane, s.best[lane], f);
       }
     } else {
       __syncthreads();
@@ -661,9 +657,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     if (warp == 0) {
       Stats b = lane < kThreads / 32 ? s_warp[lane] : Stats{-INFINITY, 0.f, 0.f};
       b = warp_join(b);
-      if (lane == 0) {
-        if (p.splits > 1) p.part[item] = b;
-        else write_row(p, c0.row, finish(b), load_token<T>(p, c0.row));
+      if (p.splits > 1) {
+        if (lane == 0) p.part[item] = b;
+      } else {
+        const Finished f = finish(b);
+        if (lane == 0) write_row(p, c0.row, f, load_token<T>(p, c0.row));
+        if constexpr (TOP) {
+          if (lane < p.top) write_top(p, c0.row, lane, space.best[lane], f);
+        }
       }
     }
     __syncthreads();  // the statistics and the list have been read
