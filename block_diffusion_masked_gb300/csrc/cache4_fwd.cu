@@ -832,6 +832,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
 // with 3 and 49 with 4.  Stages: two keep enough in flight with 8 or 12 warps (headdim 128,
 // 64 requests of up to 16000 tokens: two, three and four within 1 us of 186), and what they
 // leave is L1 for what the registers spill.
+template <int D, int ROWS>
+struct Variant;
 template <> struct Variant<64, 8> { using T = Cache4Tile<64, 1, 4, 4, 4, 4>; };
 template <> struct Variant<64, 16> { using T = Cache4Tile<64, 2, 4, 5, 3, 4>; };
 template <> struct Variant<64, 32> { using T = Cache4Tile<64, 4, 4, 3, 2, 4>; };
