@@ -129,6 +129,11 @@ KERNEL_SOURCES = {
     "dfa_cache_append_kernel": "cache.cu",
     "dfa_cache_fwd_kernel": "cache_fwd.cu",
     "dfa_cache_wide_kernel": "cache_wide.cu",
+    "dfa_cache4_append_kernel": "cache4.cu",
+    "dfa_cache_read_kernel": "cache4.cu",
+    "dfa_cache4_rows_kernel": "cache4_fwd.cu",
+    "dfa_scores_kernel": "scores.cu",
+    "dfa_scores_grad_kernel": "scores.cu",
 }
 
 
