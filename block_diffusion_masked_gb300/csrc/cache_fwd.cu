@@ -1008,17 +1008,17 @@ CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, lon
 
 // The same for the 4-bit cache (cache4_fwd.cu, cache_wide.cuh).  Measured (us) as above,
 // 512 / headdim heads for keys:
-//   headdim 128, 32 rows: 68 in a tile of 128 (the tcgen05 kernel), 82 in one of 32 (whose
+//   headdim 128, 32 rows: 65 in a tile of 128 (the tcgen05 kernel), 82 in one of 32 (whose
 //     fragments spill); 16 rows 41 in one of 16.  Headdim 64, 32 rows: 98 in one of 128, 67
 //     in one of 32; 36 rows 101 in one of 128, 128 in two of 32.
 //                      finish 4     5     6     8    10    12
 //   headdim  64,   8 rows    38    38    39    41    43    44
 //   headdim  64,  16 rows    47    46    47    47    49    50
 //   headdim  64,  32 rows    75    72    71    67    70    71
-//   headdim  64, 128 rows   111   109   108   107   110   109
+//   headdim  64, 128 rows   111   109   108   107   110   109  (104 by now)
 //   headdim 128,   8 rows    32    32    32    33    34    35
 //   headdim 128,  16 rows    43    41    41    42    43    45
-//   headdim 128, 128 rows    88    82    79    76    76    80
+//   headdim 128, 128 rows    88    82    79    76    76    80  (73 by now)
 //   headdim 256,   8 rows    34    33    33    34    34    36
 //   headdim 256,  16 rows    57    54    53    54    52    55
 // Not cut against cut: 64 requests of 500 keys and 4 heads, 8 rows 16.6 and 19.3, 16 rows

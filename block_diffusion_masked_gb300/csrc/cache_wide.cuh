@@ -26,7 +26,7 @@
 // others (setmaxnreg).
 //
 // Measured, 128 rows, headdim 128, 32 ragged requests of up to 8192 tokens
-// (342 MB, 81 GFLOP): 127 us, 2.7 TB/s, 640 TFLOP/s; 64 rows 124, headdim 64
+// (342 MB, 81 GFLOP): 124 us, 2.8 TB/s, 650 TFLOP/s; 64 rows 124, headdim 64
 // 197 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
 // takes them some 2400 cycles, of which its 128 x 128 exponentials need 512 of
 // the special function units'; what is left is latency (waits that find their
@@ -81,9 +81,10 @@ struct WideCfg {
   static constexpr int kSoftWarps = 8;
   static constexpr int kWarpConvV = 12, kWarpLoadK = 16, kWarpLoadV = 17, kWarpS = 18, kWarpPV = 19;
   static constexpr int kThreads = 32 * 20;
-  // setmaxnreg split of the launch's 96 registers a thread:
-  // 256 * 136 + 256 * 72 + 128 * 64 == 640 * 96
-  static constexpr int kRegSoft = 136, kRegConv = 72, kRegRest = 64;
+  // setmaxnreg split of the launch's 96 registers a thread: 256 * 120 + 256 * 88 + 128 * 64
+  // == 640 * 96.  None of the roles spills (with 136, 72 and 64 the 4-bit converters do: 64
+  // rows 71 us against 68, 128 rows 76 against 73; 8 bits 127 against 124.5).
+  static constexpr int kRegSoft = 120, kRegConv = 88, kRegRest = 64;
   static_assert(256 * kRegSoft + 256 * kRegConv + 128 * kRegRest <= kThreads * 96,
                 "a split above the launch's registers waits forever");
   static constexpr int kRaw = BN * D * BITS / 8;  // a raw tile of k or of v, RS of each
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
     const int g4 = D == 64 ? lane & 1 : (lane & 1) + 2 * (lane >> 4);
     auto convert4 = [&](uint32_t raw, uint32_t scales, uint32_t dst, bool mask, int group_keys) {
       constexpr int kRows = D == 64 ? 64 : 32;  // rows at a time
-#pragma unroll 1
+#pragma unroll 2  // 1: 1 to 4% slower, 4: 11%
       for (int r = r4; r < BN; r += kRows) {
         const uint32_t x = r * (D / 2) + 16 * g4;
         const uint4 w = lds128(raw + (x ^ (((x >> 7) & (D == 64 ? 3 : 7)) << 4)));
