@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float r) {
 }
 
 // Single tokens are bound by latency (lengths, page and tokens one after another), prompts
-// by issue (85% of the cycles) close to memory: 8 requests of 8190 tokens, 8 heads of 128,
+// by issue (80% of the cycles) close to memory: 8 requests of 8190 tokens, 8 heads of 128,
 // 340 MB, in 60 us, 5.6 TB/s; with their reading back 106 us, 145 before extremes were
 // packed, codes made without a division and scales written by words.
 //

@@ -38,7 +38,7 @@
 // Measured (headdim 128, 8 heads for keys): 64 ragged requests of up to 16000 tokens, 4 rows
 // to a key, 689 MB: 177 us, 3.9 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
 // rows, 126 MB: 57 us against 18.5; one request of 500 tokens, 4 heads: 10.1 us, launches
-// and latency.  Bound by the decoding: a unit is some 790 instructions of a warp, and the
+// and latency.  Bound by the decoding: a unit is some 770 instructions of a warp, and the
 // schedulers issue in 70% of the cycles while all warps have work (a copy of the kernel that
 // only loads moves 6.5 TB/s).  Ends of pieces cost a block some 10000 cycles (requests'
 // sizes, queries, own keys, join: one latency after another), which is what the shorter
