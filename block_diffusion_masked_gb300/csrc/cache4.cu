@@ -33,22 +33,27 @@ struct Append4Params {
   int rows, max_new, Hk, page_size, num_pages, max_pages, touch;
 };
 
-// The key (cache4_scale_byte) of a group of 32 values of which this thread and its three
-// neighbours hold eight each: the largest value and the largest negated one, two to an
-// operation, NaN where there is one.
-__device__ __forceinline__ unsigned group_key(const uint4& w) {
+// The key (cache4_scale_byte) of a group of 32 values: the largest value and the largest
+// negated one, two to an operation, NaN where there is one.
+__device__ __forceinline__ unsigned group_key(const uint4 (&w)[4]) {
   auto as2 = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
   auto bits = [](__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); };
-  const uint32_t hi = bits(__hmax2_nan(__hmax2_nan(as2(w.x), as2(w.y)),
-                                       __hmax2_nan(as2(w.z), as2(w.w))));
-  const uint32_t lo = bits(__hmin2_nan(__hmin2_nan(as2(w.x), as2(w.y)),
-                                       __hmin2_nan(as2(w.z), as2(w.w)))) ^
+  __nv_bfloat162 most[4], least[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    most[i] = __hmax2_nan(__hmax2_nan(as2(w[i].x), as2(w[i].y)),
+                          __hmax2_nan(as2(w[i].z), as2(w[i].w)));
+    least[i] = __hmin2_nan(__hmin2_nan(as2(w[i].x), as2(w[i].y)),
+                           __hmin2_nan(as2(w[i].z), as2(w[i].w)));
+  }
+  const uint32_t hi = bits(__hmax2_nan(__hmax2_nan(most[0], most[1]),
+                                       __hmax2_nan(most[2], most[3])));
+  const uint32_t lo = bits(__hmin2_nan(__hmin2_nan(least[0], least[1]),
+                                       __hmin2_nan(least[2], least[3]))) ^
                       0x80008000u;
   // the largest value in the low half, the largest negated one in the high half
-  uint32_t top = bits(__hmax2_nan(as2(__byte_perm(hi, lo, 0x5410)),
-                                  as2(__byte_perm(hi, lo, 0x7632))));
-  top = bits(__hmax2_nan(as2(top), as2(__shfl_xor_sync(0xffffffffu, top, 1))));
-  top = bits(__hmax2_nan(as2(top), as2(__shfl_xor_sync(0xffffffffu, top, 2))));
+  const uint32_t top = bits(__hmax2_nan(as2(__byte_perm(hi, lo, 0x5410)),
+                                        as2(__byte_perm(hi, lo, 0x7632))));
   // Of the two the larger is the group's largest magnitude (both are negative zeros at
   // least): as signed integers, of which a NaN's is the largest.
   const int pos = static_cast<short>(top & 0xffffu), neg = static_cast<short>(top >> 16);
@@ -82,19 +87,17 @@ __device__ __forceinline__ uint32_t encode8(const uint4& w, float r) {
 }
 
 // Single tokens are bound by latency (lengths, page and tokens one after another), prompts
-// by issue (80% of the cycles) close to memory: 8 requests of 8190 tokens, 8 heads of 128,
-// 340 MB, in 60 us, 5.6 TB/s; with their reading back 106 us, 145 before extremes were
-// packed, codes made without a division and scales written by words.
+// by memory: 8 requests of 8190 tokens, 8 heads of 128, 340 MB, in 53 us, 6.4 TB/s; with
+// their reading back 94 us, 145 before extremes were packed, codes made without a division,
+// scales written by words and a group given to one thread.
 //
 // One CTA per (request, touched page; key/value head; k or v), as for the 8-bit
-// append; but the tokens do not depend on one another.  Four neighbouring threads
-// hold a group of 32 values, eight each: they settle its scale by two exchanges and
-// write four bytes of codes each, one of them the scale's byte.
-template <int D, int NT, int VPT>
+// append; but the tokens do not depend on one another.  A thread takes groups of 32
+// values, so that what a scale costs is paid once (four threads to a group: 61 us).
+template <int D, int NT, int GPT>
 __global__ void __launch_bounds__(NT) dfa_cache4_append_kernel(const Append4Params p) {
-  constexpr int kVec = D / 8;  // vectors per token and head
-  constexpr int kTokens = NT * VPT / kVec < 128 ? NT * VPT / kVec : 128;
-  constexpr int kGroups = D / kCache4Group;
+  constexpr int kGroups = D / kCache4Group;  // per token and head
+  constexpr int kTokens = NT * GPT / kGroups < 128 ? NT * GPT / kGroups : 128;
   __shared__ uint8_t s_scale[kGroups][kTokens + 4];  // of tokens from a multiple of four on
   grid_launch_dependents();
   grid_dependency_wait();
@@ -116,42 +119,43 @@ __global__ void __launch_bounds__(NT) dfa_cache4_append_kernel(const Append4Para
   if (slot < p.max_pages)
     page = p.block_table[static_cast<long long>(b) * p.max_pages + slot];
   const int first = span.lo & (p.page_size - 1);  // older tokens of the page
-  const int nvec = (span.hi - span.lo) * kVec;
+  const int tokens = span.hi - span.lo, groups = tokens * kGroups;
   const long long sr = p.sr[which];
   const __nv_bfloat16* x = p.x[which] + (r0 + (span.lo - len)) * sr + h * p.sh[which];
-  uint4 w[VPT];
+  uint4 w[GPT][4];
 #pragma unroll
-  for (int u = 0; u < VPT; ++u) {
+  for (int u = 0; u < GPT; ++u) {
     const int i = u * NT + tid;
-    w[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < nvec) w[u] = *reinterpret_cast<const uint4*>(x + (i / kVec) * sr + (i % kVec) * 8);
+    const uint4* src =
+        reinterpret_cast<const uint4*>(x + (i / kGroups) * sr + (i % kGroups) * kCache4Group);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[u][e] = i < groups ? src[e] : make_uint4(0u, 0u, 0u, 0u);
   }
   if (!cache_page_ok(page, p.num_pages)) {  // nowhere to put it
     if (tid == 0) atomicOr(p.status, kStatusIndex);
     return;
   }
   const long long base = static_cast<long long>(page) * p.Hk + h;
-  uint32_t* codes =
-      reinterpret_cast<uint32_t*>(p.cache[which] + (base * p.page_size + first) * (D / 2));
+  uint4* codes =
+      reinterpret_cast<uint4*>(p.cache[which] + (base * p.page_size + first) * (D / 2));
   uint8_t* scale = p.scale[which] + base * p.page_size * (D / kCache4Group);
 #pragma unroll
-  for (int u = 0; u < VPT; ++u) {
+  for (int u = 0; u < GPT; ++u) {
     const int i = u * NT + tid;
+    if (i >= groups) break;
     const int byte = cache4_scale_byte(group_key(w[u]));
     float r;  // off by 2^-23 of itself at most
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(cache4_scale(byte)));
     r *= (1.f + 0x1p-14f) / kMost;
-    if (i < nvec) {
-      codes[i] = encode8(w[u], r);
-      const int token = i / kVec, vec = i % kVec;
-      if ((vec & 3) == 0) s_scale[vec >> 2][(first & 3) + token] = static_cast<uint8_t>(byte);
-    }
+    codes[i] = make_uint4(encode8(w[u][0], r), encode8(w[u][1], r), encode8(w[u][2], r),
+                          encode8(w[u][3], r));
+    s_scale[i % kGroups][(first & 3) + i / kGroups] = static_cast<uint8_t>(byte);
   }
   // The scales, tokens of a group next to one another: four at a time where all are new.
   if constexpr (NT > 32) __syncthreads();
   else __syncwarp();
-  const int from = first & ~3, words = (nvec / kVec + (first & 3) + 3) >> 2;
-  const int end = first + nvec / kVec;
+  const int from = first & ~3, words = (tokens + (first & 3) + 3) >> 2;
+  const int end = first + tokens;
   for (int i = tid; i < kGroups * words; i += NT) {
     const int grp = i / words, word = i - grp * words, token = from + 4 * word;
     uint8_t* dst = scale + grp * p.page_size + token;
@@ -166,26 +170,26 @@ __global__ void __launch_bounds__(NT) dfa_cache4_append_kernel(const Append4Para
   }
 }
 
-template <int D, int NT, int VPT>
+template <int D, int NT, int GPT>
 cudaError_t launch_append_block(const Append4Params& p, unsigned blocks, cudaStream_t stream) {
-  return launch_chained(dfa_cache4_append_kernel<D, NT, VPT>, dim3(blocks), dim3(NT), 0, stream,
+  return launch_chained(dfa_cache4_append_kernel<D, NT, GPT>, dim3(blocks), dim3(NT), 0, stream,
                         p);
 }
 
 template <int D>
 cudaError_t launch_append(const Append4Params& p, int batch, cudaStream_t stream) {
   const unsigned n = 2u * p.Hk * batch * p.touch;
-  const int vectors = (p.max_new < p.page_size ? p.max_new : p.page_size) * (D / 8);
-  if (vectors <= 128) return launch_append_block<D, 32, 4>(p, n, stream);
-  if (vectors <= 512) return launch_append_block<D, 128, 4>(p, n, stream);
-  // a page of 128 tokens is 1024, 2048 or 4096 vectors
+  const int groups = (p.max_new < p.page_size ? p.max_new : p.page_size) * (D / kCache4Group);
+  if (groups <= 32) return launch_append_block<D, 32, 1>(p, n, stream);
+  if (groups <= 128) return launch_append_block<D, 128, 1>(p, n, stream);
+  // a page of 128 tokens is 256, 512 or 1024 groups
   if constexpr (D == 128) {
-    if (vectors > 1024) return launch_append_block<D, 256, 8>(p, n, stream);
+    if (groups > 256) return launch_append_block<D, 256, 2>(p, n, stream);
   } else if constexpr (D == 256) {
-    if (vectors > 2048) return launch_append_block<D, 512, 8>(p, n, stream);
-    if (vectors > 1024) return launch_append_block<D, 256, 8>(p, n, stream);
+    if (groups > 512) return launch_append_block<D, 512, 2>(p, n, stream);
+    if (groups > 256) return launch_append_block<D, 256, 2>(p, n, stream);
   }
-  return launch_append_block<D, 128, 8>(p, n, stream);
+  return launch_append_block<D, 128, 2>(p, n, stream);
 }
 
 // ------------------------------------------------------------------ read
@@ -223,8 +227,8 @@ __device__ __forceinline__ int find_request(const int* cu, int batch, int row) {
 
 constexpr int kReadWarps = 8, kReadRows = 32;  // a row for each lane of a warp
 
-// Bound by memory: 80 k tokens of 8 heads of 128 read back from 4 bits in 58 us (318 MB
-// written and read at 5.5 TB/s; 91 us while each warp looked up its own rows' places).
+// Bound by memory: 80 k tokens of 8 heads of 128 read back from 4 bits in 55 us (318 MB
+// written and read at 5.8 TB/s; 91 us while each warp looked up its own rows' places).
 //
 // A block takes up to 32 rows.  The lanes of its first warp find a row's request, page and
 // place each, so that the chain of their loads is paid once; then every warp moves rows,
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(32 * kReadWarps) dfa_cache_read_kernel(const R
     const uint8_t* cache = which ? p.cache[1] : p.cache[0];
     const void* scales = which ? p.scale[1] : p.scale[0];
     const long long heads = static_cast<long long>(page) * p.Hk;
-    constexpr int kAtOnce = 8;
+    constexpr int kAtOnce = 4;  // 8 heads of 128 are 128 vectors; 8: 58 us
 #pragma unroll 1
     for (int i0 = lane; i0 < per; i0 += 32 * kAtOnce) {
       uint2 w[kAtOnce];
