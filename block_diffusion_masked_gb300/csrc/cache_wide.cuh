@@ -26,7 +26,7 @@
 // others (setmaxnreg).
 //
 // Measured, 128 rows, headdim 128, 32 ragged requests of up to 8192 tokens
-// (342 MB, 81 GFLOP): 124 us, 2.8 TB/s, 650 TFLOP/s; 64 rows 124, headdim 64
+// (342 MB, 81 GFLOP): 126 us, 2.7 TB/s, 640 TFLOP/s; 64 rows 124, headdim 64
 // 197 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
 // takes them some 2400 cycles, of which its 128 x 128 exponentials need 512 of
 // the special function units'; what is left is latency (waits that find their
@@ -35,7 +35,7 @@
 // loaded ahead, loops unrolled) made the kernel 30% slower, and rolled
 // converters made it 5% faster.  Ends of pieces take 10 us each, of which the
 // last tiles' chain is most, and the first products come after 11.  4 bits, the same
-// requests, 128 rows and 8 heads: 139 us against 43 for the products; a tile takes 2800
+// requests, 128 rows and 8 heads: 136 us against 43 for the products; a tile takes 2800
 // cycles, 1470 of them the softmax warps' own, and the converters 1800, which the rings'
 // two operand tiles hide.
 #pragma once
@@ -81,10 +81,12 @@ struct WideCfg {
   static constexpr int kSoftWarps = 8;
   static constexpr int kWarpConvV = 12, kWarpLoadK = 16, kWarpLoadV = 17, kWarpS = 18, kWarpPV = 19;
   static constexpr int kThreads = 32 * 20;
-  // setmaxnreg split of the launch's 96 registers a thread: 256 * 120 + 256 * 88 + 128 * 64
-  // == 640 * 96.  None of the roles spills (with 136, 72 and 64 the 4-bit converters do: 64
-  // rows 71 us against 68, 128 rows 76 against 73; 8 bits 127 against 124.5).
-  static constexpr int kRegSoft = 120, kRegConv = 88, kRegRest = 64;
+  // setmaxnreg split of the launch's 96 registers a thread: 256 * (120 + 88) + 128 * 64 ==
+  // 640 * 96.  No role spills (with 136, 72 and 64 the 4-bit converters do).  Measured, 128
+  // rows of headdim 128: 4 bits 136 us with 128 and 80, 138 with 120 and 88; 8 bits 129 and
+  // 126.
+  static constexpr int kRegSoft = BITS == 4 ? 128 : 120, kRegConv = BITS == 4 ? 80 : 88,
+                       kRegRest = 64;
   static_assert(256 * kRegSoft + 256 * kRegConv + 128 * kRegRest <= kThreads * 96,
                 "a split above the launch's registers waits forever");
   static constexpr int kRaw = BN * D * BITS / 8;  // a raw tile of k or of v, RS of each
@@ -627,9 +629,26 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
       float factor = 0.f;  // undoes the row's power of two, with the softmax scale
       float m = -INFINITY, l = 0.f;
       float c = pow2_bits(kCacheMinExp), inv_c = pow2_bits(-kCacheMinExp);  // unit of O
-      // One tile, in three copies so that the common one is short: cached with
-      // all its keys, cached with some, own keys (bf16, row by row).
-      constexpr int kWhole = 0, kPart = 1, kOwn = 2;
+      // The scores of keys that a cached tile does not have become -inf where they stand: a
+      // pass of its own over the few such tiles, so that the common code stays short.
+      auto hide = [&](const TileInfo& info) {
+        tc_fence_after();
+        const uint32_t s_col = t_lane + (n & 1) * BN;
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          uint32_t sr[16];
+          tmem_ld_half<16, 64>(s_col + 16 * x, sr);
+          tmem_wait_ld();
+          tmem_pin<16>(sr);
+          const int keys = info.keys[4 * half + x];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sr[e] = e < keys ? sr[e] : 0xff800000u;
+          tmem_st_half<16, 64>(s_col + 16 * x, sr);
+        }
+        tmem_wait_st();
+      };
+      // One tile, in two copies: cached ones, own keys (bf16, row by row).
+      constexpr int kCached = 0, kOwn = 1;
       auto tile = [&](auto kind, int j, const TileInfo& info) -> bool {
         constexpr int kKind = decltype(kind)::value;
         const int b = n & 1;
@@ -656,15 +675,9 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
           tmem_ld_half<32, 64>(s_col + 32 * x, sr);
           tmem_wait_ld();
           tmem_pin<32>(sr);
-          if constexpr (kKind != kWhole) {
-            uint32_t keep;
-            if constexpr (kKind == kPart) {
-              const int k0 = info.keys[4 * half + 2 * x], k1 = info.keys[4 * half + 2 * x + 1];
-              keep = ((1u << k0) - 1u) | (((1u << k1) - 1u) << 16);
-            } else {
-              const int left = end - BN * (j - k.nc) - 64 * half - 32 * x;
-              keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
-            }
+          if constexpr (kKind == kOwn) {
+            const int left = end - BN * (j - k.nc) - 64 * half - 32 * x;
+            const uint32_t keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const uint32_t mk = bit_spread(keep, e);
@@ -778,8 +791,8 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
             factor = pow2_bits(e) * p.scale_log2;
             if constexpr (BITS == 4) factor = fmaxf(factor * kCache4Unit, 1.1754944e-38f);
           }
-          if (info.whole) ok = tile(std::integral_constant<int, kWhole>{}, j, info);
-          else ok = tile(std::integral_constant<int, kPart>{}, j, info);
+          if (!info.whole) hide(info);
+          ok = tile(std::integral_constant<int, kCached>{}, j, info);
           ++cached;
         }
         if (ok) ++n;
