@@ -44,6 +44,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A logit this far below the maximum, in powers of two, has probability 0 in float32;
 // what is further, -inf too, is taken as this far, for 0 * inf is not a number.
 constexpr float kFar = -220.f;
+// Up to this magnitude of the maximum, m log2 e is rounded by 1/4 at most (extreme(), below).
+constexpr float kFirst = 0x1p22f;
 
 // ------------------------------------------------------------------ rows of logits
 
@@ -78,8 +80,9 @@ struct Logit<__nv_bfloat16> {
     }
     return make_uint4(y[0], y[1], y[2], y[3]);
   }
-  // Whether what finite() replaces, and whatever else is far, is out of m's reach.
-  __device__ static bool plain(float m) { return fabsf(m) < 1e30f; }
+  // Whether what finite() replaces, and whatever else is far, is out of m's reach, and m
+  // itself not extreme.
+  __device__ static bool plain(float m) { return fabsf(m) <= kFirst; }
   // The largest of m and N vectors' values.
   template <int N>
   __device__ static float most(float m, const uint4* w) {
@@ -155,7 +158,7 @@ struct Logit<float> {
                       __float_as_uint(f[3]));
   }
   __device__ static uint4 finite(const uint4& w) { return w; }
-  __device__ static bool plain(float m) { return fabsf(m) < 1e30f; }
+  __device__ static bool plain(float m) { return fabsf(m) <= kFirst; }
   template <int N>
   __device__ static float most(float m, const uint4* w) {
 #pragma unroll
@@ -208,19 +211,24 @@ __device__ __forceinline__ float not_far(float x) {
 struct Stats {
   float m, s, t;
 };
-// Where r would overflow, or nearly (a row of the type's lowest value), z is (x - m) log2 e
-// in its place.
-__device__ __forceinline__ bool extreme(float m) { return fabsf(m) > 1e30f && m != -INFINITY; }
+// Past kFirst z is (x - m) log2 e in its place: what the rounding of r adds to all of them
+// grows with m, and past 2^32 it alone would take a 2^z to infinity or to 0.
+__device__ __forceinline__ bool extreme(float m) { return fabsf(m) > kFirst && m != -INFINITY; }
 // (__fmul_rn: the rounding is to be the same wherever r appears, so the product is not to be
 // drawn into a sum.)
 __device__ __forceinline__ float reference(float m) {
   return m == -INFINITY ? 0.f : __fmul_rn(m, kLog2e);
 }
+// What every z against m is too large by, for r is too small by it; at most 1/4.
+__device__ __forceinline__ float excess(float m) {
+  return extreme(m) || m == -INFINITY ? 0.f : fmaf(m, kLog2e, -reference(m));
+}
 // a against the maximum m >= a.m.
 __device__ __forceinline__ Stats rebase(const Stats& a, float m) {
   if (a.m == -INFINITY) return {m, a.s, a.t};  // nothing yet, or not a number
-  const float d = not_far(extreme(a.m) || extreme(m) ? (a.m - m) * kLog2e
-                                                     : reference(a.m) - reference(m));
+  const float d = not_far(extreme(a.m) || extreme(m)
+                              ? (a.m - m) * kLog2e + (excess(m) - excess(a.m))
+                              : reference(a.m) - reference(m));
   const float f = ex2_approx(d);
   return {m, a.s * f, f * fmaf(a.s, d, a.t)};
 }
@@ -291,9 +299,7 @@ __device__ __forceinline__ Finished finish(const Stats& a) {
   f.none = a.m == -INFINITY && a.s == 0.f;
   f.nan = !f.none && !(a.s < INFINITY);
   f.m = f.nan ? NAN : a.m;
-  // every z is too large by what r is too small
-  const float off =
-      f.none || f.nan || extreme(a.m) ? 0.f : fmaf(a.m, kLog2e, -reference(a.m));
+  const float off = f.none || f.nan ? 0.f : excess(a.m);
   const float log2_s = lg2_approx(a.s) - off;
   f.log_s = f.none ? 0.f : f.nan ? NAN : log2_s * kLn2;
   f.entropy = f.none ? 0.f : f.nan ? NAN : fmaxf((log2_s - (a.t / a.s - off)) * kLn2, 0.f);

@@ -447,3 +447,43 @@ def test_long_rows_and_offsets(b):
     lp, ent, _, best, which = b.dfa_token_logprobs(x, torch.tensor([2_999_999], device=DEV), 32)
     assert b.dfa_status() == 0
     _check(x, [2_999_999], 32, lp, ent, best, which)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [-2.0 ** 21, -2.0 ** 22 + 0.25, -2.0 ** 22, -2.0 ** 22 - 0.5,
+                                  -1e9, -5e9, -1e10, -1e12, -1e20, -1e30, -2e30, 1e7, 1e10, 1e30])
+def test_scores_of_large_finite_logits(b, dtype, size):
+    """A finite mask value of any size, in whole vectors, whole threads' shares and whole
+    pieces beside ordinary logits; rows of nothing else; rows whose largest logit it is; a
+    row that passes through such sizes on its way up.  Forward and gradient.
+
+    The bounds are those of ordinary rows: a difference to the row's maximum has one
+    rounding, of itself, whatever the size of the two."""
+    V = 40000
+    at = torch.arange(V, dtype=torch.float64)
+    plain = at * 7 % 31 / 4
+    rows = [torch.full((V,), size),
+            torch.where(at % 5 == 0, plain, size),       # within every vector
+            torch.where(at < 30000, size, plain),        # a piece's beginning, whole pieces
+            torch.where(at < 10000, plain, size),        # ... its end
+            torch.where(at // 8 % 256 < 40, plain, size),  # all of most threads' shares
+            torch.where(at == V - 2, plain, size),       # but for one token
+            torch.where(at % 3 == 0, size, -math.inf),
+            -2.0 ** (101 - at // 400)]                   # -2^101 ... -2^2
+    x = torch.stack([r.double() for r in rows]).to(dtype).to(DEV)
+    t = [3, 5, 30001, 7, 9, V - 2, 0, V - 1]
+    td = torch.tensor(t, device=DEV)
+    lp, ent, stats, best, which = b.dfa_token_logprobs(x, td, 32)
+    assert b.dfa_status() == 0
+    _check(x, t, 32, lp, ent, best, which)
+    none = b.dfa_token_logprobs(x, td, 0)  # the kernel without alternatives
+    _check(x, t, 0, none[0], none[1], none[3], none[4])
+    # rows of many pieces, and one piece to a row
+    many = x.repeat(100, 1)
+    got = b.dfa_token_logprobs(many, td.repeat(100), 3)
+    _check(x, t, 3, *(got[i][:8] for i in (0, 1, 3, 4)))
+    assert all(torch.equal(got[i][:8].repeat(100, *[1] * (got[i].dim() - 1)), got[i])
+               for i in (0, 1, 3, 4))
+    gl, ge = torch.linspace(0.5, 1, 8, device=DEV), torch.linspace(1, 0.25, 8, device=DEV)
+    g = b.dfa_token_logprobs_backward(x, td, stats, ent, gl, ge)
+    _grad_check(x, t, gl, ge, g, dtype)
