@@ -97,6 +97,18 @@ __device__ __forceinline__ T lds(uint32_t addr) {
   return v;
 }
 
+// The reference of a row's exponentials is rounded, and a score less it (one operation) is
+// not: past 2^27 that alone could put a probability out of f16's range, past 2^32 out of
+// float32's, or all of a row's at 0.  So the reference is rounded down, which leaves the
+// largest score's exponent at kShift or above, and exponents are cut here, above what
+// kMostSum notices and below f16's limit.  Scores that are cut are the largest to within
+// their own rounding.  A NaN stays one.  (1 us of 177 for 64 requests of 4 rows.)
+constexpr float kMostExponent = 15.5f;
+__device__ __forceinline__ float cut_exponent(float x) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(kMostExponent));
+  return x;
+}
+
 __device__ __forceinline__ void sts(uint32_t addr, uint32_t x, uint32_t y) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
 }
@@ -407,7 +419,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
               float top = fmaxf(sc[nt][0][x], sc[nt][0][2 + x]);
 #pragma unroll
               for (int i = 1; i < KT; ++i) top = fmax3(top, sc[nt][i][x], sc[nt][i][2 + x]);
-              top *= f[nt][x];
+              top = __fmul_rd(top, f[nt][x]);
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1)
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -434,8 +446,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
           for (int i = 0; i < KT; ++i)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              float e0 = ex2_approx(fmaf(sc[nt][i][2 * y], f[nt][0], ref[0]));
-              float e1 = ex2_approx(fmaf(sc[nt][i][2 * y + 1], f[nt][1], ref[1]));
+              float e0 = ex2_approx(cut_exponent(fmaf(sc[nt][i][2 * y], f[nt][0], ref[0])));
+              float e1 = ex2_approx(cut_exponent(fmaf(sc[nt][i][2 * y + 1], f[nt][1], ref[1])));
               sum[nt][0] += e0;
               sum[nt][1] += e1;
               e0 *= weight, e1 *= weight;

@@ -75,6 +75,29 @@ struct TileInfo {
   int whole;
 };
 
+// 4 bits: scores far from 0.  The reference of a row's exponentials is rounded, and a score
+// less it (one operation) is not: past 2^27 that alone could put a probability out of f16's
+// range, past 2^32 out of float32's, or all of a row's at 0.  So a row whose largest score is
+// 2^23 or more in magnitude takes its scores by a factor smaller by 2^cool, which brings the
+// reference into [2^22, 2^23).  That divides the distances between scores too; but those
+// that matter then, below 2^-17 of the scores, are below what the scores' own sums may be off
+// by.  Returns `top` (the largest score, by the factor as it stands), the reference m and the
+// factor, for the row's new exponent, and that.  Out of line: it is rare, and the tile's code
+// is to stay short (exponents cut by an instruction each, as in cache4_fwd.cu: 145 us against
+// 137 for blocks of 32).  8 bits have no such step: 4% of their blocks of 32 for rows that
+// their limit on scores (dfa.h) excludes.
+constexpr float kFarScore = 0x1p23f;
+struct Cooled {
+  float top, m, factor;
+  int cool;
+};
+static __device__ __noinline__ Cooled recool(float top, float m, float factor, int was) {
+  const int e = static_cast<int>(__float_as_uint(top * pow2_bits(was)) >> 23 & 255u);
+  const int now = e == 255 ? 0 : max(e - (127 + 22), 0);
+  const float r = pow2_bits(was - now);
+  return {top * r, m * r, factor * r, now};
+}
+
 template <int BITS, int D, int RS>
 struct WideCfg {
   static constexpr int BM = 128, BN = 128;
@@ -628,6 +651,7 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
       const int end = r < k.R ? cache_own_end(w.rq.len, tok, w.rq.n, p.bs) : 0;
       float factor = 0.f;  // undoes the row's power of two, with the softmax scale
       float m = -INFINITY, l = 0.f;
+      int cool = 0;  // recool's exponent, 8 bits: 0
       float c = pow2_bits(kCacheMinExp), inv_c = pow2_bits(-kCacheMinExp);  // unit of O
       // The scores of keys that a cached tile does not have become -inf where they stand: a
       // pass of its own over the few such tiles, so that the common code stays short.
@@ -658,7 +682,7 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
         // number), and which of them count.
         auto groups = [&](int x, float* f, float* wt) {
           if constexpr (kKind == kOwn) {
-            f[0] = f[1] = p.scale_log2;
+            f[0] = f[1] = p.scale_log2 * pow2_bits(-cool);
             wt[0] = wt[1] = inv_c;
           } else if constexpr (BITS == 4) {  // the values' unit is O's until own keys come
             f[0] = f[1] = factor;
@@ -715,6 +739,12 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
             if (top > m) {
+              if constexpr (BITS == 4) {
+                if (__builtin_expect(fabsf(top) >= kFarScore || cool != 0, 0)) {
+                  const Cooled y = recool(top, m, factor, cool);
+                  top = y.top, m = y.m, factor = y.factor, cool = y.cool;
+                }
+              }
               const float a = ex2_approx(m - top);
               m = top;
               l *= a;
@@ -809,7 +839,7 @@ __global__ void __launch_bounds__(WideCfg<BITS, D, RS>::kThreads, 1)
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       const bool none = m == -INFINITY && l == 0.f;
       const float inv = none ? 0.f : c / l;
-      const float lse2 = none ? -INFINITY : m - kShift + lg2_approx(l);
+      const float lse2 = none ? -INFINITY : m * pow2_bits(cool) - kShift + lg2_approx(l);
       const bool single = w.whole();
       const long long at =
           (2LL * blockIdx.x + (w.first ? 0 : 1)) * C::BM + lb + (lane & 15);

@@ -430,6 +430,8 @@ int dfa_cache_append(const void *k, const void *v, const int *cu_new, const int 
  * Probabilities are rounded to f16 against cached values (2^-11; a value below
  * 2^-30 of the largest cached ones may be lost beside them) and to bf16 against
  * own ones (2^-8); scores, sums and the output are float32 in between.
+ * A row's scores, q . k / sqrt(headdim), are to stay below 2^26 in magnitude: a row
+ * that passes that may come out as infinite or not a number.
  * kv_heads divides heads, head h reads key/value head h / (heads / kv_heads).
  * batch <= 32768; the rows of one request, min(max_new, rows), are at most 2^24,
  * and 2^30 over heads / kv_heads.  With max_new 0 nothing is read or written.
@@ -480,6 +482,8 @@ int dfa_cache4_append(const void *k, const void *v, const int *cu_new, const int
  * Attention over it: arguments, results, limits and workspaces are those of
  * dfa_cache_forward (with a workspace size of its own).  The products run on the
  * cached values exactly; probabilities are rounded to f16 against them (2^-11).
+ * Scores may be of any size that float32 holds; past 2^22 those that differ by less
+ * than 2^-17 of themselves may count as equal.
  */
 long long dfa_cache4_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
                                      int headdim, int page_size, int max_pages);

@@ -751,3 +751,95 @@ def test_sampler_in_a_graph_and_on_two_streams(b, T):
         for i in range(2):
             assert same(outs[i], want[i][n]), (n, i)
     assert b.dfa_status() == 0
+
+
+def _winners(p, bs):
+    """Values (rows, H, d) of each row's likeliest key, and where that key is ahead of the
+    next one by more than the scores may be off, and by 40 besides."""
+    k, v = p["values"]
+    n, ps, (H, d) = p["cu"][-1], k.shape[2], p["q"].shape[1:]
+    q = _f64(p["q"])
+    best, clear = np.zeros((n, H, d)), np.zeros((n, H), bool)
+    for b, o in enumerate(p["lens"]):
+        pages = [int(x) for x in p["table"][b][:-(-o // ps)]]
+        for row in range(p["cu"][b], p["cu"][b + 1]):
+            at = row - p["cu"][b]
+            own = min(p["new"][b], ((o + at) // bs + 1) * bs - o) if p["k"] is not None else 0
+            for h in range(H):
+                hk = h // (H // k.shape[1])
+                kv = []
+                for c, x in ((k, p["k"]), (v, p["v"])):
+                    y = np.concatenate([c[i, hk] for i in pages])[:o]
+                    if own:
+                        y = np.concatenate([y, _f64(x[p["cu"][b]:p["cu"][b] + own, hk])])
+                    kv.append(y)
+                s = kv[0] @ q[row, h] / np.sqrt(d)
+                off = (d + 2) * 2.0 ** -23 * (np.abs(kv[0]) @ np.abs(q[row, h])).max() / np.sqrt(d)
+                first, second = np.argsort(s)[:-3:-1]
+                best[row, h] = kv[1][first]
+                clear[row, h] = s[first] - s[second] > 2 * off + 2.0 ** -21 * np.abs(s).max() + 40
+    return best, clear
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16, 40])
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("e", [24, 28, 34, 40, 60, 100, 118])
+def test_attention_of_huge_queries(b, d, H, own, e):
+    """Queries of 2^e on keys of some 2^-12: finite scores of up to 2^117.  The likeliest key
+    has all of the probability, lse is its score, and nothing is off by a power of two or not
+    a number."""
+    p = _problem([300, 40], [3, 8], H, 1, d, 32, seed=17, own=own, e=(-12, -11))
+    p["q"] = (p["q"].double().clamp(-1.9, 1.9) * 2.0 ** e).to(torch.bfloat16)
+    if own:
+        p["k"] = (p["k"].double() * 2.0 ** -11).to(torch.bfloat16)
+    out, lse = _run(b, p, 8)
+    assert b.dfa_status() == 0
+    assert lse[:, :p["cu"][-1]].isfinite().all()
+    _check(p, 8, out, lse)
+    best, clear = _winners(p, 8)
+    assert clear.mean() > 0.8
+    off = np.abs(_f64(out)[:len(best)] - best)[clear]
+    tol = (2.0 ** -8 + 2.0 ** -8 * own) * np.abs(best[clear]) + 2.0 ** -21
+    assert (off <= tol).all(), off.max()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16, 40])
+@pytest.mark.parametrize("e", [20, 30, 40, 100])
+@pytest.mark.parametrize("far", ["first", "last", "all", "ahead"])
+def test_attention_of_scores_far_apart(b, d, H, e, far):
+    """Some keys' scores are some -2^e exactly, the first ones', the last ones' or all, the
+    others' 0; or five keys' are 2^e: the likeliest keys' values have equal weights, whatever
+    the reference of a row was before they came."""
+    n, T = 700, 3
+    p = _problem([n], [T], H, 1, d, 32, seed=18, own=False)
+    at = np.arange(n)
+    far_ones = {"first": at < 400, "last": at >= 300, "all": at >= 0, "ahead": at % 150 == 77}[far]
+    # every code 8 (0), but for dim 0 of those keys: code 0, -8 scales of 2^-3
+    codes = np.full((p["kc"].shape[0], 1, 32, d), 8)
+    pages = p["table"][0]
+    for i in at[far_ones]:
+        codes[pages[i // 32], 0, i % 32, 0] = 0
+    p["kc"] = _pack(codes).to(DEV)
+    live = p["ks"].view(torch.uint8)
+    for i, page in enumerate(pages[:-(-n // 32)]):
+        live[int(page), :, :, :min(32, n - 32 * i)] = 0x30  # 2^-3
+    p["q"].zero_()  # nothing else, so that the scores are exact
+    p["q"][:, :, 0] = -2.0 ** e if far == "ahead" else 2.0 ** e
+    out, lse = _run(b, p, T)
+    assert b.dfa_status() == 0
+    best = far_ones if far in ("all", "ahead") else ~far_ones
+    score = (2.0 ** e if far == "ahead" else -2.0 ** e if far == "all" else 0.0) / np.sqrt(d)
+    v = np.concatenate([p["values"][1][int(i), 0] for i in pages])[:n][best]
+    # weights are f16 (2^-11), sums of n of them float32, the output bf16; a request's pieces
+    # are joined by their lse, which is off by 2^-22 of itself, and so by that factor's power
+    # of e: past 2^22 the pieces' weights may be any, but the output is among the values
+    off = np.abs(_f64(out) - v.mean(0))
+    piece = 2 * min(1, np.exp(2.0 ** -22 * abs(score)) - 1) if abs(score) < 2.0 ** 22 else 2
+    assert (off <= 2.0 ** -8 * np.abs(v.mean(0))
+            + (2.0 ** -10 + piece) * np.abs(v).mean(0)).all(), off.max()
+    room = 2.0 ** -7 * np.abs(v).max(0)
+    assert (_f64(out) <= v.max(0) + room).all() and (_f64(out) >= v.min(0) - room).all()
+    want = score + np.log(best.sum())
+    assert (lse.double().cpu() - want).abs().max() <= 2.0 ** -18 * (1 + abs(want))
