@@ -20,8 +20,10 @@
 // its own, once per piece) and added up in float32 times the keys' scales: 5 operations
 // for eight codes and one per group and score instead of the 9 that decoding takes.
 // q is bf16: a row is brought to f16 by a power of two of its own (its largest magnitude
-// lands in [2^14, 2^15)), which keeps every value down to 2^-27 of the row's largest
-// exact.
+// lands in [2^15, 2^16), below f16's largest as bf16 has 8 bits), which keeps every value
+// down to 2^-28 of the row's largest exact.  The codes' 2^24 is undone in two parts, 2^6 by
+// the keys' scales, the rest by the row's factor, for the whole does not fit the factor of
+// a row near bf16's largest.
 //
 // Values.  cache4_decode, with the scales of the two keys of a pair; the probabilities
 // are rounded to f16 (2^-11) while the sums use them unrounded.  Own keys and values are
@@ -341,14 +343,13 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^-e brings the row's largest magnitude into [2^14, 2^15)
-      int e = static_cast<int>(top >> 7) - 127 - 14;
+      // 2^-e brings the row's largest magnitude into [2^15, 2^16)
+      int e = static_cast<int>(top >> 7) - 127 - 15;
       if (e < -100) e = -100;
       const float inv = pow2_bits(-e);
-      // undoes that, the codes' 2^-24, with the softmax scale; finite and never 0, for
-      // a score may be 0 or -inf
-      const float f = fminf(fmaxf(pow2_bits(e) * (p.scale_log2 * 16777216.f), 0x1p-126f),
-                            0x1.fffffep127f);
+      // undoes that, and 2^-18 of the codes' 2^-24, with the softmax scale: within 2^-86 and
+      // 2^127.6, so never 0, for a score may be -inf
+      const float f = pow2_bits(e) * (p.scale_log2 * 0x1p18f);
 #pragma unroll
       for (int x = 0; x < 2; ++x) factor[nt][x] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * x);
 #pragma unroll
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // the scales of the thread's two keys
+            // the scales of the thread's two keys, times 2^6 (57344 at most)
             float ks[2];
             {
               uint32_t s2;
@@ -657,7 +658,8 @@ __global__ void __launch_bounds__(Cache4Tile<D, NT, WK, STAGES, RESIDENT, KEPT>:
                 s2 = __byte_perm(lds<unsigned short>(sct + ks_at + 16 * i + kUnit * grp), 0,
                                  0x1404);
               }
-              const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&s2));
+              const float2 f2 = __half22float2(
+                  __hmul2(*reinterpret_cast<const __half2*>(&s2), __float2half2_rn(64.f)));
               ks[0] = f2.x, ks[1] = f2.y;
             }
             const uint32_t lo = word[2 * i], hi = word[2 * i + 1];

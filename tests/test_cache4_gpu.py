@@ -843,3 +843,12 @@ def test_attention_of_scores_far_apart(b, d, H, e, far):
     assert (_f64(out) <= v.max(0) + room).all() and (_f64(out) >= v.min(0) - room).all()
     want = score + np.log(best.sum())
     assert (lse.double().cpu() - want).abs().max() <= 2.0 ** -18 * (1 + abs(want))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16, 40])
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("e", [121, 122, 124, 126])
+def test_attention_of_queries_near_the_largest(b, d, H, own, e):
+    """The same for queries of up to 2^127, whose scores are still float32 numbers."""
+    test_attention_of_huge_queries(b, d, H, own, e)

@@ -909,3 +909,21 @@ def test_captured_plan_advanced_outside_its_graph(b):
     assert pages.cache_lens.tolist() == [20, 15] and int(pages.free_count) == 12 - 2 - 1
     held = pages.block_table[0, :2].tolist() + pages.block_table[1, :1].tolist()
     assert sorted(held + pages.free_pages[:9].tolist()) == list(range(12))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H", [1, 6, 16, 40])
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 25])
+def test_attention_of_scores_up_to_their_limit(b, d, H, own, size):
+    """Scores of up to some 2^25 in magnitude: lse to float32's precision, outputs within the
+    scores' own bound."""
+    p = _problem([300, 40], [3, 8], H, 1, d, 32, seed=17, own=own)
+    q = p["q"].double()
+    top = osam.cache_attention(
+        _f64(p["q"]), _f64(p["kc"]), _f64(p["vc"]), _f64(p["ks"]), _f64(p["vs"]), p["table"],
+        p["lens"], p["cu"], _f64(p["k"]) if own else None, _f64(p["v"]) if own else None, 8)[3]
+    p["q"] = (q * 2.0 ** np.floor(np.log2(size / top.max()))).to(torch.bfloat16)
+    out, lse = _run(b, p, 8)
+    assert b.dfa_status() == 0
+    _check(p, 8, out, lse)
