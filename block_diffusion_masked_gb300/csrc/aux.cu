@@ -23,8 +23,8 @@ namespace dfa {
 // computed (the forward zeroed the accumulator).
 template <int D>
 __global__ void __launch_bounds__(256) dfa_bwd_preprocess_kernel(
-    const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
-    float* __restrict__ delta, float* __restrict__ dq_acc, int L, int H, int BH) {
+    const __nv_bfloat16* out, const __nv_bfloat16* dout, float* delta, float* dq_acc, int L, int H,
+    int BH) {
   constexpr int kLanesPerRow = D / 8;             // 8, 16 or 32
   constexpr int kRowsPerGroup = 32 / kLanesPerRow;  // rows one warp load covers
   constexpr int kUnroll = 4;
@@ -82,8 +82,7 @@ __global__ void __launch_bounds__(256) dfa_bwd_preprocess_kernel(
   }
 }
 
-__global__ void __launch_bounds__(256) dfa_dq_convert_kernel(const float4* __restrict__ src,
-                                                             uint4* __restrict__ dst,
+__global__ void __launch_bounds__(256) dfa_dq_convert_kernel(const float4* src, uint4* dst,
                                                              long long groups) {
   grid_dependency_wait();  // dq_acc comes from the kernel before this one
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
@@ -110,9 +109,8 @@ __global__ void __launch_bounds__(256) dfa_dq_convert_kernel(const float4* __res
 // P V product reads V with the keys contiguous (the K-major operand layout).
 // One block per (128 keys of one half, head, batch): the 128 x 128-byte
 // tile goes through shared memory, read and written in 16-byte units.
-__global__ void __launch_bounds__(256) dfa_fp8_v_transpose_kernel(const uint8_t* __restrict__ v,
-                                                                   uint8_t* __restrict__ vt, int n,
-                                                                   int n_pad, int H) {
+__global__ void __launch_bounds__(256) dfa_fp8_v_transpose_kernel(const uint8_t* v, uint8_t* vt,
+                                                                   int n, int n_pad, int H) {
   // tile[r][w]: bytes 4w..4w+3 of the head dims of key r (rows padded by a
   // word against bank conflicts)
   __shared__ uint32_t tile[128][33];

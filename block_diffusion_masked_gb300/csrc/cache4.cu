@@ -280,6 +280,8 @@ __global__ void __launch_bounds__(32 * kReadWarps) dfa_cache_read_kernel(const R
     const uint8_t* cache = which ? p.cache[1] : p.cache[0];
     const void* scales = which ? p.scale[1] : p.scale[0];
     const long long heads = static_cast<long long>(page) * p.Hk;
+    // (Ordinary loads: the cache may have been written by the kernel before, during which this
+    // block may have been here already, so its lines are not read-only for a kernel's time.)
     constexpr int kAtOnce = 4;  // 8 heads of 128 are 128 vectors; 8: 58 us
 #pragma unroll 1
     for (int i0 = lane; i0 < per; i0 += 32 * kAtOnce) {
@@ -293,13 +295,13 @@ __global__ void __launch_bounds__(32 * kReadWarps) dfa_cache_read_kernel(const R
         const long long token = ((heads + h) << p.page_shift) + at;
         const uint8_t* src = cache + ((token << p.vec_shift) + vec) * BITS;
         if constexpr (BITS == 4) {
-          w[e].x = __ldg(reinterpret_cast<const uint32_t*>(src));
+          w[e].x = *reinterpret_cast<const uint32_t*>(src);
           const long long group = ((heads + h) << p.vec_shift >> 2) + (vec >> 2);
           s[e] = __uint_as_float(
-              __ldg(static_cast<const uint8_t*>(scales) + (group << p.page_shift) + at));
+              static_cast<const uint8_t*>(scales)[(group << p.page_shift) + at]);
         } else {
-          w[e] = __ldg(reinterpret_cast<const uint2*>(src));
-          s[e] = __ldg(static_cast<const float*>(scales) + heads + h);
+          w[e] = *reinterpret_cast<const uint2*>(src);
+          s[e] = static_cast<const float*>(scales)[heads + h];
         }
       }
 #pragma unroll

@@ -174,6 +174,8 @@ struct Logit<float> {
 // A row as 16-byte vectors of the memory it lies in: vector v holds the row's
 // values v * kPer - lead ..., of which the first and the last vector may hold some
 // only.  Those are read value by value, so that nothing outside the row is read.
+// Ordinary loads, not those of the read-only path: a block may be there while the kernel
+// before it still writes the logits.
 template <typename T>
 struct Row {
   static constexpr int kPer = Logit<T>::kPer;
@@ -188,7 +190,7 @@ struct Row {
     uint4 w = make_uint4(none, none, none, none);
     if (v >= end) return w;
     const int e0 = v * kPer - lead;
-    if (e0 >= 0 && e0 + kPer <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + e0));
+    if (e0 >= 0 && e0 + kPer <= vocab) return *reinterpret_cast<const uint4*>(x + e0);
     alignas(16) T part[kPer];
     *reinterpret_cast<uint4*>(part) = w;
 #pragma unroll
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   auto load = [&](const uint4* x, int v, int end, uint4 (&w)[kAhead]) {
     if (v + (kAhead - 1) * kThreads < end) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) w[u] = __ldg(x + v + u * kThreads);
+      for (int u = 0; u < kAhead; ++u) w[u] = x[v + u * kThreads];
     }
   };
   auto vectors_of = [&](const Row<T>& r) {
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       uint4 rest[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead - 1; ++u)
-        if (v + u * kThreads < c.end) rest[u] = __ldg(x + v + u * kThreads);
+        if (v + u * kThreads < c.end) rest[u] = x[v + u * kThreads];
       if (c.ragged) rest[kAhead - 1] = r.load(c.v, c.hi);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             uint4 y[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
-              if (v + u * kThreads < c0.end) y[u] = __ldg(x + v + u * kThreads);
+              if (v + u * kThreads < c0.end) y[u] = x[v + u * kThreads];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
               if (v + u * kThreads < c0.end) offer(y[u], v + u * kThreads);
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll 1
         for (int q0 = 0; q0 < hots * steps; q0 += kListThreads) {
           const int v = tid < kListThreads && q0 + tid < hots * steps ? vector_of(q0 + tid) : c0.end;
-          if (v < c0.end) offer(__ldg(x + v), v);
+          if (v < c0.end) offer(x[v], v);
           __syncthreads();
           const bool full = s.count > kListKeep;
           __syncthreads();  // the count has been read
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(kThreads) dfa_scores_grad_kernel(const ScoresG
       for (int i = 0; i < kPer; ++i) f[i] = 0.f;
     } else {
       if (whole && aligned) {
-        L::unpack(__ldg(reinterpret_cast<const uint4*>(x + e0)), f);
+        L::unpack(*reinterpret_cast<const uint4*>(x + e0), f);
       } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
