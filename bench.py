@@ -119,8 +119,9 @@ def measured_peaks():
 
 # ------------------------------------------------------------------ kernels and traffic
 
-# The translation unit that defines each kernel; a kernel's identity for the
-# traffic records is the hash of that file and of the headers it includes.
+# The translation unit that defines each kernel, by its name, or by its name and first
+# template argument where those differ; a kernel's identity for the traffic
+# records is the hash of that file and of the headers it includes.
 KERNEL_SOURCES = {
     "dfa_fwd2_kernel": "fwd2.cu",
     "dfa_fwd_kernel": "fwd.cu",
@@ -129,6 +130,7 @@ KERNEL_SOURCES = {
     "dfa_cache_append_kernel": "cache.cu",
     "dfa_cache_fwd_kernel": "cache_fwd.cu",
     "dfa_cache_wide_kernel": "cache_wide.cu",
+    "dfa_cache_wide_kernel<4>": "cache4_wide.cu",
     "dfa_cache4_append_kernel": "cache4.cu",
     "dfa_cache_read_kernel": "cache4.cu",
     "dfa_cache4_rows_kernel": "cache4_fwd.cu",
@@ -155,11 +157,18 @@ def source_files(source):
     return [os.path.join(CSRC, f) for f in [source, *sorted(headers)]]
 
 
+def kernel_source(kernel):
+    """The translation unit of a kernel, given with or without template arguments."""
+    name, _, args = kernel.partition("<")
+    first = re.split(r"[,>]", args)[0].strip()
+    return KERNEL_SOURCES.get(f"{name}<{first}>") or KERNEL_SOURCES[name]
+
+
 def source_hash(kernel):
     """sha256 over the kernel's own .cu file and the headers it includes, directly
     or through one another, in the order of their names."""
     h = hashlib.sha256()
-    for f in source_files(KERNEL_SOURCES[kernel.split("<")[0]]):
+    for f in source_files(kernel_source(kernel)):
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode() + b"\0" + fh.read())
     return h.hexdigest()[:16]

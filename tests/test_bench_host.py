@@ -98,3 +98,24 @@ def test_training_kernels_do_not_include_the_samplers_headers():
     for source in ("fwd.cu", "fwd2.cu", "bwd2.cu"):
         names = {os.path.basename(f) for f in bench.source_files(source)}
         assert names == {source, "geometry.cuh", "params.cuh", "sm100.cuh"}
+
+
+def test_a_captures_kernel_names_its_sources():
+    """The kernel in a capture's title is looked up in the translation unit that the capture's
+    hash is said to be of; instances that are compiled elsewhere have entries of their own."""
+    import glob
+    import re
+
+    assert bench.kernel_source("dfa_cache_wide_kernel<8, 128>") == "cache_wide.cu"
+    assert bench.kernel_source("dfa_cache_wide_kernel<4, 128>") == "cache4_wide.cu"
+    assert bench.kernel_source("dfa_cache_wide_kernel") == "cache_wide.cu"
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(bench.PROFILES, "*.md"))):
+        with open(path) as f:
+            text = f.read()
+        title = re.match(r"# (dfa_\w+(?:<[^>]*>)?)", text)
+        named = re.search(r"^- source_sha256: [0-9a-f]{16} \(`(\w+\.cu)`", text, re.M)
+        if title and named:
+            assert bench.kernel_source(title.group(1)) == named.group(1), path
+            seen += 1
+    assert seen >= 10
