@@ -151,8 +151,9 @@ class KVCache:
     float32 (pages, kv_heads), a power-of-two scale for each page and head.
     ``bits=4``: k, v uint8 (pages, kv_heads, page_size, headdim / 2), k_scale, v_scale
     float8_e5m2 (pages, kv_heads, headdim / 32, page_size), a scale for each token, head
-    and 32 dims (``dfa_cache4_append``): 4.25 bits a value, an error of up to a 16th of
-    the largest of the 32 values (an 8th where it is of the other sign).
+    and 32 dims (``dfa_cache4_append``): 4.25 bits a value, an error of up to 5/64 of the
+    largest of the 32 values (an 8th for one of the other sign), where that is within
+    2^-11 and 7168.
     """
 
     def __init__(self, num_pages, page_size, kv_heads, headdim, device="cuda", bits=8):

@@ -162,3 +162,20 @@ def test_binding_refusals():
         b.dfa_cache4_read(*args, i, i, i, 1)
     with pytest.raises(ValueError):
         b.dfa_cache_read(*args, i, i, i, 1)
+
+
+def test_error_bound_by_the_largest_value():
+    """Where a group's largest magnitude is within 2^-11 and 7168, its scale is at most 5/4 of
+    an 8th of that: values are off by 5/64 of it at most, those of the sign that has no code
+    -8 by an 8th.  A 16th would be too little."""
+    g = np.random.default_rng(1)
+    x = torch.tensor(g.standard_normal((500, 64)) * np.exp2(g.integers(-8, 10, (500, 1))))
+    x[:64, 0] = torch.linspace(1, 1.984375, 64).double() * 16  # largest ones of each size
+    x = x.to(torch.bfloat16).double().numpy()
+    n, s = osam.quantise4(x)
+    s = np.repeat(s, 32, -1)
+    top = np.repeat(np.abs(x).reshape(500, 2, 32).max(-1), 32, -1)
+    assert top.min() > 2.0 ** -11 and top.max() < 7168
+    off, other = np.abs((n - 8) * s - x) / top, x / s > 0
+    assert off[~other].max() <= 5 / 64 and off[other].max() <= 1 / 8
+    assert off[~other].max() > 1 / 16
