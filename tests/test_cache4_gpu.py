@@ -852,3 +852,37 @@ def test_attention_of_scores_far_apart(b, d, H, e, far):
 def test_attention_of_queries_near_the_largest(b, d, H, own, e):
     """The same for queries of up to 2^127, whose scores are still float32 numbers."""
     test_attention_of_huge_queries(b, d, H, own, e)
+
+
+@pytest.mark.parametrize("e", [-14, -3, 7])
+def test_append_every_significand_beside_every_scale(b, e):
+    """All 128 significands of bf16, of either sign, beside every significand and sign of a
+    scale, over all powers of two that give |x / s| from 1/4 to 8: the codes and scales are
+    the definition's, every tie among them."""
+    d, ps = 64, 128
+    m = np.arange(128, 256) / 128.0
+    sizes = np.concatenate([m * 2.0 ** k for k in range(-2, 4)])
+    rows = []
+    for scale in (4, 5, 6, 7):
+        s = scale / 4 * 2.0 ** e  # 8 s is the largest magnitude of its groups
+        for sign in (1, -1):
+            x = np.concatenate([sizes, -sizes]) * 2.0 ** e
+            x = x[(np.abs(x) < 8 * s)]  # the largest one stands alone
+            x = np.concatenate([x, np.zeros(-x.size % 31)]).reshape(-1, 31)
+            rows.append(np.concatenate([np.full((len(x), 1), sign * 8 * s), x], 1))
+    x = torch.tensor(np.concatenate(rows))
+    x = torch.cat([x, x[:x.shape[0] % 2]]).view(-1, 1, d)
+    assert torch.equal(x.bfloat16().double(), x)
+    x = x.bfloat16().to(DEV)
+    T = x.shape[0]
+    table, cu, P = _requests([0], [T], ps, 1)
+    kc, ks = _cache(P, 1, ps, d, 1)
+    vc, vs = _cache(P, 1, ps, d, 2)
+    rc, rs = osam.append4(_f64(x), cu, [0], table, _codes(kc), _f64(ks))
+    ratio = _f64(x) / np.repeat(osam.quantise4(_f64(x))[1], 32, -1)
+    assert (np.abs(ratio) % 1 == 0.5).sum() >= 128 and np.abs(ratio).max() == 8
+    b.dfa_cache4_append(x, -x, _i32(cu), _i32([0]), _i32(table), kc, vc, ks, vs, T)
+    assert b.dfa_status() == 0
+    assert np.array_equal(_f64(ks), rs) and np.array_equal(_codes(kc), rc)
+    rc, rs = osam.append4(-_f64(x), cu, [0], table, _codes(vc), _f64(vs))
+    assert np.array_equal(_f64(vs), rs) and np.array_equal(_codes(vc), rc)
