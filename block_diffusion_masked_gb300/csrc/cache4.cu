@@ -242,6 +242,9 @@ __global__ void __launch_bounds__(32 * kReadWarps) dfa_cache_read_kernel(const R
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row0 = blockIdx.x * p.per_block, rows = min(p.per_block, p.rows - row0);
   if (warp == 0) {
+    // requests whose rows there are not: what fits is read
+    if (blockIdx.x == 0 && lane == 0 && p.cu_rows[p.batch] > p.rows)
+      atomicOr(p.status, kStatusIndex);
     int b = find_request(p.cu_rows, p.batch, row0);
     const int row = row0 + lane;
     int page = -1, place = -1;

@@ -503,7 +503,8 @@ int dfa_cache4_forward(const void *q, const void *k, const void *v, const void *
  * values are bf16 values).  cache_lens: the tokens held NOW.  Rows past
  * cu_rows[batch] are left alone.  A row whose token is not held (a position
  * negative or past the length), a page that may not be followed or a length past its
- * table gives zeros; rows out of order are left alone; each sets DFA_EDEVICE.
+ * table gives zeros; rows out of order are left alone, and so are those past `rows`;
+ * each sets DFA_EDEVICE.
  * batch <= 32768.
  */
 int dfa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale,

@@ -886,3 +886,26 @@ def test_append_every_significand_beside_every_scale(b, e):
     assert np.array_equal(_f64(ks), rs) and np.array_equal(_codes(kc), rc)
     rc, rs = osam.append4(-_f64(x), cu, [0], table, _codes(vc), _f64(vs))
     assert np.array_equal(_f64(vs), rs) and np.array_equal(_codes(vc), rc)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_read_of_more_rows_than_there_are(b, bits):
+    """cu_rows past the rows of k and v is an error; the rows that there are are right."""
+    lens, ps, d = [40, 20], 16, 64
+    table, _, P = _requests(lens, [0, 0], ps, 6)
+    if bits == 4:
+        kc, ks = _cache(P, 1, ps, d, 7)
+        values = osam.values4(_codes(kc), _f64(ks))
+    else:
+        kc = torch.randn((P, 1, ps, d), device=DEV).to(torch.float8_e4m3fn)
+        ks = torch.ones((P, 1), device=DEV)
+        values = _f64(kc)
+    cu, first = [0, 10, 16], [20, 3]
+    read = b.dfa_cache4_read if bits == 4 else b.dfa_cache_read
+    args = (kc, kc, ks, ks, _i32(table), _i32(lens), _i32(cu))
+    k, _ = read(*args, 12, first=_i32(first))
+    assert b.dfa_status() == b.DFA_EDEVICE
+    right = osam.cache_read(values, table, first, cu)
+    assert np.array_equal(_f64(k), right[:12])
+    assert np.array_equal(_f64(read(*args, 16, first=_i32(first))[0]), right)
+    assert b.dfa_status() == 0
