@@ -559,11 +559,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
     }
     const float mine = a.m;
-      const Piece c0 = c;  // the piece that is done
-      if (item + static_cast<int>(gridDim.x) < items) {
-        c = enter(item + gridDim.x);
-        load(vectors_of(row_of(c.row)), c.at, c.end, w);
-      }
+    const Piece c0 = c;  // the piece that is done
+    if (item + static_cast<int>(gridDim.x) < items) {
+      c = enter(item + gridDim.x);
+      load(vectors_of(row_of(c.row)), c.at, c.end, w);
+    }
     a = warp_join(a);
     if (lane == 0) s_warp[warp] = a;
 
@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (offers) offer(r.load(c0.v, c0.hi), c0.v);
 #pragma unroll 1
         for (int q0 = 0; q0 < hots * steps; q0 += kListThreads) {
-          const int v = tid < kListThreads && q0 + tid < hots * steps ? vector_of(q0 + tid) : c0.end;
+          const int q = q0 + tid;
+          const int v = tid < kListThreads && q < hots * steps ? vector_of(q) : c0.end;
           if (v < c0.end) offer(x[v], v);
           __syncthreads();
           const bool full = s.count > kListKeep;
