@@ -286,7 +286,12 @@ __global__ void __launch_bounds__(32 * kReadWarps) dfa_cache_read_kernel(const R
     const long long heads = static_cast<long long>(page) * p.Hk;
     // (Ordinary loads: the cache may have been written by the kernel before, during which this
     // block may have been here already, so its lines are not read-only for a kernel's time.)
-    constexpr int kAtOnce = 4;  // 8 heads of 128 are 128 vectors; 8: 58 us
+    // Vectors a lane has on their way.  80 k tokens of 1024 values, or as many values (but 2^20
+    // tokens at most) in rows of other sizes, us with 2, 4 and 8, 4 bits: rows of 64 values 283,
+    // 278, 312 (8 of a warp's lanes have a vector: such rows are bound by their number), of 256
+    // 97, 96, 113, of 512 75, 76, 82, of 1024 77, 71, 70, of 2048 86, 79, 73; 8 bits: 303, 284,
+    // 381, 117, 113, 150, 85, 86, 101, 83, 78, 84, 89, 82, 81.
+    constexpr int kAtOnce = 4;
 #pragma unroll 1
     for (int i0 = lane; i0 < per; i0 += 32 * kAtOnce) {
       uint2 w[kAtOnce];

@@ -38,7 +38,7 @@
 // pieces of a cut segment are joined by a second launch.
 //
 // Measured (headdim 128, 8 heads for keys): 64 ragged requests of up to 16000 tokens, 4 rows
-// to a key, 689 MB: 177 us, 3.9 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
+// to a key, 689 MB: 180 us, 3.8 TB/s, against 102 us for the bytes; 24 of up to 8000, 16
 // rows, 126 MB: 57 us against 18.5; one request of 500 tokens, 4 heads: 10.1 us, launches
 // and latency.  Bound by the decoding: a unit is some 770 instructions of a warp, and the
 // schedulers issue in 70% of the cycles while all warps have work (a copy of the kernel that
@@ -104,7 +104,7 @@ __device__ __forceinline__ T lds(uint32_t addr) {
 // float32's, or all of a row's at 0.  So the reference is rounded down, which leaves the
 // largest score's exponent at kShift or above, and exponents are cut here, above what
 // kMostSum notices and below f16's limit.  Scores that are cut are the largest to within
-// their own rounding.  A NaN stays one.  (1 us of 177 for 64 requests of 4 rows.)
+// their own rounding.  A NaN stays one.  (1 us of 180 for 64 requests of 4 rows.)
 constexpr float kMostExponent = 15.5f;
 __device__ __forceinline__ float cut_exponent(float x) {
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(kMostExponent));

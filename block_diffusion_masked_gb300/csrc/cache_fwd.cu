@@ -1015,7 +1015,7 @@ CachePlan cache_plan_for(int batch, int max_new, int G, int kv_heads, int d, lon
 //   headdim  64,   8 rows    38    38    39    41    43    44
 //   headdim  64,  16 rows    47    46    47    47    49    50
 //   headdim  64,  32 rows    75    72    71    67    70    71
-//   headdim  64, 128 rows   111   109   108   107   110   109  (109 by now)
+//   headdim  64, 128 rows   111   109   108   107   110   109  (107 by now)
 //   headdim 128,   8 rows    32    32    32    33    34    35
 //   headdim 128,  16 rows    43    41    41    42    43    45
 //   headdim 128, 128 rows    88    82    79    76    76    80  (73 by now)

@@ -26,8 +26,8 @@
 // others (setmaxnreg).
 //
 // Measured, 128 rows, headdim 128, 32 ragged requests of up to 8192 tokens
-// (342 MB, 81 GFLOP): 126 us, 2.7 TB/s, 640 TFLOP/s; 64 rows 124, headdim 64
-// 197 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
+// (342 MB, 81 GFLOP): 126 us, 2.7 TB/s, 640 TFLOP/s; 64 rows 118, headdim 64
+// 202 (twice the heads: twice the scores).  Bound by the softmax warps: a tile
 // takes them some 2400 cycles, of which its 128 x 128 exponentials need 512 of
 // the special function units'; what is left is latency (waits that find their
 // barrier complete, TMEM round trips) and the fetching of instructions, five
@@ -35,7 +35,7 @@
 // loaded ahead, loops unrolled) made the kernel 30% slower, and rolled
 // converters made it 5% faster.  Ends of pieces take 10 us each, of which the
 // last tiles' chain is most, and the first products come after 11.  4 bits, the same
-// requests, 128 rows and 8 heads: 136 us against 43 for the products; a tile takes 2800
+// requests, 128 rows and 8 heads: 137 us against 43 for the products; a tile takes 2800
 // cycles, 1470 of them the softmax warps' own, and the converters 1800, which the rings'
 // two operand tiles hide.
 #pragma once
@@ -107,7 +107,7 @@ struct WideCfg {
   // setmaxnreg split of the launch's 96 registers a thread: 256 * (120 + 88) + 128 * 64 ==
   // 640 * 96.  No role spills (with 136, 72 and 64 the 4-bit converters do).  Measured, 128
   // rows of headdim 128: 4 bits 136 us with 128 and 80, 138 with 120 and 88; 8 bits 129 and
-  // 126.
+  // 126 (before recool).
   static constexpr int kRegSoft = BITS == 4 ? 128 : 120, kRegConv = BITS == 4 ? 80 : 88,
                        kRegRest = 64;
   static_assert(256 * kRegSoft + 256 * kRegConv + 128 * kRegRest <= kThreads * 96,

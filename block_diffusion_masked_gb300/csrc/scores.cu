@@ -17,11 +17,13 @@
 // Bound by memory: one pass over the logits, 16 bytes a thread and access, two or three of
 // them on their way while as many are summed (some 8 operations a logit with the entropy,
 // which all rows have).  Measured: 8192 rows of 50001 bf16 logits (819 MB) 138 us, 5.9 TB/s,
-// their gradient 195 us (in and out, the ends of both still in L2); 511 rows of 131001
-// float32 logits (268 MB) with 32 alternatives 57.5 us, 4.7 TB/s; 20 rows of 32768 with 8
-// 9.6 us, two launches' latency.  Tried and slower, in place of the registers that hold the
-// next vectors: a ring in shared memory filled by asynchronous copies (148 us against 140);
-// sums two to an operation (237: the pairs have to be put together).
+// their gradient 194 us where half of the rows have a token (the others' logits are not read:
+// 1.23 GB), 256 us where all have (1.64 GB, 6.4 TB/s), 274 us for 50257 logits cut out of rows
+// of 50304, which do not lie in their vectors as the gradient does (contiguous ones 257); 511
+// rows of 131001 float32 logits (268 MB) with 32 alternatives 57.5 us, 4.7 TB/s; 20 rows of
+// 32768 with 8 9.6 us, two launches' latency.  Tried and slower, in place of the registers that
+// hold the next vectors: a ring in shared memory filled by asynchronous copies (148 us against
+// 140); sums two to an operation (237: the pairs have to be put together).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

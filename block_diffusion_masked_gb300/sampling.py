@@ -190,7 +190,8 @@ class KVCache:
     def read(self, pages, cu_rows, rows, first=None, **kwargs):
         """Tokens that ``pages`` (a :class:`PageTable`) counts as held, as the cache
         holds them: request b's from first[b] (None: 0) on, in rows [cu_rows[b],
-        cu_rows[b + 1]) of k, v (rows, kv_heads, headdim) bf16 (``dfa_cache_read``)."""
+        cu_rows[b + 1]) of k, v (rows, kv_heads, headdim) bf16 (``dfa_cache_read``).
+        A 4-bit cache that they are appended to again may round them once more."""
         read = binding.dfa_cache_read if self.bits == 8 else binding.dfa_cache4_read
         return read(self.k, self.v, self.k_scale, self.v_scale, pages.block_table,
                     pages.cache_lens, cu_rows, rows, first=first, **kwargs)

@@ -482,8 +482,8 @@ int dfa_cache4_append(const void *k, const void *v, const int *cu_new, const int
  * Attention over it: arguments, results, limits and workspaces are those of
  * dfa_cache_forward (with a workspace size of its own).  The products run on the
  * cached values exactly; probabilities are rounded to f16 against them (2^-11).
- * Scores may be of any size that float32 holds; past 2^22 those that differ by less
- * than 2^-17 of themselves may count as equal.
+ * Scores may be of any size that, times log2 e, float32 holds; past 2^22 those that
+ * differ by less than 2^-17 of themselves may count as equal.
  */
 long long dfa_cache4_workspace_bytes(int batch, int rows, int max_new, int heads, int kv_heads,
                                      int headdim, int page_size, int max_pages);
@@ -504,8 +504,12 @@ int dfa_cache4_forward(const void *q, const void *k, const void *v, const void *
  * cu_rows[batch] are left alone.  A row whose token is not held (a position
  * negative or past the length), a page that may not be followed or a length past its
  * table gives zeros; rows out of order are left alone, and so are those past `rows`;
- * each sets DFA_EDEVICE.
- * batch <= 32768.
+ * each sets DFA_EDEVICE.  batch <= 32768.
+ *
+ * Appended again, what was read from 8 bits loses nothing but subnormals of its pages'
+ * scales.  What was read from 4 bits may be rounded once more: a group whose largest
+ * value's code is less than its scale reaches (8% of those of normal values) gets a
+ * smaller scale.  After that it stays as it is.
  */
 int dfa_cache_read(const void *k_cache, const void *v_cache, const float *k_scale,
                    const float *v_scale, const int *block_table, const int *cache_lens,

@@ -179,3 +179,16 @@ def test_error_bound_by_the_largest_value():
     off, other = np.abs((n - 8) * s - x) / top, x / s > 0
     assert off[~other].max() <= 5 / 64 and off[other].max() <= 1 / 8
     assert off[~other].max() > 1 / 16
+
+
+def test_values_appended_again():
+    """What was read back and is appended again is rounded once more at most: some groups get a
+    smaller scale, by the definition, and keep it."""
+    g = np.random.default_rng(0)
+    x = torch.tensor(g.standard_normal((500, 64))).to(torch.bfloat16).double().numpy()
+    seen = [x]
+    for _ in range(3):
+        n, s = osam.quantise4(seen[-1])
+        seen.append((n - 8) * np.repeat(s, 32, -1))
+    changed = (seen[2] != seen[1]).reshape(500, 2, 32).any(-1).mean()
+    assert 0 < changed < 0.15 and np.array_equal(seen[3], seen[2])
