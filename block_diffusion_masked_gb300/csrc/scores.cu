@@ -16,11 +16,11 @@
 //
 // Bound by memory: one pass over the logits, 16 bytes a thread and access, two or three of
 // them on their way while as many are summed (some 8 operations a logit with the entropy,
-// which all rows have).  Measured: 8192 rows of 50001 bf16 logits (819 MB) 138 us, 5.9 TB/s,
+// which all rows have).  Measured: 8192 rows of 50001 bf16 logits (819 MB) 140 us, 5.9 TB/s,
 // their gradient 194 us where half of the rows have a token (the others' logits are not read:
 // 1.23 GB), 256 us where all have (1.64 GB, 6.4 TB/s), 274 us for 50257 logits cut out of rows
 // of 50304, which do not lie in their vectors as the gradient does (contiguous ones 257); 511
-// rows of 131001 float32 logits (268 MB) with 32 alternatives 57.5 us, 4.7 TB/s; 20 rows of
+// rows of 131001 float32 logits (268 MB) with 32 alternatives 55.7 us, 4.8 TB/s; 20 rows of
 // 32768 with 8 9.6 us, two launches' latency.  Tried and slower, in place of the registers that
 // hold the next vectors: a ring in shared memory filled by asynchronous copies (148 us against
 // 140); sums two to an operation (237: the pairs have to be put together).
@@ -201,6 +201,17 @@ struct Row {
     return *reinterpret_cast<const uint4*>(part);
   }
 };
+
+// Vectors that are read once, past the first-level cache: 140 us for 8192 rows of 50001 bf16
+// logits, 143 without the hint; 511 rows of 131001 float32 with alternatives 55.7 and 57.4.
+// (The gradient loses with it: 205 and 195.)
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 // max(x, kFar), NaN kept.
 __device__ __forceinline__ float not_far(float x) {
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   auto load = [&](const uint4* x, int v, int end, uint4 (&w)[kAhead]) {
     if (v + (kAhead - 1) * kThreads < end) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) w[u] = x[v + u * kThreads];
+      for (int u = 0; u < kAhead; ++u) w[u] = load_stream(x + v + u * kThreads);
     }
   };
   auto vectors_of = [&](const Row<T>& r) {
